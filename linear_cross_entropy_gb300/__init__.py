@@ -32,9 +32,14 @@ __all__ = [
     "forward_workspace_bytes", "backward_workspace_bytes", "backward_chunk_cols", "memory_report", "kernel_launch_count",
     "Profiler", "vocab_logit_sums", "vocab_order", "cce_loss_and_grad", "fused_linear_cross_entropy",
     "loss_and_grad_workspace_bytes", "raise_pending_errors",
+    "layer_norm", "rms_norm", "cce_layer_norm_forward", "cce_layer_norm_backward", "cce_rms_norm_forward",
+    "cce_rms_norm_backward", "norm_backward_workspace_bytes",
 ]
 
 _lib.load()
+
+from .norm import (cce_layer_norm_backward, cce_layer_norm_forward, cce_rms_norm_backward,  # noqa: E402
+                   cce_rms_norm_forward, layer_norm, norm_backward_workspace_bytes, rms_norm)
 
 
 def _ptr(t):

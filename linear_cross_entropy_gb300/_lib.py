@@ -1,4 +1,4 @@
-"""ctypes binding of libcce.so (declarations in include/cce.h).
+"""ctypes binding of libcce.so (declarations in include/cce.h and include/cce_ops.h).
 
 Loading fails loudly when the library has not been built: there is no
 fallback implementation.
@@ -127,6 +127,23 @@ def load() -> ctypes.CDLL:
     lib.cce_profile_read.restype = ctypes.c_int
     lib.cce_profile_phase_name.argtypes = [ctypes.c_int]
     lib.cce_profile_phase_name.restype = ctypes.c_char_p
+    # include/cce_ops.h
+    rows = [i64, i64, i64]  # inner, row stride, outer stride
+    ci, cf = ctypes.c_int, ctypes.c_float
+    lib.cce_ops_abi_version.argtypes = []
+    lib.cce_ops_abi_version.restype = ci
+    lib.cce_layer_norm_forward.argtypes = [vp] + rows + [ci, vp, vp, ci, i64, i64, cf, vp, ci, vp, vp, vp]
+    lib.cce_layer_norm_forward.restype = ci
+    lib.cce_rms_norm_forward.argtypes = [vp] + rows + [ci, vp, ci, cf, i64, i64, cf, vp, ci, vp, vp]
+    lib.cce_rms_norm_forward.restype = ci
+    lib.cce_layer_norm_backward.argtypes = ([vp] + rows + [ci, vp] + rows
+                                            + [ci, vp, ci, vp, vp, i64, i64, vp, vp, vp, vp, sz, vp])
+    lib.cce_layer_norm_backward.restype = ci
+    lib.cce_rms_norm_backward.argtypes = ([vp] + rows + [ci, vp] + rows
+                                          + [ci, vp, ci, cf, vp, i64, i64, vp, vp, vp, sz, vp])
+    lib.cce_rms_norm_backward.restype = ci
+    lib.cce_norm_backward_workspace_bytes.argtypes = [i64, i64]
+    lib.cce_norm_backward_workspace_bytes.restype = sz
     _lib = lib
     return lib
 

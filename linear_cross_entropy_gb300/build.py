@@ -22,7 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libcce.so")
-SOURCES = ("cce_api.cu", "gemm_kernels.cu", "cce_noalloc.cu", "cce_sort.cu", "cce_flce.cu")
+SOURCES = ("cce_api.cu", "gemm_kernels.cu", "cce_noalloc.cu", "cce_sort.cu", "cce_flce.cu", "norm_api.cu",
+           "norm_bf16.cu", "norm_f16.cu", "norm_f32.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -42,7 +43,7 @@ def _flags(verbose_ptxas: bool):
 
 
 def _deps_mtime() -> float:
-    paths = [os.path.join(CSRC, p) for p in os.listdir(CSRC)] + [os.path.join(INCLUDE, "cce.h"), __file__]
+    paths = [os.path.join(d, p) for d in (CSRC, INCLUDE) for p in os.listdir(d)] + [__file__]
     return max(os.path.getmtime(p) for p in paths if os.path.isfile(p))
 
 

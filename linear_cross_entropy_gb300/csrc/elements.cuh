@@ -1,0 +1,151 @@
+// Element types of the bandwidth-bound operators: vectors of VEC elements
+// loaded and stored in accesses of up to 16 bytes, converted to and from fp32.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <cstring>
+
+#include "../../include/cce_ops.h"
+
+namespace cce {
+
+template <typename T>
+struct ElemType;
+template <>
+struct ElemType<float> {
+  static constexpr int id = CCE_F32;
+};
+template <>
+struct ElemType<__half> {
+  static constexpr int id = CCE_F16;
+};
+template <>
+struct ElemType<__nv_bfloat16> {
+  static constexpr int id = CCE_BF16;
+};
+
+// VEC consecutive elements as raw words.  The access width is the vector's
+// size, 16 bytes at most (a wider vector takes several accesses).
+template <typename T, int VEC>
+struct Vec {
+  static constexpr int BYTES = static_cast<int>(sizeof(T)) * VEC;
+  static constexpr int WORDS = (BYTES + 3) / 4;
+  uint32_t w[WORDS];
+
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (BYTES >= 16) {
+#pragma unroll
+      for (int i = 0; i < BYTES / 16; ++i) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+        w[4 * i] = v.x;
+        w[4 * i + 1] = v.y;
+        w[4 * i + 2] = v.z;
+        w[4 * i + 3] = v.w;
+      }
+    } else if constexpr (BYTES == 8) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+      w[0] = v.x;
+      w[1] = v.y;
+    } else if constexpr (BYTES == 4) {
+      w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+    } else {
+      static_assert(BYTES == 2, "one 16-bit element");
+      w[0] = __ldg(reinterpret_cast<const uint16_t*>(p));
+    }
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (BYTES >= 16) {
+#pragma unroll
+      for (int i = 0; i < BYTES / 16; ++i)
+        reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    } else if constexpr (BYTES == 8) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    } else if constexpr (BYTES == 4) {
+      *reinterpret_cast<uint32_t*>(p) = w[0];
+    } else {
+      *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(w[0]);
+    }
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (sizeof(T) == 4) {
+      return __uint_as_float(w[i]);
+    } else {
+      const uint16_t h = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+      if constexpr (ElemType<T>::id == CCE_BF16) {
+        return __uint_as_float(static_cast<uint32_t>(h) << 16);
+      } else {
+        return __half2float(__ushort_as_half(h));
+      }
+    }
+  }
+  // All VEC elements from fp32, rounded to nearest even.
+  __device__ __forceinline__ void set(const float (&f)[VEC]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) w[i] = __float_as_uint(f[i]);
+    } else if constexpr (VEC == 1) {
+      w[0] = half_bits(f[0]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC / 2; ++i) {
+        if constexpr (ElemType<T>::id == CCE_BF16) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+          std::memcpy(&w[i], &h, 4);
+        } else {
+          const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+          std::memcpy(&w[i], &h, 4);
+        }
+      }
+    }
+  }
+
+ private:
+  __device__ __forceinline__ static uint32_t half_bits(float f) {
+    if constexpr (ElemType<T>::id == CCE_BF16) {
+      return __bfloat16_as_ushort(__float2bfloat16_rn(f));
+    } else {
+      return __half_as_ushort(__float2half_rn(f));
+    }
+  }
+};
+
+// VEC parameters of a run-time type as fp32 (the type is uniform over a launch).
+template <int VEC>
+__device__ __forceinline__ void load_param(const void* p, int type, int64_t i, float (&out)[VEC]) {
+  if (type == CCE_F32) {
+    Vec<float, VEC> v;
+    v.load(static_cast<const float*>(p) + i);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) out[e] = v.get(e);
+  } else if (type == CCE_BF16) {
+    Vec<__nv_bfloat16, VEC> v;
+    v.load(static_cast<const __nv_bfloat16*>(p) + i);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) out[e] = v.get(e);
+  } else {
+    Vec<__half, VEC> v;
+    v.load(static_cast<const __half*>(p) + i);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) out[e] = v.get(e);
+  }
+}
+
+__device__ __forceinline__ void store_param(void* p, int type, int64_t i, float f) {
+  if (type == CCE_F32) {
+    static_cast<float*>(p)[i] = f;
+  } else if (type == CCE_BF16) {
+    static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(f);
+  } else {
+    static_cast<__half*>(p)[i] = __float2half_rn(f);
+  }
+}
+
+}  // namespace cce

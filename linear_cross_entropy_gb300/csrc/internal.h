@@ -27,6 +27,12 @@ cudaError_t launch_selftest_wait_timeout(int32_t* dev_err, uint64_t timeout_ns, 
 // Launches the CTA-pair handshake self-test (see cce_selftest_pair_timeout).
 cudaError_t launch_selftest_pair_timeout(int32_t* dev_err, uint64_t timeout_ns, int hold, cudaStream_t stream);
 
+// The current device is one the library runs on: its SM count, and the status
+// of the check (a cce_status).
+int device_ready(int* sms);
+// Adds to cce_kernel_launch_count().
+void count_launches(int n);
+
 // Opt the GEMM kernels into their dynamic shared-memory size (once per device).
 cudaError_t prepare_gemm_kernels();
 

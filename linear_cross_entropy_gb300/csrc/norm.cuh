@@ -1,0 +1,533 @@
+// Layer norm and RMS norm kernels, forward and backward.
+//
+//   layer norm  m = sum x / D, r = 1 / sqrt(sum (x - m)^2 / D + eps), z = (x - m) r, y = z w + b
+//   RMS norm    m = 0,         r = 1 / sqrt(sum x^2 / D + eps),       z = x r,       y = z (o + w)
+//   backward    g = dy (o + w);  dx = r (g - sum(g) / D - z sum(g z) / D), the sum(g) term for layer norm only
+//               dw = sum over rows of dy z;  db = sum over rows of dy
+//
+// All of it is bound by memory: a row is read once, held in registers as raw
+// words, reduced, and written.  The variance is the sum of squared deviations
+// from the mean, taken over the registers, so nothing cancels.
+//
+// A row belongs to a group of threadIdx.x = 0 .. tpr - 1 (tpr a power of two up
+// to 32, or a multiple of 32); a block has blockDim.y groups.  Thread l of a
+// group holds the vectors l, l + tpr, ..., K of them.
+#pragma once
+
+#include <algorithm>
+
+#include "elements.cuh"
+#include "norm.h"
+
+namespace cce {
+namespace norm {
+
+constexpr int MAX_THREADS = 512;
+
+__device__ __forceinline__ float lanes_sum(float v, int width) {
+  for (int o = width >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Barrier over the warps of one group (the whole block when it is the only one).
+__device__ __forceinline__ void group_sync() {
+  if (blockDim.y == 1) {
+    __syncthreads();
+  } else {
+    asm volatile("bar.sync %0, %1;" ::"r"(threadIdx.y + 1), "r"(blockDim.x) : "memory");
+  }
+}
+
+// Sum over the group; sm has one slot for each of the group's warps.
+__device__ __forceinline__ float group_sum(float v, float* sm) {
+  const int tpr = blockDim.x;
+  if (tpr <= 32) return lanes_sum(v, tpr);
+  v = lanes_sum(v, 32);
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
+  group_sync();
+  float t = 0.0f;
+  for (int i = 0; i < tpr >> 5; ++i) t += sm[i];
+  return t;
+}
+
+__device__ __forceinline__ float2 group_sum2(float2 v, float2* sm) {
+  const int tpr = blockDim.x;
+  const int width = tpr < 32 ? tpr : 32;
+  v.x = lanes_sum(v.x, width);
+  v.y = lanes_sum(v.y, width);
+  if (tpr <= 32) return v;
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
+  group_sync();
+  float2 t = make_float2(0.0f, 0.0f);
+  for (int i = 0; i < tpr >> 5; ++i) {
+    t.x += sm[i].x;
+    t.y += sm[i].y;
+  }
+  return t;
+}
+
+template <bool LAYER, int VEC>
+__device__ __forceinline__ void load_gain(const void* w, int p_type, float offset, int64_t c, float (&g)[VEC]) {
+  if (w) {
+    load_param<VEC>(w, p_type, c, g);
+    if (!LAYER) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) g[e] += offset;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) g[e] = 1.0f;
+  }
+}
+
+// ------------------------------------------------------------------ forward
+// One row per group, one pass over memory.
+template <typename TX, typename TY, int VEC, int K, bool LAYER>
+__global__ void __launch_bounds__(MAX_THREADS) fwd_kernel(NormFwd a) {
+  __shared__ float sm[2][MAX_THREADS / 32];
+  const int l = threadIdx.x, tpr = blockDim.x;
+  float* sm0 = sm[0] + threadIdx.y * (tpr >> 5);
+  float* sm1 = sm[1] + threadIdx.y * (tpr >> 5);
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const bool live = n < a.N;  // a group without a row still takes part in its warp's shuffles
+  const TX* x = static_cast<const TX*>(a.x) + (live ? a.xm.at(static_cast<int>(n)) : 0);
+  Vec<TX, VEC> xv[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = (l + k * tpr) * VEC;
+    if (live && c < a.D) {
+      xv[k].load(x + c);
+    } else {
+      xv[k].zero();
+    }
+  }
+  const float fd = static_cast<float>(a.D);
+  float mean = 0.0f;
+  if (LAYER) {
+    float s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) s += xv[k].get(e);
+    }
+    mean = group_sum(s, sm0) / fd;
+  }
+  float q = 0.0f;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if ((l + k * tpr) * VEC < a.D) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float d = xv[k].get(e) - mean;
+        q += d * d;
+      }
+    }
+  }
+  const float rstd = 1.0f / sqrtf(group_sum(q, sm1) / fd + a.eps);
+  if (!live) return;
+  if (l == 0) {
+    if (LAYER && a.mean) a.mean[n] = mean;
+    if (a.rstd) a.rstd[n] = rstd;
+  }
+  TY* y = static_cast<TY*>(a.y) + n * a.D;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = (l + k * tpr) * VEC;
+    if (c < a.D) {
+      float w[VEC], b[VEC], o[VEC];
+      load_gain<LAYER, VEC>(a.w, a.p_type, a.offset, c, w);
+      if (LAYER && a.b) {
+        load_param<VEC>(a.b, a.p_type, c, b);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) b[e] = 0.0f;
+      }
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) o[e] = (xv[k].get(e) - mean) * rstd * w[e] + b[e];
+      Vec<TY, VEC> out;
+      out.set(o);
+      out.store(y + c);
+    }
+  }
+}
+
+// Rows too long for the registers of one block: one block per row, which
+// reads it once per sum and once more to write (from L2 after the first time).
+template <typename TX, typename TY, int VEC, bool LAYER>
+__global__ void __launch_bounds__(MAX_THREADS) fwd_long_kernel(NormFwd a) {
+  __shared__ float sm[2][MAX_THREADS / 32];
+  const int64_t n = blockIdx.x;
+  const TX* x = static_cast<const TX*>(a.x) + a.xm.at(static_cast<int>(n));
+  const float fd = static_cast<float>(a.D);
+  const int64_t first = static_cast<int64_t>(threadIdx.x) * VEC, step = static_cast<int64_t>(blockDim.x) * VEC;
+  float mean = 0.0f;
+  if (LAYER) {
+    float s = 0.0f;
+#pragma unroll 4
+    for (int64_t c = first; c < a.D; c += step) {
+      Vec<TX, VEC> v;
+      v.load(x + c);
+      float t = 0.0f;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) t += v.get(e);
+      s += t;
+    }
+    mean = group_sum(s, sm[0]) / fd;
+  }
+  float q = 0.0f;
+#pragma unroll 4
+  for (int64_t c = first; c < a.D; c += step) {
+    Vec<TX, VEC> v;
+    v.load(x + c);
+    float t = 0.0f;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const float d = v.get(e) - mean;
+      t += d * d;
+    }
+    q += t;
+  }
+  const float rstd = 1.0f / sqrtf(group_sum(q, sm[1]) / fd + a.eps);
+  if (threadIdx.x == 0) {
+    if (LAYER && a.mean) a.mean[n] = mean;
+    if (a.rstd) a.rstd[n] = rstd;
+  }
+  TY* y = static_cast<TY*>(a.y) + n * a.D;
+#pragma unroll 2
+  for (int64_t c = first; c < a.D; c += step) {
+    Vec<TX, VEC> v;
+    v.load(x + c);
+    float w[VEC], b[VEC], o[VEC];
+    load_gain<LAYER, VEC>(a.w, a.p_type, a.offset, c, w);
+    if (LAYER && a.b) {
+      load_param<VEC>(a.b, a.p_type, c, b);
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) b[e] = 0.0f;
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) o[e] = (v.get(e) - mean) * rstd * w[e] + b[e];
+    Vec<TY, VEC> out;
+    out.set(o);
+    out.store(y + c);
+  }
+}
+
+// ----------------------------------------------------------------- backward
+// Persistent blocks: a group walks rows at a stride of all groups, and each
+// thread keeps the parameter gradients of its own columns in registers over
+// all of them.  At the end a block adds its groups in order and writes one
+// partial row; reduce_kernel adds the blocks in order.
+template <typename TX, typename TY, int VEC, int K, bool LAYER>
+__global__ void __launch_bounds__(MAX_THREADS) bwd_kernel(NormBwd a) {
+  extern __shared__ float comb[];  // [groups][D], only with several groups
+  __shared__ float2 sm[2][MAX_THREADS / 32];
+  const int l = threadIdx.x, tpr = blockDim.x, groups = blockDim.y;
+  const int red = threadIdx.y * (tpr >> 5);
+  const float inv_d = 1.0f / static_cast<float>(a.D);
+  float aw[K][VEC], ab[K][VEC];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      aw[k][e] = 0.0f;
+      ab[k][e] = 0.0f;
+    }
+  }
+  int parity = 0;
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * groups; base < a.N;
+       base += static_cast<int64_t>(gridDim.x) * groups) {
+    const int64_t n = base + threadIdx.y;
+    const bool live = n < a.N;
+    const TX* x = static_cast<const TX*>(a.x) + (live ? a.xm.at(static_cast<int>(n)) : 0);
+    const TY* dy = static_cast<const TY*>(a.dy) + (live ? a.gm.at(static_cast<int>(n)) : 0);
+    Vec<TX, VEC> xv[K];
+    Vec<TY, VEC> gv[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (l + k * tpr) * VEC;
+      if (live && c < a.D) {
+        xv[k].load(x + c);
+        gv[k].load(dy + c);
+      } else {
+        xv[k].zero();
+        gv[k].zero();
+      }
+    }
+    const float rstd = live ? a.rstd[n] : 0.0f;
+    const float mean = LAYER && live ? a.mean[n] : 0.0f;
+    float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (l + k * tpr) * VEC;
+      if (c < a.D) {
+        float w[VEC];
+        load_gain<LAYER, VEC>(a.w, a.p_type, a.offset, c, w);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float z = (xv[k].get(e) - mean) * rstd;
+          const float d = gv[k].get(e);
+          const float g = d * w[e];
+          aw[k][e] += d * z;
+          if (LAYER) {
+            ab[k][e] += d;
+            s.x += g;
+          }
+          s.y += g * z;
+        }
+      }
+    }
+    if (a.dx) {
+      s = group_sum2(s, sm[parity] + red);
+      parity ^= 1;  // the other buffer next: a slower warp may still read this one
+      s.x *= inv_d;
+      s.y *= inv_d;
+      TX* dx = static_cast<TX*>(a.dx) + n * a.D;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int c = (l + k * tpr) * VEC;
+        if (live && c < a.D) {
+          float w[VEC], o[VEC];
+          load_gain<LAYER, VEC>(a.w, a.p_type, a.offset, c, w);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            const float z = (xv[k].get(e) - mean) * rstd;
+            o[e] = rstd * (gv[k].get(e) * w[e] - (s.x + z * s.y));
+          }
+          Vec<TX, VEC> out;
+          out.set(o);
+          out.store(dx + c);
+        }
+      }
+    }
+  }
+  for (int pass = 0; pass < (LAYER ? 2 : 1); ++pass) {
+    if (!(pass == 0 ? a.dw : a.db)) continue;
+    float* part = (pass == 0 ? a.part_w : a.part_b) + static_cast<int64_t>(blockIdx.x) * a.D;
+    if (groups > 1) __syncthreads();  // comb free again
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (l + k * tpr) * VEC;
+      if (c < a.D) {
+        float* to = groups > 1 ? comb + threadIdx.y * a.D + c : part + c;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) to[e] = pass == 0 ? aw[k][e] : ab[k][e];
+      }
+    }
+    if (groups > 1) {
+      __syncthreads();
+      for (int c = threadIdx.y * tpr + l; c < a.D; c += tpr * groups) {
+        float t = 0.0f;
+        for (int g = 0; g < groups; ++g) t += comb[g * a.D + c];
+        part[c] = t;
+      }
+    }
+  }
+}
+
+// Rows too long for the registers of one block: grad_x by one block per row in
+// two passes over it, the parameter gradients column-wise by cols_kernel.
+template <typename TX, typename TY, int VEC, bool LAYER>
+__global__ void __launch_bounds__(MAX_THREADS) bwd_long_kernel(NormBwd a) {
+  __shared__ float2 sm[MAX_THREADS / 32];
+  const int64_t n = blockIdx.x;
+  const TX* x = static_cast<const TX*>(a.x) + a.xm.at(static_cast<int>(n));
+  const TY* dy = static_cast<const TY*>(a.dy) + a.gm.at(static_cast<int>(n));
+  TX* dx = static_cast<TX*>(a.dx) + n * a.D;
+  const float inv_d = 1.0f / static_cast<float>(a.D);
+  const float rstd = a.rstd[n], mean = LAYER ? a.mean[n] : 0.0f;
+  const int64_t first = static_cast<int64_t>(threadIdx.x) * VEC, step = static_cast<int64_t>(blockDim.x) * VEC;
+  float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll 2
+  for (int64_t c = first; c < a.D; c += step) {
+    Vec<TX, VEC> xv;
+    Vec<TY, VEC> gv;
+    float w[VEC];
+    xv.load(x + c);
+    gv.load(dy + c);
+    load_gain<LAYER, VEC>(a.w, a.p_type, a.offset, c, w);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const float z = (xv.get(e) - mean) * rstd, g = gv.get(e) * w[e];
+      if (LAYER) s.x += g;
+      s.y += g * z;
+    }
+  }
+  s = group_sum2(s, sm);
+  s.x *= inv_d;
+  s.y *= inv_d;
+#pragma unroll 2
+  for (int64_t c = first; c < a.D; c += step) {
+    Vec<TX, VEC> xv;
+    Vec<TY, VEC> gv;
+    float w[VEC], o[VEC];
+    xv.load(x + c);
+    gv.load(dy + c);
+    load_gain<LAYER, VEC>(a.w, a.p_type, a.offset, c, w);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const float z = (xv.get(e) - mean) * rstd;
+      o[e] = rstd * (gv.get(e) * w[e] - (s.x + z * s.y));
+    }
+    Vec<TX, VEC> out;
+    out.set(o);
+    out.store(dx + c);
+  }
+}
+
+// Partial parameter gradients column-wise: a thread sums VEC columns over the
+// rows blockIdx.y, blockIdx.y + gridDim.y, ...
+template <typename TX, typename TY, int VEC, bool LAYER>
+__global__ void __launch_bounds__(128) cols_kernel(NormBwd a) {
+  const int64_t c = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) * VEC;
+  if (c >= a.D) return;
+  float aw[VEC], ab[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    aw[e] = 0.0f;
+    ab[e] = 0.0f;
+  }
+#pragma unroll 4
+  for (int64_t n = blockIdx.y; n < a.N; n += gridDim.y) {
+    Vec<TX, VEC> xv;
+    Vec<TY, VEC> gv;
+    xv.load(static_cast<const TX*>(a.x) + a.xm.at(static_cast<int>(n)) + c);
+    gv.load(static_cast<const TY*>(a.dy) + a.gm.at(static_cast<int>(n)) + c);
+    const float rstd = a.rstd[n], mean = LAYER ? a.mean[n] : 0.0f;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      aw[e] += gv.get(e) * ((xv.get(e) - mean) * rstd);
+      if (LAYER) ab[e] += gv.get(e);
+    }
+  }
+  const int64_t at = static_cast<int64_t>(blockIdx.y) * a.D + c;
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    if (a.dw) a.part_w[at + e] = aw[e];
+    if (LAYER && a.db) a.part_b[at + e] = ab[e];
+  }
+}
+
+// The parameter gradients from `parts` partial rows (0 parts: zeros).  A block
+// adds 32 columns: its warps take the parts w, w + 16, ... in order, and warp 0
+// adds the warps in order.  blockIdx.y = 0: the weight's, 1: the bias's.
+constexpr int REDUCE_WARPS = 16;
+inline __global__ void __launch_bounds__(32 * REDUCE_WARPS) reduce_kernel(const float* part_w, const float* part_b,
+                                                                          int parts, int D, int p_type, void* dw,
+                                                                          void* db) {
+  __shared__ float ws[REDUCE_WARPS][32];
+  void* out = blockIdx.y == 0 ? dw : db;
+  if (!out) return;
+  const float* part = blockIdx.y == 0 ? part_w : part_b;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
+  float s = 0.0f;
+  if (c < D) {
+#pragma unroll 4
+    for (int p = threadIdx.y; p < parts; p += REDUCE_WARPS) s += part[static_cast<int64_t>(p) * D + c];
+  }
+  ws[threadIdx.y][threadIdx.x] = s;
+  __syncthreads();
+  if (threadIdx.y == 0 && c < D) {
+    s = 0.0f;
+    for (int i = 0; i < REDUCE_WARPS; ++i) s += ws[i][threadIdx.x];
+    store_param(out, p_type, c, s);
+  }
+}
+
+// ------------------------------------------------------------------- launch
+inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Threads of a group that covers `vecs` vectors, K each.
+inline int group_threads(int64_t vecs, int K) {
+  const int64_t t = cdiv(vecs, K);
+  if (t > 32) return static_cast<int>(cdiv(t, 32) * 32);
+  int p = 1;
+  while (p < t) p *= 2;
+  return p;
+}
+
+template <typename TX, typename TY, int VEC, int K, bool LAYER>
+cudaError_t run_fwd(const NormFwd& a, int tpr, cudaStream_t s) {
+  const int groups = std::max(1, 256 / tpr);
+  const dim3 block(tpr, groups);
+  fwd_kernel<TX, TY, VEC, K, LAYER><<<static_cast<unsigned>(cdiv(a.N, groups)), block, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename TX, typename TY, int VEC, bool LAYER>
+cudaError_t fwd(const NormFwd& a, cudaStream_t s, int* launches) {
+  if (a.N == 0) return cudaSuccess;
+  ++*launches;
+  const int64_t vecs = cdiv(a.D, VEC);
+  if (vecs <= 128) return run_fwd<TX, TY, VEC, 1, LAYER>(a, group_threads(vecs, 1), s);
+  if (vecs <= 2 * MAX_THREADS) return run_fwd<TX, TY, VEC, 2, LAYER>(a, group_threads(vecs, 2), s);
+  if (vecs <= 4 * MAX_THREADS) return run_fwd<TX, TY, VEC, 4, LAYER>(a, group_threads(vecs, 4), s);
+  if (vecs <= 8 * MAX_THREADS) return run_fwd<TX, TY, VEC, 8, LAYER>(a, group_threads(vecs, 8), s);
+  fwd_long_kernel<TX, TY, VEC, LAYER><<<static_cast<unsigned>(a.N), MAX_THREADS, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename TX, typename TY, int VEC, int K, bool LAYER>
+cudaError_t run_bwd(const NormBwd& a, int tpr, int* parts, cudaStream_t s) {
+  const int groups = MAX_THREADS / tpr;
+  *parts = static_cast<int>(std::min<int64_t>(NORM_MAX_PARTS, cdiv(a.N, groups)));
+  const size_t smem = groups > 1 ? sizeof(float) * static_cast<size_t>(groups) * a.D : 0;
+  bwd_kernel<TX, TY, VEC, K, LAYER><<<*parts, dim3(tpr, groups), smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename TX, typename TY, int VEC, bool LAYER>
+cudaError_t bwd(const NormBwd& a, cudaStream_t s, int* launches) {
+  cudaError_t e = cudaSuccess;
+  int parts = 0;
+  if (a.N > 0 && (a.dx || a.dw || a.db)) {
+    ++*launches;
+    const int64_t vecs = cdiv(a.D, VEC);
+    constexpr int MOST = VEC == 1 ? 16 : 32 / VEC;  // vectors per thread whose sums fit in registers
+    if (vecs <= MAX_THREADS) {
+      e = run_bwd<TX, TY, VEC, 1, LAYER>(a, group_threads(vecs, 1), &parts, s);
+    } else if (vecs <= 2 * MAX_THREADS) {
+      e = run_bwd<TX, TY, VEC, 2, LAYER>(a, group_threads(vecs, 2), &parts, s);
+    } else if (MOST > 4 && vecs <= 4 * MAX_THREADS) {
+      e = run_bwd<TX, TY, VEC, 4, LAYER>(a, group_threads(vecs, 4), &parts, s);
+    } else if (vecs <= static_cast<int64_t>(MOST) * MAX_THREADS) {
+      e = run_bwd<TX, TY, VEC, MOST, LAYER>(a, group_threads(vecs, MOST), &parts, s);
+    } else {
+      if (a.dx) bwd_long_kernel<TX, TY, VEC, LAYER><<<static_cast<unsigned>(a.N), MAX_THREADS, 0, s>>>(a);
+      if (a.dw || a.db) {
+        const int64_t tiles = cdiv(vecs, 128);
+        parts = static_cast<int>(
+            std::min<int64_t>({NORM_MAX_PARTS, cdiv(a.N, 8), std::max<int64_t>(1, 1216 / tiles)}));
+        *launches += a.dx ? 1 : 0;
+        cols_kernel<TX, TY, VEC, LAYER>
+            <<<dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(parts)), 128, 0, s>>>(a);
+      }
+      e = cudaGetLastError();
+    }
+    if (e != cudaSuccess) return e;
+  }
+  if (a.dw || a.db) {
+    ++*launches;
+    reduce_kernel<<<dim3(static_cast<unsigned>(cdiv(a.D, 32)), LAYER ? 2 : 1), dim3(32, REDUCE_WARPS), 0, s>>>(
+        a.part_w, a.part_b, parts, a.D, a.p_type, a.dw, a.db);
+    e = cudaGetLastError();
+  }
+  return e;
+}
+
+template <typename TX, typename TY>
+cudaError_t fwd_any(const NormFwd& a, bool layer, bool wide, cudaStream_t s, int* launches) {
+  constexpr int VEC = 16 / sizeof(TX);
+  if (layer) return wide ? fwd<TX, TY, VEC, true>(a, s, launches) : fwd<TX, TY, 1, true>(a, s, launches);
+  return wide ? fwd<TX, TY, VEC, false>(a, s, launches) : fwd<TX, TY, 1, false>(a, s, launches);
+}
+
+template <typename TX, typename TY>
+cudaError_t bwd_any(const NormBwd& a, bool layer, bool wide, cudaStream_t s, int* launches) {
+  constexpr int VEC = 16 / sizeof(TX);
+  if (layer) return wide ? bwd<TX, TY, VEC, true>(a, s, launches) : bwd<TX, TY, 1, true>(a, s, launches);
+  return wide ? bwd<TX, TY, VEC, false>(a, s, launches) : bwd<TX, TY, 1, false>(a, s, launches);
+}
+
+}  // namespace norm
+}  // namespace cce

@@ -1,0 +1,66 @@
+// Layer norm and RMS norm: arguments of the kernels and their launchers, shared
+// by the entry points (ops_api.cu) and the per-type translation units.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+namespace cce {
+
+// Start of row n in elements: rows in runs of `inner` at row_stride, the runs
+// at outer_stride.
+struct RowMap {
+  int64_t row_stride, outer_stride;
+  int inner;
+
+  __device__ __forceinline__ int64_t at(int n) const {
+    if (n < inner) return n * row_stride;
+    const int o = n / inner;
+    return o * outer_stride + (n - o * inner) * row_stride;
+  }
+};
+
+struct NormFwd {
+  const void* x;
+  RowMap xm;
+  const void* w;  // may be null
+  const void* b;  // may be null
+  void* y;
+  float* mean;  // may be null
+  float* rstd;  // may be null
+  int p_type, N, D;
+  float eps, offset;
+};
+
+struct NormBwd {
+  const void* dy;
+  RowMap gm;
+  const void* x;
+  RowMap xm;
+  const void* w;  // may be null
+  const float* mean;
+  const float* rstd;
+  void* dx;       // may be null
+  void* dw;       // may be null
+  void* db;       // may be null
+  float* part_w;  // [parts][D]
+  float* part_b;  // [parts][D]
+  int p_type, N, D;
+  float offset;
+};
+
+// Blocks whose partial parameter gradients are added at the end, at most.
+constexpr int NORM_MAX_PARTS = 304;
+
+// y_type is what x_type allows (the entry points check); `layer` picks layer norm or RMS norm;
+// `wide` says that every pointer and stride allows 16-byte accesses of x.
+cudaError_t launch_norm_fwd_bf16(const NormFwd& a, bool layer, bool wide, cudaStream_t s, int* launches);
+cudaError_t launch_norm_fwd_f16(const NormFwd& a, bool layer, bool wide, cudaStream_t s, int* launches);
+cudaError_t launch_norm_fwd_f32(const NormFwd& a, int y_type, bool layer, bool wide, cudaStream_t s, int* launches);
+cudaError_t launch_norm_bwd_bf16(const NormBwd& a, bool layer, bool wide, cudaStream_t s, int* launches);
+cudaError_t launch_norm_bwd_f16(const NormBwd& a, bool layer, bool wide, cudaStream_t s, int* launches);
+cudaError_t launch_norm_bwd_f32(const NormBwd& a, int y_type, bool layer, bool wide, cudaStream_t s, int* launches);
+
+}  // namespace cce

@@ -1,0 +1,352 @@
+"""Layer norm and RMS norm on the GPU against the 64-bit formulas: every type
+and layout, sizes on both sides of each kernel's limits, strided rows, empty
+inputs, extreme values, streams and graphs."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import ops
+from tests import ops_util as U
+
+pytestmark = pytest.mark.gpu
+
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+PAIRS = [(BF16, BF16), (F16, F16), (F32, F32), (F32, BF16), (F32, F16)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def cce():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    from tests.conftest import build_library
+    build_library()
+    import linear_cross_entropy_gb300
+    return linear_cross_entropy_gb300
+
+
+def _randn(gen, *shape):
+    return torch.randn(shape, generator=gen, device="cuda")
+
+
+def _inputs(seed, shape, x_type, y_type, p_type, mean=0.2):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    D = shape[-1]
+    x = (_randn(gen, *shape) * torch.exp(0.5 * _randn(gen, D)) + mean).to(x_type)
+    w = (1 + 0.3 * _randn(gen, D)).to(p_type)
+    b = (0.3 * _randn(gen, D)).to(p_type)
+    return x, w, b, _randn(gen, *shape).to(y_type)
+
+
+def _check(cce, x, w, b, dy, layer, eps=1e-5, offset=0.0, out_dtype=None):
+    """Forward and direct backward against 64 bits."""
+    D = x.shape[-1]
+    xd = U.f64(x)
+    gain = (w.double().cpu().numpy() + (0.0 if layer else offset)) if w is not None else np.ones(D)
+    bias = b.double().cpu().numpy() if b is not None and layer else np.zeros(D)
+    mean, rstd = ops.norm_stats(xd, eps, layer)
+    if layer:
+        y, m, r = cce.cce_layer_norm_forward(x, w, b, eps, out_dtype=out_dtype)
+        U.within(m, mean, np.abs(xd).mean(axis=1), F32, "mean")
+    else:
+        y, r = cce.cce_rms_norm_forward(x, w, eps, weight_offset=offset, out_dtype=out_dtype)
+    assert y.shape == x.shape and y.is_contiguous() and y.dtype == (out_dtype or x.dtype)
+    U.within(y, ops.norm_forward(xd, gain, bias, mean, rstd), U.forward_magnitude(xd, gain, bias, mean, rstd), y.dtype,
+             "y")
+    if dy is None:
+        return
+    # the backward on the statistics that the forward gave, taken as they are
+    rd = r.double().cpu().numpy()
+    md = m.double().cpu().numpy() if layer else np.zeros(rd.shape)
+    if layer:
+        dx, dw, db = cce.cce_layer_norm_backward(dy, x, w, m, r, param_dtype=None if w is not None else F32)
+    else:
+        dx, dw = cce.cce_rms_norm_backward(dy, x, w, r, weight_offset=offset)
+        assert (dw is None) == (w is None)
+    gd = U.f64(dy)
+    ex, ew, eb = ops.norm_backward(gd, xd, gain, md, rd, layer)
+    mx, mw, mb = U.backward_magnitudes(gd, xd, gain, md, rd, layer)
+    assert dx.shape == x.shape and dx.dtype == x.dtype
+    U.within(dx, ex, mx, dx.dtype, "dx")
+    if dw is not None:
+        U.within(dw, ew, mw, dw.dtype, "dw")
+    if layer:
+        U.within(db, eb, mb, db.dtype, "db")
+
+
+@pytest.mark.parametrize("layer", [True, False])
+@pytest.mark.parametrize("N,D", [(1, 1), (1, 8), (3, 5), (1, 896), (2, 64), (33, 63), (5, 128), (1000, 128), (17, 256),
+                                 (700, 1001), (33, 1024), (257, 2304), (1, 4096), (40, 4096), (9, 4097), (19, 6152),
+                                 (3, 8200), (5, 8191), (4, 16384), (5, 16392), (3, 20001), (2, 33000), (1, 70000)])
+def test_sizes(cce, layer, N, D):
+    x, w, b, dy = _inputs(N * 7919 + D, (N, D), BF16, BF16, BF16)
+    _check(cce, x, w, b, dy, layer)
+
+
+@pytest.mark.parametrize("layer", [True, False])
+@pytest.mark.parametrize("x_type,y_type", PAIRS)
+@pytest.mark.parametrize("p_type", [BF16, F16, F32])
+@pytest.mark.parametrize("D", [40, 333, 1000, 2052, 5000, 9000, 17000])
+def test_types(cce, layer, x_type, y_type, p_type, D):
+    x, w, b, dy = _inputs(D, (21, D), x_type, y_type, p_type)
+    _check(cce, x, w, b, dy, layer, out_dtype=y_type)
+
+
+@pytest.mark.parametrize("N,D", [(5000, 64), (3001, 896), (20000, 130), (4099, 2304)])
+def test_many_rows(cce, N, D):
+    for layer in (True, False):
+        x, w, b, dy = _inputs(N, (N, D), BF16, BF16, F32)
+        _check(cce, x, w, b, dy, layer)
+
+
+def test_weight_offset_and_missing_parameters(cce):
+    x, w, b, dy = _inputs(5, (37, 520), BF16, BF16, BF16)
+    _check(cce, x, w - 1, None, dy, False, offset=1.0)
+    _check(cce, x, None, None, dy, True)
+    _check(cce, x, None, b, dy, True)
+    _check(cce, x, w, None, dy, True)
+    _check(cce, x, None, None, dy, False, offset=1.0)
+
+
+@pytest.mark.parametrize("layer", [True, False])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_strided_rows(cce, layer, dtype):
+    """Rows of views: shifted sequences, column slices on and off 16-byte
+    boundaries, every other row, transposed leading dimensions, expanded rows."""
+    x, w, b, dy = _inputs(11, (4, 9, 640), dtype, dtype, dtype)
+    cuts = [lambda t: t[:, :-1], lambda t: t[:, 1:], lambda t: t[..., :320], lambda t: t[..., 8:328],
+            lambda t: t[..., 3:323], lambda t: t[:, ::2, 1:301], lambda t: t.transpose(0, 1), lambda t: t[0, 0],
+            lambda t: t[..., ::2], lambda t: t[1:2, :5].expand(3, 5, 640)]
+    for cut in cuts:
+        xv, gv = cut(x), cut(dy)
+        D = xv.shape[-1]
+        _check(cce, xv, w[:D].contiguous(), b[:D].contiguous(), gv, layer)
+        _check(cce, xv, w[:D].contiguous(), b[:D].contiguous(), gv.contiguous(), layer)
+
+
+def test_parameters_off_their_alignment(cce):
+    x, w, b, dy = _inputs(12, (19, 65), BF16, BF16, BF16)
+    _check(cce, x[:, 1:].contiguous(), w[1:], b[1:], dy[:, 1:].contiguous(), True)
+    _check(cce, x[:, 1:].contiguous(), w[1:], None, dy[:, 1:].contiguous(), False)
+
+
+def test_no_rows(cce):
+    w = torch.ones(48, device="cuda", dtype=BF16)
+    x = torch.empty(0, 48, device="cuda", dtype=BF16)
+    y, m, r = cce.cce_layer_norm_forward(x, w, w)
+    assert y.shape == (0, 48) and m.numel() == 0
+    dx, dw, db = cce.cce_layer_norm_backward(x, x, w, m, r)
+    assert dx.shape == (0, 48) and not dw.any() and not db.any()
+    y, r = cce.cce_rms_norm_forward(x.view(3, 0, 48), w)
+    assert y.shape == (3, 0, 48)
+    dx, dw = cce.cce_rms_norm_backward(x, x, w, r)
+    assert not dw.any()
+
+
+def test_only_what_is_needed(cce):
+    x, w, b, dy = _inputs(13, (50, 264), BF16, BF16, F32)
+    y, m, r = cce.cce_layer_norm_forward(x, w, b)
+    full = cce.cce_layer_norm_backward(dy, x, w, m, r)
+    for need in [(True, False, False), (False, True, False), (False, False, True), (True, True, False),
+                 (False, True, True)]:
+        part = cce.cce_layer_norm_backward(dy, x, w, m, r, need_dx=need[0], need_dweight=need[1], need_dbias=need[2])
+        for want, p, f in zip(need, part, full):
+            assert torch.equal(p, f) if want else p is None
+    y2, m2, r2 = cce.cce_layer_norm_forward(x, w, b, stats=False)
+    assert torch.equal(y, y2) and m2 is None and r2 is None
+
+
+def test_mean_far_from_zero_does_not_cancel(cce):
+    """Rows around 1000 with deviations around 1: sums of squares would leave
+    nothing of the variance in fp32; the squared deviations keep it."""
+    for D in (100, 896, 4096, 30000):
+        x, w, b, dy = _inputs(D, (6, D), F32, F32, F32, mean=1000.0)
+        _check(cce, x, w, b, dy, True)
+
+
+def test_constant_and_zero_rows(cce):
+    x = torch.zeros(4, 136, device="cuda", dtype=F32)
+    x[1] = 7.0
+    x[2] = -2.5
+    w = torch.full((136,), 2.0, device="cuda")
+    b = torch.full((136,), 0.5, device="cuda")
+    y, m, r = cce.cce_layer_norm_forward(x, w, b, 1e-5)
+    assert torch.equal(y, torch.full_like(y, 0.5)) and m.tolist() == [0.0, 7.0, -2.5, 0.0]
+    dx, dw, db = cce.cce_layer_norm_backward(torch.ones_like(x), x, w, m, r)
+    assert torch.isfinite(dx).all() and not dw.any() and torch.equal(db, torch.full_like(db, 4.0))
+    y, r = cce.cce_rms_norm_forward(x[:1], w, 1e-6)
+    assert not y.any()
+
+
+def test_a_bad_row_stays_its_own(cce):
+    """NaN and infinities spoil their row and the parameters' gradients, no other row."""
+    x, w, b, dy = _inputs(17, (40, 200), BF16, BF16, BF16)
+    good = cce.cce_layer_norm_forward(x, w, b)
+    gdx = cce.cce_layer_norm_backward(dy, x, w, *good[1:])[0]
+    x2 = x.clone()
+    x2[3, 5], x2[9, 0], x2[39, 199] = float("nan"), float("inf"), float("-inf")
+    y, m, r = cce.cce_layer_norm_forward(x2, w, b)
+    dx, dw, _ = cce.cce_layer_norm_backward(dy, x2, w, m, r)
+    for n in range(40):
+        if n in (3, 9, 39):
+            assert torch.isnan(y[n]).any() and torch.isnan(dx[n]).any()
+        else:
+            assert torch.equal(y[n], good[0][n]) and torch.equal(dx[n], gdx[n])
+    assert torch.isnan(dw).all()
+
+
+@pytest.mark.parametrize("layer", [True, False])
+def test_autograd_matches_the_direct_calls(cce, layer):
+    x, w, b, dy = _inputs(19, (3, 11, 328), BF16, BF16, F32)
+    leaves = [t.clone().requires_grad_() for t in ((x, w, b) if layer else (x, w))]
+    y = cce.layer_norm(*leaves) if layer else cce.rms_norm(*leaves, weight_offset=0.5)
+    y.backward(dy)
+    if layer:
+        y0, m, r = cce.cce_layer_norm_forward(x, w, b)
+        want = cce.cce_layer_norm_backward(dy, x, w, m, r)
+    else:
+        y0, r = cce.cce_rms_norm_forward(x, w, weight_offset=0.5)
+        want = cce.cce_rms_norm_backward(dy, x, w, r, weight_offset=0.5)
+    assert torch.equal(y, y0)
+    for leaf, g in zip(leaves, want):
+        assert torch.equal(leaf.grad, g) and leaf.grad.dtype == leaf.dtype
+    # an expanded upstream gradient, some leaves frozen
+    leaves = [t.clone() for t in ((x, w, b) if layer else (x, w))]
+    leaves[1].requires_grad_()
+    y = cce.layer_norm(*leaves) if layer else cce.rms_norm(*leaves)
+    y.float().sum().backward()
+    assert leaves[0].grad is None and leaves[1].grad is not None
+    with torch.no_grad():
+        assert not (cce.layer_norm(*leaves) if layer else cce.rms_norm(*leaves)).requires_grad
+    # a bias that trains alone
+    if layer:
+        b2 = b.clone().requires_grad_()
+        cce.layer_norm(x, None, b2).backward(dy)
+        U.within(b2.grad, U.f64(dy).sum(axis=0), np.abs(U.f64(dy)).sum(axis=0), F32, "db")
+
+
+def test_no_second_derivative(cce):
+    x, w, b, dy = _inputs(23, (4, 64), F32, F32, F32)
+    x.requires_grad_()
+    (g,) = torch.autograd.grad(cce.layer_norm(x, w, b), x, dy, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()
+
+
+@pytest.mark.parametrize("layer", [True, False])
+def test_gradient_against_differences_of_the_kernel(cce, layer):
+    """The derivative along a direction from two forward calls.  The two-sided
+    difference of step h is off by its truncation, which the 64-bit formula
+    gives, and by the roundings of y over 2h."""
+    N, D, h, eps = 6, 200, 2.0 ** -5, 1e-5
+    x, w, b, dy = _inputs(29, (N, D), F32, F32, F32)
+    v = torch.randn(N, D, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    lo, hi = x - h * v, x + h * v  # as rounded; the true direction is (hi - lo) / 2h
+    c = U.f64(dy)
+
+    def f(t):
+        y = cce.layer_norm(t, w, b, eps) if layer else cce.rms_norm(t, w, eps)
+        return float((U.f64(y) * c).sum())
+
+    gain = w.double().cpu().numpy()
+    bias = b.double().cpu().numpy() if layer else np.zeros(D)
+
+    def exact(t):
+        t = U.f64(t)
+        return float((ops.norm_forward(t, gain, bias, *ops.norm_stats(t, eps, layer)) * c).sum())
+
+    xd = U.f64(x)
+    mean, rstd = ops.norm_stats(xd, eps, layer)
+    ex, _, _ = ops.norm_backward(c, xd, gain, mean, rstd, layer)
+    direction = (U.f64(hi) - U.f64(lo)) / (2 * h)
+    truncation = abs((exact(hi) - exact(lo)) / (2 * h) - float((ex * direction).sum()))
+    rounding = sum(float((np.abs(c) * U.U32 * U.forward_magnitude(U.f64(t), gain, bias,
+                                                                  *ops.norm_stats(U.f64(t), eps, layer))).sum())
+                   for t in (lo, hi)) / (2 * h)
+    x.requires_grad_()
+    y = cce.layer_norm(x, w, b, eps) if layer else cce.rms_norm(x, w, eps)
+    (dx,) = torch.autograd.grad(y, x, dy)
+    slope = float((U.f64(dx) * direction).sum())
+    own = float((U.U32 * U.backward_magnitudes(c, xd, gain, mean, rstd, layer)[0] * np.abs(direction)).sum())
+    assert abs((f(hi) - f(lo)) / (2 * h) - slope) <= truncation + rounding + own
+
+
+def test_repeated_calls_are_bitwise_equal(cce):
+    x, w, b, dy = _inputs(31, (3000, 896), BF16, BF16, F32)
+    first = None
+    for _ in range(3):
+        y, m, r = cce.cce_layer_norm_forward(x, w, b)
+        got = (y, m, r) + cce.cce_layer_norm_backward(dy, x, w, m, r)
+        first = first or got
+        assert all(torch.equal(a, b) for a, b in zip(got, first))
+
+
+def test_on_another_stream(cce):
+    x, w, b, dy = _inputs(37, (513, 1024), BF16, BF16, BF16)
+    want = cce.cce_layer_norm_forward(x, w, b)
+    dwant = cce.cce_layer_norm_backward(dy, x, w, *want[1:])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = cce.cce_layer_norm_forward(x, w, b)
+        dgot = cce.cce_layer_norm_backward(dy, x, w, *got[1:])
+    got2 = cce.cce_rms_norm_forward(x, w, stream=s)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want + dwant, got + dgot))
+    assert torch.equal(got2[0], cce.cce_rms_norm_forward(x, w)[0])
+
+
+def test_captured_into_a_graph(cce):
+    """Forward and backward in one graph, replayed on new values, while an
+    eager graph of other leaves is alive."""
+    x, w, b, dy = _inputs(41, (300, 2304), BF16, BF16, BF16)
+    alive = cce.layer_norm(x.clone().requires_grad_(), w, b)
+    cce.cce_layer_norm_backward(dy, x, w, *cce.cce_layer_norm_forward(x, w, b)[1:])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, m, r = cce.cce_layer_norm_forward(x, w, b)
+        dx, dw, db = cce.cce_layer_norm_backward(dy, x, w, m, r)
+    x.copy_(_inputs(42, (300, 2304), BF16, BF16, BF16)[0])
+    graph.replay()
+    want = cce.cce_layer_norm_forward(x, w, b)
+    dwant = cce.cce_layer_norm_backward(dy, x, w, *want[1:])
+    assert all(torch.equal(a, b) for a, b in zip((y, m, r, dx, dw, db), want + dwant))
+    assert alive.requires_grad
+
+
+def test_rows_past_two_to_the_31_elements(cce):
+    """Offsets need 64 bits: the last rows of a 2.3-billion-element input."""
+    N, D = 70001, 32768
+    x = torch.empty(N, D, device="cuda", dtype=BF16)
+    for i in range(0, N, 10000):
+        x[i:i + 10000].normal_()
+    w = torch.full((D,), 1.5, device="cuda", dtype=BF16)
+    y, r = cce.cce_rms_norm_forward(x, w)
+    dx, _ = cce.cce_rms_norm_backward(y, x, w, r, need_dweight=False)
+    for rows in (slice(0, 3), slice(65535, 65538), slice(N - 3, N)):
+        ys, rs = cce.cce_rms_norm_forward(x[rows].clone(), w)
+        assert torch.equal(y[rows], ys) and torch.equal(r[rows], rs)
+        assert torch.equal(dx[rows], cce.cce_rms_norm_backward(ys, x[rows].clone(), w, rs, need_dweight=False)[0])
+
+
+def test_refusals_on_the_gpu(cce):
+    x, w, b, dy = _inputs(43, (4, 64), BF16, BF16, BF16)
+    y, m, r = cce.cce_layer_norm_forward(x, w, b)
+    bad = [lambda: cce.layer_norm(x.double(), w), lambda: cce.layer_norm(x, w[:32]), lambda: cce.layer_norm(x, w.cpu()),
+           lambda: cce.layer_norm(x, w, b.float()), lambda: cce.layer_norm(x, w.double()),
+           lambda: cce.layer_norm(x, w, out_dtype=F32), lambda: cce.layer_norm(x, w, out_dtype=F16),
+           lambda: cce.rms_norm(x.long(), w), lambda: cce.rms_norm(x, w.view(1, 64)),
+           lambda: cce.rms_norm(x, w.expand(2, 64)[:, 0]), lambda: cce.rms_norm(x[:, :0]),
+           lambda: cce.rms_norm(torch.zeros((), device="cuda")),
+           lambda: cce.cce_layer_norm_backward(dy.float(), x, w, m, r),
+           lambda: cce.cce_layer_norm_backward(dy[:2], x, w, m, r),
+           lambda: cce.cce_layer_norm_backward(dy, x, w, m[:2], r),
+           lambda: cce.cce_layer_norm_backward(dy, x, w, m, r.half()),
+           lambda: cce.cce_rms_norm_backward(dy.cpu(), x, w, r)]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(cce.CCEError):
+        cce.layer_norm(x, w, b, eps=-1.0)
+    with pytest.raises(cce.CCEError):
+        cce.rms_norm(x, w, weight_offset=float("nan"))
