@@ -94,6 +94,55 @@ cce_status cce_rms_norm_backward(const void* grad_y, int64_t g_inner, int64_t g_
  * sizes).  Pure host arithmetic; needs no GPU. */
 size_t cce_norm_backward_workspace_bytes(int64_t N, int64_t D);
 
+/*
+ * Global gradient norm and clipping over any number of tensors.
+ *
+ * Tensors come as two host arrays, read during the call:
+ *   dense    [n_dense][4] int64: {input pointer, output pointer, number of
+ *            elements (0 is skipped), input type + 256 * output type}.  Input
+ *            and output are contiguous blocks of memory in the same order.
+ *   strided  n_strided descriptors of tensors whose elements are not one block.
+ * Outputs are read by cce_clip_grads only.  An output is the input itself (in
+ * place, same type) or memory that overlaps no other input or output: dense
+ * blocks that do overlap return CCE_ERR_ARG.
+ */
+typedef struct {
+  const void* in;
+  void* out;
+  int32_t in_type, out_type;
+  int64_t size[4];       /* dimensions, 1 where there are fewer; the last varies fastest */
+  int64_t in_stride[4];  /* in elements, >= 0 */
+  int64_t out_stride[4]; /* in elements, >= 0 */
+} cce_strided;
+
+#define CCE_NORM_INF 0
+#define CCE_NORM_2 2
+
+/*
+ * *norm (fp32, device, written) = sqrt(sum x^2) (CCE_NORM_2) or max |x|
+ * (CCE_NORM_INF) over all elements; 0 without any.  Squares that leave fp32's
+ * range are summed in fp64, so the norm is right wherever fp32 can hold it; an
+ * infinity or NaN among the elements gives infinity or NaN.
+ */
+cce_status cce_grad_norm(const int64_t* dense /* host */, int64_t n_dense, const cce_strided* strided /* host */,
+                         int64_t n_strided, int norm_type, float* norm, void* workspace, size_t ws_bytes,
+                         void* stream);
+
+/*
+ * The norm as above, then output = input * min(1, max_norm / (norm + eps)),
+ * rounded once to the output's type.  A factor of 1 leaves tensors that are
+ * clipped in place untouched.  An infinite norm gives factor 0, a NaN gives
+ * NaN.  max_norm >= 0 (infinity: never clip) and a finite eps >= 0, else
+ * CCE_ERR_ARG.
+ */
+cce_status cce_clip_grads(const int64_t* dense /* host */, int64_t n_dense, const cce_strided* strided /* host */,
+                          int64_t n_strided, int norm_type, float max_norm, float eps, float* norm, void* workspace,
+                          size_t ws_bytes, void* stream);
+
+/* Bytes of workspace for that many tensors (0 for negative counts).  Pure
+ * host arithmetic; needs no GPU. */
+size_t cce_grad_norm_workspace_bytes(int64_t n_dense, int64_t n_strided);
+
 #ifdef __cplusplus
 }
 #endif

@@ -33,11 +33,13 @@ __all__ = [
     "Profiler", "vocab_logit_sums", "vocab_order", "cce_loss_and_grad", "fused_linear_cross_entropy",
     "loss_and_grad_workspace_bytes", "raise_pending_errors",
     "layer_norm", "rms_norm", "cce_layer_norm_forward", "cce_layer_norm_backward", "cce_rms_norm_forward",
-    "cce_rms_norm_backward", "norm_backward_workspace_bytes",
+    "cce_rms_norm_backward", "norm_backward_workspace_bytes", "clip_grad_norm_", "cce_clip_grads", "cce_grad_norm",
+    "grad_norm_workspace_bytes",
 ]
 
 _lib.load()
 
+from .grads import cce_clip_grads, cce_grad_norm, clip_grad_norm_, grad_norm_workspace_bytes  # noqa: E402
 from .norm import (cce_layer_norm_backward, cce_layer_norm_forward, cce_rms_norm_backward,  # noqa: E402
                    cce_rms_norm_forward, layer_norm, norm_backward_workspace_bytes, rms_norm)
 

@@ -46,6 +46,13 @@ class MemoryReport(ctypes.Structure):
     ]
 
 
+class Strided(ctypes.Structure):
+    """cce_strided of include/cce_ops.h."""
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("in_type", ctypes.c_int32),
+                ("out_type", ctypes.c_int32), ("size", ctypes.c_int64 * 4), ("in_stride", ctypes.c_int64 * 4),
+                ("out_stride", ctypes.c_int64 * 4)]
+
+
 _lib = None
 
 
@@ -144,6 +151,12 @@ def load() -> ctypes.CDLL:
     lib.cce_rms_norm_backward.restype = ci
     lib.cce_norm_backward_workspace_bytes.argtypes = [i64, i64]
     lib.cce_norm_backward_workspace_bytes.restype = sz
+    lib.cce_grad_norm.argtypes = [vp, i64, vp, i64, ci, vp, vp, sz, vp]
+    lib.cce_grad_norm.restype = ci
+    lib.cce_clip_grads.argtypes = [vp, i64, vp, i64, ci, cf, cf, vp, vp, sz, vp]
+    lib.cce_clip_grads.restype = ci
+    lib.cce_grad_norm_workspace_bytes.argtypes = [i64, i64]
+    lib.cce_grad_norm_workspace_bytes.restype = sz
     _lib = lib
     return lib
 

@@ -23,7 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libcce.so")
 SOURCES = ("cce_api.cu", "gemm_kernels.cu", "cce_noalloc.cu", "cce_sort.cu", "cce_flce.cu", "norm_api.cu",
-           "norm_bf16.cu", "norm_f16.cu", "norm_f32.cu")
+           "norm_bf16.cu", "norm_f16.cu", "norm_f32.cu", "grad_clip.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -40,25 +40,31 @@ struct Vec {
 #pragma unroll
     for (int i = 0; i < WORDS; ++i) w[i] = 0u;
   }
+  // From memory that nothing writes while the kernel runs.
   __device__ __forceinline__ void load(const T* p) {
     if constexpr (BYTES >= 16) {
 #pragma unroll
-      for (int i = 0; i < BYTES / 16; ++i) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
-        w[4 * i] = v.x;
-        w[4 * i + 1] = v.y;
-        w[4 * i + 2] = v.z;
-        w[4 * i + 3] = v.w;
-      }
+      for (int i = 0; i < BYTES / 16; ++i) words4(i, __ldg(reinterpret_cast<const uint4*>(p) + i));
     } else if constexpr (BYTES == 8) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-      w[0] = v.x;
-      w[1] = v.y;
+      words2(__ldg(reinterpret_cast<const uint2*>(p)));
     } else if constexpr (BYTES == 4) {
       w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
     } else {
       static_assert(BYTES == 2, "one 16-bit element");
       w[0] = __ldg(reinterpret_cast<const uint16_t*>(p));
+    }
+  }
+  // From memory that the kernel itself writes.
+  __device__ __forceinline__ void load_written(const T* p) {
+    if constexpr (BYTES >= 16) {
+#pragma unroll
+      for (int i = 0; i < BYTES / 16; ++i) words4(i, reinterpret_cast<const uint4*>(p)[i]);
+    } else if constexpr (BYTES == 8) {
+      words2(*reinterpret_cast<const uint2*>(p));
+    } else if constexpr (BYTES == 4) {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else {
+      w[0] = *reinterpret_cast<const uint16_t*>(p);
     }
   }
   __device__ __forceinline__ void store(T* p) const {
@@ -108,6 +114,16 @@ struct Vec {
   }
 
  private:
+  __device__ __forceinline__ void words4(int i, const uint4& v) {
+    w[4 * i] = v.x;
+    w[4 * i + 1] = v.y;
+    w[4 * i + 2] = v.z;
+    w[4 * i + 3] = v.w;
+  }
+  __device__ __forceinline__ void words2(const uint2& v) {
+    w[0] = v.x;
+    w[1] = v.y;
+  }
   __device__ __forceinline__ static uint32_t half_bits(float f) {
     if constexpr (ElemType<T>::id == CCE_BF16) {
       return __bfloat16_as_ushort(__float2bfloat16_rn(f));
