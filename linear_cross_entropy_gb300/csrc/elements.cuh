@@ -133,6 +133,43 @@ struct Vec {
   }
 };
 
+// Two fp32 values in a register pair, for the packed fp32 instructions (one issue slot for two results).
+struct Pair {
+  unsigned long long v;
+
+  __device__ __forceinline__ static Pair of(float lo, float hi) {
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(lo), "f"(hi));
+    return p;
+  }
+  __device__ __forceinline__ static Pair both(float f) { return of(f, f); }
+  __device__ __forceinline__ float2 get() const {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+  }
+  __device__ __forceinline__ float sum() const {
+    const float2 f = get();
+    return f.x + f.y;
+  }
+};
+
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  Pair r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Pair mul(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
 // VEC parameters of a run-time type as fp32 (the type is uniform over a launch).
 template <int VEC>
 __device__ __forceinline__ void load_param(const void* p, int type, int64_t i, float (&out)[VEC]) {

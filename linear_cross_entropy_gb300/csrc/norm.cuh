@@ -80,25 +80,85 @@ __device__ __forceinline__ void load_gain(const void* w, int p_type, float offse
   }
 }
 
+template <bool LAYER, int VEC>
+__device__ __forceinline__ void load_bias(const void* b, int p_type, int64_t c, float (&f)[VEC]) {
+  if (LAYER && b) {
+    load_param<VEC>(b, p_type, c, f);
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) f[e] = 0.0f;
+  }
+}
+
+// The K vectors of a thread as fp32 pairs, E = K * VEC / 2 of them.  With VEC = 1 a
+// pair is two of the thread's columns.
+template <typename T, int VEC, int K>
+__device__ __forceinline__ void unpack(const Vec<T, VEC> (&v)[K], Pair (&p)[K * VEC / 2]) {
+#pragma unroll
+  for (int i = 0; i < K * VEC / 2; ++i) {
+    p[i] = Pair::of(v[2 * i / VEC].get(2 * i % VEC), v[(2 * i + 1) / VEC].get((2 * i + 1) % VEC));
+  }
+}
+
+// Whether a thread holds its vector k.  Every thread holds the first KF, so
+// that only the others are checked.
+template <int KF>
+__device__ __forceinline__ bool holds(int k, int vecs) {
+  return k < KF || static_cast<int>(threadIdx.x + k * blockDim.x) < vecs;
+}
+
+// Parameters in shared memory as fp32.  The vectors' float4 quarters lie apart,
+// so that a warp's 16-byte reads fall on consecutive addresses.
+template <int VEC>
+__device__ __forceinline__ void put_param(float* sm, int vecs, int c, const float (&f)[VEC]) {
+  if constexpr (VEC == 1) {
+    sm[c] = f[0];
+  } else {
+#pragma unroll
+    for (int h = 0; h < VEC / 4; ++h)
+      reinterpret_cast<float4*>(sm)[h * vecs + c] = make_float4(f[4 * h], f[4 * h + 1], f[4 * h + 2], f[4 * h + 3]);
+  }
+}
+
+template <int VEC>
+__device__ __forceinline__ void get_param(const float* sm, int vecs, int c, float (&f)[VEC]) {
+  if constexpr (VEC == 1) {
+    f[0] = sm[c];
+  } else {
+#pragma unroll
+    for (int h = 0; h < VEC / 4; ++h) {
+      const float4 v = reinterpret_cast<const float4*>(sm)[h * vecs + c];
+      f[4 * h] = v.x;
+      f[4 * h + 1] = v.y;
+      f[4 * h + 2] = v.z;
+      f[4 * h + 3] = v.w;
+    }
+  }
+}
+
 // ------------------------------------------------------------------ forward
-// One row per group, one pass over memory.
+// Few rows: a block of up to 512 threads per row, so that a row's loads are all
+// in flight at once; parameters are loaded beside them.
 template <typename TX, typename TY, int VEC, int K, bool LAYER>
-__global__ void __launch_bounds__(MAX_THREADS) fwd_kernel(NormFwd a) {
+__global__ void __launch_bounds__(MAX_THREADS) fwd_few_kernel(NormFwd a) {
   __shared__ float sm[2][MAX_THREADS / 32];
   const int l = threadIdx.x, tpr = blockDim.x;
-  float* sm0 = sm[0] + threadIdx.y * (tpr >> 5);
-  float* sm1 = sm[1] + threadIdx.y * (tpr >> 5);
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
-  const bool live = n < a.N;  // a group without a row still takes part in its warp's shuffles
-  const TX* x = static_cast<const TX*>(a.x) + (live ? a.xm.at(static_cast<int>(n)) : 0);
+  const int64_t n = blockIdx.x;
+  const TX* x = static_cast<const TX*>(a.x) + a.xm.at(static_cast<int>(n));
   Vec<TX, VEC> xv[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int c = (l + k * tpr) * VEC;
-    if (live && c < a.D) {
-      xv[k].load(x + c);
-    } else {
-      xv[k].zero();
+    xv[k].zero();
+    if (c < a.D) xv[k].load(x + c);
+  }
+  float w[K][VEC], b[K][VEC];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = (l + k * tpr) * VEC;
+    if (c < a.D) {
+      load_gain<LAYER, VEC>(a.w, a.p_type, a.offset, c, w[k]);
+      load_bias<LAYER, VEC>(a.b, a.p_type, c, b[k]);
     }
   }
   const float fd = static_cast<float>(a.D);
@@ -110,7 +170,7 @@ __global__ void __launch_bounds__(MAX_THREADS) fwd_kernel(NormFwd a) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) s += xv[k].get(e);
     }
-    mean = group_sum(s, sm0) / fd;
+    mean = group_sum(s, sm[0]) / fd;
   }
   float q = 0.0f;
 #pragma unroll
@@ -123,8 +183,7 @@ __global__ void __launch_bounds__(MAX_THREADS) fwd_kernel(NormFwd a) {
       }
     }
   }
-  const float rstd = 1.0f / sqrtf(group_sum(q, sm1) / fd + a.eps);
-  if (!live) return;
+  const float rstd = 1.0f / sqrtf(group_sum(q, sm[1]) / fd + a.eps);
   if (l == 0) {
     if (LAYER && a.mean) a.mean[n] = mean;
     if (a.rstd) a.rstd[n] = rstd;
@@ -134,19 +193,117 @@ __global__ void __launch_bounds__(MAX_THREADS) fwd_kernel(NormFwd a) {
   for (int k = 0; k < K; ++k) {
     const int c = (l + k * tpr) * VEC;
     if (c < a.D) {
-      float w[VEC], b[VEC], o[VEC];
-      load_gain<LAYER, VEC>(a.w, a.p_type, a.offset, c, w);
-      if (LAYER && a.b) {
-        load_param<VEC>(a.b, a.p_type, c, b);
-      } else {
+      float o[VEC];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) b[e] = 0.0f;
-      }
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) o[e] = (xv[k].get(e) - mean) * rstd * w[e] + b[e];
+      for (int e = 0; e < VEC; ++e) o[e] = (xv[k].get(e) - mean) * rstd * w[k][e] + b[k][e];
       Vec<TY, VEC> out;
       out.set(o);
       out.store(y + c);
+    }
+  }
+}
+
+// Many rows: persistent blocks whose groups walk rows at a stride of all groups.
+// A thread holds up to 64 values of a row, so that most rows are a warp's or
+// less and their sums are shuffles alone; the next row is loaded while this one
+// is reduced.  The parameters wait in shared memory as fp32.
+template <typename TX, typename TY, int VEC, int K, int KF, bool LAYER>
+__global__ void __launch_bounds__(MAX_THREADS) fwd_kernel(NormFwd a) {
+  constexpr int E = K * VEC / 2;
+  extern __shared__ __align__(16) float params[];  // gain [D], then the bias [D] of a layer norm
+  __shared__ float sm[4][MAX_THREADS / 32];
+  const int l = threadIdx.x, tpr = blockDim.x, groups = blockDim.y;
+  const int vecs = a.D / VEC, slot = threadIdx.y * (tpr >> 5);
+  float* gain = params;
+  float* bias = params + a.D;
+  const int step = gridDim.x * groups;
+  Vec<TX, VEC> xv[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) xv[k].zero();
+  auto load_row = [&](int64_t n) {
+    if (n >= a.N) return;
+    const TX* x = static_cast<const TX*>(a.x) + a.xm.at(static_cast<int>(n));
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (holds<KF>(k, vecs)) xv[k].load(x + (l + k * tpr) * VEC);
+    }
+  };
+  int64_t base = static_cast<int64_t>(blockIdx.x) * groups;
+  load_row(base + threadIdx.y);
+  for (int c = threadIdx.y * tpr + l; c < vecs; c += tpr * groups) {
+    float f[VEC];
+    load_gain<LAYER, VEC>(a.w, a.p_type, a.offset, static_cast<int64_t>(c) * VEC, f);
+    put_param<VEC>(gain, vecs, c, f);
+    if (LAYER) {
+      load_bias<LAYER, VEC>(a.b, a.p_type, static_cast<int64_t>(c) * VEC, f);
+      put_param<VEC>(bias, vecs, c, f);
+    }
+  }
+  __syncthreads();
+  const float fd = static_cast<float>(a.D);
+  int buf = 0;
+  for (; base < a.N; base += step) {
+    const int64_t n = base + threadIdx.y;
+    Pair d[E];
+    unpack<TX, VEC, K>(xv, d);
+    load_row(n + step);
+    float mean = 0.0f;
+    if (LAYER) {
+      Pair s[2] = {Pair::both(0.0f), Pair::both(0.0f)};  // two chains
+#pragma unroll
+      for (int i = 0; i < E; ++i) s[i & 1] = add(s[i & 1], d[i]);
+      mean = group_sum(add(s[0], s[1]).sum(), sm[buf] + slot) / fd;
+      const Pair minus = Pair::both(-mean);
+#pragma unroll
+      for (int i = 0; i < E; ++i) d[i] = add(d[i], minus);
+    }
+    Pair q[2] = {Pair::both(0.0f), Pair::both(0.0f)};
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int k0 = 2 * i / VEC, k1 = (2 * i + 1) / VEC;
+      if constexpr (LAYER && VEC == 1) {  // columns that are not there would add mean^2
+        const float2 f = d[i].get();
+        d[i] = Pair::of(holds<KF>(k0, vecs) ? f.x : 0.0f, holds<KF>(k1, vecs) ? f.y : 0.0f);
+        q[i & 1] = fma(d[i], d[i], q[i & 1]);
+      } else {
+        if (!LAYER || holds<KF>(k0, vecs)) q[i & 1] = fma(d[i], d[i], q[i & 1]);
+      }
+    }
+    const float rstd = 1.0f / sqrtf(group_sum(add(q[0], q[1]).sum(), sm[buf + 1] + slot) / fd + a.eps);
+    buf ^= 2;  // the other slots for the next row: a slower warp may still read these
+    if (n >= a.N) continue;
+    if (l == 0) {
+      if (LAYER && a.mean) a.mean[n] = mean;
+      if (a.rstd) a.rstd[n] = rstd;
+    }
+    TY* y = static_cast<TY*>(a.y) + n * a.D;
+    const Pair r = Pair::both(rstd);
+#pragma unroll
+    for (int i = 0; i < E; ++i) d[i] = mul(d[i], r);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (holds<KF>(k, vecs)) {
+        const int c = l + k * tpr;
+        float w[VEC], b[VEC], o[VEC];
+        get_param<VEC>(gain, vecs, c, w);
+        if (LAYER) get_param<VEC>(bias, vecs, c, b);
+        if constexpr (VEC == 1) {
+          const float2 f = d[k / 2].get();
+          const float z = k & 1 ? f.y : f.x;
+          o[0] = LAYER ? z * w[0] + b[0] : z * w[0];
+        } else {
+#pragma unroll
+          for (int i = 0; i < VEC / 2; ++i) {
+            const Pair z = d[k * VEC / 2 + i], g = Pair::of(w[2 * i], w[2 * i + 1]);
+            const float2 f = (LAYER ? fma(z, g, Pair::of(b[2 * i], b[2 * i + 1])) : mul(z, g)).get();
+            o[2 * i] = f.x;
+            o[2 * i + 1] = f.y;
+          }
+        }
+        Vec<TY, VEC> out;
+        out.set(o);
+        out.store(y + static_cast<int64_t>(c) * VEC);
+      }
     }
   }
 }
@@ -199,12 +356,7 @@ __global__ void __launch_bounds__(MAX_THREADS) fwd_long_kernel(NormFwd a) {
     v.load(x + c);
     float w[VEC], b[VEC], o[VEC];
     load_gain<LAYER, VEC>(a.w, a.p_type, a.offset, c, w);
-    if (LAYER && a.b) {
-      load_param<VEC>(a.b, a.p_type, c, b);
-    } else {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) b[e] = 0.0f;
-    }
+    load_bias<LAYER, VEC>(a.b, a.p_type, c, b);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) o[e] = (v.get(e) - mean) * rstd * w[e] + b[e];
     Vec<TY, VEC> out;
@@ -412,7 +564,7 @@ __global__ void __launch_bounds__(128) cols_kernel(NormBwd a) {
 // adds 32 columns: its warps take the parts w, w + 16, ... in order, and warp 0
 // adds the warps in order.  blockIdx.y = 0: the weight's, 1: the bias's.
 constexpr int REDUCE_WARPS = 16;
-inline __global__ void __launch_bounds__(32 * REDUCE_WARPS) reduce_kernel(const float* part_w, const float* part_b,
+static __global__ void __launch_bounds__(32 * REDUCE_WARPS) reduce_kernel(const float* part_w, const float* part_b,
                                                                           int parts, int D, int p_type, void* dw,
                                                                           void* db) {
   __shared__ float ws[REDUCE_WARPS][32];
@@ -447,10 +599,27 @@ inline int group_threads(int64_t vecs, int K) {
 }
 
 template <typename TX, typename TY, int VEC, int K, bool LAYER>
+cudaError_t run_fwd_few(const NormFwd& a, int64_t vecs, cudaStream_t s) {
+  fwd_few_kernel<TX, TY, VEC, K, LAYER><<<static_cast<unsigned>(a.N), group_threads(vecs, K), 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+constexpr int MAX_SMEM = 227 * 1024 - 2048;  // of a block, less what the kernels declare
+
+template <typename TX, typename TY, int VEC, int K, int KF, bool LAYER>
 cudaError_t run_fwd(const NormFwd& a, int tpr, cudaStream_t s) {
-  const int groups = std::max(1, 256 / tpr);
-  const dim3 block(tpr, groups);
-  fwd_kernel<TX, TY, VEC, K, LAYER><<<static_cast<unsigned>(cdiv(a.N, groups)), block, 0, s>>>(a);
+  const int smem = static_cast<int>(sizeof(float)) * a.D * (LAYER ? 2 : 1);
+  // Two blocks of 256 threads fill an SM's registers; where their parameters do not fit twice, one of 512.
+  const bool pair = 2 * (smem + 2048) <= MAX_SMEM;
+  const int groups = std::max(1, (pair ? 256 : MAX_THREADS) / tpr);
+  const int per_sm = std::max(1, MAX_THREADS / (tpr * groups));
+  const int grid = static_cast<int>(std::min<int64_t>(cdiv(a.N, groups), a.sms * per_sm));
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(fwd_kernel<TX, TY, VEC, K, KF, LAYER>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  fwd_kernel<TX, TY, VEC, K, KF, LAYER><<<grid, dim3(tpr, groups), smem, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -458,11 +627,38 @@ template <typename TX, typename TY, int VEC, bool LAYER>
 cudaError_t fwd(const NormFwd& a, cudaStream_t s, int* launches) {
   if (a.N == 0) return cudaSuccess;
   ++*launches;
-  const int64_t vecs = cdiv(a.D, VEC);
-  if (vecs <= 128) return run_fwd<TX, TY, VEC, 1, LAYER>(a, group_threads(vecs, 1), s);
-  if (vecs <= 2 * MAX_THREADS) return run_fwd<TX, TY, VEC, 2, LAYER>(a, group_threads(vecs, 2), s);
-  if (vecs <= 4 * MAX_THREADS) return run_fwd<TX, TY, VEC, 4, LAYER>(a, group_threads(vecs, 4), s);
-  if (vecs <= 8 * MAX_THREADS) return run_fwd<TX, TY, VEC, 8, LAYER>(a, group_threads(vecs, 8), s);
+  const int64_t vecs = a.D / VEC;
+  if (a.N <= a.sms) {
+    if (vecs <= MAX_THREADS) return run_fwd_few<TX, TY, VEC, 1, LAYER>(a, vecs, s);
+    if (vecs <= 4 * MAX_THREADS) return run_fwd_few<TX, TY, VEC, 4, LAYER>(a, vecs, s);
+  }
+  const bool fits = static_cast<int64_t>(sizeof(float)) * a.D * (LAYER ? 2 : 1) <= MAX_SMEM;
+  if constexpr (VEC > 1) {
+    const int tpr = group_threads(vecs, vecs <= 64 ? 4 : 8);
+    if (fits && tpr <= MAX_THREADS) {
+      switch (cdiv(vecs, tpr)) {  // vectors a thread; all but its last are there in every thread
+        case 1: return run_fwd<TX, TY, VEC, 1, 0, LAYER>(a, tpr, s);
+        case 2: return run_fwd<TX, TY, VEC, 2, 1, LAYER>(a, tpr, s);
+        case 3: return run_fwd<TX, TY, VEC, 3, 2, LAYER>(a, tpr, s);
+        case 4: return run_fwd<TX, TY, VEC, 4, 3, LAYER>(a, tpr, s);
+        case 5: return run_fwd<TX, TY, VEC, 5, 4, LAYER>(a, tpr, s);
+        case 6: return run_fwd<TX, TY, VEC, 6, 5, LAYER>(a, tpr, s);
+        case 7: return run_fwd<TX, TY, VEC, 7, 6, LAYER>(a, tpr, s);
+        default: return run_fwd<TX, TY, VEC, 8, 7, LAYER>(a, tpr, s);
+      }
+    }
+  } else {
+    const int K = vecs <= 32 ? 4 : vecs <= 128 ? 8 : vecs <= 512 ? 16 : 32;
+    const int tpr = group_threads(vecs, K);
+    if (fits && tpr <= MAX_THREADS) {
+      switch (K) {
+        case 4: return run_fwd<TX, TY, VEC, 4, 0, LAYER>(a, tpr, s);
+        case 8: return run_fwd<TX, TY, VEC, 8, 4, LAYER>(a, tpr, s);
+        case 16: return run_fwd<TX, TY, VEC, 16, 8, LAYER>(a, tpr, s);
+        default: return run_fwd<TX, TY, VEC, 32, 16, LAYER>(a, tpr, s);
+      }
+    }
+  }
   fwd_long_kernel<TX, TY, VEC, LAYER><<<static_cast<unsigned>(a.N), MAX_THREADS, 0, s>>>(a);
   return cudaGetLastError();
 }

@@ -32,6 +32,7 @@ struct NormFwd {
   float* rstd;  // may be null
   int p_type, N, D;
   float eps, offset;
+  int sms;  // of the device
 };
 
 struct NormBwd {
@@ -49,6 +50,7 @@ struct NormBwd {
   float* part_b;  // [parts][D]
   int p_type, N, D;
   float offset;
+  int sms;  // of the device
 };
 
 // Blocks whose partial parameter gradients are added at the end, at most.

@@ -58,7 +58,7 @@ cce_status forward(const void* x, const Rows& xr, int x_type, const void* w, con
   const bool wide = D % vec == 0 && rows_wide(x, xr, x_type, vec) && rows_wide(y, Rows{1, D, 0}, y_type, vec) &&
                     param_wide(w, p_type, vec) && param_wide(b, p_type, vec);
   const NormFwd a{x,    row_map(xr), w,      b,   y, mean, rstd, p_type, static_cast<int>(N), static_cast<int>(D),
-                  eps, offset};
+                  eps, offset, sms};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int launches = 0;
   const cudaError_t e = x_type == CCE_F32    ? launch_norm_fwd_f32(a, y_type, layer, wide, s, &launches)
@@ -104,7 +104,8 @@ cce_status backward(const void* dy, const Rows& gr, int y_type, const void* x, c
                   p_type,
                   static_cast<int>(N),
                   static_cast<int>(D),
-                  offset};
+                  offset,
+                  sms};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int launches = 0;
   const cudaError_t e = x_type == CCE_F32    ? launch_norm_bwd_f32(a, y_type, layer, wide, s, &launches)
