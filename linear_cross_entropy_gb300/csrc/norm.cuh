@@ -50,17 +50,19 @@ __device__ __forceinline__ float group_sum(float v, float* sm) {
   return t;
 }
 
+// Of two values; without BOTH, of .y alone.
+template <bool BOTH>
 __device__ __forceinline__ float2 group_sum2(float2 v, float2* sm) {
   const int tpr = blockDim.x;
   const int width = tpr < 32 ? tpr : 32;
-  v.x = lanes_sum(v.x, width);
+  if (BOTH) v.x = lanes_sum(v.x, width);
   v.y = lanes_sum(v.y, width);
   if (tpr <= 32) return v;
   if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
   group_sync();
   float2 t = make_float2(0.0f, 0.0f);
   for (int i = 0; i < tpr >> 5; ++i) {
-    t.x += sm[i].x;
+    if (BOTH) t.x += sm[i].x;
     t.y += sm[i].y;
   }
   return t;
@@ -366,111 +368,176 @@ __global__ void __launch_bounds__(MAX_THREADS) fwd_long_kernel(NormFwd a) {
 }
 
 // ----------------------------------------------------------------- backward
-// Persistent blocks: a group walks rows at a stride of all groups, and each
-// thread keeps the parameter gradients of its own columns in registers over
-// all of them.  At the end a block adds its groups in order and writes one
+// Persistent blocks, one per SM: a group walks rows at a stride of all groups,
+// and each thread keeps the parameter gradients of its own columns in registers
+// over all of them.  At the end a block adds its groups in order and writes one
 // partial row; reduce_kernel adds the blocks in order.
-template <typename TX, typename TY, int VEC, int K, bool LAYER>
-__global__ void __launch_bounds__(MAX_THREADS) bwd_kernel(NormBwd a) {
-  extern __shared__ float comb[];  // [groups][D], only with several groups
-  __shared__ float2 sm[2][MAX_THREADS / 32];
+//
+// The columns' sums are what fills the registers, so a thread holds 16 values of
+// a row (32 in rows that need it) and a row is spread over more threads than in
+// the forward.  PREFETCH loads the next row while this one is reduced.
+template <typename TX, int VEC, int K, bool LAYER>
+constexpr int bwd_threads() {
+  return !LAYER && sizeof(TX) == 2 && VEC > 1 && K * VEC <= 16 ? 768 : 512;
+}
+
+template <typename TX, typename TY, int VEC, int K, int KF, bool LAYER, bool PREFETCH>
+__global__ void __launch_bounds__(bwd_threads<TX, VEC, K, LAYER>(), 1) bwd_kernel(NormBwd a) {
+  constexpr int E = K * VEC / 2;
+  extern __shared__ __align__(16) float shared[];  // the gain [D]; at the end [groups][D] sums
+  __shared__ float2 sm[2][bwd_threads<TX, VEC, K, LAYER>() / 32];
   const int l = threadIdx.x, tpr = blockDim.x, groups = blockDim.y;
-  const int red = threadIdx.y * (tpr >> 5);
+  const int vecs = a.D / VEC, slot = threadIdx.y * (tpr >> 5);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   const float inv_d = 1.0f / static_cast<float>(a.D);
-  float aw[K][VEC], ab[K][VEC];
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      aw[k][e] = 0.0f;
-      ab[k][e] = 0.0f;
-    }
-  }
-  int parity = 0;
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * groups; base < a.N;
-       base += static_cast<int64_t>(gridDim.x) * groups) {
-    const int64_t n = base + threadIdx.y;
-    const bool live = n < a.N;
-    const TX* x = static_cast<const TX*>(a.x) + (live ? a.xm.at(static_cast<int>(n)) : 0);
-    const TY* dy = static_cast<const TY*>(a.dy) + (live ? a.gm.at(static_cast<int>(n)) : 0);
-    Vec<TX, VEC> xv[K];
-    Vec<TY, VEC> gv[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (l + k * tpr) * VEC;
-      if (live && c < a.D) {
-        xv[k].load(x + c);
-        gv[k].load(dy + c);
-      } else {
-        xv[k].zero();
-        gv[k].zero();
-      }
-    }
-    const float rstd = live ? a.rstd[n] : 0.0f;
-    const float mean = LAYER && live ? a.mean[n] : 0.0f;
-    float2 s = make_float2(0.0f, 0.0f);
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (l + k * tpr) * VEC;
-      if (c < a.D) {
-        float w[VEC];
-        load_gain<LAYER, VEC>(a.w, a.p_type, a.offset, c, w);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float z = (xv[k].get(e) - mean) * rstd;
-          const float d = gv[k].get(e);
-          const float g = d * w[e];
-          aw[k][e] += d * z;
-          if (LAYER) {
-            ab[k][e] += d;
-            s.x += g;
-          }
-          s.y += g * z;
-        }
-      }
-    }
-    if (a.dx) {
-      s = group_sum2(s, sm[parity] + red);
-      parity ^= 1;  // the other buffer next: a slower warp may still read this one
-      s.x *= inv_d;
-      s.y *= inv_d;
-      TX* dx = static_cast<TX*>(a.dx) + n * a.D;
+
+  Vec<TX, VEC> xv[K];
+  Vec<TY, VEC> gv[K];
+  float mean = 0.0f, rstd = 0.0f;
+  auto load_row = [&](int64_t n) {
+    if (n < a.N) {
+      const TX* x = static_cast<const TX*>(a.x) + a.xm.at(static_cast<int>(n));
+      const TY* dy = static_cast<const TY*>(a.dy) + a.gm.at(static_cast<int>(n));
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        const int c = (l + k * tpr) * VEC;
-        if (live && c < a.D) {
-          float w[VEC], o[VEC];
-          load_gain<LAYER, VEC>(a.w, a.p_type, a.offset, c, w);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const float z = (xv[k].get(e) - mean) * rstd;
-            o[e] = rstd * (gv[k].get(e) * w[e] - (s.x + z * s.y));
-          }
-          Vec<TX, VEC> out;
-          out.set(o);
-          out.store(dx + c);
+        if (holds<KF>(k, vecs)) {
+          xv[k].load(x + (l + k * tpr) * VEC);
+          gv[k].load(dy + (l + k * tpr) * VEC);
         }
       }
+      if (LAYER) mean = a.mean[n];
+      rstd = a.rstd[n];
+    } else {  // a row of zeros adds nothing
+#pragma unroll
+      for (int k = 0; k < K; ++k) gv[k].zero();
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    xv[k].zero();
+    gv[k].zero();
+  }
+  int64_t base = static_cast<int64_t>(blockIdx.x) * groups;
+  if (PREFETCH) load_row(base + threadIdx.y);
+  for (int c = threadIdx.y * tpr + l; c < vecs; c += tpr * groups) {
+    float f[VEC];
+    load_gain<LAYER, VEC>(a.w, a.p_type, a.offset, static_cast<int64_t>(c) * VEC, f);
+    put_param<VEC>(shared, vecs, c, f);
+  }
+  __syncthreads();
+
+  Pair aw[E], ab[LAYER ? E : 1];
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    aw[i] = Pair::both(0.0f);
+    if (LAYER) ab[i] = Pair::both(0.0f);
+  }
+  int buf = 0;
+  for (; base < a.N; base += step) {
+    const int64_t n = base + threadIdx.y;
+    if (!PREFETCH) load_row(n);
+    Vec<TX, VEC> x[K];
+    Vec<TY, VEC> g[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      x[k] = xv[k];
+      g[k] = gv[k];
+    }
+    const float row_rstd = rstd, row_mean = mean;
+    if (PREFETCH) load_row(n + step);
+    // z = x rstd - mean rstd
+    const Pair r = Pair::both(row_rstd), m = Pair::both(-row_mean * row_rstd);
+    float2 s;
+    {
+      Pair xp[E], dp[E], s1 = Pair::both(0.0f), s2 = Pair::both(0.0f);
+      unpack<TX, VEC, K>(x, xp);
+      unpack<TY, VEC, K>(g, dp);
+      auto gather = [&](int i, Pair w) {
+        const Pair z = LAYER ? fma(xp[i], r, m) : mul(xp[i], r);
+        const Pair t = mul(dp[i], w);
+        aw[i] = fma(dp[i], z, aw[i]);
+        if (LAYER) {
+          ab[i] = add(ab[i], dp[i]);
+          s1 = add(s1, t);
+        }
+        s2 = fma(t, z, s2);
+      };
+      if constexpr (VEC == 1) {
+#pragma unroll
+        for (int k = 0; k < K; k += 2) {  // where a column is not there its dy is 0, and any gain does
+          gather(k / 2, Pair::of(shared[holds<KF>(k, vecs) ? l + k * tpr : 0],
+                                 shared[holds<KF>(k + 1, vecs) ? l + (k + 1) * tpr : 0]));
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          if (!holds<KF>(k, vecs)) continue;
+          float w[VEC];
+          get_param<VEC>(shared, vecs, l + k * tpr, w);
+#pragma unroll
+          for (int i = 0; i < VEC / 2; ++i) gather(k * VEC / 2 + i, Pair::of(w[2 * i], w[2 * i + 1]));
+        }
+      }
+      s = make_float2(LAYER ? s1.sum() : 0.0f, s2.sum());
+    }
+    if (!a.dx) continue;
+    s = group_sum2<LAYER>(s, sm[buf] + slot);
+    buf ^= 1;  // the other slots for the next row: a slower warp may still read these
+    if (n >= a.N) continue;
+    TX* dx = static_cast<TX*>(a.dx) + n * a.D;
+    const Pair c1 = Pair::both(-s.x * inv_d * row_rstd), c2 = Pair::both(-s.y * inv_d * row_rstd);
+    Pair xp[E], dp[E];
+    unpack<TX, VEC, K>(x, xp);
+    unpack<TY, VEC, K>(g, dp);
+    // rstd (g - sum(g) / D - z sum(g z) / D)
+    auto grad = [&](int i, Pair w) {
+      const Pair z = LAYER ? fma(xp[i], r, m) : mul(xp[i], r);
+      return fma(mul(dp[i], w), r, LAYER ? fma(z, c2, c1) : mul(z, c2)).get();
+    };
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (!holds<KF>(k, vecs)) continue;
+      float w[VEC], f[VEC];
+      get_param<VEC>(shared, vecs, l + k * tpr, w);
+      if constexpr (VEC == 1) {
+        const float2 t = grad(k / 2, Pair::both(w[0]));
+        f[0] = k & 1 ? t.y : t.x;
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) {
+          const float2 t = grad(k * VEC / 2 + i, Pair::of(w[2 * i], w[2 * i + 1]));
+          f[2 * i] = t.x;
+          f[2 * i + 1] = t.y;
+        }
+      }
+      Vec<TX, VEC> out;
+      out.set(f);
+      out.store(dx + (l + k * tpr) * VEC);
     }
   }
+
+#pragma unroll
   for (int pass = 0; pass < (LAYER ? 2 : 1); ++pass) {
     if (!(pass == 0 ? a.dw : a.db)) continue;
     float* part = (pass == 0 ? a.part_w : a.part_b) + static_cast<int64_t>(blockIdx.x) * a.D;
-    if (groups > 1) __syncthreads();  // comb free again
+    if (groups > 1) __syncthreads();  // the gain, or the other pass's sums, have been read
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int c = (l + k * tpr) * VEC;
-      if (c < a.D) {
-        float* to = groups > 1 ? comb + threadIdx.y * a.D + c : part + c;
+      if (holds<KF>(k, vecs)) {
+        const int c = (l + k * tpr) * VEC;
+        float* to = groups > 1 ? shared + threadIdx.y * a.D + c : part + c;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) to[e] = pass == 0 ? aw[k][e] : ab[k][e];
+        for (int e = 0; e < VEC; ++e) {
+          const float2 t = (pass == 0 ? aw : ab)[LAYER || pass == 0 ? (k * VEC + e) / 2 : 0].get();
+          to[e] = (k * VEC + e) & 1 ? t.y : t.x;
+        }
       }
     }
     if (groups > 1) {
       __syncthreads();
       for (int c = threadIdx.y * tpr + l; c < a.D; c += tpr * groups) {
         float t = 0.0f;
-        for (int g = 0; g < groups; ++g) t += comb[g * a.D + c];
+        for (int g = 0; g < groups; ++g) t += shared[g * a.D + c];
         part[c] = t;
       }
     }
@@ -505,7 +572,7 @@ __global__ void __launch_bounds__(MAX_THREADS) bwd_long_kernel(NormBwd a) {
       s.y += g * z;
     }
   }
-  s = group_sum2(s, sm);
+  s = group_sum2<LAYER>(s, sm);
   s.x *= inv_d;
   s.y *= inv_d;
 #pragma unroll 2
@@ -604,7 +671,8 @@ cudaError_t run_fwd_few(const NormFwd& a, int64_t vecs, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-constexpr int MAX_SMEM = 227 * 1024 - 2048;  // of a block, less what the kernels declare
+constexpr int MAX_SMEM = 227 * 1024 - 2048;   // dynamic shared memory of a block, beside what the kernels declare
+constexpr int PLAIN_SMEM = 48 * 1024 - 2048;  // of a block that has not asked for more
 
 template <typename TX, typename TY, int VEC, int K, int KF, bool LAYER>
 cudaError_t run_fwd(const NormFwd& a, int tpr, cudaStream_t s) {
@@ -614,7 +682,7 @@ cudaError_t run_fwd(const NormFwd& a, int tpr, cudaStream_t s) {
   const int groups = std::max(1, (pair ? 256 : MAX_THREADS) / tpr);
   const int per_sm = std::max(1, MAX_THREADS / (tpr * groups));
   const int grid = static_cast<int>(std::min<int64_t>(cdiv(a.N, groups), a.sms * per_sm));
-  if (smem > 48 * 1024) {
+  if (smem > PLAIN_SMEM) {
     const cudaError_t e = cudaFuncSetAttribute(fwd_kernel<TX, TY, VEC, K, KF, LAYER>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -663,37 +731,66 @@ cudaError_t fwd(const NormFwd& a, cudaStream_t s, int* launches) {
   return cudaGetLastError();
 }
 
-template <typename TX, typename TY, int VEC, int K, bool LAYER>
+template <typename TX, typename TY, int VEC, int K, int KF, bool LAYER>
 cudaError_t run_bwd(const NormBwd& a, int tpr, int* parts, cudaStream_t s) {
-  const int groups = MAX_THREADS / tpr;
-  *parts = static_cast<int>(std::min<int64_t>(NORM_MAX_PARTS, cdiv(a.N, groups)));
-  const size_t smem = groups > 1 ? sizeof(float) * static_cast<size_t>(groups) * a.D : 0;
-  bwd_kernel<TX, TY, VEC, K, LAYER><<<*parts, dim3(tpr, groups), smem, s>>>(a);
+  constexpr bool PREFETCH = K * VEC <= 16;
+  const int groups = std::max(1, bwd_threads<TX, VEC, K, LAYER>() / tpr);
+  *parts = static_cast<int>(std::min<int64_t>({NORM_MAX_PARTS, a.sms, cdiv(a.N, groups)}));
+  const int smem = static_cast<int>(sizeof(float)) * groups * a.D;
+  if (smem > PLAIN_SMEM) {
+    const cudaError_t e = cudaFuncSetAttribute(bwd_kernel<TX, TY, VEC, K, KF, LAYER, PREFETCH>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  bwd_kernel<TX, TY, VEC, K, KF, LAYER, PREFETCH><<<*parts, dim3(tpr, groups), smem, s>>>(a);
   return cudaGetLastError();
+}
+
+// Launches bwd_kernel for rows that the registers of one block hold; false for longer ones.
+template <typename TX, typename TY, int VEC, bool LAYER>
+bool bwd_in_registers(const NormBwd& a, int* parts, cudaStream_t s, cudaError_t* e) {
+  const int64_t vecs = a.D / VEC;
+  if constexpr (VEC > 1) {
+    constexpr int K = 16 / VEC;
+    const int most = bwd_threads<TX, VEC, K, LAYER>();
+    int tpr = group_threads(vecs, K);
+    if (tpr <= most) {
+      switch (cdiv(vecs, tpr)) {  // vectors a thread; all but its last are there in every thread
+        case 1: *e = run_bwd<TX, TY, VEC, 1, 0, LAYER>(a, tpr, parts, s); break;
+        case 2: *e = run_bwd<TX, TY, VEC, 2, 1, LAYER>(a, tpr, parts, s); break;
+        case 3: *e = run_bwd<TX, TY, VEC, K < 3 ? 2 : 3, K < 3 ? 1 : 2, LAYER>(a, tpr, parts, s); break;
+        default: *e = run_bwd<TX, TY, VEC, K, K - 1, LAYER>(a, tpr, parts, s); break;
+      }
+      return true;
+    }
+    tpr = group_threads(vecs, 2 * K);
+    if (tpr > bwd_threads<TX, VEC, 2 * K, LAYER>()) return false;
+    *e = run_bwd<TX, TY, VEC, 2 * K, K, LAYER>(a, tpr, parts, s);
+  } else {
+    const int K = vecs <= 32 ? 4 : vecs <= 16 * MAX_THREADS ? 16 : 32;
+    const int tpr = group_threads(vecs, K);
+    if (tpr > MAX_THREADS) return false;
+    switch (K) {
+      case 4: *e = run_bwd<TX, TY, VEC, 4, 0, LAYER>(a, tpr, parts, s); break;
+      case 16: *e = run_bwd<TX, TY, VEC, 16, 8, LAYER>(a, tpr, parts, s); break;
+      default: *e = run_bwd<TX, TY, VEC, 32, 16, LAYER>(a, tpr, parts, s); break;
+    }
+  }
+  return true;
 }
 
 template <typename TX, typename TY, int VEC, bool LAYER>
 cudaError_t bwd(const NormBwd& a, cudaStream_t s, int* launches) {
-  cudaError_t e = cudaSuccess;
   int parts = 0;
   if (a.N > 0 && (a.dx || a.dw || a.db)) {
     ++*launches;
-    const int64_t vecs = cdiv(a.D, VEC);
-    constexpr int MOST = VEC == 1 ? 16 : 32 / VEC;  // vectors per thread whose sums fit in registers
-    if (vecs <= MAX_THREADS) {
-      e = run_bwd<TX, TY, VEC, 1, LAYER>(a, group_threads(vecs, 1), &parts, s);
-    } else if (vecs <= 2 * MAX_THREADS) {
-      e = run_bwd<TX, TY, VEC, 2, LAYER>(a, group_threads(vecs, 2), &parts, s);
-    } else if (MOST > 4 && vecs <= 4 * MAX_THREADS) {
-      e = run_bwd<TX, TY, VEC, 4, LAYER>(a, group_threads(vecs, 4), &parts, s);
-    } else if (vecs <= static_cast<int64_t>(MOST) * MAX_THREADS) {
-      e = run_bwd<TX, TY, VEC, MOST, LAYER>(a, group_threads(vecs, MOST), &parts, s);
-    } else {
+    cudaError_t e = cudaSuccess;
+    if (!bwd_in_registers<TX, TY, VEC, LAYER>(a, &parts, s, &e)) {
       if (a.dx) bwd_long_kernel<TX, TY, VEC, LAYER><<<static_cast<unsigned>(a.N), MAX_THREADS, 0, s>>>(a);
       if (a.dw || a.db) {
-        const int64_t tiles = cdiv(vecs, 128);
+        const int64_t tiles = cdiv(a.D / VEC, 128);
         parts = static_cast<int>(
-            std::min<int64_t>({NORM_MAX_PARTS, cdiv(a.N, 8), std::max<int64_t>(1, 1216 / tiles)}));
+            std::min<int64_t>({NORM_MAX_PARTS, cdiv(a.N, 8), std::max<int64_t>(1, 8 * a.sms / tiles)}));
         *launches += a.dx ? 1 : 0;
         cols_kernel<TX, TY, VEC, LAYER>
             <<<dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(parts)), 128, 0, s>>>(a);
@@ -702,13 +799,11 @@ cudaError_t bwd(const NormBwd& a, cudaStream_t s, int* launches) {
     }
     if (e != cudaSuccess) return e;
   }
-  if (a.dw || a.db) {
-    ++*launches;
-    reduce_kernel<<<dim3(static_cast<unsigned>(cdiv(a.D, 32)), LAYER ? 2 : 1), dim3(32, REDUCE_WARPS), 0, s>>>(
-        a.part_w, a.part_b, parts, a.D, a.p_type, a.dw, a.db);
-    e = cudaGetLastError();
-  }
-  return e;
+  if (!a.dw && !a.db) return cudaSuccess;
+  ++*launches;
+  reduce_kernel<<<dim3(static_cast<unsigned>(cdiv(a.D, 32)), LAYER ? 2 : 1), dim3(32, REDUCE_WARPS), 0, s>>>(
+      a.part_w, a.part_b, parts, a.D, a.p_type, a.dw, a.db);
+  return cudaGetLastError();
 }
 
 template <typename TX, typename TY>
