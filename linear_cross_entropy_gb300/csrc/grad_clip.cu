@@ -4,17 +4,16 @@
 //
 // Bound by memory: every element is read once for the norm and, unless the
 // factor is 1 in place, read again and written.  The tensors are cut into
-// chunks and persistent blocks take the chunks in turn, so that a launch
-// covers hundreds of tensors of any size; the table of tensors travels in the
-// kernel's parameters (no copy to the device, nothing to keep alive for a
-// captured graph).  The second pass walks the chunks backwards: what the first
-// pass read last is still in L2.
+// chunks, which the blocks of one launch take in turn, so that a launch covers
+// hundreds of tensors of any size; the table of tensors travels in the kernel's
+// parameters (no copy to the device, nothing to keep alive for a captured
+// graph).  The second pass walks the chunks backwards: what the first pass read
+// last is still in L2.
 //
-// A thread sums the squares of up to 64 values in fp32 and carries the sum
-// over its chunks in fp64; block partials and the total are fp64, added in a
-// fixed order.  Where those 64 squares overflow, or are so small that
-// underflow could show (below 2^-100 and not zero), the thread sums them again
-// in fp64.
+// A thread sums the squares of up to 64 values in fp32 and goes on in fp64;
+// block partials and the total are fp64, added in a fixed order.  Where those
+// squares overflow, or are so small that underflow could show (below 2^-100 and
+// not zero), the thread sums its values of the chunk again in fp64.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -31,14 +30,13 @@ namespace {
 
 constexpr int THREADS = 256;
 constexpr int UNROLL = 8;                  // 16-byte loads in flight per thread
-constexpr int CHUNK = THREADS * UNROLL * 8;  // elements: one unrolled round of 16-bit values
-constexpr int SMALL_CHUNK = CHUNK / 4;
+constexpr int ROUND = THREADS * UNROLL * 8;  // elements of one unrolled round of 16-bit values
 constexpr int GRID = 608;                  // 152 SMs x 4 resident blocks
 constexpr int MAX_TENSORS = 1000;          // per launch: what 32 KB of parameters hold
 constexpr int FEW_TENSORS = 32;            // a launch with 1 KB of them
 // Of one tensor: then the chunks of MAX_TENSORS of them can be counted in 32 bits.
 constexpr int64_t MAX_ELEMENTS = int64_t(1) << 35;
-static_assert(MAX_ELEMENTS / CHUNK * MAX_TENSORS < int64_t(1) << 32, "chunk numbers");
+static_assert(MAX_ELEMENTS / ROUND * MAX_TENSORS < int64_t(1) << 32, "chunk numbers");
 
 struct Tensor {
   const void* in;
@@ -55,6 +53,7 @@ struct Batch {
   int count;
   int chunk;  // elements
   uint32_t chunks;
+  int in_place;  // every output is its input
 };
 static_assert(sizeof(Batch<MAX_TENSORS>) <= 32000 + 64, "kernel parameters");
 
@@ -66,9 +65,10 @@ struct Clip {
   float* norm;  // written by block 0, may be null
 };
 
+// The last tensor whose first chunk is <= chunk.
 template <int M>
 __device__ __forceinline__ int find_tensor(const Batch<M>& b, uint32_t chunk) {
-  int lo = 0, hi = b.count - 1;  // the last tensor whose first chunk is <= chunk
+  int lo = 0, hi = b.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (b.t[mid].first_chunk <= chunk) {
@@ -98,11 +98,13 @@ __device__ double block_join(double v, bool inf) {
   return v;
 }
 
-// What a thread gathers over a chunk: squares or the largest magnitude.
+// What a thread gathers: squares or the largest magnitude.
 struct Gather {
-  double total = 0.0;  // over the chunks
-  float s = 0.0f;      // of this chunk: sum of squares, or the largest magnitude
-  uint32_t any = 0u;   // bits of the chunk's values but the signs
+  double total = 0.0;      // over the chunks
+  double chunk = 0.0;      // over the rounds of this chunk
+  float s = 0.0f;          // of this round: sum of squares, or the largest magnitude
+  uint32_t any = 0u;       // bits of the round's values but the signs
+  bool outside = false;    // a round of this chunk left fp32's range
 
   template <typename T, int VEC>
   __device__ __forceinline__ void add(const Vec<T, VEC>& v, bool inf) {
@@ -122,7 +124,13 @@ struct Gather {
       for (int i = 0; i < Vec<T, VEC>::WORDS; ++i) any |= v.w[i] & (sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu);
     }
   }
-  __device__ __forceinline__ bool out_of_range() const { return !(s <= 3.0e38f) || (s < 0x1p-100f && any != 0u); }
+  __device__ __forceinline__ void end_round(bool inf) {
+    if (inf) return;
+    outside = outside || !(s <= 3.0e38f) || (s < 0x1p-100f && any != 0u);
+    chunk += s;
+    s = 0.0f;
+    any = 0u;
+  }
 };
 
 // The thread's squares of a chunk again, in fp64.
@@ -146,26 +154,29 @@ __device__ __noinline__ double squares64(const T* p, int n) {
   return t;
 }
 
+// Rounds of U vectors a thread from vector v on, while whole rounds are left.
+template <int U, typename T, int VEC>
+__device__ __forceinline__ void gather_rounds(const T* p, int vecs, int& v, bool inf, Gather& g) {
+#pragma unroll 1
+  for (; v + THREADS * (U - 1) < vecs; v += THREADS * U) {
+    Vec<T, VEC> x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u].load(p + static_cast<int64_t>(v + u * THREADS) * VEC);
+#pragma unroll
+    for (int u = 0; u < U; ++u) g.add(x[u], inf);
+    if (U == UNROLL) g.end_round(inf);
+  }
+}
+
 template <typename T, int VEC>
 __device__ __forceinline__ void gather_chunk(const T* p, int n, bool inf, Gather& g) {
   const int vecs = n / VEC;
-  g.s = 0.0f;
-  g.any = 0u;
+  g.chunk = 0.0;
+  g.outside = false;
   int v = threadIdx.x;
-#pragma unroll 1
-  for (; v + THREADS * (UNROLL - 1) < vecs; v += THREADS * UNROLL) {
-    Vec<T, VEC> x[UNROLL];
-#pragma unroll
-    for (int u = 0; u < UNROLL; ++u) x[u].load(p + static_cast<int64_t>(v + u * THREADS) * VEC);
-#pragma unroll
-    for (int u = 0; u < UNROLL; ++u) g.add(x[u], inf);
-  }
-#pragma unroll 1
-  for (; v < vecs; v += THREADS) {
-    Vec<T, VEC> x;
-    x.load(p + static_cast<int64_t>(v) * VEC);
-    g.add(x, inf);
-  }
+  gather_rounds<UNROLL, T, VEC>(p, vecs, v, inf, g);
+  gather_rounds<2, T, VEC>(p, vecs, v, inf, g);
+  gather_rounds<1, T, VEC>(p, vecs, v, inf, g);
   if constexpr (VEC > 1) {
     const int i = vecs * VEC + threadIdx.x;
     if (i < n) {
@@ -174,13 +185,8 @@ __device__ __forceinline__ void gather_chunk(const T* p, int n, bool inf, Gather
       g.add(x, inf);
     }
   }
-  if (inf) {
-    g.total = larger(g.total, g.s);
-  } else if (g.out_of_range()) {
-    g.total += squares64<T, VEC>(p, n);
-  } else {
-    g.total += g.s;
-  }
+  g.end_round(inf);
+  if (!inf) g.total += g.outside ? squares64<T, VEC>(p, n) : g.chunk;
 }
 
 template <typename T>
@@ -197,6 +203,7 @@ template <int M>
 __global__ void __launch_bounds__(THREADS, 4) norm_kernel(const __grid_constant__ Batch<M> b, int norm_type,
                                                        double* part) {
   const bool inf = norm_type == CCE_NORM_INF;
+  let_next_start();
   Gather g;
   for (uint32_t c = blockIdx.x; c < b.chunks; c += gridDim.x) {
     const Tensor& t = b.t[find_tensor(b, c)];
@@ -210,13 +217,14 @@ __global__ void __launch_bounds__(THREADS, 4) norm_kernel(const __grid_constant_
       gather_typed<__half>(t.in, off, n, t.wide_in, inf, g);
     }
   }
-  const double v = block_join(g.total, inf);
+  const double v = block_join(inf ? static_cast<double>(g.s) : g.total, inf);
   if (threadIdx.x == 0) part[blockIdx.x] = v;
 }
 
 // The norm from the block partials: every block computes it, in the same order.
 __device__ float total_norm(const Clip& k) {
   __shared__ float result;
+  wait_for_previous();
   const bool inf = k.norm_type == CCE_NORM_INF;
   double v = 0.0;
   for (int i = threadIdx.x; i < k.parts; i += THREADS) v = join(v, k.part[i], inf);
@@ -246,24 +254,25 @@ __device__ __forceinline__ void scale_vec(const Vec<TI, VEC>& x, TO* q, float f)
   y.store(q);
 }
 
+template <int U, typename TI, typename TO, int VEC>
+__device__ __forceinline__ void scale_rounds(const TI* p, TO* q, int vecs, int& v, float f) {
+#pragma unroll 1
+  for (; v + THREADS * (U - 1) < vecs; v += THREADS * U) {
+    Vec<TI, VEC> x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u].load_written(p + static_cast<int64_t>(v + u * THREADS) * VEC);
+#pragma unroll
+    for (int u = 0; u < U; ++u) scale_vec<TI, TO, VEC>(x[u], q + static_cast<int64_t>(v + u * THREADS) * VEC, f);
+  }
+}
+
 template <typename TI, typename TO, int VEC>
 __device__ __forceinline__ void scale_chunk(const TI* p, TO* q, int n, float f) {
   const int vecs = n / VEC;
   int v = threadIdx.x;
-#pragma unroll 1
-  for (; v + THREADS * (UNROLL - 1) < vecs; v += THREADS * UNROLL) {
-    Vec<TI, VEC> x[UNROLL];
-#pragma unroll
-    for (int u = 0; u < UNROLL; ++u) x[u].load_written(p + static_cast<int64_t>(v + u * THREADS) * VEC);
-#pragma unroll
-    for (int u = 0; u < UNROLL; ++u) scale_vec<TI, TO, VEC>(x[u], q + static_cast<int64_t>(v + u * THREADS) * VEC, f);
-  }
-#pragma unroll 1
-  for (; v < vecs; v += THREADS) {
-    Vec<TI, VEC> x;
-    x.load_written(p + static_cast<int64_t>(v) * VEC);
-    scale_vec<TI, TO, VEC>(x, q + static_cast<int64_t>(v) * VEC, f);
-  }
+  scale_rounds<UNROLL, TI, TO, VEC>(p, q, vecs, v, f);
+  scale_rounds<2, TI, TO, VEC>(p, q, vecs, v, f);
+  scale_rounds<1, TI, TO, VEC>(p, q, vecs, v, f);
   if constexpr (VEC > 1) {
     const int i = vecs * VEC + threadIdx.x;
     if (i < n) {
@@ -278,8 +287,8 @@ template <typename TI, typename TO>
 __device__ __forceinline__ void scale_typed(const Tensor& t, int64_t off, int n, float f) {
   const TI* p = static_cast<const TI*>(t.in) + off;
   TO* q = static_cast<TO*>(t.out) + off;
-  if (t.wide_both) {
-    scale_chunk<TI, TO, 16 / sizeof(TI)>(p, q, n, f);
+  if (t.wide_both) {  // neither access wider than 16 bytes, so that both are on consecutive addresses
+    scale_chunk<TI, TO, 16 / (sizeof(TI) > sizeof(TO) ? sizeof(TI) : sizeof(TO))>(p, q, n, f);
   } else {
     scale_chunk<TI, TO, 1>(p, q, n, f);
   }
@@ -299,6 +308,7 @@ __device__ __forceinline__ void scale_from(const Tensor& t, int64_t off, int n, 
 template <int M>
 __global__ void __launch_bounds__(THREADS, 4) scale_kernel(const __grid_constant__ Batch<M> b, Clip k) {
   const float f = clip_factor(k, total_norm(k));
+  if (f == 1.0f && b.in_place) return;
   for (uint32_t i = blockIdx.x; i < b.chunks; i += gridDim.x) {
     const uint32_t c = b.chunks - 1 - i;
     const Tensor& t = b.t[find_tensor(b, c)];
@@ -454,6 +464,7 @@ template <int M>
 void fill_batch(Batch<M>& b, const int64_t* dense, int64_t n_dense, int chunk, int64_t* next) {
   b.count = 0;
   b.chunk = chunk;
+  b.in_place = 1;
   int64_t chunks = 0;
   for (; *next < n_dense && b.count < M; ++*next) {
     const Row r = table_row(dense, *next);
@@ -464,6 +475,7 @@ void fill_batch(Batch<M>& b, const int64_t* dense, int64_t n_dense, int chunk, i
     t.out = r.out;
     t.n = r.n;
     t.first_chunk = static_cast<uint32_t>(chunks);
+    if (r.in != r.out) b.in_place = 0;
     t.in_type = static_cast<uint8_t>(r.in_type);
     t.out_type = static_cast<uint8_t>(r.out_type);
     t.wide_in = multiple(r.in, 16);
@@ -475,6 +487,15 @@ void fill_batch(Batch<M>& b, const int64_t* dense, int64_t n_dense, int chunk, i
 
 int grid_of(uint32_t chunks) { return static_cast<int>(std::min<uint32_t>(GRID, chunks)); }
 
+// A block spends a third of a microsecond on a chunk beside its memory, so
+// chunks are as large as leaves every block some of them (4 rounds: four
+// chunks a block at least), and a quarter of a round where a round would leave
+// SMs without work.
+int chunk_of(int64_t total) {
+  if (total >= int64_t(4) * GRID * 4 * ROUND) return 4 * ROUND;
+  return total >= int64_t(GRID) * ROUND ? ROUND : ROUND / 4;
+}
+
 // The norm pass (clip null) or the scaling pass over the dense tensors.
 template <int M>
 cudaError_t run_dense(const int64_t* dense, int64_t n_dense, int chunk, int norm_type, const Clip* clip, double* part,
@@ -485,7 +506,9 @@ cudaError_t run_dense(const int64_t* dense, int64_t n_dense, int chunk, int norm
     if (b.count == 0) continue;
     const int grid = grid_of(b.chunks);
     if (clip) {
-      scale_kernel<M><<<grid, THREADS, 0, s>>>(b, *clip);
+      // the first one follows a norm kernel
+      const cudaError_t e = launch_after(scale_kernel<M>, dim3(grid), dim3(THREADS), s, b, *clip);
+      if (e != cudaSuccess) return e;
     } else {
       norm_kernel<M><<<grid, THREADS, 0, s>>>(b, norm_type, part + *parts);
       *parts += grid;
@@ -501,8 +524,7 @@ cudaError_t pass(const int64_t* dense, int64_t n_dense, const cce_strided* strid
                  const Clip* clip, double* part, int* parts, cudaStream_t s, int* launches) {
   int64_t total = 0;
   for (int64_t i = 0; i < n_dense; ++i) total += dense[4 * i + 2];
-  // Under one full chunk a block, smaller ones spread the work over more SMs.
-  const int chunk = total < static_cast<int64_t>(GRID) * CHUNK ? SMALL_CHUNK : CHUNK;
+  const int chunk = chunk_of(total);
   cudaError_t e = n_dense <= FEW_TENSORS
                       ? run_dense<FEW_TENSORS>(dense, n_dense, chunk, norm_type, clip, part, parts, s, launches)
                       : run_dense<MAX_TENSORS>(dense, n_dense, chunk, norm_type, clip, part, parts, s, launches);
@@ -552,9 +574,8 @@ cce_status run(const int64_t* dense, int64_t n_dense, const cce_strided* strided
   if (e == cudaSuccess && clipping && parts > 0)
     e = pass(dense, n_dense, strided, n_strided, norm_type, &k, part, &parts, s, &launches);
   if (e == cudaSuccess && (!clipping || parts == 0)) {
-    finish_kernel<<<1, THREADS, 0, s>>>(k);
+    e = launch_after(finish_kernel, dim3(1), dim3(THREADS), s, k);
     ++launches;
-    e = cudaGetLastError();
   }
   count_launches(launches);
   return e == cudaSuccess ? CCE_OK : CCE_ERR_CUDA;

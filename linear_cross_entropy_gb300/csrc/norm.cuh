@@ -417,6 +417,7 @@ __global__ void __launch_bounds__(bwd_threads<TX, VEC, K, LAYER>(), 1) bwd_kerne
     xv[k].zero();
     gv[k].zero();
   }
+  let_next_start();
   int64_t base = static_cast<int64_t>(blockIdx.x) * groups;
   if (PREFETCH) load_row(base + threadIdx.y);
   for (int c = threadIdx.y * tpr + l; c < vecs; c += tpr * groups) {
@@ -635,6 +636,7 @@ static __global__ void __launch_bounds__(32 * REDUCE_WARPS) reduce_kernel(const 
                                                                           int parts, int D, int p_type, void* dw,
                                                                           void* db) {
   __shared__ float ws[REDUCE_WARPS][32];
+  wait_for_previous();
   void* out = blockIdx.y == 0 ? dw : db;
   if (!out) return;
   const float* part = blockIdx.y == 0 ? part_w : part_b;
@@ -801,9 +803,8 @@ cudaError_t bwd(const NormBwd& a, cudaStream_t s, int* launches) {
   }
   if (!a.dw && !a.db) return cudaSuccess;
   ++*launches;
-  reduce_kernel<<<dim3(static_cast<unsigned>(cdiv(a.D, 32)), LAYER ? 2 : 1), dim3(32, REDUCE_WARPS), 0, s>>>(
-      a.part_w, a.part_b, parts, a.D, a.p_type, a.dw, a.db);
-  return cudaGetLastError();
+  return launch_after(reduce_kernel, dim3(static_cast<unsigned>(cdiv(a.D, 32)), LAYER ? 2 : 1), dim3(32, REDUCE_WARPS),
+                      s, a.part_w, a.part_b, parts, a.D, a.p_type, a.dw, a.db);
 }
 
 template <typename TX, typename TY>

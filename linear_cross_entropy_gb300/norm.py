@@ -19,7 +19,7 @@ from torch.autograd.function import once_differentiable
 from . import _lib
 
 TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 _l = _lib.load()
 _layer_forward, _layer_backward = _l.cce_layer_norm_forward, _l.cce_layer_norm_backward
@@ -60,6 +60,7 @@ def _check(x, weight, bias, name="x"):
         raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
     if x.dtype not in TYPES:
         raise ValueError(f"{name} must be bfloat16, float16 or float32, got {x.dtype}")
+    index = x.get_device()
     shape = x.shape
     if not shape or shape[-1] < 1:
         raise ValueError(f"{name} needs a last dimension of at least one element, got shape {tuple(shape)}")
@@ -68,11 +69,11 @@ def _check(x, weight, bias, name="x"):
     for what, p in (("weight", weight), ("bias", bias)):
         if p is None:
             continue
-        if p.device != x.device:
+        if p.get_device() != index:
             raise ValueError(f"{what} must be on {x.device}, got {p.device}")
         if p.dtype not in TYPES:
             raise ValueError(f"{what} must be bfloat16, float16 or float32, got {p.dtype}")
-        if p.dim() != 1 or p.shape[0] != D or not p.is_contiguous():
+        if p.shape != (D,) or not p.is_contiguous():
             raise ValueError(f"{what} must be contiguous [{D}], got shape {tuple(p.shape)}")
         if p_type is not None and p.dtype != p_type:
             raise ValueError(f"weight and bias must have one type, got {p_type} and {p.dtype}")
@@ -94,7 +95,14 @@ def _ptr(t):
 
 
 def _on_device(x):
-    return x.device.index == torch.cuda.current_device()
+    return x.get_device() == _current_device()
+
+
+def _result(x, dtype):
+    """A contiguous tensor of x's shape."""
+    if dtype == x.dtype and x.is_contiguous():
+        return torch.empty_like(x)
+    return torch.empty(x.shape, dtype=dtype, device=x.device)
 
 
 def cce_layer_norm_forward(x, weight=None, bias=None, eps=1e-5, *, out_dtype=None, stats=True, stream=None):
@@ -110,12 +118,13 @@ def cce_layer_norm_forward(x, weight=None, bias=None, eps=1e-5, *, out_dtype=Non
             return cce_layer_norm_forward(x, weight, bias, eps, out_dtype=out_dtype, stats=stats)
     dev = x.device
     x, inner, row, outer = _rows(x)
-    y = torch.empty(x.shape, dtype=y_type, device=dev)
+    y = _result(x, y_type)
     mean = torch.empty(N, dtype=torch.float32, device=dev) if stats else None
     rstd = torch.empty(N, dtype=torch.float32, device=dev) if stats else None
     st = _layer_forward(x.data_ptr(), inner, row, outer, TYPES[x.dtype], _ptr(weight), _ptr(bias), TYPES[p_type], N,
-                        D, eps, y.data_ptr(), TYPES[y_type], _ptr(mean), _ptr(rstd), _raw_stream(dev.index))
-    _lib.check(st, "cce_layer_norm_forward")
+                        D, eps, y.data_ptr(), TYPES[y_type], _ptr(mean), _ptr(rstd), _raw_stream(x.get_device()))
+    if st:
+        _lib.check(st, "cce_layer_norm_forward")
     return y, mean, rstd
 
 
@@ -132,23 +141,24 @@ def cce_rms_norm_forward(x, weight=None, eps=1e-6, *, weight_offset=0.0, out_dty
             return cce_rms_norm_forward(x, weight, eps, weight_offset=weight_offset, out_dtype=out_dtype, stats=stats)
     dev = x.device
     x, inner, row, outer = _rows(x)
-    y = torch.empty(x.shape, dtype=y_type, device=dev)
+    y = _result(x, y_type)
     rstd = torch.empty(N, dtype=torch.float32, device=dev) if stats else None
     st = _rms_forward(x.data_ptr(), inner, row, outer, TYPES[x.dtype], _ptr(weight), TYPES[p_type], weight_offset, N,
-                      D, eps, y.data_ptr(), TYPES[y_type], _ptr(rstd), _raw_stream(dev.index))
-    _lib.check(st, "cce_rms_norm_forward")
+                      D, eps, y.data_ptr(), TYPES[y_type], _ptr(rstd), _raw_stream(x.get_device()))
+    if st:
+        _lib.check(st, "cce_rms_norm_forward")
     return y, rstd
 
 
 def _check_backward(grad_y, x, N, stats):
-    if not grad_y.is_cuda or grad_y.device != x.device:
+    if grad_y.get_device() != x.get_device():
         raise ValueError(f"grad_y must be on {x.device}, got {grad_y.device}")
     if grad_y.shape != x.shape:
         raise ValueError(f"grad_y must have the shape of x, {tuple(x.shape)}, got {tuple(grad_y.shape)}")
     if grad_y.dtype != x.dtype and (x.dtype != torch.float32 or grad_y.dtype not in TYPES):
         raise ValueError(f"grad_y must be {x.dtype}, or a 16-bit type for float32 x, got {grad_y.dtype}")
     for what, s in stats:
-        if s.device != x.device or s.dtype != torch.float32 or s.numel() != N or not s.is_contiguous():
+        if s.get_device() != x.get_device() or s.dtype != torch.float32 or s.numel() != N or not s.is_contiguous():
             raise ValueError(f"{what} must be contiguous float32 with {N} values on {x.device}")
 
 
@@ -174,15 +184,16 @@ def cce_layer_norm_backward(grad_y, x, weight, mean, rstd, *, need_dx=True, need
     dev = x.device
     x, xi, xr, xo = _rows(x)
     grad_y, gi, gr, go = _rows(grad_y)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if need_dx else None
+    dx = _result(x, x.dtype) if need_dx else None
     dw = torch.empty(D, dtype=p_type, device=dev) if need_dweight else None
     db = torch.empty(D, dtype=p_type, device=dev) if need_dbias else None
     need = _workspace_bytes(N, D) if need_dweight or need_dbias else 0
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     st = _layer_backward(grad_y.data_ptr(), gi, gr, go, TYPES[grad_y.dtype], x.data_ptr(), xi, xr, xo, TYPES[x.dtype],
                          _ptr(weight), TYPES[p_type], mean.data_ptr(), rstd.data_ptr(), N, D, _ptr(dx), _ptr(dw),
-                         _ptr(db), _ptr(ws), need, _raw_stream(dev.index))
-    _lib.check(st, "cce_layer_norm_backward")
+                         _ptr(db), _ptr(ws), need, _raw_stream(x.get_device()))
+    if st:
+        _lib.check(st, "cce_layer_norm_backward")
     return dx, dw, db
 
 
@@ -203,14 +214,15 @@ def cce_rms_norm_backward(grad_y, x, weight, rstd, *, weight_offset=0.0, need_dx
     dev = x.device
     x, xi, xr, xo = _rows(x)
     grad_y, gi, gr, go = _rows(grad_y)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if need_dx else None
+    dx = _result(x, x.dtype) if need_dx else None
     dw = torch.empty(D, dtype=p_type, device=dev) if need_dweight and weight is not None else None
     need = _workspace_bytes(N, D) if dw is not None else 0
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     st = _rms_backward(grad_y.data_ptr(), gi, gr, go, TYPES[grad_y.dtype], x.data_ptr(), xi, xr, xo, TYPES[x.dtype],
                        _ptr(weight), TYPES[p_type], weight_offset, rstd.data_ptr(), N, D, _ptr(dx), _ptr(dw),
-                       _ptr(ws), need, _raw_stream(dev.index))
-    _lib.check(st, "cce_rms_norm_backward")
+                       _ptr(ws), need, _raw_stream(x.get_device()))
+    if st:
+        _lib.check(st, "cce_rms_norm_backward")
     return dx, dw
 
 
