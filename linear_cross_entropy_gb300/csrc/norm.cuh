@@ -18,6 +18,7 @@
 
 #include "elements.cuh"
 #include "norm.h"
+#include "ptx.cuh"
 
 namespace cce {
 namespace norm {
@@ -92,14 +93,11 @@ __device__ __forceinline__ void load_bias(const void* b, int p_type, int64_t c, 
   }
 }
 
-// The K vectors of a thread as fp32 pairs, E = K * VEC / 2 of them.  With VEC = 1 a
-// pair is two of the thread's columns.
+// Pair i of the K * VEC / 2 fp32 pairs in the K vectors of a thread.  With VEC = 1
+// a pair is two of the thread's columns.
 template <typename T, int VEC, int K>
-__device__ __forceinline__ void unpack(const Vec<T, VEC> (&v)[K], Pair (&p)[K * VEC / 2]) {
-#pragma unroll
-  for (int i = 0; i < K * VEC / 2; ++i) {
-    p[i] = Pair::of(v[2 * i / VEC].get(2 * i % VEC), v[(2 * i + 1) / VEC].get((2 * i + 1) % VEC));
-  }
+__device__ __forceinline__ Pair pair_of(const Vec<T, VEC> (&v)[K], int i) {
+  return Pair::of(v[2 * i / VEC].get(2 * i % VEC), v[(2 * i + 1) / VEC].get((2 * i + 1) % VEC));
 }
 
 // Whether a thread holds its vector k.  Every thread holds the first KF, so
@@ -247,7 +245,8 @@ __global__ void __launch_bounds__(MAX_THREADS) fwd_kernel(NormFwd a) {
   for (; base < a.N; base += step) {
     const int64_t n = base + threadIdx.y;
     Pair d[E];
-    unpack<TX, VEC, K>(xv, d);
+#pragma unroll
+    for (int i = 0; i < E; ++i) d[i] = pair_of<TX, VEC, K>(xv, i);
     load_row(n + step);
     float mean = 0.0f;
     if (LAYER) {
@@ -371,7 +370,8 @@ __global__ void __launch_bounds__(MAX_THREADS) fwd_long_kernel(NormFwd a) {
 // Persistent blocks, one per SM: a group walks rows at a stride of all groups,
 // and each thread keeps the parameter gradients of its own columns in registers
 // over all of them.  At the end a block adds its groups in order and writes one
-// partial row; reduce_kernel adds the blocks in order.
+// partial row; reduce_kernel adds the blocks in order.  Few rows are left to the
+// blocks of one cluster, which add their sums themselves: no second launch.
 //
 // The columns' sums are what fills the registers, so a thread holds 16 values of
 // a row (32 in rows that need it) and a row is spread over more threads than in
@@ -381,10 +381,16 @@ constexpr int bwd_threads() {
   return !LAYER && sizeof(TX) == 2 && VEC > 1 && K * VEC <= 16 ? 768 : 512;
 }
 
+__device__ __forceinline__ float load_cluster(uint32_t addr) {
+  float f;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(addr) : "memory");
+  return f;
+}
+
 template <typename TX, typename TY, int VEC, int K, int KF, bool LAYER, bool PREFETCH>
 __global__ void __launch_bounds__(bwd_threads<TX, VEC, K, LAYER>(), 1) bwd_kernel(NormBwd a) {
   constexpr int E = K * VEC / 2;
-  extern __shared__ __align__(16) float shared[];  // the gain [D]; at the end [groups][D] sums
+  extern __shared__ __align__(16) float shared[];  // the gain [D]; at the end the groups' sums
   __shared__ float2 sm[2][bwd_threads<TX, VEC, K, LAYER>() / 32];
   const int l = threadIdx.x, tpr = blockDim.x, groups = blockDim.y;
   const int vecs = a.D / VEC, slot = threadIdx.y * (tpr >> 5);
@@ -450,15 +456,14 @@ __global__ void __launch_bounds__(bwd_threads<TX, VEC, K, LAYER>(), 1) bwd_kerne
     const Pair r = Pair::both(row_rstd), m = Pair::both(-row_mean * row_rstd);
     float2 s;
     {
-      Pair xp[E], dp[E], s1 = Pair::both(0.0f), s2 = Pair::both(0.0f);
-      unpack<TX, VEC, K>(x, xp);
-      unpack<TY, VEC, K>(g, dp);
+      Pair s1 = Pair::both(0.0f), s2 = Pair::both(0.0f);
       auto gather = [&](int i, Pair w) {
-        const Pair z = LAYER ? fma(xp[i], r, m) : mul(xp[i], r);
-        const Pair t = mul(dp[i], w);
-        aw[i] = fma(dp[i], z, aw[i]);
+        const Pair xp = pair_of<TX, VEC, K>(x, i), dp = pair_of<TY, VEC, K>(g, i);
+        const Pair z = LAYER ? fma(xp, r, m) : mul(xp, r);
+        const Pair t = mul(dp, w);
+        aw[i] = fma(dp, z, aw[i]);
         if (LAYER) {
-          ab[i] = add(ab[i], dp[i]);
+          ab[i] = add(ab[i], dp);
           s1 = add(s1, t);
         }
         s2 = fma(t, z, s2);
@@ -487,13 +492,11 @@ __global__ void __launch_bounds__(bwd_threads<TX, VEC, K, LAYER>(), 1) bwd_kerne
     if (n >= a.N) continue;
     TX* dx = static_cast<TX*>(a.dx) + n * a.D;
     const Pair c1 = Pair::both(-s.x * inv_d * row_rstd), c2 = Pair::both(-s.y * inv_d * row_rstd);
-    Pair xp[E], dp[E];
-    unpack<TX, VEC, K>(x, xp);
-    unpack<TY, VEC, K>(g, dp);
     // rstd (g - sum(g) / D - z sum(g z) / D)
     auto grad = [&](int i, Pair w) {
-      const Pair z = LAYER ? fma(xp[i], r, m) : mul(xp[i], r);
-      return fma(mul(dp[i], w), r, LAYER ? fma(z, c2, c1) : mul(z, c2)).get();
+      const Pair xp = pair_of<TX, VEC, K>(x, i), dp = pair_of<TY, VEC, K>(g, i);
+      const Pair z = LAYER ? fma(xp, r, m) : mul(xp, r);
+      return fma(mul(dp, w), r, LAYER ? fma(z, c2, c1) : mul(z, c2)).get();
     };
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -517,32 +520,69 @@ __global__ void __launch_bounds__(bwd_threads<TX, VEC, K, LAYER>(), 1) bwd_kerne
     }
   }
 
+  // Several groups: their sums side by side in shared memory (the weight's, then
+  // the bias's), added in order.  One group: straight into the partial row.
+  if (!a.dw && !a.db) return;
+  const bool side_by_side = groups > 1 || a.cluster;
+  if (side_by_side) __syncthreads();  // the gain has been read
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * a.D;
 #pragma unroll
   for (int pass = 0; pass < (LAYER ? 2 : 1); ++pass) {
     if (!(pass == 0 ? a.dw : a.db)) continue;
-    float* part = (pass == 0 ? a.part_w : a.part_b) + static_cast<int64_t>(blockIdx.x) * a.D;
-    if (groups > 1) __syncthreads();  // the gain, or the other pass's sums, have been read
+    float* part =
+        side_by_side ? shared + (pass * groups + threadIdx.y) * a.D : (pass == 0 ? a.part_w : a.part_b) + row;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if (holds<KF>(k, vecs)) {
-        const int c = (l + k * tpr) * VEC;
-        float* to = groups > 1 ? shared + threadIdx.y * a.D + c : part + c;
+      if (!holds<KF>(k, vecs)) continue;
+      float* to = part + (l + k * tpr) * VEC;
+      if constexpr (VEC == 1) {
+        const float2 t = (pass == 0 ? aw : ab)[LAYER || pass == 0 ? k / 2 : 0].get();
+        *to = k & 1 ? t.y : t.x;
+      } else {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float2 t = (pass == 0 ? aw : ab)[LAYER || pass == 0 ? (k * VEC + e) / 2 : 0].get();
-          to[e] = (k * VEC + e) & 1 ? t.y : t.x;
+        for (int h = 0; h < VEC / 4; ++h) {
+          const int i = LAYER || pass == 0 ? k * VEC / 2 + 2 * h : 0;
+          const float2 t = (pass == 0 ? aw : ab)[i].get(), u = (pass == 0 ? aw : ab)[LAYER || pass == 0 ? i + 1 : 0].get();
+          reinterpret_cast<float4*>(to)[h] = make_float4(t.x, t.y, u.x, u.y);
         }
       }
     }
-    if (groups > 1) {
-      __syncthreads();
-      for (int c = threadIdx.y * tpr + l; c < a.D; c += tpr * groups) {
-        float t = 0.0f;
-        for (int g = 0; g < groups; ++g) t += shared[g * a.D + c];
-        part[c] = t;
-      }
+  }
+  if (!side_by_side) return;
+  __syncthreads();
+  const int tid = threadIdx.y * tpr + l, threads = tpr * groups;
+  for (int c = tid; c < a.D; c += threads) {
+    float t = 0.0f, u = 0.0f;
+    if (a.dw) {
+      for (int g = 0; g < groups; ++g) t += shared[g * a.D + c];
+    }
+    if (LAYER && a.db) {
+      for (int g = 0; g < groups; ++g) u += shared[(groups + g) * a.D + c];
+    }
+    if (a.cluster) {  // only this thread reads or writes column c of this block
+      shared[c] = t;
+      if (LAYER) shared[groups * a.D + c] = u;
+    } else {
+      if (a.dw) a.part_w[row + c] = t;
+      if (LAYER && a.db) a.part_b[row + c] = u;
     }
   }
+  if (!a.cluster) return;
+  // The grid is one cluster: the blocks share out the columns and add one
+  // another's sums in the order of their ranks.
+  cluster_sync();
+  const uint32_t at = smem_u32(shared), ranks = gridDim.x;
+  for (int c = static_cast<int>(blockIdx.x) * threads + tid; c < a.D; c += static_cast<int>(ranks) * threads) {
+    float t = 0.0f, u = 0.0f;
+    for (uint32_t r = 0; r < ranks; ++r) {
+      const uint32_t other = mapa_shared(at, r);
+      t += load_cluster(other + 4u * c);
+      if (LAYER) u += load_cluster(other + 4u * (groups * a.D + c));
+    }
+    if (a.dw) store_param(a.dw, a.p_type, c, t);
+    if (LAYER && a.db) store_param(a.db, a.p_type, c, u);
+  }
+  cluster_sync();  // no block leaves while another reads its sums
 }
 
 // Rows too long for the registers of one block: grad_x by one block per row in
@@ -629,9 +669,10 @@ __global__ void __launch_bounds__(128) cols_kernel(NormBwd a) {
 }
 
 // The parameter gradients from `parts` partial rows (0 parts: zeros).  A block
-// adds 32 columns: its warps take the parts w, w + 16, ... in order, and warp 0
-// adds the warps in order.  blockIdx.y = 0: the weight's, 1: the bias's.
-constexpr int REDUCE_WARPS = 16;
+// adds 32 columns: its warps take the parts w, w + 32, ... in order (five of 152,
+// all in flight at once), and warp 0 adds the warps in order.  blockIdx.y = 0:
+// the weight's, 1: the bias's.
+constexpr int REDUCE_WARPS = 32;
 static __global__ void __launch_bounds__(32 * REDUCE_WARPS) reduce_kernel(const float* part_w, const float* part_b,
                                                                           int parts, int D, int p_type, void* dw,
                                                                           void* db) {
@@ -643,7 +684,7 @@ static __global__ void __launch_bounds__(32 * REDUCE_WARPS) reduce_kernel(const 
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
   float s = 0.0f;
   if (c < D) {
-#pragma unroll 4
+#pragma unroll 5
     for (int p = threadIdx.y; p < parts; p += REDUCE_WARPS) s += part[static_cast<int64_t>(p) * D + c];
   }
   ws[threadIdx.y][threadIdx.x] = s;
@@ -733,19 +774,44 @@ cudaError_t fwd(const NormFwd& a, cudaStream_t s, int* launches) {
   return cudaGetLastError();
 }
 
+constexpr int CLUSTER = 8;  // blocks, the portable limit
+#ifndef CLUSTER_ROWS
+#define CLUSTER_ROWS 1
+#endif
+
 template <typename TX, typename TY, int VEC, int K, int KF, bool LAYER>
 cudaError_t run_bwd(const NormBwd& a, int tpr, int* parts, cudaStream_t s) {
-  constexpr bool PREFETCH = K * VEC <= 16;
+  // Where the sums of 24 values and the two rows fit beside each other: not those of a layer norm.
+  constexpr bool PREFETCH = K * VEC <= (LAYER ? 16 : 24);
   const int groups = std::max(1, bwd_threads<TX, VEC, K, LAYER>() / tpr);
-  *parts = static_cast<int>(std::min<int64_t>({NORM_MAX_PARTS, a.sms, cdiv(a.N, groups)}));
-  const int smem = static_cast<int>(sizeof(float)) * groups * a.D;
+  NormBwd b = a;
+  b.cluster = (a.dw || a.db) && a.N <= static_cast<int64_t>(CLUSTER_ROWS) * CLUSTER * groups;
+  int blocks = static_cast<int>(std::min<int64_t>({NORM_MAX_PARTS, a.sms, cdiv(a.N, groups)}));
+  if (b.cluster) {
+    int size = 1;
+    while (size < blocks && size < CLUSTER) size *= 2;
+    blocks = size;
+  }
+  *parts = b.cluster ? 0 : blocks;
+  auto kernel = bwd_kernel<TX, TY, VEC, K, KF, LAYER, PREFETCH>;
+  const int smem = static_cast<int>(sizeof(float)) * a.D * ((groups > 1 || b.cluster) && LAYER ? 2 * groups : groups);
   if (smem > PLAIN_SMEM) {
-    const cudaError_t e = cudaFuncSetAttribute(bwd_kernel<TX, TY, VEC, K, KF, LAYER, PREFETCH>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  bwd_kernel<TX, TY, VEC, K, KF, LAYER, PREFETCH><<<*parts, dim3(tpr, groups), smem, s>>>(a);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = b.cluster ? static_cast<unsigned>(blocks) : 1u;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(tpr, groups);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, b);
 }
 
 // Launches bwd_kernel for rows that the registers of one block hold; false for longer ones.
@@ -765,9 +831,12 @@ bool bwd_in_registers(const NormBwd& a, int* parts, cudaStream_t s, cudaError_t*
       }
       return true;
     }
-    tpr = group_threads(vecs, 2 * K);
-    if (tpr > bwd_threads<TX, VEC, 2 * K, LAYER>()) return false;
-    *e = run_bwd<TX, TY, VEC, 2 * K, K, LAYER>(a, tpr, parts, s);
+    if (vecs > 2 * K * MAX_THREADS) return false;
+    // as few values a thread as 512 threads allow
+    const bool most_values = vecs > 3 * K / 2 * MAX_THREADS;
+    tpr = group_threads(vecs, most_values ? 2 * K : 3 * K / 2);
+    *e = most_values ? run_bwd<TX, TY, VEC, 2 * K, 3 * K / 2, LAYER>(a, tpr, parts, s)
+                     : run_bwd<TX, TY, VEC, 3 * K / 2, K, LAYER>(a, tpr, parts, s);
   } else {
     const int K = vecs <= 32 ? 4 : vecs <= 16 * MAX_THREADS ? 16 : 32;
     const int tpr = group_threads(vecs, K);
@@ -801,7 +870,7 @@ cudaError_t bwd(const NormBwd& a, cudaStream_t s, int* launches) {
     }
     if (e != cudaSuccess) return e;
   }
-  if (!a.dw && !a.db) return cudaSuccess;
+  if ((!a.dw && !a.db) || (a.N > 0 && parts == 0)) return cudaSuccess;  // parts == 0: the cluster has written them
   ++*launches;
   return launch_after(reduce_kernel, dim3(static_cast<unsigned>(cdiv(a.D, 32)), LAYER ? 2 : 1), dim3(32, REDUCE_WARPS),
                       s, a.part_w, a.part_b, parts, a.D, a.p_type, a.dw, a.db);

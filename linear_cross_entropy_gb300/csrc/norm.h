@@ -50,7 +50,8 @@ struct NormBwd {
   float* part_b;  // [parts][D]
   int p_type, N, D;
   float offset;
-  int sms;  // of the device
+  int sms;            // of the device
+  bool cluster = false;  // the launcher's: the grid is one cluster that writes dw and db
 };
 
 // Blocks whose partial parameter gradients are added at the end, at most.
