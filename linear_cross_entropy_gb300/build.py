@@ -22,8 +22,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libcce.so")
-SOURCES = ("cce_api.cu", "gemm_kernels.cu", "cce_noalloc.cu", "cce_sort.cu", "cce_flce.cu", "norm_api.cu",
-           "norm_bf16.cu", "norm_f16.cu", "norm_f32.cu", "grad_clip.cu")
+SOURCES = ("cce_api.cu", "gemm_kernels.cu", "cce_noalloc.cu", "cce_sort.cu", "cce_flce.cu", "grad_clip.cu",
+           "norm_api.cu") + tuple(f"norm_{p}_{t}.cu" for p in ("fwd", "bwd")
+                                  for t in ("bf16", "f16", "f32", "f32_bf16", "f32_f16"))
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -80,6 +80,44 @@ struct Vec {
       *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(w[0]);
     }
   }
+  // Elements lo .. hi - 1 alone, the others 0.
+  __device__ __forceinline__ void load_some(const T* p, int lo, int hi) {
+    zero();
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      if (e >= lo && e < hi) {
+        if constexpr (sizeof(T) == 4) {
+          w[e] = __ldg(reinterpret_cast<const uint32_t*>(p) + e);
+        } else {
+          w[e / 2] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(p) + e)) << (16 * (e & 1));
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void store_some(T* p, int lo, int hi) const {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      if (e >= lo && e < hi) {
+        if constexpr (sizeof(T) == 4) {
+          reinterpret_cast<uint32_t*>(p)[e] = w[e];
+        } else {
+          reinterpret_cast<uint16_t*>(p)[e] = static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)));
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void keep(int lo, int hi) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      if (e < lo || e >= hi) {
+        if constexpr (sizeof(T) == 4) {
+          w[e] = 0u;
+        } else {
+          w[e / 2] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
+        }
+      }
+    }
+  }
   __device__ __forceinline__ float get(int i) const {
     if constexpr (sizeof(T) == 4) {
       return __uint_as_float(w[i]);

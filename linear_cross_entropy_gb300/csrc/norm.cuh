@@ -9,6 +9,12 @@
 // words, reduced, and written.  The variance is the sum of squared deviations
 // from the mean, taken over the registers, so nothing cancels.
 //
+// Rows whose starts are not 16-byte aligned (odd widths) are read and written in
+// aligned vectors all the same (SHIFTED): vector v of row n covers the columns
+// v * VEC - s ... with s = n * D mod VEC, the same s for every matrix of the call,
+// and only the row's two end vectors are partial.  Where the matrices disagree
+// on s, VEC is 1.
+//
 // A row belongs to a group of threadIdx.x = 0 .. tpr - 1 (tpr a power of two up
 // to 32, or a multiple of 32); a block has blockDim.y groups.  Thread l of a
 // group holds the vectors l, l + tpr, ..., K of them.
@@ -100,41 +106,106 @@ __device__ __forceinline__ Pair pair_of(const Vec<T, VEC> (&v)[K], int i) {
   return Pair::of(v[2 * i / VEC].get(2 * i % VEC), v[(2 * i + 1) / VEC].get((2 * i + 1) % VEC));
 }
 
-// Whether a thread holds its vector k.  Every thread holds the first KF, so
-// that only the others are checked.
-template <int KF>
-__device__ __forceinline__ bool holds(int k, int vecs) {
-  return k < KF || static_cast<int>(threadIdx.x + k * blockDim.x) < vecs;
-}
+// Where a row lies in a thread's vectors.  Every row has the first KF vectors of
+// every thread, so that only the others are checked.
+template <int VEC, int KF, bool SHIFTED>
+struct Place {
+  int D, vecs;    // columns; vectors that a row may touch
+  int s = 0;      // columns by which the row starts inside vector 0
+  int used;       // vectors that this row touches
 
-// Parameters in shared memory as fp32.  The vectors' float4 quarters lie apart,
-// so that a warp's 16-byte reads fall on consecutive addresses.
-template <int VEC>
-__device__ __forceinline__ void put_param(float* sm, int vecs, int c, const float (&f)[VEC]) {
-  if constexpr (VEC == 1) {
-    sm[c] = f[0];
-  } else {
-#pragma unroll
-    for (int h = 0; h < VEC / 4; ++h)
-      reinterpret_cast<float4*>(sm)[h * vecs + c] = make_float4(f[4 * h], f[4 * h + 1], f[4 * h + 2], f[4 * h + 3]);
-  }
-}
-
-template <int VEC>
-__device__ __forceinline__ void get_param(const float* sm, int vecs, int c, float (&f)[VEC]) {
-  if constexpr (VEC == 1) {
-    f[0] = sm[c];
-  } else {
-#pragma unroll
-    for (int h = 0; h < VEC / 4; ++h) {
-      const float4 v = reinterpret_cast<const float4*>(sm)[h * vecs + c];
-      f[4 * h] = v.x;
-      f[4 * h + 1] = v.y;
-      f[4 * h + 2] = v.z;
-      f[4 * h + 3] = v.w;
+  __device__ __forceinline__ explicit Place(int d)
+      : D(d), vecs(SHIFTED ? (d + 2 * VEC - 2) / VEC : d / VEC), used(vecs) {}
+  __device__ __forceinline__ void row(int64_t n) {
+    if constexpr (SHIFTED) {
+      s = static_cast<int>(n * (D & (VEC - 1))) & (VEC - 1);
+      used = (D + s + VEC - 1) / VEC;
     }
   }
-}
+  __device__ __forceinline__ int vec(int k) const { return static_cast<int>(threadIdx.x + k * blockDim.x); }
+  __device__ __forceinline__ bool has(int k) const { return k < KF || vec(k) < used; }
+  __device__ __forceinline__ int column(int k) const { return vec(k) * VEC - s; }  // of the vector's first element
+  // The elements lo .. hi - 1 of vector k are the row's.
+  __device__ __forceinline__ int lo(int k) const { return SHIFTED ? max(0, -column(k)) : 0; }
+  __device__ __forceinline__ int hi(int k) const { return SHIFTED ? min(VEC, D - column(k)) : VEC; }
+  __device__ __forceinline__ bool whole(int k) const {
+    return !SHIFTED || (column(k) >= 0 && column(k) + VEC <= D);
+  }
+
+  // Vector k of the row at p; `last`: there may be no memory behind the row.
+  template <typename T>
+  __device__ __forceinline__ void load(Vec<T, VEC>& v, const T* p, int k, bool last) const {
+    if (whole(k)) {
+      v.load(p + column(k));
+    } else if (last) {
+      v.load_some(p + column(k), lo(k), hi(k));
+    } else {
+      v.load(p + column(k));
+      v.keep(lo(k), hi(k));
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(const Vec<T, VEC>& v, T* p, int k) const {
+    if (whole(k)) {
+      v.store(p + column(k));
+    } else {
+      v.store_some(p + column(k), lo(k), hi(k));
+    }
+  }
+
+  // Parameters in shared memory as fp32.  A vector's float4 quarters (SHIFTED: its
+  // elements) lie `vecs` apart, so that a warp's reads fall on consecutive addresses.
+  __device__ __forceinline__ int param_floats() const { return SHIFTED ? VEC * vecs : D; }
+  __device__ __forceinline__ void put_param(float* sm, int c, const float (&f)[VEC]) const {  // vector c of the D columns
+    if constexpr (SHIFTED || VEC == 1) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) sm[e * vecs + c] = f[e];
+    } else {
+#pragma unroll
+      for (int h = 0; h < VEC / 4; ++h)
+        reinterpret_cast<float4*>(sm)[h * vecs + c] = make_float4(f[4 * h], f[4 * h + 1], f[4 * h + 2], f[4 * h + 3]);
+    }
+  }
+  // Of the columns of vector k; any value for those that are not the row's.
+  __device__ __forceinline__ void get_param(const float* sm, int k, float (&f)[VEC]) const {
+    const int v = vec(k);
+    if constexpr (SHIFTED || VEC == 1) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const int at = e - s;  // column v * VEC + at; never before the first, never past the last of all planes
+        f[e] = sm[(at & (VEC - 1)) * vecs + v + (at < 0 ? -1 : 0)];
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < VEC / 4; ++h) {
+        const float4 q = reinterpret_cast<const float4*>(sm)[h * vecs + v];
+        f[4 * h] = q.x;
+        f[4 * h + 1] = q.y;
+        f[4 * h + 2] = q.z;
+        f[4 * h + 3] = q.w;
+      }
+    }
+  }
+  // All of a block's threads: the parameters of the D columns, 0 past them.
+  template <typename Load>
+  __device__ __forceinline__ void fill(float* sm, Load load) const {
+    const int tid = threadIdx.y * blockDim.x + threadIdx.x, threads = blockDim.x * blockDim.y;
+    for (int c = tid; c < vecs; c += threads) {
+      float f[VEC];
+      if constexpr (SHIFTED) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          float one[1] = {0.0f};
+          if (c * VEC + e < D) load(static_cast<int64_t>(c) * VEC + e, one);
+          f[e] = one[0];
+        }
+      } else {
+        load(static_cast<int64_t>(c) * VEC, f);
+      }
+      put_param(sm, c, f);
+    }
+  }
+};
 
 // ------------------------------------------------------------------ forward
 // Few rows: a block of up to 512 threads per row, so that a row's loads are all
@@ -207,43 +278,41 @@ __global__ void __launch_bounds__(MAX_THREADS) fwd_few_kernel(NormFwd a) {
 // A thread holds up to 64 values of a row, so that most rows are a warp's or
 // less and their sums are shuffles alone; the next row is loaded while this one
 // is reduced.  The parameters wait in shared memory as fp32.
-template <typename TX, typename TY, int VEC, int K, int KF, bool LAYER>
+template <typename TX, typename TY, int VEC, int K, int KF, bool LAYER, bool SHIFTED>
 __global__ void __launch_bounds__(MAX_THREADS) fwd_kernel(NormFwd a) {
   constexpr int E = K * VEC / 2;
-  extern __shared__ __align__(16) float params[];  // gain [D], then the bias [D] of a layer norm
+  extern __shared__ __align__(16) float gain[];  // then the bias of a layer norm
   __shared__ float sm[4][MAX_THREADS / 32];
-  const int l = threadIdx.x, tpr = blockDim.x, groups = blockDim.y;
-  const int vecs = a.D / VEC, slot = threadIdx.y * (tpr >> 5);
-  float* gain = params;
-  float* bias = params + a.D;
+  const int groups = blockDim.y, slot = threadIdx.y * (blockDim.x >> 5);
   const int step = gridDim.x * groups;
+  Place<VEC, KF, SHIFTED> next(a.D);
+  float* bias = gain + next.param_floats();
   Vec<TX, VEC> xv[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) xv[k].zero();
   auto load_row = [&](int64_t n) {
     if (n >= a.N) return;
+    next.row(n);
     const TX* x = static_cast<const TX*>(a.x) + a.xm.at(static_cast<int>(n));
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if (holds<KF>(k, vecs)) xv[k].load(x + (l + k * tpr) * VEC);
+      if (next.has(k)) {
+        next.load(xv[k], x, k, n == a.N - 1);
+      } else if (SHIFTED) {
+        xv[k].zero();
+      }
     }
   };
   int64_t base = static_cast<int64_t>(blockIdx.x) * groups;
   load_row(base + threadIdx.y);
-  for (int c = threadIdx.y * tpr + l; c < vecs; c += tpr * groups) {
-    float f[VEC];
-    load_gain<LAYER, VEC>(a.w, a.p_type, a.offset, static_cast<int64_t>(c) * VEC, f);
-    put_param<VEC>(gain, vecs, c, f);
-    if (LAYER) {
-      load_bias<LAYER, VEC>(a.b, a.p_type, static_cast<int64_t>(c) * VEC, f);
-      put_param<VEC>(bias, vecs, c, f);
-    }
-  }
+  next.fill(gain, [&](int64_t c, auto& f) { load_gain<LAYER>(a.w, a.p_type, a.offset, c, f); });
+  if (LAYER) next.fill(bias, [&](int64_t c, auto& f) { load_bias<LAYER>(a.b, a.p_type, c, f); });
   __syncthreads();
   const float fd = static_cast<float>(a.D);
   int buf = 0;
   for (; base < a.N; base += step) {
     const int64_t n = base + threadIdx.y;
+    const Place<VEC, KF, SHIFTED> place = next;
     Pair d[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) d[i] = pair_of<TX, VEC, K>(xv, i);
@@ -257,23 +326,37 @@ __global__ void __launch_bounds__(MAX_THREADS) fwd_kernel(NormFwd a) {
       const Pair minus = Pair::both(-mean);
 #pragma unroll
       for (int i = 0; i < E; ++i) d[i] = add(d[i], minus);
+      if constexpr (VEC == 1) {  // columns that are not there would add mean^2
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          const float2 f = d[i].get();
+          d[i] = Pair::of(place.has(2 * i) ? f.x : 0.0f, place.has(2 * i + 1) ? f.y : 0.0f);
+        }
+      } else if constexpr (SHIFTED) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          if (!place.whole(k)) {
+            const int lo = place.lo(k), hi = place.hi(k);
+#pragma unroll
+            for (int i = 0; i < VEC / 2; ++i) {
+              const float2 f = d[k * VEC / 2 + i].get();
+              d[k * VEC / 2 + i] = Pair::of(2 * i >= lo && 2 * i < hi ? f.x : 0.0f,
+                                            2 * i + 1 >= lo && 2 * i + 1 < hi ? f.y : 0.0f);
+            }
+          }
+        }
+      }
     }
     Pair q[2] = {Pair::both(0.0f), Pair::both(0.0f)};
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      const int k0 = 2 * i / VEC, k1 = (2 * i + 1) / VEC;
-      if constexpr (LAYER && VEC == 1) {  // columns that are not there would add mean^2
-        const float2 f = d[i].get();
-        d[i] = Pair::of(holds<KF>(k0, vecs) ? f.x : 0.0f, holds<KF>(k1, vecs) ? f.y : 0.0f);
-        q[i & 1] = fma(d[i], d[i], q[i & 1]);
-      } else {
-        if (!LAYER || holds<KF>(k0, vecs)) q[i & 1] = fma(d[i], d[i], q[i & 1]);
-      }
+      // elsewhere a vector that is not there is 0
+      if (!LAYER || VEC == 1 || SHIFTED || place.has(2 * i / VEC)) q[i & 1] = fma(d[i], d[i], q[i & 1]);
     }
     const float rstd = 1.0f / sqrtf(group_sum(add(q[0], q[1]).sum(), sm[buf + 1] + slot) / fd + a.eps);
     buf ^= 2;  // the other slots for the next row: a slower warp may still read these
     if (n >= a.N) continue;
-    if (l == 0) {
+    if (threadIdx.x == 0) {
       if (LAYER && a.mean) a.mean[n] = mean;
       if (a.rstd) a.rstd[n] = rstd;
     }
@@ -283,11 +366,10 @@ __global__ void __launch_bounds__(MAX_THREADS) fwd_kernel(NormFwd a) {
     for (int i = 0; i < E; ++i) d[i] = mul(d[i], r);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if (holds<KF>(k, vecs)) {
-        const int c = l + k * tpr;
+      if (place.has(k)) {
         float w[VEC], b[VEC], o[VEC];
-        get_param<VEC>(gain, vecs, c, w);
-        if (LAYER) get_param<VEC>(bias, vecs, c, b);
+        place.get_param(gain, k, w);
+        if (LAYER) place.get_param(bias, k, b);
         if constexpr (VEC == 1) {
           const float2 f = d[k / 2].get();
           const float z = k & 1 ? f.y : f.x;
@@ -303,7 +385,7 @@ __global__ void __launch_bounds__(MAX_THREADS) fwd_kernel(NormFwd a) {
         }
         Vec<TY, VEC> out;
         out.set(o);
-        out.store(y + static_cast<int64_t>(c) * VEC);
+        place.store(out, y, k);
       }
     }
   }
@@ -387,16 +469,17 @@ __device__ __forceinline__ float load_cluster(uint32_t addr) {
   return f;
 }
 
-template <typename TX, typename TY, int VEC, int K, int KF, bool LAYER, bool PREFETCH>
+template <typename TX, typename TY, int VEC, int K, int KF, bool LAYER, bool SHIFTED, bool PREFETCH>
 __global__ void __launch_bounds__(bwd_threads<TX, VEC, K, LAYER>(), 1) bwd_kernel(NormBwd a) {
   constexpr int E = K * VEC / 2;
-  extern __shared__ __align__(16) float shared[];  // the gain [D]; at the end the groups' sums
+  extern __shared__ __align__(16) float shared[];  // the gain; at the end the groups' sums
   __shared__ float2 sm[2][bwd_threads<TX, VEC, K, LAYER>() / 32];
-  const int l = threadIdx.x, tpr = blockDim.x, groups = blockDim.y;
-  const int vecs = a.D / VEC, slot = threadIdx.y * (tpr >> 5);
+  const int l = threadIdx.x, tpr = blockDim.x, groups = blockDim.y, slot = threadIdx.y * (tpr >> 5);
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   const float inv_d = 1.0f / static_cast<float>(a.D);
 
+  // A group's rows are all shifted alike: there is one row, or `step` is a multiple of VEC.
+  Place<VEC, KF, SHIFTED> place(a.D);
   Vec<TX, VEC> xv[K];
   Vec<TY, VEC> gv[K];
   float mean = 0.0f, rstd = 0.0f;
@@ -406,9 +489,9 @@ __global__ void __launch_bounds__(bwd_threads<TX, VEC, K, LAYER>(), 1) bwd_kerne
       const TY* dy = static_cast<const TY*>(a.dy) + a.gm.at(static_cast<int>(n));
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        if (holds<KF>(k, vecs)) {
-          xv[k].load(x + (l + k * tpr) * VEC);
-          gv[k].load(dy + (l + k * tpr) * VEC);
+        if (place.has(k)) {
+          place.load(xv[k], x, k, n == a.N - 1);
+          place.load(gv[k], dy, k, n == a.N - 1);
         }
       }
       if (LAYER) mean = a.mean[n];
@@ -425,12 +508,9 @@ __global__ void __launch_bounds__(bwd_threads<TX, VEC, K, LAYER>(), 1) bwd_kerne
   }
   let_next_start();
   int64_t base = static_cast<int64_t>(blockIdx.x) * groups;
+  place.row(base + threadIdx.y);
   if (PREFETCH) load_row(base + threadIdx.y);
-  for (int c = threadIdx.y * tpr + l; c < vecs; c += tpr * groups) {
-    float f[VEC];
-    load_gain<LAYER, VEC>(a.w, a.p_type, a.offset, static_cast<int64_t>(c) * VEC, f);
-    put_param<VEC>(shared, vecs, c, f);
-  }
+  place.fill(shared, [&](int64_t c, auto& f) { load_gain<LAYER>(a.w, a.p_type, a.offset, c, f); });
   __syncthreads();
 
   Pair aw[E], ab[LAYER ? E : 1];
@@ -471,15 +551,15 @@ __global__ void __launch_bounds__(bwd_threads<TX, VEC, K, LAYER>(), 1) bwd_kerne
       if constexpr (VEC == 1) {
 #pragma unroll
         for (int k = 0; k < K; k += 2) {  // where a column is not there its dy is 0, and any gain does
-          gather(k / 2, Pair::of(shared[holds<KF>(k, vecs) ? l + k * tpr : 0],
-                                 shared[holds<KF>(k + 1, vecs) ? l + (k + 1) * tpr : 0]));
+          gather(k / 2, Pair::of(shared[place.has(k) ? place.vec(k) : 0],
+                                 shared[place.has(k + 1) ? place.vec(k + 1) : 0]));
         }
       } else {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-          if (!holds<KF>(k, vecs)) continue;
+          if (!place.has(k)) continue;
           float w[VEC];
-          get_param<VEC>(shared, vecs, l + k * tpr, w);
+          place.get_param(shared, k, w);
 #pragma unroll
           for (int i = 0; i < VEC / 2; ++i) gather(k * VEC / 2 + i, Pair::of(w[2 * i], w[2 * i + 1]));
         }
@@ -500,9 +580,9 @@ __global__ void __launch_bounds__(bwd_threads<TX, VEC, K, LAYER>(), 1) bwd_kerne
     };
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if (!holds<KF>(k, vecs)) continue;
+      if (!place.has(k)) continue;
       float w[VEC], f[VEC];
-      get_param<VEC>(shared, vecs, l + k * tpr, w);
+      place.get_param(shared, k, w);
       if constexpr (VEC == 1) {
         const float2 t = grad(k / 2, Pair::both(w[0]));
         f[0] = k & 1 ? t.y : t.x;
@@ -516,14 +596,14 @@ __global__ void __launch_bounds__(bwd_threads<TX, VEC, K, LAYER>(), 1) bwd_kerne
       }
       Vec<TX, VEC> out;
       out.set(f);
-      out.store(dx + (l + k * tpr) * VEC);
+      place.store(out, dx, k);
     }
   }
 
   // Several groups: their sums side by side in shared memory (the weight's, then
   // the bias's), added in order.  One group: straight into the partial row.
   if (!a.dw && !a.db) return;
-  const bool side_by_side = groups > 1 || a.cluster;
+  const bool side_by_side = SHIFTED || groups > 1 || a.cluster;
   if (side_by_side) __syncthreads();  // the gain has been read
   const int64_t row = static_cast<int64_t>(blockIdx.x) * a.D;
 #pragma unroll
@@ -531,18 +611,26 @@ __global__ void __launch_bounds__(bwd_threads<TX, VEC, K, LAYER>(), 1) bwd_kerne
     if (!(pass == 0 ? a.dw : a.db)) continue;
     float* part =
         side_by_side ? shared + (pass * groups + threadIdx.y) * a.D : (pass == 0 ? a.part_w : a.part_b) + row;
+    auto value = [&](int i) { return (pass == 0 ? aw : ab)[LAYER || pass == 0 ? i : 0].get(); };
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if (!holds<KF>(k, vecs)) continue;
-      float* to = part + (l + k * tpr) * VEC;
+      if (!place.has(k)) continue;
+      float* to = part + place.column(k);
       if constexpr (VEC == 1) {
-        const float2 t = (pass == 0 ? aw : ab)[LAYER || pass == 0 ? k / 2 : 0].get();
+        const float2 t = value(k / 2);
         *to = k & 1 ? t.y : t.x;
+      } else if constexpr (SHIFTED) {
+        const int lo = place.lo(k), hi = place.hi(k);
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) {
+          const float2 t = value(k * VEC / 2 + i);
+          if (2 * i >= lo && 2 * i < hi) to[2 * i] = t.x;
+          if (2 * i + 1 >= lo && 2 * i + 1 < hi) to[2 * i + 1] = t.y;
+        }
       } else {
 #pragma unroll
         for (int h = 0; h < VEC / 4; ++h) {
-          const int i = LAYER || pass == 0 ? k * VEC / 2 + 2 * h : 0;
-          const float2 t = (pass == 0 ? aw : ab)[i].get(), u = (pass == 0 ? aw : ab)[LAYER || pass == 0 ? i + 1 : 0].get();
+          const float2 t = value(k * VEC / 2 + 2 * h), u = value(k * VEC / 2 + 2 * h + 1);
           reinterpret_cast<float4*>(to)[h] = make_float4(t.x, t.y, u.x, u.y);
         }
       }
@@ -717,86 +805,120 @@ cudaError_t run_fwd_few(const NormFwd& a, int64_t vecs, cudaStream_t s) {
 constexpr int MAX_SMEM = 227 * 1024 - 2048;   // dynamic shared memory of a block, beside what the kernels declare
 constexpr int PLAIN_SMEM = 48 * 1024 - 2048;  // of a block that has not asked for more
 
-template <typename TX, typename TY, int VEC, int K, int KF, bool LAYER>
+// Vectors that a row may touch, and floats of its parameters in shared memory.
+template <int VEC, bool SHIFTED>
+int64_t row_vecs(int64_t D) {
+  return SHIFTED ? (D + 2 * VEC - 2) / VEC : D / VEC;
+}
+template <int VEC, bool SHIFTED>
+int64_t param_floats(int64_t D) {
+  return SHIFTED ? VEC * row_vecs<VEC, SHIFTED>(D) : D;
+}
+
+template <typename TX, typename TY, int VEC, int K, int KF, bool LAYER, bool SHIFTED>
 cudaError_t run_fwd(const NormFwd& a, int tpr, cudaStream_t s) {
-  const int smem = static_cast<int>(sizeof(float)) * a.D * (LAYER ? 2 : 1);
+  auto kernel = fwd_kernel<TX, TY, VEC, K, KF, LAYER, SHIFTED>;
+  const int smem = static_cast<int>(sizeof(float) * param_floats<VEC, SHIFTED>(a.D)) * (LAYER ? 2 : 1);
   // Two blocks of 256 threads fill an SM's registers; where their parameters do not fit twice, one of 512.
   const bool pair = 2 * (smem + 2048) <= MAX_SMEM;
   const int groups = std::max(1, (pair ? 256 : MAX_THREADS) / tpr);
   const int per_sm = std::max(1, MAX_THREADS / (tpr * groups));
   const int grid = static_cast<int>(std::min<int64_t>(cdiv(a.N, groups), a.sms * per_sm));
   if (smem > PLAIN_SMEM) {
-    const cudaError_t e = cudaFuncSetAttribute(fwd_kernel<TX, TY, VEC, K, KF, LAYER>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  fwd_kernel<TX, TY, VEC, K, KF, LAYER><<<grid, dim3(tpr, groups), smem, s>>>(a);
+  kernel<<<grid, dim3(tpr, groups), smem, s>>>(a);
   return cudaGetLastError();
 }
 
-template <typename TX, typename TY, int VEC, bool LAYER>
-cudaError_t fwd(const NormFwd& a, cudaStream_t s, int* launches) {
-  if (a.N == 0) return cudaSuccess;
-  ++*launches;
-  const int64_t vecs = a.D / VEC;
-  if (a.N <= a.sms) {
-    if (vecs <= MAX_THREADS) return run_fwd_few<TX, TY, VEC, 1, LAYER>(a, vecs, s);
-    if (vecs <= 4 * MAX_THREADS) return run_fwd_few<TX, TY, VEC, 4, LAYER>(a, vecs, s);
-  }
-  const bool fits = static_cast<int64_t>(sizeof(float)) * a.D * (LAYER ? 2 : 1) <= MAX_SMEM;
+// Launches fwd_kernel for rows that the registers of one block hold; false for longer ones.
+template <typename TX, typename TY, int VEC, bool LAYER, bool SHIFTED>
+bool fwd_in_registers(const NormFwd& a, cudaStream_t s, cudaError_t* e) {
+  const int64_t vecs = row_vecs<VEC, SHIFTED>(a.D);
+  if (static_cast<int64_t>(sizeof(float)) * param_floats<VEC, SHIFTED>(a.D) * (LAYER ? 2 : 1) > MAX_SMEM) return false;
   if constexpr (VEC > 1) {
     const int tpr = group_threads(vecs, vecs <= 64 ? 4 : 8);
-    if (fits && tpr <= MAX_THREADS) {
-      switch (cdiv(vecs, tpr)) {  // vectors a thread; all but its last are there in every thread
-        case 1: return run_fwd<TX, TY, VEC, 1, 0, LAYER>(a, tpr, s);
-        case 2: return run_fwd<TX, TY, VEC, 2, 1, LAYER>(a, tpr, s);
-        case 3: return run_fwd<TX, TY, VEC, 3, 2, LAYER>(a, tpr, s);
-        case 4: return run_fwd<TX, TY, VEC, 4, 3, LAYER>(a, tpr, s);
-        case 5: return run_fwd<TX, TY, VEC, 5, 4, LAYER>(a, tpr, s);
-        case 6: return run_fwd<TX, TY, VEC, 6, 5, LAYER>(a, tpr, s);
-        case 7: return run_fwd<TX, TY, VEC, 7, 6, LAYER>(a, tpr, s);
-        default: return run_fwd<TX, TY, VEC, 8, 7, LAYER>(a, tpr, s);
-      }
+    if (tpr > MAX_THREADS) return false;
+    switch (cdiv(vecs, tpr)) {  // vectors a thread; all but its last are there in every thread
+      case 1: *e = run_fwd<TX, TY, VEC, 1, 0, LAYER, SHIFTED>(a, tpr, s); break;
+      case 2: *e = run_fwd<TX, TY, VEC, 2, 1, LAYER, SHIFTED>(a, tpr, s); break;
+      case 3: *e = run_fwd<TX, TY, VEC, 3, 2, LAYER, SHIFTED>(a, tpr, s); break;
+      case 4: *e = run_fwd<TX, TY, VEC, 4, 3, LAYER, SHIFTED>(a, tpr, s); break;
+      case 5: *e = run_fwd<TX, TY, VEC, 5, 4, LAYER, SHIFTED>(a, tpr, s); break;
+      case 6: *e = run_fwd<TX, TY, VEC, 6, 5, LAYER, SHIFTED>(a, tpr, s); break;
+      case 7: *e = run_fwd<TX, TY, VEC, 7, 6, LAYER, SHIFTED>(a, tpr, s); break;
+      default: *e = run_fwd<TX, TY, VEC, 8, 7, LAYER, SHIFTED>(a, tpr, s); break;
     }
   } else {
-    const int K = vecs <= 32 ? 4 : vecs <= 128 ? 8 : vecs <= 512 ? 16 : 32;
+    const int K = vecs <= 32 ? 4 : vecs <= 128 ? 8 : 16;
     const int tpr = group_threads(vecs, K);
-    if (fits && tpr <= MAX_THREADS) {
-      switch (K) {
-        case 4: return run_fwd<TX, TY, VEC, 4, 0, LAYER>(a, tpr, s);
-        case 8: return run_fwd<TX, TY, VEC, 8, 4, LAYER>(a, tpr, s);
-        case 16: return run_fwd<TX, TY, VEC, 16, 8, LAYER>(a, tpr, s);
-        default: return run_fwd<TX, TY, VEC, 32, 16, LAYER>(a, tpr, s);
-      }
+    if (tpr > MAX_THREADS) return false;
+    switch (K) {
+      case 4: *e = run_fwd<TX, TY, VEC, 4, 0, LAYER, SHIFTED>(a, tpr, s); break;
+      case 8: *e = run_fwd<TX, TY, VEC, 8, 4, LAYER, SHIFTED>(a, tpr, s); break;
+      default: *e = run_fwd<TX, TY, VEC, 16, 8, LAYER, SHIFTED>(a, tpr, s); break;
     }
   }
+  return true;
+}
+
+// A block per row for few rows, and for those that are too long.
+template <typename TX, typename TY, int VEC, bool LAYER>
+bool fwd_few(const NormFwd& a, cudaStream_t s, cudaError_t* e) {
+  const int64_t vecs = a.D / VEC;
+  if (a.N > a.sms || vecs > 4 * MAX_THREADS) return false;
+  *e = vecs <= MAX_THREADS ? run_fwd_few<TX, TY, VEC, 1, LAYER>(a, vecs, s)
+                           : run_fwd_few<TX, TY, VEC, 4, LAYER>(a, vecs, s);
+  return true;
+}
+
+template <typename TX, typename TY, int VEC, bool LAYER>
+cudaError_t fwd_long(const NormFwd& a, cudaStream_t s) {
   fwd_long_kernel<TX, TY, VEC, LAYER><<<static_cast<unsigned>(a.N), MAX_THREADS, 0, s>>>(a);
   return cudaGetLastError();
 }
 
-constexpr int CLUSTER = 8;  // blocks, the portable limit
-#ifndef CLUSTER_ROWS
-#define CLUSTER_ROWS 1
-#endif
+template <typename TX, typename TY, bool LAYER>
+cudaError_t fwd(const NormFwd& a, Access access, cudaStream_t s, int* launches) {
+  constexpr int VEC = 16 / sizeof(TX);
+  if (a.N == 0) return cudaSuccess;
+  ++*launches;
+  cudaError_t e = cudaSuccess;
+  if (access == Access::WIDE) {
+    if (fwd_few<TX, TY, VEC, LAYER>(a, s, &e) || fwd_in_registers<TX, TY, VEC, LAYER, false>(a, s, &e)) return e;
+    return fwd_long<TX, TY, VEC, LAYER>(a, s);
+  }
+  if (fwd_few<TX, TY, 1, LAYER>(a, s, &e)) return e;
+  if (access == Access::SHIFTED && fwd_in_registers<TX, TY, VEC, LAYER, true>(a, s, &e)) return e;
+  if (fwd_in_registers<TX, TY, 1, LAYER, false>(a, s, &e)) return e;
+  return fwd_long<TX, TY, 1, LAYER>(a, s);
+}
 
-template <typename TX, typename TY, int VEC, int K, int KF, bool LAYER>
+constexpr int CLUSTER = 8;  // blocks, the portable limit
+template <typename TX, typename TY, int VEC, int K, int KF, bool LAYER, bool SHIFTED>
 cudaError_t run_bwd(const NormBwd& a, int tpr, int* parts, cudaStream_t s) {
   // Where the sums of 24 values and the two rows fit beside each other: not those of a layer norm.
   constexpr bool PREFETCH = K * VEC <= (LAYER ? 16 : 24);
+  auto kernel = bwd_kernel<TX, TY, VEC, K, KF, LAYER, SHIFTED, PREFETCH>;
   const int groups = std::max(1, bwd_threads<TX, VEC, K, LAYER>() / tpr);
   NormBwd b = a;
-  b.cluster = (a.dw || a.db) && a.N <= static_cast<int64_t>(CLUSTER_ROWS) * CLUSTER * groups;
-  int blocks = static_cast<int>(std::min<int64_t>({NORM_MAX_PARTS, a.sms, cdiv(a.N, groups)}));
+  // One row a group at most: 18.3 us a call from Python against 23.5 with a second launch, the GPU's time within 1 us.
+  b.cluster = (a.dw || a.db) && a.N <= static_cast<int64_t>(CLUSTER) * groups;
+  // In multiples of 8 blocks, so that a group's rows are all shifted alike.
+  int blocks = static_cast<int>(std::min<int64_t>(std::min(NORM_MAX_PARTS, std::max(8, a.sms / 8 * 8)),
+                                                  cdiv(a.N, groups)));
   if (b.cluster) {
     int size = 1;
-    while (size < blocks && size < CLUSTER) size *= 2;
+    while (size < blocks) size *= 2;
     blocks = size;
   }
   *parts = b.cluster ? 0 : blocks;
-  auto kernel = bwd_kernel<TX, TY, VEC, K, KF, LAYER, PREFETCH>;
-  const int smem = static_cast<int>(sizeof(float)) * a.D * ((groups > 1 || b.cluster) && LAYER ? 2 * groups : groups);
+  const int64_t sums = static_cast<int64_t>(a.D) * groups * (LAYER && (SHIFTED || groups > 1 || b.cluster) ? 2 : 1);
+  const int64_t smem = static_cast<int64_t>(sizeof(float)) * std::max(sums, param_floats<VEC, SHIFTED>(a.D));
   if (smem > PLAIN_SMEM) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
   cudaLaunchAttribute attr{};
@@ -815,19 +937,18 @@ cudaError_t run_bwd(const NormBwd& a, int tpr, int* parts, cudaStream_t s) {
 }
 
 // Launches bwd_kernel for rows that the registers of one block hold; false for longer ones.
-template <typename TX, typename TY, int VEC, bool LAYER>
+template <typename TX, typename TY, int VEC, bool LAYER, bool SHIFTED>
 bool bwd_in_registers(const NormBwd& a, int* parts, cudaStream_t s, cudaError_t* e) {
-  const int64_t vecs = a.D / VEC;
+  const int64_t vecs = row_vecs<VEC, SHIFTED>(a.D);
   if constexpr (VEC > 1) {
     constexpr int K = 16 / VEC;
-    const int most = bwd_threads<TX, VEC, K, LAYER>();
     int tpr = group_threads(vecs, K);
-    if (tpr <= most) {
+    if (tpr <= bwd_threads<TX, VEC, K, LAYER>()) {
       switch (cdiv(vecs, tpr)) {  // vectors a thread; all but its last are there in every thread
-        case 1: *e = run_bwd<TX, TY, VEC, 1, 0, LAYER>(a, tpr, parts, s); break;
-        case 2: *e = run_bwd<TX, TY, VEC, 2, 1, LAYER>(a, tpr, parts, s); break;
-        case 3: *e = run_bwd<TX, TY, VEC, K < 3 ? 2 : 3, K < 3 ? 1 : 2, LAYER>(a, tpr, parts, s); break;
-        default: *e = run_bwd<TX, TY, VEC, K, K - 1, LAYER>(a, tpr, parts, s); break;
+        case 1: *e = run_bwd<TX, TY, VEC, 1, 0, LAYER, SHIFTED>(a, tpr, parts, s); break;
+        case 2: *e = run_bwd<TX, TY, VEC, 2, 1, LAYER, SHIFTED>(a, tpr, parts, s); break;
+        case 3: *e = run_bwd<TX, TY, VEC, K < 3 ? 2 : 3, K < 3 ? 1 : 2, LAYER, SHIFTED>(a, tpr, parts, s); break;
+        default: *e = run_bwd<TX, TY, VEC, K, K - 1, LAYER, SHIFTED>(a, tpr, parts, s); break;
       }
       return true;
     }
@@ -835,38 +956,45 @@ bool bwd_in_registers(const NormBwd& a, int* parts, cudaStream_t s, cudaError_t*
     // as few values a thread as 512 threads allow
     const bool most_values = vecs > 3 * K / 2 * MAX_THREADS;
     tpr = group_threads(vecs, most_values ? 2 * K : 3 * K / 2);
-    *e = most_values ? run_bwd<TX, TY, VEC, 2 * K, 3 * K / 2, LAYER>(a, tpr, parts, s)
-                     : run_bwd<TX, TY, VEC, 3 * K / 2, K, LAYER>(a, tpr, parts, s);
+    *e = most_values ? run_bwd<TX, TY, VEC, 2 * K, 3 * K / 2 - 1, LAYER, SHIFTED>(a, tpr, parts, s)
+                     : run_bwd<TX, TY, VEC, 3 * K / 2, K - 1, LAYER, SHIFTED>(a, tpr, parts, s);
   } else {
-    const int K = vecs <= 32 ? 4 : vecs <= 16 * MAX_THREADS ? 16 : 32;
+    const int K = vecs <= 32 ? 4 : 16;
     const int tpr = group_threads(vecs, K);
     if (tpr > MAX_THREADS) return false;
-    switch (K) {
-      case 4: *e = run_bwd<TX, TY, VEC, 4, 0, LAYER>(a, tpr, parts, s); break;
-      case 16: *e = run_bwd<TX, TY, VEC, 16, 8, LAYER>(a, tpr, parts, s); break;
-      default: *e = run_bwd<TX, TY, VEC, 32, 16, LAYER>(a, tpr, parts, s); break;
-    }
+    *e = K == 4 ? run_bwd<TX, TY, VEC, 4, 0, LAYER, SHIFTED>(a, tpr, parts, s)
+                : run_bwd<TX, TY, VEC, 16, 8, LAYER, SHIFTED>(a, tpr, parts, s);
   }
   return true;
 }
 
 template <typename TX, typename TY, int VEC, bool LAYER>
-cudaError_t bwd(const NormBwd& a, cudaStream_t s, int* launches) {
+cudaError_t bwd_long(const NormBwd& a, int* parts, cudaStream_t s, int* launches) {
+  if (a.dx) bwd_long_kernel<TX, TY, VEC, LAYER><<<static_cast<unsigned>(a.N), MAX_THREADS, 0, s>>>(a);
+  if (a.dw || a.db) {
+    const int64_t tiles = cdiv(a.D / VEC, 128);
+    *parts =
+        static_cast<int>(std::min<int64_t>({NORM_MAX_PARTS, cdiv(a.N, 8), std::max<int64_t>(1, 8 * a.sms / tiles)}));
+    *launches += a.dx ? 1 : 0;
+    cols_kernel<TX, TY, VEC, LAYER>
+        <<<dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(*parts)), 128, 0, s>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+template <typename TX, typename TY, bool LAYER>
+cudaError_t bwd(const NormBwd& a, Access access, cudaStream_t s, int* launches) {
+  constexpr int VEC = 16 / sizeof(TX);
   int parts = 0;
   if (a.N > 0 && (a.dx || a.dw || a.db)) {
     ++*launches;
     cudaError_t e = cudaSuccess;
-    if (!bwd_in_registers<TX, TY, VEC, LAYER>(a, &parts, s, &e)) {
-      if (a.dx) bwd_long_kernel<TX, TY, VEC, LAYER><<<static_cast<unsigned>(a.N), MAX_THREADS, 0, s>>>(a);
-      if (a.dw || a.db) {
-        const int64_t tiles = cdiv(a.D / VEC, 128);
-        parts = static_cast<int>(
-            std::min<int64_t>({NORM_MAX_PARTS, cdiv(a.N, 8), std::max<int64_t>(1, 8 * a.sms / tiles)}));
-        *launches += a.dx ? 1 : 0;
-        cols_kernel<TX, TY, VEC, LAYER>
-            <<<dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(parts)), 128, 0, s>>>(a);
-      }
-      e = cudaGetLastError();
+    if (access == Access::WIDE) {
+      if (!bwd_in_registers<TX, TY, VEC, LAYER, false>(a, &parts, s, &e))
+        e = bwd_long<TX, TY, VEC, LAYER>(a, &parts, s, launches);
+    } else if (!(access == Access::SHIFTED && bwd_in_registers<TX, TY, VEC, LAYER, true>(a, &parts, s, &e)) &&
+               !bwd_in_registers<TX, TY, 1, LAYER, false>(a, &parts, s, &e)) {
+      e = bwd_long<TX, TY, 1, LAYER>(a, &parts, s, launches);
     }
     if (e != cudaSuccess) return e;
   }
@@ -874,20 +1002,6 @@ cudaError_t bwd(const NormBwd& a, cudaStream_t s, int* launches) {
   ++*launches;
   return launch_after(reduce_kernel, dim3(static_cast<unsigned>(cdiv(a.D, 32)), LAYER ? 2 : 1), dim3(32, REDUCE_WARPS),
                       s, a.part_w, a.part_b, parts, a.D, a.p_type, a.dw, a.db);
-}
-
-template <typename TX, typename TY>
-cudaError_t fwd_any(const NormFwd& a, bool layer, bool wide, cudaStream_t s, int* launches) {
-  constexpr int VEC = 16 / sizeof(TX);
-  if (layer) return wide ? fwd<TX, TY, VEC, true>(a, s, launches) : fwd<TX, TY, 1, true>(a, s, launches);
-  return wide ? fwd<TX, TY, VEC, false>(a, s, launches) : fwd<TX, TY, 1, false>(a, s, launches);
-}
-
-template <typename TX, typename TY>
-cudaError_t bwd_any(const NormBwd& a, bool layer, bool wide, cudaStream_t s, int* launches) {
-  constexpr int VEC = 16 / sizeof(TX);
-  if (layer) return wide ? bwd<TX, TY, VEC, true>(a, s, launches) : bwd<TX, TY, 1, true>(a, s, launches);
-  return wide ? bwd<TX, TY, VEC, false>(a, s, launches) : bwd<TX, TY, 1, false>(a, s, launches);
 }
 
 }  // namespace norm

@@ -57,13 +57,20 @@ struct NormBwd {
 // Blocks whose partial parameter gradients are added at the end, at most.
 constexpr int NORM_MAX_PARTS = 304;
 
-// y_type is what x_type allows (the entry points check); `layer` picks layer norm or RMS norm;
-// `wide` says that every pointer and stride allows 16-byte accesses of x.
-cudaError_t launch_norm_fwd_bf16(const NormFwd& a, bool layer, bool wide, cudaStream_t s, int* launches);
-cudaError_t launch_norm_fwd_f16(const NormFwd& a, bool layer, bool wide, cudaStream_t s, int* launches);
-cudaError_t launch_norm_fwd_f32(const NormFwd& a, int y_type, bool layer, bool wide, cudaStream_t s, int* launches);
-cudaError_t launch_norm_bwd_bf16(const NormBwd& a, bool layer, bool wide, cudaStream_t s, int* launches);
-cudaError_t launch_norm_bwd_f16(const NormBwd& a, bool layer, bool wide, cudaStream_t s, int* launches);
-cudaError_t launch_norm_bwd_f32(const NormBwd& a, int y_type, bool layer, bool wide, cudaStream_t s, int* launches);
+// How rows can be read and written: in aligned 16-byte vectors of x; in such
+// vectors that the row's start divides, alike in every matrix; element by element.
+enum class Access { WIDE, SHIFTED, SINGLE };
+
+// The pair of types is one the entry points allow; `layer` picks layer norm or RMS norm.
+cudaError_t launch_norm_fwd_bf16(const NormFwd& a, bool layer, Access access, cudaStream_t s, int* launches);
+cudaError_t launch_norm_fwd_f16(const NormFwd& a, bool layer, Access access, cudaStream_t s, int* launches);
+cudaError_t launch_norm_fwd_f32(const NormFwd& a, bool layer, Access access, cudaStream_t s, int* launches);
+cudaError_t launch_norm_fwd_f32_bf16(const NormFwd& a, bool layer, Access access, cudaStream_t s, int* launches);
+cudaError_t launch_norm_fwd_f32_f16(const NormFwd& a, bool layer, Access access, cudaStream_t s, int* launches);
+cudaError_t launch_norm_bwd_bf16(const NormBwd& a, bool layer, Access access, cudaStream_t s, int* launches);
+cudaError_t launch_norm_bwd_f16(const NormBwd& a, bool layer, Access access, cudaStream_t s, int* launches);
+cudaError_t launch_norm_bwd_f32(const NormBwd& a, bool layer, Access access, cudaStream_t s, int* launches);
+cudaError_t launch_norm_bwd_f32_bf16(const NormBwd& a, bool layer, Access access, cudaStream_t s, int* launches);
+cudaError_t launch_norm_bwd_f32_f16(const NormBwd& a, bool layer, Access access, cudaStream_t s, int* launches);
 
 }  // namespace cce

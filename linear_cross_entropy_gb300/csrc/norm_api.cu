@@ -11,6 +11,7 @@
 namespace cce {
 namespace {
 
+constexpr int64_t SHIFTED_MIN = 64;  // columns from which a row's two partial vectors are the lesser part
 constexpr int64_t LIMIT = int64_t(1) << 31;
 
 struct Rows {
@@ -31,6 +32,11 @@ RowMap row_map(const Rows& r) {
 // Whether rows at p can be read and written `vec` elements at a time.
 bool rows_wide(const void* p, const Rows& r, int type, int vec) {
   return multiple(p, std::min(16, vec * type_bytes(type))) && r.row_stride % vec == 0 && r.outer_stride % vec == 0;
+}
+// Whether every row of a matrix starts at its index times D, modulo vec, from an aligned base.
+bool rows_shifted(const void* p, const Rows& r, int type, int vec, int64_t N, int64_t D) {
+  return multiple(p, std::min(16, vec * type_bytes(type))) && r.inner >= N &&
+         (N <= 1 || (r.row_stride >= D && (r.row_stride - D) % vec == 0));
 }
 bool param_wide(const void* p, int type, int vec) { return multiple(p, std::min(16, vec * type_bytes(type))); }
 
@@ -55,15 +61,24 @@ cce_status forward(const void* x, const Rows& xr, int x_type, const void* w, con
   const cce_status st = static_cast<cce_status>(device_ready(&sms));
   if (st != CCE_OK) return st;
   const int vec = 16 / type_bytes(x_type);
-  const bool wide = D % vec == 0 && rows_wide(x, xr, x_type, vec) && rows_wide(y, Rows{1, D, 0}, y_type, vec) &&
-                    param_wide(w, p_type, vec) && param_wide(b, p_type, vec);
+  const Rows dense{N, D, 0};
+  const Access access = D % vec == 0 && rows_wide(x, xr, x_type, vec) && rows_wide(y, dense, y_type, vec) &&
+                                param_wide(w, p_type, vec) && param_wide(b, p_type, vec)
+                            ? Access::WIDE
+                        : D >= SHIFTED_MIN && rows_shifted(x, xr, x_type, vec, N, D) &&
+                                rows_shifted(y, dense, y_type, vec, N, D)
+                            ? Access::SHIFTED
+                            : Access::SINGLE;
   const NormFwd a{x,    row_map(xr), w,      b,   y, mean, rstd, p_type, static_cast<int>(N), static_cast<int>(D),
                   eps, offset, sms};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int launches = 0;
-  const cudaError_t e = x_type == CCE_F32    ? launch_norm_fwd_f32(a, y_type, layer, wide, s, &launches)
-                        : x_type == CCE_BF16 ? launch_norm_fwd_bf16(a, layer, wide, s, &launches)
-                                             : launch_norm_fwd_f16(a, layer, wide, s, &launches);
+  const auto launch = x_type == CCE_BF16  ? launch_norm_fwd_bf16
+                      : x_type == CCE_F16   ? launch_norm_fwd_f16
+                      : y_type == CCE_F32   ? launch_norm_fwd_f32
+                      : y_type == CCE_BF16  ? launch_norm_fwd_f32_bf16
+                                            : launch_norm_fwd_f32_f16;
+  const cudaError_t e = launch(a, layer, access, s, &launches);
   count_launches(launches);
   return status_of(e);
 }
@@ -86,8 +101,14 @@ cce_status backward(const void* dy, const Rows& gr, int y_type, const void* x, c
   const cce_status st = static_cast<cce_status>(device_ready(&sms));
   if (st != CCE_OK) return st;
   const int vec = 16 / type_bytes(x_type);
-  const bool wide = D % vec == 0 && rows_wide(x, xr, x_type, vec) && rows_wide(dy, gr, y_type, vec) &&
-                    rows_wide(dx, Rows{1, D, 0}, x_type, vec) && param_wide(w, p_type, vec);
+  const Rows dense{N, D, 0};
+  const Access access = D % vec == 0 && rows_wide(x, xr, x_type, vec) && rows_wide(dy, gr, y_type, vec) &&
+                                rows_wide(dx, dense, x_type, vec) && param_wide(w, p_type, vec)
+                            ? Access::WIDE
+                        : D >= SHIFTED_MIN && rows_shifted(x, xr, x_type, vec, N, D) &&
+                                rows_shifted(dy, gr, y_type, vec, N, D) && rows_shifted(dx, dense, x_type, vec, N, D)
+                            ? Access::SHIFTED
+                            : Access::SINGLE;
   char* ws = static_cast<char*>(workspace);
   const NormBwd a{dy,
                   row_map(gr),
@@ -108,9 +129,12 @@ cce_status backward(const void* dy, const Rows& gr, int y_type, const void* x, c
                   sms};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int launches = 0;
-  const cudaError_t e = x_type == CCE_F32    ? launch_norm_bwd_f32(a, y_type, layer, wide, s, &launches)
-                        : x_type == CCE_BF16 ? launch_norm_bwd_bf16(a, layer, wide, s, &launches)
-                                             : launch_norm_bwd_f16(a, layer, wide, s, &launches);
+  const auto launch = x_type == CCE_BF16  ? launch_norm_bwd_bf16
+                      : x_type == CCE_F16   ? launch_norm_bwd_f16
+                      : y_type == CCE_F32   ? launch_norm_bwd_f32
+                      : y_type == CCE_BF16  ? launch_norm_bwd_f32_bf16
+                                            : launch_norm_bwd_f32_f16;
+  const cudaError_t e = launch(a, layer, access, s, &launches);
   count_launches(launches);
   return status_of(e);
 }

@@ -98,6 +98,55 @@ def test_many_rows(cce, N, D):
         _check(cce, x, w, b, dy, layer)
 
 
+@pytest.mark.parametrize("layer", [True, False])
+@pytest.mark.parametrize("x_type,y_type", PAIRS)
+@pytest.mark.parametrize("N,D", [(5001, 333), (2003, 1003), (1700, 65), (333, 4099), (190, 9001)])
+def test_many_odd_rows(cce, layer, x_type, y_type, N, D):
+    """Rows that start at any place of a 16-byte word, several to a thread group."""
+    x, w, b, dy = _inputs(N + D, (N, D), x_type, y_type, F32)
+    _check(cce, x, w, b, dy, layer, out_dtype=y_type)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_odd_rows_at_a_pitch(cce, dtype):
+    """Odd widths inside wider matrices: at pitches that keep every matrix's rows
+    alike (a multiple of 16 bytes more), at others, and overlapping windows."""
+    for D, pitch in [(333, 333 + 16), (333, 340), (1001, 1001 + 8), (129, 250)]:
+        x, w, b, dy = _inputs(D + pitch, (700, pitch), dtype, dtype, dtype)
+        for layer in (True, False):
+            _check(cce, x[:, :D], w[:D].contiguous(), b[:D].contiguous(), dy[:, :D].contiguous(), layer)
+            _check(cce, x[:, :D], w[:D].contiguous(), b[:D].contiguous(), dy[:, :D], layer)
+    flat, w, b, dy = _inputs(3, (2000,), dtype, dtype, dtype)
+    windows = flat.as_strided((900, 129), (1, 1))
+    _check(cce, windows, w[:129].contiguous(), b[:129].contiguous(), torch.randn(900, 129, device="cuda").to(dtype), True)
+
+
+@pytest.mark.parametrize("N,D", [(1, 65), (3, 333), (500, 1001), (2000, 67), (40, 4097)])
+def test_nothing_is_written_outside_the_results(cce, N, D):
+    """y, dx and the parameters' gradients between guard values, through the C ABI."""
+    from linear_cross_entropy_gb300 import _lib
+    lib = _lib.load()
+    x, w, b, dy = _inputs(N + D, (N, D), BF16, BF16, BF16)
+    guard = 64
+    y, dx = (torch.full((guard + N * D + guard,), 7.0, device="cuda", dtype=BF16) for _ in range(2))
+    dw, db = (torch.full((guard + D + guard,), 7.0, device="cuda", dtype=BF16) for _ in range(2))
+    mean, rstd = (torch.full((guard + N + guard,), 7.0, device="cuda") for _ in range(2))
+    at = lambda t: t.data_ptr() + guard * t.element_size()  # noqa: E731
+    stream = torch.cuda.current_stream().cuda_stream
+    assert lib.cce_layer_norm_forward(x.data_ptr(), N, D, 0, 2, w.data_ptr(), b.data_ptr(), 2, N, D, 1e-5, at(y), 2,
+                                      at(mean), at(rstd), stream) == 0
+    need = lib.cce_norm_backward_workspace_bytes(N, D)
+    ws = torch.full((need + 4096,), 85, device="cuda", dtype=torch.uint8)
+    assert lib.cce_layer_norm_backward(dy.data_ptr(), N, D, 0, 2, x.data_ptr(), N, D, 0, 2, w.data_ptr(), 2, at(mean),
+                                       at(rstd), N, D, at(dx), at(dw), at(db), ws.data_ptr(), need, stream) == 0
+    want = cce.cce_layer_norm_forward(x, w, b)
+    dwant = cce.cce_layer_norm_backward(dy, x, w, *want[1:])
+    for t, ref in zip((y, mean, rstd, dx, dw, db), want + dwant):
+        assert (t[:guard] == 7.0).all() and (t[-guard:] == 7.0).all()
+        assert torch.equal(t[guard:-guard], ref.reshape(-1))
+    assert (ws[need:] == 85).all()
+
+
 def test_weight_offset_and_missing_parameters(cce):
     x, w, b, dy = _inputs(5, (37, 520), BF16, BF16, BF16)
     _check(cce, x, w - 1, None, dy, False, offset=1.0)
