@@ -31,8 +31,13 @@ namespace norm {
 
 constexpr int MAX_THREADS = 512;
 
+// Over `width` neighbouring lanes (a power of two); every step is there, those that cross groups add nothing.
 __device__ __forceinline__ float lanes_sum(float v, int width) {
-  for (int o = width >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float t = __shfl_xor_sync(0xffffffffu, v, o);
+    if (o < width) v += t;
+  }
   return v;
 }
 
@@ -45,32 +50,53 @@ __device__ __forceinline__ void group_sync() {
   }
 }
 
-// Sum over the group; sm has one slot for each of the group's warps.
+// Slots in shared memory for one value of every warp of a block, each group's
+// padded to a multiple of four.
+constexpr int slots(int threads) { return threads / 16; }
+__device__ __forceinline__ int group_slots() { return ((blockDim.x >> 5) + 3) & ~3; }
+
+// Lane 0 of a warp puts its value, of the last warp zeros behind it too.
+__device__ __forceinline__ void put_slot(float* sm, float v) {
+  const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  sm[warp] = v;
+  if (warp == warps - 1) {
+    for (int i = warps; i & 3; ++i) sm[i] = 0.0f;
+  }
+}
+
+// Sum over the group; sm: the group's slots.
 __device__ __forceinline__ float group_sum(float v, float* sm) {
   const int tpr = blockDim.x;
-  if (tpr <= 32) return lanes_sum(v, tpr);
-  v = lanes_sum(v, 32);
-  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
+  v = lanes_sum(v, min(tpr, 32));
+  if (tpr <= 32) return v;
+  if ((threadIdx.x & 31) == 0) put_slot(sm, v);
   group_sync();
   float t = 0.0f;
-  for (int i = 0; i < tpr >> 5; ++i) t += sm[i];
+#pragma unroll 1
+  for (int i = 0; i < tpr >> 5; i += 4) {
+    const float4 q = *reinterpret_cast<const float4*>(sm + i);
+    t += (q.x + q.y) + (q.z + q.w);
+  }
   return t;
 }
 
-// Of two values; without BOTH, of .y alone.
-template <bool BOTH>
-__device__ __forceinline__ float2 group_sum2(float2 v, float2* sm) {
+// Of two values; sm: the group's slots for the first, `second` floats on those for the second.
+__device__ __forceinline__ float2 group_sum2(float2 v, float* sm, int second) {
   const int tpr = blockDim.x;
-  const int width = tpr < 32 ? tpr : 32;
-  if (BOTH) v.x = lanes_sum(v.x, width);
-  v.y = lanes_sum(v.y, width);
+  v.x = lanes_sum(v.x, min(tpr, 32));
+  v.y = lanes_sum(v.y, min(tpr, 32));
   if (tpr <= 32) return v;
-  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
+  if ((threadIdx.x & 31) == 0) {
+    put_slot(sm, v.x);
+    put_slot(sm + second, v.y);
+  }
   group_sync();
   float2 t = make_float2(0.0f, 0.0f);
-  for (int i = 0; i < tpr >> 5; ++i) {
-    if (BOTH) t.x += sm[i].x;
-    t.y += sm[i].y;
+#pragma unroll 1
+  for (int i = 0; i < tpr >> 5; i += 4) {
+    const float4 p = *reinterpret_cast<const float4*>(sm + i), q = *reinterpret_cast<const float4*>(sm + second + i);
+    t.x += (p.x + p.y) + (p.z + p.w);
+    t.y += (q.x + q.y) + (q.z + q.w);
   }
   return t;
 }
@@ -132,17 +158,20 @@ struct Place {
     return !SHIFTED || (column(k) >= 0 && column(k) + VEC <= D);
   }
 
-  // Vector k of the row at p; `last`: there may be no memory behind the row.
+  // Vector k of the row at p; `last`: there may be no memory behind the row.  The
+  // vector brings its neighbours' elements: trim() drops them, once it is used
+  // (here it would wait for the load).
   template <typename T>
   __device__ __forceinline__ void load(Vec<T, VEC>& v, const T* p, int k, bool last) const {
-    if (whole(k)) {
-      v.load(p + column(k));
-    } else if (last) {
+    if (SHIFTED && last && !whole(k)) {
       v.load_some(p + column(k), lo(k), hi(k));
     } else {
       v.load(p + column(k));
-      v.keep(lo(k), hi(k));
     }
+  }
+  template <typename T>
+  __device__ __forceinline__ void trim(Vec<T, VEC>& v, int k) const {
+    if (SHIFTED && !whole(k)) v.keep(lo(k), hi(k));
   }
   template <typename T>
   __device__ __forceinline__ void store(const Vec<T, VEC>& v, T* p, int k) const {
@@ -212,7 +241,7 @@ struct Place {
 // in flight at once; parameters are loaded beside them.
 template <typename TX, typename TY, int VEC, int K, bool LAYER>
 __global__ void __launch_bounds__(MAX_THREADS) fwd_few_kernel(NormFwd a) {
-  __shared__ float sm[2][MAX_THREADS / 32];
+  __shared__ __align__(16) float sm[2][slots(MAX_THREADS)];
   const int l = threadIdx.x, tpr = blockDim.x;
   const int64_t n = blockIdx.x;
   const TX* x = static_cast<const TX*>(a.x) + a.xm.at(static_cast<int>(n));
@@ -282,8 +311,8 @@ template <typename TX, typename TY, int VEC, int K, int KF, bool LAYER, bool SHI
 __global__ void __launch_bounds__(MAX_THREADS) fwd_kernel(NormFwd a) {
   constexpr int E = K * VEC / 2;
   extern __shared__ __align__(16) float gain[];  // then the bias of a layer norm
-  __shared__ float sm[4][MAX_THREADS / 32];
-  const int groups = blockDim.y, slot = threadIdx.y * (blockDim.x >> 5);
+  __shared__ __align__(16) float sm[4][slots(MAX_THREADS)];
+  const int groups = blockDim.y, slot = threadIdx.y * group_slots();
   const int step = gridDim.x * groups;
   Place<VEC, KF, SHIFTED> next(a.D);
   float* bias = gain + next.param_floats();
@@ -313,6 +342,8 @@ __global__ void __launch_bounds__(MAX_THREADS) fwd_kernel(NormFwd a) {
   for (; base < a.N; base += step) {
     const int64_t n = base + threadIdx.y;
     const Place<VEC, KF, SHIFTED> place = next;
+#pragma unroll
+    for (int k = 0; k < K; ++k) place.trim(xv[k], k);
     Pair d[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) d[i] = pair_of<TX, VEC, K>(xv, i);
@@ -395,7 +426,7 @@ __global__ void __launch_bounds__(MAX_THREADS) fwd_kernel(NormFwd a) {
 // reads it once per sum and once more to write (from L2 after the first time).
 template <typename TX, typename TY, int VEC, bool LAYER>
 __global__ void __launch_bounds__(MAX_THREADS) fwd_long_kernel(NormFwd a) {
-  __shared__ float sm[2][MAX_THREADS / 32];
+  __shared__ __align__(16) float sm[2][slots(MAX_THREADS)];
   const int64_t n = blockIdx.x;
   const TX* x = static_cast<const TX*>(a.x) + a.xm.at(static_cast<int>(n));
   const float fd = static_cast<float>(a.D);
@@ -473,8 +504,9 @@ template <typename TX, typename TY, int VEC, int K, int KF, bool LAYER, bool SHI
 __global__ void __launch_bounds__(bwd_threads<TX, VEC, K, LAYER>(), 1) bwd_kernel(NormBwd a) {
   constexpr int E = K * VEC / 2;
   extern __shared__ __align__(16) float shared[];  // the gain; at the end the groups' sums
-  __shared__ float2 sm[2][bwd_threads<TX, VEC, K, LAYER>() / 32];
-  const int l = threadIdx.x, tpr = blockDim.x, groups = blockDim.y, slot = threadIdx.y * (tpr >> 5);
+  constexpr int SLOTS = slots(bwd_threads<TX, VEC, K, LAYER>());
+  __shared__ __align__(16) float sm[2][2][SLOTS];
+  const int l = threadIdx.x, tpr = blockDim.x, groups = blockDim.y, slot = threadIdx.y * group_slots();
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   const float inv_d = 1.0f / static_cast<float>(a.D);
 
@@ -529,6 +561,8 @@ __global__ void __launch_bounds__(bwd_threads<TX, VEC, K, LAYER>(), 1) bwd_kerne
     for (int k = 0; k < K; ++k) {
       x[k] = xv[k];
       g[k] = gv[k];
+      place.trim(x[k], k);
+      place.trim(g[k], k);
     }
     const float row_rstd = rstd, row_mean = mean;
     if (PREFETCH) load_row(n + step);
@@ -567,7 +601,7 @@ __global__ void __launch_bounds__(bwd_threads<TX, VEC, K, LAYER>(), 1) bwd_kerne
       s = make_float2(LAYER ? s1.sum() : 0.0f, s2.sum());
     }
     if (!a.dx) continue;
-    s = group_sum2<LAYER>(s, sm[buf] + slot);
+    s = LAYER ? group_sum2(s, sm[buf][0] + slot, SLOTS) : make_float2(0.0f, group_sum(s.y, sm[buf][0] + slot));
     buf ^= 1;  // the other slots for the next row: a slower warp may still read these
     if (n >= a.N) continue;
     TX* dx = static_cast<TX*>(a.dx) + n * a.D;
@@ -677,7 +711,7 @@ __global__ void __launch_bounds__(bwd_threads<TX, VEC, K, LAYER>(), 1) bwd_kerne
 // two passes over it, the parameter gradients column-wise by cols_kernel.
 template <typename TX, typename TY, int VEC, bool LAYER>
 __global__ void __launch_bounds__(MAX_THREADS) bwd_long_kernel(NormBwd a) {
-  __shared__ float2 sm[MAX_THREADS / 32];
+  __shared__ __align__(16) float sm[2][slots(MAX_THREADS)];
   const int64_t n = blockIdx.x;
   const TX* x = static_cast<const TX*>(a.x) + a.xm.at(static_cast<int>(n));
   const TY* dy = static_cast<const TY*>(a.dy) + a.gm.at(static_cast<int>(n));
@@ -701,7 +735,7 @@ __global__ void __launch_bounds__(MAX_THREADS) bwd_long_kernel(NormBwd a) {
       s.y += g * z;
     }
   }
-  s = group_sum2<LAYER>(s, sm);
+  s = LAYER ? group_sum2(s, sm[0], slots(MAX_THREADS)) : make_float2(0.0f, group_sum(s.y, sm[0]));
   s.x *= inv_d;
   s.y *= inv_d;
 #pragma unroll 2

@@ -15,10 +15,10 @@ struct RowMap {
   int64_t row_stride, outer_stride;
   int inner;
 
-  __device__ __forceinline__ int64_t at(int n) const {
+  __device__ __forceinline__ int64_t at(int64_t n) const {
     if (n < inner) return n * row_stride;
-    const int o = n / inner;
-    return o * outer_stride + (n - o * inner) * row_stride;
+    const int o = static_cast<int>(n) / inner;
+    return o * outer_stride + (n - static_cast<int64_t>(o) * inner) * row_stride;
   }
 };
 
