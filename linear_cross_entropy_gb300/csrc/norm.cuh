@@ -897,11 +897,16 @@ bool fwd_in_registers(const NormFwd& a, cudaStream_t s, cudaError_t* e) {
   return true;
 }
 
-// A block per row for few rows, and for those that are too long.
+// A block per row while an SM has four rows or 16 KiB of them at most.  Measured
+// on both sides (bf16 layer norm): 608 x 2,048 3.6 us against 3.9 by the
+// persistent groups, 912 x 2,048 4.6 against 3.9; 304 x 4,096 3.6 against 4.5,
+// 608 x 4,096 5.2 against 4.4.
 template <typename TX, typename TY, int VEC, bool LAYER>
 bool fwd_few(const NormFwd& a, cudaStream_t s, cudaError_t* e) {
   const int64_t vecs = a.D / VEC;
-  if (a.N > a.sms || vecs > 4 * MAX_THREADS) return false;
+  if (a.N > 4 * a.sms || static_cast<int64_t>(sizeof(TX)) * a.N * a.D > int64_t(16384) * a.sms ||
+      vecs > 4 * MAX_THREADS)
+    return false;
   *e = vecs <= MAX_THREADS ? run_fwd_few<TX, TY, VEC, 1, LAYER>(a, vecs, s)
                            : run_fwd_few<TX, TY, VEC, 4, LAYER>(a, vecs, s);
   return true;
