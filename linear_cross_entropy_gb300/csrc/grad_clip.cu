@@ -204,6 +204,7 @@ __global__ void __launch_bounds__(THREADS, 4) norm_kernel(const __grid_constant_
                                                        double* part) {
   const bool inf = norm_type == CCE_NORM_INF;
   let_next_start();
+  wait_for_previous();
   Gather g;
   for (uint32_t c = blockIdx.x; c < b.chunks; c += gridDim.x) {
     const Tensor& t = b.t[find_tensor(b, c)];
@@ -506,16 +507,15 @@ cudaError_t run_dense(const int64_t* dense, int64_t n_dense, int chunk, int norm
     if (b.count == 0) continue;
     const int grid = grid_of(b.chunks);
     if (clip) {
-      // the first one follows a norm kernel
-      const cudaError_t e = launch_after(scale_kernel<M>, dim3(grid), dim3(THREADS), s, b, *clip);
+      const cudaError_t e = launch_after(scale_kernel<M>, dim3(grid), dim3(THREADS), 0, 1, s, b, *clip);
       if (e != cudaSuccess) return e;
     } else {
-      norm_kernel<M><<<grid, THREADS, 0, s>>>(b, norm_type, part + *parts);
+      const cudaError_t e =
+          launch_after(norm_kernel<M>, dim3(grid), dim3(THREADS), 0, 1, s, b, norm_type, part + *parts);
+      if (e != cudaSuccess) return e;
       *parts += grid;
     }
     ++*launches;
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
@@ -574,7 +574,7 @@ cce_status run(const int64_t* dense, int64_t n_dense, const cce_strided* strided
   if (e == cudaSuccess && clipping && parts > 0)
     e = pass(dense, n_dense, strided, n_strided, norm_type, &k, part, &parts, s, &launches);
   if (e == cudaSuccess && (!clipping || parts == 0)) {
-    e = launch_after(finish_kernel, dim3(1), dim3(THREADS), s, k);
+    e = launch_after(finish_kernel, dim3(1), dim3(THREADS), 0, 1, s, k);
     ++launches;
   }
   count_launches(launches);

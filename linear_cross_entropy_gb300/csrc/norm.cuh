@@ -332,6 +332,8 @@ __global__ void __launch_bounds__(MAX_THREADS) fwd_kernel(NormFwd a) {
       }
     }
   };
+  let_next_start();
+  wait_for_previous();
   int64_t base = static_cast<int64_t>(blockIdx.x) * groups;
   load_row(base + threadIdx.y);
   next.fill(gain, [&](int64_t c, auto& f) { load_gain<LAYER>(a.w, a.p_type, a.offset, c, f); });
@@ -539,6 +541,7 @@ __global__ void __launch_bounds__(bwd_threads<TX, VEC, K, LAYER>(), 1) bwd_kerne
     gv[k].zero();
   }
   let_next_start();
+  wait_for_previous();
   int64_t base = static_cast<int64_t>(blockIdx.x) * groups;
   place.row(base + threadIdx.y);
   if (PREFETCH) load_row(base + threadIdx.y);
@@ -832,8 +835,8 @@ inline int group_threads(int64_t vecs, int K) {
 
 template <typename TX, typename TY, int VEC, int K, bool LAYER>
 cudaError_t run_fwd_few(const NormFwd& a, int64_t vecs, cudaStream_t s) {
-  fwd_few_kernel<TX, TY, VEC, K, LAYER><<<static_cast<unsigned>(a.N), group_threads(vecs, K), 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_after(fwd_few_kernel<TX, TY, VEC, K, LAYER>, dim3(static_cast<unsigned>(a.N)),
+                      dim3(group_threads(vecs, K)), 0, 1, s, a);
 }
 
 constexpr int MAX_SMEM = 227 * 1024 - 2048;   // dynamic shared memory of a block, beside what the kernels declare
@@ -862,8 +865,7 @@ cudaError_t run_fwd(const NormFwd& a, int tpr, cudaStream_t s) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  kernel<<<grid, dim3(tpr, groups), smem, s>>>(a);
-  return cudaGetLastError();
+  return launch_after(kernel, dim3(grid), dim3(tpr, groups), smem, 1, s, a);
 }
 
 // Launches fwd_kernel for rows that the registers of one block hold; false for longer ones.
@@ -960,19 +962,8 @@ cudaError_t run_bwd(const NormBwd& a, int tpr, int* parts, cudaStream_t s) {
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = b.cluster ? static_cast<unsigned>(blocks) : 1u;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(tpr, groups);
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, b);
+  return launch_after(kernel, dim3(blocks), dim3(tpr, groups), static_cast<size_t>(smem),
+                      b.cluster ? static_cast<unsigned>(blocks) : 1u, s, b);
 }
 
 // Launches bwd_kernel for rows that the registers of one block hold; false for longer ones.
@@ -1039,8 +1030,8 @@ cudaError_t bwd(const NormBwd& a, Access access, cudaStream_t s, int* launches) 
   }
   if ((!a.dw && !a.db) || (a.N > 0 && parts == 0)) return cudaSuccess;  // parts == 0: the cluster has written them
   ++*launches;
-  return launch_after(reduce_kernel, dim3(static_cast<unsigned>(cdiv(a.D, 32)), LAYER ? 2 : 1), dim3(32, REDUCE_WARPS),
-                      s, a.part_w, a.part_b, parts, a.D, a.p_type, a.dw, a.db);
+  return launch_after(reduce_kernel, dim3(static_cast<unsigned>(cdiv(a.D, 32)), LAYER ? 2 : 1), dim3(32, REDUCE_WARPS), 0,
+                      1, s, a.part_w, a.part_b, parts, a.D, a.p_type, a.dw, a.db);
 }
 
 }  // namespace norm
