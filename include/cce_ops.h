@@ -21,7 +21,7 @@
  * and grad_y may be strided views: row n starts (n / inner) * outer_stride +
  * (n % inner) * row_stride elements after the pointer (a plain matrix has
  * inner = N).  Strides are >= 0; rows of an input may coincide.  Outputs y and
- * grad_x are dense [N, D].
+ * grad_x are dense [N, D].  Outputs of a norm overlap no input.
  */
 #ifndef CCE_OPS_GB300_H
 #define CCE_OPS_GB300_H
@@ -49,8 +49,11 @@ int cce_ops_abi_version(void);
  *   mean, rstd      [N] fp32 (written), each may be NULL; the backward needs
  *                   them.
  * N = 0 is fine (nothing is launched); D >= 1.  N, D < 2^31.  Pointers need the
- * alignment of their element; 16-byte aligned rows (and D a multiple of 16
- * bytes) take the wide path.  The squared deviations must not overflow fp32.
+ * alignment of their element.  Fastest are rows of a multiple of 16 bytes that
+ * start on 16 bytes; next, matrices whose rows all start alike (any D, at least
+ * 64, aligned pointers, pitches that differ from D by a multiple of 16 bytes of
+ * x).  A row whose squared deviations overflow fp32 gets rstd 0; one with
+ * a NaN or an infinity becomes NaN, the other rows keep their results.
  */
 cce_status cce_layer_norm_forward(const void* x, int64_t x_inner, int64_t x_row_stride, int64_t x_outer_stride,
                                   int x_type, const void* weight, const void* bias, int p_type, int64_t N, int64_t D,

@@ -862,7 +862,7 @@ cudaError_t run_fwd(const NormFwd& a, int tpr, cudaStream_t s) {
   const int per_sm = std::max(1, MAX_THREADS / (tpr * groups));
   const int grid = static_cast<int>(std::min<int64_t>(cdiv(a.N, groups), a.sms * per_sm));
   if (smem > PLAIN_SMEM) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM);
     if (e != cudaSuccess) return e;
   }
   return launch_after(kernel, dim3(grid), dim3(tpr, groups), smem, 1, s, a);
@@ -959,7 +959,7 @@ cudaError_t run_bwd(const NormBwd& a, int tpr, int* parts, cudaStream_t s) {
   const int64_t smem = static_cast<int64_t>(sizeof(float)) * std::max(sums, param_floats<VEC, SHIFTED>(a.D));
   if (smem > PLAIN_SMEM) {
     const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM);
     if (e != cudaSuccess) return e;
   }
   return launch_after(kernel, dim3(blocks), dim3(tpr, groups), static_cast<size_t>(smem),

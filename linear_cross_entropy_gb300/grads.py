@@ -18,7 +18,7 @@ import math
 import torch
 
 from . import _lib
-from .norm import TYPES, _raw_stream
+from .norm import TYPES, _current_device, _raw_stream
 
 _l = _lib.load()
 _grad_norm, _clip_grads, _workspace_bytes = _l.cce_grad_norm, _l.cce_clip_grads, _l.cce_grad_norm_workspace_bytes
@@ -73,7 +73,7 @@ def _strided_row(g, o, written, dense, strided):
                                 *((ctypes.c_int64 * 4)(*col) for col in zip(*dims))))
 
 
-def _refuse(t, dev, what):
+def _check(t, dev, what):
     if not isinstance(t, torch.Tensor) or t.layout != torch.strided:
         raise ValueError(f"{what} must be dense tensors")
     if not t.is_cuda:
@@ -85,29 +85,41 @@ def _refuse(t, dev, what):
 
 
 def _tables(grads, outs, dev):
-    dense, strided = [], []
-    for g in grads:
-        if not g.is_cuda or g.dtype not in TYPES or g.device != dev or g.layout != torch.strided:
-            _refuse(g, dev, "gradients")
-    if outs is None:
-        for g in grads:
-            if g.is_contiguous():
-                p = g.data_ptr()
-                dense += (p, p, g.numel(), TYPES[g.dtype] * 257)
-            elif g.numel():
-                _strided_row(g, g, False, dense, strided)
-    else:
+    """The library's tables of the tensors: (array of dense rows, list of strided ones)."""
+    dense, strided, index, types = [], [], dev.index, TYPES
+    try:
+        if outs is None:
+            outs = grads
+            written = False
+        else:
+            written = True
         for g, o in zip(grads, outs):
-            if o is not g:
-                if not o.is_cuda or o.dtype not in TYPES or o.device != dev or o.layout != torch.strided:
-                    _refuse(o, dev, "out")
+            gt = types.get(g.dtype)
+            if gt is None or g.get_device() != index:
+                _check(g, dev, "gradients")
+            if o is g:
+                if g.is_contiguous():
+                    at = g.data_ptr()
+                    dense += (at, at, g.numel(), gt * 257)
+                    continue
+            else:
+                ot = types.get(o.dtype)
+                if ot is None or o.get_device() != index:
+                    _check(o, dev, "out")
                 if o.shape != g.shape:
                     raise ValueError(f"out must have the shapes of the gradients: {tuple(o.shape)} for "
                                      f"{tuple(g.shape)}")
-            if g.is_contiguous() and (o is g or o.is_contiguous()):
-                dense += (g.data_ptr(), o.data_ptr(), g.numel(), TYPES[g.dtype] + (TYPES[o.dtype] << 8))
-            elif g.numel():
-                _strided_row(g, o, True, dense, strided)
+                if g.is_contiguous() and o.is_contiguous():
+                    dense += (g.data_ptr(), o.data_ptr(), g.numel(), gt + (ot << 8))
+                    continue
+            _check(g, dev, "gradients")
+            _check(o, dev, "out")
+            if g.numel():
+                _strided_row(g, o, written, dense, strided)
+    except (RuntimeError, AttributeError):  # what is no dense tensor has no such methods
+        for t in (*grads, *outs):
+            _check(t, dev, "gradients and out")
+        raise
     return array.array("q", dense), strided
 
 
@@ -117,8 +129,8 @@ def _call(grads, outs, norm_type, max_norm, eps, stream):
         with torch.cuda.stream(stream):
             return _call(grads, outs, norm_type, max_norm, eps, None)
     if not grads[0].is_cuda:
-        _refuse(grads[0], dev, "gradients")
-    if dev.index != torch.cuda.current_device():
+        _check(grads[0], dev, "gradients")
+    if dev.index != _current_device():
         with torch.cuda.device(dev):
             return _call(grads, outs, norm_type, max_norm, eps, None)
     dense, strided = _tables(grads, outs, dev)
