@@ -10,6 +10,7 @@ import os
 
 import torch  # noqa: F401  (loads the CUDA runtime libcce.so links against)
 
+NATIVE_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_native.so")
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libcce.so")
 
 CCE_OK = 0
@@ -60,9 +61,11 @@ def load() -> ctypes.CDLL:
     global _lib
     if _lib is not None:
         return _lib
-    if not os.path.exists(LIB_PATH):
+    for path in (LIB_PATH, NATIVE_PATH):
+        if os.path.exists(path):
+            continue
         raise ImportError(
-            f"{LIB_PATH} is not built; run `python -m linear_cross_entropy_gb300.build` "
+            f"{path} is not built; run `python -m linear_cross_entropy_gb300.build` "
             "(there is no non-CUDA fallback)")
     lib = ctypes.CDLL(LIB_PATH)
     vp, i64, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t

@@ -6,7 +6,9 @@
 
 Each translation unit is compiled in parallel, then linked into
 linear_cross_entropy_gb300/libcce.so against the shared CUDA runtime (the
-one PyTorch loads), so both use the same runtime state.
+one PyTorch loads), so both use the same runtime state.  csrc/binding.cpp
+becomes the Python module _native.so beside it (g++, against this Python's and
+PyTorch's headers), which calls libcce.so.
 """
 from __future__ import annotations
 
@@ -14,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -22,9 +25,11 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libcce.so")
+NATIVE = os.path.join(PKG, "_native.so")
 SOURCES = ("cce_api.cu", "gemm_kernels.cu", "cce_noalloc.cu", "cce_sort.cu", "cce_flce.cu", "grad_clip.cu",
            "norm_api.cu") + tuple(f"norm_{p}_{t}.cu" for p in ("fwd", "bwd")
                                   for t in ("bf16", "f16", "f32", "f32_bf16", "f32_f16"))
+BINDING = "binding.cpp"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -49,7 +54,22 @@ def _deps_mtime() -> float:
 
 
 def up_to_date() -> bool:
-    return os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime()
+    return all(os.path.exists(p) and os.path.getmtime(p) >= _deps_mtime() for p in (LIB, NATIVE))
+
+
+def _torch_flags():
+    """Compile and link flags of a Python module over PyTorch."""
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    include = [sysconfig.get_paths()["include"], os.path.join(base, "include"),
+               os.path.join(base, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
+    compile_flags = ["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+                     f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for d in include:
+        compile_flags += ["-isystem", d]
+    link_flags = ["-L" + os.path.join(base, "lib"), "-ltorch", "-ltorch_cpu", "-ltorch_python", "-lc10", "-lc10_cuda"]
+    return compile_flags, link_flags
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
@@ -59,24 +79,30 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     cc = nvcc()
     flags = _flags(verbose_ptxas)
 
+    torch_compile, torch_link = _torch_flags()
+    cxx = os.environ.get("CXX") or "g++"
+
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
-        cmd = [cc] + flags + ["-c", os.path.join(CSRC, src), "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
+        cmd = [cc] + flags if src.endswith(".cu") else [cxx] + torch_compile
+        r = subprocess.run(cmd + ["-c", os.path.join(CSRC, src), "-o", obj], capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"{os.path.basename(cmd[0])} failed for {src}:\n{r.stdout}\n{r.stderr}")
         if verbose_ptxas:
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        objs = list(ex.map(compile_one, SOURCES))
-    tmp = LIB + ".tmp"
-    cmd = [cc] + ARCH + ["-shared", "--cudart", "shared", "-o", tmp] + objs
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
+    def link(cmd, out):
+        tmp = out + ".tmp"
+        r = subprocess.run(cmd + ["-o", tmp], capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, out)
+
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        *objs, binding = ex.map(compile_one, SOURCES + (BINDING,))
+    link([cc] + ARCH + ["-shared", "--cudart", "shared"] + objs, LIB)
+    link([cxx, "-shared", binding, "-L" + PKG, "-l:libcce.so", "-Wl,-rpath,$ORIGIN"] + torch_link, NATIVE)
     return LIB
 
 

@@ -273,6 +273,50 @@ def test_autograd_matches_the_direct_calls(cce, layer):
         U.within(b2.grad, U.f64(dy).sum(axis=0), np.abs(U.f64(dy)).sum(axis=0), F32, "db")
 
 
+def test_autograd_without_parameters(cce):
+    """Every choice of parameters and of leaves that train."""
+    x, w, b, dy = _inputs(21, (9, 96), F32, F32, F32)
+    for have_w, have_b in [(False, False), (True, False), (False, True), (True, True)]:
+        for train in [(True, True, True), (True, False, False), (False, True, True), (False, True, False),
+                      (False, False, True)]:
+            leaves = [t.clone().requires_grad_(r) for t, r in zip((x, w, b), train)]
+            args = [leaves[0], leaves[1] if have_w else None, leaves[2] if have_b else None]
+            if not any(a is not None and a.requires_grad for a in args):
+                continue
+            cce.layer_norm(*args).backward(dy)
+            y, m, r = cce.cce_layer_norm_forward(x, w if have_w else None, b if have_b else None)
+            want = cce.cce_layer_norm_backward(dy, x, w if have_w else None, m, r, param_dtype=None if have_w else F32)
+            for leaf, a, g in zip(leaves, args, want):
+                assert (leaf.grad is None) == (a is None or not a.requires_grad)
+                if leaf.grad is not None:
+                    assert torch.equal(leaf.grad, g)
+    x2 = x.clone().requires_grad_()
+    cce.rms_norm(x2).backward(dy)
+    y, r = cce.cce_rms_norm_forward(x)
+    assert torch.equal(x2.grad, cce.cce_rms_norm_backward(dy, x, None, r)[0])
+
+
+def test_step_captured_into_a_graph(cce):
+    """Forward and backward of the autograd form in a graph, while an eager graph
+    of other leaves is alive.  (One of the same leaves may not be: their
+    accumulation nodes would bring its stream into the capture.)"""
+    x, w, b, dy = _inputs(45, (64, 333), BF16, BF16, F32)
+    others = [t.clone().requires_grad_() for t in (x, w, b)]
+    alive = cce.layer_norm(*others)
+    leaves = [t.clone().requires_grad_() for t in (x, w, b)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.autograd.grad(cce.layer_norm(*leaves), leaves, dy)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = torch.autograd.grad(cce.layer_norm(*leaves), leaves, dy)
+    graph.replay()
+    want = torch.autograd.grad(alive, others, dy)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_no_second_derivative(cce):
     x, w, b, dy = _inputs(23, (4, 64), F32, F32, F32)
     x.requires_grad_()
