@@ -34,7 +34,7 @@ template <typename T, int VEC>
 struct Vec {
   static constexpr int BYTES = static_cast<int>(sizeof(T)) * VEC;
   static constexpr int WORDS = (BYTES + 3) / 4;
-  uint32_t w[WORDS];
+  alignas(BYTES >= 16 ? 16 : 4 * WORDS) uint32_t w[WORDS];
 
   __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -170,6 +170,23 @@ struct Vec {
     }
   }
 };
+
+// Copies that pass the registers by: a thread's own 4, 8 or 16 bytes from global
+// to shared memory, in groups that it waits for (all but the newest N of them).
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* shared, const void* global) {
+  const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(shared));
+  if constexpr (BYTES == 16) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(global) : "memory");
+  } else {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(global), "n"(BYTES) : "memory");
+  }
+}
+__device__ __forceinline__ void end_copy_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_copy_groups() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // Two fp32 values in a register pair, for the packed fp32 instructions (one issue slot for two results).
 struct Pair {

@@ -490,10 +490,28 @@ __global__ void __launch_bounds__(MAX_THREADS) fwd_long_kernel(NormFwd a) {
 //
 // The columns' sums are what fills the registers, so a thread holds 16 values of
 // a row (32 in rows that need it) and a row is spread over more threads than in
-// the forward.  PREFETCH loads the next row while this one is reduced.
+// the forward.  The next rows wait in a ring of shared memory: each thread copies
+// its own vectors there, so a thread waits for nothing but its own copies.
+//
+// Threads of a block: as many as the sums leave registers for.  A layer norm's
+// have the bias's beside the weight's; its rows of 257 to 320 threads fit twice
+// in 640 (bf16 8,192 x 5,120: 56 us against 65), where fewer registers cost the
+// others 0.5 us a call.
 template <typename TX, int VEC, int K, bool LAYER>
 constexpr int bwd_threads() {
   return !LAYER && sizeof(TX) == 2 && VEC > 1 && K * VEC <= 16 ? 768 : 512;
+}
+constexpr int WIDER = 640;
+// A group of several warps has the barrier of its number plus one, of 16 that there are.
+static_assert(768 / 64 + 1 <= 16, "barriers of a block");
+// Rows in the ring: one where a thread holds more than 16 values, none for single elements.
+template <int VEC, int K>
+constexpr int bwd_ring() {
+  return VEC == 1 ? 0 : K * VEC > 16 ? 1 : 2;
+}
+template <typename TX, typename TY, int VEC, int K, int THREADS>
+constexpr int bwd_ring_bytes() {
+  return bwd_ring<VEC, K>() * THREADS * K * VEC * static_cast<int>(sizeof(TX) + sizeof(TY));
 }
 
 __device__ __forceinline__ float load_cluster(uint32_t addr) {
@@ -502,50 +520,59 @@ __device__ __forceinline__ float load_cluster(uint32_t addr) {
   return f;
 }
 
-template <typename TX, typename TY, int VEC, int K, int KF, bool LAYER, bool SHIFTED, bool PREFETCH>
-__global__ void __launch_bounds__(bwd_threads<TX, VEC, K, LAYER>(), 1) bwd_kernel(NormBwd a) {
-  constexpr int E = K * VEC / 2;
-  extern __shared__ __align__(16) float shared[];  // the gain; at the end the groups' sums
-  constexpr int SLOTS = slots(bwd_threads<TX, VEC, K, LAYER>());
+template <typename TX, typename TY, int VEC, int K, int KF, bool LAYER, bool SHIFTED, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1) bwd_kernel(NormBwd a) {
+  constexpr int E = K * VEC / 2, RING = bwd_ring<VEC, K>();
+  constexpr int AHEAD = RING > 0 ? RING : 1;  // rows whose statistics are loaded
+  extern __shared__ __align__(16) float dynamic[];  // the ring, then the gain; at the end the groups' sums
+  Vec<TX, VEC>* const ring_x = reinterpret_cast<Vec<TX, VEC>*>(dynamic);  // [RING][K][THREADS]
+  Vec<TY, VEC>* const ring_g = reinterpret_cast<Vec<TY, VEC>*>(ring_x + RING * K * THREADS);
+  float* const gain = dynamic + bwd_ring_bytes<TX, TY, VEC, K, THREADS>() / sizeof(float);
+  constexpr int SLOTS = slots(THREADS);
   __shared__ __align__(16) float sm[2][2][SLOTS];
   const int l = threadIdx.x, tpr = blockDim.x, groups = blockDim.y, slot = threadIdx.y * group_slots();
+  const int own = threadIdx.y * tpr + l;
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   const float inv_d = 1.0f / static_cast<float>(a.D);
 
   // A group's rows are all shifted alike: there is one row, or `step` is a multiple of VEC.
   Place<VEC, KF, SHIFTED> place(a.D);
-  Vec<TX, VEC> xv[K];
-  Vec<TY, VEC> gv[K];
-  float mean = 0.0f, rstd = 0.0f;
-  auto load_row = [&](int64_t n) {
+  float mean[AHEAD], rstd[AHEAD];
+  auto load_stats = [&](int64_t n, int i) {
+    mean[i] = LAYER && n < a.N ? a.mean[n] : 0.0f;
+    rstd[i] = n < a.N ? a.rstd[n] : 0.0f;
+  };
+  // Requests row n into place `at` of the ring.
+  auto request = [&](int64_t n, int at) {
     if (n < a.N) {
       const TX* x = static_cast<const TX*>(a.x) + a.xm.at(static_cast<int>(n));
       const TY* dy = static_cast<const TY*>(a.dy) + a.gm.at(static_cast<int>(n));
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        if (place.has(k)) {
-          place.load(xv[k], x, k, n == a.N - 1);
-          place.load(gv[k], dy, k, n == a.N - 1);
+        if (!place.has(k)) continue;
+        Vec<TX, VEC>* const to_x = ring_x + (at * K + k) * THREADS + own;
+        Vec<TY, VEC>* const to_g = ring_g + (at * K + k) * THREADS + own;
+        if (SHIFTED && n == a.N - 1 && !place.whole(k)) {  // there may be no memory behind the last row
+          to_x->load_some(x + place.column(k), place.lo(k), place.hi(k));
+          to_g->load_some(dy + place.column(k), place.lo(k), place.hi(k));
+        } else {
+          copy_async<sizeof(Vec<TX, VEC>)>(to_x, x + place.column(k));
+          copy_async<sizeof(Vec<TY, VEC>)>(to_g, dy + place.column(k));
         }
       }
-      if (LAYER) mean = a.mean[n];
-      rstd = a.rstd[n];
-    } else {  // a row of zeros adds nothing
-#pragma unroll
-      for (int k = 0; k < K; ++k) gv[k].zero();
     }
+    end_copy_group();
   };
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    xv[k].zero();
-    gv[k].zero();
-  }
   let_next_start();
   wait_for_previous();
   int64_t base = static_cast<int64_t>(blockIdx.x) * groups;
   place.row(base + threadIdx.y);
-  if (PREFETCH) load_row(base + threadIdx.y);
-  place.fill(shared, [&](int64_t c, auto& f) { load_gain<LAYER>(a.w, a.p_type, a.offset, c, f); });
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) {
+    if constexpr (RING > 0) request(base + threadIdx.y + i * step, i);
+    load_stats(base + threadIdx.y + i * step, i);
+  }
+  place.fill(gain, [&](int64_t c, auto& f) { load_gain<LAYER>(a.w, a.p_type, a.offset, c, f); });
   __syncthreads();
 
   Pair aw[E], ab[LAYER ? E : 1];
@@ -554,21 +581,39 @@ __global__ void __launch_bounds__(bwd_threads<TX, VEC, K, LAYER>(), 1) bwd_kerne
     aw[i] = Pair::both(0.0f);
     if (LAYER) ab[i] = Pair::both(0.0f);
   }
-  int buf = 0;
+  int buf = 0, at = 0;
   for (; base < a.N; base += step) {
     const int64_t n = base + threadIdx.y;
-    if (!PREFETCH) load_row(n);
     Vec<TX, VEC> x[K];
     Vec<TY, VEC> g[K];
+    const float row_mean = mean[0], row_rstd = rstd[0];
+    if constexpr (RING > 0) wait_copy_groups<RING - 1>();
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      x[k] = xv[k];
-      g[k] = gv[k];
-      place.trim(x[k], k);
-      place.trim(g[k], k);
+      x[k].zero();
+      g[k].zero();  // a row of zeros adds nothing
+      if (n < a.N && place.has(k)) {
+        if constexpr (RING > 0) {
+          x[k] = ring_x[(at * K + k) * THREADS + own];
+          g[k] = ring_g[(at * K + k) * THREADS + own];
+          place.trim(x[k], k);
+          place.trim(g[k], k);
+        } else {
+          x[k].load(static_cast<const TX*>(a.x) + a.xm.at(static_cast<int>(n)) + place.column(k));
+          g[k].load(static_cast<const TY*>(a.dy) + a.gm.at(static_cast<int>(n)) + place.column(k));
+        }
+      }
     }
-    const float row_rstd = rstd, row_mean = mean;
-    if (PREFETCH) load_row(n + step);
+    if constexpr (RING > 0) {
+      request(n + RING * step, at);
+      at = at + 1 == RING ? 0 : at + 1;
+    }
+#pragma unroll
+    for (int i = 0; i + 1 < AHEAD; ++i) {
+      mean[i] = mean[i + 1];
+      rstd[i] = rstd[i + 1];
+    }
+    load_stats(n + AHEAD * step, AHEAD - 1);
     // z = x rstd - mean rstd
     const Pair r = Pair::both(row_rstd), m = Pair::both(-row_mean * row_rstd);
     float2 s;
@@ -588,15 +633,15 @@ __global__ void __launch_bounds__(bwd_threads<TX, VEC, K, LAYER>(), 1) bwd_kerne
       if constexpr (VEC == 1) {
 #pragma unroll
         for (int k = 0; k < K; k += 2) {  // where a column is not there its dy is 0, and any gain does
-          gather(k / 2, Pair::of(shared[place.has(k) ? place.vec(k) : 0],
-                                 shared[place.has(k + 1) ? place.vec(k + 1) : 0]));
+          gather(k / 2, Pair::of(gain[place.has(k) ? place.vec(k) : 0],
+                                 gain[place.has(k + 1) ? place.vec(k + 1) : 0]));
         }
       } else {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
           if (!place.has(k)) continue;
           float w[VEC];
-          place.get_param(shared, k, w);
+          place.get_param(gain, k, w);
 #pragma unroll
           for (int i = 0; i < VEC / 2; ++i) gather(k * VEC / 2 + i, Pair::of(w[2 * i], w[2 * i + 1]));
         }
@@ -619,7 +664,7 @@ __global__ void __launch_bounds__(bwd_threads<TX, VEC, K, LAYER>(), 1) bwd_kerne
     for (int k = 0; k < K; ++k) {
       if (!place.has(k)) continue;
       float w[VEC], f[VEC];
-      place.get_param(shared, k, w);
+      place.get_param(gain, k, w);
       if constexpr (VEC == 1) {
         const float2 t = grad(k / 2, Pair::both(w[0]));
         f[0] = k & 1 ? t.y : t.x;
@@ -641,13 +686,14 @@ __global__ void __launch_bounds__(bwd_threads<TX, VEC, K, LAYER>(), 1) bwd_kerne
   // the bias's), added in order.  One group: straight into the partial row.
   if (!a.dw && !a.db) return;
   const bool side_by_side = SHIFTED || groups > 1 || a.cluster;
-  if (side_by_side) __syncthreads();  // the gain has been read
+  float* const sums = dynamic;
+  if (side_by_side) __syncthreads();  // the gain and the ring have been read
   const int64_t row = static_cast<int64_t>(blockIdx.x) * a.D;
 #pragma unroll
   for (int pass = 0; pass < (LAYER ? 2 : 1); ++pass) {
     if (!(pass == 0 ? a.dw : a.db)) continue;
     float* part =
-        side_by_side ? shared + (pass * groups + threadIdx.y) * a.D : (pass == 0 ? a.part_w : a.part_b) + row;
+        side_by_side ? sums + (pass * groups + threadIdx.y) * a.D : (pass == 0 ? a.part_w : a.part_b) + row;
     auto value = [&](int i) { return (pass == 0 ? aw : ab)[LAYER || pass == 0 ? i : 0].get(); };
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -679,14 +725,14 @@ __global__ void __launch_bounds__(bwd_threads<TX, VEC, K, LAYER>(), 1) bwd_kerne
   for (int c = tid; c < a.D; c += threads) {
     float t = 0.0f, u = 0.0f;
     if (a.dw) {
-      for (int g = 0; g < groups; ++g) t += shared[g * a.D + c];
+      for (int g = 0; g < groups; ++g) t += sums[g * a.D + c];
     }
     if (LAYER && a.db) {
-      for (int g = 0; g < groups; ++g) u += shared[(groups + g) * a.D + c];
+      for (int g = 0; g < groups; ++g) u += sums[(groups + g) * a.D + c];
     }
     if (a.cluster) {  // only this thread reads or writes column c of this block
-      shared[c] = t;
-      if (LAYER) shared[groups * a.D + c] = u;
+      sums[c] = t;
+      if (LAYER) sums[groups * a.D + c] = u;
     } else {
       if (a.dw) a.part_w[row + c] = t;
       if (LAYER && a.db) a.part_b[row + c] = u;
@@ -696,11 +742,11 @@ __global__ void __launch_bounds__(bwd_threads<TX, VEC, K, LAYER>(), 1) bwd_kerne
   // The grid is one cluster: the blocks share out the columns and add one
   // another's sums in the order of their ranks.
   cluster_sync();
-  const uint32_t at = smem_u32(shared), ranks = gridDim.x;
+  const uint32_t here = smem_u32(sums), ranks = gridDim.x;
   for (int c = static_cast<int>(blockIdx.x) * threads + tid; c < a.D; c += static_cast<int>(ranks) * threads) {
     float t = 0.0f, u = 0.0f;
     for (uint32_t r = 0; r < ranks; ++r) {
-      const uint32_t other = mapa_shared(at, r);
+      const uint32_t other = mapa_shared(here, r);
       t += load_cluster(other + 4u * c);
       if (LAYER) u += load_cluster(other + 4u * (groups * a.D + c));
     }
@@ -937,12 +983,11 @@ cudaError_t fwd(const NormFwd& a, Access access, cudaStream_t s, int* launches) 
 }
 
 constexpr int CLUSTER = 8;  // blocks, the portable limit
-template <typename TX, typename TY, int VEC, int K, int KF, bool LAYER, bool SHIFTED>
+template <typename TX, typename TY, int VEC, int K, int KF, bool LAYER, bool SHIFTED,
+          int THREADS = bwd_threads<TX, VEC, K, LAYER>()>
 cudaError_t run_bwd(const NormBwd& a, int tpr, int* parts, cudaStream_t s) {
-  // Where the sums of 24 values and the two rows fit beside each other: not those of a layer norm.
-  constexpr bool PREFETCH = K * VEC <= (LAYER ? 16 : 24);
-  auto kernel = bwd_kernel<TX, TY, VEC, K, KF, LAYER, SHIFTED, PREFETCH>;
-  const int groups = std::max(1, bwd_threads<TX, VEC, K, LAYER>() / tpr);
+  auto kernel = bwd_kernel<TX, TY, VEC, K, KF, LAYER, SHIFTED, THREADS>;
+  const int groups = std::max(1, THREADS / tpr);
   NormBwd b = a;
   // One row a group at most: 18.3 us a call from Python against 23.5 with a second launch, the GPU's time within 1 us.
   b.cluster = (a.dw || a.db) && a.N <= static_cast<int64_t>(CLUSTER) * groups;
@@ -956,7 +1001,8 @@ cudaError_t run_bwd(const NormBwd& a, int tpr, int* parts, cudaStream_t s) {
   }
   *parts = b.cluster ? 0 : blocks;
   const int64_t sums = static_cast<int64_t>(a.D) * groups * (LAYER && (SHIFTED || groups > 1 || b.cluster) ? 2 : 1);
-  const int64_t smem = static_cast<int64_t>(sizeof(float)) * std::max(sums, param_floats<VEC, SHIFTED>(a.D));
+  const int64_t smem = std::max<int64_t>(
+      sizeof(float) * sums, bwd_ring_bytes<TX, TY, VEC, K, THREADS>() + sizeof(float) * param_floats<VEC, SHIFTED>(a.D));
   if (smem > PLAIN_SMEM) {
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM);
@@ -973,6 +1019,12 @@ bool bwd_in_registers(const NormBwd& a, int* parts, cudaStream_t s, cudaError_t*
   if constexpr (VEC > 1) {
     constexpr int K = 16 / VEC;
     int tpr = group_threads(vecs, K);
+    if constexpr (LAYER && VEC == 8) {
+      if (2 * tpr > MAX_THREADS && 2 * tpr <= WIDER) {
+        *e = run_bwd<TX, TY, VEC, K, K - 1, LAYER, SHIFTED, WIDER>(a, tpr, parts, s);
+        return true;
+      }
+    }
     if (tpr <= bwd_threads<TX, VEC, K, LAYER>()) {
       switch (cdiv(vecs, tpr)) {  // vectors a thread; all but its last are there in every thread
         case 1: *e = run_bwd<TX, TY, VEC, 1, 0, LAYER, SHIFTED>(a, tpr, parts, s); break;
