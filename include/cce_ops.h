@@ -12,8 +12,8 @@
  *
  * Element types
  * -------------
- * CCE_F32, CCE_F16, CCE_BF16.  Arithmetic is fp32 throughout (gradient norms
- * finish in fp64); each output is rounded once, to nearest even.
+ * CCE_F32, CCE_F16, CCE_BF16.  Arithmetic is fp32 throughout, with the sums of a
+ * gradient norm as pairs of fp32 values; each output is rounded once, to nearest even.
  *
  * Rows
  * ----
@@ -123,8 +123,8 @@ typedef struct {
 
 /*
  * *norm (fp32, device, written) = sqrt(sum x^2) (CCE_NORM_2) or max |x|
- * (CCE_NORM_INF) over all elements; 0 without any.  Squares that leave fp32's
- * range are summed in fp64, so the norm is right wherever fp32 can hold it; an
+ * (CCE_NORM_INF) over all elements; 0 without any.  Where squares leave fp32's
+ * range they are summed in fp64, so the norm is right wherever fp32 can hold it; an
  * infinity or NaN among the elements gives infinity or NaN.
  */
 cce_status cce_grad_norm(const int64_t* dense /* host */, int64_t n_dense, const cce_strided* strided /* host */,

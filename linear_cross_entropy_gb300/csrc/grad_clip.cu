@@ -10,10 +10,16 @@
 // graph).  The second pass walks the chunks backwards: what the first pass read
 // last is still in L2.
 //
-// A thread sums the squares of up to 64 values in fp32 and goes on in fp64;
-// block partials and the total are fp64, added in a fixed order.  Where those
-// squares overflow, or are so small that underflow could show (below 2^-100 and
-// not zero), the thread sums its values of the chunk again in fp64.
+// Measured: the norm of an 805 MB bf16 tensor 114 us (7.1 TB/s); 444 M bf16
+// gradients in 291 tensors clipped into fp32, 888 MB read twice and 1.8 GB
+// written, 558 us (6.4 TB/s); 0.5 M values 5.2 us for both launches, all latency.
+//
+// A thread sums the squares of up to 64 values in fp32; from there on a sum is a
+// pair of fp32 values, the rounded sum and what the roundings lost, up to the
+// norm itself.  fp64 adds are slow on a GB300: with them 14.7 M bf16 values were
+// clipped into fp32 in 27 us and not 18.  Where a block's sum overflows, or is so
+// small that squares may have underflowed, the block goes over its values again
+// in fp64.  Every order is fixed.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -31,7 +37,8 @@ namespace {
 constexpr int THREADS = 256;
 constexpr int UNROLL = 8;                  // 16-byte loads in flight per thread
 constexpr int ROUND = THREADS * UNROLL * 8;  // elements of one unrolled round of 16-bit values
-constexpr int GRID = 608;                  // 152 SMs x 4 resident blocks
+// 152 SMs x 4 resident blocks: 2 an SM clip the 444 M values in 590 us, 3 in 579, 4 in 567.
+constexpr int GRID = 608;
 constexpr int MAX_TENSORS = 1000;          // per launch: what 32 KB of parameters hold
 constexpr int FEW_TENSORS = 32;            // a launch with 1 KB of them
 // Of one tensor: then the chunks of MAX_TENSORS of them can be counted in 32 bits.
@@ -57,8 +64,15 @@ struct Batch {
 };
 static_assert(sizeof(Batch<MAX_TENSORS>) <= 32000 + 64, "kernel parameters");
 
+// A block's part of the norm: the sum of squares as hi + lo, or, where hi is
+// infinite, as `wide`; or the largest magnitude as hi.
+struct Part {
+  float hi, lo;
+  double wide;
+};
+
 struct Clip {
-  const double* part;
+  const Part* part;
   int parts;
   int norm_type;
   float max_norm, eps;
@@ -81,39 +95,69 @@ __device__ __forceinline__ int find_tensor(const Batch<M>& b, uint32_t chunk) {
 }
 
 // Larger of two magnitudes; NaN wins.
-__device__ __forceinline__ double larger(double a, double b) { return b > a || b != b ? b : a; }
+__device__ __forceinline__ float larger(float a, float b) { return b > a || b != b ? b : a; }
 
-__device__ __forceinline__ double join(double a, double b, bool inf) { return inf ? larger(a, b) : a + b; }
+// A sum of fp32 values with what its roundings lost (Knuth's exact two-term sum).
+struct Sum {
+  float hi = 0.0f, lo = 0.0f;
+
+  __device__ __forceinline__ void add(float v, float low = 0.0f) {
+    const float t = hi + v, part = t - hi;
+    lo += ((hi - (t - part)) + (v - part)) + low;
+    hi = t;
+  }
+};
 
 // Over the block, in a fixed order; the result is thread 0's.
-__device__ double block_join(double v, bool inf) {
+__device__ Sum block_sum(Sum v, bool inf) {
+  __shared__ float2 sm[THREADS / 32];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float hi = __shfl_down_sync(0xffffffffu, v.hi, o), lo = __shfl_down_sync(0xffffffffu, v.lo, o);
+    if (inf) {
+      v.hi = larger(v.hi, hi);
+    } else {
+      v.add(hi, lo);
+    }
+  }
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = make_float2(v.hi, v.lo);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int w = 1; w < THREADS / 32; ++w) {
+      if (inf) {
+        v.hi = larger(v.hi, sm[w].x);
+      } else {
+        v.add(sm[w].x, sm[w].y);
+      }
+    }
+  }
+  return v;
+}
+
+__device__ double block_sum64(double v) {
   __shared__ double sm[THREADS / 32];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = join(v, __shfl_down_sync(0xffffffffu, v, o), inf);
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_down_sync(0xffffffffu, v, o);
   if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int w = 1; w < THREADS / 32; ++w) v = join(v, sm[w], inf);
+    for (int w = 1; w < THREADS / 32; ++w) v += sm[w];
   }
   return v;
 }
 
 // What a thread gathers: squares or the largest magnitude.
 struct Gather {
-  double total = 0.0;      // over the chunks
-  double chunk = 0.0;      // over the rounds of this chunk
-  float s = 0.0f;          // of this round: sum of squares, or the largest magnitude
-  uint32_t any = 0u;       // bits of the round's values but the signs
-  bool outside = false;    // a round of this chunk left fp32's range
+  Sum sum;            // of the rounds that have ended
+  float s = 0.0f;     // of this round: sum of squares; or the largest magnitude
+  uint32_t any = 0u;  // bits of the values but the signs
 
   template <typename T, int VEC>
   __device__ __forceinline__ void add(const Vec<T, VEC>& v, bool inf) {
     if (inf) {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float m = fabsf(v.get(e));
-        s = m > s || m != m ? m : s;
-      }
+      for (int e = 0; e < VEC; ++e) s = larger(s, fabsf(v.get(e)));
     } else {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
@@ -126,32 +170,26 @@ struct Gather {
   }
   __device__ __forceinline__ void end_round(bool inf) {
     if (inf) return;
-    outside = outside || !(s <= 3.0e38f) || (s < 0x1p-100f && any != 0u);
-    chunk += s;
+    sum.add(s);
     s = 0.0f;
-    any = 0u;
   }
 };
 
-// The thread's squares of a chunk again, in fp64.
-template <typename T, int VEC>
-__device__ __noinline__ double squares64(const T* p, int n) {
-  double t = 0.0;
-  for (int v = threadIdx.x; v < n / VEC; v += THREADS) {
-    Vec<T, VEC> x;
-    x.load(p + static_cast<int64_t>(v) * VEC);
-    for (int e = 0; e < VEC; ++e) {
-      const double d = x.get(e);
-      t += d * d;
-    }
+// The block's part of the norm.  Fewer than 2^31 squares lose less than 2^-119 to
+// underflow, which is nothing beside a sum of 2^-80; below that, and where fp32
+// overflows, `again` returns the sum of the thread's squares in fp64.
+template <typename Again>
+__device__ __forceinline__ void put_part(const Gather& g, bool inf, Part* part, Again again) {
+  Sum v = g.sum;
+  if (inf) v.hi = g.s;
+  v = block_sum(v, inf);
+  Part p{v.hi, v.lo, 0.0};
+  const bool fits = inf || (v.hi >= 0x1p-80f && v.hi <= 3.0e38f);
+  if (__syncthreads_or(threadIdx.x == 0 && !fits) && __syncthreads_or(g.any != 0u)) {
+    p.wide = block_sum64(again());
+    p.hi = INFINITY;
   }
-  for (int i = n / VEC * VEC + threadIdx.x; i < n; i += THREADS) {
-    Vec<T, 1> x;
-    x.load(p + i);
-    const double d = x.get(0);
-    t += d * d;
-  }
-  return t;
+  if (threadIdx.x == 0) part[blockIdx.x] = p;
 }
 
 // Rounds of U vectors a thread from vector v on, while whole rounds are left.
@@ -164,15 +202,13 @@ __device__ __forceinline__ void gather_rounds(const T* p, int vecs, int& v, bool
     for (int u = 0; u < U; ++u) x[u].load(p + static_cast<int64_t>(v + u * THREADS) * VEC);
 #pragma unroll
     for (int u = 0; u < U; ++u) g.add(x[u], inf);
-    if (U == UNROLL) g.end_round(inf);
+    g.end_round(inf);
   }
 }
 
 template <typename T, int VEC>
 __device__ __forceinline__ void gather_chunk(const T* p, int n, bool inf, Gather& g) {
   const int vecs = n / VEC;
-  g.chunk = 0.0;
-  g.outside = false;
   int v = threadIdx.x;
   gather_rounds<UNROLL, T, VEC>(p, vecs, v, inf, g);
   gather_rounds<2, T, VEC>(p, vecs, v, inf, g);
@@ -180,13 +216,12 @@ __device__ __forceinline__ void gather_chunk(const T* p, int n, bool inf, Gather
   if constexpr (VEC > 1) {
     const int i = vecs * VEC + threadIdx.x;
     if (i < n) {
-      Vec<T, 1> x;
-      x.load(p + i);
-      g.add(x, inf);
+      Vec<T, 1> x[1];
+      x[0].load(p + i);
+      g.add(x[0], inf);
+      g.end_round(inf);
     }
   }
-  g.end_round(inf);
-  if (!inf) g.total += g.outside ? squares64<T, VEC>(p, n) : g.chunk;
 }
 
 template <typename T>
@@ -199,9 +234,15 @@ __device__ __forceinline__ void gather_typed(const void* in, int64_t off, int n,
   }
 }
 
+__device__ __forceinline__ float load_any(const void* p, int type, int64_t i) {
+  if (type == CCE_F32) return static_cast<const float*>(p)[i];
+  if (type == CCE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+  return __half2float(static_cast<const __half*>(p)[i]);
+}
+
 template <int M>
 __global__ void __launch_bounds__(THREADS, 4) norm_kernel(const __grid_constant__ Batch<M> b, int norm_type,
-                                                       double* part) {
+                                                       Part* part) {
   const bool inf = norm_type == CCE_NORM_INF;
   let_next_start();
   wait_for_previous();
@@ -218,8 +259,29 @@ __global__ void __launch_bounds__(THREADS, 4) norm_kernel(const __grid_constant_
       gather_typed<__half>(t.in, off, n, t.wide_in, inf, g);
     }
   }
-  const double v = block_join(inf ? static_cast<double>(g.s) : g.total, inf);
-  if (threadIdx.x == 0) part[blockIdx.x] = v;
+  put_part(g, inf, part, [&] {
+    double wide = 0.0;
+    for (uint32_t c = blockIdx.x; c < b.chunks; c += gridDim.x) {
+      const Tensor& t = b.t[find_tensor(b, c)];
+      const int64_t off = static_cast<int64_t>(c - t.first_chunk) * b.chunk;
+      const int64_t end = min(off + b.chunk, t.n);
+      for (int64_t i = off + threadIdx.x; i < end; i += THREADS) {
+        const double f = load_any(t.in, t.in_type, i);
+        wide += f * f;
+      }
+    }
+    return wide;
+  });
+}
+
+// Thread 0's result.
+__device__ float wide_norm(const Part* part, int parts) {
+  double t = 0.0;
+  for (int i = threadIdx.x; i < parts; i += THREADS) {
+    const Part p = part[i];
+    t += p.hi < INFINITY ? static_cast<double>(p.hi) + static_cast<double>(p.lo) : p.wide;
+  }
+  return static_cast<float>(sqrt(block_sum64(t)));
 }
 
 // The norm from the block partials: every block computes it, in the same order.
@@ -227,14 +289,24 @@ __device__ float total_norm(const Clip& k) {
   __shared__ float result;
   wait_for_previous();
   const bool inf = k.norm_type == CCE_NORM_INF;
-  double v = 0.0;
-  for (int i = threadIdx.x; i < k.parts; i += THREADS) v = join(v, k.part[i], inf);
-  v = block_join(v, inf);
-  if (threadIdx.x == 0) {
-    result = static_cast<float>(inf ? v : sqrt(v));
-    if (blockIdx.x == 0 && k.norm) *k.norm = result;
+  Sum v;
+  for (int i = threadIdx.x; i < k.parts; i += THREADS) {
+    const float2 p = *reinterpret_cast<const float2*>(k.part + i);
+    if (inf) {
+      v.hi = larger(v.hi, p.x);
+    } else {
+      v.add(p.x, p.y);
+    }
   }
+  v = block_sum(v, inf);
+  if (threadIdx.x == 0) result = inf ? v.hi : v.hi + v.lo <= 3.0e38f ? sqrtf(v.hi + v.lo) : INFINITY;
   __syncthreads();
+  if (!inf && !(result < INFINITY)) {  // a block's part or the total is outside fp32's range
+    const float wide = wide_norm(k.part, k.parts);
+    if (threadIdx.x == 0) result = wide;
+    __syncthreads();
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0 && k.norm) *k.norm = result;
   return result;
 }
 
@@ -327,12 +399,6 @@ __global__ void __launch_bounds__(THREADS, 4) scale_kernel(const __grid_constant
 }
 
 // ---------------------------------------------------------- strided tensors
-__device__ __forceinline__ float load_any(const void* p, int type, int64_t i) {
-  if (type == CCE_F32) return static_cast<const float*>(p)[i];
-  if (type == CCE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-  return __half2float(static_cast<const __half*>(p)[i]);
-}
-
 __device__ __forceinline__ void strided_offsets(const cce_strided& t, int64_t i, int64_t* in, int64_t* out) {
   int64_t a = 0, b = 0;
 #pragma unroll
@@ -346,20 +412,31 @@ __device__ __forceinline__ void strided_offsets(const cce_strided& t, int64_t i,
   *out = b + i * t.out_stride[0];
 }
 
-// One element at a time, all sums in fp64: few tensors take this path.
+// One element at a time: few tensors take this path.
 __global__ void __launch_bounds__(THREADS) strided_norm_kernel(const __grid_constant__ cce_strided t, int64_t n,
-                                                               int norm_type, double* part) {
+                                                               int norm_type, Part* part) {
   const bool inf = norm_type == CCE_NORM_INF;
-  double v = 0.0;
-  for (int64_t i = blockIdx.x * static_cast<int64_t>(THREADS) + threadIdx.x; i < n;
-       i += static_cast<int64_t>(gridDim.x) * THREADS) {
+  const int64_t first = blockIdx.x * static_cast<int64_t>(THREADS) + threadIdx.x;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * THREADS;
+  Gather g;
+  for (int64_t i = first; i < n; i += step) {
     int64_t a, b;
     strided_offsets(t, i, &a, &b);
-    const double x = load_any(t.in, t.in_type, a);
-    v = inf ? larger(v, fabs(x)) : v + x * x;
+    Vec<float, 1> x;
+    x.w[0] = __float_as_uint(load_any(t.in, t.in_type, a));
+    g.add(x, inf);
+    g.end_round(inf);
   }
-  v = block_join(v, inf);
-  if (threadIdx.x == 0) part[blockIdx.x] = v;
+  put_part(g, inf, part, [&] {
+    double wide = 0.0;
+    for (int64_t i = first; i < n; i += step) {
+      int64_t a, b;
+      strided_offsets(t, i, &a, &b);
+      const double f = load_any(t.in, t.in_type, a);
+      wide += f * f;
+    }
+    return wide;
+  });
 }
 
 __global__ void __launch_bounds__(THREADS) strided_scale_kernel(const __grid_constant__ cce_strided t, int64_t n,
@@ -488,18 +565,20 @@ void fill_batch(Batch<M>& b, const int64_t* dense, int64_t n_dense, int chunk, i
 
 int grid_of(uint32_t chunks) { return static_cast<int>(std::min<uint32_t>(GRID, chunks)); }
 
-// A block spends a third of a microsecond on a chunk beside its memory, so
-// chunks are as large as leaves every block some of them (4 rounds: four
-// chunks a block at least), and a quarter of a round where a round would leave
-// SMs without work.
+// Elements of a chunk: one unrolled round of 16-bit values, but
+// - a quarter of it where that leaves half of the blocks without work: 0.5 M bf16
+//   values are clipped into fp32 in 5.2 us and not 5.7, 1 M in 5.2 and not 5.8;
+//   2 M, where it would fill the grid, take 6.7 us so and 6.2 in whole rounds;
+// - four rounds where every block still has four such chunks: 305 M values take
+//   395 us and not 397, 287 and not 290 into bf16.
 int chunk_of(int64_t total) {
-  if (total >= int64_t(4) * GRID * 4 * ROUND) return 4 * ROUND;
-  return total >= int64_t(GRID) * ROUND ? ROUND : ROUND / 4;
+  if (total <= int64_t(GRID / 2) * (ROUND / 4)) return ROUND / 4;
+  return total >= int64_t(16) * GRID * ROUND ? 4 * ROUND : ROUND;
 }
 
 // The norm pass (clip null) or the scaling pass over the dense tensors.
 template <int M>
-cudaError_t run_dense(const int64_t* dense, int64_t n_dense, int chunk, int norm_type, const Clip* clip, double* part,
+cudaError_t run_dense(const int64_t* dense, int64_t n_dense, int chunk, int norm_type, const Clip* clip, Part* part,
                       int* parts, cudaStream_t s, int* launches) {
   Batch<M> b;
   for (int64_t next = 0; next < n_dense;) {
@@ -521,7 +600,7 @@ cudaError_t run_dense(const int64_t* dense, int64_t n_dense, int chunk, int norm
 }
 
 cudaError_t pass(const int64_t* dense, int64_t n_dense, const cce_strided* strided, int64_t n_strided, int norm_type,
-                 const Clip* clip, double* part, int* parts, cudaStream_t s, int* launches) {
+                 const Clip* clip, Part* part, int* parts, cudaStream_t s, int* launches) {
   int64_t total = 0;
   for (int64_t i = 0; i < n_dense; ++i) total += dense[4 * i + 2];
   const int chunk = chunk_of(total);
@@ -546,7 +625,7 @@ cudaError_t pass(const int64_t* dense, int64_t n_dense, const cce_strided* strid
 
 size_t workspace_bytes(int64_t n_dense, int64_t n_strided) {
   const int64_t launches = std::max<int64_t>(1, cdiv64(n_dense, MAX_TENSORS)) + n_strided;
-  return sizeof(double) * GRID * static_cast<size_t>(launches);
+  return sizeof(Part) * GRID * static_cast<size_t>(launches);
 }
 
 cce_status run(const int64_t* dense, int64_t n_dense, const cce_strided* strided, int64_t n_strided, int norm_type,
@@ -567,7 +646,7 @@ cce_status run(const int64_t* dense, int64_t n_dense, const cce_strided* strided
   st = static_cast<cce_status>(device_ready(&sms));
   if (st != CCE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  double* part = static_cast<double*>(workspace);
+  Part* part = static_cast<Part*>(workspace);
   int parts = 0, launches = 0;
   cudaError_t e = pass(dense, n_dense, strided, n_strided, norm_type, nullptr, part, &parts, s, &launches);
   const Clip k{part, parts, norm_type, max_norm, eps, norm};
