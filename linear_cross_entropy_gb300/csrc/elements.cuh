@@ -225,24 +225,28 @@ __device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) {
   return r;
 }
 
-// VEC parameters of a run-time type as fp32 (the type is uniform over a launch).
-template <int VEC>
-__device__ __forceinline__ void load_param(const void* p, int type, int64_t i, float (&out)[VEC]) {
-  if (type == CCE_F32) {
-    Vec<float, VEC> v;
-    v.load(static_cast<const float*>(p) + i);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) out[e] = v.get(e);
-  } else if (type == CCE_BF16) {
-    Vec<__nv_bfloat16, VEC> v;
-    v.load(static_cast<const __nv_bfloat16*>(p) + i);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) out[e] = v.get(e);
+template <typename T, int VEC, bool SOME>
+__device__ __forceinline__ void load_param_as(const T* p, int n, float (&out)[VEC]) {
+  Vec<T, VEC> v;
+  if constexpr (SOME) {
+    v.load_some(p, 0, n);
   } else {
-    Vec<__half, VEC> v;
-    v.load(static_cast<const __half*>(p) + i);
+    v.load(p);
+  }
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) out[e] = v.get(e);
+  for (int e = 0; e < VEC; ++e) out[e] = v.get(e);
+}
+
+// VEC parameters of a run-time type as fp32 (the type is uniform over a launch).
+// SOME: the first n alone, the others 0, at any element's alignment.
+template <int VEC, bool SOME = false>
+__device__ __forceinline__ void load_param(const void* p, int type, int64_t i, float (&out)[VEC], int n = VEC) {
+  if (type == CCE_F32) {
+    load_param_as<float, VEC, SOME>(static_cast<const float*>(p) + i, n, out);
+  } else if (type == CCE_BF16) {
+    load_param_as<__nv_bfloat16, VEC, SOME>(static_cast<const __nv_bfloat16*>(p) + i, n, out);
+  } else {
+    load_param_as<__half, VEC, SOME>(static_cast<const __half*>(p) + i, n, out);
   }
 }
 

@@ -101,13 +101,17 @@ __device__ __forceinline__ float2 group_sum2(float2 v, float* sm, int second) {
   return t;
 }
 
-template <bool LAYER, int VEC>
-__device__ __forceinline__ void load_gain(const void* w, int p_type, float offset, int64_t c, float (&g)[VEC]) {
+// The gain and the bias of VEC columns; SOME: of the first n, the others 0.
+template <bool LAYER, int VEC, bool SOME = false>
+__device__ __forceinline__ void load_gain(const void* w, int p_type, float offset, int64_t c, float (&g)[VEC],
+                                          int n = VEC) {
   if (w) {
-    load_param<VEC>(w, p_type, c, g);
+    load_param<VEC, SOME>(w, p_type, c, g, n);
     if (!LAYER) {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) g[e] += offset;
+      for (int e = 0; e < VEC; ++e) {
+        if (!SOME || e < n) g[e] += offset;
+      }
     }
   } else {
 #pragma unroll
@@ -115,10 +119,10 @@ __device__ __forceinline__ void load_gain(const void* w, int p_type, float offse
   }
 }
 
-template <bool LAYER, int VEC>
-__device__ __forceinline__ void load_bias(const void* b, int p_type, int64_t c, float (&f)[VEC]) {
+template <bool LAYER, int VEC, bool SOME = false>
+__device__ __forceinline__ void load_bias(const void* b, int p_type, int64_t c, float (&f)[VEC], int n = VEC) {
   if (LAYER && b) {
-    load_param<VEC>(b, p_type, c, f);
+    load_param<VEC, SOME>(b, p_type, c, f, n);
   } else {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) f[e] = 0.0f;
@@ -215,22 +219,13 @@ struct Place {
       }
     }
   }
-  // All of a block's threads: the parameters of the D columns, 0 past them.
+  // All of a block's threads: the parameters of the D columns; what `load` makes of none past them.
   template <typename Load>
   __device__ __forceinline__ void fill(float* sm, Load load) const {
     const int tid = threadIdx.y * blockDim.x + threadIdx.x, threads = blockDim.x * blockDim.y;
     for (int c = tid; c < vecs; c += threads) {
       float f[VEC];
-      if constexpr (SHIFTED) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          float one[1] = {0.0f};
-          if (c * VEC + e < D) load(static_cast<int64_t>(c) * VEC + e, one);
-          f[e] = one[0];
-        }
-      } else {
-        load(static_cast<int64_t>(c) * VEC, f);
-      }
+      load(static_cast<int64_t>(c) * VEC, f, min(VEC, D - c * VEC));
       put_param(sm, c, f);
     }
   }
@@ -344,8 +339,12 @@ __global__ void __launch_bounds__(MAX_THREADS) fwd_kernel(NormFwd a) {
   wait_for_previous();
   int64_t base = static_cast<int64_t>(blockIdx.x) * groups;
   load_row(base + threadIdx.y);
-  next.fill(gain, [&](int64_t c, auto& f) { load_gain<LAYER>(a.w, a.p_type, a.offset, c, f); });
-  if (LAYER) next.fill(bias, [&](int64_t c, auto& f) { load_bias<LAYER>(a.b, a.p_type, c, f); });
+  next.fill(gain, [&](int64_t c, auto& f, int n) {
+    load_gain<LAYER, VEC, SHIFTED>(a.w, a.p_type, a.offset, c, f, n);
+  });
+  if (LAYER) {
+    next.fill(bias, [&](int64_t c, auto& f, int n) { load_bias<LAYER, VEC, SHIFTED>(a.b, a.p_type, c, f, n); });
+  }
   __syncthreads();
   const float fd = static_cast<float>(a.D);
   int buf = 0;
@@ -507,7 +506,7 @@ __global__ void __launch_bounds__(MAX_THREADS) fwd_long_kernel(NormFwd a) {
 // TB/s); 8,192 x 2,304 25 and 28 us, 3 to 5 us of it the parameters' gradients.
 // With the next row in registers instead of the ring 125 and 142 us; with three
 // or four rows in it 120 and 138.  Odd widths pay for their partial vectors: 16,384
-// x 1,001 29 and 33 us, x 1,024 21 and 24 us.
+// x 1,001 29 and 33 us, x 1,024 22 and 25 us.
 //
 // Threads of a block: as many as the sums leave registers for.  A layer norm's
 // have the bias's beside the weight's; its rows of 257 to 320 threads fit twice
@@ -588,7 +587,9 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_kernel(NormBwd a) {
     if constexpr (RING > 0) request(base + threadIdx.y + i * step, i);
     load_stats(base + threadIdx.y + i * step, i);
   }
-  place.fill(gain, [&](int64_t c, auto& f) { load_gain<LAYER>(a.w, a.p_type, a.offset, c, f); });
+  place.fill(gain, [&](int64_t c, auto& f, int n) {
+    load_gain<LAYER, VEC, SHIFTED>(a.w, a.p_type, a.offset, c, f, n);
+  });
   __syncthreads();
 
   Pair aw[E], ab[LAYER ? E : 1];
