@@ -241,6 +241,8 @@ __global__ void __launch_bounds__(MAX_THREADS) fwd_few_kernel(NormFwd a) {
   const int l = threadIdx.x, tpr = blockDim.x;
   const int64_t n = blockIdx.x;
   const TX* x = static_cast<const TX*>(a.x) + a.xm.at(static_cast<int>(n));
+  let_next_start();
+  wait_for_previous();
   Vec<TX, VEC> xv[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) {

@@ -388,6 +388,31 @@ def test_on_another_stream(cce):
     assert torch.equal(got2[0], cce.cce_rms_norm_forward(x, w)[0])
 
 
+@pytest.mark.parametrize("rows", [1, 300, 5000])
+@pytest.mark.parametrize("D", [1024, 1001, 20000])
+def test_calls_that_read_what_the_call_before_writes(cce, rows, D):
+    """Long calls, each with a short one behind it that reads the rows written last."""
+    N = (1 << 25) // D
+    x, w, b, dy = _inputs(81, (N, D), BF16, BF16, BF16)
+    y, mean, rstd = cce.cce_layer_norm_forward(x, w, b)
+    dx, dw, db = cce.cce_layer_norm_backward(dy, x, w, mean, rstd)
+    torch.cuda.synchronize()
+    last = [cce.cce_layer_norm_forward(t[-rows:], w, b, 1e-5)[0] for t in (y, dx)]
+    norm = cce.cce_grad_norm([dx, dw, db])
+    torch.cuda.synchronize()
+    for _ in range(3):
+        del y, dx
+        y, mean, rstd = cce.cce_layer_norm_forward(x, w, b)
+        after_y = cce.cce_layer_norm_forward(y[-rows:], w, b, 1e-5)[0]
+        dx, dw, db = cce.cce_layer_norm_backward(dy, x, w, mean, rstd)
+        after_dx = cce.cce_layer_norm_forward(dx[-rows:], w, b, 1e-5)[0]
+        dx.fill_(float("nan"))  # what a late reader would see
+        dx, dw, db = cce.cce_layer_norm_backward(dy, x, w, mean, rstd)
+        after_norm = cce.cce_grad_norm([dx, dw, db])
+        assert torch.equal(after_y, last[0]) and torch.equal(after_dx, last[1])
+        assert torch.equal(after_norm, norm)
+
+
 def test_captured_into_a_graph(cce):
     """Forward and backward in one graph, replayed on new values, while an
     eager graph of other leaves is alive."""
