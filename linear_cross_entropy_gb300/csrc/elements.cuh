@@ -118,6 +118,23 @@ struct Vec {
       }
     }
   }
+  // Becomes the elements shift .. shift + VEC - 1 of lo and hi in a row, 0 <= shift < VEC.
+  __device__ __forceinline__ void join(const Vec& lo, const Vec& hi, int shift) {
+    uint32_t a[2 * WORDS];
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) {
+      a[i] = lo.w[i];
+      a[WORDS + i] = hi.w[i];
+    }
+    const int bytes = shift * static_cast<int>(sizeof(T));
+#pragma unroll
+    for (int step = WORDS / 2; step > 0; step /= 2) {
+#pragma unroll
+      for (int i = 0; i + step < 2 * WORDS; ++i) a[i] = bytes & 4 * step ? a[i + step] : a[i];
+    }
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) w[i] = sizeof(T) == 4 ? a[i] : __funnelshift_r(a[i], a[i + 1], 8 * (bytes & 3));
+  }
   __device__ __forceinline__ float get(int i) const {
     if constexpr (sizeof(T) == 4) {
       return __uint_as_float(w[i]);

@@ -9,11 +9,12 @@
 // words, reduced, and written.  The variance is the sum of squared deviations
 // from the mean, taken over the registers, so nothing cancels.
 //
-// Rows whose starts are not 16-byte aligned (odd widths) are read and written in
-// aligned vectors all the same (SHIFTED): vector v of row n covers the columns
-// v * VEC - s ... with s = n * D mod VEC, the same s for every matrix of the call,
-// and only the row's two end vectors are partial.  Where the matrices disagree
-// on s, VEC is 1.
+// Rows whose starts are not 16-byte aligned (odd widths, views) are read and
+// written in aligned vectors all the same (SHIFTED): vector v of row n covers the
+// columns v * VEC - s ... for a row whose start lies s elements behind a vector's,
+// and only the row's two end vectors are partial.  s is the output's; where a
+// row of an input has another s (REALIGNED), each of the output's vectors is
+// joined from the two of the input's that hold its columns.
 //
 // A row belongs to a group of threadIdx.x = 0 .. tpr - 1 (tpr a power of two up
 // to 32, or a multiple of 32); a block has blockDim.y groups.  Thread l of a
@@ -21,6 +22,7 @@
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 
 #include "elements.cuh"
 #include "norm.h"
@@ -138,17 +140,19 @@ __device__ __forceinline__ Pair pair_of(const Vec<T, VEC> (&v)[K], int i) {
 
 // Where a row lies in a thread's vectors.  Every row has the first KF vectors of
 // every thread, so that only the others are checked.
-template <int VEC, int KF, bool SHIFTED>
+template <int VEC, int KF, Access A>
 struct Place {
+  static constexpr bool REALIGNED = A == Access::REALIGNED, SHIFTED = REALIGNED || A == Access::SHIFTED;
   int D, vecs;    // columns; vectors that a row may touch
+  int first;      // s of row 0
   int s = 0;      // columns by which the row starts inside vector 0
   int used;       // vectors that this row touches
 
-  __device__ __forceinline__ explicit Place(int d)
-      : D(d), vecs(SHIFTED ? (d + 2 * VEC - 2) / VEC : d / VEC), used(vecs) {}
+  __device__ __forceinline__ Place(int d, int shift)
+      : D(d), vecs(SHIFTED ? (d + 2 * VEC - 2) / VEC : d / VEC), first(REALIGNED ? shift : 0), used(vecs) {}
   __device__ __forceinline__ void row(int64_t n) {
     if constexpr (SHIFTED) {
-      s = static_cast<int>(n * (D & (VEC - 1))) & (VEC - 1);
+      s = static_cast<int>(n * (D & (VEC - 1)) + first) & (VEC - 1);
       used = (D + s + VEC - 1) / VEC;
     }
   }
@@ -162,15 +166,28 @@ struct Place {
     return !SHIFTED || (column(k) >= 0 && column(k) + VEC <= D);
   }
 
-  // Vector k of the row at p; `last`: there may be no memory behind the row.  The
-  // vector brings its neighbours' elements: trim() drops them, once it is used
-  // (here it would wait for the load).
+  // The s of an input's row n.
   template <typename T>
-  __device__ __forceinline__ void load(Vec<T, VEC>& v, const T* p, int k, bool last) const {
-    if (SHIFTED && last && !whole(k)) {
-      v.load_some(p + column(k), lo(k), hi(k));
+  __device__ __forceinline__ int own(const T* row) const {
+    return REALIGNED ? static_cast<int>(reinterpret_cast<uintptr_t>(row) / sizeof(T)) & (VEC - 1) : s;
+  }
+  __device__ __forceinline__ bool has(int k, int o) const {  // with s = o
+    return REALIGNED ? k < KF || vec(k) * VEC - o < D : has(k);
+  }
+  // Whether the vector from column c of row n on, which starts at element `at` of
+  // `end`, may be read whole: no memory need be around the matrix.
+  __device__ __forceinline__ bool readable(int c, bool last, int64_t at, int64_t end) const {
+    if (!SHIFTED || (!REALIGNED && !last) || (c >= 0 && c + VEC <= D)) return true;
+    return REALIGNED && at + c >= 0 && at + c + VEC <= end;
+  }
+  // The row's vector from column c on.  It brings its neighbours' elements: trim()
+  // drops them, once it is used (here it would wait for the load).
+  template <typename T>
+  __device__ __forceinline__ void load(Vec<T, VEC>& v, const T* row, int c, bool last, int64_t at, int64_t end) const {
+    if (readable(c, last, at, end)) {
+      v.load(row + c);
     } else {
-      v.load(p + column(k));
+      v.load_some(row + c, max(0, -c), min(VEC, D - c));
     }
   }
   template <typename T>
@@ -312,14 +329,15 @@ __global__ void __launch_bounds__(MAX_THREADS) fwd_few_kernel(NormFwd a) {
 // instead of the last one 99 us; with one block of 128 threads a row and no row
 // ahead 254 us.  Rows spread over more threads pay more for their sums: 16,384 x
 // 4,096 takes 46 us with 64 values a thread, 48 us with 32, 64 us with 16.
-template <typename TX, typename TY, int VEC, int K, int KF, bool LAYER, bool SHIFTED>
+template <typename TX, typename TY, int VEC, int K, int KF, bool LAYER, Access A>
 __global__ void __launch_bounds__(MAX_THREADS) fwd_kernel(NormFwd a) {
+  constexpr bool REALIGNED = A == Access::REALIGNED, SHIFTED = REALIGNED || A == Access::SHIFTED;
   constexpr int E = K * VEC / 2;
   extern __shared__ __align__(16) float gain[];  // then the bias of a layer norm
   __shared__ __align__(16) float sm[4][slots(MAX_THREADS)];
   const int groups = blockDim.y, slot = threadIdx.y * group_slots();
   const int step = gridDim.x * groups;
-  Place<VEC, KF, SHIFTED> next(a.D);
+  Place<VEC, KF, A> next(a.D, a.shift);
   float* bias = gain + next.param_floats();
   Vec<TX, VEC> xv[K];
 #pragma unroll
@@ -327,13 +345,34 @@ __global__ void __launch_bounds__(MAX_THREADS) fwd_kernel(NormFwd a) {
   auto load_row = [&](int64_t n) {
     if (n >= a.N) return;
     next.row(n);
-    const TX* x = static_cast<const TX*>(a.x) + a.xm.at(static_cast<int>(n));
+    const int64_t at = a.xm.at(static_cast<int>(n));
+    const TX* x = static_cast<const TX*>(a.x) + at;
+    const int o = next.own(x);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if (next.has(k)) {
-        next.load(xv[k], x, k, n == a.N - 1);
+      if (next.has(k, o)) {
+        next.load(xv[k], x, next.vec(k) * VEC - o, n == a.N - 1, at, a.x_end);
       } else if (SHIFTED) {
         xv[k].zero();
+      }
+    }
+  };
+  // The vectors of a row of x as y's: the neighbours of a thread's vectors are in L1.
+  auto realign = [&](int64_t n, const Place<VEC, KF, A>& place) {
+    const int64_t at = a.xm.at(static_cast<int>(n));
+    const TX* x = static_cast<const TX*>(a.x) + at;
+    const int o = place.own(x), by = o - place.s;
+    if (by == 0) return;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (place.vec(k) + (by < 0 ? -1 : 1)) * VEC - o;
+      Vec<TX, VEC> other;
+      other.zero();
+      if (c > -VEC && c < a.D) place.load(other, x, c, false, at, a.x_end);
+      if (by < 0) {
+        xv[k].join(other, xv[k], by + VEC);
+      } else {
+        xv[k].join(xv[k], other, by);
       }
     }
   };
@@ -352,7 +391,10 @@ __global__ void __launch_bounds__(MAX_THREADS) fwd_kernel(NormFwd a) {
   int buf = 0;
   for (; base < a.N; base += step) {
     const int64_t n = base + threadIdx.y;
-    const Place<VEC, KF, SHIFTED> place = next;
+    const Place<VEC, KF, A> place = next;
+    if constexpr (REALIGNED) {
+      if (n < a.N) realign(n, place);
+    }
 #pragma unroll
     for (int k = 0; k < K; ++k) place.trim(xv[k], k);
     Pair d[E];
@@ -537,8 +579,9 @@ __device__ __forceinline__ float load_cluster(uint32_t addr) {
   return f;
 }
 
-template <typename TX, typename TY, int VEC, int K, int KF, bool LAYER, bool SHIFTED, int THREADS>
+template <typename TX, typename TY, int VEC, int K, int KF, bool LAYER, Access A, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1) bwd_kernel(NormBwd a) {
+  constexpr bool REALIGNED = A == Access::REALIGNED, SHIFTED = REALIGNED || A == Access::SHIFTED;
   constexpr int E = K * VEC / 2, RING = bwd_ring<VEC, K>();
   constexpr int AHEAD = RING > 0 ? RING : 1;  // rows whose statistics are loaded
   extern __shared__ __align__(16) float dynamic[];  // the ring, then the gain; at the end the groups' sums
@@ -553,32 +596,64 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_kernel(NormBwd a) {
   const float inv_d = 1.0f / static_cast<float>(a.D);
 
   // A group's rows are all shifted alike: there is one row, or `step` is a multiple of VEC.
-  Place<VEC, KF, SHIFTED> place(a.D);
+  Place<VEC, KF, A> place(a.D, a.shift);
   float mean[AHEAD], rstd[AHEAD];
   auto load_stats = [&](int64_t n, int i) {
     mean[i] = LAYER && n < a.N ? a.mean[n] : 0.0f;
     rstd[i] = n < a.N ? a.rstd[n] : 0.0f;
   };
   // Requests row n into place `at` of the ring.
-  auto request = [&](int64_t n, int at) {
-    if (n < a.N) {
-      const TX* x = static_cast<const TX*>(a.x) + a.xm.at(static_cast<int>(n));
-      const TY* dy = static_cast<const TY*>(a.dy) + a.gm.at(static_cast<int>(n));
+  auto request_from = [&](auto* ring, const auto* m, bool last, int64_t row, int64_t end, int at) {
+    using V = std::remove_reference_t<decltype(*ring)>;
+    m += row;
+    const int o = place.own(m);
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        if (!place.has(k)) continue;
-        Vec<TX, VEC>* const to_x = ring_x + (at * K + k) * THREADS + own;
-        Vec<TY, VEC>* const to_g = ring_g + (at * K + k) * THREADS + own;
-        if (SHIFTED && n == a.N - 1 && !place.whole(k)) {  // there may be no memory behind the last row
-          to_x->load_some(x + place.column(k), place.lo(k), place.hi(k));
-          to_g->load_some(dy + place.column(k), place.lo(k), place.hi(k));
-        } else {
-          copy_async<sizeof(Vec<TX, VEC>)>(to_x, x + place.column(k));
-          copy_async<sizeof(Vec<TY, VEC>)>(to_g, dy + place.column(k));
-        }
+    for (int k = 0; k < K; ++k) {
+      if (!place.has(k, o)) continue;
+      V* const to = ring + (at * K + k) * THREADS + own;
+      const int c = place.vec(k) * VEC - o;
+      if (place.readable(c, last, row, end)) {
+        copy_async<sizeof(V)>(to, m + c);
+      } else {
+        to->load_some(m + c, max(0, -c), min(VEC, a.D - c));
       }
     }
+  };
+  auto request = [&](int64_t n, int at) {
+    if (n < a.N) {
+      const bool last = n == a.N - 1;
+      request_from(ring_x, static_cast<const TX*>(a.x), last, a.xm.at(static_cast<int>(n)), a.x_end, at);
+      request_from(ring_g, static_cast<const TY*>(a.dy), last, a.gm.at(static_cast<int>(n)), a.dy_end, at);
+    }
     end_copy_group();
+  };
+  // Vector k of an input whose rows are shifted by `by` more than dx's.
+  auto take = [&](auto& v, const auto* ring, int at, int k, int by) {
+    const auto* const mine = ring + (at * K + k) * THREADS + own;
+    if (!REALIGNED || by == 0) {
+      v = *mine;
+      return;
+    }
+    // The neighbouring vector; what lies before the first and behind the last is trimmed.
+    int to = by < 0 ? -1 : 1, k2 = k;
+    if (l + to < 0 || l + to >= tpr) {
+      k2 += to;
+      to -= to * tpr;
+    }
+    const auto* const other = k2 < 0 || k2 >= K ? mine : ring + (at * K + k2) * THREADS + own + to;
+    if (by < 0) {
+      v.join(*other, *mine, by + VEC);
+    } else {
+      v.join(*mine, *other, by);
+    }
+  };
+  // The threads that share a row's vectors.
+  auto row_sync = [&] {
+    if (tpr > 32) {
+      group_sync();
+    } else {
+      __syncwarp();
+    }
   };
   let_next_start();
   wait_for_previous();
@@ -607,14 +682,22 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_kernel(NormBwd a) {
     Vec<TY, VEC> g[K];
     const float row_mean = mean[0], row_rstd = rstd[0];
     if constexpr (RING > 0) wait_copy_groups<RING - 1>();
+    int by_x = 0, by_g = 0;
+    if constexpr (REALIGNED) {
+      row_sync();  // the other threads' copies are there too
+      if (n < a.N) {
+        by_x = place.own(static_cast<const TX*>(a.x) + a.xm.at(static_cast<int>(n))) - place.s;
+        by_g = place.own(static_cast<const TY*>(a.dy) + a.gm.at(static_cast<int>(n))) - place.s;
+      }
+    }
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       x[k].zero();
       g[k].zero();  // a row of zeros adds nothing
       if (n < a.N && place.has(k)) {
         if constexpr (RING > 0) {
-          x[k] = ring_x[(at * K + k) * THREADS + own];
-          g[k] = ring_g[(at * K + k) * THREADS + own];
+          take(x[k], ring_x, at, k, by_x);
+          take(g[k], ring_g, at, k, by_g);
           place.trim(x[k], k);
           place.trim(g[k], k);
         } else {
@@ -624,6 +707,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_kernel(NormBwd a) {
       }
     }
     if constexpr (RING > 0) {
+      if (REALIGNED) row_sync();  // and have been read
       request(n + RING * step, at);
       at = at + 1 == RING ? 0 : at + 1;
     }
@@ -909,19 +993,20 @@ constexpr int MAX_SMEM = 227 * 1024 - 2048;   // dynamic shared memory of a bloc
 constexpr int PLAIN_SMEM = 48 * 1024 - 2048;  // of a block that has not asked for more
 
 // Vectors that a row may touch, and floats of its parameters in shared memory.
-template <int VEC, bool SHIFTED>
+constexpr bool is_shifted(Access access) { return access == Access::SHIFTED || access == Access::REALIGNED; }
+template <int VEC, Access A>
 int64_t row_vecs(int64_t D) {
-  return SHIFTED ? (D + 2 * VEC - 2) / VEC : D / VEC;
+  return is_shifted(A) ? (D + 2 * VEC - 2) / VEC : D / VEC;
 }
-template <int VEC, bool SHIFTED>
+template <int VEC, Access A>
 int64_t param_floats(int64_t D) {
-  return SHIFTED ? VEC * row_vecs<VEC, SHIFTED>(D) : D;
+  return is_shifted(A) ? VEC * row_vecs<VEC, A>(D) : D;
 }
 
-template <typename TX, typename TY, int VEC, int K, int KF, bool LAYER, bool SHIFTED>
+template <typename TX, typename TY, int VEC, int K, int KF, bool LAYER, Access A>
 cudaError_t run_fwd(const NormFwd& a, int tpr, cudaStream_t s) {
-  auto kernel = fwd_kernel<TX, TY, VEC, K, KF, LAYER, SHIFTED>;
-  const int smem = static_cast<int>(sizeof(float) * param_floats<VEC, SHIFTED>(a.D)) * (LAYER ? 2 : 1);
+  auto kernel = fwd_kernel<TX, TY, VEC, K, KF, LAYER, A>;
+  const int smem = static_cast<int>(sizeof(float) * param_floats<VEC, A>(a.D)) * (LAYER ? 2 : 1);
   // Two blocks of 256 threads fill an SM's registers; where their parameters do not fit twice, one of 512.
   const bool pair = 2 * (smem + 2048) <= MAX_SMEM;
   const int groups = std::max(1, (pair ? 256 : MAX_THREADS) / tpr);
@@ -935,33 +1020,26 @@ cudaError_t run_fwd(const NormFwd& a, int tpr, cudaStream_t s) {
 }
 
 // Launches fwd_kernel for rows that the registers of one block hold; false for longer ones.
-template <typename TX, typename TY, int VEC, bool LAYER, bool SHIFTED>
+template <typename TX, typename TY, int VEC, bool LAYER, Access A>
 bool fwd_in_registers(const NormFwd& a, cudaStream_t s, cudaError_t* e) {
-  const int64_t vecs = row_vecs<VEC, SHIFTED>(a.D);
-  if (static_cast<int64_t>(sizeof(float)) * param_floats<VEC, SHIFTED>(a.D) * (LAYER ? 2 : 1) > MAX_SMEM) return false;
+  const int64_t vecs = row_vecs<VEC, A>(a.D);
+  if (static_cast<int64_t>(sizeof(float)) * param_floats<VEC, A>(a.D) * (LAYER ? 2 : 1) > MAX_SMEM) return false;
   if constexpr (VEC > 1) {
     // Short rows with 4 vectors a thread: 65,536 x 256 15.2 us against 16.0 with 8; 1,024 wide 46.0 against 45.5.
     const int tpr = group_threads(vecs, vecs <= 64 ? 4 : 8);
     if (tpr > MAX_THREADS) return false;
     switch (cdiv(vecs, tpr)) {  // vectors a thread; all but its last are there in every thread
-      case 1: *e = run_fwd<TX, TY, VEC, 1, 0, LAYER, SHIFTED>(a, tpr, s); break;
-      case 2: *e = run_fwd<TX, TY, VEC, 2, 1, LAYER, SHIFTED>(a, tpr, s); break;
-      case 3: *e = run_fwd<TX, TY, VEC, 3, 2, LAYER, SHIFTED>(a, tpr, s); break;
-      case 4: *e = run_fwd<TX, TY, VEC, 4, 3, LAYER, SHIFTED>(a, tpr, s); break;
-      case 5: *e = run_fwd<TX, TY, VEC, 5, 4, LAYER, SHIFTED>(a, tpr, s); break;
-      case 6: *e = run_fwd<TX, TY, VEC, 6, 5, LAYER, SHIFTED>(a, tpr, s); break;
-      case 7: *e = run_fwd<TX, TY, VEC, 7, 6, LAYER, SHIFTED>(a, tpr, s); break;
-      default: *e = run_fwd<TX, TY, VEC, 8, 7, LAYER, SHIFTED>(a, tpr, s); break;
+      case 1: *e = run_fwd<TX, TY, VEC, 1, 0, LAYER, A>(a, tpr, s); break;
+      case 2: *e = run_fwd<TX, TY, VEC, 2, 1, LAYER, A>(a, tpr, s); break;
+      case 3: *e = run_fwd<TX, TY, VEC, 3, 2, LAYER, A>(a, tpr, s); break;
+      case 4: *e = run_fwd<TX, TY, VEC, 4, 3, LAYER, A>(a, tpr, s); break;
+      case 5: *e = run_fwd<TX, TY, VEC, 5, 4, LAYER, A>(a, tpr, s); break;
+      case 6: *e = run_fwd<TX, TY, VEC, 6, 5, LAYER, A>(a, tpr, s); break;
+      case 7: *e = run_fwd<TX, TY, VEC, 7, 6, LAYER, A>(a, tpr, s); break;
+      default: *e = run_fwd<TX, TY, VEC, 8, 7, LAYER, A>(a, tpr, s); break;
     }
   } else {
-    const int K = vecs <= 32 ? 4 : vecs <= 128 ? 8 : 16;
-    const int tpr = group_threads(vecs, K);
-    if (tpr > MAX_THREADS) return false;
-    switch (K) {
-      case 4: *e = run_fwd<TX, TY, VEC, 4, 0, LAYER, SHIFTED>(a, tpr, s); break;
-      case 8: *e = run_fwd<TX, TY, VEC, 8, 4, LAYER, SHIFTED>(a, tpr, s); break;
-      default: *e = run_fwd<TX, TY, VEC, 16, 8, LAYER, SHIFTED>(a, tpr, s); break;
-    }
+    *e = run_fwd<TX, TY, VEC, 4, 0, LAYER, A>(a, group_threads(vecs, 4), s);
   }
   return true;
 }
@@ -994,20 +1072,23 @@ cudaError_t fwd(const NormFwd& a, Access access, cudaStream_t s, int* launches) 
   ++*launches;
   cudaError_t e = cudaSuccess;
   if (access == Access::WIDE) {
-    if (fwd_few<TX, TY, VEC, LAYER>(a, s, &e) || fwd_in_registers<TX, TY, VEC, LAYER, false>(a, s, &e)) return e;
+    if (fwd_few<TX, TY, VEC, LAYER>(a, s, &e) || fwd_in_registers<TX, TY, VEC, LAYER, Access::WIDE>(a, s, &e))
+      return e;
     return fwd_long<TX, TY, VEC, LAYER>(a, s);
   }
   if (fwd_few<TX, TY, 1, LAYER>(a, s, &e)) return e;
-  if (access == Access::SHIFTED && fwd_in_registers<TX, TY, VEC, LAYER, true>(a, s, &e)) return e;
-  if (fwd_in_registers<TX, TY, 1, LAYER, false>(a, s, &e)) return e;
+  if (access == Access::SHIFTED     ? fwd_in_registers<TX, TY, VEC, LAYER, Access::SHIFTED>(a, s, &e)
+      : access == Access::REALIGNED ? fwd_in_registers<TX, TY, VEC, LAYER, Access::REALIGNED>(a, s, &e)
+                                    : fwd_in_registers<TX, TY, 1, LAYER, Access::SINGLE>(a, s, &e))
+    return e;
   return fwd_long<TX, TY, 1, LAYER>(a, s);
 }
 
 constexpr int CLUSTER = 8;  // blocks, the portable limit
-template <typename TX, typename TY, int VEC, int K, int KF, bool LAYER, bool SHIFTED,
+template <typename TX, typename TY, int VEC, int K, int KF, bool LAYER, Access A,
           int THREADS = bwd_threads<TX, VEC, K, LAYER>()>
 cudaError_t run_bwd(const NormBwd& a, int tpr, int* parts, cudaStream_t s) {
-  auto kernel = bwd_kernel<TX, TY, VEC, K, KF, LAYER, SHIFTED, THREADS>;
+  auto kernel = bwd_kernel<TX, TY, VEC, K, KF, LAYER, A, THREADS>;
   const int groups = std::max(1, THREADS / tpr);
   NormBwd b = a;
   // One row a group at most: one launch less, 4 us of a call's host time; the GPU's time is within 1 us either way
@@ -1022,9 +1103,9 @@ cudaError_t run_bwd(const NormBwd& a, int tpr, int* parts, cudaStream_t s) {
     blocks = size;
   }
   *parts = b.cluster ? 0 : blocks;
-  const int64_t sums = static_cast<int64_t>(a.D) * groups * (LAYER && (SHIFTED || groups > 1 || b.cluster) ? 2 : 1);
+  const int64_t sums = static_cast<int64_t>(a.D) * groups * (LAYER && (is_shifted(A) || groups > 1 || b.cluster) ? 2 : 1);
   const int64_t smem = std::max<int64_t>(
-      sizeof(float) * sums, bwd_ring_bytes<TX, TY, VEC, K, THREADS>() + sizeof(float) * param_floats<VEC, SHIFTED>(a.D));
+      sizeof(float) * sums, bwd_ring_bytes<TX, TY, VEC, K, THREADS>() + sizeof(float) * param_floats<VEC, A>(a.D));
   if (smem > PLAIN_SMEM) {
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM);
@@ -1035,24 +1116,24 @@ cudaError_t run_bwd(const NormBwd& a, int tpr, int* parts, cudaStream_t s) {
 }
 
 // Launches bwd_kernel for rows that the registers of one block hold; false for longer ones.
-template <typename TX, typename TY, int VEC, bool LAYER, bool SHIFTED>
+template <typename TX, typename TY, int VEC, bool LAYER, Access A>
 bool bwd_in_registers(const NormBwd& a, int* parts, cudaStream_t s, cudaError_t* e) {
-  const int64_t vecs = row_vecs<VEC, SHIFTED>(a.D);
+  const int64_t vecs = row_vecs<VEC, A>(a.D);
   if constexpr (VEC > 1) {
     constexpr int K = 16 / VEC;
     int tpr = group_threads(vecs, K);
     if constexpr (LAYER && VEC == 8) {
       if (2 * tpr > MAX_THREADS && 2 * tpr <= WIDER) {
-        *e = run_bwd<TX, TY, VEC, K, K - 1, LAYER, SHIFTED, WIDER>(a, tpr, parts, s);
+        *e = run_bwd<TX, TY, VEC, K, K - 1, LAYER, A, WIDER>(a, tpr, parts, s);
         return true;
       }
     }
     if (tpr <= bwd_threads<TX, VEC, K, LAYER>()) {
       switch (cdiv(vecs, tpr)) {  // vectors a thread; all but its last are there in every thread
-        case 1: *e = run_bwd<TX, TY, VEC, 1, 0, LAYER, SHIFTED>(a, tpr, parts, s); break;
-        case 2: *e = run_bwd<TX, TY, VEC, 2, 1, LAYER, SHIFTED>(a, tpr, parts, s); break;
-        case 3: *e = run_bwd<TX, TY, VEC, K < 3 ? 2 : 3, K < 3 ? 1 : 2, LAYER, SHIFTED>(a, tpr, parts, s); break;
-        default: *e = run_bwd<TX, TY, VEC, K, K - 1, LAYER, SHIFTED>(a, tpr, parts, s); break;
+        case 1: *e = run_bwd<TX, TY, VEC, 1, 0, LAYER, A>(a, tpr, parts, s); break;
+        case 2: *e = run_bwd<TX, TY, VEC, 2, 1, LAYER, A>(a, tpr, parts, s); break;
+        case 3: *e = run_bwd<TX, TY, VEC, K < 3 ? 2 : 3, K < 3 ? 1 : 2, LAYER, A>(a, tpr, parts, s); break;
+        default: *e = run_bwd<TX, TY, VEC, K, K - 1, LAYER, A>(a, tpr, parts, s); break;
       }
       return true;
     }
@@ -1060,14 +1141,10 @@ bool bwd_in_registers(const NormBwd& a, int* parts, cudaStream_t s, cudaError_t*
     // as few values a thread as 512 threads allow
     const bool most_values = vecs > 3 * K / 2 * MAX_THREADS;
     tpr = group_threads(vecs, most_values ? 2 * K : 3 * K / 2);
-    *e = most_values ? run_bwd<TX, TY, VEC, 2 * K, 3 * K / 2 - 1, LAYER, SHIFTED>(a, tpr, parts, s)
-                     : run_bwd<TX, TY, VEC, 3 * K / 2, K - 1, LAYER, SHIFTED>(a, tpr, parts, s);
+    *e = most_values ? run_bwd<TX, TY, VEC, 2 * K, 3 * K / 2 - 1, LAYER, A>(a, tpr, parts, s)
+                     : run_bwd<TX, TY, VEC, 3 * K / 2, K - 1, LAYER, A>(a, tpr, parts, s);
   } else {
-    const int K = vecs <= 32 ? 4 : 16;
-    const int tpr = group_threads(vecs, K);
-    if (tpr > MAX_THREADS) return false;
-    *e = K == 4 ? run_bwd<TX, TY, VEC, 4, 0, LAYER, SHIFTED>(a, tpr, parts, s)
-                : run_bwd<TX, TY, VEC, 16, 8, LAYER, SHIFTED>(a, tpr, parts, s);
+    *e = run_bwd<TX, TY, VEC, 4, 0, LAYER, A>(a, group_threads(vecs, 4), parts, s);
   }
   return true;
 }
@@ -1094,10 +1171,11 @@ cudaError_t bwd(const NormBwd& a, Access access, cudaStream_t s, int* launches) 
     ++*launches;
     cudaError_t e = cudaSuccess;
     if (access == Access::WIDE) {
-      if (!bwd_in_registers<TX, TY, VEC, LAYER, false>(a, &parts, s, &e))
+      if (!bwd_in_registers<TX, TY, VEC, LAYER, Access::WIDE>(a, &parts, s, &e))
         e = bwd_long<TX, TY, VEC, LAYER>(a, &parts, s, launches);
-    } else if (!(access == Access::SHIFTED && bwd_in_registers<TX, TY, VEC, LAYER, true>(a, &parts, s, &e)) &&
-               !bwd_in_registers<TX, TY, 1, LAYER, false>(a, &parts, s, &e)) {
+    } else if (!(access == Access::SHIFTED     ? bwd_in_registers<TX, TY, VEC, LAYER, Access::SHIFTED>(a, &parts, s, &e)
+                 : access == Access::REALIGNED ? bwd_in_registers<TX, TY, VEC, LAYER, Access::REALIGNED>(a, &parts, s, &e)
+                                               : bwd_in_registers<TX, TY, 1, LAYER, Access::SINGLE>(a, &parts, s, &e))) {
       e = bwd_long<TX, TY, 1, LAYER>(a, &parts, s, launches);
     }
     if (e != cudaSuccess) return e;

@@ -33,6 +33,9 @@ struct NormFwd {
   int p_type, N, D;
   float eps, offset;
   int sms;  // of the device
+  // With Access::REALIGNED:
+  int shift;      // elements by which y starts behind a vector's start
+  int64_t x_end;  // elements from x to the end of its last row
 };
 
 struct NormBwd {
@@ -50,16 +53,20 @@ struct NormBwd {
   float* part_b;  // [parts][D]
   int p_type, N, D;
   float offset;
-  int sms;            // of the device
+  int sms;  // of the device
+  // With Access::REALIGNED:
+  int shift;              // elements by which dx starts behind a vector's start
+  int64_t x_end, dy_end;  // elements from x and dy to the end of their last rows
   bool cluster = false;  // the launcher's: the grid is one cluster that writes dw and db
 };
 
 // Blocks whose partial parameter gradients are added at the end, at most.
 constexpr int NORM_MAX_PARTS = 304;
 
-// How rows can be read and written: in aligned 16-byte vectors of x; in such
-// vectors that the row's start divides, alike in every matrix; element by element.
-enum class Access { WIDE, SHIFTED, SINGLE };
+// How rows are read and written: in aligned vectors of 16 bytes of x, which rows
+// consist of; in such vectors, whose elements a row's start shifts, alike in every
+// matrix; the same, shifted otherwise in some; by elements.
+enum class Access { WIDE, SHIFTED, REALIGNED, SINGLE };
 
 // The pair of types is one the entry points allow; `layer` picks layer norm or RMS norm.
 cudaError_t launch_norm_fwd_bf16(const NormFwd& a, bool layer, Access access, cudaStream_t s, int* launches);

@@ -33,10 +33,22 @@ RowMap row_map(const Rows& r) {
 bool rows_wide(const void* p, const Rows& r, int type, int vec) {
   return multiple(p, std::min(16, vec * type_bytes(type))) && r.row_stride % vec == 0 && r.outer_stride % vec == 0;
 }
-// Whether every row of a matrix starts at its index times D, modulo vec, from an aligned base.
+// Elements by which p lies behind a vector's start.
+int shift_of(const void* p, int type, int vec) {
+  return static_cast<int>(reinterpret_cast<uintptr_t>(p) / static_cast<uintptr_t>(type_bytes(type))) & (vec - 1);
+}
+// Whether every row of a matrix starts at its index times D, modulo vec, from an
+// aligned base, and the last one lies behind all others.
 bool rows_shifted(const void* p, const Rows& r, int type, int vec, int64_t N, int64_t D) {
-  return multiple(p, std::min(16, vec * type_bytes(type))) && r.inner >= N &&
+  return shift_of(p, type, vec) == 0 && r.inner >= N &&
          (N <= 1 || (r.row_stride >= D && (r.row_stride - D) % vec == 0));
+}
+// Elements to the end of the last row in memory.
+int64_t rows_end(const Rows& r, int64_t N, int64_t D) {
+  if (N == 0) return 0;
+  const int64_t inner = std::min(r.inner, N), runs = N / inner, rest = N % inner;
+  const int64_t whole = (runs - 1) * r.outer_stride + (inner - 1) * r.row_stride;
+  return D + (rest > 0 ? std::max(whole, runs * r.outer_stride + (rest - 1) * r.row_stride) : whole);
 }
 bool param_wide(const void* p, int type, int vec) { return multiple(p, std::min(16, vec * type_bytes(type))); }
 
@@ -65,12 +77,25 @@ cce_status forward(const void* x, const Rows& xr, int x_type, const void* w, con
   const Access access = D % vec == 0 && rows_wide(x, xr, x_type, vec) && rows_wide(y, dense, y_type, vec) &&
                                 param_wide(w, p_type, vec) && param_wide(b, p_type, vec)
                             ? Access::WIDE
-                        : D >= SHIFTED_MIN && rows_shifted(x, xr, x_type, vec, N, D) &&
-                                rows_shifted(y, dense, y_type, vec, N, D)
+                        : D < SHIFTED_MIN ? Access::SINGLE
+                        : rows_shifted(x, xr, x_type, vec, N, D) && rows_shifted(y, dense, y_type, vec, N, D)
                             ? Access::SHIFTED
-                            : Access::SINGLE;
-  const NormFwd a{x,    row_map(xr), w,      b,   y, mean, rstd, p_type, static_cast<int>(N), static_cast<int>(D),
-                  eps, offset, sms};
+                            : Access::REALIGNED;
+  const NormFwd a{x,
+                  row_map(xr),
+                  w,
+                  b,
+                  y,
+                  mean,
+                  rstd,
+                  p_type,
+                  static_cast<int>(N),
+                  static_cast<int>(D),
+                  eps,
+                  offset,
+                  sms,
+                  shift_of(y, y_type, vec),
+                  rows_end(xr, N, D)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int launches = 0;
   const auto launch = x_type == CCE_BF16  ? launch_norm_fwd_bf16
@@ -105,10 +130,11 @@ cce_status backward(const void* dy, const Rows& gr, int y_type, const void* x, c
   const Access access = D % vec == 0 && rows_wide(x, xr, x_type, vec) && rows_wide(dy, gr, y_type, vec) &&
                                 rows_wide(dx, dense, x_type, vec) && param_wide(w, p_type, vec)
                             ? Access::WIDE
-                        : D >= SHIFTED_MIN && rows_shifted(x, xr, x_type, vec, N, D) &&
-                                rows_shifted(dy, gr, y_type, vec, N, D) && rows_shifted(dx, dense, x_type, vec, N, D)
+                        : D < SHIFTED_MIN ? Access::SINGLE
+                        : rows_shifted(x, xr, x_type, vec, N, D) && rows_shifted(dy, gr, y_type, vec, N, D) &&
+                                rows_shifted(dx, dense, x_type, vec, N, D)
                             ? Access::SHIFTED
-                            : Access::SINGLE;
+                            : Access::REALIGNED;
   char* ws = static_cast<char*>(workspace);
   const NormBwd a{dy,
                   row_map(gr),
@@ -126,7 +152,10 @@ cce_status backward(const void* dy, const Rows& gr, int y_type, const void* x, c
                   static_cast<int>(N),
                   static_cast<int>(D),
                   offset,
-                  sms};
+                  sms,
+                  shift_of(dx ? dx : x, x_type, vec),
+                  rows_end(xr, N, D),
+                  rows_end(gr, N, D)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int launches = 0;
   const auto launch = x_type == CCE_BF16  ? launch_norm_bwd_bf16

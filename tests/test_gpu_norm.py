@@ -121,6 +121,71 @@ def test_odd_rows_at_a_pitch(cce, dtype):
     _check(cce, windows, w[:129].contiguous(), b[:129].contiguous(), torch.randn(900, 129, device="cuda").to(dtype), True)
 
 
+def _among_nans(t, run, before, pitch, gap):
+    """The rows of t at `pitch`, every `run` of them `gap` apart, `before` elements
+    into a buffer of NaNs that ends with the last row."""
+    N, D = t.shape
+    runs, outer = N // run, run * pitch + gap
+    buf = torch.full((before + runs * outer - gap - pitch + D,), float("nan"), device="cuda", dtype=t.dtype)
+    view = buf.as_strided((runs, run, D), (outer, pitch, 1), before)
+    view.copy_(t.view(runs, run, D))
+    return view
+
+
+@pytest.mark.parametrize("layer", [True, False])
+@pytest.mark.parametrize("x_type,y_type", PAIRS)
+@pytest.mark.parametrize("N,D", [(1400, 64), (2100, 65), (1400, 333), (1400, 1001), (840, 1000), (700, 2049), (700, 5003),
+                                 (350, 13001)])
+def test_matrices_shifted_apart(cce, layer, x_type, y_type, N, D):
+    """Rows of x and dy at starts that no vector divides, each matrix's in its own
+    way, in runs, among NaNs; sizes past those of the kernels for few rows."""
+    x, w, b, dy = _inputs(N + D, (N, D), x_type, y_type, BF16)
+    for run, x_place, dy_place in [(N, (1, D, 0), (0, D, 0)), (7, (0, D, D), (0, D, D)),
+                                   (70, (5, D + 3, 1), (2, D, 6)), (14, (0, D, 0), (7, D + 1, 5))]:
+        _check(cce, _among_nans(x, run, *x_place), w, b, _among_nans(dy, run, *dy_place), layer)
+
+
+@pytest.mark.parametrize("layer", [True, False])
+@pytest.mark.parametrize("y_at,dx_at", [(64, 65), (67, 64), (61, 70)])
+@pytest.mark.parametrize("N,D", [(700, 1001), (1500, 136), (2000, 67)])
+def test_results_off_their_alignment(cce, layer, y_at, dx_at, N, D):
+    """y and dx at any element of a buffer, through the C ABI."""
+    from linear_cross_entropy_gb300 import _lib
+    lib = _lib.load()
+    x, w, b, dy = _inputs(N + D, (N, D), BF16, BF16, BF16)
+    y, dx = (torch.full((at + N * D + 64,), 7.0, device="cuda", dtype=BF16) for at in (y_at, dx_at))
+    dw, db = (torch.empty(D, device="cuda", dtype=BF16) for _ in range(2))
+    mean, rstd = (torch.empty(N, device="cuda") for _ in range(2))
+    need = lib.cce_norm_backward_workspace_bytes(N, D)
+    ws = torch.empty(need, device="cuda", dtype=torch.uint8)
+    stream = torch.cuda.current_stream().cuda_stream
+    rows, y_p, dx_p = (N, D, 0), y.data_ptr() + 2 * y_at, dx.data_ptr() + 2 * dx_at
+    if layer:
+        assert lib.cce_layer_norm_forward(x.data_ptr(), *rows, 2, w.data_ptr(), b.data_ptr(), 2, N, D, 1e-5, y_p, 2,
+                                          mean.data_ptr(), rstd.data_ptr(), stream) == 0
+        assert lib.cce_layer_norm_backward(dy.data_ptr(), *rows, 2, x.data_ptr(), *rows, 2, w.data_ptr(), 2,
+                                           mean.data_ptr(), rstd.data_ptr(), N, D, dx_p, dw.data_ptr(), db.data_ptr(),
+                                           ws.data_ptr(), need, stream) == 0
+    else:
+        assert lib.cce_rms_norm_forward(x.data_ptr(), *rows, 2, w.data_ptr(), 2, 0.0, N, D, 1e-5, y_p, 2,
+                                        rstd.data_ptr(), stream) == 0
+        assert lib.cce_rms_norm_backward(dy.data_ptr(), *rows, 2, x.data_ptr(), *rows, 2, w.data_ptr(), 2, 0.0,
+                                         rstd.data_ptr(), N, D, dx_p, dw.data_ptr(), ws.data_ptr(), need, stream) == 0
+    xd, gd, gain = U.f64(x), U.f64(dy), w.double().cpu().numpy()
+    bias = b.double().cpu().numpy() if layer else np.zeros(D)
+    m, r = ops.norm_stats(xd, 1e-5, layer)
+    U.within(y[y_at:-64].view(N, D), ops.norm_forward(xd, gain, bias, m, r), U.forward_magnitude(xd, gain, bias, m, r),
+             BF16, "y")
+    rd = rstd.double().cpu().numpy()
+    md = mean.double().cpu().numpy() if layer else np.zeros(N)
+    for got, exact, size, name in zip((dx[dx_at:-64].view(N, D), dw, db), ops.norm_backward(gd, xd, gain, md, rd, layer),
+                                      U.backward_magnitudes(gd, xd, gain, md, rd, layer), ("dx", "dw", "db")):
+        if layer or name != "db":
+            U.within(got, exact, size, BF16, name)
+    for t, at in ((y, y_at), (dx, dx_at)):
+        assert (t[:at] == 7.0).all() and (t[-64:] == 7.0).all()
+
+
 @pytest.mark.parametrize("N,D", [(1, 65), (3, 333), (500, 1001), (2000, 67), (40, 4097)])
 def test_nothing_is_written_outside_the_results(cce, N, D):
     """y, dx and the parameters' gradients between guard values, through the C ABI."""
