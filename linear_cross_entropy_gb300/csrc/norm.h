@@ -1,5 +1,5 @@
 // Layer norm and RMS norm: arguments of the kernels and their launchers, shared
-// by the entry points (ops_api.cu) and the per-type translation units.
+// by the entry points (norm_api.cu) and the per-type translation units.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -11,7 +11,11 @@
 namespace cce {
 namespace {
 
-constexpr int64_t SHIFTED_MIN = 64;  // columns from which a row's two partial vectors are the lesser part
+// Columns from which rows are taken in vectors wherever they start: a row's two partial vectors are then the lesser
+// part.  With rows shifted otherwise in one matrix than in another, fp16, 16 x 1,023 x 2,049 without every last token:
+// forward and backward of a layer norm 58 and 111 us, by elements 80 and 235; 1,029 x 1,001 7.2 and 10.7, by elements
+// 5.9 and 14.1.
+constexpr int64_t SHIFTED_MIN = 64;
 constexpr int64_t LIMIT = int64_t(1) << 31;
 
 struct Rows {
