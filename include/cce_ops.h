@@ -20,8 +20,10 @@
  * A norm works on N rows of D elements, unit stride inside a row.  Inputs x
  * and grad_y may be strided views: row n starts (n / inner) * outer_stride +
  * (n % inner) * row_stride elements after the pointer (a plain matrix has
- * inner = N).  Strides are >= 0; rows of an input may coincide.  Outputs y and
- * grad_x are dense [N, D].  Outputs of a norm overlap no input.
+ * inner = N).  Strides are >= 0; rows of an input may coincide.  Of what lies
+ * between the first and the last element of an input, aligned words of 16 bytes
+ * that hold an element of a row may be read whole.  Outputs y and grad_x are
+ * dense [N, D].  Outputs of a norm overlap no input.
  */
 #ifndef CCE_OPS_GB300_H
 #define CCE_OPS_GB300_H
@@ -52,7 +54,7 @@ int cce_ops_abi_version(void);
  * alignment of their element.  Fastest are rows of a multiple of 16 bytes that
  * start on 16 bytes; next, matrices whose rows all start alike (any D, at least
  * 64, aligned pointers, pitches that differ from D by a multiple of 16 bytes of
- * x).  A row whose squared deviations overflow fp32 gets rstd 0; one with
+ * x), then others of at least 64 columns.  A row whose squared deviations overflow fp32 gets rstd 0; one with
  * a NaN or an infinity becomes NaN, the other rows keep their results.
  */
 cce_status cce_layer_norm_forward(const void* x, int64_t x_inner, int64_t x_row_stride, int64_t x_outer_stride,

@@ -9,8 +9,10 @@ x is bf16, fp16 or fp32 with any number of leading dimensions; the result has
 x's type, or with out_dtype a 16-bit type from fp32 rows.  Arithmetic and the
 saved statistics are fp32.  Rows may be strided (hidden[:, :-1] is read in
 place); the result is contiguous.  Calls run on the current stream of x's
-device and can be captured into a CUDA graph.  Arguments that do not fit raise
-ValueError, a status of the library CCEError.
+device and can be captured into a CUDA graph (a backward pass while no graph of
+autograd that was made outside of the capture holds the same leaves: torch ties
+their accumulation to the stream of the first).  Arguments that do not fit
+raise ValueError, a status of the library CCEError.
 """
 from __future__ import annotations
 
