@@ -1029,9 +1029,14 @@ bool fwd_in_registers(const NormFwd& a, cudaStream_t s, cudaError_t* e) {
     // Short rows with 4 vectors a thread: 65,536 x 256 15.2 us against 16.0 with 8; 1,024 wide 46.0 against 45.5.
     const int tpr = group_threads(vecs, vecs <= 64 ? 4 : 8);
     if (tpr > MAX_THREADS) return false;
-    switch (cdiv(vecs, tpr)) {  // vectors a thread; all but its last are there in every thread
-      case 1: *e = run_fwd<TX, TY, VEC, 1, 0, LAYER, A>(a, tpr, s); break;
-      case 2: *e = run_fwd<TX, TY, VEC, 2, 1, LAYER, A>(a, tpr, s); break;
+    const int64_t each = cdiv(vecs, tpr);  // vectors a thread; all but its last are there in every thread
+    if constexpr (!is_shifted(A)) {      // whose rows have columns enough for three
+      if (each <= 2) {
+        *e = each == 1 ? run_fwd<TX, TY, VEC, 1, 0, LAYER, A>(a, tpr, s) : run_fwd<TX, TY, VEC, 2, 1, LAYER, A>(a, tpr, s);
+        return true;
+      }
+    }
+    switch (each) {
       case 3: *e = run_fwd<TX, TY, VEC, 3, 2, LAYER, A>(a, tpr, s); break;
       case 4: *e = run_fwd<TX, TY, VEC, 4, 3, LAYER, A>(a, tpr, s); break;
       case 5: *e = run_fwd<TX, TY, VEC, 5, 4, LAYER, A>(a, tpr, s); break;
@@ -1130,12 +1135,16 @@ bool bwd_in_registers(const NormBwd& a, int* parts, cudaStream_t s, cudaError_t*
       }
     }
     if (tpr <= bwd_threads<TX, VEC, K, LAYER>()) {
-      switch (cdiv(vecs, tpr)) {  // vectors a thread; all but its last are there in every thread
-        case 1: *e = run_bwd<TX, TY, VEC, 1, 0, LAYER, A>(a, tpr, parts, s); break;
-        case 2: *e = run_bwd<TX, TY, VEC, 2, 1, LAYER, A>(a, tpr, parts, s); break;
-        case 3: *e = run_bwd<TX, TY, VEC, K < 3 ? 2 : 3, K < 3 ? 1 : 2, LAYER, A>(a, tpr, parts, s); break;
-        default: *e = run_bwd<TX, TY, VEC, K, K - 1, LAYER, A>(a, tpr, parts, s); break;
+      const int64_t each = cdiv(vecs, tpr);  // vectors a thread; all but its last are there in every thread
+      if constexpr (!is_shifted(A)) {      // whose rows have columns enough for more than half of K
+        if (each <= K / 2) {
+          *e = each == 1 ? run_bwd<TX, TY, VEC, 1, 0, LAYER, A>(a, tpr, parts, s)
+                         : run_bwd<TX, TY, VEC, 2, 1, LAYER, A>(a, tpr, parts, s);
+          return true;
+        }
       }
+      *e = each < K ? run_bwd<TX, TY, VEC, K / 2 + 1, K / 2, LAYER, A>(a, tpr, parts, s)
+                    : run_bwd<TX, TY, VEC, K, K - 1, LAYER, A>(a, tpr, parts, s);
       return true;
     }
     if (vecs > 2 * K * MAX_THREADS) return false;
