@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(MAX_THREADS) fwd_long_kernel(NormFwd a) {
 //
 // Bound by memory, a layer norm by the registers that keep fewer rows in flight:
 // bf16 65,536 x 2,048, 805 MB, RMS norm 119 us (6.8 TB/s), layer norm 137 us (5.9
-// TB/s); 8,192 x 2,304 25 and 28 us, 3 to 5 us of it the parameters' gradients.
+// TB/s); 8,192 x 2,304 24 and 27 us, 3 us of it the parameters' gradients.
 // With the next row in registers instead of the ring 125 and 142 us; with three
 // or four rows in it 120 and 138.  Odd widths pay for their partial vectors: 16,384
 // x 1,001 29 and 34 us, x 1,024 22 and 25 us.
@@ -944,15 +944,14 @@ __global__ void __launch_bounds__(128) cols_kernel(NormBwd a) {
 }
 
 // The parameter gradients from `parts` partial rows (0 parts: zeros).  A block
-// adds 32 columns: its warps take the parts w, w + 32, ... in order (five of 152,
-// all in flight at once), and warp 0 adds the warps in order.  blockIdx.y = 0:
-// the weight's, 1: the bias's.  Bound by latency: 3.7 us alone for 2 x 152 x 2,304,
-// about 2 us behind the kernel that it follows.
-constexpr int REDUCE_WARPS = 32;
-static __global__ void __launch_bounds__(32 * REDUCE_WARPS) reduce_kernel(const float* part_w, const float* part_b,
-                                                                          int parts, int D, int p_type, void* dw,
-                                                                          void* db) {
-  __shared__ float ws[REDUCE_WARPS][32];
+// adds 32 columns: its warps take the parts w, w + WARPS, ... in order, LOADS of
+// them in flight at once, and warp 0 adds the warps in order.  blockIdx.y = 0: the
+// weight's, 1: the bias's.  Bound by latency, about 2 us behind the kernel that it
+// follows; with the loads in a loop of five instead, 3.
+template <int WARPS, int LOADS>
+__global__ void __launch_bounds__(32 * WARPS) reduce_kernel(const float* part_w, const float* part_b, int parts, int D,
+                                                            int p_type, void* dw, void* db) {
+  __shared__ float ws[WARPS][32];
   wait_for_previous();
   void* out = blockIdx.y == 0 ? dw : db;
   if (!out) return;
@@ -960,14 +959,22 @@ static __global__ void __launch_bounds__(32 * REDUCE_WARPS) reduce_kernel(const 
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
   float s = 0.0f;
   if (c < D) {
-#pragma unroll 5
-    for (int p = threadIdx.y; p < parts; p += REDUCE_WARPS) s += part[static_cast<int64_t>(p) * D + c];
+    for (int first = threadIdx.y; first < parts; first += WARPS * LOADS) {
+      float v[LOADS];
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) {
+        const int p = first + i * WARPS;
+        v[i] = p < parts ? part[static_cast<int64_t>(p) * D + c] : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) s += v[i];
+    }
   }
   ws[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
   if (threadIdx.y == 0 && c < D) {
     s = 0.0f;
-    for (int i = 0; i < REDUCE_WARPS; ++i) s += ws[i][threadIdx.x];
+    for (int i = 0; i < WARPS; ++i) s += ws[i][threadIdx.x];
     store_param(out, p_type, c, s);
   }
 }
@@ -1192,8 +1199,16 @@ cudaError_t bwd(const NormBwd& a, Access access, cudaStream_t s, int* launches) 
   }
   if ((!a.dw && !a.db) || (a.N > 0 && parts == 0)) return cudaSuccess;  // parts == 0: the cluster has written them
   ++*launches;
-  return launch_after(reduce_kernel, dim3(static_cast<unsigned>(cdiv(a.D, 32)), LAYER ? 2 : 1), dim3(32, REDUCE_WARPS), 0,
-                      1, s, a.part_w, a.part_b, parts, a.D, a.p_type, a.dw, a.db);
+  const dim3 grid(static_cast<unsigned>(cdiv(a.D, 32)), LAYER ? 2 : 1);
+  // Both hold the 152 parts of a full grid at once.  Few warps start sooner, where an SM has one block of them: layer
+  // norm of 9,360 x 896 15.1 us and 16.2 with 16 warps, 3,640 x 2,304 16.1 and 16.9, but 2,048 x 4,096, 256 blocks,
+  // 18.3 and 17.2; 8,376 x 1,001, behind the longer end of a kernel of shifted rows, 22.3 and 21.3.
+  if (static_cast<int64_t>(grid.x) * grid.y <= a.sms && a.D % 8 == 0) {
+    return launch_after(reduce_kernel<8, 20>, grid, dim3(32, 8), 0, 1, s, a.part_w, a.part_b, parts, a.D, a.p_type,
+                        a.dw, a.db);
+  }
+  return launch_after(reduce_kernel<16, 10>, grid, dim3(32, 16), 0, 1, s, a.part_w, a.part_b, parts, a.D, a.p_type,
+                      a.dw, a.db);
 }
 
 }  // namespace norm
