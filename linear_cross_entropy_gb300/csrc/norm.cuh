@@ -789,7 +789,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_kernel(NormBwd a) {
   // Several groups: their sums side by side in shared memory (the weight's, then
   // the bias's), added in order.  One group: straight into the partial row.
   if (!a.dw && !a.db) return;
-  const bool side_by_side = SHIFTED || groups > 1 || a.cluster;
+  const bool side_by_side = SHIFTED || groups > 1;
   float* const sums = dynamic;
   if (side_by_side) __syncthreads();  // the gain and the ring have been read
   const int64_t row = static_cast<int64_t>(blockIdx.x) * a.D;
@@ -1104,9 +1104,10 @@ cudaError_t run_bwd(const NormBwd& a, int tpr, int* parts, cudaStream_t s) {
   auto kernel = bwd_kernel<TX, TY, VEC, K, KF, LAYER, A, THREADS>;
   const int groups = std::max(1, THREADS / tpr);
   NormBwd b = a;
-  // One row a group at most: one launch less, 4 us of a call's host time; the GPU's time is within 1 us either way
-  // (64 x 896 5.4 us by the cluster, 5.4 by two launches; with two rows a group 7.2 against 5.4).
-  b.cluster = (a.dw || a.db) && a.N <= static_cast<int64_t>(CLUSTER) * groups;
+  // One row a group at most, of a quarter of the block's threads: one launch less, 1 x 896 4.5 us against 4.9 by two,
+  // 300 x 128 5.2 against 5.8, 64 x 896 5.5 both; with two rows a group 7.2 against 5.4, with longer rows 7.9 against
+  // 7.0 (16 x 4,096).
+  b.cluster = (a.dw || a.db) && groups >= 4 && a.N <= static_cast<int64_t>(CLUSTER) * groups;
   // In multiples of 8 blocks, so that a group's rows are all shifted alike.
   int blocks = static_cast<int>(std::min<int64_t>(std::min(NORM_MAX_PARTS, std::max(8, a.sms / 8 * 8)),
                                                   cdiv(a.N, groups)));
@@ -1116,7 +1117,7 @@ cudaError_t run_bwd(const NormBwd& a, int tpr, int* parts, cudaStream_t s) {
     blocks = size;
   }
   *parts = b.cluster ? 0 : blocks;
-  const int64_t sums = static_cast<int64_t>(a.D) * groups * (LAYER && (is_shifted(A) || groups > 1 || b.cluster) ? 2 : 1);
+  const int64_t sums = static_cast<int64_t>(a.D) * groups * (LAYER && (is_shifted(A) || groups > 1) ? 2 : 1);
   const int64_t smem = std::max<int64_t>(
       sizeof(float) * sums, bwd_ring_bytes<TX, TY, VEC, K, THREADS>() + sizeof(float) * param_floats<VEC, A>(a.D));
   if (smem > PLAIN_SMEM) {
