@@ -40,33 +40,12 @@ struct Vec {
 #pragma unroll
     for (int i = 0; i < WORDS; ++i) w[i] = 0u;
   }
-  // From memory that nothing writes while the kernel runs.
-  __device__ __forceinline__ void load(const T* p) {
-    if constexpr (BYTES >= 16) {
-#pragma unroll
-      for (int i = 0; i < BYTES / 16; ++i) words4(i, __ldg(reinterpret_cast<const uint4*>(p) + i));
-    } else if constexpr (BYTES == 8) {
-      words2(__ldg(reinterpret_cast<const uint2*>(p)));
-    } else if constexpr (BYTES == 4) {
-      w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-    } else {
-      static_assert(BYTES == 2, "one 16-bit element");
-      w[0] = __ldg(reinterpret_cast<const uint16_t*>(p));
-    }
-  }
-  // From memory that the kernel itself writes.
-  __device__ __forceinline__ void load_written(const T* p) {
-    if constexpr (BYTES >= 16) {
-#pragma unroll
-      for (int i = 0; i < BYTES / 16; ++i) words4(i, reinterpret_cast<const uint4*>(p)[i]);
-    } else if constexpr (BYTES == 8) {
-      words2(*reinterpret_cast<const uint2*>(p));
-    } else if constexpr (BYTES == 4) {
-      w[0] = *reinterpret_cast<const uint32_t*>(p);
-    } else {
-      w[0] = *reinterpret_cast<const uint16_t*>(p);
-    }
-  }
+  // Ordinary loads: a kernel started by launch_after() reads what the kernel before it was still writing when it
+  // started, and only these are ordered behind wait_for_previous().
+  __device__ __forceinline__ void load(const T* p) { load_as<false>(p); }
+  // From memory that nothing writes from the kernel's start to its end: not in a kernel started by launch_after().
+  // These may be moved across the kernel's own stores.
+  __device__ __forceinline__ void load_constant(const T* p) { load_as<true>(p); }
   __device__ __forceinline__ void store(T* p) const {
     if constexpr (BYTES >= 16) {
 #pragma unroll
@@ -87,9 +66,9 @@ struct Vec {
     for (int e = 0; e < VEC; ++e) {
       if (e >= lo && e < hi) {
         if constexpr (sizeof(T) == 4) {
-          w[e] = __ldg(reinterpret_cast<const uint32_t*>(p) + e);
+          w[e] = reinterpret_cast<const uint32_t*>(p)[e];
         } else {
-          w[e / 2] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(p) + e)) << (16 * (e & 1));
+          w[e / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[e]) << (16 * (e & 1));
         }
       }
     }
@@ -169,6 +148,28 @@ struct Vec {
   }
 
  private:
+  template <bool CONSTANT, typename W>
+  __device__ __forceinline__ static W word(const W* p) {
+    if constexpr (CONSTANT) {
+      return __ldg(p);
+    } else {
+      return *p;
+    }
+  }
+  template <bool CONSTANT>
+  __device__ __forceinline__ void load_as(const T* p) {
+    if constexpr (BYTES >= 16) {
+#pragma unroll
+      for (int i = 0; i < BYTES / 16; ++i) words4(i, word<CONSTANT>(reinterpret_cast<const uint4*>(p) + i));
+    } else if constexpr (BYTES == 8) {
+      words2(word<CONSTANT>(reinterpret_cast<const uint2*>(p)));
+    } else if constexpr (BYTES == 4) {
+      w[0] = word<CONSTANT>(reinterpret_cast<const uint32_t*>(p));
+    } else {
+      static_assert(BYTES == 2, "one 16-bit element");
+      w[0] = word<CONSTANT>(reinterpret_cast<const uint16_t*>(p));
+    }
+  }
   __device__ __forceinline__ void words4(int i, const uint4& v) {
     w[4 * i] = v.x;
     w[4 * i + 1] = v.y;
@@ -242,11 +243,14 @@ __device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) {
   return r;
 }
 
-template <typename T, int VEC, bool SOME>
+template <typename T, int VEC, bool SOME, bool CONSTANT>
 __device__ __forceinline__ void load_param_as(const T* p, int n, float (&out)[VEC]) {
+  static_assert(!SOME || !CONSTANT, "load_some is ordinary");
   Vec<T, VEC> v;
   if constexpr (SOME) {
     v.load_some(p, 0, n);
+  } else if constexpr (CONSTANT) {
+    v.load_constant(p);
   } else {
     v.load(p);
   }
@@ -255,15 +259,15 @@ __device__ __forceinline__ void load_param_as(const T* p, int n, float (&out)[VE
 }
 
 // VEC parameters of a run-time type as fp32 (the type is uniform over a launch).
-// SOME: the first n alone, the others 0, at any element's alignment.
-template <int VEC, bool SOME = false>
+// SOME: the first n alone, the others 0, at any element's alignment.  CONSTANT: by load_constant().
+template <int VEC, bool SOME = false, bool CONSTANT = false>
 __device__ __forceinline__ void load_param(const void* p, int type, int64_t i, float (&out)[VEC], int n = VEC) {
   if (type == CCE_F32) {
-    load_param_as<float, VEC, SOME>(static_cast<const float*>(p) + i, n, out);
+    load_param_as<float, VEC, SOME, CONSTANT>(static_cast<const float*>(p) + i, n, out);
   } else if (type == CCE_BF16) {
-    load_param_as<__nv_bfloat16, VEC, SOME>(static_cast<const __nv_bfloat16*>(p) + i, n, out);
+    load_param_as<__nv_bfloat16, VEC, SOME, CONSTANT>(static_cast<const __nv_bfloat16*>(p) + i, n, out);
   } else {
-    load_param_as<__half, VEC, SOME>(static_cast<const __half*>(p) + i, n, out);
+    load_param_as<__half, VEC, SOME, CONSTANT>(static_cast<const __half*>(p) + i, n, out);
   }
 }
 

@@ -333,7 +333,7 @@ __device__ __forceinline__ void scale_rounds(const TI* p, TO* q, int vecs, int& 
   for (; v + THREADS * (U - 1) < vecs; v += THREADS * U) {
     Vec<TI, VEC> x[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) x[u].load_written(p + static_cast<int64_t>(v + u * THREADS) * VEC);
+    for (int u = 0; u < U; ++u) x[u].load(p + static_cast<int64_t>(v + u * THREADS) * VEC);
 #pragma unroll
     for (int u = 0; u < U; ++u) scale_vec<TI, TO, VEC>(x[u], q + static_cast<int64_t>(v + u * THREADS) * VEC, f);
   }
@@ -350,7 +350,7 @@ __device__ __forceinline__ void scale_chunk(const TI* p, TO* q, int n, float f) 
     const int i = vecs * VEC + threadIdx.x;
     if (i < n) {
       Vec<TI, 1> x;
-      x.load_written(p + i);
+      x.load(p + i);
       scale_vec<TI, TO, 1>(x, q + i, f);
     }
   }

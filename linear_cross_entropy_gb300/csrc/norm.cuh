@@ -103,12 +103,12 @@ __device__ __forceinline__ float2 group_sum2(float2 v, float* sm, int second) {
   return t;
 }
 
-// The gain and the bias of VEC columns; SOME: of the first n, the others 0.
-template <bool LAYER, int VEC, bool SOME = false>
+// The gain and the bias of VEC columns; SOME: of the first n, the others 0.  CONSTANT: by load_constant().
+template <bool LAYER, int VEC, bool SOME = false, bool CONSTANT = false>
 __device__ __forceinline__ void load_gain(const void* w, int p_type, float offset, int64_t c, float (&g)[VEC],
                                           int n = VEC) {
   if (w) {
-    load_param<VEC, SOME>(w, p_type, c, g, n);
+    load_param<VEC, SOME, CONSTANT>(w, p_type, c, g, n);
     if (!LAYER) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
@@ -121,10 +121,10 @@ __device__ __forceinline__ void load_gain(const void* w, int p_type, float offse
   }
 }
 
-template <bool LAYER, int VEC, bool SOME = false>
+template <bool LAYER, int VEC, bool SOME = false, bool CONSTANT = false>
 __device__ __forceinline__ void load_bias(const void* b, int p_type, int64_t c, float (&f)[VEC], int n = VEC) {
   if (LAYER && b) {
-    load_param<VEC, SOME>(b, p_type, c, f, n);
+    load_param<VEC, SOME, CONSTANT>(b, p_type, c, f, n);
   } else {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) f[e] = 0.0f;
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(MAX_THREADS) fwd_long_kernel(NormFwd a) {
 #pragma unroll 4
     for (int64_t c = first; c < a.D; c += step) {
       Vec<TX, VEC> v;
-      v.load(x + c);
+      v.load_constant(x + c);
       float t = 0.0f;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) t += v.get(e);
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(MAX_THREADS) fwd_long_kernel(NormFwd a) {
 #pragma unroll 4
   for (int64_t c = first; c < a.D; c += step) {
     Vec<TX, VEC> v;
-    v.load(x + c);
+    v.load_constant(x + c);
     float t = 0.0f;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
@@ -522,10 +522,10 @@ __global__ void __launch_bounds__(MAX_THREADS) fwd_long_kernel(NormFwd a) {
 #pragma unroll 2
   for (int64_t c = first; c < a.D; c += step) {
     Vec<TX, VEC> v;
-    v.load(x + c);
+    v.load_constant(x + c);
     float w[VEC], b[VEC], o[VEC];
-    load_gain<LAYER, VEC>(a.w, a.p_type, a.offset, c, w);
-    load_bias<LAYER, VEC>(a.b, a.p_type, c, b);
+    load_gain<LAYER, VEC, false, true>(a.w, a.p_type, a.offset, c, w);
+    load_bias<LAYER, VEC, false, true>(a.b, a.p_type, c, b);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) o[e] = (v.get(e) - mean) * rstd * w[e] + b[e];
     Vec<TY, VEC> out;
@@ -878,9 +878,9 @@ __global__ void __launch_bounds__(MAX_THREADS) bwd_long_kernel(NormBwd a) {
     Vec<TX, VEC> xv;
     Vec<TY, VEC> gv;
     float w[VEC];
-    xv.load(x + c);
-    gv.load(dy + c);
-    load_gain<LAYER, VEC>(a.w, a.p_type, a.offset, c, w);
+    xv.load_constant(x + c);
+    gv.load_constant(dy + c);
+    load_gain<LAYER, VEC, false, true>(a.w, a.p_type, a.offset, c, w);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       const float z = (xv.get(e) - mean) * rstd, g = gv.get(e) * w[e];
@@ -896,9 +896,9 @@ __global__ void __launch_bounds__(MAX_THREADS) bwd_long_kernel(NormBwd a) {
     Vec<TX, VEC> xv;
     Vec<TY, VEC> gv;
     float w[VEC], o[VEC];
-    xv.load(x + c);
-    gv.load(dy + c);
-    load_gain<LAYER, VEC>(a.w, a.p_type, a.offset, c, w);
+    xv.load_constant(x + c);
+    gv.load_constant(dy + c);
+    load_gain<LAYER, VEC, false, true>(a.w, a.p_type, a.offset, c, w);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       const float z = (xv.get(e) - mean) * rstd;
@@ -926,8 +926,8 @@ __global__ void __launch_bounds__(128) cols_kernel(NormBwd a) {
   for (int64_t n = blockIdx.y; n < a.N; n += gridDim.y) {
     Vec<TX, VEC> xv;
     Vec<TY, VEC> gv;
-    xv.load(static_cast<const TX*>(a.x) + a.xm.at(static_cast<int>(n)) + c);
-    gv.load(static_cast<const TY*>(a.dy) + a.gm.at(static_cast<int>(n)) + c);
+    xv.load_constant(static_cast<const TX*>(a.x) + a.xm.at(static_cast<int>(n)) + c);
+    gv.load_constant(static_cast<const TY*>(a.dy) + a.gm.at(static_cast<int>(n)) + c);
     const float rstd = a.rstd[n], mean = LAYER ? a.mean[n] : 0.0f;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
