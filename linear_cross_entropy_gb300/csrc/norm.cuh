@@ -718,14 +718,15 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_kernel(NormBwd a) {
       rstd[i] = rstd[i + 1];
     }
     load_stats(n + AHEAD * step, AHEAD - 1);
-    // z = x rstd - mean rstd
-    const Pair r = Pair::both(row_rstd), m = Pair::both(-row_mean * row_rstd);
+    // z = (x - mean) rstd: the difference loses next to nothing where x is near the mean.  As x rstd - mean rstd, one
+    // instruction less, every z of a row would carry the rounding of mean rstd.
+    const Pair r = Pair::both(row_rstd), m = Pair::both(-row_mean);
     float2 s;
     {
       Pair s1 = Pair::both(0.0f), s2 = Pair::both(0.0f);
       auto gather = [&](int i, Pair w) {
         const Pair xp = pair_of<TX, VEC, K>(x, i), dp = pair_of<TY, VEC, K>(g, i);
-        const Pair z = LAYER ? fma(xp, r, m) : mul(xp, r);
+        const Pair z = mul(LAYER ? add(xp, m) : xp, r);
         const Pair t = mul(dp, w);
         aw[i] = fma(dp, z, aw[i]);
         if (LAYER) {
@@ -761,7 +762,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_kernel(NormBwd a) {
     // rstd (g - sum(g) / D - z sum(g z) / D)
     auto grad = [&](int i, Pair w) {
       const Pair xp = pair_of<TX, VEC, K>(x, i), dp = pair_of<TY, VEC, K>(g, i);
-      const Pair z = LAYER ? fma(xp, r, m) : mul(xp, r);
+      const Pair z = mul(LAYER ? add(xp, m) : xp, r);
       return fma(mul(dp, w), r, LAYER ? fma(z, c2, c1) : mul(z, c2)).get();
     };
 #pragma unroll
