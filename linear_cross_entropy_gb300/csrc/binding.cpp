@@ -7,10 +7,13 @@
 // host does around them is most of their time.  Here instead of in Python, with
 // the autograd nodes in C++ as well, the backward pass runs on the autograd
 // engine's thread without the interpreter.
+#include <ATen/TracerMode.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/custom_function.h>
+#include <torch/csrc/autograd/forward_grad.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/csrc/utils/pybind.h>
 
@@ -46,6 +49,30 @@ template <typename... Parts>
   std::ostringstream s;
   (s << ... << parts);
   throw std::invalid_argument(s.str());
+}
+
+// What the calls cannot do by their nature; Python sees NotImplementedError.
+struct Unsupported : std::runtime_error {
+  using std::runtime_error::runtime_error;
+};
+
+// The kernels are launched beside torch's dispatcher, so what torch records or carries along there would miss them
+// without a word: a traced graph would hold an empty tensor, a tangent would be read as 0.
+void refuse_tracing() {
+  if (at::tracer::impl::is_dispatch_enabled() ||
+      c10::impl::TorchDispatchModeTLS::get_mode(c10::impl::TorchDispatchModeKey::PROXY).has_value())
+    throw Unsupported("a call of this operator cannot be traced: its kernels would not be in the graph");
+}
+
+// Whether a tensor can have a tangent now.
+bool tangents_live() { return torch::autograd::ForwardADLevel::try_get_by_idx(0) != nullptr; }
+
+template <typename... Tensors>
+void refuse_tangents(bool live, const Tensors&... tensors) {
+  if (!live) return;
+  const auto has = [](const Tensor& t) { return t.defined() && t._fw_grad(0).defined(); };
+  if ((has(tensors) || ...))
+    throw Unsupported("this operator has no forward-mode derivative: an argument has a tangent");
 }
 
 const char* type_name(at::ScalarType t) {
@@ -121,6 +148,8 @@ struct Sizes {
 };
 
 Sizes check_norm(const Tensor& x, const Tensor& weight, const Tensor& bias) {
+  refuse_tracing();
+  refuse_tangents(tangents_live(), x, weight, bias);
   if (!x.is_cuda()) refuse("x must be a CUDA tensor (no CPU path)");
   checked_type(x, "x");
   if (x.dim() == 0 || x.size(-1) < 1) refuse("x needs a last dimension of at least one element, got shape ", x.sizes());
@@ -187,6 +216,7 @@ std::tuple<Tensor, Tensor> rms_forward(const Tensor& x, const Tensor& weight, do
 }
 
 void check_backward(const Tensor& g, const Tensor& x, int64_t N, const Tensor& stat, const char* name) {
+  refuse_tangents(tangents_live(), g, stat);
   if (g.device() != x.device()) refuse("grad_y must be on ", x.device(), ", got ", g.device());
   if (g.sizes() != x.sizes()) refuse("grad_y must have the shape of x, ", x.sizes(), ", got ", g.sizes());
   if (g.scalar_type() != x.scalar_type() && (x.scalar_type() != at::kFloat || type_code(g.scalar_type()) < 0))
@@ -397,11 +427,14 @@ struct Tables {
 // The norm of the tensors; with outs, clipped by it into them.
 Tensor clip(const std::vector<Tensor>& grads, const std::vector<Tensor>* outs, int norm_type, double max_norm,
             double eps) {
+  refuse_tracing();
+  const bool live = tangents_live();
   Tables t;
   t.dense.reserve(4 * grads.size());
   for (size_t i = 0; i < grads.size(); ++i) {
     const Tensor& g = grads[i];
     const Tensor& o = outs ? (*outs)[i] : g;
+    refuse_tangents(live, g, o);
     check_dense(g, grads[0], "gradients");
     if (!o.is_same(g)) {
       check_dense(o, grads[0], "out");
@@ -440,6 +473,8 @@ PYBIND11_MODULE(_native, m) {
   py::register_local_exception_translator([](std::exception_ptr p) {
     try {
       if (p) std::rethrow_exception(p);
+    } catch (const Unsupported& e) {
+      PyErr_SetString(PyExc_NotImplementedError, e.what());
     } catch (const StatusError& e) {
       const py::object type = py::module_::import("linear_cross_entropy_gb300._lib").attr("CCEError");
       PyErr_SetObject(type.ptr(), type(e.status, e.what()).ptr());

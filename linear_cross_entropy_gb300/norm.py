@@ -12,7 +12,8 @@ place); the result is contiguous.  Calls run on the current stream of x's
 device and can be captured into a CUDA graph (a backward pass while no graph of
 autograd that was made outside of the capture holds the same leaves: torch ties
 their accumulation to the stream of the first).  Arguments that do not fit
-raise ValueError, a status of the library CCEError.
+raise ValueError, a status of the library CCEError.  Forward-mode derivatives and
+tracing (torch.jit.trace, make_fx) raise NotImplementedError.
 """
 from __future__ import annotations
 
