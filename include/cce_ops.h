@@ -136,9 +136,9 @@ cce_status cce_grad_norm(const int64_t* dense /* host */, int64_t n_dense, const
 /*
  * The norm as above, then output = input * min(1, max_norm / (norm + eps)),
  * rounded once to the output's type.  A factor of 1 leaves tensors that are
- * clipped in place untouched.  An infinite norm gives factor 0, a NaN gives
- * NaN.  max_norm >= 0 (infinity: never clip) and a finite eps >= 0, else
- * CCE_ERR_ARG.
+ * clipped in place untouched.  A NaN norm gives a factor of NaN.  An infinite
+ * norm gives 0, or 1 if max_norm is infinite too; norm + eps = 0 gives 1.
+ * max_norm >= 0 (infinity: never clip) and a finite eps >= 0, else CCE_ERR_ARG.
  */
 cce_status cce_clip_grads(const int64_t* dense /* host */, int64_t n_dense, const cce_strided* strided /* host */,
                           int64_t n_strided, int norm_type, float max_norm, float eps, float* norm, void* workspace,

@@ -312,9 +312,11 @@ __device__ float total_norm(const Clip& k) {
 
 __global__ void __launch_bounds__(THREADS) finish_kernel(Clip k) { total_norm(k); }
 
+// NaN for a NaN norm.  Where the quotient of two other values would be one, an infinite norm below an infinite limit or
+// 0 by 0, nothing is clipped.
 __device__ __forceinline__ float clip_factor(const Clip& k, float norm) {
   const float f = k.max_norm / (norm + k.eps);
-  return f < 1.0f || f != f ? f : 1.0f;
+  return f < 1.0f || norm != norm ? f : 1.0f;
 }
 
 template <typename TI, typename TO, int VEC>

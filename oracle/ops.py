@@ -40,5 +40,8 @@ def global_norm(tensors, norm_type=2.0):
 
 
 def clip_factor(norm, max_norm, eps=1e-6):
-    """min(1, max_norm / (norm + eps)); NaN stays NaN."""
-    return np.minimum(1.0, max_norm / (norm + eps))
+    """min(1, max_norm / (norm + eps)); NaN for a NaN norm, 1 where the quotient is infinity by infinity or 0 by 0."""
+    if np.isnan(norm):
+        return float("nan")
+    with np.errstate(invalid="ignore", divide="ignore"):
+        return float(np.fmin(1.0, np.float64(max_norm) / np.float64(norm + eps)))
