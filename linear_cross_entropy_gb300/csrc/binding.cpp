@@ -95,6 +95,9 @@ int checked_type(const Tensor& t, const char* name) {
   return code;
 }
 
+// The values themselves in memory: of torch's lazily negated views a copy.
+Tensor plain(const Tensor& t) { return t.defined() && t.is_neg() ? t.resolve_neg() : t; }
+
 void* pointer(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 
 void* stream_of(const Tensor& t) { return c10::cuda::getCurrentCUDAStream(t.get_device()).stream(); }
@@ -108,7 +111,8 @@ struct Rows {
   int64_t inner = int64_t(1) << 31, row = 0, outer = 0;
 };
 
-Rows rows_of(const Tensor& t) {
+Rows rows_of(const Tensor& given) {
+  const Tensor t = plain(given);
   Rows r;
   r.t = t;
   const int64_t last = t.dim() - 1;
@@ -188,10 +192,11 @@ std::tuple<Tensor, Tensor, Tensor> layer_forward(const Tensor& x, const Tensor& 
   const at::ScalarType y_type = result_type(x, out);
   const c10::cuda::CUDAGuard guard(x.device());
   const Rows r = rows_of(x);
+  const Tensor w = plain(weight), b = plain(bias);
   Tensor y = at::empty(x.sizes(), x.options().dtype(y_type));
   Tensor mean = statistics(x, s.N, stats), rstd = statistics(x, s.N, stats);
   check_status(cce_layer_norm_forward(pointer(r.t), r.inner, r.row, r.outer, type_code(x.scalar_type()),
-                                      pointer(weight), pointer(bias), type_code(s.p_type), s.N, s.D,
+                                      pointer(w), pointer(b), type_code(s.p_type), s.N, s.D,
                                       static_cast<float>(eps), pointer(y), type_code(y_type),
                                       static_cast<float*>(pointer(mean)), static_cast<float*>(pointer(rstd)),
                                       stream_of(x)),
@@ -205,9 +210,10 @@ std::tuple<Tensor, Tensor> rms_forward(const Tensor& x, const Tensor& weight, do
   const at::ScalarType y_type = result_type(x, out);
   const c10::cuda::CUDAGuard guard(x.device());
   const Rows r = rows_of(x);
+  const Tensor w = plain(weight);
   Tensor y = at::empty(x.sizes(), x.options().dtype(y_type));
   Tensor rstd = statistics(x, s.N, stats);
-  check_status(cce_rms_norm_forward(pointer(r.t), r.inner, r.row, r.outer, type_code(x.scalar_type()), pointer(weight),
+  check_status(cce_rms_norm_forward(pointer(r.t), r.inner, r.row, r.outer, type_code(x.scalar_type()), pointer(w),
                                     type_code(s.p_type), static_cast<float>(offset), s.N, s.D,
                                     static_cast<float>(eps), pointer(y), type_code(y_type),
                                     static_cast<float*>(pointer(rstd)), stream_of(x)),
@@ -222,7 +228,8 @@ void check_backward(const Tensor& g, const Tensor& x, int64_t N, const Tensor& s
   if (g.scalar_type() != x.scalar_type() && (x.scalar_type() != at::kFloat || type_code(g.scalar_type()) < 0))
     refuse("grad_y must be ", type_name(x.scalar_type()), ", or a 16-bit type for float32 x, got ",
            type_name(g.scalar_type()));
-  if (stat.device() != x.device() || stat.scalar_type() != at::kFloat || stat.numel() != N || !stat.is_contiguous())
+  if (stat.device() != x.device() || stat.scalar_type() != at::kFloat || stat.numel() != N || !stat.is_contiguous() ||
+      stat.is_neg())
     refuse(name, " must be contiguous float32 with ", N, " values on ", x.device());
 }
 
@@ -239,6 +246,7 @@ std::tuple<Tensor, Tensor, Tensor> layer_backward(const Tensor& g, const Tensor&
   check_backward(g, x, s.N, rstd, "rstd");
   const c10::cuda::CUDAGuard guard(x.device());
   const Rows xr = rows_of(x), gr = rows_of(g);
+  const Tensor w = plain(weight);
   const auto params = x.options().dtype(s.p_type);
   Tensor dx = need_dx ? at::empty(x.sizes(), x.options()) : Tensor();
   Tensor dw = need_dw ? at::empty({s.D}, params) : Tensor(), db = need_db ? at::empty({s.D}, params) : Tensor();
@@ -246,7 +254,7 @@ std::tuple<Tensor, Tensor, Tensor> layer_backward(const Tensor& g, const Tensor&
   Tensor ws = need ? at::empty({static_cast<int64_t>(need)}, x.options().dtype(at::kByte)) : Tensor();
   check_status(
       cce_layer_norm_backward(pointer(gr.t), gr.inner, gr.row, gr.outer, type_code(g.scalar_type()), pointer(xr.t),
-                              xr.inner, xr.row, xr.outer, type_code(x.scalar_type()), pointer(weight),
+                              xr.inner, xr.row, xr.outer, type_code(x.scalar_type()), pointer(w),
                               type_code(s.p_type), static_cast<const float*>(pointer(mean)),
                               static_cast<const float*>(pointer(rstd)), s.N, s.D, pointer(dx), pointer(dw),
                               pointer(db), pointer(ws), need, stream_of(x)),
@@ -260,6 +268,7 @@ std::tuple<Tensor, Tensor> rms_backward(const Tensor& g, const Tensor& x, const 
   check_backward(g, x, s.N, rstd, "rstd");
   const c10::cuda::CUDAGuard guard(x.device());
   const Rows xr = rows_of(x), gr = rows_of(g);
+  const Tensor w = plain(weight);
   need_dw = need_dw && weight.defined();
   Tensor dx = need_dx ? at::empty(x.sizes(), x.options()) : Tensor();
   Tensor dw = need_dw ? at::empty({s.D}, x.options().dtype(s.p_type)) : Tensor();
@@ -267,7 +276,7 @@ std::tuple<Tensor, Tensor> rms_backward(const Tensor& g, const Tensor& x, const 
   Tensor ws = need ? at::empty({static_cast<int64_t>(need)}, x.options().dtype(at::kByte)) : Tensor();
   check_status(
       cce_rms_norm_backward(pointer(gr.t), gr.inner, gr.row, gr.outer, type_code(g.scalar_type()), pointer(xr.t),
-                            xr.inner, xr.row, xr.outer, type_code(x.scalar_type()), pointer(weight),
+                            xr.inner, xr.row, xr.outer, type_code(x.scalar_type()), pointer(w),
                             type_code(s.p_type), static_cast<float>(offset),
                             static_cast<const float*>(pointer(rstd)), s.N, s.D, pointer(dx), pointer(dw), pointer(ws),
                             need, stream_of(x)),
@@ -440,6 +449,7 @@ Tensor clip(const std::vector<Tensor>& grads, const std::vector<Tensor>* outs, i
       check_dense(o, grads[0], "out");
       if (o.sizes() != g.sizes())
         refuse("out must have the shapes of the gradients: ", o.sizes(), " for ", g.sizes());
+      if (o.is_neg() != g.is_neg()) refuse("a gradient or its out is a negated view (resolve_neg), the other is not");
     }
     if (g.is_contiguous() && o.is_contiguous()) {
       t.add_dense(g, o);
