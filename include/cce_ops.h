@@ -108,8 +108,8 @@ size_t cce_norm_backward_workspace_bytes(int64_t N, int64_t D);
  *            and output are contiguous blocks of memory in the same order.
  *   strided  n_strided descriptors of tensors whose elements are not one block.
  * Outputs are read by cce_clip_grads only.  An output is the input itself (in
- * place, same type) or memory that overlaps no other input or output: dense
- * blocks that do overlap return CCE_ERR_ARG.
+ * place, same type and strides) or memory that overlaps no other input or
+ * output: dense blocks that do overlap return CCE_ERR_ARG.
  */
 typedef struct {
   const void* in;

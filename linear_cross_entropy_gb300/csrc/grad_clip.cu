@@ -504,7 +504,12 @@ cce_status check_tables(const int64_t* dense, int64_t n_dense, const cce_strided
     if (!t.in || (outputs && !t.out)) return CCE_ERR_NULL;
     if (!multiple(t.in, type_bytes(t.in_type)) || (outputs && !multiple(t.out, type_bytes(t.out_type))))
       return CCE_ERR_ALIGN;
-    if (outputs && t.in == t.out && t.in_type != t.out_type) return CCE_ERR_ARG;
+    if (outputs && t.in == t.out) {
+      if (t.in_type != t.out_type) return CCE_ERR_ARG;
+      for (int d = 0; d < 4; ++d) {  // otherwise ordered: threads would write what others have yet to read
+        if (t.size[d] > 1 && t.in_stride[d] != t.out_stride[d]) return CCE_ERR_ARG;
+      }
+    }
   }
   return CCE_OK;
 }
