@@ -58,9 +58,9 @@ extern "C" {
 typedef enum {
   CCE_OK = 0,
   CCE_ERR_NULL = 1,         /* a required pointer is NULL */
-  CCE_ERR_SHAPE = 2,        /* N, D or V out of range, or D % 8 != 0 */
-  CCE_ERR_ALIGN = 3,        /* a buffer is not 16-byte aligned */
-  CCE_ERR_ARG = 4,          /* bad reduction or filter_eps */
+  CCE_ERR_SHAPE = 2,        /* a size or stride out of range, or the classifier's D % 8 != 0 */
+  CCE_ERR_ALIGN = 3,        /* a buffer is not aligned as its header says */
+  CCE_ERR_ARG = 4,          /* bad reduction, flag, type or number; tensors that overlap */
   CCE_ERR_WORKSPACE = 5,    /* ws_bytes smaller than the query */
   CCE_ERR_DEVICE = 6,       /* current device is not compute capability 10.3 */
   CCE_ERR_CUDA = 7,         /* a CUDA runtime/driver call failed */

@@ -37,12 +37,16 @@ using OptType = std::optional<at::ScalarType>;
 // A status of the library; Python sees it as CCEError.
 struct StatusError : std::runtime_error {
   int status;
-  StatusError(int s, const char* call) : std::runtime_error(call), status(s) {}
+  StatusError(int s, const std::string& what) : std::runtime_error(what), status(s) {}
 };
 
-void check_status(cce_status st, const char* call) {
-  if (st != CCE_OK) throw StatusError(st, call);
+// `args`: what CCE_ERR_ARG is left to mean once the tensors have been checked here.
+void check_status(cce_status st, const char* call, const char* args) {
+  if (st != CCE_OK) throw StatusError(st, st == CCE_ERR_ARG ? std::string(call) + " (" + args + ")" : call);
 }
+const char* const NORM_ARGS = "eps must be finite and at least 0, weight_offset finite";
+const char* const CLIP_ARGS =
+    "eps must be finite and at least 0, and no tensor that is written may overlap another or be given twice";
 
 template <typename... Parts>
 [[noreturn]] void refuse(const Parts&... parts) {  // ValueError
@@ -200,7 +204,7 @@ std::tuple<Tensor, Tensor, Tensor> layer_forward(const Tensor& x, const Tensor& 
                                       static_cast<float>(eps), pointer(y), type_code(y_type),
                                       static_cast<float*>(pointer(mean)), static_cast<float*>(pointer(rstd)),
                                       stream_of(x)),
-               "cce_layer_norm_forward");
+               "cce_layer_norm_forward", NORM_ARGS);
   return {y, mean, rstd};
 }
 
@@ -217,7 +221,7 @@ std::tuple<Tensor, Tensor> rms_forward(const Tensor& x, const Tensor& weight, do
                                     type_code(s.p_type), static_cast<float>(offset), s.N, s.D,
                                     static_cast<float>(eps), pointer(y), type_code(y_type),
                                     static_cast<float*>(pointer(rstd)), stream_of(x)),
-               "cce_rms_norm_forward");
+               "cce_rms_norm_forward", NORM_ARGS);
   return {y, rstd};
 }
 
@@ -258,7 +262,7 @@ std::tuple<Tensor, Tensor, Tensor> layer_backward(const Tensor& g, const Tensor&
                               type_code(s.p_type), static_cast<const float*>(pointer(mean)),
                               static_cast<const float*>(pointer(rstd)), s.N, s.D, pointer(dx), pointer(dw),
                               pointer(db), pointer(ws), need, stream_of(x)),
-      "cce_layer_norm_backward");
+      "cce_layer_norm_backward", NORM_ARGS);
   return {dx, dw, db};
 }
 
@@ -280,7 +284,7 @@ std::tuple<Tensor, Tensor> rms_backward(const Tensor& g, const Tensor& x, const 
                             type_code(s.p_type), static_cast<float>(offset),
                             static_cast<const float*>(pointer(rstd)), s.N, s.D, pointer(dx), pointer(dw), pointer(ws),
                             need, stream_of(x)),
-      "cce_rms_norm_backward");
+      "cce_rms_norm_backward", NORM_ARGS);
   return {dx, dw};
 }
 
@@ -465,12 +469,12 @@ Tensor clip(const std::vector<Tensor>& grads, const std::vector<Tensor>* outs, i
   if (!outs) {
     check_status(cce_grad_norm(t.dense.data(), rows, t.strided.data(), strided, norm_type, norm.data_ptr<float>(),
                                ws.data_ptr(), need, stream_of(norm)),
-                 "cce_grad_norm");
+                 "cce_grad_norm", CLIP_ARGS);
     return norm;
   }
   check_status(cce_clip_grads(t.dense.data(), rows, t.strided.data(), strided, norm_type, static_cast<float>(max_norm),
                               static_cast<float>(eps), norm.data_ptr<float>(), ws.data_ptr(), need, stream_of(norm)),
-               "cce_clip_grads");
+               "cce_clip_grads", CLIP_ARGS);
   for (const Tensor& o : *outs) {  // autograd learns that these were written
     if (!o.is_inference()) o.unsafeGetTensorImpl()->bump_version();
   }

@@ -721,9 +721,12 @@ const char* cce_status_string(cce_status s) {
   switch (s) {
     case CCE_OK: return "ok";
     case CCE_ERR_NULL: return "null pointer";
-    case CCE_ERR_SHAPE: return "bad shape (need 1 <= N, V < 2^31; 8 <= D < 2^31, D % 8 == 0)";
-    case CCE_ERR_ALIGN: return "buffer not 16-byte aligned";
-    case CCE_ERR_ARG: return "bad argument (reduction or filter_eps)";
+    case CCE_ERR_SHAPE:
+      return "a size or stride is out of its range (the classifier: 1 <= N, V < 2^31; 8 <= D < 2^31, D % 8 == 0)";
+    case CCE_ERR_ALIGN:
+      return "a buffer is not aligned (16 bytes; rows, parameters and gradients of cce_ops.h: their element)";
+    case CCE_ERR_ARG:
+      return "bad argument (a reduction, flag or element type, a number out of its range, or tensors that overlap)";
     case CCE_ERR_WORKSPACE: return "workspace too small";
     case CCE_ERR_DEVICE: return "current device is not compute capability 10.3 (sm_103a)";
     case CCE_ERR_CUDA: return "CUDA error";
