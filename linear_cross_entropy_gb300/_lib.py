@@ -10,6 +10,8 @@ import os
 
 import torch  # noqa: F401  (loads the CUDA runtime libcce.so links against)
 
+from . import build
+
 NATIVE_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_native.so")
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libcce.so")
 
@@ -64,9 +66,10 @@ def load() -> ctypes.CDLL:
     for path in (LIB_PATH, NATIVE_PATH):
         if os.path.exists(path):
             continue
-        raise ImportError(
-            f"{path} is not built; run `python -m linear_cross_entropy_gb300.build` "
-            "(there is no non-CUDA fallback)")
+        raise ImportError(f"{path} is not built; run `{build.COMMAND}` (there is no non-CUDA fallback)")
+    if build.built_for() not in ("", build.versions()):
+        raise ImportError(f"{NATIVE_PATH} was built for {build.built_for()}, and this is {build.versions()}; run "
+                          f"`{build.COMMAND}`")
     lib = ctypes.CDLL(LIB_PATH)
     vp, i64, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t
     lib.cce_forward_workspace_bytes.argtypes = [i64, i64, i64]

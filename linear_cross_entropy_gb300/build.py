@@ -8,7 +8,8 @@ Each translation unit is compiled in parallel, then linked into
 linear_cross_entropy_gb300/libcce.so against the shared CUDA runtime (the
 one PyTorch loads), so both use the same runtime state.  csrc/binding.cpp
 becomes the Python module _native.so beside it (g++, against this Python's and
-PyTorch's headers), which calls libcce.so.
+PyTorch's headers), which calls libcce.so.  It works with that Python and that
+PyTorch only, so their versions are kept beside the objects.
 """
 from __future__ import annotations
 
@@ -26,6 +27,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libcce.so")
 NATIVE = os.path.join(PKG, "_native.so")
+BUILT_FOR = os.path.join(BUILD, "native_for.txt")
+COMMAND = "python linear_cross_entropy_gb300/build.py"
 SOURCES = ("cce_api.cu", "gemm_kernels.cu", "cce_noalloc.cu", "cce_sort.cu", "cce_flce.cu", "grad_clip.cu",
            "norm_api.cu") + tuple(f"norm_{p}_{t}.cu" for p in ("fwd", "bwd")
                                   for t in ("bf16", "f16", "f32", "f32_bf16", "f32_f16"))
@@ -53,8 +56,23 @@ def _deps_mtime() -> float:
     return max(os.path.getmtime(p) for p in paths if os.path.isfile(p))
 
 
+def versions() -> str:
+    """What _native.so is bound to."""
+    import torch
+    return f"{sys.implementation.cache_tag}, torch {torch.__version__}"
+
+
+def built_for() -> str:
+    """versions() when _native.so was linked, "" if that is not known."""
+    try:
+        with open(BUILT_FOR) as f:
+            return f.read()
+    except FileNotFoundError:
+        return ""
+
+
 def up_to_date() -> bool:
-    return all(os.path.exists(p) and os.path.getmtime(p) >= _deps_mtime() for p in (LIB, NATIVE))
+    return built_for() == versions() and all(os.path.exists(p) and os.path.getmtime(p) >= _deps_mtime() for p in (LIB, NATIVE))
 
 
 def _torch_flags():
@@ -103,6 +121,8 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         *objs, binding = ex.map(compile_one, SOURCES + (BINDING,))
     link([cc] + ARCH + ["-shared", "--cudart", "shared"] + objs, LIB)
     link([cxx, "-shared", binding, "-L" + PKG, "-l:libcce.so", "-Wl,-rpath,$ORIGIN"] + torch_link, NATIVE)
+    with open(BUILT_FOR, "w") as f:
+        f.write(versions())
     return LIB
 
 
