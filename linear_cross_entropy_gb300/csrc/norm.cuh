@@ -1136,7 +1136,7 @@ bool bwd_in_registers(const NormBwd& a, int* parts, cudaStream_t s, cudaError_t*
   const int64_t vecs = row_vecs<VEC, A>(a.D);
   if constexpr (VEC > 1) {
     constexpr int K = 16 / VEC;
-    int tpr = group_threads(vecs, K);
+    const int tpr = group_threads(vecs, K);
     if constexpr (LAYER && VEC == 8) {
       if (2 * tpr > MAX_THREADS && 2 * tpr <= WIDER) {
         *e = run_bwd<TX, TY, VEC, K, K - 1, LAYER, A, WIDER>(a, tpr, parts, s);
@@ -1157,11 +1157,14 @@ bool bwd_in_registers(const NormBwd& a, int* parts, cudaStream_t s, cudaError_t*
       return true;
     }
     if (vecs > 2 * K * MAX_THREADS) return false;
-    // as few values a thread as 512 threads allow
-    const bool most_values = vecs > 3 * K / 2 * MAX_THREADS;
-    tpr = group_threads(vecs, most_values ? 2 * K : 3 * K / 2);
-    *e = most_values ? run_bwd<TX, TY, VEC, 2 * K, 3 * K / 2 - 1, LAYER, A>(a, tpr, parts, s)
-                     : run_bwd<TX, TY, VEC, 3 * K / 2, K - 1, LAYER, A>(a, tpr, parts, s);
+    // as few values a thread as 512 threads allow; blocks of more have taken all rows of up to 3 K / 2 vectors
+    if constexpr (K * bwd_threads<TX, VEC, K, LAYER>() < 3 * K / 2 * MAX_THREADS) {
+      if (vecs <= 3 * K / 2 * MAX_THREADS) {
+        *e = run_bwd<TX, TY, VEC, 3 * K / 2, K - 1, LAYER, A>(a, group_threads(vecs, 3 * K / 2), parts, s);
+        return true;
+      }
+    }
+    *e = run_bwd<TX, TY, VEC, 2 * K, 3 * K / 2 - 1, LAYER, A>(a, group_threads(vecs, 2 * K), parts, s);
   } else {
     *e = run_bwd<TX, TY, VEC, 4, 0, LAYER, A>(a, group_threads(vecs, 4), parts, s);
   }
