@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(MAX_THREADS) fwd_few_kernel(NormFwd a) {
 // ahead 254 us.  Rows spread over more threads pay more for their sums: 16,384 x
 // 4,096 takes 46 us with 64 values a thread, 48 us with 32, 64 us with 16.
 template <typename TX, typename TY, int VEC, int K, int KF, bool LAYER, Access A>
-__global__ void __launch_bounds__(MAX_THREADS) fwd_kernel(NormFwd a) {
+__global__ void __launch_bounds__(MAX_THREADS, 1) fwd_kernel(NormFwd a) {
   constexpr bool REALIGNED = A == Access::REALIGNED, SHIFTED = REALIGNED || A == Access::SHIFTED;
   constexpr int E = K * VEC / 2;
   extern __shared__ __align__(16) float gain[];  // then the bias of a layer norm
