@@ -8,7 +8,8 @@
  * owns every buffer (workspaces included; the library allocates no device
  * memory), argument checks run before anything is launched and return a
  * cce_status, calls are asynchronous on `stream`, outputs are overwritten.
- * Every result is deterministic: the order of every sum is fixed by the sizes.
+ * Every result is deterministic: the order of every sum is fixed by the sizes,
+ * types, strides and alignments of the arguments and by the device.
  *
  * Element types
  * -------------
@@ -55,7 +56,7 @@ int cce_ops_abi_version(void);
  * start on 16 bytes; next, matrices whose rows all start alike (any D, at least
  * 64, aligned pointers, pitches that differ from D by a multiple of 16 bytes of
  * x), then others of at least 64 columns.  A row whose squared deviations overflow fp32 gets rstd 0; one with
- * a NaN or an infinity becomes NaN, the other rows keep their results.
+ * a NaN or an infinity, or whose sum overflows fp32, becomes NaN; the other rows keep their results.
  */
 cce_status cce_layer_norm_forward(const void* x, int64_t x_inner, int64_t x_row_stride, int64_t x_outer_stride,
                                   int x_type, const void* weight, const void* bias, int p_type, int64_t N, int64_t D,

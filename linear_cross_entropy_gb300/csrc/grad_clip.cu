@@ -414,7 +414,8 @@ __device__ __forceinline__ void strided_offsets(const cce_strided& t, int64_t i,
   *out = b + i * t.out_stride[0];
 }
 
-// One element at a time: few tensors take this path.
+// One element at a time: few tensors take this path.  The left half of the columns of 8,192 x 4,096 bf16 values, 33 MB:
+// from L2: norm 99 us, clipped into bf16 207; as one block of memory 7 and 14.
 __global__ void __launch_bounds__(THREADS) strided_norm_kernel(const __grid_constant__ cce_strided t, int64_t n,
                                                                int norm_type, Part* part) {
   const bool inf = norm_type == CCE_NORM_INF;

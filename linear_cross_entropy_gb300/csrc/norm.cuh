@@ -329,6 +329,9 @@ __global__ void __launch_bounds__(MAX_THREADS) fwd_few_kernel(NormFwd a) {
 // instead of the last one 99 us; with one block of 128 threads a row and no row
 // ahead 254 us.  Rows spread over more threads pay more for their sums: 16,384 x
 // 4,096 takes 46 us with 64 values a thread, 48 us with 32, 64 us with 16.
+//
+// The bound of one block an SM stands for the 512 threads an SM that run_fwd launches: without it the compiler held
+// some variants to 64 registers, and they spilled (fp32 32,768 x 561 into bf16 33.6 us, with it 29.4).
 template <typename TX, typename TY, int VEC, int K, int KF, bool LAYER, Access A>
 __global__ void __launch_bounds__(MAX_THREADS, 1) fwd_kernel(NormFwd a) {
   constexpr bool REALIGNED = A == Access::REALIGNED, SHIFTED = REALIGNED || A == Access::SHIFTED;
@@ -478,7 +481,11 @@ __global__ void __launch_bounds__(MAX_THREADS, 1) fwd_kernel(NormFwd a) {
 
 // Rows too long for the registers of one block: one block per row, which
 // reads it once per sum and once more to write (from L2 after the first time).
-// bf16 512 x 20,000: 18 us for a layer norm.
+// These are rows of more than 16,384 fp32 columns, of more than 32,768 16-bit ones
+// for an RMS norm, and of more than 28,800 for a layer norm, whose gain and bias
+// fill shared memory first.
+// bf16 2,048 x 30,000, layer norm: 71 us (3.5 TB/s of the bytes read and written
+// once); 2,048 x 33,000, RMS norm: 52 us; 2,048 x 33,001, by elements, 187 us.
 template <typename TX, typename TY, int VEC, bool LAYER>
 __global__ void __launch_bounds__(MAX_THREADS) fwd_long_kernel(NormFwd a) {
   __shared__ __align__(16) float sm[2][slots(MAX_THREADS)];
@@ -548,7 +555,10 @@ __global__ void __launch_bounds__(MAX_THREADS) fwd_long_kernel(NormFwd a) {
 //
 // Bound by memory, a layer norm by the registers that keep fewer rows in flight:
 // bf16 65,536 x 2,048, 805 MB, RMS norm 119 us (6.8 TB/s), layer norm 137 us (5.9
-// TB/s); 8,192 x 2,304 24 and 27 us, 3 us of it the parameters' gradients.
+// TB/s); 8,192 x 2,304 24 and 27 us, 3 us of it the parameters' gradients.  A
+// layer norm of 12,289 to 16,384 columns, 32 values a thread with both sums,
+// spills 68 to 348 bytes a thread: 4,096 x 16,384 110 us in bf16 (59 at a copy's
+// rate) and 180 in fp32 (119), 4,096 x 12,288 59 and 105.
 // With the next row in registers instead of the ring 125 and 142 us; with three
 // or four rows in it 120 and 138.  Odd widths pay for their partial vectors: 16,384
 // x 1,001 29 and 34 us, x 1,024 22 and 25 us.
@@ -862,7 +872,9 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_kernel(NormBwd a) {
 }
 
 // Rows too long for the registers of one block: grad_x by one block per row in
-// two passes over it, the parameter gradients column-wise by cols_kernel.
+// two passes over it, the parameter gradients column-wise by cols_kernel.  bf16
+// 2,048 x 20,000: 99 us for a layer norm, 90 for an RMS norm; 2,048 x 20,001, by
+// elements, 289 us.
 template <typename TX, typename TY, int VEC, bool LAYER>
 __global__ void __launch_bounds__(MAX_THREADS) bwd_long_kernel(NormBwd a) {
   __shared__ __align__(16) float sm[2][slots(MAX_THREADS)];
@@ -1016,7 +1028,9 @@ template <typename TX, typename TY, int VEC, int K, int KF, bool LAYER, Access A
 cudaError_t run_fwd(const NormFwd& a, int tpr, cudaStream_t s) {
   auto kernel = fwd_kernel<TX, TY, VEC, K, KF, LAYER, A>;
   const int smem = static_cast<int>(sizeof(float) * param_floats<VEC, A>(a.D)) * (LAYER ? 2 : 1);
-  // Two blocks of 256 threads fill an SM's registers; where their parameters do not fit twice, one of 512.
+  // Two blocks of 256 threads an SM, where their parameters do not fit twice one of 512: with five to eight vectors of
+  // 16-bit values a thread (120 to 128 registers) these fill the registers.  Fewer vectors (40 to 64 registers for one
+  // to three of them) leave up to half of the registers idle, and groups of 96 threads some of the warps.
   const bool pair = 2 * (smem + 2048) <= MAX_SMEM;
   const int groups = std::max(1, (pair ? 256 : MAX_THREADS) / tpr);
   const int per_sm = std::max(1, MAX_THREADS / (tpr * groups));

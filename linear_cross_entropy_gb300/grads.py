@@ -7,7 +7,9 @@ waits for the GPU.
 
 cce_clip_grads writes the clipped gradients in place or into other tensors
 (say, the 32-bit buffers of an optimiser).  Calls run on the current stream of
-the gradients' device and can be captured into a CUDA graph.
+the gradients' device and can be captured into a CUDA graph.  Tensors with a
+forward-mode tangent and tracing (torch.jit.trace, make_fx) raise
+NotImplementedError.
 """
 from __future__ import annotations
 
@@ -54,8 +56,9 @@ def cce_clip_grads(grads, max_norm, norm_type=2.0, *, out=None, eps=CLIP_EPS, st
 
     In place, or with out into tensors of the same shapes, whose types may be
     others (then the gradients are left as they are).  Tensors that are written
-    must not overlap.  The norm is not checked: a NaN or infinity goes into the
-    gradients (clip_grad_norm_ can raise instead)."""
+    must not overlap.  The norm is not checked: a NaN goes into the gradients, an
+    infinity makes them 0 and itself NaN, unless max_norm is infinite too
+    (clip_grad_norm_ can raise instead)."""
     grads = list(grads)
     if out is not None:
         out = list(out)
