@@ -35,11 +35,19 @@ __all__ = [
     "layer_norm", "rms_norm", "cce_layer_norm_forward", "cce_layer_norm_backward", "cce_rms_norm_forward",
     "cce_rms_norm_backward", "norm_backward_workspace_bytes", "clip_grad_norm_", "cce_clip_grads", "cce_grad_norm",
     "grad_norm_workspace_bytes",
+    "linear", "gated_linear", "cce_linear_forward", "cce_linear_backward", "cce_gated_linear_forward",
+    "cce_gated_linear_backward", "linear_forward_workspace_bytes", "linear_backward_workspace_bytes",
+    "gated_linear_forward_workspace_bytes", "gated_linear_backward_workspace_bytes",
 ]
 
 _lib.load()
 
+from . import _native  # noqa: E402
 from .grads import cce_clip_grads, cce_grad_norm, clip_grad_norm_, grad_norm_workspace_bytes  # noqa: E402
+from .layers import (cce_gated_linear_backward, cce_gated_linear_forward, cce_linear_backward,  # noqa: E402
+                     cce_linear_forward, gated_linear, gated_linear_backward_workspace_bytes,
+                     gated_linear_forward_workspace_bytes, linear, linear_backward_workspace_bytes,
+                     linear_forward_workspace_bytes)
 from .norm import (cce_layer_norm_backward, cce_layer_norm_forward, cce_rms_norm_backward,  # noqa: E402
                    cce_rms_norm_forward, layer_norm, norm_backward_workspace_bytes, rms_norm)
 
@@ -178,9 +186,10 @@ _deferred = _DeferredErrors()
 
 def raise_pending_errors():
     """Waits for the autograd calls issued so far (linear_cross_entropy,
-    fused_linear_cross_entropy) and raises CCEError if one of them set a
-    device error word."""
+    fused_linear_cross_entropy, linear, gated_linear) and raises CCEError if
+    one of them set a device error word."""
     _deferred.poll(wait=True)
+    _raise_word(_native.layers_take_error(), "a linear layer")
 
 
 def cce_forward(E, C, x, ignore_index=-100, reduction="mean", *, softcap=0.0, skip_ignored=False, stream=None,

@@ -1,4 +1,4 @@
-"""ctypes binding of libcce.so (declarations in include/cce.h and include/cce_ops.h).
+"""ctypes binding of libcce.so (declarations in include/cce*.h).
 
 Loading fails loudly when the library has not been built: there is no
 fallback implementation.
@@ -163,6 +163,25 @@ def load() -> ctypes.CDLL:
     lib.cce_clip_grads.restype = ci
     lib.cce_grad_norm_workspace_bytes.argtypes = [i64, i64]
     lib.cce_grad_norm_workspace_bytes.restype = sz
+    # include/cce_layers.h
+    lib.cce_layers_abi_version.argtypes = []
+    lib.cce_layers_abi_version.restype = ci
+    mat = [vp, i64]  # pointer, pitch
+    lib.cce_linear_forward.argtypes = (mat + mat + [ci, vp, ci] + mat + [ci, i64, i64, i64] + mat + [ci] + mat
+                                       + [vp, sz, vp])
+    lib.cce_linear_backward.argtypes = (mat + [ci] + mat + mat + [ci] + mat + [ci, i64, i64, i64, vp, vp, vp, ci, vp,
+                                                                               sz, vp])
+    lib.cce_gated_linear_forward.argtypes = (mat + mat + mat + [ci, ci, i64, i64, i64] + mat
+                                             + [vp, vp, i64, vp, sz, vp])
+    lib.cce_gated_linear_backward.argtypes = (mat * 4 + [ci] + mat + mat + [ci, i64, i64, i64, vp, vp, vp, vp, sz, vp])
+    lib.cce_layers_take_error.argtypes = [vp, vp]
+    for name in ("cce_linear_forward", "cce_linear_backward", "cce_gated_linear_forward", "cce_gated_linear_backward",
+                 "cce_layers_take_error"):
+        getattr(lib, name).restype = ci
+    for name in ("linear_forward", "linear_backward", "gated_linear_forward", "gated_linear_backward"):
+        query = getattr(lib, f"cce_{name}_workspace_bytes")
+        query.argtypes = [i64, i64, i64]
+        query.restype = sz
     _lib = lib
     return lib
 

@@ -6,8 +6,8 @@
 
 Each translation unit is compiled in parallel, then linked into
 linear_cross_entropy_gb300/libcce.so against the shared CUDA runtime (the
-one PyTorch loads), so both use the same runtime state.  csrc/binding.cpp
-becomes the Python module _native.so beside it (g++, against this Python's and
+one PyTorch loads), so both use the same runtime state.  csrc/binding*.cpp
+become the Python module _native.so beside it (g++, against this Python's and
 PyTorch's headers), which calls libcce.so.  It works with that Python and that
 PyTorch only, so their versions are kept beside the objects.
 """
@@ -30,9 +30,9 @@ NATIVE = os.path.join(PKG, "_native.so")
 BUILT_FOR = os.path.join(BUILD, "native_for.txt")
 COMMAND = "python linear_cross_entropy_gb300/build.py"
 SOURCES = ("cce_api.cu", "gemm_kernels.cu", "cce_noalloc.cu", "cce_sort.cu", "cce_flce.cu", "grad_clip.cu",
-           "norm_api.cu") + tuple(f"norm_{p}_{t}.cu" for p in ("fwd", "bwd")
+           "norm_api.cu", "layers_api.cu", "linear_gemm.cu", "linear_few.cu", "linear_pass.cu") + tuple(f"norm_{p}_{t}.cu" for p in ("fwd", "bwd")
                                   for t in ("bf16", "f16", "f32", "f32_bf16", "f32_f16"))
-BINDING = "binding.cpp"
+BINDINGS = ("binding.cpp", "binding_layers.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -117,10 +117,11 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, out)
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        *objs, binding = ex.map(compile_one, SOURCES + (BINDING,))
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + len(BINDINGS)) as ex:
+        compiled = list(ex.map(compile_one, SOURCES + BINDINGS))
+    objs, bindings = compiled[:len(SOURCES)], compiled[len(SOURCES):]
     link([cc] + ARCH + ["-shared", "--cudart", "shared"] + objs, LIB)
-    link([cxx, "-shared", binding, "-L" + PKG, "-l:libcce.so", "-Wl,-rpath,$ORIGIN"] + torch_link, NATIVE)
+    link([cxx, "-shared", *bindings, "-L" + PKG, "-l:libcce.so", "-Wl,-rpath,$ORIGIN"] + torch_link, NATIVE)
     with open(BUILT_FOR, "w") as f:
         f.write(versions())
     return LIB

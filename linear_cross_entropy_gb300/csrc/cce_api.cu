@@ -18,6 +18,7 @@
 
 #include "../../include/cce.h"
 #include "internal.h"
+#include "linear.h"
 
 namespace cce {
 namespace {
@@ -562,12 +563,13 @@ struct DeviceInfo {
   bool ok = false;
   int sms = 0;
   int pair_clusters = 0;  // CTA pairs of the forward GEMM resident at once
+  int linear_pairs = 0;   // and of the layers' GEMM
 };
 std::mutex g_mu;
 DeviceInfo g_dev[64];
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
-cce_status device_check(int* sms, int* pair_clusters = nullptr) {
+cce_status device_check(int* sms, int* pair_clusters = nullptr, int* linear_pairs = nullptr) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
     cudaGetLastError();
@@ -586,11 +588,12 @@ cce_status device_check(int* sms, int* pair_clusters = nullptr) {
     d.ok = (major == 10 && minor == 3);
     d.sms = sms;
     if (d.ok) {
-      if (prepare_gemm_kernels() != cudaSuccess) {
+      if (prepare_gemm_kernels() != cudaSuccess || prepare_linear_gemm() != cudaSuccess) {
         cudaGetLastError();
         return CCE_ERR_CUDA;
       }
       d.pair_clusters = gemm_pair_clusters(sms);
+      d.linear_pairs = linear_pair_units(sms);
       if (!g_encode) {
         cudaDriverEntryPointQueryResult q;
         void* fn = nullptr;
@@ -608,6 +611,7 @@ cce_status device_check(int* sms, int* pair_clusters = nullptr) {
   if (!d.ok) return CCE_ERR_DEVICE;
   *sms = d.sms;
   if (pair_clusters) *pair_clusters = d.pair_clusters;
+  if (linear_pairs) *linear_pairs = d.linear_pairs;
   return CCE_OK;
 }
 
@@ -704,6 +708,14 @@ cce_status cuda_status(cudaError_t e) {
 }  // namespace
 
 int device_ready(int* sms) { return device_check(sms); }
+
+int layers_device_ready(int* sms, int* pairs) { return device_check(sms, nullptr, pairs); }
+
+bool encode_operand(CUtensorMap* m, bool bf16, const void* p, uint64_t inner, uint64_t outer, uint64_t pitch,
+                    uint32_t box_inner, uint32_t box_outer) {
+  return make_tmap(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, p, inner, outer,
+                   pitch, box_inner, box_outer);
+}
 
 void count_launches(int n) { g_launches += static_cast<uint64_t>(n); }
 

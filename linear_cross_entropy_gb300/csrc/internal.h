@@ -30,6 +30,11 @@ cudaError_t launch_selftest_pair_timeout(int32_t* dev_err, uint64_t timeout_ns, 
 // The current device is one the library runs on: its SM count, and the status
 // of the check (a cce_status).
 int device_ready(int* sms);
+// The same for the layers' products: also how many CTA pairs of their kernel fit on the device at once.
+int layers_device_ready(int* sms, int* pairs);
+// A 2-D tensor map over 16-bit values, 128-byte swizzle; after device_ready().
+bool encode_operand(CUtensorMap* m, bool bf16, const void* p, uint64_t inner, uint64_t outer, uint64_t pitch,
+                    uint32_t box_inner, uint32_t box_outer);
 // Adds to cce_kernel_launch_count().
 void count_launches(int n);
 

@@ -1,0 +1,575 @@
+// Entry points of the layers in front of the head (include/cce_layers.h):
+// argument checks, workspace layout, the choice of tiles, launches.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "../../include/cce_layers.h"
+#include "internal.h"
+#include "linear.h"
+
+namespace cce {
+namespace {
+
+constexpr int64_t LIMIT = (int64_t(1) << 31) - 512;
+constexpr int64_t MATRIX = int64_t(1) << 45;  // elements of one
+
+bool multiple(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(bytes) == 0; }
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t type_bytes(int t) { return t == CCE_F32 ? 4 : 2; }
+bool type_ok(int t) { return t == CCE_F32 || t == CCE_F16 || t == CCE_BF16; }
+bool operand_type(int t) { return t == CCE_F16 || t == CCE_BF16; }
+bool act_ok(int act) { return act >= CCE_ACT_NONE && act <= CCE_ACT_SILU; }
+bool sizes_ok(int64_t M, int64_t N, int64_t K) {
+  return M >= 0 && M < LIMIT && N >= 1 && N < LIMIT && K >= 1 && K < LIMIT && M * N < MATRIX && M * K < MATRIX &&
+         N * K < MATRIX;
+}
+size_t round256(size_t b) { return (b + 255) / 256 * 256; }
+
+// ----------------------------------------------------------------- tiles
+// What decides over the tiles of a product: sizes alone, so that a workspace can be
+// sized without a device.
+struct Shape {
+  int I, J;
+  int kb;      // 64-deep blocks of K
+  bool b_mn;   // B comes in groups of 64 j
+};
+struct Choice {
+  int jt, splits, kb_split;
+  int64_t items;
+  double item_cycles;
+};
+struct Plan {
+  bool pair;
+  Choice c[LIN_MAX_PROBLEMS];
+  double cycles;
+};
+
+constexpr int UNITS = 152;                       // SMs
+constexpr int64_t MAX_PART_BYTES = 256ll << 20;  // of a product's partial sums
+
+int64_t i_tiles(const Shape& s, bool pair) { return cdiv(s.I, pair ? 2 * LIN_BI : LIN_BI); }
+
+// Cycles of one work item: its blocks of K at the slower of the tensor core (8,192
+// flops a cycle and SM) and the loads (56 bytes a cycle and SM from L2), and what a
+// tile costs beside them.
+double item_cycles(int jt, int kb, bool pair, bool gated) {
+  const int mats = gated ? 2 : 1;
+  const double mma = 2.0 * jt * mats;
+  const double load = (mats * LIN_BI + (pair ? jt / 2 : jt)) * 128.0 / 56.0;
+  return kb * std::max(mma, load) + 500.0;
+}
+
+// The longest of the units' shares: unit u takes items u, u + units, ... of the
+// problems one after another.
+double makespan(const Choice* c, int n, int units) {
+  int64_t ends[LIN_MAX_PROBLEMS], at = 0;
+  for (int q = 0; q < n; ++q) ends[q] = at += c[q].items;
+  const auto count = [&](int64_t end, int64_t u) { return end > u ? (end - u - 1) / units + 1 : 0; };
+  double worst = 0.0;
+  const auto share = [&](int64_t u) {
+    double t = 0.0;
+    int64_t before = 0;
+    for (int q = 0; q < n; ++q) {
+      const int64_t to = count(ends[q], u);
+      t += static_cast<double>(to - before) * c[q].item_cycles;
+      before = to;
+    }
+    worst = std::max(worst, t);
+  };
+  share(0);
+  for (int q = 0; q < n; ++q) share(ends[q] % units);  // a count changes at these units only
+  return worst;
+}
+
+double join_cycles(const Shape& s, const Choice& c, bool gated) {
+  if (c.splits == 1) return 0.0;
+  return 4000.0 + (c.splits * (gated ? 2.0 : 1.0) + 1.0) * s.I * s.J * 4.0 / 2500.0;
+}
+
+// Tries the widths and splits of problem q with the others as they are.
+void choose(const Shape* s, int n, int q, bool pair, bool gated, Plan* best) {
+  const int units = pair ? UNITS / 2 : UNITS;
+  const int mats = gated ? 2 : 1;
+  const int widest = gated ? 128 : 256;
+  const int step = s[q].b_mn ? (pair ? 128 : 64) : 32;
+  Plan p = *best;
+  for (int jt = step; jt <= widest; jt += step) {
+    if (jt > step && jt - step >= s[q].J) break;  // a narrower one holds all rows
+    const int64_t tiles = i_tiles(s[q], pair) * cdiv(s[q].J, jt);
+    for (int splits = 1; splits <= std::min(s[q].kb, 64); splits = splits < 8 ? splits + 1 : splits + 4) {
+      if (splits > 1 && (tiles * (splits - 1) > 2 * units ||
+                         int64_t(splits) * mats * s[q].I * s[q].J * 4 > MAX_PART_BYTES))
+        break;
+      Choice& c = p.c[q];
+      c.jt = jt;
+      c.kb_split = static_cast<int>(cdiv(s[q].kb, splits));
+      c.splits = static_cast<int>(cdiv(s[q].kb, c.kb_split));
+      if (c.splits != splits) continue;  // the same as fewer splits
+      c.items = tiles * splits;
+      c.item_cycles = item_cycles(jt, c.kb_split, pair, gated);
+      p.cycles = makespan(p.c, n, units);
+      for (int r = 0; r < n; ++r) p.cycles += join_cycles(s[r], p.c[r], gated);
+      if (best->cycles < 0.0 || p.cycles < best->cycles) *best = p;
+    }
+  }
+}
+
+Plan plan_tiles(const Shape* s, int n, bool gated) {
+  Plan best{};
+  best.cycles = -1.0;
+  for (const bool pair : {true, false}) {
+    Plan p{};
+    p.pair = pair;
+    p.cycles = -1.0;
+    for (int q = 0; q < n; ++q) {  // each alone, then each with the others
+      Plan one{};
+      one.pair = pair;
+      one.cycles = -1.0;
+      choose(s + q, 1, 0, pair, gated, &one);
+      p.c[q] = one.c[0];
+    }
+    for (int q = 0; q < n; ++q) {
+      p.cycles = -1.0;
+      choose(s, n, q, pair, gated, &p);
+    }
+    if (best.cycles < 0.0 || p.cycles < best.cycles) best = p;
+  }
+  return best;
+}
+
+// Plans are functions of sizes alone; searching one takes some 10 us.
+struct Planned {
+  Shape s[LIN_MAX_PROBLEMS];
+  int n = 0;
+  bool gated;
+  Plan plan;
+};
+
+Plan plan_of(const Shape* s, int n, bool gated) {
+  static thread_local Planned kept[64];
+  uint64_t h = static_cast<uint64_t>(n * 2 + gated);
+  for (int q = 0; q < n; ++q) {
+    for (const int v : {s[q].I, s[q].J, s[q].kb, static_cast<int>(s[q].b_mn)})
+      h = (h ^ static_cast<uint64_t>(v)) * 0x9e3779b97f4a7c15ull;
+  }
+  Planned& k = kept[h >> 58];
+  const auto same = [&] {
+    if (k.n != n || k.gated != gated) return false;
+    for (int q = 0; q < n; ++q) {
+      const Shape &a = k.s[q], &b = s[q];
+      if (a.I != b.I || a.J != b.J || a.kb != b.kb || a.b_mn != b.b_mn) return false;
+    }
+    return true;
+  };
+  if (!same()) {
+    for (int q = 0; q < n; ++q) k.s[q] = s[q];
+    k.n = n;
+    k.gated = gated;
+    k.plan = plan_tiles(s, n, gated);
+  }
+  return k.plan;
+}
+
+size_t part_bytes(const Shape& s, const Choice& c, bool gated) {
+  return c.splits == 1 ? 0 : round256(size_t(4) * c.splits * (gated ? 2 : 1) * s.I * s.J);
+}
+
+size_t parts_bytes(const Shape* s, int n, bool gated) {
+  const Plan p = plan_of(s, n, gated);
+  size_t b = 0;
+  for (int q = 0; q < n; ++q) b += part_bytes(s[q], p.c[q], gated);
+  return b;
+}
+
+// ---------------------------------------------------------------- products
+struct Operand {
+  const void* p;
+  int64_t pitch;
+};
+
+// One product: out[J][I] over `parts` pairs of operands.
+struct Product {
+  Shape s;
+  int parts;
+  Operand a[2], b[2];
+  bool a_mn;
+  int klen[2];
+  LinEpilogue e;
+};
+
+Shape shape_of(int64_t I, int64_t J, int64_t K, int parts, bool b_mn) {
+  return Shape{static_cast<int>(I), static_cast<int>(J), static_cast<int>(parts * cdiv(K, LIN_BK)), b_mn};
+}
+
+// The products in one launch, and the joins of those whose K is split.  `part`:
+// room for their partial sums.
+cce_status run_products(const Product* in, int n, bool gated, bool bf16, void* part, int sms, int pairs,
+                        cudaStream_t s, int* launches) {
+  Shape shapes[LIN_MAX_PROBLEMS];
+  for (int q = 0; q < n; ++q) shapes[q] = in[q].s;
+  const Plan plan = plan_of(shapes, n, gated);
+  if (plan.pair && pairs < 1) return CCE_ERR_CUDA;
+  LinArgs a{};
+  a.problems = n;
+  a.bf16 = bf16;
+  char* at = static_cast<char*>(part);
+  int64_t items = 0;
+  for (int q = 0; q < n; ++q) {
+    const Product& f = in[q];
+    const Choice& c = plan.c[q];
+    LinProblem& p = a.p[q];
+    p.I = f.s.I;
+    p.J = f.s.J;
+    p.klen[0] = f.klen[0];
+    p.klen[1] = f.parts > 1 && !gated ? f.klen[1] : 0;
+    p.kb_first = static_cast<int>(cdiv(f.klen[0], LIN_BK));
+    p.kb_all = f.s.kb;
+    p.a_mn = f.a_mn;
+    p.b_mn = f.s.b_mn;
+    p.jt = c.jt;
+    p.i_tiles = static_cast<int>(i_tiles(f.s, plan.pair));
+    p.j_tiles = static_cast<int>(cdiv(f.s.J, c.jt));
+    p.splits = c.splits;
+    p.kb_split = c.kb_split;
+    p.group = std::min(p.i_tiles, 8);
+    if (c.items >= LIMIT) return CCE_ERR_SHAPE;
+    p.items = static_cast<int>(c.items);
+    items += c.items;
+    p.part = reinterpret_cast<float*>(at);
+    at += part_bytes(f.s, c, gated);
+    p.e = f.e;
+    const uint32_t b_box = static_cast<uint32_t>(plan.pair ? c.jt / 2 : c.jt);
+    for (int m = 0; m < f.parts; ++m) {
+      const int k = f.klen[gated ? 0 : m];
+      bool ok = f.a_mn ? encode_operand(&p.a[m], bf16, f.a[m].p, p.I, k, f.a[m].pitch, 64, LIN_BK)
+                       : encode_operand(&p.a[m], bf16, f.a[m].p, k, p.I, f.a[m].pitch, LIN_BK, LIN_BI);
+      if (!gated || m == 0)
+        ok = ok && (f.s.b_mn ? encode_operand(&p.b[m], bf16, f.b[m].p, p.J, k, f.b[m].pitch, 64, LIN_BK)
+                             : encode_operand(&p.b[m], bf16, f.b[m].p, k, p.J, f.b[m].pitch, LIN_BK, b_box));
+      if (!ok) return CCE_ERR_CUDA;
+    }
+  }
+  if (items >= LIMIT) return CCE_ERR_SHAPE;
+  a.items = static_cast<int>(items);
+  const int units = static_cast<int>(std::min<int64_t>(plan.pair ? pairs : sms, items));
+  cudaError_t e = launch_linear_gemm(a, plan.pair, gated, units, s);
+  ++*launches;
+  for (int q = 0; q < n && e == cudaSuccess; ++q) {
+    if (a.p[q].splits == 1) continue;
+    e = launch_linear_join(a.p[q], gated, bf16, sms, s);
+    ++*launches;
+  }
+  return e == cudaSuccess ? CCE_OK : CCE_ERR_CUDA;
+}
+
+// ------------------------------------------------------------------ checks
+struct Matrix {
+  const void* p;
+  int64_t pitch;
+  int type;
+  int64_t rows, cols;
+};
+
+// An operand of a product: on 16 bytes, whole vectors a row.
+cce_status check_operand(const Matrix& m) {
+  if (m.rows > 0 && !m.p) return CCE_ERR_NULL;
+  if (m.pitch < m.cols || m.pitch >= (int64_t(1) << 31)) return CCE_ERR_SHAPE;
+  if (!multiple(m.p, 16) || m.pitch % 8 != 0) return CCE_ERR_ALIGN;
+  return CCE_OK;
+}
+cce_status check_matrix(const Matrix& m, bool optional = false) {
+  if (!m.p) return optional || m.rows == 0 ? CCE_OK : CCE_ERR_NULL;
+  if (m.pitch < m.cols) return CCE_ERR_SHAPE;
+  return multiple(m.p, type_bytes(m.type)) ? CCE_OK : CCE_ERR_ALIGN;
+}
+cce_status check_workspace(const void* ws, size_t have, size_t need) {
+  if (!ws) return CCE_ERR_NULL;
+  if (!multiple(ws, 256)) return CCE_ERR_ALIGN;
+  return have < need ? CCE_ERR_WORKSPACE : CCE_OK;
+}
+template <typename... S>
+cce_status first_of(S... s) {
+  cce_status r = CCE_OK;
+  ((r = r == CCE_OK ? s : r), ...);
+  return r;
+}
+
+size_t forward_bytes(int64_t M, int64_t N, int64_t K, bool gated) {
+  if (!sizes_ok(M, N, K)) return 0;
+  if (M <= LIN_FEW_ROWS) return 16;
+  const Shape s = shape_of(N, M, K, 1, false);
+  return std::max<size_t>(16, parts_bytes(&s, 1, gated));
+}
+
+cce_status forward(const Matrix& x, const Matrix* w, bool gated, int64_t M, int64_t N, int64_t K, const LinEpilogue& e,
+                   void* ws, cudaStream_t stream) {
+  int sms = 0, pairs = 0, launches = 0;
+  cce_status st = static_cast<cce_status>(layers_device_ready(&sms, &pairs));
+  if (st != CCE_OK || M == 0) return st;
+  const bool bf16 = x.type == CCE_BF16;
+  if (M <= LIN_FEW_ROWS) {
+    const LinFew f{{w[0].p, w[gated ? 1 : 0].p}, {w[0].pitch, w[gated ? 1 : 0].pitch}, x.p, x.pitch, static_cast<int>(N),
+                   static_cast<int>(M), static_cast<int>(K), e};
+    st = launch_linear_few(f, gated, bf16, sms, stream) == cudaSuccess ? CCE_OK : CCE_ERR_CUDA;
+    ++launches;
+  } else {
+    Product p{};
+    p.s = shape_of(N, M, K, 1, false);
+    p.parts = gated ? 2 : 1;
+    for (int m = 0; m < p.parts; ++m) {
+      p.a[m] = Operand{w[m].p, w[m].pitch};
+      p.klen[m] = static_cast<int>(K);
+    }
+    p.b[0] = Operand{x.p, x.pitch};
+    p.e = e;
+    st = run_products(&p, 1, gated, bf16, ws, sms, pairs, stream, &launches);
+  }
+  count_launches(launches);
+  return st;
+}
+
+// ---------------------------------------------------------------- backward
+struct BackwardShapes {
+  Shape dx, dw;
+};
+BackwardShapes backward_shapes(int64_t M, int64_t N, int64_t K, int mats) {
+  return {shape_of(K, M, N, mats, false), shape_of(K, N, M, 1, true)};
+}
+
+// dz for the products, the row sums' parts, and the products' partial sums, in this order.
+struct BackwardLayout {
+  size_t dz, sums, parts;
+  int64_t pitch;
+  size_t total() const { return std::max<size_t>(16, dz + sums + parts); }
+};
+
+BackwardLayout backward_layout(int64_t M, int64_t N, int64_t K, int mats) {
+  BackwardLayout l{};
+  l.pitch = cdiv(N, 8) * 8;
+  l.dz = round256(size_t(2) * mats * M * l.pitch);
+  l.sums = mats == 1 ? round256(size_t(4) * LIN_GRAD_PARTS * N) : 0;
+  if (M == 0) return l;
+  const BackwardShapes b = backward_shapes(M, N, K, mats);
+  const Shape all[3] = {b.dw, mats == 2 ? b.dw : b.dx, b.dx};
+  // whatever is asked for: dx alone, the weights' alone, one of a gated layer's with dx, all
+  const Shape with_one[2] = {b.dw, b.dx}, twice[2] = {b.dw, b.dw};
+  l.parts = std::max({parts_bytes(&b.dx, 1, false), parts_bytes(&b.dw, 1, false), parts_bytes(with_one, 2, false),
+                      mats == 2 ? parts_bytes(twice, 2, false) : 0, mats == 2 ? parts_bytes(all, 3, false) : 0});
+  return l;
+}
+
+size_t backward_bytes(int64_t M, int64_t N, int64_t K, int mats) {
+  return sizes_ok(M, N, K) ? backward_layout(M, N, K, mats).total() : 0;
+}
+
+LinEpilogue dense_out(void* y, int64_t pitch, int type) {
+  LinEpilogue e{};
+  e.y = y;
+  e.y_pitch = pitch;
+  e.y_type = type;
+  return e;
+}
+
+// From the parts of dz to the gradients asked for.  weights, grad_w: mats of them.
+cce_status backward_products(const Operand* dz, const Matrix& x, const Matrix* w, int mats, int64_t M, int64_t N,
+                             int64_t K, void* grad_x, void* const* grad_w, void* parts, int sms, int pairs,
+                             cudaStream_t s, int* launches) {
+  const BackwardShapes b = backward_shapes(M, N, K, mats);
+  const int type = x.type;
+  Product p[LIN_MAX_PROBLEMS]{};
+  int n = 0;
+  for (int m = 0; m < mats; ++m) {
+    if (!grad_w[m]) continue;
+    p[n].s = b.dw;
+    p[n].parts = 1;
+    p[n].a[0] = Operand{x.p, x.pitch};
+    p[n].b[0] = dz[m];
+    p[n].a_mn = true;
+    p[n].klen[0] = static_cast<int>(M);
+    p[n++].e = dense_out(grad_w[m], K, type);
+  }
+  if (grad_x) {
+    p[n].s = b.dx;
+    p[n].parts = mats;
+    for (int m = 0; m < mats; ++m) {
+      p[n].a[m] = Operand{w[m].p, w[m].pitch};
+      p[n].b[m] = dz[m];
+      p[n].klen[m] = static_cast<int>(N);
+    }
+    p[n].a_mn = true;
+    p[n++].e = dense_out(grad_x, K, type);
+  }
+  return n == 0 ? CCE_OK : run_products(p, n, false, type == CCE_BF16, parts, sms, pairs, s, launches);
+}
+
+cce_status zero(void* p, size_t bytes, cudaStream_t s) {
+  return !p || cudaMemsetAsync(p, 0, bytes, s) == cudaSuccess ? CCE_OK : CCE_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace cce
+
+using namespace cce;
+
+extern "C" {
+
+int cce_layers_abi_version(void) { return 100; }
+
+size_t cce_linear_forward_workspace_bytes(int64_t M, int64_t N, int64_t K) { return forward_bytes(M, N, K, false); }
+size_t cce_gated_linear_forward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  return forward_bytes(M, N, K, true);
+}
+size_t cce_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) { return backward_bytes(M, N, K, 1); }
+size_t cce_gated_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  return backward_bytes(M, N, K, 2);
+}
+
+cce_status cce_linear_forward(const void* x, int64_t x_pitch, const void* weight, int64_t w_pitch, int type,
+                              const void* bias, int bias_type, const void* residual, int64_t res_pitch, int act,
+                              int64_t M, int64_t N, int64_t K, void* y, int64_t y_pitch, int y_type, void* z,
+                              int64_t z_pitch, void* workspace, size_t ws_bytes, void* stream) {
+  if (!operand_type(type) || !type_ok(bias_type) || (y_type != type && y_type != CCE_F32) || !act_ok(act))
+    return CCE_ERR_ARG;
+  if (!sizes_ok(M, N, K)) return CCE_ERR_SHAPE;
+  const Matrix xm{x, x_pitch, type, M, K}, wm{weight, w_pitch, type, N, K};
+  const cce_status st =
+      first_of(check_operand(xm), check_operand(wm), check_matrix({bias, N, bias_type, 1, N}, true),
+               check_matrix({residual, res_pitch, y_type, M, N}, true), check_matrix({y, y_pitch, y_type, M, N}),
+               check_matrix({z, z_pitch, type, M, N}, true),
+               check_workspace(workspace, ws_bytes, forward_bytes(M, N, K, false)));
+  if (st != CCE_OK) return st;
+  const LinEpilogue e{y, y_pitch, bias, residual, res_pitch, {z, nullptr}, z_pitch, y_type, bias_type, act};
+  return forward(xm, &wm, false, M, N, K, e, workspace, static_cast<cudaStream_t>(stream));
+}
+
+cce_status cce_gated_linear_forward(const void* x, int64_t x_pitch, const void* gate_weight, int64_t gw_pitch,
+                                    const void* up_weight, int64_t uw_pitch, int type, int act, int64_t M, int64_t N,
+                                    int64_t K, void* y, int64_t y_pitch, void* gate, void* up, int64_t z_pitch,
+                                    void* workspace, size_t ws_bytes, void* stream) {
+  if (!operand_type(type) || !act_ok(act)) return CCE_ERR_ARG;
+  if (!sizes_ok(M, N, K)) return CCE_ERR_SHAPE;
+  if (!gate != !up) return CCE_ERR_NULL;
+  const Matrix xm{x, x_pitch, type, M, K};
+  const Matrix wm[2] = {{gate_weight, gw_pitch, type, N, K}, {up_weight, uw_pitch, type, N, K}};
+  const cce_status st = first_of(check_operand(xm), check_operand(wm[0]), check_operand(wm[1]),
+                                 check_matrix({y, y_pitch, type, M, N}), check_matrix({gate, z_pitch, type, M, N}, true),
+                                 check_matrix({up, z_pitch, type, M, N}, true),
+                                 check_workspace(workspace, ws_bytes, forward_bytes(M, N, K, true)));
+  if (st != CCE_OK) return st;
+  const LinEpilogue e{y, y_pitch, nullptr, nullptr, 0, {gate, up}, z_pitch, type, type, act};
+  return forward(xm, wm, true, M, N, K, e, workspace, static_cast<cudaStream_t>(stream));
+}
+
+cce_status cce_linear_backward(const void* grad_y, int64_t g_pitch, int y_type, const void* x, int64_t x_pitch,
+                               const void* weight, int64_t w_pitch, int type, const void* z, int64_t z_pitch, int act,
+                               int64_t M, int64_t N, int64_t K, void* grad_x, void* grad_weight, void* grad_bias,
+                               int bias_type, void* workspace, size_t ws_bytes, void* stream) {
+  if (!operand_type(type) || !type_ok(bias_type) || (y_type != type && y_type != CCE_F32) || !act_ok(act))
+    return CCE_ERR_ARG;
+  if (!sizes_ok(M, N, K)) return CCE_ERR_SHAPE;
+  const Matrix xm{x, x_pitch, type, M, K}, wm{weight, w_pitch, type, N, K};
+  cce_status st = first_of(
+      check_matrix({grad_y, g_pitch, y_type, M, N}), check_operand(xm), check_operand(wm),
+      check_matrix({z, z_pitch, type, M, N}, act == CCE_ACT_NONE), check_matrix({grad_x, K, type, M, K}, true),
+      check_matrix({grad_weight, K, type, N, K}, true), check_matrix({grad_bias, N, bias_type, 1, N}, true),
+      check_workspace(workspace, ws_bytes, backward_bytes(M, N, K, 1)));
+  if (st != CCE_OK) return st;
+  int sms = 0, pairs = 0, launches = 0;
+  st = static_cast<cce_status>(layers_device_ready(&sms, &pairs));
+  if (st != CCE_OK) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (M == 0)
+    return first_of(zero(grad_weight, size_t(2) * N * K, s), zero(grad_bias, size_t(type_bytes(bias_type)) * N, s));
+  const BackwardLayout l = backward_layout(M, N, K, 1);
+  char* ws = static_cast<char*>(workspace);
+  // without an activation the products read grad_y itself where they can
+  Operand dz{grad_y, g_pitch};
+  const bool direct = act == CCE_ACT_NONE && y_type == type && multiple(grad_y, 16) && g_pitch % 8 == 0 &&
+                      g_pitch < (int64_t(1) << 31);
+  const bool staged = !direct && (grad_x || grad_weight);
+  if (staged) dz = Operand{ws, l.pitch};
+  if (staged || grad_bias) {
+    LinGrad g{};
+    g.dy = grad_y;
+    g.dy_pitch = g_pitch;
+    g.dy_type = y_type;
+    g.z[0] = act == CCE_ACT_NONE ? nullptr : z;
+    g.z_pitch[0] = z_pitch;
+    g.dz[0] = staged ? ws : nullptr;
+    g.dz_pitch = l.pitch;
+    g.part = grad_bias ? reinterpret_cast<float*>(ws + l.dz) : nullptr;
+    g.db = grad_bias;
+    g.db_type = bias_type;
+    g.M = static_cast<int>(M);
+    g.N = static_cast<int>(N);
+    g.act = act;
+    if (launch_linear_grad(g, false, type == CCE_BF16, sms, s, &launches) != cudaSuccess) st = CCE_ERR_CUDA;
+  }
+  if (st == CCE_OK)
+    st = backward_products(&dz, xm, &wm, 1, M, N, K, grad_x, &grad_weight, ws + l.dz + l.sums, sms, pairs, s,
+                           &launches);
+  count_launches(launches);
+  return st;
+}
+
+cce_status cce_gated_linear_backward(const void* grad_y, int64_t g_pitch, const void* x, int64_t x_pitch,
+                                     const void* gate_weight, int64_t gw_pitch, const void* up_weight,
+                                     int64_t uw_pitch, int type, const void* gate, int64_t gate_pitch, const void* up,
+                                     int64_t up_pitch, int act, int64_t M, int64_t N, int64_t K, void* grad_x,
+                                     void* grad_gate_weight, void* grad_up_weight, void* workspace, size_t ws_bytes,
+                                     void* stream) {
+  if (!operand_type(type) || !act_ok(act)) return CCE_ERR_ARG;
+  if (!sizes_ok(M, N, K)) return CCE_ERR_SHAPE;
+  const Matrix xm{x, x_pitch, type, M, K};
+  const Matrix wm[2] = {{gate_weight, gw_pitch, type, N, K}, {up_weight, uw_pitch, type, N, K}};
+  cce_status st = first_of(
+      check_matrix({grad_y, g_pitch, type, M, N}), check_operand(xm), check_operand(wm[0]), check_operand(wm[1]),
+      check_matrix({gate, gate_pitch, type, M, N}), check_matrix({up, up_pitch, type, M, N}),
+      check_matrix({grad_x, K, type, M, K}, true), check_matrix({grad_gate_weight, K, type, N, K}, true),
+      check_matrix({grad_up_weight, K, type, N, K}, true),
+      check_workspace(workspace, ws_bytes, backward_bytes(M, N, K, 2)));
+  if (st != CCE_OK) return st;
+  int sms = 0, pairs = 0, launches = 0;
+  st = static_cast<cce_status>(layers_device_ready(&sms, &pairs));
+  if (st != CCE_OK) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (M == 0)
+    return first_of(zero(grad_gate_weight, size_t(2) * N * K, s), zero(grad_up_weight, size_t(2) * N * K, s));
+  if (!grad_x && !grad_gate_weight && !grad_up_weight) return CCE_OK;
+  const BackwardLayout l = backward_layout(M, N, K, 2);
+  char* ws = static_cast<char*>(workspace);
+  LinGrad g{};
+  g.dy = grad_y;
+  g.dy_pitch = g_pitch;
+  g.dy_type = type;
+  g.z[0] = gate;
+  g.z[1] = up;
+  g.z_pitch[0] = gate_pitch;
+  g.z_pitch[1] = up_pitch;
+  // one matrix after the other: rows of each start on 16 bytes
+  g.dz[0] = ws;
+  g.dz[1] = ws + size_t(2) * M * l.pitch;
+  g.dz_pitch = l.pitch;
+  g.M = static_cast<int>(M);
+  g.N = static_cast<int>(N);
+  g.act = act;
+  if (launch_linear_grad(g, true, type == CCE_BF16, sms, s, &launches) != cudaSuccess) st = CCE_ERR_CUDA;
+  const Operand dz[2] = {{g.dz[0], l.pitch}, {g.dz[1], l.pitch}};
+  void* grad_w[2] = {grad_gate_weight, grad_up_weight};
+  if (st == CCE_OK)
+    st = backward_products(dz, xm, wm, 2, M, N, K, grad_x, grad_w, ws + l.dz, sms, pairs, s, &launches);
+  count_launches(launches);
+  return st;
+}
+
+cce_status cce_layers_take_error(int32_t* word, void* stream) {
+  if (!word) return CCE_ERR_NULL;
+  int sms = 0;
+  const cce_status st = static_cast<cce_status>(device_ready(&sms));
+  if (st != CCE_OK) return st;
+  return take_linear_error(word, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CCE_OK : CCE_ERR_CUDA;
+}
+
+}  // extern "C"

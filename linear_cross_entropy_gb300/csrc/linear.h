@@ -1,0 +1,98 @@
+// Products with a fused epilogue (include/cce_layers.h): arguments of the kernels
+// and their launchers, shared by the entry points (layers_api.cu), the tcgen05
+// GEMM (linear_gemm.cu) and the kernels around it (linear_few.cu, linear_pass.cu).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+namespace cce {
+
+// What happens to an accumulator on its way out: z = acc + bias[i], y = f(z) +
+// residual, with [J][I] matrices whose index i is contiguous.  Gated: y = f(z0) z1.
+struct LinEpilogue {
+  void* y;
+  int64_t y_pitch;
+  const void* bias;  // [I], may be null
+  const void* res;   // of y's type, may be null
+  int64_t res_pitch;
+  void* z[2];  // pre-activations in the operands' type, may be null
+  int64_t z_pitch;
+  int y_type, bias_type, act;
+};
+
+// out[j][i] = epilogue(sum over k of A(i, k) B(j, k)).  The sum may run over two
+// pairs of operands in turn (dx of a gated layer); gated forward: a[0] and a[1]
+// are the gate's and the up projection's weights, both against b[0].
+struct LinProblem {
+  CUtensorMap a[2];
+  CUtensorMap b[2];
+  int I, J;
+  int klen[2];   // elements of either part of the sum (klen[1] = 0: one part)
+  int kb_first;  // 64-deep blocks of the first part
+  int kb_all;
+  int a_mn, b_mn;  // operand stored with its I (J) index contiguous
+  int jt;          // tile width in J
+  int i_tiles, j_tiles, splits, kb_split;  // kb_split: blocks of K per split
+  int group;       // i tiles that are walked together
+  int items;       // i_tiles * j_tiles * splits
+  float* part;     // splits > 1: [splits][GATED ? 2 : 1][J][I]
+  LinEpilogue e;
+};
+
+constexpr int LIN_MAX_PROBLEMS = 3;
+struct LinArgs {
+  LinProblem p[LIN_MAX_PROBLEMS];
+  int problems;
+  int items;
+  int bf16;  // operands are bf16, else fp16
+};
+
+constexpr int LIN_BI = 128;  // rows of the MMA a CTA: I extent of a tile
+constexpr int LIN_BK = 64;
+
+// The launch as `units` persistent CTAs or CTA pairs.
+cudaError_t launch_linear_gemm(const LinArgs& a, bool pair, bool gated, int units, cudaStream_t s);
+// CTA pairs that are resident at once.
+int linear_pair_units(int sms);
+cudaError_t prepare_linear_gemm();
+// The device's error word (CCE_DEVERR_*) of these kernels, taken and cleared behind `s`.
+cudaError_t take_linear_error(int32_t* word, cudaStream_t s);
+
+// y = epilogue of the sums over the splits of a problem.
+cudaError_t launch_linear_join(const LinProblem& p, bool gated, bool bf16, int sms, cudaStream_t s);
+
+// Few rows: out[j][i] = epilogue(sum over k of w[i][k] x[j][k]), J <= LIN_FEW_ROWS.
+struct LinFew {
+  const void* w[2];
+  int64_t w_pitch[2];
+  const void* x;
+  int64_t x_pitch;
+  int I, J, K;
+  LinEpilogue e;
+};
+constexpr int LIN_FEW_ROWS = 16;
+cudaError_t launch_linear_few(const LinFew& a, bool gated, bool bf16, int sms, cudaStream_t s);
+
+// The element-wise part of the backward pass: dz = dy f'(z) (gated: dgate = dy u
+// f'(g) and dup = dy f(g)) in the operands' type, and the sums of dz over the rows.
+struct LinGrad {
+  const void* dy;
+  int64_t dy_pitch;
+  int dy_type;
+  const void* z[2];
+  int64_t z_pitch[2];
+  void* dz[2];  // may be null (sums alone)
+  int64_t dz_pitch;
+  float* part;  // [parts][N], may be null (no sums)
+  void* db;
+  int db_type;
+  int M, N, act;
+};
+constexpr int LIN_GRAD_PARTS = 256;
+cudaError_t launch_linear_grad(const LinGrad& a, bool gated, bool bf16, int sms, cudaStream_t s, int* launches);
+
+}  // namespace cce

@@ -1,0 +1,141 @@
+// A layer over few rows (decoding): out[j][i] = epilogue(sum over k of w[i][k] x[j][k])
+// for up to 16 rows j.
+//
+// Bound by reading the weights once, so nothing is staged: a warp reads 16-byte
+// vectors of 16 weight rows straight into the fragments of mma.m16n8k16, whose k
+// index is free to be permuted as long as both operands are permuted alike.  (A
+// tcgen05 MMA wants its operands in shared memory and 128 weight rows a CTA, and
+// there are too few of those to keep 152 SMs reading.)  The eight warps of a block
+// take every eighth 64 of k and add up through shared memory in a fixed order.
+#include "internal.h"
+#include "linear.h"
+#include "linear_epilogue.cuh"
+
+namespace cce {
+namespace {
+
+constexpr int WARPS = 8;
+constexpr int ROWS = 16;  // of w, a block
+
+template <bool BF16>
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  if constexpr (BF16) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  } else {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  }
+}
+
+// Eight values from k on, zeros behind K (a multiple of 8 or padded to one: vectors are whole).
+__device__ __forceinline__ uint4 vector_at(const uint16_t* row, int k, int K, bool there) {
+  if (!there || k >= K) return make_uint4(0u, 0u, 0u, 0u);
+  uint4 v = *reinterpret_cast<const uint4*>(row + k);
+  const int n = K - k;
+  if (n < 8) {  // the last vector of an odd width: what lies behind may be anything
+    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = 2 * i + 1 < n ? w[i] : 2 * i < n ? w[i] & 0xffffu : 0u;
+  }
+  return v;
+}
+
+template <bool BF16, int NT, bool GATED, int UNROLL>
+__global__ void __launch_bounds__(32 * WARPS) few_kernel(const __grid_constant__ LinFew a) {
+  constexpr int MATS = GATED ? 2 : 1;
+  __shared__ float sums[WARPS][MATS][ROWS][8 * NT + 1];
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+  const int g = lane >> 2, t = lane & 3;
+  const int i0 = static_cast<int>(blockIdx.x) * ROWS;
+  let_next_start();
+  wait_for_previous();
+  // rows of w behind the last one are read as the last one, and not written
+  const uint16_t* w[MATS][2];
+#pragma unroll
+  for (int m = 0; m < MATS; ++m) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      w[m][h] = static_cast<const uint16_t*>(a.w[m]) + static_cast<int64_t>(min(i0 + g + 8 * h, a.I - 1)) * a.w_pitch[m];
+  }
+  const uint16_t* x[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+    x[n] = static_cast<const uint16_t*>(a.x) + static_cast<int64_t>(min(g + 8 * n, a.J - 1)) * a.x_pitch;
+
+  float c[MATS][NT][4];
+#pragma unroll
+  for (int m = 0; m < MATS; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) c[m][n][q] = 0.0f;
+
+  // a step is 32 of k: thread t of a row has 8t .. 8t + 7; the first four of them are one MMA's, the others the next one's
+  for (int k0 = warp * 64; k0 < a.K; k0 += 64 * WARPS * (UNROLL / 2)) {
+    uint4 wv[UNROLL][MATS][2], xv[UNROLL][NT];
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+      const int k = k0 + (u >> 1) * 64 * WARPS + (u & 1) * 32 + 8 * t;
+#pragma unroll
+      for (int m = 0; m < MATS; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) wv[u][m][h] = vector_at(w[m][h], k, a.K, true);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) xv[u][n] = vector_at(x[n], k, a.K, g + 8 * n < a.J);
+    }
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int m = 0; m < MATS; ++m) {
+          const uint4 &lo = wv[u][m][0], &hi = wv[u][m][1], &b = xv[u][n];
+          mma<BF16>(c[m][n], lo.x, hi.x, lo.y, hi.y, b.x, b.y);
+          mma<BF16>(c[m][n], lo.z, hi.z, lo.w, hi.w, b.z, b.w);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < MATS; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) sums[warp][m][g + 8 * (q >> 1)][8 * n + 2 * t + (q & 1)] = c[m][n][q];
+  __syncthreads();
+  const int r = static_cast<int>(threadIdx.x) % ROWS, j = static_cast<int>(threadIdx.x) / ROWS;
+  const int i = i0 + r;
+  if (j >= 8 * NT || j >= a.J || i >= a.I) return;
+  float z0[1] = {0.0f}, z1[1] = {0.0f};
+#pragma unroll
+  for (int v = 0; v < WARPS; ++v) {
+    z0[0] += sums[v][0][r][j];
+    if (GATED) z1[0] += sums[v][MATS - 1][r][j];
+  }
+  const float bias = a.e.bias ? load_scalar(a.e.bias, a.e.bias_type, i) : 0.0f;
+  finish_column<GATED>(a.e, BF16, bias, i, j, 1, z0, z1);
+}
+static_assert(32 * WARPS == ROWS * LIN_FEW_ROWS, "one result a thread");
+
+template <bool BF16, int NT>
+cudaError_t launch(const LinFew& a, bool gated, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>((a.I + ROWS - 1) / ROWS)), block(32 * WARPS);
+  return gated ? launch_after(few_kernel<BF16, NT, true, 4>, grid, block, 0, 1, s, a)
+               : launch_after(few_kernel<BF16, NT, false, 8>, grid, block, 0, 1, s, a);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_few(const LinFew& a, bool gated, bool bf16, int sms, cudaStream_t s) {
+  (void)sms;
+  if (bf16) return a.J <= 8 ? launch<true, 1>(a, gated, s) : launch<true, 2>(a, gated, s);
+  return a.J <= 8 ? launch<false, 1>(a, gated, s) : launch<false, 2>(a, gated, s);
+}
+
+}  // namespace cce

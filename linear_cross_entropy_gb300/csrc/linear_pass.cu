@@ -1,0 +1,200 @@
+// Element-wise passes of the layers in front of the head, all bound by memory:
+//
+//   join  the epilogue over the partial sums of a product whose K was split
+//   grad  dz = dy f'(z), or of a gated layer dgate = dy u f'(g) and dup = dy f(g),
+//         in the type of the products that follow, and the sums of dz over the rows
+#include <algorithm>
+
+#include "internal.h"
+#include "linear.h"
+#include "linear_epilogue.cuh"
+
+namespace cce {
+namespace {
+
+constexpr int THREADS = 256;
+constexpr int JOIN_ROWS = 4;
+
+template <bool GATED>
+__global__ void __launch_bounds__(THREADS) join_kernel(const float* part, int I, int J, int splits, LinEpilogue e,
+                                                       bool bf16) {
+  let_next_start();
+  wait_for_previous();
+  const int i = static_cast<int>(blockIdx.x) * THREADS + static_cast<int>(threadIdx.x);
+  if (i >= I) return;
+  const float bias = e.bias ? load_scalar(e.bias, e.bias_type, i) : 0.0f;
+  for (int64_t row = static_cast<int64_t>(blockIdx.y) * JOIN_ROWS; row < J; row += static_cast<int64_t>(gridDim.y) * JOIN_ROWS) {
+    const int j0 = static_cast<int>(row), n = min(JOIN_ROWS, J - j0);
+    float z0[JOIN_ROWS] = {}, z1[JOIN_ROWS] = {};
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {  // in order
+      const float* p = part + (static_cast<int64_t>(s * (GATED ? 2 : 1)) * J + j0) * I + i;
+#pragma unroll
+      for (int u = 0; u < JOIN_ROWS; ++u) {
+        if (u < n) {
+          z0[u] += p[static_cast<int64_t>(u) * I];
+          if (GATED) z1[u] += p[(static_cast<int64_t>(J) + u) * I];
+        }
+      }
+    }
+    finish_column<GATED>(e, bf16, bias, i, j0, n, z0, z1);
+  }
+}
+
+// ------------------------------------------------------------------- backward
+constexpr int COLS = 32, GROUPS = THREADS / COLS;  // a block: vectors of a row, rows at a time
+constexpr int UNROLL = 4;                          // rows of a thread in flight
+
+template <int ACT, bool GATED, int VEC>
+__device__ __forceinline__ void grad_as(float (&d0)[VEC], float (&d1)[VEC], const float (&dy)[VEC],
+                                        const float (&z0)[VEC], const float (&z1)[VEC]) {
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    const float2 f = activate_both<ACT>(z0[e]);
+    if (GATED) {
+      d0[e] = dy[e] * z1[e] * f.y;
+      d1[e] = dy[e] * f.x;
+    } else {
+      d0[e] = dy[e] * f.y;
+    }
+  }
+}
+
+template <typename T, typename TY, bool GATED, int VEC>
+__global__ void __launch_bounds__(THREADS) grad_kernel(const __grid_constant__ LinGrad a) {
+  let_next_start();
+  wait_for_previous();
+  const int tx = static_cast<int>(threadIdx.x) % COLS, ty = static_cast<int>(threadIdx.x) / COLS;
+  const int col = (static_cast<int>(blockIdx.x) * COLS + tx) * VEC;
+  float sum[VEC] = {};
+  if (col < a.N) {
+    const int64_t step = static_cast<int64_t>(gridDim.y) * GROUPS;
+    for (int64_t r0 = static_cast<int64_t>(blockIdx.y) * GROUPS + ty; r0 < a.M; r0 += step * UNROLL) {
+      Vec<TY, VEC> dy[UNROLL];
+      Vec<T, VEC> z0[UNROLL], z1[UNROLL];
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u) {
+        const int64_t r = r0 + u * step;
+        if (r < a.M) {
+          dy[u].load(static_cast<const TY*>(a.dy) + r * a.dy_pitch + col);
+          if (a.act != CCE_ACT_NONE || GATED) z0[u].load(static_cast<const T*>(a.z[0]) + r * a.z_pitch[0] + col);
+          if (GATED) z1[u].load(static_cast<const T*>(a.z[1]) + r * a.z_pitch[1] + col);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u) {
+        const int64_t r = r0 + u * step;
+        if (r >= a.M) break;
+        float g[VEC], f0[VEC], f1[VEC], d0[VEC], d1[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          g[e] = dy[u].get(e);
+          f0[e] = z0[u].get(e);
+          if (GATED) f1[e] = z1[u].get(e);
+        }
+        switch (a.act) {
+          case CCE_ACT_RELU: grad_as<CCE_ACT_RELU, GATED>(d0, d1, g, f0, f1); break;
+          case CCE_ACT_GELU: grad_as<CCE_ACT_GELU, GATED>(d0, d1, g, f0, f1); break;
+          case CCE_ACT_GELU_TANH: grad_as<CCE_ACT_GELU_TANH, GATED>(d0, d1, g, f0, f1); break;
+          case CCE_ACT_SILU: grad_as<CCE_ACT_SILU, GATED>(d0, d1, g, f0, f1); break;
+          default: grad_as<CCE_ACT_NONE, GATED>(d0, d1, g, f0, f1); break;
+        }
+        Vec<T, VEC> o;
+        if (a.dz[0]) {
+          o.set(d0);
+          o.store(static_cast<T*>(a.dz[0]) + r * a.dz_pitch + col);
+        }
+        if (GATED) {
+          o.set(d1);
+          o.store(static_cast<T*>(a.dz[1]) + r * a.dz_pitch + col);
+        }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) sum[e] += d0[e];
+      }
+    }
+  }
+  if (!a.part) return;
+  __shared__ float sums[GROUPS][COLS * VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) sums[ty][tx * VEC + e] = sum[e];
+  __syncthreads();
+  for (int c = static_cast<int>(threadIdx.x); c < COLS * VEC; c += THREADS) {
+    const int at = static_cast<int>(blockIdx.x) * COLS * VEC + c;
+    if (at >= a.N) break;
+    float t = 0.0f;
+#pragma unroll
+    for (int v = 0; v < GROUPS; ++v) t += sums[v][c];
+    a.part[static_cast<int64_t>(blockIdx.y) * a.N + at] = t;
+  }
+}
+
+// db[c] = the sum of the blocks' sums, in a fixed order.
+__global__ void __launch_bounds__(THREADS) sum_kernel(const float* part, int parts, int N, void* db, int type) {
+  let_next_start();
+  wait_for_previous();
+  __shared__ float sums[GROUPS][COLS];
+  const int tx = static_cast<int>(threadIdx.x) % COLS, ty = static_cast<int>(threadIdx.x) / COLS;
+  const int c = static_cast<int>(blockIdx.x) * COLS + tx;
+  float t = 0.0f;
+  if (c < N) {
+#pragma unroll 8
+    for (int p = ty; p < parts; p += GROUPS) t += part[static_cast<int64_t>(p) * N + c];
+  }
+  sums[ty][tx] = t;
+  __syncthreads();
+  if (ty != 0 || c >= N) return;
+#pragma unroll
+  for (int v = 1; v < GROUPS; ++v) t += sums[v][tx];
+  store_param(db, type, c, t);
+}
+
+bool multiple(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(bytes) == 0; }
+
+template <typename T, typename TY, bool GATED>
+cudaError_t launch_grad(const LinGrad& a, int sms, cudaStream_t s, int* launches) {
+  // vectors of 8: whole rows of them at 16 bytes in every matrix (dy of fp32 rows as two)
+  bool wide = a.N % 8 == 0 && a.dy_pitch % 8 == 0 && multiple(a.dy, 16);
+  for (int m = 0; m < (GATED ? 2 : 1); ++m) {
+    if (a.z[m]) wide = wide && a.z_pitch[m] % 8 == 0 && multiple(a.z[m], 16);
+    if (a.dz[m]) wide = wide && a.dz_pitch % 8 == 0 && multiple(a.dz[m], 16);
+  }
+  const int vec = wide ? 8 : 1;
+  const int x = (a.N + COLS * vec - 1) / (COLS * vec);
+  // six blocks an SM, no more than there are rows for
+  const int y = std::max(1, std::min({LIN_GRAD_PARTS, (6 * sms + x - 1) / x, (a.M + GROUPS * UNROLL - 1) / (GROUPS * UNROLL)}));
+  const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(y));
+  cudaError_t e = wide ? launch_after(grad_kernel<T, TY, GATED, 8>, grid, dim3(THREADS), 0, 1, s, a)
+                       : launch_after(grad_kernel<T, TY, GATED, 1>, grid, dim3(THREADS), 0, 1, s, a);
+  ++*launches;
+  if (e == cudaSuccess && a.part) {
+    e = launch_after(sum_kernel, dim3(static_cast<unsigned>((a.N + COLS - 1) / COLS)), dim3(THREADS), 0, 1, s,
+                     static_cast<const float*>(a.part), y, a.N, a.db, a.db_type);
+    ++*launches;
+  }
+  return e;
+}
+
+template <typename T>
+cudaError_t launch_grad_of(const LinGrad& a, bool gated, int sms, cudaStream_t s, int* launches) {
+  if (gated) return launch_grad<T, T, true>(a, sms, s, launches);
+  return a.dy_type == CCE_F32 ? launch_grad<T, float, false>(a, sms, s, launches)
+                              : launch_grad<T, T, false>(a, sms, s, launches);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_join(const LinProblem& p, bool gated, bool bf16, int sms, cudaStream_t s) {
+  const int x = (p.I + THREADS - 1) / THREADS;
+  const int y = std::max(1, std::min((p.J + JOIN_ROWS - 1) / JOIN_ROWS, (8 * sms + x - 1) / x));
+  const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(y));
+  const float* part = p.part;
+  return gated ? launch_after(join_kernel<true>, grid, dim3(THREADS), 0, 1, s, part, p.I, p.J, p.splits, p.e, bf16)
+               : launch_after(join_kernel<false>, grid, dim3(THREADS), 0, 1, s, part, p.I, p.J, p.splits, p.e, bf16);
+}
+
+cudaError_t launch_linear_grad(const LinGrad& a, bool gated, bool bf16, int sms, cudaStream_t s, int* launches) {
+  return bf16 ? launch_grad_of<__nv_bfloat16>(a, gated, sms, s, launches)
+              : launch_grad_of<__half>(a, gated, sms, s, launches);
+}
+
+}  // namespace cce
