@@ -717,6 +717,17 @@ bool encode_operand(CUtensorMap* m, bool bf16, const void* p, uint64_t inner, ui
                    pitch, box_inner, box_outer);
 }
 
+bool encode_groups(CUtensorMap* m, bool bf16, const void* p, uint64_t inner, uint64_t outer, uint64_t pitch,
+                   uint32_t box_rows, uint32_t groups) {
+  cuuint64_t dims[3] = {64, outer, inner / 64};
+  cuuint64_t strides[2] = {pitch * 2, 128};
+  cuuint32_t box[3] = {64, box_rows, groups};
+  cuuint32_t es[3] = {1, 1, 1};
+  return g_encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(p),
+                  dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 void count_launches(int n) { g_launches += static_cast<uint64_t>(n); }
 
 }  // namespace cce

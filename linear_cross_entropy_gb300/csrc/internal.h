@@ -35,6 +35,9 @@ int layers_device_ready(int* sms, int* pairs);
 // A 2-D tensor map over 16-bit values, 128-byte swizzle; after device_ready().
 bool encode_operand(CUtensorMap* m, bool bf16, const void* p, uint64_t inner, uint64_t outer, uint64_t pitch,
                     uint32_t box_inner, uint32_t box_outer);
+// The same rows (inner % 64 == 0) as {64, outer, inner / 64}, with boxes of {64, box_rows, groups}.
+bool encode_groups(CUtensorMap* m, bool bf16, const void* p, uint64_t inner, uint64_t outer, uint64_t pitch,
+                   uint32_t box_rows, uint32_t groups);
 // Adds to cce_kernel_launch_count().
 void count_launches(int n);
 

@@ -32,8 +32,8 @@ size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 // sized without a device.
 struct Shape {
   int I, J;
-  int kb;      // 64-deep blocks of K
-  bool b_mn;   // B comes in groups of 64 j
+  int K, parts;  // `parts` sums of K
+  bool b_mn;     // B comes in groups of 64 j
 };
 struct Choice {
   int jt, splits, kb_split;
@@ -49,16 +49,16 @@ struct Plan {
 constexpr int UNITS = 152;                       // SMs
 constexpr int64_t MAX_PART_BYTES = 256ll << 20;  // of a product's partial sums
 
-int64_t i_tiles(const Shape& s, bool pair) { return cdiv(s.I, pair ? 2 * LIN_BI : LIN_BI); }
+int64_t i_tiles(const Shape& s, bool pair, bool gated) { return cdiv(s.I, (pair ? 2 : 1) * (gated ? LIN_BI / 2 : LIN_BI)); }
+int k_blocks(const Shape& s, bool pair) { return static_cast<int>(s.parts * cdiv(s.K, lin_bk(pair))); }
 
 // Cycles of one work item: its blocks of K at the slower of the tensor core (8,192
 // flops a cycle and SM) and the loads (56 bytes a cycle and SM from L2), and what a
 // tile costs beside them.
-double item_cycles(int jt, int kb, bool pair, bool gated) {
-  const int mats = gated ? 2 : 1;
-  const double mma = 2.0 * jt * mats;
-  const double load = (mats * LIN_BI + (pair ? jt / 2 : jt)) * 128.0 / 56.0;
-  return kb * std::max(mma, load) + 500.0;
+double item_cycles(int jt, int kb, bool pair) {
+  const double mma = 2.0 * jt;
+  const double load = (LIN_BI + (pair ? jt / 2 : jt)) * 128.0 / 56.0;
+  return kb * std::max(mma, load) * (lin_bk(pair) / 64) + 500.0;
 }
 
 // The longest of the units' shares: unit u takes items u, u + units, ... of the
@@ -92,23 +92,23 @@ double join_cycles(const Shape& s, const Choice& c, bool gated) {
 void choose(const Shape* s, int n, int q, bool pair, bool gated, Plan* best) {
   const int units = pair ? UNITS / 2 : UNITS;
   const int mats = gated ? 2 : 1;
-  const int widest = gated ? 128 : 256;
+  const int kb = k_blocks(s[q], pair);
   const int step = s[q].b_mn ? (pair ? 128 : 64) : 32;
   Plan p = *best;
-  for (int jt = step; jt <= widest; jt += step) {
+  for (int jt = step; jt <= 256; jt += step) {
     if (jt > step && jt - step >= s[q].J) break;  // a narrower one holds all rows
-    const int64_t tiles = i_tiles(s[q], pair) * cdiv(s[q].J, jt);
-    for (int splits = 1; splits <= std::min(s[q].kb, 64); splits = splits < 8 ? splits + 1 : splits + 4) {
+    const int64_t tiles = i_tiles(s[q], pair, gated) * cdiv(s[q].J, jt);
+    for (int splits = 1; splits <= std::min(kb, 64); splits = splits < 8 ? splits + 1 : splits + 4) {
       if (splits > 1 && (tiles * (splits - 1) > 2 * units ||
                          int64_t(splits) * mats * s[q].I * s[q].J * 4 > MAX_PART_BYTES))
         break;
       Choice& c = p.c[q];
       c.jt = jt;
-      c.kb_split = static_cast<int>(cdiv(s[q].kb, splits));
-      c.splits = static_cast<int>(cdiv(s[q].kb, c.kb_split));
+      c.kb_split = static_cast<int>(cdiv(kb, splits));
+      c.splits = static_cast<int>(cdiv(kb, c.kb_split));
       if (c.splits != splits) continue;  // the same as fewer splits
       c.items = tiles * splits;
-      c.item_cycles = item_cycles(jt, c.kb_split, pair, gated);
+      c.item_cycles = item_cycles(jt, c.kb_split, pair);
       p.cycles = makespan(p.c, n, units);
       for (int r = 0; r < n; ++r) p.cycles += join_cycles(s[r], p.c[r], gated);
       if (best->cycles < 0.0 || p.cycles < best->cycles) *best = p;
@@ -151,7 +151,7 @@ Plan plan_of(const Shape* s, int n, bool gated) {
   static thread_local Planned kept[64];
   uint64_t h = static_cast<uint64_t>(n * 2 + gated);
   for (int q = 0; q < n; ++q) {
-    for (const int v : {s[q].I, s[q].J, s[q].kb, static_cast<int>(s[q].b_mn)})
+    for (const int v : {s[q].I, s[q].J, s[q].K, s[q].parts, static_cast<int>(s[q].b_mn)})
       h = (h ^ static_cast<uint64_t>(v)) * 0x9e3779b97f4a7c15ull;
   }
   Planned& k = kept[h >> 58];
@@ -159,7 +159,7 @@ Plan plan_of(const Shape* s, int n, bool gated) {
     if (k.n != n || k.gated != gated) return false;
     for (int q = 0; q < n; ++q) {
       const Shape &a = k.s[q], &b = s[q];
-      if (a.I != b.I || a.J != b.J || a.kb != b.kb || a.b_mn != b.b_mn) return false;
+      if (a.I != b.I || a.J != b.J || a.K != b.K || a.parts != b.parts || a.b_mn != b.b_mn) return false;
     }
     return true;
   };
@@ -192,15 +192,22 @@ struct Operand {
 // One product: out[J][I] over `parts` pairs of operands.
 struct Product {
   Shape s;
-  int parts;
-  Operand a[2], b[2];
+  Operand a[2], b[2];  // gated: both weights, and x
   bool a_mn;
-  int klen[2];
   LinEpilogue e;
 };
 
 Shape shape_of(int64_t I, int64_t J, int64_t K, int parts, bool b_mn) {
-  return Shape{static_cast<int>(I), static_cast<int>(J), static_cast<int>(parts * cdiv(K, LIN_BK)), b_mn};
+  return Shape{static_cast<int>(I), static_cast<int>(J), static_cast<int>(K), parts, b_mn};
+}
+
+// The map of an operand with `rows` of its own index in a tile: boxes of 64 contiguous
+// elements, in 3 dimensions all of a stage's.
+bool encode(CUtensorMap* m, bool bf16, const Operand& o, int K, int own, bool mn, bool whole, uint32_t bk, int rows) {
+  const uint64_t inner = mn ? own : K, outer = mn ? K : own;
+  const uint32_t box_rows = mn ? bk : static_cast<uint32_t>(rows), groups = (mn ? rows : static_cast<int>(bk)) / 64;
+  return whole ? encode_groups(m, bf16, o.p, inner, outer, o.pitch, box_rows, groups)
+               : encode_operand(m, bf16, o.p, inner, outer, o.pitch, 64, box_rows);
 }
 
 // The products in one launch, and the joins of those whose K is split.  `part`:
@@ -211,25 +218,34 @@ cce_status run_products(const Product* in, int n, bool gated, bool bf16, void* p
   for (int q = 0; q < n; ++q) shapes[q] = in[q].s;
   const Plan plan = plan_of(shapes, n, gated);
   if (plan.pair && pairs < 1) return CCE_ERR_CUDA;
+  // the tensor maps are made by the driver, which wants this thread to have a context
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess || cudaSetDevice(device) != cudaSuccess) return CCE_ERR_CUDA;
+  const uint32_t bk = static_cast<uint32_t>(lin_bk(plan.pair));
   LinArgs a{};
   a.problems = n;
   a.bf16 = bf16;
   char* at = static_cast<char*>(part);
   int64_t items = 0;
+  int widest = 0;
   for (int q = 0; q < n; ++q) {
     const Product& f = in[q];
     const Choice& c = plan.c[q];
+    const int parts = f.s.parts;
     LinProblem& p = a.p[q];
     p.I = f.s.I;
     p.J = f.s.J;
-    p.klen[0] = f.klen[0];
-    p.klen[1] = f.parts > 1 && !gated ? f.klen[1] : 0;
-    p.kb_first = static_cast<int>(cdiv(f.klen[0], LIN_BK));
-    p.kb_all = f.s.kb;
+    p.klen[0] = f.s.K;
+    p.klen[1] = parts > 1 ? f.s.K : 0;
+    p.kb_first = static_cast<int>(cdiv(f.s.K, bk));
+    p.kb_all = k_blocks(f.s, plan.pair);
     p.a_mn = f.a_mn;
     p.b_mn = f.s.b_mn;
+    // a third dimension of groups of 64 would reach past the row's end otherwise
+    p.a_3d = !gated && (f.a_mn ? p.I : f.s.K) % 64 == 0;
+    p.b_3d = (f.s.b_mn ? p.J : f.s.K) % 64 == 0;
     p.jt = c.jt;
-    p.i_tiles = static_cast<int>(i_tiles(f.s, plan.pair));
+    p.i_tiles = static_cast<int>(i_tiles(f.s, plan.pair, gated));
     p.j_tiles = static_cast<int>(cdiv(f.s.J, c.jt));
     p.splits = c.splits;
     p.kb_split = c.kb_split;
@@ -240,19 +256,20 @@ cce_status run_products(const Product* in, int n, bool gated, bool bf16, void* p
     p.part = reinterpret_cast<float*>(at);
     at += part_bytes(f.s, c, gated);
     p.e = f.e;
-    const uint32_t b_box = static_cast<uint32_t>(plan.pair ? c.jt / 2 : c.jt);
-    for (int m = 0; m < f.parts; ++m) {
-      const int k = f.klen[gated ? 0 : m];
-      bool ok = f.a_mn ? encode_operand(&p.a[m], bf16, f.a[m].p, p.I, k, f.a[m].pitch, 64, LIN_BK)
-                       : encode_operand(&p.a[m], bf16, f.a[m].p, k, p.I, f.a[m].pitch, LIN_BK, LIN_BI);
-      if (!gated || m == 0)
-        ok = ok && (f.s.b_mn ? encode_operand(&p.b[m], bf16, f.b[m].p, p.J, k, f.b[m].pitch, 64, LIN_BK)
-                             : encode_operand(&p.b[m], bf16, f.b[m].p, k, p.J, f.b[m].pitch, LIN_BK, b_box));
-      if (!ok) return CCE_ERR_CUDA;
+    const int b_rows = plan.pair ? c.jt / 2 : c.jt;
+    widest = std::max(widest, b_rows);
+    for (int m = 0; m < (gated ? 2 : parts); ++m) {
+      if (!encode(&p.a[m], bf16, f.a[m], f.s.K, p.I, f.a_mn, p.a_3d, bk, gated ? LIN_BI / 2 : LIN_BI))
+        return CCE_ERR_CUDA;
+    }
+    for (int m = 0; m < parts; ++m) {
+      if (!encode(&p.b[m], bf16, f.b[m], f.s.K, p.J, f.s.b_mn, p.b_3d, bk, b_rows)) return CCE_ERR_CUDA;
     }
   }
   if (items >= LIMIT) return CCE_ERR_SHAPE;
   a.items = static_cast<int>(items);
+  a.stage_bytes = (LIN_BI + widest) * static_cast<int>(bk) * 2;
+  a.stages = std::min(LIN_MAX_STAGES, LIN_RING_BYTES / a.stage_bytes);
   const int units = static_cast<int>(std::min<int64_t>(plan.pair ? pairs : sms, items));
   cudaError_t e = launch_linear_gemm(a, plan.pair, gated, units, s);
   ++*launches;
@@ -317,11 +334,7 @@ cce_status forward(const Matrix& x, const Matrix* w, bool gated, int64_t M, int6
   } else {
     Product p{};
     p.s = shape_of(N, M, K, 1, false);
-    p.parts = gated ? 2 : 1;
-    for (int m = 0; m < p.parts; ++m) {
-      p.a[m] = Operand{w[m].p, w[m].pitch};
-      p.klen[m] = static_cast<int>(K);
-    }
+    for (int m = 0; m < (gated ? 2 : 1); ++m) p.a[m] = Operand{w[m].p, w[m].pitch};
     p.b[0] = Operand{x.p, x.pitch};
     p.e = e;
     st = run_products(&p, 1, gated, bf16, ws, sms, pairs, stream, &launches);
@@ -383,20 +396,16 @@ cce_status backward_products(const Operand* dz, const Matrix& x, const Matrix* w
   for (int m = 0; m < mats; ++m) {
     if (!grad_w[m]) continue;
     p[n].s = b.dw;
-    p[n].parts = 1;
     p[n].a[0] = Operand{x.p, x.pitch};
     p[n].b[0] = dz[m];
     p[n].a_mn = true;
-    p[n].klen[0] = static_cast<int>(M);
     p[n++].e = dense_out(grad_w[m], K, type);
   }
   if (grad_x) {
     p[n].s = b.dx;
-    p[n].parts = mats;
     for (int m = 0; m < mats; ++m) {
       p[n].a[m] = Operand{w[m].p, w[m].pitch};
       p[n].b[m] = dz[m];
-      p[n].klen[m] = static_cast<int>(N);
     }
     p[n].a_mn = true;
     p[n++].e = dense_out(grad_x, K, type);

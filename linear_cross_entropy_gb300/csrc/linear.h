@@ -27,14 +27,18 @@ struct LinEpilogue {
 // out[j][i] = epilogue(sum over k of A(i, k) B(j, k)).  The sum may run over two
 // pairs of operands in turn (dx of a gated layer); gated forward: a[0] and a[1]
 // are the gate's and the up projection's weights, both against b[0].
+// Tensor maps: an operand whose contiguous extent is a multiple of 64 comes in one
+// 3-D box a stage (its groups of 64 as the third dimension), another in 2-D boxes,
+// one a group.
 struct LinProblem {
   CUtensorMap a[2];
   CUtensorMap b[2];
   int I, J;
   int klen[2];   // elements of either part of the sum (klen[1] = 0: one part)
-  int kb_first;  // 64-deep blocks of the first part
+  int kb_first;  // blocks of K of the first part
   int kb_all;
-  int a_mn, b_mn;  // operand stored with its I (J) index contiguous
+  int8_t a_mn, b_mn;  // operand stored with its I (J) index contiguous
+  int8_t a_3d, b_3d;
   int jt;          // tile width in J
   int i_tiles, j_tiles, splits, kb_split;  // kb_split: blocks of K per split
   int group;       // i tiles that are walked together
@@ -49,10 +53,14 @@ struct LinArgs {
   int problems;
   int items;
   int bf16;  // operands are bf16, else fp16
+  int stages, stage_bytes;
 };
 
-constexpr int LIN_BI = 128;  // rows of the MMA a CTA: I extent of a tile
-constexpr int LIN_BK = 64;
+constexpr int LIN_BI = 128;  // rows of the MMA a CTA: I extent of a tile (gated: 64 of each weight)
+// Blocks of K: a stage's depth.  A pair's loads are issued half as often with the deeper one.
+constexpr int lin_bk(bool pair) { return pair ? 128 : 64; }
+constexpr int LIN_RING_BYTES = 192 * 1024;
+constexpr int LIN_MAX_STAGES = 10;
 
 // The launch as `units` persistent CTAs or CTA pairs.
 cudaError_t launch_linear_gemm(const LinArgs& a, bool pair, bool gated, int units, cudaStream_t s);

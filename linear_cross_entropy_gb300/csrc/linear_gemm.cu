@@ -12,15 +12,17 @@
 //   dx = dz W        A = W  [N, K] along i = K   B = dz [M, N] along k = N
 //   dW = dz^T x      A = x  [M, K] along i = K   B = dz [M, N] along j = N
 //
-// Up to three products run in one launch (dx and both dW of a gated layer).  A
-// gated forward has two accumulators a tile, gate and up, whose A tiles share
-// the B tile; dx of a gated layer runs one sum over two pairs of operands.
+// Up to three products run in one launch (dx and both dW of a gated layer); dx of a
+// gated layer is one sum over two pairs of operands.  A gated forward's 128 MMA
+// rows are 64 of each weight, so that its loads and MMAs are those of a layer twice
+// as wide; the warps that hold a gate's rows and those with the up projection's
+// exchange half of their values in shared memory.
 //
-// Roles (320 threads): warp 0 lane 0 loads (TMA, 64-deep stages, as many as fit in
-// 192 KiB), warp 1 lane 0 issues tcgen05.mma into one of two TMEM accumulators, warps 2
-// to 9 are the epilogue (warp w reads TMEM lanes 32 (w % 4) to + 31, and every
-// second 32 columns).  CTA pairs share an MMA of M = 256: each CTA holds 128 rows
-// of A and half of B's columns.
+// Roles (576 threads): warp 0 lane 0 loads (TMA; a pair's stages are 128 deep in K, a
+// single CTA's 64, as many as fit in 192 KiB), warp 1 lane 0 issues tcgen05.mma into
+// one of two TMEM accumulators, the other 16 warps are the epilogue (warp w reads TMEM
+// lanes 32 (w % 4) to + 31, and every fourth 16 columns).  CTA pairs share an MMA of
+// M = 256: each CTA holds 128 rows of A and half of B's columns.
 //
 // Bound by the tensor cores for many rows, and by reading the weights for few.
 #include "gemm_args.h"
@@ -32,40 +34,51 @@
 namespace cce {
 namespace {
 
-constexpr int EPI_WARPS = 8;
+constexpr int EPI_WARPS = 16;
+constexpr int PHASES = EPI_WARPS / 4;  // warps that share the columns of 32 TMEM lanes
 constexpr int THREADS = 64 + 32 * EPI_WARPS;
 constexpr int ACC_COLS = 256;  // TMEM columns of one of the two accumulators
-constexpr int RING_BYTES = 192 * 1024;
-constexpr int MAX_RING = 12;
-constexpr int A_BYTES = LIN_BI * LIN_BK * 2;  // one A tile of a stage
-constexpr int SMEM = 1024 + RING_BYTES + 512;
+constexpr int CHUNK = 16;      // columns that a warp reads at a time
+constexpr int HALF = CHUNK / 2;  // and finishes: 96 registers a thread hold no more
+constexpr int GROUP = 64 * 128;  // bytes of 64 rows of 128 bytes
+// gated: what a warp hands over, twice
+constexpr int SWAP_BYTES = 2 * HALF * 32 * 4;
+constexpr int BAR_BYTES_LIN = 512;
+
+template <bool GATED>
+constexpr int shared_bytes() {
+  return 1024 + LIN_RING_BYTES + BAR_BYTES_LIN + (GATED ? EPI_WARPS * SWAP_BYTES : 0);
+}
+static_assert(shared_bytes<true>() <= 227 * 1024, "shared memory of a CTA");
 
 __device__ int32_t linear_error;  // CCE_DEVERR_* of waits that ran out
 
 struct Shared {
   uint8_t* ring;
-  uint64_t* full;       // [MAX_RING]
-  uint64_t* empty;      // [MAX_RING]
+  uint64_t* full;       // [LIN_MAX_STAGES]
+  uint64_t* empty;      // [LIN_MAX_STAGES]
   uint64_t* acc_full;   // [2]
   uint64_t* acc_empty;  // [2]
   uint64_t* drain;
   uint32_t* tmem;
   int* abort_flag;
+  float* swap;  // gated: [EPI_WARPS][2][HALF][32]
 };
 
 __device__ __forceinline__ Shared carve(uint8_t* raw) {
   Shared s;
   s.ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  s.full = reinterpret_cast<uint64_t*>(s.ring + RING_BYTES);
-  s.empty = s.full + MAX_RING;
-  s.acc_full = s.empty + MAX_RING;
+  s.full = reinterpret_cast<uint64_t*>(s.ring + LIN_RING_BYTES);
+  s.empty = s.full + LIN_MAX_STAGES;
+  s.acc_full = s.empty + LIN_MAX_STAGES;
   s.acc_empty = s.acc_full + 2;
   s.drain = s.acc_empty + 2;
   s.tmem = reinterpret_cast<uint32_t*>(s.drain + 1);
   s.abort_flag = reinterpret_cast<int*>(s.tmem + 1);
+  s.swap = reinterpret_cast<float*>(s.ring + LIN_RING_BYTES + BAR_BYTES_LIN);
   return s;
 }
-static_assert(8 * (2 * MAX_RING + 5) + 8 <= 512, "barriers fit");
+static_assert(8 * (2 * LIN_MAX_STAGES + 5) + 8 <= BAR_BYTES_LIN, "barriers fit");
 
 struct Tile {
   const LinProblem* p;
@@ -95,36 +108,55 @@ __device__ __forceinline__ Tile tile_of(const LinArgs& a, int item) {
   return t;
 }
 
-// Bytes of a CTA's B tile in a stage, and of a stage.
+// A box to `to`, whose bytes are counted on the stage's barrier (of a pair: the even CTA's).
 template <bool PAIR>
-__device__ __forceinline__ int b_rows(const LinProblem& p) {
-  return PAIR ? p.jt / 2 : p.jt;
-}
+struct Loader {
+  uint64_t* bar;
+  uint32_t lead;  // the barrier's cluster address
 
-template <bool PAIR, bool GATED>
-struct Ring {
-  // of the widest tile
-  static constexpr int kBytes = (GATED ? 2 : 1) * A_BYTES + (GATED ? 128 : 256) / (PAIR ? 2 : 1) * LIN_BK * 2;
-  static constexpr int kStages = RING_BYTES / kBytes < MAX_RING ? RING_BYTES / kBytes : MAX_RING;
-};
-
-template <bool PAIR>
-__device__ __forceinline__ void load_box(const CUtensorMap* m, uint64_t* bar, uint32_t lead, uint8_t* to, int x, int y) {
-  if constexpr (PAIR) {
-    tma_load_2d_pair(m, lead, to, x, y);
-  } else {
-    tma_load_2d(m, bar, to, x, y);
+  __device__ __forceinline__ void box2(const CUtensorMap* m, uint8_t* to, int x, int y) const {
+    if constexpr (PAIR) {
+      tma_load_2d_pair(m, lead, to, x, y);
+    } else {
+      tma_load_2d(m, bar, to, x, y);
+    }
   }
-}
+  __device__ __forceinline__ void box3(const CUtensorMap* m, uint8_t* to, int x, int y, int z) const {
+    if constexpr (PAIR) {
+      tma_load_3d_pair(m, lead, to, x, y, z);
+    } else {
+      tma_load_3d(m, bar, to, x, y, z);
+    }
+  }
+  // `rows` rows from r0 on of an operand, the block of K at k0.  Along k: 64 of k are
+  // `pitch` bytes apart; along its own index: 64 of them.
+  __device__ __forceinline__ void operand(const CUtensorMap* m, bool mn, bool whole, uint8_t* to, int r0, int rows,
+                                          int k0, int pitch) const {
+    constexpr int BK = lin_bk(PAIR);
+    if (mn) {
+      if (whole) {
+        box3(m, to, 0, k0, r0 >> 6);
+      } else {
+        for (int r = 0; r < rows; r += 64) box2(m, to + r * 2 * BK, r0 + r, k0);
+      }
+    } else if (whole) {
+      box3(m, to, 0, r0, k0 >> 6);
+    } else {
+#pragma unroll
+      for (int k = 0; k < BK; k += 64) box2(m, to + (k >> 6) * pitch, k0 + k, r0);
+    }
+  }
+};
 
 template <bool PAIR, bool GATED>
 __device__ __forceinline__ void load_loop(const LinArgs& a, const Shared& s) {
-  using R = Ring<PAIR, GATED>;
+  constexpr int BK = lin_bk(PAIR), A_BYTES = LIN_BI * BK * 2;
   volatile int* abort_flag = s.abort_flag;
   const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
   const int unit = PAIR ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
   const int units = PAIR ? static_cast<int>(cluster_count_x()) : static_cast<int>(gridDim.x);
   const uint32_t lead = PAIR ? mapa_shared(smem_u32(s.full), 0) : 0u;
+  const int stages = a.stages, stage_bytes = a.stage_bytes;
   int stage = 0;
   uint32_t phase = 0;
   uint32_t issued = 0, issued_par = 0;  // per stage: ever issued, parity of its last phase
@@ -132,41 +164,31 @@ __device__ __forceinline__ void load_loop(const LinArgs& a, const Shared& s) {
   for (int item = unit; ok && item < a.items; item += units) {
     const Tile t = tile_of(a, item);
     const LinProblem& p = *t.p;
-    const int rows = b_rows<PAIR>(p);
-    const int i0 = t.it * (PAIR ? 2 * LIN_BI : LIN_BI) + rank * LIN_BI;
+    const bool a_mn = p.a_mn, b_mn = p.b_mn, a_3d = p.a_3d, b_3d = p.b_3d;
+    const int rows = PAIR ? p.jt / 2 : p.jt;
+    const int i0 = (t.it * (PAIR ? 2 : 1) + rank) * (GATED ? LIN_BI / 2 : LIN_BI);
     const int j0 = t.jt * p.jt + rank * rows;
-    const uint32_t bytes = static_cast<uint32_t>(((GATED ? 2 : 1) * A_BYTES + rows * LIN_BK * 2) * (PAIR ? 2 : 1));
+    const uint32_t bytes = static_cast<uint32_t>((A_BYTES + rows * BK * 2) * (PAIR ? 2 : 1));
     for (int kb = t.kb; kb < t.kb_end; ++kb) {
       if (!wait_bounded(&s.empty[stage], phase ^ 1u, abort_flag, &linear_error)) {
         ok = false;
         break;
       }
-      uint64_t* bar = &s.full[stage];
-      const uint32_t bar_lead = lead + 8u * static_cast<uint32_t>(stage);
-      uint8_t* to = s.ring + stage * R::kBytes;
-      const int part = kb >= p.kb_first ? 1 : 0;
-      const int k0 = (part ? kb - p.kb_first : kb) * LIN_BK;
-      if (rank == 0) mbar_arrive_expect_tx(bar, bytes);
-#pragma unroll
-      for (int g = 0; g < (GATED ? 2 : 1); ++g) {
-        const CUtensorMap* m = &p.a[GATED ? g : part];
-        if (p.a_mn) {  // two groups of 64 i, one row of 128 bytes for each k
-          load_box<PAIR>(m, bar, bar_lead, to, i0, k0);
-          load_box<PAIR>(m, bar, bar_lead, to + A_BYTES / 2, i0 + 64, k0);
-        } else {
-          load_box<PAIR>(m, bar, bar_lead, to, k0, i0);
-        }
-        to += A_BYTES;
-      }
-      const CUtensorMap* m = &p.b[part];
-      if (p.b_mn) {
-        for (int r = 0; r < rows; r += 64) load_box<PAIR>(m, bar, bar_lead, to + r * LIN_BK * 2, j0 + r, k0);
+      const Loader<PAIR> load{&s.full[stage], lead + 8u * static_cast<uint32_t>(stage)};
+      uint8_t* to = s.ring + stage * stage_bytes;
+      if (rank == 0) mbar_arrive_expect_tx(&s.full[stage], bytes);
+      const int part = !GATED && kb >= p.kb_first ? 1 : 0;
+      const int k0 = (part ? kb - p.kb_first : kb) * BK;
+      if constexpr (GATED) {
+        load.operand(&p.a[0], false, false, to, i0, 64, k0, 2 * GROUP);
+        load.operand(&p.a[1], false, false, to + GROUP, i0, 64, k0, 2 * GROUP);
       } else {
-        load_box<PAIR>(m, bar, bar_lead, to, k0, j0);
+        load.operand(&p.a[part], a_mn, a_3d, to, i0, LIN_BI, k0, 2 * GROUP);
       }
+      load.operand(&p.b[part], b_mn, b_3d, to + A_BYTES, j0, rows, k0, rows * 128);
       issued |= 1u << stage;
       issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
-      if (++stage == R::kStages) {
+      if (++stage == stages) {
         stage = 0;
         phase ^= 1u;
       }
@@ -179,7 +201,7 @@ __device__ __forceinline__ void load_loop(const LinArgs& a, const Shared& s) {
     while (globaltimer() - t0 < 10000000ull) {
     }
   } else {
-    for (int i = 0; i < R::kStages; ++i) {
+    for (int i = 0; i < stages; ++i) {
       if (issued & (1u << i)) {
         volatile int none = 0;
         wait_bounded(&s.full[i], (issued_par >> i) & 1u, &none, nullptr);
@@ -188,13 +210,14 @@ __device__ __forceinline__ void load_loop(const LinArgs& a, const Shared& s) {
   }
 }
 
-template <bool PAIR, bool GATED>
+template <bool PAIR>
 __device__ __forceinline__ void mma_loop(const LinArgs& a, const Shared& s, uint32_t tmem) {
   if (PAIR && cluster_ctarank() != 0) return;  // the even CTA issues for both
-  using R = Ring<PAIR, GATED>;
+  constexpr int BK = lin_bk(PAIR), A_BYTES = LIN_BI * BK * 2;
   volatile int* abort_flag = s.abort_flag;
   const int unit = PAIR ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
   const int units = PAIR ? static_cast<int>(cluster_count_x()) : static_cast<int>(gridDim.x);
+  const int stages = a.stages, stage_bytes = a.stage_bytes;
   int stage = 0, acc = 0;
   uint32_t phase = 0, acc_phase = 0;
   bool any = false, ok = true;
@@ -204,10 +227,12 @@ __device__ __forceinline__ void mma_loop(const LinArgs& a, const Shared& s, uint
     const bool a_mn = p.a_mn, b_mn = p.b_mn;
     // bits 7-9 and 10-12 of the descriptor: 1 = bf16, 0 = fp16
     const uint32_t idesc = idesc_bf16(PAIR ? 2 * LIN_BI : LIN_BI, p.jt, a_mn, b_mn) & (a.bf16 ? ~0u : ~((1u << 7) | (1u << 10)));
-    // along its own index: 64-element groups of 64 rows of 128 bytes, 16 of k are 16 rows; along
-    // k: 16 of k are 32 bytes of a row
-    const uint32_t a_lbo = a_mn ? LIN_BK * 128u : 16u, b_lbo = b_mn ? LIN_BK * 128u : 16u;
-    const uint64_t a_step = a_mn ? 2048u >> 4 : 32u >> 4, b_step = b_mn ? 2048u >> 4 : 32u >> 4;
+    // along its own index: 64-element groups of BK rows of 128 bytes, 16 of k are 16 rows; along
+    // k: 16 of k are 32 bytes of a row, 64 of k all rows
+    const uint32_t a_lbo = a_mn ? BK * 128u : 16u, b_lbo = b_mn ? BK * 128u : 16u;
+    const uint32_t a_step = (a_mn ? 2048u : 32u) >> 4, b_step = (b_mn ? 2048u : 32u) >> 4;
+    const uint32_t a_next = (a_mn ? 8192u : 2u * GROUP) >> 4;
+    const uint32_t b_next = (b_mn ? 8192u : (PAIR ? p.jt / 2 : p.jt) * 128u) >> 4;
     if (!wait_bounded(&s.acc_empty[acc], acc_phase ^ 1u, abort_flag, &linear_error)) break;
     tc_fence_after();
     const uint32_t d = tmem + static_cast<uint32_t>(acc * ACC_COLS);
@@ -219,24 +244,23 @@ __device__ __forceinline__ void mma_loop(const LinArgs& a, const Shared& s, uint
       }
       tc_fence_after();
       const int part = kb >= p.kb_first ? 1 : 0;
-      const int left = p.klen[part] - (part ? kb - p.kb_first : kb) * LIN_BK;
-      const int steps = left >= LIN_BK ? LIN_BK / 16 : (left + 15) / 16;  // behind K's end there are zeros
-      const uint32_t at = smem_u32(s.ring + stage * R::kBytes);
-      const uint64_t b_desc = smem_desc_sw128(at + (GATED ? 2 : 1) * A_BYTES, b_lbo, 1024u);
-#pragma unroll
-      for (int g = 0; g < (GATED ? 2 : 1); ++g) {
-        const uint64_t a_desc = smem_desc_sw128(at + g * A_BYTES, a_lbo, 1024u);
-        const uint32_t to = d + static_cast<uint32_t>(g * ACC_COLS / 2);
-#pragma unroll
-        for (int k = 0; k < LIN_BK / 16; ++k) {
-          if (k < steps) {
-            if constexpr (PAIR) {
-              mma_bf16_pair(to, a_desc + a_step * k, b_desc + b_step * k, idesc, accumulate | (k > 0));
-            } else {
-              mma_bf16(to, a_desc + a_step * k, b_desc + b_step * k, idesc, accumulate | (k > 0));
-            }
-          }
+      const int left = p.klen[part] - (part ? kb - p.kb_first : kb) * BK;
+      const uint32_t at = smem_u32(s.ring + stage * stage_bytes);
+      const uint64_t a_desc = smem_desc_sw128(at, a_lbo, 1024u);
+      const uint64_t b_desc = smem_desc_sw128(at + A_BYTES, b_lbo, 1024u);
+      const auto mma = [&](int k) {
+        const uint64_t ad = a_desc + (k >> 2) * a_next + (k & 3) * a_step, bd = b_desc + (k >> 2) * b_next + (k & 3) * b_step;
+        if constexpr (PAIR) {
+          mma_bf16_pair(d, ad, bd, idesc, accumulate | (k > 0));
+        } else {
+          mma_bf16(d, ad, bd, idesc, accumulate | (k > 0));
         }
+      };
+      if (left >= BK) {
+#pragma unroll
+        for (int k = 0; k < BK / 16; ++k) mma(k);
+      } else {
+        for (int k = 0; 16 * k < left; ++k) mma(k);  // behind K's end there are zeros
       }
       accumulate = 1;
       any = true;
@@ -245,7 +269,7 @@ __device__ __forceinline__ void mma_loop(const LinArgs& a, const Shared& s, uint
       } else {
         mma_commit(&s.empty[stage]);
       }
-      if (++stage == R::kStages) {
+      if (++stage == stages) {
         stage = 0;
         phase ^= 1u;
       }
@@ -270,60 +294,95 @@ __device__ __forceinline__ void mma_loop(const LinArgs& a, const Shared& s, uint
   }
 }
 
+// Of two warps.
+__device__ __forceinline__ void meet(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool both(int id, bool mine) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, %2, 64, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(static_cast<uint32_t>(mine)), "r"(id)
+      : "memory");
+  return all != 0;
+}
+
 template <bool PAIR, bool GATED>
 __device__ __forceinline__ void epilogue_loop(const LinArgs& a, const Shared& s, uint32_t tmem, int warp) {
   const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
   const int unit = PAIR ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
   const int units = PAIR ? static_cast<int>(cluster_count_x()) : static_cast<int>(gridDim.x);
-  const int quarter = warp & 3, half = (warp - 2) >> 2;
+  const int lane = static_cast<int>(lane_id());
+  const int quarter = warp & 3, phase_of = (warp - 2) >> 2;
+  // gated: lanes 0 to 63 are the gate's rows, the others the up projection's
+  const int up = GATED ? quarter >> 1 : 0;
+  const int lanes = GATED ? (quarter & 1) * 32 : quarter * 32;
+  // a warp's buffer, and that of the one with the same rows of the other weight
+  float* const mine = s.swap + ((quarter * PHASES) + phase_of) * (SWAP_BYTES / 4) + lane;
+  float* const other = s.swap + (((quarter ^ 2) * PHASES) + phase_of) * (SWAP_BYTES / 4) + lane;
+  const int barrier = 1 + (quarter & 1) * PHASES + phase_of;
   const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
   const uint32_t release = PAIR ? mapa_shared(smem_u32(s.acc_empty), 0) : smem_u32(s.acc_empty);
-  int acc = 0;
+  int acc = 0, flip = 0;
   uint32_t acc_phase = 0;
   for (int item = unit; item < a.items; item += units) {
     const Tile t = tile_of(a, item);
     const LinProblem& p = *t.p;
-    const int i = t.it * (PAIR ? 2 * LIN_BI : LIN_BI) + rank * LIN_BI + quarter * 32 + static_cast<int>(lane_id());
+    const int i = (t.it * (PAIR ? 2 : 1) + rank) * (GATED ? LIN_BI / 2 : LIN_BI) + lanes + lane;
     const bool inside = i < p.I;
     const float bias = p.e.bias && p.splits == 1 && inside ? load_scalar(p.e.bias, p.e.bias_type, i) : 0.0f;
-    if (!warp_wait_bounded(&s.acc_full[acc], acc_phase, s.abort_flag, &linear_error)) break;
+    bool ok = warp_wait_bounded(&s.acc_full[acc], acc_phase, s.abort_flag, &linear_error);
+    if constexpr (GATED) ok = both(barrier, ok);  // where a wait ran out, neither waits for the other any more
+    if (!ok) break;
     tc_fence_after();
     const uint32_t from = lane_base + static_cast<uint32_t>(acc * ACC_COLS);
-    for (int c = half; c < p.jt / 32; c += 2) {
-      const int j0 = t.jt * p.jt + 32 * c;
-      const int n = min(32, p.J - j0);
-      if (n <= 0) break;  // the same in all lanes
-      uint32_t r0[32], r1[32];
+    for (int c = phase_of; c < p.jt / CHUNK; c += PHASES) {
+      const int j0 = t.jt * p.jt + CHUNK * c;
+      const int n = min(CHUNK, p.J - j0);
+      if (n <= 0) break;  // the same in all lanes, and in both warps of a gated exchange
+      uint32_t r[CHUNK];
       __syncwarp();  // the lanes outside of the matrix are back
-      tmem_ld32(from + 32 * c, r0);
-      if constexpr (GATED) tmem_ld32(from + ACC_COLS / 2 + 32 * c, r1);
+      tmem_ld16(from + CHUNK * c, r);
       tmem_ld_wait();
-      if (!inside) continue;
       if (p.splits > 1) {  // a partial sum
-        float* to = p.part + (static_cast<int64_t>(t.split * (GATED ? 2 : 1)) * p.J + j0) * p.I + i;
+        if (!inside) continue;
+        float* to = p.part + (static_cast<int64_t>(t.split * (GATED ? 2 : 1) + up) * p.J + j0) * p.I + i;
 #pragma unroll
-        for (int u = 0; u < 32; ++u) {
-          if (u < n) {
-            to[static_cast<int64_t>(u) * p.I] = __uint_as_float(r0[u]);
-            if constexpr (GATED) to[(static_cast<int64_t>(p.J) + u) * p.I] = __uint_as_float(r1[u]);
-          }
+        for (int u = 0; u < CHUNK; ++u, to += p.I) {
+          if (u < n) *to = __uint_as_float(r[u]);
         }
-      } else {
+      } else if constexpr (GATED) {
+        // the gate's warp finishes the first half of the columns, the other the second
+        float* const give = mine + flip * HALF * 32;
+        const float* const take = other + flip * HALF * 32;
 #pragma unroll
-        for (int h = 0; h < 32; h += 16) {  // in two halves: a whole column with its residual spills
-          float z0[16], z1[16];
+        for (int u = 0; u < HALF; ++u) give[u * 32] = __uint_as_float(up ? r[u] : r[HALF + u]);
+        meet(barrier);
+        float z0[HALF], z1[HALF];
 #pragma unroll
-          for (int u = 0; u < 16; ++u) {
-            z0[u] = __uint_as_float(r0[h + u]);
-            if constexpr (GATED) z1[u] = __uint_as_float(r1[h + u]);
-          }
-          if (h < n) finish_column<GATED>(p.e, a.bf16, bias, i, j0 + h, n - h, z0, z1);
+        for (int u = 0; u < HALF; ++u) {
+          const float own = __uint_as_float(up ? r[HALF + u] : r[u]), got = take[u * 32];
+          z0[u] = up ? got : own;
+          z1[u] = up ? own : got;
+        }
+        flip ^= 1;  // the other warp has read this buffer before it meets the next barrier
+        const int left = n - up * HALF;
+        if (inside && left > 0) finish_column<true>(p.e, a.bf16, 0.0f, i, j0 + up * HALF, left, z0, z1);
+      } else if (inside) {
+#pragma unroll
+        for (int h = 0; h < CHUNK; h += HALF) {
+          float z[HALF];
+#pragma unroll
+          for (int u = 0; u < HALF; ++u) z[u] = __uint_as_float(r[h + u]);
+          if (h < n) finish_column<false>(p.e, a.bf16, bias, i, j0 + h, n - h, z, z);
         }
       }
     }
     tc_fence_before();
     __syncwarp();
-    if (lane_id() == 0) {
+    if (lane == 0) {
       if constexpr (PAIR) {
         mbar_arrive_cluster(release + 8u * static_cast<uint32_t>(acc));
       } else {
@@ -342,7 +401,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
   const int warp = static_cast<int>(threadIdx.x >> 5);
   let_next_start();
   if (threadIdx.x == 0) {
-    for (int i = 0; i < Ring<PAIR, GATED>::kStages; ++i) {
+    for (int i = 0; i < a.stages; ++i) {
       mbar_init(&s.full[i], 1);
       mbar_init(&s.empty[i], 1);
     }
@@ -373,7 +432,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
   if (warp == 0) {
     if (lane_id() == 0) load_loop<PAIR, GATED>(a, s);
   } else if (warp == 1) {
-    if (lane_id() == 0) mma_loop<PAIR, GATED>(a, s, tmem);
+    if (lane_id() == 0) mma_loop<PAIR>(a, s, tmem);
   } else {
     epilogue_loop<PAIR, GATED>(a, s, tmem, warp);
   }
@@ -393,7 +452,8 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
 
 template <bool PAIR, bool GATED>
 cudaError_t set_shared() {
-  return cudaFuncSetAttribute(linear_kernel<PAIR, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  return cudaFuncSetAttribute(linear_kernel<PAIR, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              shared_bytes<GATED>());
 }
 
 }  // namespace
@@ -415,11 +475,11 @@ int linear_pair_units(int sms) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(sms / 2 * 2));
   cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = SMEM;
+  cfg.dynamicSmemBytes = shared_bytes<true>();
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, linear_kernel<true, false>, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, linear_kernel<true, true>, &cfg) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
@@ -430,11 +490,11 @@ cudaError_t launch_linear_gemm(const LinArgs& a, bool pair, bool gated, int unit
   const dim3 grid(static_cast<unsigned>(pair ? 2 * units : units)), block(THREADS);
   const unsigned cluster = pair ? 2 : 1;
   if (pair) {
-    return gated ? launch_after(linear_kernel<true, true>, grid, block, SMEM, cluster, s, a)
-                 : launch_after(linear_kernel<true, false>, grid, block, SMEM, cluster, s, a);
+    return gated ? launch_after(linear_kernel<true, true>, grid, block, shared_bytes<true>(), cluster, s, a)
+                 : launch_after(linear_kernel<true, false>, grid, block, shared_bytes<false>(), cluster, s, a);
   }
-  return gated ? launch_after(linear_kernel<false, true>, grid, block, SMEM, cluster, s, a)
-               : launch_after(linear_kernel<false, false>, grid, block, SMEM, cluster, s, a);
+  return gated ? launch_after(linear_kernel<false, true>, grid, block, shared_bytes<true>(), cluster, s, a)
+               : launch_after(linear_kernel<false, false>, grid, block, shared_bytes<false>(), cluster, s, a);
 }
 
 cudaError_t take_linear_error(int32_t* word, cudaStream_t s) {

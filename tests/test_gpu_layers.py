@@ -401,3 +401,21 @@ def test_refusals(cce):
     for call, match in refused:
         with pytest.raises(ValueError, match=match):
             call()
+
+
+def test_backward_without_an_activation_on_a_fresh_thread(cce):
+    """Nothing runs on the autograd engine's thread before the products' own launch."""
+    x = torch.randn(300, 64, device="cuda").bfloat16().requires_grad_()
+    w = torch.randn(72, 64, device="cuda").bfloat16()
+    g = torch.randn(300, 72, device="cuda").bfloat16()
+    import threading
+    got = []
+    y = cce.linear(x, w)
+
+    def run():
+        with torch.cuda.device(0):
+            got.append(torch.autograd.grad(y, x, g)[0])
+    t = threading.Thread(target=run)
+    t.start()
+    t.join()
+    assert torch.equal(got[0], cce.cce_linear_backward(g, x, w)[0])
