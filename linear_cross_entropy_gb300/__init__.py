@@ -38,6 +38,7 @@ __all__ = [
     "linear", "gated_linear", "cce_linear_forward", "cce_linear_backward", "cce_gated_linear_forward",
     "cce_gated_linear_backward", "linear_forward_workspace_bytes", "linear_backward_workspace_bytes",
     "gated_linear_forward_workspace_bytes", "gated_linear_backward_workspace_bytes",
+    "AdamW", "cce_adamw_step", "cce_adamw8_step", "adamw_scales",
 ]
 
 _lib.load()
@@ -50,6 +51,7 @@ from .layers import (cce_gated_linear_backward, cce_gated_linear_forward, cce_li
                      linear_forward_workspace_bytes)
 from .norm import (cce_layer_norm_backward, cce_layer_norm_forward, cce_rms_norm_backward,  # noqa: E402
                    cce_rms_norm_forward, layer_norm, norm_backward_workspace_bytes, rms_norm)
+from .optim import AdamW, adamw_scales, cce_adamw8_step, cce_adamw_step  # noqa: E402
 
 
 def _ptr(t):

@@ -56,6 +56,22 @@ class Strided(ctypes.Structure):
                 ("out_stride", ctypes.c_int64 * 4)]
 
 
+class AdamWTensor(ctypes.Structure):
+    """cce_adamw_tensor of include/cce_optim.h."""
+    _fields_ = [("grad", ctypes.c_void_p), ("param", ctypes.c_void_p), ("master", ctypes.c_void_p),
+                ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p), ("exp_avg_scale", ctypes.c_void_p),
+                ("rms_scale", ctypes.c_void_p), ("n", ctypes.c_int64), ("grad_type", ctypes.c_int32),
+                ("param_type", ctypes.c_int32), ("weight_decay", ctypes.c_float)]
+
+
+class AdamWOptions(ctypes.Structure):
+    """cce_adamw_options of include/cce_optim.h."""
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", ctypes.c_int64), ("step_ptr", ctypes.c_void_p),
+                ("lr_ptr", ctypes.c_void_p), ("norm", ctypes.c_void_p), ("max_norm", ctypes.c_float),
+                ("eps_norm", ctypes.c_float), ("seed", ctypes.c_uint32)]
+
+
 _lib = None
 
 
@@ -182,6 +198,11 @@ def load() -> ctypes.CDLL:
         query = getattr(lib, f"cce_{name}_workspace_bytes")
         query.argtypes = [i64, i64, i64]
         query.restype = sz
+    # include/cce_optim.h
+    lib.cce_optim_abi_version.argtypes = []
+    lib.cce_optim_abi_version.restype = ci
+    lib.cce_adamw_step.argtypes = [ctypes.POINTER(AdamWTensor), i64, ci, ctypes.POINTER(AdamWOptions), vp]
+    lib.cce_adamw_step.restype = ci
     _lib = lib
     return lib
 

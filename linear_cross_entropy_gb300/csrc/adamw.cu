@@ -1,0 +1,555 @@
+// AdamW over many tensors in one launch, states in 32 or 8 bits (include/cce_optim.h).
+//
+// Bound by memory: each value is read once and written once (bf16 parameters and
+// gradients: 22 bytes a value with 32-bit states, 10 with 8-bit ones).  The tensors
+// are cut into chunks, which the blocks of a launch take in turn; the table of
+// tensors travels in the kernel's parameters (nothing to copy, nothing to keep alive
+// for a captured graph).  The clipping factor is applied on the way, so the
+// gradients need no pass of their own once their norm is known.
+//
+// 8 bits: a warp has a block of 256 values in its registers, eight a lane, so the
+// new scales are two warp maxima and nothing is read twice.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <new>
+
+#include "../../include/cce_optim.h"
+#include "elements.cuh"
+#include "internal.h"
+
+namespace cce {
+namespace {
+
+constexpr int THREADS = 256;
+constexpr int WARPS = THREADS / 32;
+constexpr int VEC = 8;                // values of a thread at a time
+constexpr int ROUND = THREADS * VEC;  // of a block
+constexpr int BLOCKS_PER_SM = 4;
+constexpr int MAX_TENSORS = 360;  // per launch: what 32 KB of parameters hold
+constexpr int FEW_TENSORS = 16;
+constexpr int64_t MAX_ELEMENTS = int64_t(1) << 35;  // of one tensor
+constexpr float E4M3_MAX = 448.0f, E4M3_MIN = 0x1p-9f, BLOCK_MIN = 0x1p-116f;
+static_assert(CCE_ADAMW_BLOCK == 32 * VEC, "a block is a warp's");
+
+struct Tensor {
+  const void* g;
+  void* p;
+  float* master;
+  void* m;
+  void* v;
+  float* ms;
+  float* rs;
+  int64_t n;
+  int64_t first_block;  // 8 bits: blocks of the call's tensors before this one
+  uint32_t first_chunk;
+  float decay;  // weight decay
+  int wide;     // whole vectors start on their size
+};
+
+template <int M>
+struct Batch {
+  Tensor t[M];
+  int count;
+  int chunk;  // elements
+  uint32_t chunks;
+};
+
+struct Rule {
+  float beta1, rest1, beta2, rest2, eps;  // rest: 1 - beta
+  float log1, log2;                       // natural logarithms of the betas
+  float lr;
+  float correct1, correct2;  // 1 - beta^t
+  const int64_t* step;       // may be null
+  const float* lr_ptr;       // may be null
+  const float* norm;         // may be null
+  float max_norm, eps_norm;
+  uint32_t seed, t;
+};
+static_assert(sizeof(Batch<MAX_TENSORS>) + sizeof(Rule) <= 32764, "kernel parameters");
+
+template <int M>
+__device__ __forceinline__ int find_tensor(const Batch<M>& b, uint32_t chunk) {
+  int lo = 0, hi = b.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (b.t[mid].first_chunk <= chunk) {
+      lo = mid;
+    } else {
+      hi = mid - 1;
+    }
+  }
+  return lo;
+}
+
+__host__ __device__ inline uint32_t mix(uint32_t x) {
+  x ^= x >> 16;
+  x *= 0x85ebca6bu;
+  x ^= x >> 13;
+  x *= 0xc2b2ae35u;
+  return x ^ (x >> 16);
+}
+
+// What an update needs beside its values; the same in all threads.
+struct Now {
+  float factor;    // of the gradients
+  float lr;
+  float size;      // lr / (1 - beta1^t)
+  float inv_root;  // 1 / sqrt(1 - beta2^t)
+  uint32_t key;
+};
+
+__device__ __forceinline__ Now now_of(const Rule& r) {
+  Now n;
+  n.factor = 1.0f;
+  if (r.norm) {  // as clipping does: NaN for a NaN norm, 1 where the quotient of infinities or zeros would be NaN
+    const float norm = *r.norm, f = r.max_norm / (norm + r.eps_norm);
+    n.factor = f < 1.0f || norm != norm ? f : 1.0f;
+  }
+  n.lr = r.lr_ptr ? *r.lr_ptr : r.lr;
+  float c1 = r.correct1, c2 = r.correct2;
+  uint32_t t = r.t;
+  if (r.step) {
+    const int64_t step = max(*r.step, static_cast<int64_t>(1));
+    t = static_cast<uint32_t>(step);
+    c1 = -expm1f(static_cast<float>(step) * r.log1);
+    c2 = -expm1f(static_cast<float>(step) * r.log2);
+  }
+  n.size = n.lr / c1;
+  n.inv_root = 1.0f / sqrtf(c2);
+  n.key = mix(mix(r.seed) ^ t);
+  return n;
+}
+
+// m and v become the new ones, w the new weight; returns sqrt(v).
+__device__ __forceinline__ float update(const Rule& r, const Now& now, float keep, float g, float& m, float& v,
+                                        float& w) {
+  g *= now.factor;
+  m = r.beta1 * m + r.rest1 * g;
+  v = r.beta2 * v + r.rest2 * g * g;
+  const float root = sqrtf(v);
+  w = w * keep - now.size * m / (root * now.inv_root + r.eps);
+  return root;
+}
+
+template <int N, typename P, typename G, bool MASTER>
+__device__ __forceinline__ void update_vector(const Rule& r, const Now& now, float keep, const Tensor& t, int64_t i) {
+  Vec<G, N> g;
+  Vec<P, N> p;
+  Vec<float, N> w, m, v;
+  g.load(static_cast<const G*>(t.g) + i);
+  if constexpr (MASTER) {
+    w.load(t.master + i);
+  } else {
+    p.load(static_cast<const P*>(t.p) + i);
+  }
+  m.load(static_cast<const float*>(t.m) + i);
+  v.load(static_cast<const float*>(t.v) + i);
+  float wf[N], mf[N], vf[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    if constexpr (MASTER) {
+      wf[e] = w.get(e);
+    } else {
+      wf[e] = p.get(e);
+    }
+    mf[e] = m.get(e);
+    vf[e] = v.get(e);
+    update(r, now, keep, g.get(e), mf[e], vf[e], wf[e]);
+  }
+  m.set(mf);
+  v.set(vf);
+  p.set(wf);
+  m.store(static_cast<float*>(t.m) + i);
+  v.store(static_cast<float*>(t.v) + i);
+  p.store(static_cast<P*>(t.p) + i);
+  if constexpr (MASTER) {
+    w.set(wf);
+    w.store(t.master + i);
+  }
+}
+
+template <int M, typename P, typename G, bool MASTER>
+__global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) adamw_kernel(const __grid_constant__ Batch<M> b,
+                                                                       const __grid_constant__ Rule r) {
+  let_next_start();
+  wait_for_previous();
+  const Now now = now_of(r);
+  for (uint32_t c = blockIdx.x; c < b.chunks; c += gridDim.x) {
+    const Tensor& t = b.t[find_tensor(b, c)];
+    const int64_t at = static_cast<int64_t>(c - t.first_chunk) * b.chunk;
+    const int64_t end = min(at + b.chunk, t.n);
+    const float keep = 1.0f - now.lr * t.decay;
+    int64_t from = at;
+    if (t.wide) {
+      const int64_t whole = at + (end - at) / VEC * VEC;
+      for (int64_t i = at + threadIdx.x * VEC; i < whole; i += ROUND)
+        update_vector<VEC, P, G, MASTER>(r, now, keep, t, i);
+      from = whole;
+    }
+    for (int64_t i = from + threadIdx.x; i < end; i += THREADS) update_vector<1, P, G, MASTER>(r, now, keep, t, i);
+  }
+}
+
+// -------------------------------------------------------------------- 8 bits
+__device__ __forceinline__ float2 from_e4m3(uint32_t two) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// Values that e4m3 holds (or NaN).
+__device__ __forceinline__ uint32_t to_e4m3(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// a in [0, 448] to floor(a / step + u) step, u in [0, 1); NaN stays NaN.
+__device__ __forceinline__ float round_e4m3(float a, uint32_t u16) {
+  // the step is 2^-3 of a's power of two, 2^-9 at least
+  const uint32_t power = max(__float_as_uint(a) >> 23, 121u);  // 2^-6
+  const float step = __uint_as_float((power - 3u) << 23), inv = __uint_as_float((257u - power) << 23);
+  // times a power of two is exact
+  const float q = floorf(__fadd_rn(a * inv, static_cast<float>(u16) * 0x1p-16f)) * step;
+  return q > E4M3_MAX ? E4M3_MAX : q;
+}
+
+// Larger of two magnitudes; NaN wins.
+__device__ __forceinline__ float larger(float a, float b) { return b > a || b != b ? b : a; }
+
+__device__ __forceinline__ float warp_larger(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = larger(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// The n values (n <= 256) of one block from element `at` of t on, by a warp.
+template <typename P, typename G, bool MASTER>
+__device__ __forceinline__ void update_block(const Rule& r, const Now& now, float keep, const Tensor& t, int64_t at,
+                                             int n) {
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  const int64_t block = at / CCE_ADAMW_BLOCK, i = at + lane * VEC;
+  const int mine = min(max(n - lane * VEC, 0), VEC);
+  const bool wide = t.wide && mine == VEC;
+  Vec<G, VEC> g;
+  Vec<P, VEC> p;
+  Vec<float, VEC> w;
+  uint32_t mq[2] = {0u, 0u}, rq[2] = {0u, 0u};
+  uint8_t* const m8 = static_cast<uint8_t*>(t.m) + i;
+  uint8_t* const r8 = static_cast<uint8_t*>(t.v) + i;
+  if (wide) {
+    g.load(static_cast<const G*>(t.g) + i);
+    if constexpr (MASTER) {
+      w.load(t.master + i);
+    } else {
+      p.load(static_cast<const P*>(t.p) + i);
+    }
+    const uint2 a = *reinterpret_cast<const uint2*>(m8), b = *reinterpret_cast<const uint2*>(r8);
+    mq[0] = a.x, mq[1] = a.y, rq[0] = b.x, rq[1] = b.y;
+  } else {
+    g.load_some(static_cast<const G*>(t.g) + i, 0, mine);
+    if constexpr (MASTER) {
+      w.load_some(t.master + i, 0, mine);
+    } else {
+      p.load_some(static_cast<const P*>(t.p) + i, 0, mine);
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      if (e < mine) {
+        mq[e / 4] |= static_cast<uint32_t>(m8[e]) << (8 * (e & 3));
+        rq[e / 4] |= static_cast<uint32_t>(r8[e]) << (8 * (e & 3));
+      }
+    }
+  }
+  const float ms = t.ms[block], rs = t.rs[block];
+  float mf[VEC], rf[VEC], wf[VEC], m_most = 0.0f, r_most = 0.0f;
+#pragma unroll
+  for (int e = 0; e < VEC; e += 2) {
+    const float2 a = from_e4m3(mq[e / 4] >> (8 * (e & 3))), b = from_e4m3(rq[e / 4] >> (8 * (e & 3)));
+    mf[e] = a.x * ms, mf[e + 1] = a.y * ms, rf[e] = b.x * rs, rf[e + 1] = b.y * rs;
+  }
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    if constexpr (MASTER) {
+      wf[e] = w.get(e);
+    } else {
+      wf[e] = p.get(e);
+    }
+    float v = rf[e] * rf[e];
+    rf[e] = update(r, now, keep, g.get(e), mf[e], v, wf[e]);
+    if (e < mine) {
+      m_most = larger(m_most, fabsf(mf[e]));
+      r_most = larger(r_most, rf[e]);
+    }
+  }
+  m_most = warp_larger(m_most);
+  r_most = warp_larger(r_most);
+  const bool m_none = m_most < BLOCK_MIN, r_none = r_most < BLOCK_MIN;
+  const float m_inv = m_none ? 0.0f : E4M3_MAX / m_most, r_inv = r_none ? 0.0f : E4M3_MAX / r_most;
+  const uint64_t place = static_cast<uint64_t>(t.first_block + block) * CCE_ADAMW_BLOCK + lane * VEC;
+  const uint32_t key = mix(now.key ^ static_cast<uint32_t>(place >> 32));
+  float mo[VEC], ro[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    const uint32_t word = mix((static_cast<uint32_t>(place) + e) ^ key);
+    float a = fabsf(mf[e]) * m_inv, b = rf[e] * r_inv;
+    a = a > E4M3_MAX ? E4M3_MAX : a;
+    b = b > E4M3_MAX ? E4M3_MAX : b;
+    mo[e] = copysignf(round_e4m3(a, word & 0xffffu), mf[e]);
+    const float q = round_e4m3(b, word >> 16);
+    ro[e] = b > 0.0f && q < E4M3_MIN ? E4M3_MIN : q;
+  }
+  uint32_t mw[2], rw[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    mw[h] = to_e4m3(mo[4 * h], mo[4 * h + 1]) | to_e4m3(mo[4 * h + 2], mo[4 * h + 3]) << 16;
+    rw[h] = to_e4m3(ro[4 * h], ro[4 * h + 1]) | to_e4m3(ro[4 * h + 2], ro[4 * h + 3]) << 16;
+  }
+  p.set(wf);
+  if constexpr (MASTER) w.set(wf);
+  if (wide) {
+    p.store(static_cast<P*>(t.p) + i);
+    if constexpr (MASTER) w.store(t.master + i);
+    *reinterpret_cast<uint2*>(m8) = make_uint2(mw[0], mw[1]);
+    *reinterpret_cast<uint2*>(r8) = make_uint2(rw[0], rw[1]);
+  } else {
+    p.store_some(static_cast<P*>(t.p) + i, 0, mine);
+    if constexpr (MASTER) w.store_some(t.master + i, 0, mine);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      if (e < mine) {
+        m8[e] = static_cast<uint8_t>(mw[e / 4] >> (8 * (e & 3)));
+        r8[e] = static_cast<uint8_t>(rw[e / 4] >> (8 * (e & 3)));
+      }
+    }
+  }
+  if (lane == 0) {
+    t.ms[block] = m_none ? 0.0f : m_most / E4M3_MAX;
+    t.rs[block] = r_none ? 0.0f : r_most / E4M3_MAX;
+  }
+}
+
+template <int M, typename P, typename G, bool MASTER>
+__global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) adamw8_kernel(const __grid_constant__ Batch<M> b,
+                                                                        const __grid_constant__ Rule r) {
+  let_next_start();
+  wait_for_previous();
+  const Now now = now_of(r);
+  const int warp = static_cast<int>(threadIdx.x >> 5);
+  for (uint32_t c = blockIdx.x; c < b.chunks; c += gridDim.x) {
+    const Tensor& t = b.t[find_tensor(b, c)];
+    const int64_t at = static_cast<int64_t>(c - t.first_chunk) * b.chunk;
+    const int64_t end = min(at + b.chunk, t.n);
+    const float keep = 1.0f - now.lr * t.decay;
+    for (int64_t i = at + warp * CCE_ADAMW_BLOCK; i < end; i += WARPS * CCE_ADAMW_BLOCK)
+      update_block<P, G, MASTER>(r, now, keep, t, i, static_cast<int>(min(end - i, static_cast<int64_t>(CCE_ADAMW_BLOCK))));
+  }
+}
+
+// ---------------------------------------------------------------------- host
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t type_bytes(int t) { return t == CCE_F32 ? 4 : 2; }
+bool type_ok(int t) { return t == CCE_F32 || t == CCE_F16 || t == CCE_BF16; }
+bool multiple(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(bytes) == 0; }
+bool finite_positive(double v) { return std::isfinite(v) && v >= 0.0; }
+
+cce_status check_tensor(const cce_adamw_tensor& t, bool eight) {
+  if (!type_ok(t.grad_type) || !type_ok(t.param_type) || !finite_positive(t.weight_decay)) return CCE_ERR_ARG;
+  if (t.n < 0 || t.n >= MAX_ELEMENTS) return CCE_ERR_SHAPE;
+  if (t.n == 0) return CCE_OK;
+  if (!t.grad || !t.param || !t.exp_avg || !t.exp_avg_sq || (eight && (!t.exp_avg_scale || !t.rms_scale)))
+    return CCE_ERR_NULL;
+  if (!multiple(t.grad, type_bytes(t.grad_type)) || !multiple(t.param, type_bytes(t.param_type)) ||
+      !multiple(t.master, 4) || (!eight && (!multiple(t.exp_avg, 4) || !multiple(t.exp_avg_sq, 4))) ||
+      (eight && (!multiple(t.exp_avg_scale, 4) || !multiple(t.rms_scale, 4))))
+    return CCE_ERR_ALIGN;
+  return CCE_OK;
+}
+
+// Memory that is written and overlaps other memory would be read and written in
+// any order by the blocks of a launch.
+struct Span {
+  uintptr_t lo, hi;
+  bool out;
+};
+
+cce_status check_overlap(const cce_adamw_tensor* t, int64_t n, bool eight) {
+  Span* spans = new (std::nothrow) Span[7 * static_cast<size_t>(std::max<int64_t>(1, n))];
+  if (!spans) return CCE_ERR_CUDA;
+  int64_t m = 0;
+  const auto add = [&](const void* p, int64_t bytes, bool out) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    if (p) spans[m++] = Span{lo, lo + static_cast<uintptr_t>(bytes), out};
+  };
+  for (int64_t i = 0; i < n; ++i) {
+    const cce_adamw_tensor& a = t[i];
+    if (a.n == 0) continue;
+    add(a.grad, a.n * type_bytes(a.grad_type), false);
+    add(a.param, a.n * type_bytes(a.param_type), true);
+    add(a.master, a.n * 4, true);
+    add(a.exp_avg, a.n * (eight ? 1 : 4), true);
+    add(a.exp_avg_sq, a.n * (eight ? 1 : 4), true);
+    if (eight) {
+      add(a.exp_avg_scale, cdiv(a.n, CCE_ADAMW_BLOCK) * 4, true);
+      add(a.rms_scale, cdiv(a.n, CCE_ADAMW_BLOCK) * 4, true);
+    }
+  }
+  std::sort(spans, spans + m, [](const Span& a, const Span& b) { return a.lo < b.lo; });
+  uintptr_t end_any = 0, end_out = 0;
+  bool bad = false;
+  for (int64_t i = 0; i < m; ++i) {
+    bad = bad || spans[i].lo < (spans[i].out ? end_any : end_out);
+    end_any = std::max(end_any, spans[i].hi);
+    if (spans[i].out) end_out = std::max(end_out, spans[i].hi);
+  }
+  delete[] spans;
+  return bad ? CCE_ERR_ARG : CCE_OK;
+}
+
+struct Call {
+  const cce_adamw_tensor* t;
+  int64_t n;
+  bool eight;
+  int chunk, grid;
+  Rule r;
+  cudaStream_t s;
+  int launches;
+};
+
+template <int M, typename P, typename G, bool MASTER>
+cudaError_t run_batches(Call& c) {
+  Batch<M> b;
+  int64_t next = 0, blocks = 0;
+  while (next < c.n) {
+    b.count = 0;
+    b.chunk = c.chunk;
+    int64_t chunks = 0;
+    for (; next < c.n && b.count < M; ++next) {
+      const cce_adamw_tensor& a = c.t[next];
+      const int64_t before = blocks;
+      blocks += cdiv(a.n, CCE_ADAMW_BLOCK);
+      if (a.n == 0 || a.param_type != ElemType<P>::id || a.grad_type != ElemType<G>::id || !a.master == MASTER)
+        continue;
+      Tensor& t = b.t[b.count++];
+      t.g = a.grad;
+      t.p = a.param;
+      t.master = a.master;
+      t.m = a.exp_avg;
+      t.v = a.exp_avg_sq;
+      t.ms = a.exp_avg_scale;
+      t.rs = a.rms_scale;
+      t.n = a.n;
+      t.first_block = before;
+      t.first_chunk = static_cast<uint32_t>(chunks);
+      t.decay = a.weight_decay;
+      t.wide = multiple(a.grad, 16) && multiple(a.param, 16) && multiple(a.master, 16) &&
+               multiple(a.exp_avg, c.eight ? 8 : 16) && multiple(a.exp_avg_sq, c.eight ? 8 : 16);
+      chunks += cdiv(a.n, c.chunk);
+    }
+    if (b.count == 0) continue;
+    b.chunks = static_cast<uint32_t>(chunks);
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(c.grid, chunks)));
+    const cudaError_t e = c.eight ? launch_after(adamw8_kernel<M, P, G, MASTER>, grid, dim3(THREADS), 0, 1, c.s, b, c.r)
+                                  : launch_after(adamw_kernel<M, P, G, MASTER>, grid, dim3(THREADS), 0, 1, c.s, b, c.r);
+    if (e != cudaSuccess) return e;
+    ++c.launches;
+  }
+  return cudaSuccess;
+}
+
+template <typename P, typename G, bool MASTER>
+cudaError_t run_kind(Call& c) {
+  return c.n <= FEW_TENSORS ? run_batches<FEW_TENSORS, P, G, MASTER>(c) : run_batches<MAX_TENSORS, P, G, MASTER>(c);
+}
+
+template <typename P, bool MASTER>
+cudaError_t run_param(Call& c, int grad_type) {
+  if (grad_type == CCE_F32) return run_kind<P, float, MASTER>(c);
+  return grad_type == CCE_BF16 ? run_kind<P, __nv_bfloat16, MASTER>(c) : run_kind<P, __half, MASTER>(c);
+}
+
+cudaError_t run_all(Call& c) {
+  // one launch for each kind of types that there is
+  bool seen[3][3][2] = {};
+  for (int64_t i = 0; i < c.n; ++i) {
+    const cce_adamw_tensor& a = c.t[i];
+    if (a.n == 0) continue;
+    bool& done = seen[a.param_type][a.grad_type][a.master != nullptr];
+    if (done) continue;
+    done = true;
+    cudaError_t e;
+    if (a.param_type == CCE_F32) {
+      e = a.master ? run_param<float, true>(c, a.grad_type) : run_param<float, false>(c, a.grad_type);
+    } else if (a.param_type == CCE_BF16) {
+      e = a.master ? run_param<__nv_bfloat16, true>(c, a.grad_type) : run_param<__nv_bfloat16, false>(c, a.grad_type);
+    } else {
+      e = a.master ? run_param<__half, true>(c, a.grad_type) : run_param<__half, false>(c, a.grad_type);
+    }
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+}  // namespace cce
+
+using namespace cce;
+
+extern "C" {
+
+int cce_optim_abi_version(void) { return 100; }
+
+cce_status cce_adamw_step(const cce_adamw_tensor* tensors, int64_t n_tensors, int state_bits,
+                          const cce_adamw_options* o, void* stream) {
+  if (n_tensors < 0) return CCE_ERR_SHAPE;
+  if (!o || (n_tensors > 0 && !tensors)) return CCE_ERR_NULL;
+  const auto beta_ok = [](double b) { return b >= 0.0 && b < 1.0; };
+  if ((state_bits != 32 && state_bits != 8) || !beta_ok(o->beta1) || !beta_ok(o->beta2) || !finite_positive(o->lr) ||
+      !finite_positive(o->eps) || (!o->step_ptr && o->step < 1))
+    return CCE_ERR_ARG;
+  if (o->norm && (!(o->max_norm >= 0.0f) || !finite_positive(o->eps_norm))) return CCE_ERR_ARG;
+  if (!multiple(o->step_ptr, 8) || !multiple(o->lr_ptr, 4) || !multiple(o->norm, 4)) return CCE_ERR_ALIGN;
+  const bool eight = state_bits == 8;
+  int64_t total = 0;
+  for (int64_t i = 0; i < n_tensors; ++i) {
+    const cce_status st = check_tensor(tensors[i], eight);
+    if (st != CCE_OK) return st;
+    total += tensors[i].n;
+  }
+  cce_status st = check_overlap(tensors, n_tensors, eight);
+  if (st != CCE_OK) return st;
+  int sms = 0;
+  st = static_cast<cce_status>(device_ready(&sms));
+  if (st != CCE_OK) return st;
+  const double t = static_cast<double>(o->step);
+  Rule r{};
+  r.beta1 = static_cast<float>(o->beta1);
+  r.rest1 = static_cast<float>(1.0 - o->beta1);
+  r.beta2 = static_cast<float>(o->beta2);
+  r.rest2 = static_cast<float>(1.0 - o->beta2);
+  r.eps = static_cast<float>(o->eps);
+  r.log1 = static_cast<float>(std::log(o->beta1));
+  r.log2 = static_cast<float>(std::log(o->beta2));
+  r.lr = static_cast<float>(o->lr);
+  r.correct1 = static_cast<float>(1.0 - std::pow(o->beta1, t));
+  r.correct2 = static_cast<float>(1.0 - std::pow(o->beta2, t));
+  r.step = o->step_ptr;
+  r.lr_ptr = o->lr_ptr;
+  r.norm = o->norm;
+  r.max_norm = o->max_norm;
+  r.eps_norm = o->eps_norm;
+  r.seed = o->seed;
+  r.t = static_cast<uint32_t>(o->step);
+  // four rounds of a block, one where that leaves blocks without work
+  const int grid = sms * BLOCKS_PER_SM;
+  Call c{tensors, n_tensors, eight, total >= int64_t(4) * grid * ROUND ? 4 * ROUND : ROUND, grid, r,
+         static_cast<cudaStream_t>(stream), 0};
+  const cudaError_t e = run_all(c);
+  count_launches(c.launches);
+  return e == cudaSuccess ? CCE_OK : CCE_ERR_CUDA;
+}
+
+}  // extern "C"

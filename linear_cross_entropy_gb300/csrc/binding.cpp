@@ -1,4 +1,4 @@
-// Python module _native: the norms and the clipping on torch tensors, over the
+// Python module _native: here the norms and the clipping on torch tensors, over the
 // C ABI of include/cce_ops.h.  It checks arguments, describes strided rows,
 // allocates results and workspaces with torch, and calls the library on the
 // current stream.
@@ -349,7 +349,7 @@ PYBIND11_MODULE(_native, m) {
       PyErr_SetString(PyExc_NotImplementedError, e.what());
     } catch (const StatusError& e) {
       const py::object type = py::module_::import("linear_cross_entropy_gb300._lib").attr("CCEError");
-      PyErr_SetObject(type.ptr(), type(e.status, e.what()).ptr());
+      PyErr_SetObject(type.ptr(), type(e.status, e.call).ptr());
     }
   });
   using Free = py::call_guard<py::gil_scoped_release>;
@@ -389,6 +389,7 @@ PYBIND11_MODULE(_native, m) {
          double max_norm, double eps) { return clip(grads, outs ? &*outs : &grads, norm_type, max_norm, eps); },
       Free());
   bind_layers(m);
+  bind_optim(m);
   m.def("rows", [](const Tensor& t) {
     const Rows r = rows_of(t);
     return py::make_tuple(r.t, r.inner, r.row, r.outer);

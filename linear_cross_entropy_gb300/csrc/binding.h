@@ -28,10 +28,13 @@ using at::Tensor;
 using OptTensor = std::optional<Tensor>;
 using OptType = std::optional<at::ScalarType>;
 
-// A status of the library; Python sees it as CCEError.
+// A status of the library; Python sees it as CCEError, and from a backward pass, which runs on the autograd engine's
+// thread, as a RuntimeError of the same text.
 struct StatusError : std::runtime_error {
   int status;
-  StatusError(int s, const std::string& what) : std::runtime_error(what), status(s) {}
+  std::string call;
+  StatusError(int s, const std::string& c)
+      : std::runtime_error(c + ": " + cce_status_string(static_cast<cce_status>(s))), status(s), call(c) {}
 };
 
 // `args`: what CCE_ERR_ARG is left to mean once the tensors have been checked here.
@@ -158,5 +161,6 @@ inline Tensor given(const OptTensor& t) { return t ? *t : Tensor(); }
 
 // The parts, each in a file of its own.
 void bind_layers(pybind11::module_& m);
+void bind_optim(pybind11::module_& m);
 
 }  // namespace binding
