@@ -6,8 +6,6 @@
 #include "elements.cuh"
 #include "linear.h"
 
-#include <type_traits>
-
 namespace cce {
 
 template <int ACT, int M>
@@ -34,79 +32,134 @@ __device__ __forceinline__ float load_scalar(const void* p, int type, int64_t i)
   return f[0];
 }
 
-// Rows j0 .. j0 + n - 1 of column i, all inside of the matrices; n = M with FULL.
-// z0: the product with x (gated: the gate's), z1: gated: the up projection's.
-template <bool BF16, bool Y32, bool GATED, bool FULL, int M>
-__device__ __forceinline__ void finish_column_as(const LinEpilogue& e, float bias, int i, int j0, int n,
-                                                 float (&z0)[M], float (&z1)[M]) {
-  using Y = typename std::conditional<Y32, float, uint16_t>::type;
-  float res[M];
-  if (!GATED && e.res) {  // all loads in flight at once
-    const Y* p = static_cast<const Y*>(e.res) + static_cast<int64_t>(j0) * e.res_pitch + i;
+// Loads and stores of a column's rows, `pitch` bytes apart.  They are volatile so that
+// they stay in order and each address is the last one and a pitch: with all addresses in
+// registers at once the epilogue spilled.
+__device__ __forceinline__ void store16(char* p, uint32_t v) {
+  asm volatile("{\n\t.reg .b16 h, g;\n\tmov.b32 {h, g}, %1;\n\tst.global.b16 [%0], h;\n\t}" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ void store16_high(char* p, uint32_t v) {
+  asm volatile("{\n\t.reg .b16 h, g;\n\tmov.b32 {h, g}, %1;\n\tst.global.b16 [%0], g;\n\t}" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ void store32(char* p, float v) {
+  asm volatile("st.global.f32 [%0], %1;" ::"l"(p), "f"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t load16(const char* p) {
+  uint16_t v;
+  asm volatile("ld.global.b16 %0, [%1];" : "=h"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t load32(const char* p) {
+  uint32_t v;
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
+// M values to rows of a 16-bit matrix, rounded to nearest even; the first n of them.
+template <bool FULL, int M>
+__device__ __forceinline__ void store_rows16(char* p, int64_t pitch, const uint32_t (&two)[(M + 1) / 2], int n) {
 #pragma unroll
-    for (int u = 0; u < M; ++u, p += e.res_pitch) {
-      if (FULL || u < n) {
-        if constexpr (Y32) {
-          res[u] = *p;
-        } else {
-          res[u] = from_bits16<BF16>(*p);
-        }
-      }
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < M; ++u) z0[u] += bias;
-  if (e.z[0]) {
-    uint16_t* p = static_cast<uint16_t*>(e.z[0]) + static_cast<int64_t>(j0) * e.z_pitch + i;
-    uint16_t* q = static_cast<uint16_t*>(e.z[1]) + static_cast<int64_t>(j0) * e.z_pitch + i;
-#pragma unroll
-    for (int u = 0; u < M; ++u, p += e.z_pitch, q += e.z_pitch) {
-      if (FULL || u < n) {
-        *p = to_bits16<BF16>(z0[u]);
-        if (GATED) *q = to_bits16<BF16>(z1[u]);
-      }
-    }
-  }
-  activate_all(e.act, z0);
-  Y* p = static_cast<Y*>(e.y) + static_cast<int64_t>(j0) * e.y_pitch + i;
-#pragma unroll
-  for (int u = 0; u < M; ++u, p += e.y_pitch) {
-    if (FULL || u < n) {
-      float y = z0[u];
-      if (GATED) y *= z1[u];
-      if (!GATED && e.res) y += res[u];
-      if constexpr (Y32) {
-        *p = y;
-      } else {
-        *p = to_bits16<BF16>(y);
-      }
+  for (int u = 0; u < M; ++u, p += pitch) {
+    if (!FULL && u >= n) continue;
+    if (u & 1) {
+      store16_high(p, two[u / 2]);
+    } else {
+      store16(p, two[u / 2]);
     }
   }
 }
 
-template <bool BF16, bool Y32, bool GATED, int M>
-__device__ __forceinline__ void finish_column_of(const LinEpilogue& e, float bias, int i, int j0, int n, float (&z0)[M],
-                                                 float (&z1)[M]) {
-  if (M == 1 || n >= M) {
-    finish_column_as<BF16, Y32, GATED, true>(e, bias, i, j0, n, z0, z1);
+template <int M>
+__device__ __forceinline__ void put_rows16(void* base, int64_t pitch, int64_t at, bool bf16, const float (&f)[M], int n) {
+  uint32_t two[(M + 1) / 2];
+  if (bf16) {
+#pragma unroll
+    for (int u = 0; u < M; u += 2) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f[u], u + 1 < M ? f[u + 1 < M ? u + 1 : u] : 0.0f);
+      two[u / 2] = *reinterpret_cast<const uint32_t*>(&h);
+    }
   } else {
-    finish_column_as<BF16, Y32, GATED, false>(e, bias, i, j0, n, z0, z1);
+#pragma unroll
+    for (int u = 0; u < M; u += 2) {
+      const __half2 h = __floats2half2_rn(f[u], u + 1 < M ? f[u + 1 < M ? u + 1 : u] : 0.0f);
+      two[u / 2] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  char* p = static_cast<char*>(base) + at * 2;
+  if (n >= M) {
+    store_rows16<true, M>(p, pitch * 2, two, n);
+  } else {
+    store_rows16<false, M>(p, pitch * 2, two, n);
   }
 }
 
+template <int M>
+__device__ __forceinline__ void put_rows32(void* base, int64_t pitch, int64_t at, const float (&f)[M], int n) {
+  char* p = static_cast<char*>(base) + at * 4;
+#pragma unroll
+  for (int u = 0; u < M; ++u, p += pitch * 4) {
+    if (u < n) store32(p, f[u]);
+  }
+}
+
+// The residual's rows as they are in memory: loaded ahead of what they are added to.
+template <int M>
+struct Residual {
+  uint32_t raw[M];
+
+  __device__ __forceinline__ void load(const LinEpilogue& e, int i, int j0, int n) {
+    const int64_t at = static_cast<int64_t>(j0) * e.res_pitch + i;
+    if (e.y_type == CCE_F32) {
+      const char* p = static_cast<const char*>(e.res) + at * 4;
+#pragma unroll
+      for (int u = 0; u < M; ++u, p += e.res_pitch * 4) raw[u] = u < n ? load32(p) : 0u;
+    } else {
+      const char* p = static_cast<const char*>(e.res) + at * 2;
+#pragma unroll
+      for (int u = 0; u < M; ++u, p += e.res_pitch * 2) raw[u] = u < n ? load16(p) : 0u;
+    }
+  }
+  __device__ __forceinline__ void add_to(const LinEpilogue& e, bool bf16, float (&f)[M]) const {
+    if (e.y_type == CCE_F32) {
+#pragma unroll
+      for (int u = 0; u < M; ++u) f[u] += __uint_as_float(raw[u]);
+    } else if (bf16) {
+#pragma unroll
+      for (int u = 0; u < M; ++u) f[u] += __uint_as_float(raw[u] << 16);
+    } else {
+#pragma unroll
+      for (int u = 0; u < M; ++u) f[u] += __half2float(__ushort_as_half(static_cast<uint16_t>(raw[u])));
+    }
+  }
+};
+
+// Rows j0 .. j0 + min(n, M) - 1 of column i, all inside of the matrices.  z0: the
+// product with x (gated: the gate's), z1: gated: the up projection's; res: loaded if
+// there is a residual.
 template <bool GATED, int M>
 __device__ __forceinline__ void finish_column(const LinEpilogue& e, bool bf16, float bias, int i, int j0, int n,
-                                              float (&z0)[M], float (&z1)[M]) {
+                                              float (&z0)[M], const float (&z1)[M], const Residual<M>& res) {
+  if (!GATED && e.bias) {
+#pragma unroll
+    for (int u = 0; u < M; ++u) z0[u] += bias;
+  }
+  if (e.z[0]) {
+    const int64_t at = static_cast<int64_t>(j0) * e.z_pitch + i;
+    put_rows16(e.z[0], e.z_pitch, at, bf16, z0, n);
+    if (GATED) put_rows16(e.z[1], e.z_pitch, at, bf16, z1, n);
+  }
+  activate_all(e.act, z0);
+  if (GATED) {
+#pragma unroll
+    for (int u = 0; u < M; ++u) z0[u] *= z1[u];
+  } else if (e.res) {
+    res.add_to(e, bf16, z0);
+  }
+  const int64_t at = static_cast<int64_t>(j0) * e.y_pitch + i;
   if (!GATED && e.y_type == CCE_F32) {
-    if (bf16) {
-      finish_column_of<true, true, GATED>(e, bias, i, j0, n, z0, z1);
-    } else {
-      finish_column_of<false, true, GATED>(e, bias, i, j0, n, z0, z1);
-    }
-  } else if (bf16) {
-    finish_column_of<true, false, GATED>(e, bias, i, j0, n, z0, z1);
+    put_rows32(e.y, e.y_pitch, at, z0, n);
   } else {
-    finish_column_of<false, false, GATED>(e, bias, i, j0, n, z0, z1);
+    put_rows16(e.y, e.y_pitch, at, bf16, z0, n);
   }
 }
 

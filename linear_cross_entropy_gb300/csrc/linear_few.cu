@@ -33,29 +33,57 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
   }
 }
 
-// Eight values from k on, zeros behind K (a multiple of 8 or padded to one: vectors are whole).
-__device__ __forceinline__ uint4 vector_at(const uint16_t* row, int k, int K, bool there) {
-  if (!there || k >= K) return make_uint4(0u, 0u, 0u, 0u);
+// Eight values from k on, zeros behind K: what lies there may be anything.
+__device__ __forceinline__ uint4 vector_at(const uint16_t* row, int k, int K) {
+  if (k >= K) return make_uint4(0u, 0u, 0u, 0u);
   uint4 v = *reinterpret_cast<const uint4*>(row + k);
+  uint32_t* w = reinterpret_cast<uint32_t*>(&v);
   const int n = K - k;
-  if (n < 8) {  // the last vector of an odd width: what lies behind may be anything
-    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = 2 * i + 1 < n ? w[i] : 2 * i < n ? w[i] & 0xffffu : 0u;
-  }
+  for (int i = 0; i < 4; ++i) w[i] = 2 * i + 1 < n ? w[i] : 2 * i < n ? w[i] & 0xffffu : 0u;
   return v;
 }
 
-template <bool BF16, int NT, bool GATED, int UNROLL>
-__global__ void __launch_bounds__(32 * WARPS) few_kernel(const __grid_constant__ LinFew a) {
+// 32 of k of the fragments: thread t of a row has 8t .. 8t + 7, of which the first four are one MMA's, the others the
+// next one's.
+template <bool BF16, int NT, int MATS>
+struct Step {
+  uint4 w[MATS][2], x[NT];
+
+  // INSIDE: all of them are below K, and the loads of several steps are in flight at once.
+  template <bool INSIDE>
+  __device__ __forceinline__ void load(const uint16_t* const (&wp)[MATS][2], const uint16_t* const (&xp)[NT], int k, int K) {
+#pragma unroll
+    for (int m = 0; m < MATS; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        w[m][h] = INSIDE ? *reinterpret_cast<const uint4*>(wp[m][h] + k) : vector_at(wp[m][h], k, K);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) x[n] = INSIDE ? *reinterpret_cast<const uint4*>(xp[n] + k) : vector_at(xp[n], k, K);
+  }
+  __device__ __forceinline__ void add_to(float (&c)[MATS][NT][4]) const {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int m = 0; m < MATS; ++m) {
+        mma<BF16>(c[m][n], w[m][0].x, w[m][1].x, w[m][0].y, w[m][1].y, x[n].x, x[n].y);
+        mma<BF16>(c[m][n], w[m][0].z, w[m][1].z, w[m][0].w, w[m][1].w, x[n].z, x[n].w);
+      }
+    }
+  }
+};
+
+template <bool BF16, int NT, bool GATED>
+__global__ void __launch_bounds__(32 * WARPS, 2) few_kernel(const __grid_constant__ LinFew a) {
   constexpr int MATS = GATED ? 2 : 1;
+  constexpr int UNROLL = GATED ? 2 : 4;  // steps in flight: eight vectors of the weights a thread
   __shared__ float sums[WARPS][MATS][ROWS][8 * NT + 1];
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   const int g = lane >> 2, t = lane & 3;
   const int i0 = static_cast<int>(blockIdx.x) * ROWS;
   let_next_start();
   wait_for_previous();
-  // rows of w behind the last one are read as the last one, and not written
+  // rows behind the last one, of w and of x, are read as the last one, and their results not written
   const uint16_t* w[MATS][2];
 #pragma unroll
   for (int m = 0; m < MATS; ++m) {
@@ -68,39 +96,31 @@ __global__ void __launch_bounds__(32 * WARPS) few_kernel(const __grid_constant__
   for (int n = 0; n < NT; ++n)
     x[n] = static_cast<const uint16_t*>(a.x) + static_cast<int64_t>(min(g + 8 * n, a.J - 1)) * a.x_pitch;
 
-  float c[MATS][NT][4];
+  float c[MATS][NT][4] = {};
+  // a warp's k: two steps at 64 (warp + WARPS q), q = 0, 1, ...
+  constexpr int STRIDE = 64 * WARPS;
+  int k = warp * 64 + 8 * t;
+  const int last = a.K - 64 + 8 * t;  // the last k whose two steps are inside
+#pragma unroll 1
+  for (; k + STRIDE * (UNROLL / 2 - 1) <= last; k += STRIDE * (UNROLL / 2)) {
+    Step<BF16, NT, MATS> s[UNROLL];
 #pragma unroll
-  for (int m = 0; m < MATS; ++m)
+    for (int u = 0; u < UNROLL; ++u) s[u].template load<true>(w, x, k + (u >> 1) * STRIDE + (u & 1) * 32, a.K);
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) c[m][n][q] = 0.0f;
-
-  // a step is 32 of k: thread t of a row has 8t .. 8t + 7; the first four of them are one MMA's, the others the next one's
-  for (int k0 = warp * 64; k0 < a.K; k0 += 64 * WARPS * (UNROLL / 2)) {
-    uint4 wv[UNROLL][MATS][2], xv[UNROLL][NT];
-#pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
-      const int k = k0 + (u >> 1) * 64 * WARPS + (u & 1) * 32 + 8 * t;
-#pragma unroll
-      for (int m = 0; m < MATS; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) wv[u][m][h] = vector_at(w[m][h], k, a.K, true);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) xv[u][n] = vector_at(x[n], k, a.K, g + 8 * n < a.J);
+    for (int u = 0; u < UNROLL; ++u) s[u].add_to(c);
+  }
+#pragma unroll 1
+  for (; k - 8 * t < a.K; k += STRIDE) {
+    Step<BF16, NT, MATS> s[2];
+    if (k <= last) {
+      s[0].template load<true>(w, x, k, a.K);
+      s[1].template load<true>(w, x, k + 32, a.K);
+    } else {
+      s[0].template load<false>(w, x, k, a.K);
+      s[1].template load<false>(w, x, k + 32, a.K);
     }
-#pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int m = 0; m < MATS; ++m) {
-          const uint4 &lo = wv[u][m][0], &hi = wv[u][m][1], &b = xv[u][n];
-          mma<BF16>(c[m][n], lo.x, hi.x, lo.y, hi.y, b.x, b.y);
-          mma<BF16>(c[m][n], lo.z, hi.z, lo.w, hi.w, b.z, b.w);
-        }
-      }
-    }
+    s[0].add_to(c);
+    s[1].add_to(c);
   }
 #pragma unroll
   for (int m = 0; m < MATS; ++m)
@@ -119,15 +139,17 @@ __global__ void __launch_bounds__(32 * WARPS) few_kernel(const __grid_constant__
     if (GATED) z1[0] += sums[v][MATS - 1][r][j];
   }
   const float bias = a.e.bias ? load_scalar(a.e.bias, a.e.bias_type, i) : 0.0f;
-  finish_column<GATED>(a.e, BF16, bias, i, j, 1, z0, z1);
+  Residual<1> res;
+  if (!GATED && a.e.res) res.load(a.e, i, j, 1);
+  finish_column<GATED>(a.e, BF16, bias, i, j, 1, z0, z1, res);
 }
 static_assert(32 * WARPS == ROWS * LIN_FEW_ROWS, "one result a thread");
 
 template <bool BF16, int NT>
 cudaError_t launch(const LinFew& a, bool gated, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>((a.I + ROWS - 1) / ROWS)), block(32 * WARPS);
-  return gated ? launch_after(few_kernel<BF16, NT, true, 4>, grid, block, 0, 1, s, a)
-               : launch_after(few_kernel<BF16, NT, false, 8>, grid, block, 0, 1, s, a);
+  return gated ? launch_after(few_kernel<BF16, NT, true>, grid, block, 0, 1, s, a)
+               : launch_after(few_kernel<BF16, NT, false>, grid, block, 0, 1, s, a);
 }
 
 }  // namespace

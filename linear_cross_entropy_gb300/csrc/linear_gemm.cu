@@ -39,7 +39,7 @@ constexpr int PHASES = EPI_WARPS / 4;  // warps that share the columns of 32 TME
 constexpr int THREADS = 64 + 32 * EPI_WARPS;
 constexpr int ACC_COLS = 256;  // TMEM columns of one of the two accumulators
 constexpr int CHUNK = 16;      // columns that a warp reads at a time
-constexpr int HALF = CHUNK / 2;  // and finishes: 96 registers a thread hold no more
+constexpr int HALF = CHUNK / 2;
 constexpr int GROUP = 64 * 128;  // bytes of 64 rows of 128 bytes
 // gated: what a warp hands over, twice
 constexpr int SWAP_BYTES = 2 * HALF * 32 * 4;
@@ -170,7 +170,7 @@ __device__ __forceinline__ void load_loop(const LinArgs& a, const Shared& s) {
     const int j0 = t.jt * p.jt + rank * rows;
     const uint32_t bytes = static_cast<uint32_t>((A_BYTES + rows * BK * 2) * (PAIR ? 2 : 1));
     for (int kb = t.kb; kb < t.kb_end; ++kb) {
-      if (!wait_bounded(&s.empty[stage], phase ^ 1u, abort_flag, &linear_error)) {
+      if (!wait_bounded_long(&s.empty[stage], phase ^ 1u, abort_flag, &linear_error)) {
         ok = false;
         break;
       }
@@ -204,7 +204,7 @@ __device__ __forceinline__ void load_loop(const LinArgs& a, const Shared& s) {
     for (int i = 0; i < stages; ++i) {
       if (issued & (1u << i)) {
         volatile int none = 0;
-        wait_bounded(&s.full[i], (issued_par >> i) & 1u, &none, nullptr);
+        wait_bounded_long(&s.full[i], (issued_par >> i) & 1u, &none, nullptr);
       }
     }
   }
@@ -233,12 +233,12 @@ __device__ __forceinline__ void mma_loop(const LinArgs& a, const Shared& s, uint
     const uint32_t a_step = (a_mn ? 2048u : 32u) >> 4, b_step = (b_mn ? 2048u : 32u) >> 4;
     const uint32_t a_next = (a_mn ? 8192u : 2u * GROUP) >> 4;
     const uint32_t b_next = (b_mn ? 8192u : (PAIR ? p.jt / 2 : p.jt) * 128u) >> 4;
-    if (!wait_bounded(&s.acc_empty[acc], acc_phase ^ 1u, abort_flag, &linear_error)) break;
+    if (!wait_bounded_long(&s.acc_empty[acc], acc_phase ^ 1u, abort_flag, &linear_error)) break;
     tc_fence_after();
     const uint32_t d = tmem + static_cast<uint32_t>(acc * ACC_COLS);
     uint32_t accumulate = 0;
     for (int kb = t.kb; kb < t.kb_end; ++kb) {
-      if (!wait_bounded(&s.full[stage], phase, abort_flag, &linear_error)) {
+      if (!wait_bounded_long(&s.full[stage], phase, abort_flag, &linear_error)) {
         ok = false;
         break;
       }
@@ -333,7 +333,9 @@ __device__ __forceinline__ void epilogue_loop(const LinArgs& a, const Shared& s,
     const int i = (t.it * (PAIR ? 2 : 1) + rank) * (GATED ? LIN_BI / 2 : LIN_BI) + lanes + lane;
     const bool inside = i < p.I;
     const float bias = p.e.bias && p.splits == 1 && inside ? load_scalar(p.e.bias, p.e.bias_type, i) : 0.0f;
-    bool ok = warp_wait_bounded(&s.acc_full[acc], acc_phase, s.abort_flag, &linear_error);
+    bool ok = true;
+    if (lane == 0) ok = wait_bounded_long(&s.acc_full[acc], acc_phase, s.abort_flag, &linear_error);
+    ok = __shfl_sync(0xffffffffu, ok, 0);
     if constexpr (GATED) ok = both(barrier, ok);  // where a wait ran out, neither waits for the other any more
     if (!ok) break;
     tc_fence_after();
@@ -343,16 +345,17 @@ __device__ __forceinline__ void epilogue_loop(const LinArgs& a, const Shared& s,
       const int n = min(CHUNK, p.J - j0);
       if (n <= 0) break;  // the same in all lanes, and in both warps of a gated exchange
       uint32_t r[CHUNK];
+      Residual<CHUNK> res;
+      if (!GATED && p.e.res && p.splits == 1 && inside) res.load(p.e, i, j0, n);
       __syncwarp();  // the lanes outside of the matrix are back
       tmem_ld16(from + CHUNK * c, r);
       tmem_ld_wait();
       if (p.splits > 1) {  // a partial sum
         if (!inside) continue;
-        float* to = p.part + (static_cast<int64_t>(t.split * (GATED ? 2 : 1) + up) * p.J + j0) * p.I + i;
+        float z[CHUNK];
 #pragma unroll
-        for (int u = 0; u < CHUNK; ++u, to += p.I) {
-          if (u < n) *to = __uint_as_float(r[u]);
-        }
+        for (int u = 0; u < CHUNK; ++u) z[u] = __uint_as_float(r[u]);
+        put_rows32(p.part, p.I, (static_cast<int64_t>(t.split * (GATED ? 2 : 1) + up) * p.J + j0) * p.I + i, z, n);
       } else if constexpr (GATED) {
         // the gate's warp finishes the first half of the columns, the other the second
         float* const give = mine + flip * HALF * 32;
@@ -369,15 +372,12 @@ __device__ __forceinline__ void epilogue_loop(const LinArgs& a, const Shared& s,
         }
         flip ^= 1;  // the other warp has read this buffer before it meets the next barrier
         const int left = n - up * HALF;
-        if (inside && left > 0) finish_column<true>(p.e, a.bf16, 0.0f, i, j0 + up * HALF, left, z0, z1);
+        if (inside && left > 0) finish_column<true>(p.e, a.bf16, 0.0f, i, j0 + up * HALF, left, z0, z1, Residual<HALF>{});
       } else if (inside) {
+        float z[CHUNK];
 #pragma unroll
-        for (int h = 0; h < CHUNK; h += HALF) {
-          float z[HALF];
-#pragma unroll
-          for (int u = 0; u < HALF; ++u) z[u] = __uint_as_float(r[h + u]);
-          if (h < n) finish_column<false>(p.e, a.bf16, bias, i, j0 + h, n - h, z, z);
-        }
+        for (int u = 0; u < CHUNK; ++u) z[u] = __uint_as_float(r[u]);
+        finish_column<false>(p.e, a.bf16, bias, i, j0, n, z, z, res);
       }
     }
     tc_fence_before();

@@ -26,6 +26,8 @@ __global__ void __launch_bounds__(THREADS) join_kernel(const float* part, int I,
   for (int64_t row = static_cast<int64_t>(blockIdx.y) * JOIN_ROWS; row < J; row += static_cast<int64_t>(gridDim.y) * JOIN_ROWS) {
     const int j0 = static_cast<int>(row), n = min(JOIN_ROWS, J - j0);
     float z0[JOIN_ROWS] = {}, z1[JOIN_ROWS] = {};
+    Residual<JOIN_ROWS> res;
+    if (!GATED && e.res) res.load(e, i, j0, n);
 #pragma unroll 4
     for (int s = 0; s < splits; ++s) {  // in order
       const float* p = part + (static_cast<int64_t>(s * (GATED ? 2 : 1)) * J + j0) * I + i;
@@ -37,7 +39,7 @@ __global__ void __launch_bounds__(THREADS) join_kernel(const float* part, int I,
         }
       }
     }
-    finish_column<GATED>(e, bf16, bias, i, j0, n, z0, z1);
+    finish_column<GATED>(e, bf16, bias, i, j0, n, z0, z1, res);
   }
 }
 

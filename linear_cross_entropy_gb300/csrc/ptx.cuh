@@ -104,6 +104,36 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, vol
   return wait_bounded_ns<kCluster>(bar, parity, abort_flag, dev_err, CCE_WAIT_TIMEOUT_NS);
 }
 
+// The same for roles that wait long: the thread sleeps up to 10 us in the barrier between its looks at the clock and
+// the abort flag, and leaves the issue slots to the others.
+__device__ __forceinline__ bool mbar_try_wait_long(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(10000u)
+      : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ bool wait_bounded_long(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                                  int32_t* dev_err) {
+  const uint32_t b = smem_u32(bar);
+  if (mbar_try_wait_long(b, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  while (true) {
+    if (mbar_try_wait_long(b, parity)) return true;
+    if (*abort_flag) return false;
+    if (globaltimer() - t0 > CCE_WAIT_TIMEOUT_NS) {
+      *abort_flag = 1;
+      if (dev_err) atomicOr(reinterpret_cast<int*>(dev_err), CCE_DEVERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+
 // Warp-uniform bounded wait: lane 0 waits, the result is broadcast.
 __device__ __forceinline__ bool warp_wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                                   int32_t* dev_err) {
