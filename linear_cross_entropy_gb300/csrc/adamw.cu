@@ -8,7 +8,12 @@
 // gradients need no pass of their own once their norm is known.
 //
 // 8 bits: a warp has a block of 256 values in its registers, eight a lane, so the
-// new scales are two warp maxima and nothing is read twice.
+// new scales are two warp maxima and nothing is read twice.  What it spends is
+// instructions, some 70 a value, so the arithmetic is in packed fp32 pairs.
+//
+// m and v are the sums of the formula with every operation rounded, no product fused
+// into a sum: what decides over a value's rounding to 8 bits is then the same wherever
+// the formula is evaluated in fp32.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -105,7 +110,7 @@ __device__ __forceinline__ Now now_of(const Rule& r) {
   Now n;
   n.factor = 1.0f;
   if (r.norm) {  // as clipping does: NaN for a NaN norm, 1 where the quotient of infinities or zeros would be NaN
-    const float norm = *r.norm, f = r.max_norm / (norm + r.eps_norm);
+    const float norm = *r.norm, f = __frcp_rn(norm + r.eps_norm) * r.max_norm;
     n.factor = f < 1.0f || norm != norm ? f : 1.0f;
   }
   n.lr = r.lr_ptr ? *r.lr_ptr : r.lr;
@@ -123,15 +128,16 @@ __device__ __forceinline__ Now now_of(const Rule& r) {
   return n;
 }
 
-// m and v become the new ones, w the new weight; returns sqrt(v).
-__device__ __forceinline__ float update(const Rule& r, const Now& now, float keep, float g, float& m, float& v,
-                                        float& w) {
-  g *= now.factor;
-  m = r.beta1 * m + r.rest1 * g;
-  v = r.beta2 * v + r.rest2 * g * g;
-  const float root = sqrtf(v);
-  w = w * keep - now.size * m / (root * now.inv_root + r.eps);
-  return root;
+// Two gradients' m and v.
+__device__ __forceinline__ void average(const Rule& r, const Now& now, Pair g, Pair& m, Pair& v) {
+  g = mul(g, Pair::both(now.factor));
+  m = add(mul(Pair::both(r.beta1), m), mul(Pair::both(r.rest1), g));
+  v = add(mul(Pair::both(r.beta2), v), mul(mul(Pair::both(r.rest2), g), g));
+}
+
+// The new weight.
+__device__ __forceinline__ float step_weight(const Rule& r, const Now& now, float keep, float w, float m, float root) {
+  return fmaf(w, keep, -__fdividef(now.size * m, fmaf(root, now.inv_root, r.eps)));
 }
 
 template <int N, typename P, typename G, bool MASTER>
@@ -149,15 +155,22 @@ __device__ __forceinline__ void update_vector(const Rule& r, const Now& now, flo
   v.load(static_cast<const float*>(t.v) + i);
   float wf[N], mf[N], vf[N];
 #pragma unroll
+  for (int e = 0; e < N; e += 2) {
+    constexpr int NEXT = N > 1 ? 1 : 0;
+    Pair m2 = Pair::of(m.get(e), m.get(e + NEXT)), v2 = Pair::of(v.get(e), v.get(e + NEXT));
+    average(r, now, Pair::of(g.get(e), g.get(e + NEXT)), m2, v2);
+    const float2 mm = m2.get(), vv = v2.get();
+    mf[e] = mm.x, vf[e] = vv.x;
+    if constexpr (N > 1) mf[e + 1] = mm.y, vf[e + 1] = vv.y;
+  }
+#pragma unroll
   for (int e = 0; e < N; ++e) {
     if constexpr (MASTER) {
       wf[e] = w.get(e);
     } else {
       wf[e] = p.get(e);
     }
-    mf[e] = m.get(e);
-    vf[e] = v.get(e);
-    update(r, now, keep, g.get(e), mf[e], vf[e], wf[e]);
+    wf[e] = step_weight(r, now, keep, wf[e], mf[e], sqrtf(vf[e]));
   }
   m.set(mf);
   v.set(vf);
@@ -207,23 +220,37 @@ __device__ __forceinline__ uint32_t to_e4m3(float lo, float hi) {
   return r;
 }
 
-// a in [0, 448] to floor(a / step + u) step, u in [0, 1); NaN stays NaN.
-__device__ __forceinline__ float round_e4m3(float a, uint32_t u16) {
-  // the step is 2^-3 of a's power of two, 2^-9 at least
-  const uint32_t power = max(__float_as_uint(a) >> 23, 121u);  // 2^-6
-  const float step = __uint_as_float((power - 3u) << 23), inv = __uint_as_float((257u - power) << 23);
-  // times a power of two is exact
-  const float q = floorf(__fadd_rn(a * inv, static_cast<float>(u16) * 0x1p-16f)) * step;
-  return q > E4M3_MAX ? E4M3_MAX : q;
+// Larger and smaller of two values; NaN wins.
+__device__ __forceinline__ float larger(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
-
-// Larger of two magnitudes; NaN wins.
-__device__ __forceinline__ float larger(float a, float b) { return b > a || b != b ? b : a; }
+__device__ __forceinline__ float smaller(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 
 __device__ __forceinline__ float warp_larger(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = larger(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
+}
+
+// Two a in [0, 448] to floor(a / step + u) step; NaN stays NaN.  step: 2^-3 of a's power of two, 2^-9 at least.  u:
+// numbers in [1, 2), whose 16 bits behind the point are the random ones.
+__device__ __forceinline__ float2 round_e4m3(Pair a, float u_lo, float u_hi) {
+  constexpr uint32_t POWER = 0x7f800000u, THREE = 3u << 23, LEAST = 121u << 23, ONE_SQUARED = 254u << 23;
+  const float2 f = a.get();
+  const uint32_t lo = max(__float_as_uint(f.x) & POWER, LEAST) - THREE, hi = max(__float_as_uint(f.y) & POWER, LEAST) - THREE;
+  const Pair step = Pair::of(__uint_as_float(lo), __uint_as_float(hi));
+  const Pair inv = Pair::of(__uint_as_float(ONE_SQUARED - lo), __uint_as_float(ONE_SQUARED - hi));  // powers of two: exact
+  const Pair u = add(Pair::of(u_lo, u_hi), Pair::both(-1.0f));
+  // below 2^22 a sum with 2^23 rounded down is the floor
+  const Pair q = add(add_down(add(mul(a, inv), u), Pair::both(0x1p23f)), Pair::both(-0x1p23f));
+  const float2 r = mul(q, step).get();
+  return make_float2(smaller(r.x, E4M3_MAX), smaller(r.y, E4M3_MAX));
 }
 
 // The n values (n <= 256) of one block from element `at` of t on, by a warp.
@@ -264,43 +291,54 @@ __device__ __forceinline__ void update_block(const Rule& r, const Now& now, floa
       }
     }
   }
-  const float ms = t.ms[block], rs = t.rs[block];
-  float mf[VEC], rf[VEC], wf[VEC], m_most = 0.0f, r_most = 0.0f;
+  const Pair ms = Pair::both(t.ms[block]), rs = Pair::both(t.rs[block]);
+  Pair m2[VEC / 2], r2[VEC / 2];
+  float wf[VEC], m_most = 0.0f, r_most = 0.0f;
 #pragma unroll
   for (int e = 0; e < VEC; e += 2) {
     const float2 a = from_e4m3(mq[e / 4] >> (8 * (e & 3))), b = from_e4m3(rq[e / 4] >> (8 * (e & 3)));
-    mf[e] = a.x * ms, mf[e + 1] = a.y * ms, rf[e] = b.x * rs, rf[e + 1] = b.y * rs;
-  }
+    Pair m = mul(Pair::of(a.x, a.y), ms), v = mul(Pair::of(b.x, b.y), rs);
+    v = mul(v, v);
+    average(r, now, Pair::of(g.get(e), g.get(e + 1)), m, v);
+    const float2 mm = m.get(), vv = v.get();
+    const float root[2] = {__fsqrt_rn(vv.x), __fsqrt_rn(vv.y)};
+    const float mean[2] = {mm.x, mm.y};
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) {
-    if constexpr (MASTER) {
-      wf[e] = w.get(e);
-    } else {
-      wf[e] = p.get(e);
+    for (int h = 0; h < 2; ++h) {
+      if constexpr (MASTER) {
+        wf[e + h] = w.get(e + h);
+      } else {
+        wf[e + h] = p.get(e + h);
+      }
+      wf[e + h] = step_weight(r, now, keep, wf[e + h], mean[h], root[h]);
+      // (elements behind the tensor's end are zeros, and so are their states)
+      m_most = larger(m_most, fabsf(mean[h]));
+      r_most = larger(r_most, root[h]);
     }
-    float v = rf[e] * rf[e];
-    rf[e] = update(r, now, keep, g.get(e), mf[e], v, wf[e]);
-    if (e < mine) {
-      m_most = larger(m_most, fabsf(mf[e]));
-      r_most = larger(r_most, rf[e]);
-    }
+    m2[e / 2] = m;
+    r2[e / 2] = Pair::of(root[0], root[1]);
   }
   m_most = warp_larger(m_most);
   r_most = warp_larger(r_most);
   const bool m_none = m_most < BLOCK_MIN, r_none = r_most < BLOCK_MIN;
-  const float m_inv = m_none ? 0.0f : E4M3_MAX / m_most, r_inv = r_none ? 0.0f : E4M3_MAX / r_most;
+  const Pair m_inv = Pair::both(m_none ? 0.0f : __frcp_rn(m_most) * E4M3_MAX);
+  const Pair r_inv = Pair::both(r_none ? 0.0f : __frcp_rn(r_most) * E4M3_MAX);
   const uint64_t place = static_cast<uint64_t>(t.first_block + block) * CCE_ADAMW_BLOCK + lane * VEC;
   const uint32_t key = mix(now.key ^ static_cast<uint32_t>(place >> 32));
   float mo[VEC], ro[VEC];
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) {
-    const uint32_t word = mix((static_cast<uint32_t>(place) + e) ^ key);
-    float a = fabsf(mf[e]) * m_inv, b = rf[e] * r_inv;
-    a = a > E4M3_MAX ? E4M3_MAX : a;
-    b = b > E4M3_MAX ? E4M3_MAX : b;
-    mo[e] = copysignf(round_e4m3(a, word & 0xffffu), mf[e]);
-    const float q = round_e4m3(b, word >> 16);
-    ro[e] = b > 0.0f && q < E4M3_MIN ? E4M3_MIN : q;
+  for (int e = 0; e < VEC; e += 2) {
+    const uint32_t x = mix((static_cast<uint32_t>(place) + e) ^ key), y = mix((static_cast<uint32_t>(place) + e + 1) ^ key);
+    const float2 mm = m2[e / 2].get();
+    const float2 a = mul(Pair::of(fabsf(mm.x), fabsf(mm.y)), m_inv).get(), b = mul(r2[e / 2], r_inv).get();
+    // 16 bits behind the point of 1.0
+    const auto low = [](uint32_t w) { return __uint_as_float((w & 0xffffu) << 7 | 0x3f800000u); };
+    const auto high = [](uint32_t w) { return __uint_as_float(w >> 9 & 0x7fff80u | 0x3f800000u); };
+    const float2 mr = round_e4m3(Pair::of(smaller(a.x, E4M3_MAX), smaller(a.y, E4M3_MAX)), low(x), low(y));
+    const float2 rr = round_e4m3(Pair::of(smaller(b.x, E4M3_MAX), smaller(b.y, E4M3_MAX)), high(x), high(y));
+    mo[e] = copysignf(mr.x, mm.x), mo[e + 1] = copysignf(mr.y, mm.y);
+    // a positive root stays one
+    ro[e] = larger(rr.x, b.x > 0.0f ? E4M3_MIN : 0.0f), ro[e + 1] = larger(rr.y, b.y > 0.0f ? E4M3_MIN : 0.0f);
   }
   uint32_t mw[2], rw[2];
 #pragma unroll
@@ -327,8 +365,8 @@ __device__ __forceinline__ void update_block(const Rule& r, const Now& now, floa
     }
   }
   if (lane == 0) {
-    t.ms[block] = m_none ? 0.0f : m_most / E4M3_MAX;
-    t.rs[block] = r_none ? 0.0f : r_most / E4M3_MAX;
+    t.ms[block] = m_none ? 0.0f : m_most * (1.0f / E4M3_MAX);
+    t.rs[block] = r_none ? 0.0f : r_most * (1.0f / E4M3_MAX);
   }
 }
 

@@ -232,6 +232,11 @@ __device__ __forceinline__ Pair add(Pair a, Pair b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
   return r;
 }
+__device__ __forceinline__ Pair add_down(Pair a, Pair b) {  // rounded towards minus infinity
+  Pair r;
+  asm("add.rm.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
 __device__ __forceinline__ Pair mul(Pair a, Pair b) {
   Pair r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));

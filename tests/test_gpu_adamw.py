@@ -131,25 +131,31 @@ def test_step_and_rate_on_the_device(cce, t):
 
 
 @pytest.mark.parametrize("fraction", [0.3, 2.0, math.inf])
-@pytest.mark.parametrize("bits", [8, 32])
-def test_clipping_on_the_way(cce, fraction, bits):
-    """The same bits as clipping the gradients first, where those are fp32."""
+def test_clipping_on_the_way(cce, fraction):
+    """The factor is a quotient of the fp32 norm: two roundings more for each gradient."""
     p, g, m, v = make(3, [(500, 5), (4096,)], F32, F32)
     norm = cce.cce_grad_norm(g)
     limit = fraction * norm.item()
-    clipped = [torch.empty_like(t) for t in g]
-    cce.cce_clip_grads(g, limit, out=clipped)
-    outs = []
-    for grads, more in ((g, dict(grad_norm=norm, max_norm=limit)), (clipped, {})):
-        a = [t.clone() for t in p]
-        if bits == 32:
-            s = [[t.clone() for t in m], [t.clone() for t in v]]
-            cce.cce_adamw_step(a, grads, *s, 5, **HYPER, **more)
-        else:
-            s = eight_bit_state(cce, p)
-            cce.cce_adamw8_step(a, grads, *s, 5, **HYPER, **more)
-        outs.append(a + [t.view(torch.uint8) if t.dtype == F8 else t for x in s for t in x])
-    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    factor = min(1.0, limit / (norm.item() + 1e-6))
+    refs = [reference(a.double(), b, c.double(), d.double(), 5, HYPER["lr"], HYPER["betas"], HYPER["eps"],
+                      HYPER["weight_decay"], factor) for a, b, c, d in zip(p, g, m, v)]
+    cce.cce_adamw_step(p, g, m, v, 5, **HYPER, grad_norm=norm, max_norm=limit)
+    for i, (w1, m1, v1, w_terms, m_terms) in enumerate(refs):
+        close(p[i], w1, w_terms, "param")
+        close(m[i], m1, m_terms, "m")
+        close(v[i], v1, v1, "v")
+    p, g, _, _ = make(3, [(500, 5), (4096,)], F32, F32)
+    state, place = eight_bit_state(cce, p), 0
+    refs = [reference(padded(a), padded(b), 0.0 * padded(a), 0.0 * padded(a), 5, HYPER["lr"], HYPER["betas"], HYPER["eps"],
+                      HYPER["weight_decay"], factor) for a, b in zip(p, g)]
+    cce.cce_adamw8_step(p, g, *state, 5, **HYPER, grad_norm=norm, max_norm=limit)
+    for i, (w1, m1, v1, w_terms, m_terms) in enumerate(refs):
+        n = p[i].numel()
+        words = words_of(0, 5, place, w1.numel())
+        place += w1.numel()
+        close(p[i].reshape(-1), w1.reshape(-1)[:n], w_terms.reshape(-1)[:n], "param")
+        check_held(state[0][i], state[1][i], m1, m_terms, words & 0xFFFF, False, "m")
+        check_held(state[2][i], state[3][i], v1.sqrt(), v1.sqrt(), words >> 16, True, "root of v")
 
 
 def test_norms_that_are_not_finite(cce):
@@ -182,9 +188,15 @@ def mix(x):
     return x ^ (x >> 16)
 
 
-def padded(t, fill=0.0):
+def words_of(seed, t, place, n):
+    """The random words of n values in whole blocks from `place` on, below 2^32."""
+    at = torch.arange(n, device="cuda").view(-1, 256) + place
+    return mix(at ^ mix(mix(mix(seed) ^ t) ^ 0))
+
+
+def padded(t):
     n = t.numel()
-    flat = torch.full((-(-n // 256) * 256,), fill, dtype=torch.float64, device="cuda")
+    flat = torch.zeros(-(-n // 256) * 256, dtype=torch.float64, device="cuda")
     flat[:n] = t.double().reshape(-1)
     return flat.view(-1, 256)
 
@@ -237,9 +249,8 @@ def test_update_in_8_bits(cce, shapes, p_type, g_type, master, offset):
         cce.cce_adamw8_step(p, g, *state, t, masters=masters, seed=seed, **HYPER)
         for i, (w1, m1, v1, w_terms, m_terms) in enumerate(refs):
             n = p[i].numel()
-            at = torch.arange(w1.numel(), device="cuda").view(-1, 256) + place
+            words = words_of(seed, t, place, w1.numel())
             place += w1.numel()
-            words = mix((at & 0xFFFFFFFF) ^ mix(mix(mix(seed) ^ t) ^ 0))
             close(p[i].reshape(-1), w1.reshape(-1)[:n], w_terms.reshape(-1)[:n], "param")
             check_held(state[0][i], state[1][i], m1, m_terms, words & 0xFFFF, False, "m")
             check_held(state[2][i], state[3][i], v1.sqrt(), v1.sqrt(), words >> 16, True, "root of v")
