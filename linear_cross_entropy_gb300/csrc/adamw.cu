@@ -72,6 +72,7 @@ struct Rule {
   const float* norm;         // may be null
   float max_norm, eps_norm;
   uint32_t seed, t;
+  float one;  // 1
 };
 static_assert(sizeof(Batch<MAX_TENSORS>) + sizeof(Rule) <= 32764, "kernel parameters");
 
@@ -128,11 +129,13 @@ __device__ __forceinline__ Now now_of(const Rule& r) {
   return n;
 }
 
-// Two gradients' m and v.
+// Two gradients' m and v.  The sums are fma(a, 1, b) with a 1 that the compiler does not know: it fuses a packed
+// product into a packed addition, both rounded, all the same.
 __device__ __forceinline__ void average(const Rule& r, const Now& now, Pair g, Pair& m, Pair& v) {
+  const Pair one = Pair::both(r.one);
   g = mul(g, Pair::both(now.factor));
-  m = add(mul(Pair::both(r.beta1), m), mul(Pair::both(r.rest1), g));
-  v = add(mul(Pair::both(r.beta2), v), mul(mul(Pair::both(r.rest2), g), g));
+  m = fma(mul(Pair::both(r.beta1), m), one, mul(Pair::both(r.rest1), g));
+  v = fma(mul(Pair::both(r.beta2), v), one, mul(mul(Pair::both(r.rest2), g), g));
 }
 
 // The new weight.
@@ -220,15 +223,10 @@ __device__ __forceinline__ uint32_t to_e4m3(float lo, float hi) {
   return r;
 }
 
-// Larger and smaller of two values; NaN wins.
+// Larger of two values; NaN wins.
 __device__ __forceinline__ float larger(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float smaller(float a, float b) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
 
@@ -238,19 +236,21 @@ __device__ __forceinline__ float warp_larger(float v) {
   return v;
 }
 
-// Two a in [0, 448] to floor(a / step + u) step; NaN stays NaN.  step: 2^-3 of a's power of two, 2^-9 at least.  u:
-// numbers in [1, 2), whose 16 bits behind the point are the random ones.
-__device__ __forceinline__ float2 round_e4m3(Pair a, float u_lo, float u_hi) {
+// 16 random bits as a number in [1, 2).
+__device__ __forceinline__ float behind_one(uint32_t u16) { return __uint_as_float(u16 * 128u + 0x3f800000u); }
+
+// Two a in [0, 448] to floor(a / step + u - 1) step; NaN stays NaN.  step: 2^-3 of a's power of two, 2^-9 at least; u
+// from behind_one().  An a that roundings brought above 448, by 2^-22 of it at most, becomes 448 all the same: a / step
+// is then below 14 + 2^-18, and u - 1 at most 1 - 2^-16.
+__device__ __forceinline__ float2 round_e4m3(float a_lo, float a_hi, float u_lo, float u_hi) {
   constexpr uint32_t POWER = 0x7f800000u, THREE = 3u << 23, LEAST = 121u << 23, ONE_SQUARED = 254u << 23;
-  const float2 f = a.get();
-  const uint32_t lo = max(__float_as_uint(f.x) & POWER, LEAST) - THREE, hi = max(__float_as_uint(f.y) & POWER, LEAST) - THREE;
+  const uint32_t lo = max(__float_as_uint(a_lo) & POWER, LEAST) - THREE, hi = max(__float_as_uint(a_hi) & POWER, LEAST) - THREE;
   const Pair step = Pair::of(__uint_as_float(lo), __uint_as_float(hi));
   const Pair inv = Pair::of(__uint_as_float(ONE_SQUARED - lo), __uint_as_float(ONE_SQUARED - hi));  // powers of two: exact
   const Pair u = add(Pair::of(u_lo, u_hi), Pair::both(-1.0f));
   // below 2^22 a sum with 2^23 rounded down is the floor
-  const Pair q = add(add_down(add(mul(a, inv), u), Pair::both(0x1p23f)), Pair::both(-0x1p23f));
-  const float2 r = mul(q, step).get();
-  return make_float2(smaller(r.x, E4M3_MAX), smaller(r.y, E4M3_MAX));
+  const Pair q = add(add_down(fma(Pair::of(a_lo, a_hi), inv, u), Pair::both(0x1p23f)), Pair::both(-0x1p23f));
+  return mul(q, step).get();
 }
 
 // The n values (n <= 256) of one block from element `at` of t on, by a warp.
@@ -321,21 +321,16 @@ __device__ __forceinline__ void update_block(const Rule& r, const Now& now, floa
   m_most = warp_larger(m_most);
   r_most = warp_larger(r_most);
   const bool m_none = m_most < BLOCK_MIN, r_none = r_most < BLOCK_MIN;
-  const Pair m_inv = Pair::both(m_none ? 0.0f : __frcp_rn(m_most) * E4M3_MAX);
-  const Pair r_inv = Pair::both(r_none ? 0.0f : __frcp_rn(r_most) * E4M3_MAX);
+  const float m_inv = m_none ? 0.0f : __frcp_rn(m_most) * E4M3_MAX, r_inv = r_none ? 0.0f : __frcp_rn(r_most) * E4M3_MAX;
   const uint64_t place = static_cast<uint64_t>(t.first_block + block) * CCE_ADAMW_BLOCK + lane * VEC;
   const uint32_t key = mix(now.key ^ static_cast<uint32_t>(place >> 32));
   float mo[VEC], ro[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; e += 2) {
     const uint32_t x = mix((static_cast<uint32_t>(place) + e) ^ key), y = mix((static_cast<uint32_t>(place) + e + 1) ^ key);
-    const float2 mm = m2[e / 2].get();
-    const float2 a = mul(Pair::of(fabsf(mm.x), fabsf(mm.y)), m_inv).get(), b = mul(r2[e / 2], r_inv).get();
-    // 16 bits behind the point of 1.0
-    const auto low = [](uint32_t w) { return __uint_as_float((w & 0xffffu) << 7 | 0x3f800000u); };
-    const auto high = [](uint32_t w) { return __uint_as_float(w >> 9 & 0x7fff80u | 0x3f800000u); };
-    const float2 mr = round_e4m3(Pair::of(smaller(a.x, E4M3_MAX), smaller(a.y, E4M3_MAX)), low(x), low(y));
-    const float2 rr = round_e4m3(Pair::of(smaller(b.x, E4M3_MAX), smaller(b.y, E4M3_MAX)), high(x), high(y));
+    const float2 mm = m2[e / 2].get(), b = mul(r2[e / 2], Pair::both(r_inv)).get();
+    const float2 mr = round_e4m3(fabsf(mm.x) * m_inv, fabsf(mm.y) * m_inv, behind_one(x & 0xffffu), behind_one(y & 0xffffu));
+    const float2 rr = round_e4m3(b.x, b.y, behind_one(x >> 16), behind_one(y >> 16));
     mo[e] = copysignf(mr.x, mm.x), mo[e + 1] = copysignf(mr.y, mm.y);
     // a positive root stays one
     ro[e] = larger(rr.x, b.x > 0.0f ? E4M3_MIN : 0.0f), ro[e + 1] = larger(rr.y, b.y > 0.0f ? E4M3_MIN : 0.0f);
@@ -581,6 +576,7 @@ cce_status cce_adamw_step(const cce_adamw_tensor* tensors, int64_t n_tensors, in
   r.eps_norm = o->eps_norm;
   r.seed = o->seed;
   r.t = static_cast<uint32_t>(o->step);
+  r.one = 1.0f;
   // four rounds of a block, one where that leaves blocks without work
   const int grid = sms * BLOCKS_PER_SM;
   Call c{tensors, n_tensors, eight, total >= int64_t(4) * grid * ROUND ? 4 * ROUND : ROUND, grid, r,
