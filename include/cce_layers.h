@@ -18,10 +18,12 @@
  * are exact in fp32 and are summed in fp32 on the tensor cores.  x and weights
  * start on 16 bytes and have pitches of a multiple of 8 elements, at least K, that
  * are below 2^31; what lies between a row's end and the next row's start is not
- * read into results and may hold anything.  Other matrices need the alignment of
- * their element alone.
- * Sizes: M >= 0 rows, N >= 1 outputs and K >= 1 inputs of a layer, all < 2^31 - 512,
- * any two of them multiplied < 2^45.  Workspaces start on 256 bytes.
+ * read into results and may hold anything (whole aligned words of 16 bytes that hold
+ * an element are read).  Other matrices need the alignment of their element alone, and
+ * pitches below 2^30.
+ * Sizes: M >= 0 rows, < 2^31 - 512, N >= 1 outputs and K >= 1 inputs of a layer, both
+ * < 2^30, any two of the three multiplied < 2^45.  Workspaces start on 256 bytes; where
+ * a query gives 16, none is needed and it may be NULL.
  * M = 0 is fine: nothing is launched, or zero weight gradients are written.
  *
  * Activations
@@ -59,7 +61,7 @@ cce_status cce_linear_forward(const void* x, int64_t x_pitch, const void* weight
                               int64_t M, int64_t N, int64_t K, void* y, int64_t y_pitch, int y_type, void* z,
                               int64_t z_pitch, void* workspace, size_t ws_bytes, void* stream);
 
-/* Bytes of workspace (0 for invalid sizes; at least 16 otherwise).  Pure host arithmetic; needs no GPU. */
+/* Bytes of workspace (0 for invalid sizes; 16 where none is needed).  Pure host arithmetic; needs no GPU. */
 size_t cce_linear_forward_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /*

@@ -30,7 +30,8 @@ NATIVE = os.path.join(PKG, "_native.so")
 BUILT_FOR = os.path.join(BUILD, "native_for.txt")
 COMMAND = "python linear_cross_entropy_gb300/build.py"
 SOURCES = ("cce_api.cu", "gemm_kernels.cu", "cce_noalloc.cu", "cce_sort.cu", "cce_flce.cu", "grad_clip.cu",
-           "norm_api.cu", "layers_api.cu", "linear_gemm.cu", "linear_few.cu", "linear_pass.cu", "adamw.cu") + tuple(f"norm_{p}_{t}.cu" for p in ("fwd", "bwd")
+           "norm_api.cu", "layers_api.cu", "linear_gemm.cu", "linear_few.cu", "linear_pass.cu", "adamw.cu", "linear_gemm_relu.cu",
+           "linear_gemm_gelu.cu", "linear_gemm_gelu_tanh.cu", "linear_gemm_silu.cu") + tuple(f"norm_{p}_{t}.cu" for p in ("fwd", "bwd")
                                   for t in ("bf16", "f16", "f32", "f32_bf16", "f32_f16"))
 BINDINGS = ("binding.cpp", "binding_layers.cpp", "binding_optim.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

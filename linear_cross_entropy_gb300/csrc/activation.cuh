@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "../../include/cce_layers.h"
+#include "elements.cuh"
 
 namespace cce {
 
@@ -50,14 +51,23 @@ __device__ __forceinline__ float gelu_gate(float z) {
   return z < 0.0f ? s : 1.0f - s;
 }
 
-// -0 at minus infinity, as the limit is.
+// Every activation but relu vanishes towards minus infinity: from -1e30 on, where its gate is 0, z counts as that, or it
+// would be infinity times 0.  (As a choice between results the compiler makes a branch of it, and 16 activations
+// of a thread run one after another: gelu took 1,600 cycles and not some 300.)  A NaN stays one.
+__device__ __forceinline__ float from_below(float z) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(z), "f"(-1e30f));
+  return r;
+}
+
 template <int ACT>
 __device__ __forceinline__ float activate(float z) {
   if constexpr (ACT == CCE_ACT_RELU) return z < 0.0f ? 0.0f : z;  // a NaN stays one
-  if constexpr (ACT == CCE_ACT_GELU) return z == -INFINITY ? -0.0f : z * gelu_gate(z);
-  if constexpr (ACT == CCE_ACT_GELU_TANH) return z == -INFINITY ? -0.0f : z * gelu_tanh_gate(z);
-  if constexpr (ACT == CCE_ACT_SILU) return z == -INFINITY ? -0.0f : z * logistic(z);
-  return z;
+  if constexpr (ACT == CCE_ACT_NONE) return z;
+  z = from_below(z);
+  if constexpr (ACT == CCE_ACT_GELU) return z * gelu_gate(z);
+  if constexpr (ACT == CCE_ACT_GELU_TANH) return z * gelu_tanh_gate(z);
+  return z * logistic(z);
 }
 
 // f(z) and f'(z).  The terms z f'' of infinite z vanish: z is held within +-200, where every gate is 0 or 1 to the last bit.
@@ -82,6 +92,68 @@ __device__ __forceinline__ float2 activate_both(float z) {
     return make_float2(activate<ACT>(z), s * fmaf(c, 1.0f - s, 1.0f));
   }
   return make_float2(z, 1.0f);
+}
+
+// ------------------------------------------------------------- in pairs
+// The forward's activations, two at a time in packed fp32: reciprocals and powers of two share one slow unit of an SM,
+// so that only one of them is taken there.
+
+// 1 / (1 + 2^x).  2^x is the Taylor polynomial of degree 6 of 2^f, |f| <= 1/2 (within 1.2e-7), times 2^n; at x = 128
+// and above it is infinite and the result 0.
+__device__ __forceinline__ Pair logistic_of_power(Pair x) {
+  constexpr float ROUND = 12582912.0f;  // 1.5 2^23: adding it leaves the nearest integer in the low bits
+  const float2 v = x.get();
+  const Pair c = Pair::of(fminf(fmaxf(v.x, -126.0f), 128.0f), fminf(fmaxf(v.y, -126.0f), 128.0f));
+  const Pair t = add(c, Pair::both(ROUND));
+  const Pair f = add(c, mul(add(t, Pair::both(-ROUND)), Pair::both(-1.0f)));
+  Pair s = fma(Pair::both(1.5403530e-4f), f, Pair::both(1.3333558e-3f));
+  s = fma(s, f, Pair::both(9.6181291e-3f));
+  s = fma(s, f, Pair::both(5.5504109e-2f));
+  s = fma(s, f, Pair::both(2.4022651e-1f));
+  s = fma(s, f, Pair::both(6.9314718e-1f));
+  const float2 p = fma(s, f, Pair::both(1.0f)).get(), n = t.get();
+  const auto scaled = [](float m, float e) { return __uint_as_float(__float_as_uint(e) * (1u << 23) + __float_as_uint(m)); };
+  const float2 d = add(Pair::of(scaled(p.x, n.x), scaled(p.y, n.y)), Pair::both(1.0f)).get();
+  return Pair::of(reciprocal_fast(d.x), reciprocal_fast(d.y));
+}
+
+// The normal distribution function by formula 7.1.28 of the Handbook: erfc(x) = (1 + a1 x + ... + a6 x^6)^-16, x >= 0,
+// within 3e-7.
+__device__ __forceinline__ Pair normal_pair(Pair z) {
+  constexpr float R = 0.70710678f;  // x = R |z|, and the powers of R go into the coefficients
+  const float2 v = z.get();
+  const Pair m = Pair::of(fabsf(v.x), fabsf(v.y));
+  Pair s = fma(Pair::both(0.0000430638f * R * R * R * R * R * R), m, Pair::both(0.0002765672f * R * R * R * R * R));
+  s = fma(s, m, Pair::both(0.0001520143f * R * R * R * R));
+  s = fma(s, m, Pair::both(0.0092705272f * R * R * R));
+  s = fma(s, m, Pair::both(0.0422820123f * R * R));
+  s = fma(s, m, Pair::both(0.0705230784f * R));
+  s = fma(s, m, Pair::both(1.0f));
+  s = mul(s, s);
+  s = mul(s, s);
+  s = mul(s, s);
+  const float2 d = mul(s, s).get();
+  const float lo = 0.5f * reciprocal_fast(d.x), hi = 0.5f * reciprocal_fast(d.y);
+  return Pair::of(v.x < 0.0f ? lo : 1.0f - lo, v.y < 0.0f ? hi : 1.0f - hi);
+}
+
+template <int ACT>
+__device__ __forceinline__ void activate_pair(float& lo, float& hi) {
+  if constexpr (ACT == CCE_ACT_NONE || ACT == CCE_ACT_RELU) {
+    lo = activate<ACT>(lo);
+    hi = activate<ACT>(hi);
+  } else {
+    const Pair z = Pair::of(from_below(lo), from_below(hi));
+    Pair gate;
+    if constexpr (ACT == CCE_ACT_GELU) gate = normal_pair(z);
+    if constexpr (ACT == CCE_ACT_SILU) gate = logistic_of_power(mul(z, Pair::both(-LOG2_E)));
+    if constexpr (ACT == CCE_ACT_GELU_TANH)
+      gate = logistic_of_power(
+          mul(z, fma(mul(z, z), Pair::both(-2.0f * LOG2_E * GELU_C3), Pair::both(-2.0f * LOG2_E * GELU_C))));
+    const float2 y = mul(z, gate).get();
+    lo = y.x;
+    hi = y.y;
+  }
 }
 
 // One of the 16-bit operand types from fp32, to nearest even.

@@ -564,12 +564,14 @@ struct DeviceInfo {
   int sms = 0;
   int pair_clusters = 0;  // CTA pairs of the forward GEMM resident at once
   int linear_pairs = 0;   // and of the layers' GEMM
+  int32_t* linear_error = nullptr;  // its error word
 };
 std::mutex g_mu;
 DeviceInfo g_dev[64];
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
-cce_status device_check(int* sms, int* pair_clusters = nullptr, int* linear_pairs = nullptr) {
+cce_status device_check(int* sms, int* pair_clusters = nullptr, int* linear_pairs = nullptr,
+                        int32_t** linear_error = nullptr) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
     cudaGetLastError();
@@ -588,7 +590,7 @@ cce_status device_check(int* sms, int* pair_clusters = nullptr, int* linear_pair
     d.ok = (major == 10 && minor == 3);
     d.sms = sms;
     if (d.ok) {
-      if (prepare_gemm_kernels() != cudaSuccess || prepare_linear_gemm() != cudaSuccess) {
+      if (prepare_gemm_kernels() != cudaSuccess || prepare_linear_gemm(&d.linear_error) != cudaSuccess) {
         cudaGetLastError();
         return CCE_ERR_CUDA;
       }
@@ -612,6 +614,7 @@ cce_status device_check(int* sms, int* pair_clusters = nullptr, int* linear_pair
   *sms = d.sms;
   if (pair_clusters) *pair_clusters = d.pair_clusters;
   if (linear_pairs) *linear_pairs = d.linear_pairs;
+  if (linear_error) *linear_error = d.linear_error;
   return CCE_OK;
 }
 
@@ -709,12 +712,23 @@ cce_status cuda_status(cudaError_t e) {
 
 int device_ready(int* sms) { return device_check(sms); }
 
-int layers_device_ready(int* sms, int* pairs) { return device_check(sms, nullptr, pairs); }
+int layers_device_ready(int* sms, int* pairs, int32_t** error) { return device_check(sms, nullptr, pairs, error); }
 
 bool encode_operand(CUtensorMap* m, bool bf16, const void* p, uint64_t inner, uint64_t outer, uint64_t pitch,
                     uint32_t box_inner, uint32_t box_outer) {
   return make_tmap(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, p, inner, outer,
                    pitch, box_inner, box_outer);
+}
+
+bool encode_turns(CUtensorMap* m, bool bf16, const void* p, uint64_t inner, uint64_t outer, uint64_t pitch,
+                  uint64_t distance) {
+  cuuint64_t dims[4] = {inner, 16, 2, outer / 16};
+  cuuint64_t strides[3] = {pitch * 2, distance, 16 * pitch * 2};
+  cuuint32_t box[4] = {64, 16, 2, 4};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return g_encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(p),
+                  dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool encode_groups(CUtensorMap* m, bool bf16, const void* p, uint64_t inner, uint64_t outer, uint64_t pitch,

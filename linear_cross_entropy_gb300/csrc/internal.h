@@ -30,14 +30,18 @@ cudaError_t launch_selftest_pair_timeout(int32_t* dev_err, uint64_t timeout_ns, 
 // The current device is one the library runs on: its SM count, and the status
 // of the check (a cce_status).
 int device_ready(int* sms);
-// The same for the layers' products: also how many CTA pairs of their kernel fit on the device at once.
-int layers_device_ready(int* sms, int* pairs);
+// The same for the layers' products: also how many CTA pairs of their kernel fit on the device at once, and its error word.
+int layers_device_ready(int* sms, int* pairs, int32_t** error);
 // A 2-D tensor map over 16-bit values, 128-byte swizzle; after device_ready().
 bool encode_operand(CUtensorMap* m, bool bf16, const void* p, uint64_t inner, uint64_t outer, uint64_t pitch,
                     uint32_t box_inner, uint32_t box_outer);
 // The same rows (inner % 64 == 0) as {64, outer, inner / 64}, with boxes of {64, box_rows, groups}.
 bool encode_groups(CUtensorMap* m, bool bf16, const void* p, uint64_t inner, uint64_t outer, uint64_t pitch,
                    uint32_t box_rows, uint32_t groups);
+// 16-bit rows of two matrices `distance` bytes apart, in turns of 16: {inner, 16, 2, outer / 16} (outer % 16 == 0), with
+// boxes of {64, 16, 2, 4}.
+bool encode_turns(CUtensorMap* m, bool bf16, const void* p, uint64_t inner, uint64_t outer, uint64_t pitch,
+                  uint64_t distance);
 // Adds to cce_kernel_launch_count().
 void count_launches(int n);
 

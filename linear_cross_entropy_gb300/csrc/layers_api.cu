@@ -13,7 +13,10 @@ namespace cce {
 namespace {
 
 constexpr int64_t LIMIT = (int64_t(1) << 31) - 512;
+constexpr int64_t WIDTH = int64_t(1) << 30;   // of a row
 constexpr int64_t MATRIX = int64_t(1) << 45;  // elements of one
+
+constexpr size_t NO_WORKSPACE = 16;           // what the queries give where none is needed
 
 bool multiple(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(bytes) == 0; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -22,7 +25,7 @@ bool type_ok(int t) { return t == CCE_F32 || t == CCE_F16 || t == CCE_BF16; }
 bool operand_type(int t) { return t == CCE_F16 || t == CCE_BF16; }
 bool act_ok(int act) { return act >= CCE_ACT_NONE && act <= CCE_ACT_SILU; }
 bool sizes_ok(int64_t M, int64_t N, int64_t K) {
-  return M >= 0 && M < LIMIT && N >= 1 && N < LIMIT && K >= 1 && K < LIMIT && M * N < MATRIX && M * K < MATRIX &&
+  return M >= 0 && M < LIMIT && N >= 1 && N < WIDTH && K >= 1 && K < WIDTH && M * N < MATRIX && M * K < MATRIX &&
          N * K < MATRIX;
 }
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
@@ -184,6 +187,13 @@ size_t parts_bytes(const Shape* s, int n, bool gated) {
 }
 
 // ---------------------------------------------------------------- products
+struct Device {
+  int sms = 0, pairs = 0;
+  int32_t* error = nullptr;
+
+  cce_status ready() { return static_cast<cce_status>(layers_device_ready(&sms, &pairs, &error)); }
+};
+
 struct Operand {
   const void* p;
   int64_t pitch;
@@ -212,12 +222,12 @@ bool encode(CUtensorMap* m, bool bf16, const Operand& o, int K, int own, bool mn
 
 // The products in one launch, and the joins of those whose K is split.  `part`:
 // room for their partial sums.
-cce_status run_products(const Product* in, int n, bool gated, bool bf16, void* part, int sms, int pairs,
-                        cudaStream_t s, int* launches) {
+cce_status run_products(const Product* in, int n, bool gated, bool bf16, void* part, const Device& on, cudaStream_t s,
+                        int* launches) {
   Shape shapes[LIN_MAX_PROBLEMS];
   for (int q = 0; q < n; ++q) shapes[q] = in[q].s;
   const Plan plan = plan_of(shapes, n, gated);
-  if (plan.pair && pairs < 1) return CCE_ERR_CUDA;
+  if (plan.pair && on.pairs < 1) return CCE_ERR_CUDA;
   // the tensor maps are made by the driver, which wants this thread to have a context
   int device = 0;
   if (cudaGetDevice(&device) != cudaSuccess || cudaSetDevice(device) != cudaSuccess) return CCE_ERR_CUDA;
@@ -225,6 +235,7 @@ cce_status run_products(const Product* in, int n, bool gated, bool bf16, void* p
   LinArgs a{};
   a.problems = n;
   a.bf16 = bf16;
+  a.error = on.error;
   char* at = static_cast<char*>(part);
   int64_t items = 0;
   int widest = 0;
@@ -256,11 +267,21 @@ cce_status run_products(const Product* in, int n, bool gated, bool bf16, void* p
     p.part = reinterpret_cast<float*>(at);
     at += part_bytes(f.s, c, gated);
     p.e = f.e;
+    const bool rows_16 = f.e.y_type != CCE_F32 && multiple(f.e.y, 16) && f.e.y_pitch % 8 == 0;
+    const bool z_16 = !f.e.z[0] || (multiple(f.e.z[0], 16) && multiple(f.e.z[1], 16) && f.e.z_pitch % 8 == 0);
+    p.wide = c.splits == 1 && rows_16 && z_16 && p.I % 8 == 0;
     const int b_rows = plan.pair ? c.jt / 2 : c.jt;
     widest = std::max(widest, b_rows);
-    for (int m = 0; m < (gated ? 2 : parts); ++m) {
-      if (!encode(&p.a[m], bf16, f.a[m], f.s.K, p.I, f.a_mn, p.a_3d, bk, gated ? LIN_BI / 2 : LIN_BI))
-        return CCE_ERR_CUDA;
+    if (gated) {
+      const uintptr_t g = reinterpret_cast<uintptr_t>(f.a[0].p), u = reinterpret_cast<uintptr_t>(f.a[1].p);
+      p.up_first = u < g;
+      // one map over both weights, if their distance is one that a stride can have
+      p.a_4d = f.a[0].pitch == f.a[1].pitch && p.I % LIN_TURN == 0 && u != g && (u < g ? g - u : u - g) < (uint64_t(1) << 40) &&
+               encode_turns(&p.a[0], bf16, f.a[p.up_first].p, f.s.K, p.I, f.a[0].pitch, u < g ? g - u : u - g);
+      if (!p.a_4d) p.up_first = 0;
+    }
+    for (int m = 0; m < (gated ? 2 : parts) && !p.a_4d; ++m) {
+      if (!encode(&p.a[m], bf16, f.a[m], f.s.K, p.I, f.a_mn, p.a_3d, bk, gated ? LIN_TURN : LIN_BI)) return CCE_ERR_CUDA;
     }
     for (int m = 0; m < parts; ++m) {
       if (!encode(&p.b[m], bf16, f.b[m], f.s.K, p.J, f.s.b_mn, p.b_3d, bk, b_rows)) return CCE_ERR_CUDA;
@@ -270,12 +291,12 @@ cce_status run_products(const Product* in, int n, bool gated, bool bf16, void* p
   a.items = static_cast<int>(items);
   a.stage_bytes = (LIN_BI + widest) * static_cast<int>(bk) * 2;
   a.stages = std::min(LIN_MAX_STAGES, LIN_RING_BYTES / a.stage_bytes);
-  const int units = static_cast<int>(std::min<int64_t>(plan.pair ? pairs : sms, items));
+  const int units = static_cast<int>(std::min<int64_t>(plan.pair ? on.pairs : on.sms, items));
   cudaError_t e = launch_linear_gemm(a, plan.pair, gated, units, s);
   ++*launches;
   for (int q = 0; q < n && e == cudaSuccess; ++q) {
     if (a.p[q].splits == 1) continue;
-    e = launch_linear_join(a.p[q], gated, bf16, sms, s);
+    e = launch_linear_join(a.p[q], gated, bf16, on.sms, s);
     ++*launches;
   }
   return e == cudaSuccess ? CCE_OK : CCE_ERR_CUDA;
@@ -298,10 +319,11 @@ cce_status check_operand(const Matrix& m) {
 }
 cce_status check_matrix(const Matrix& m, bool optional = false) {
   if (!m.p) return optional || m.rows == 0 ? CCE_OK : CCE_ERR_NULL;
-  if (m.pitch < m.cols) return CCE_ERR_SHAPE;
+  if (m.pitch < m.cols || m.pitch >= (int64_t(1) << 30)) return CCE_ERR_SHAPE;
   return multiple(m.p, type_bytes(m.type)) ? CCE_OK : CCE_ERR_ALIGN;
 }
 cce_status check_workspace(const void* ws, size_t have, size_t need) {
+  if (need <= NO_WORKSPACE) return CCE_OK;
   if (!ws) return CCE_ERR_NULL;
   if (!multiple(ws, 256)) return CCE_ERR_ALIGN;
   return have < need ? CCE_ERR_WORKSPACE : CCE_OK;
@@ -315,21 +337,22 @@ cce_status first_of(S... s) {
 
 size_t forward_bytes(int64_t M, int64_t N, int64_t K, bool gated) {
   if (!sizes_ok(M, N, K)) return 0;
-  if (M <= LIN_FEW_ROWS) return 16;
+  if (M <= LIN_FEW_ROWS) return NO_WORKSPACE;
   const Shape s = shape_of(N, M, K, 1, false);
-  return std::max<size_t>(16, parts_bytes(&s, 1, gated));
+  return std::max<size_t>(NO_WORKSPACE, parts_bytes(&s, 1, gated));
 }
 
 cce_status forward(const Matrix& x, const Matrix* w, bool gated, int64_t M, int64_t N, int64_t K, const LinEpilogue& e,
                    void* ws, cudaStream_t stream) {
-  int sms = 0, pairs = 0, launches = 0;
-  cce_status st = static_cast<cce_status>(layers_device_ready(&sms, &pairs));
+  Device on;
+  int launches = 0;
+  cce_status st = on.ready();
   if (st != CCE_OK || M == 0) return st;
   const bool bf16 = x.type == CCE_BF16;
   if (M <= LIN_FEW_ROWS) {
     const LinFew f{{w[0].p, w[gated ? 1 : 0].p}, {w[0].pitch, w[gated ? 1 : 0].pitch}, x.p, x.pitch, static_cast<int>(N),
                    static_cast<int>(M), static_cast<int>(K), e};
-    st = launch_linear_few(f, gated, bf16, sms, stream) == cudaSuccess ? CCE_OK : CCE_ERR_CUDA;
+    st = launch_linear_few(f, gated, bf16, stream) == cudaSuccess ? CCE_OK : CCE_ERR_CUDA;
     ++launches;
   } else {
     Product p{};
@@ -337,7 +360,7 @@ cce_status forward(const Matrix& x, const Matrix* w, bool gated, int64_t M, int6
     for (int m = 0; m < (gated ? 2 : 1); ++m) p.a[m] = Operand{w[m].p, w[m].pitch};
     p.b[0] = Operand{x.p, x.pitch};
     p.e = e;
-    st = run_products(&p, 1, gated, bf16, ws, sms, pairs, stream, &launches);
+    st = run_products(&p, 1, gated, bf16, ws, on, stream, &launches);
   }
   count_launches(launches);
   return st;
@@ -355,7 +378,7 @@ BackwardShapes backward_shapes(int64_t M, int64_t N, int64_t K, int mats) {
 struct BackwardLayout {
   size_t dz, sums, parts;
   int64_t pitch;
-  size_t total() const { return std::max<size_t>(16, dz + sums + parts); }
+  size_t total() const { return std::max<size_t>(NO_WORKSPACE, dz + sums + parts); }
 };
 
 BackwardLayout backward_layout(int64_t M, int64_t N, int64_t K, int mats) {
@@ -387,7 +410,7 @@ LinEpilogue dense_out(void* y, int64_t pitch, int type) {
 
 // From the parts of dz to the gradients asked for.  weights, grad_w: mats of them.
 cce_status backward_products(const Operand* dz, const Matrix& x, const Matrix* w, int mats, int64_t M, int64_t N,
-                             int64_t K, void* grad_x, void* const* grad_w, void* parts, int sms, int pairs,
+                             int64_t K, void* grad_x, void* const* grad_w, void* parts, const Device& on,
                              cudaStream_t s, int* launches) {
   const BackwardShapes b = backward_shapes(M, N, K, mats);
   const int type = x.type;
@@ -410,7 +433,7 @@ cce_status backward_products(const Operand* dz, const Matrix& x, const Matrix* w
     p[n].a_mn = true;
     p[n++].e = dense_out(grad_x, K, type);
   }
-  return n == 0 ? CCE_OK : run_products(p, n, false, type == CCE_BF16, parts, sms, pairs, s, launches);
+  return n == 0 ? CCE_OK : run_products(p, n, false, type == CCE_BF16, parts, on, s, launches);
 }
 
 cce_status zero(void* p, size_t bytes, cudaStream_t s) {
@@ -485,8 +508,9 @@ cce_status cce_linear_backward(const void* grad_y, int64_t g_pitch, int y_type, 
       check_matrix({grad_weight, K, type, N, K}, true), check_matrix({grad_bias, N, bias_type, 1, N}, true),
       check_workspace(workspace, ws_bytes, backward_bytes(M, N, K, 1)));
   if (st != CCE_OK) return st;
-  int sms = 0, pairs = 0, launches = 0;
-  st = static_cast<cce_status>(layers_device_ready(&sms, &pairs));
+  Device on;
+  int launches = 0;
+  st = on.ready();
   if (st != CCE_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (M == 0)
@@ -514,10 +538,10 @@ cce_status cce_linear_backward(const void* grad_y, int64_t g_pitch, int y_type, 
     g.M = static_cast<int>(M);
     g.N = static_cast<int>(N);
     g.act = act;
-    if (launch_linear_grad(g, false, type == CCE_BF16, sms, s, &launches) != cudaSuccess) st = CCE_ERR_CUDA;
+    if (launch_linear_grad(g, false, type == CCE_BF16, on.sms, s, &launches) != cudaSuccess) st = CCE_ERR_CUDA;
   }
   if (st == CCE_OK)
-    st = backward_products(&dz, xm, &wm, 1, M, N, K, grad_x, &grad_weight, ws + l.dz + l.sums, sms, pairs, s,
+    st = backward_products(&dz, xm, &wm, 1, M, N, K, grad_x, &grad_weight, ws + l.dz + l.sums, on, s,
                            &launches);
   count_launches(launches);
   return st;
@@ -540,8 +564,9 @@ cce_status cce_gated_linear_backward(const void* grad_y, int64_t g_pitch, const 
       check_matrix({grad_up_weight, K, type, N, K}, true),
       check_workspace(workspace, ws_bytes, backward_bytes(M, N, K, 2)));
   if (st != CCE_OK) return st;
-  int sms = 0, pairs = 0, launches = 0;
-  st = static_cast<cce_status>(layers_device_ready(&sms, &pairs));
+  Device on;
+  int launches = 0;
+  st = on.ready();
   if (st != CCE_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (M == 0)
@@ -564,11 +589,11 @@ cce_status cce_gated_linear_backward(const void* grad_y, int64_t g_pitch, const 
   g.M = static_cast<int>(M);
   g.N = static_cast<int>(N);
   g.act = act;
-  if (launch_linear_grad(g, true, type == CCE_BF16, sms, s, &launches) != cudaSuccess) st = CCE_ERR_CUDA;
+  if (launch_linear_grad(g, true, type == CCE_BF16, on.sms, s, &launches) != cudaSuccess) st = CCE_ERR_CUDA;
   const Operand dz[2] = {{g.dz[0], l.pitch}, {g.dz[1], l.pitch}};
   void* grad_w[2] = {grad_gate_weight, grad_up_weight};
   if (st == CCE_OK)
-    st = backward_products(dz, xm, wm, 2, M, N, K, grad_x, grad_w, ws + l.dz, sms, pairs, s, &launches);
+    st = backward_products(dz, xm, wm, 2, M, N, K, grad_x, grad_w, ws + l.dz, on, s, &launches);
   count_launches(launches);
   return st;
 }

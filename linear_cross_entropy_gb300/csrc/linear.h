@@ -26,7 +26,8 @@ struct LinEpilogue {
 
 // out[j][i] = epilogue(sum over k of A(i, k) B(j, k)).  The sum may run over two
 // pairs of operands in turn (dx of a gated layer); gated forward: a[0] and a[1]
-// are the gate's and the up projection's weights, both against b[0].
+// are the gate's and the up projection's weights, both against b[0], in turns of 16
+// rows (a_4d: one map over both, whichever lies first in memory).
 // Tensor maps: an operand whose contiguous extent is a multiple of 64 comes in one
 // 3-D box a stage (its groups of 64 as the third dimension), another in 2-D boxes,
 // one a group.
@@ -38,11 +39,12 @@ struct LinProblem {
   int kb_first;  // blocks of K of the first part
   int kb_all;
   int8_t a_mn, b_mn;  // operand stored with its I (J) index contiguous
-  int8_t a_3d, b_3d;
+  int8_t a_3d, b_3d, a_4d, up_first;
   int jt;          // tile width in J
   int i_tiles, j_tiles, splits, kb_split;  // kb_split: blocks of K per split
   int group;       // i tiles that are walked together
   int items;       // i_tiles * j_tiles * splits
+  int wide;        // 16-bit results (and no partial sums) whose rows start on 16 bytes, I a multiple of 8
   float* part;     // splits > 1: [splits][GATED ? 2 : 1][J][I]
   LinEpilogue e;
 };
@@ -54,19 +56,30 @@ struct LinArgs {
   int items;
   int bf16;  // operands are bf16, else fp16
   int stages, stage_bytes;
+  int32_t* error;  // the device's error word (CCE_DEVERR_*)
 };
 
 constexpr int LIN_BI = 128;  // rows of the MMA a CTA: I extent of a tile (gated: 64 of each weight)
 // Blocks of K: a stage's depth.  A pair's loads are issued half as often with the deeper one.
 constexpr int lin_bk(bool pair) { return pair ? 128 : 64; }
+constexpr int LIN_TURN = 16;  // gated: rows of a weight after which the other's come
 constexpr int LIN_RING_BYTES = 192 * 1024;
 constexpr int LIN_MAX_STAGES = 10;
 
 // The launch as `units` persistent CTAs or CTA pairs.
 cudaError_t launch_linear_gemm(const LinArgs& a, bool pair, bool gated, int units, cudaStream_t s);
+cudaError_t launch_linear_gemm_relu(const LinArgs& a, bool pair, bool gated, int units, cudaStream_t s);
+cudaError_t launch_linear_gemm_gelu(const LinArgs& a, bool pair, bool gated, int units, cudaStream_t s);
+cudaError_t launch_linear_gemm_gelu_tanh(const LinArgs& a, bool pair, bool gated, int units, cudaStream_t s);
+cudaError_t launch_linear_gemm_silu(const LinArgs& a, bool pair, bool gated, int units, cudaStream_t s);
+cudaError_t prepare_linear_gemm_relu();
+cudaError_t prepare_linear_gemm_gelu();
+cudaError_t prepare_linear_gemm_gelu_tanh();
+cudaError_t prepare_linear_gemm_silu();
 // CTA pairs that are resident at once.
 int linear_pair_units(int sms);
-cudaError_t prepare_linear_gemm();
+// Once for a device; gives its error word.
+cudaError_t prepare_linear_gemm(int32_t** error);
 // The device's error word (CCE_DEVERR_*) of these kernels, taken and cleared behind `s`.
 cudaError_t take_linear_error(int32_t* word, cudaStream_t s);
 
@@ -83,7 +96,7 @@ struct LinFew {
   LinEpilogue e;
 };
 constexpr int LIN_FEW_ROWS = 16;
-cudaError_t launch_linear_few(const LinFew& a, bool gated, bool bf16, int sms, cudaStream_t s);
+cudaError_t launch_linear_few(const LinFew& a, bool gated, bool bf16, cudaStream_t s);
 
 // The element-wise part of the backward pass: dz = dy f'(z) (gated: dgate = dy u
 // f'(g) and dup = dy f(g)) in the operands' type, and the sums of dz over the rows.

@@ -11,7 +11,11 @@ namespace cce {
 template <int ACT, int M>
 __device__ __forceinline__ void activate_as(float (&z)[M]) {
 #pragma unroll
-  for (int u = 0; u < M; ++u) z[u] = activate<ACT>(z[u]);
+  for (int u = 0; u + 1 < M; u += 2) activate_pair<ACT>(z[u], z[u + 1]);
+  if constexpr (M % 2 != 0) {
+    float none = 0.0f;
+    activate_pair<ACT>(z[M - 1], none);
+  }
 }
 
 // The activation is uniform over a launch: one branch for M values.
@@ -32,34 +36,70 @@ __device__ __forceinline__ float load_scalar(const void* p, int type, int64_t i)
   return f[0];
 }
 
-// Loads and stores of a column's rows, `pitch` bytes apart.  They are volatile so that
-// they stay in order and each address is the last one and a pitch: with all addresses in
+// Loads and stores of a column's rows, a pitch apart.  They are volatile so that they
+// stay in order and each address is the last one and a pitch: with all addresses in
 // registers at once the epilogue spilled.
 __device__ __forceinline__ void store16(char* p, uint32_t v) {
-  asm volatile("{\n\t.reg .b16 h, g;\n\tmov.b32 {h, g}, %1;\n\tst.global.b16 [%0], h;\n\t}" ::"l"(p), "r"(v) : "memory");
+  asm volatile("{\n\t.reg .b16 h, g;\n\tmov.b32 {h, g}, %1;\n\tst.global.b16 [%0], h;\n\t}" ::"l"(p), "r"(v));
 }
 __device__ __forceinline__ void store16_high(char* p, uint32_t v) {
-  asm volatile("{\n\t.reg .b16 h, g;\n\tmov.b32 {h, g}, %1;\n\tst.global.b16 [%0], g;\n\t}" ::"l"(p), "r"(v) : "memory");
+  asm volatile("{\n\t.reg .b16 h, g;\n\tmov.b32 {h, g}, %1;\n\tst.global.b16 [%0], g;\n\t}" ::"l"(p), "r"(v));
 }
 __device__ __forceinline__ void store32(char* p, float v) {
-  asm volatile("st.global.f32 [%0], %1;" ::"l"(p), "f"(v) : "memory");
+  asm volatile("st.global.f32 [%0], %1;" ::"l"(p), "f"(v));
 }
 __device__ __forceinline__ uint32_t load16(const char* p) {
   uint16_t v;
-  asm volatile("ld.global.b16 %0, [%1];" : "=h"(v) : "l"(p) : "memory");
+  asm volatile("ld.global.b16 %0, [%1];" : "=h"(v) : "l"(p));
   return v;
 }
 __device__ __forceinline__ uint32_t load32(const char* p) {
   uint32_t v;
-  asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
   return v;
 }
 
+// A thread's place in the matrices of an epilogue, in registers: kernel parameters
+// behind a run-time index cost a load for each use.
+struct Column {
+  char *y = nullptr, *z = nullptr;
+  const char* res = nullptr;
+  uint32_t y_step = 0, z_step = 0, res_step = 0;  // bytes from row to row
+  float bias = 0.0f;
+  int act = 0;
+  bool bf16 = false, y32 = false, has_bias = false;
+
+  template <bool GATED>
+  __device__ __forceinline__ void start(const LinEpilogue& e, bool operands_bf16, int i, int j) {
+    bf16 = operands_bf16;
+    y32 = !GATED && e.y_type == CCE_F32;
+    act = e.act;
+    const uint32_t bytes = y32 ? 4 : 2;
+    y_step = static_cast<uint32_t>(e.y_pitch) * bytes;
+    y = static_cast<char*>(e.y) + static_cast<int64_t>(j) * y_step + static_cast<int64_t>(i) * bytes;
+    if (e.z[0]) {
+      z_step = static_cast<uint32_t>(e.z_pitch) * 2;
+      z = static_cast<char*>(e.z[0]) + static_cast<int64_t>(j) * z_step + static_cast<int64_t>(i) * 2;
+    }
+    if (!GATED && e.res) {
+      res_step = static_cast<uint32_t>(e.res_pitch) * bytes;
+      res = static_cast<const char*>(e.res) + static_cast<int64_t>(j) * res_step + static_cast<int64_t>(i) * bytes;
+    }
+    has_bias = !GATED && e.bias;
+    if (has_bias) bias = load_scalar(e.bias, e.bias_type, i);
+  }
+  __device__ __forceinline__ void skip(uint32_t rows) {
+    y += static_cast<uint64_t>(rows) * y_step;
+    if (z) z += static_cast<uint64_t>(rows) * z_step;
+    if (res) res += static_cast<uint64_t>(rows) * res_step;
+  }
+};
+
 // M values to rows of a 16-bit matrix, rounded to nearest even; the first n of them.
 template <bool FULL, int M>
-__device__ __forceinline__ void store_rows16(char* p, int64_t pitch, const uint32_t (&two)[(M + 1) / 2], int n) {
+__device__ __forceinline__ void store_rows16(char* p, uint32_t step, const uint32_t (&two)[(M + 1) / 2], int n) {
 #pragma unroll
-  for (int u = 0; u < M; ++u, p += pitch) {
+  for (int u = 0; u < M; ++u, p += step) {
     if (!FULL && u >= n) continue;
     if (u & 1) {
       store16_high(p, two[u / 2]);
@@ -70,7 +110,7 @@ __device__ __forceinline__ void store_rows16(char* p, int64_t pitch, const uint3
 }
 
 template <int M>
-__device__ __forceinline__ void put_rows16(void* base, int64_t pitch, int64_t at, bool bf16, const float (&f)[M], int n) {
+__device__ __forceinline__ void put_rows16(char* p, uint32_t step, bool bf16, const float (&f)[M], int n) {
   uint32_t two[(M + 1) / 2];
   if (bf16) {
 #pragma unroll
@@ -85,19 +125,17 @@ __device__ __forceinline__ void put_rows16(void* base, int64_t pitch, int64_t at
       two[u / 2] = *reinterpret_cast<const uint32_t*>(&h);
     }
   }
-  char* p = static_cast<char*>(base) + at * 2;
   if (n >= M) {
-    store_rows16<true, M>(p, pitch * 2, two, n);
+    store_rows16<true, M>(p, step, two, n);
   } else {
-    store_rows16<false, M>(p, pitch * 2, two, n);
+    store_rows16<false, M>(p, step, two, n);
   }
 }
 
 template <int M>
-__device__ __forceinline__ void put_rows32(void* base, int64_t pitch, int64_t at, const float (&f)[M], int n) {
-  char* p = static_cast<char*>(base) + at * 4;
+__device__ __forceinline__ void put_rows32(char* p, uint32_t step, const float (&f)[M], int n) {
 #pragma unroll
-  for (int u = 0; u < M; ++u, p += pitch * 4) {
+  for (int u = 0; u < M; ++u, p += step) {
     if (u < n) store32(p, f[u]);
   }
 }
@@ -107,23 +145,21 @@ template <int M>
 struct Residual {
   uint32_t raw[M];
 
-  __device__ __forceinline__ void load(const LinEpilogue& e, int i, int j0, int n) {
-    const int64_t at = static_cast<int64_t>(j0) * e.res_pitch + i;
-    if (e.y_type == CCE_F32) {
-      const char* p = static_cast<const char*>(e.res) + at * 4;
+  __device__ __forceinline__ void load(const Column& c, int n) {
+    const char* p = c.res;
+    if (c.y32) {
 #pragma unroll
-      for (int u = 0; u < M; ++u, p += e.res_pitch * 4) raw[u] = u < n ? load32(p) : 0u;
+      for (int u = 0; u < M; ++u, p += c.res_step) raw[u] = u < n ? load32(p) : 0u;
     } else {
-      const char* p = static_cast<const char*>(e.res) + at * 2;
 #pragma unroll
-      for (int u = 0; u < M; ++u, p += e.res_pitch * 2) raw[u] = u < n ? load16(p) : 0u;
+      for (int u = 0; u < M; ++u, p += c.res_step) raw[u] = u < n ? load16(p) : 0u;
     }
   }
-  __device__ __forceinline__ void add_to(const LinEpilogue& e, bool bf16, float (&f)[M]) const {
-    if (e.y_type == CCE_F32) {
+  __device__ __forceinline__ void add_to(const Column& c, float (&f)[M]) const {
+    if (c.y32) {
 #pragma unroll
       for (int u = 0; u < M; ++u) f[u] += __uint_as_float(raw[u]);
-    } else if (bf16) {
+    } else if (c.bf16) {
 #pragma unroll
       for (int u = 0; u < M; ++u) f[u] += __uint_as_float(raw[u] << 16);
     } else {
@@ -133,33 +169,30 @@ struct Residual {
   }
 };
 
-// Rows j0 .. j0 + min(n, M) - 1 of column i, all inside of the matrices.  z0: the
-// product with x (gated: the gate's), z1: gated: the up projection's; res: loaded if
-// there is a residual.
+// min(n, M) rows from the column's place on.  z0: the product with x (gated: the
+// gate's), z1: gated: the up projection's; res: loaded if there is a residual.
 template <bool GATED, int M>
-__device__ __forceinline__ void finish_column(const LinEpilogue& e, bool bf16, float bias, int i, int j0, int n,
-                                              float (&z0)[M], const float (&z1)[M], const Residual<M>& res) {
-  if (!GATED && e.bias) {
+__device__ __forceinline__ void finish_column(const LinEpilogue& e, const Column& c, int n, float (&z0)[M], const float (&z1)[M],
+                                              const Residual<M>& res) {
+  if (!GATED && c.has_bias) {
 #pragma unroll
-    for (int u = 0; u < M; ++u) z0[u] += bias;
+    for (int u = 0; u < M; ++u) z0[u] += c.bias;
   }
-  if (e.z[0]) {
-    const int64_t at = static_cast<int64_t>(j0) * e.z_pitch + i;
-    put_rows16(e.z[0], e.z_pitch, at, bf16, z0, n);
-    if (GATED) put_rows16(e.z[1], e.z_pitch, at, bf16, z1, n);
+  if (c.z) {
+    put_rows16(c.z, c.z_step, c.bf16, z0, n);
+    if (GATED) put_rows16(c.z + (static_cast<char*>(e.z[1]) - static_cast<char*>(e.z[0])), c.z_step, c.bf16, z1, n);
   }
-  activate_all(e.act, z0);
+  activate_all(c.act, z0);
   if (GATED) {
 #pragma unroll
     for (int u = 0; u < M; ++u) z0[u] *= z1[u];
-  } else if (e.res) {
-    res.add_to(e, bf16, z0);
+  } else if (c.res) {
+    res.add_to(c, z0);
   }
-  const int64_t at = static_cast<int64_t>(j0) * e.y_pitch + i;
-  if (!GATED && e.y_type == CCE_F32) {
-    put_rows32(e.y, e.y_pitch, at, z0, n);
+  if (!GATED && c.y32) {
+    put_rows32(c.y, c.y_step, z0, n);
   } else {
-    put_rows16(e.y, e.y_pitch, at, bf16, z0, n);
+    put_rows16(c.y, c.y_step, c.bf16, z0, n);
   }
 }
 

@@ -138,10 +138,11 @@ __global__ void __launch_bounds__(32 * WARPS, 2) few_kernel(const __grid_constan
     z0[0] += sums[v][0][r][j];
     if (GATED) z1[0] += sums[v][MATS - 1][r][j];
   }
-  const float bias = a.e.bias ? load_scalar(a.e.bias, a.e.bias_type, i) : 0.0f;
+  Column col;
+  col.start<GATED>(a.e, BF16, i, j);
   Residual<1> res;
-  if (!GATED && a.e.res) res.load(a.e, i, j, 1);
-  finish_column<GATED>(a.e, BF16, bias, i, j, 1, z0, z1, res);
+  if (col.res) res.load(col, 1);
+  finish_column<GATED>(a.e, col, 1, z0, z1, res);
 }
 static_assert(32 * WARPS == ROWS * LIN_FEW_ROWS, "one result a thread");
 
@@ -154,8 +155,7 @@ cudaError_t launch(const LinFew& a, bool gated, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_linear_few(const LinFew& a, bool gated, bool bf16, int sms, cudaStream_t s) {
-  (void)sms;
+cudaError_t launch_linear_few(const LinFew& a, bool gated, bool bf16, cudaStream_t s) {
   if (bf16) return a.J <= 8 ? launch<true, 1>(a, gated, s) : launch<true, 2>(a, gated, s);
   return a.J <= 8 ? launch<false, 1>(a, gated, s) : launch<false, 2>(a, gated, s);
 }

@@ -1,0 +1,751 @@
+// Persistent, warp-specialised tcgen05 GEMM of the layers in front of the head:
+//
+//   out[j][i] = epilogue(sum over k of A(i, k) B(j, k))
+//
+// A holds what becomes the contiguous index of the output (weights in the
+// forward pass, so that few tokens make narrow tiles and not empty MMA rows, and a
+// thread of the epilogue keeps its four biases in registers), B its rows (tokens).  Either may
+// be stored with k contiguous or with its own index contiguous:
+//
+//   forward          A = W  [N, K] along k       B = x  [M, K] along k
+//   dx = dz W        A = W  [N, K] along i = K   B = dz [M, N] along k = N
+//   dW = dz^T x      A = x  [M, K] along i = K   B = dz [M, N] along j = N
+//
+// Up to three products run in one launch (dx and both dW of a gated layer); dx of a
+// gated layer is one sum over two pairs of operands.  A gated forward's 128 MMA
+// rows are 64 of each weight in turns of 16, so that its loads and MMAs are those of a
+// layer twice as wide, and a thread of the epilogue has both values of an output.
+//
+// Roles (352 threads): lane 0 of warp 0 loads A, that of warp 10 B (TMA; a pair's stages
+// are 128 deep in K, a single CTA's 64, as many as fit in 192 KiB; one thread for both
+// needed 560 of a stage's 950 cycles: TIME_TWO), warp 1 lane 0 issues tcgen05.mma into
+// one of two TMEM accumulators, warps 2 to 9 are the epilogue (warp w reads TMEM
+// lanes 32 (w % 4) to + 31, and every second 32 columns).  CTA pairs share an MMA of
+// M = 256: each CTA holds 128 rows of A and half of B's columns.
+//
+// The epilogue reads the accumulator in the layout of matrix fragments, so that 16-bit
+// results pass through shared memory by transposing matrix stores and leave in vectors of
+// 16 bytes: with a store of 2 bytes a thread and value a tile of 128 x 256 took 3.7 us
+// beside the MMAs, TIME_EPI so.  Results whose rows are off 16 bytes and fp32 ones are
+// stored directly, 8 values of a row together.
+//
+// Bound by the tensor cores for many rows, and by reading the weights for few.
+#pragma once
+
+#include "gemm_args.h"
+#include "internal.h"
+#include "linear.h"
+#include "linear_epilogue.cuh"
+#include "ptx.cuh"
+
+namespace cce {
+namespace lin {
+
+constexpr int EPI_WARPS = 8;
+constexpr int PHASES = EPI_WARPS / 4;  // warps that share the columns of 32 TMEM lanes
+constexpr int THREADS = 96 + 32 * EPI_WARPS;
+constexpr int ACC_COLS = 256;  // TMEM columns of one of the two accumulators
+constexpr int CHUNK = 32;           // columns of a warp at a time
+constexpr int GROUP = 64 * 128;  // bytes of 64 rows of 128 bytes
+constexpr int TURN = LIN_TURN;
+constexpr int STAGING = 32 * CHUNK * 2;  // a warp's tile
+constexpr int BAR_BYTES_LIN = 512;
+
+constexpr int SHARED = 1024 + LIN_RING_BYTES + EPI_WARPS * STAGING + BAR_BYTES_LIN;
+static_assert(SHARED <= 227 * 1024, "shared memory of a CTA");
+
+struct Shared {
+  uint8_t* ring;
+  uint64_t* full;       // [LIN_MAX_STAGES]
+  uint64_t* empty;      // [LIN_MAX_STAGES]
+  uint64_t* acc_full;   // [2]
+  uint64_t* acc_empty;  // [2]
+  uint64_t* drain;
+  uint32_t* tmem;
+  int* abort_flag;
+  uint8_t* staging;  // [EPI_WARPS][STAGING]
+};
+
+__device__ __forceinline__ Shared carve(uint8_t* raw) {
+  Shared s;
+  s.ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  s.staging = s.ring + LIN_RING_BYTES;
+  s.full = reinterpret_cast<uint64_t*>(s.staging + EPI_WARPS * STAGING);
+  s.empty = s.full + LIN_MAX_STAGES;
+  s.acc_full = s.empty + LIN_MAX_STAGES;
+  s.acc_empty = s.acc_full + 2;
+  s.drain = s.acc_empty + 2;
+  s.tmem = reinterpret_cast<uint32_t*>(s.drain + 1);
+  s.abort_flag = reinterpret_cast<int*>(s.tmem + 1);
+  return s;
+}
+static_assert(8 * (2 * LIN_MAX_STAGES + 5) + 8 <= BAR_BYTES_LIN, "barriers fit");
+
+struct Tile {
+  const LinProblem* p;
+  int it, jt, split;
+  int kb, kb_end;  // blocks of K
+};
+
+__device__ __forceinline__ Tile tile_of(const LinArgs& a, int item) {
+  int q = 0;
+  while (q + 1 < a.problems && item >= a.p[q].items) item -= a.p[q++].items;
+  Tile t;
+  t.p = &a.p[q];
+  const LinProblem& p = *t.p;
+  // groups of i tiles, inside of which i runs fastest, then j, then the splits: tiles that
+  // run at the same time share rows of A and of B in L2
+  const int per_split = p.i_tiles * p.j_tiles;
+  t.split = item / per_split;
+  item -= t.split * per_split;
+  const int per_group = p.group * p.j_tiles;
+  const int g = item / per_group;
+  item -= g * per_group;
+  const int width = min(p.group, p.i_tiles - g * p.group);
+  t.jt = item / width;
+  t.it = g * p.group + item - t.jt * width;
+  t.kb = t.split * p.kb_split;
+  t.kb_end = min(p.kb_all, t.kb + p.kb_split);
+  return t;
+}
+
+// A box to `to`, whose bytes are counted on the stage's barrier (of a pair: the even CTA's).
+template <bool PAIR>
+struct Loader {
+  uint64_t* bar;
+  uint32_t lead;  // the barrier's cluster address
+
+  __device__ __forceinline__ void box2(const CUtensorMap* m, uint8_t* to, int x, int y) const {
+    if constexpr (PAIR) {
+      tma_load_2d_pair(m, lead, to, x, y);
+    } else {
+      tma_load_2d(m, bar, to, x, y);
+    }
+  }
+  __device__ __forceinline__ void box3(const CUtensorMap* m, uint8_t* to, int x, int y, int z) const {
+    if constexpr (PAIR) {
+      tma_load_3d_pair(m, lead, to, x, y, z);
+    } else {
+      tma_load_3d(m, bar, to, x, y, z);
+    }
+  }
+  // Gated: 64 rows of each weight from i0 on, in turns.
+  __device__ __forceinline__ void turns(const LinProblem& p, uint8_t* to, int i0, int k0) const {
+#pragma unroll
+    for (int k = 0; k < lin_bk(PAIR); k += 64, to += 2 * GROUP) {
+      if (p.a_4d) {
+        if constexpr (PAIR) {
+          tma_load_4d_pair(&p.a[0], lead, to, k0 + k, 0, 0, i0 / TURN);
+        } else {
+          tma_load_4d(&p.a[0], bar, to, k0 + k, 0, 0, i0 / TURN);
+        }
+      } else {
+        for (int r = 0; r < 2 * LIN_BI / 2 / TURN; ++r) box2(&p.a[r & 1], to + r * TURN * 128, k0 + k, i0 + (r >> 1) * TURN);
+      }
+    }
+  }
+  // `rows` rows from r0 on of an operand, the block of K at k0.  Along k: 64 of k are
+  // `pitch` bytes apart; along its own index: 64 of them.
+  __device__ __forceinline__ void operand(const CUtensorMap* m, bool mn, bool whole, uint8_t* to, int r0, int rows,
+                                          int k0, int pitch) const {
+    constexpr int BK = lin_bk(PAIR);
+    if (mn) {
+      if (whole) {
+        box3(m, to, 0, k0, r0 >> 6);
+      } else {
+        for (int r = 0; r < rows; r += 64) box2(m, to + r * 2 * BK, r0 + r, k0);
+      }
+    } else if (whole) {
+      box3(m, to, 0, r0, k0 >> 6);
+    } else {
+#pragma unroll
+      for (int k = 0; k < BK; k += 64) box2(m, to + (k >> 6) * pitch, k0 + k, r0);
+    }
+  }
+};
+
+// The loads of A, whose thread announces the bytes of both, or of B.
+template <bool PAIR, bool GATED, bool A>
+__device__ __forceinline__ void load_loop(const LinArgs& a, const Shared& s) {
+  constexpr int BK = lin_bk(PAIR), A_BYTES = LIN_BI * BK * 2;
+  volatile int* abort_flag = s.abort_flag;
+  const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
+  const int unit = PAIR ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
+  const int units = PAIR ? static_cast<int>(cluster_count_x()) : static_cast<int>(gridDim.x);
+  const uint32_t lead = PAIR ? mapa_shared(smem_u32(s.full), 0) : 0u;
+  const int stages = a.stages, stage_bytes = a.stage_bytes;
+  int stage = 0;
+  uint32_t phase = 0;
+  uint32_t issued = 0, issued_par = 0;  // per stage: ever issued, parity of its last phase
+  bool ok = true;
+  Tile next = tile_of(a, unit);
+  for (int item = unit; ok && item < a.items; item += units) {
+    const Tile t = next;
+    const LinProblem& p = *t.p;
+    const int kb_first = p.kb_first;
+    const bool mn = A ? p.a_mn : p.b_mn, whole = A ? p.a_3d : p.b_3d;
+    const int rows = PAIR ? p.jt / 2 : p.jt;
+    const int i0 = (t.it * (PAIR ? 2 : 1) + rank) * (GATED ? LIN_BI / 2 : LIN_BI);
+    const int j0 = t.jt * p.jt + rank * rows;
+    const uint32_t bytes = static_cast<uint32_t>((A_BYTES + rows * BK * 2) * (PAIR ? 2 : 1));
+    for (int kb = t.kb; kb < t.kb_end; ++kb) {
+      if (!wait_bounded_long(&s.empty[stage], phase ^ 1u, abort_flag, a.error)) {
+        ok = false;
+        break;
+      }
+      const Loader<PAIR> load{&s.full[stage], lead + 8u * static_cast<uint32_t>(stage)};
+      uint8_t* to = s.ring + stage * stage_bytes;
+      if (A && rank == 0) mbar_arrive_expect_tx(&s.full[stage], bytes);
+      const int part = !GATED && kb >= kb_first ? 1 : 0;
+      const int k0 = (part ? kb - kb_first : kb) * BK;
+      if constexpr (!A) {
+        load.operand(&p.b[part], mn, whole, to + A_BYTES, j0, rows, k0, rows * 128);
+      } else if constexpr (GATED) {
+        load.turns(p, to, i0, k0);
+      } else {
+        load.operand(&p.a[part], mn, whole, to, i0, LIN_BI, k0, 2 * GROUP);
+      }
+      issued |= 1u << stage;
+      issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+      if (++stage == stages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+      if (kb == t.kb && item + units < a.items) next = tile_of(a, item + units);
+    }
+  }
+  if (!*abort_flag) return;
+  if (PAIR && rank != 0) {
+    // this CTA's copies complete on the other's barriers: 10 ms for those in flight
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < 10000000ull) {
+    }
+  } else {
+    for (int i = 0; i < stages; ++i) {
+      if (issued & (1u << i)) {
+        volatile int none = 0;
+        wait_bounded_long(&s.full[i], (issued_par >> i) & 1u, &none, nullptr);
+      }
+    }
+  }
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void mma_loop(const LinArgs& a, const Shared& s, uint32_t tmem) {
+  if (PAIR && cluster_ctarank() != 0) return;  // the even CTA issues for both
+  constexpr int BK = lin_bk(PAIR), A_BYTES = LIN_BI * BK * 2;
+  volatile int* abort_flag = s.abort_flag;
+  const int unit = PAIR ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
+  const int units = PAIR ? static_cast<int>(cluster_count_x()) : static_cast<int>(gridDim.x);
+  const int stages = a.stages, stage_bytes = a.stage_bytes;
+  int stage = 0, acc = 0;
+  uint32_t phase = 0, acc_phase = 0;
+  bool any = false, ok = true;
+  // (the divisions for the next tile are made while this one's MMAs run: some 700 cycles between two tiles otherwise)
+  Tile next = tile_of(a, unit);
+  for (int item = unit; ok && item < a.items; item += units) {
+    const Tile t = next;
+    const LinProblem& p = *t.p;
+    const bool a_mn = p.a_mn, b_mn = p.b_mn;
+    const int kb_first = p.kb_first, klen0 = p.klen[0], klen1 = p.klen[1];
+    // bits 7-9 and 10-12 of the descriptor: 1 = bf16, 0 = fp16
+    const uint32_t idesc = idesc_bf16(PAIR ? 2 * LIN_BI : LIN_BI, p.jt, a_mn, b_mn) & (a.bf16 ? ~0u : ~((1u << 7) | (1u << 10)));
+    // along its own index: 64-element groups of BK rows of 128 bytes, 16 of k are 16 rows; along
+    // k: 16 of k are 32 bytes of a row, 64 of k all rows
+    const uint32_t a_lbo = a_mn ? BK * 128u : 16u, b_lbo = b_mn ? BK * 128u : 16u;
+    const uint32_t a_step = (a_mn ? 2048u : 32u) >> 4, b_step = (b_mn ? 2048u : 32u) >> 4;
+    const uint32_t a_next = (a_mn ? 8192u : 2u * GROUP) >> 4;
+    const uint32_t b_next = (b_mn ? 8192u : (PAIR ? p.jt / 2 : p.jt) * 128u) >> 4;
+    if (!wait_bounded_long(&s.acc_empty[acc], acc_phase ^ 1u, abort_flag, a.error)) break;
+    tc_fence_after();
+    const uint32_t d = tmem + static_cast<uint32_t>(acc * ACC_COLS);
+    uint32_t accumulate = 0;
+    for (int kb = t.kb; kb < t.kb_end; ++kb) {
+      if (!wait_bounded_long(&s.full[stage], phase, abort_flag, a.error)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const int left = kb < kb_first ? klen0 - kb * BK : klen1 - (kb - kb_first) * BK;
+      const uint32_t at = smem_u32(s.ring + stage * stage_bytes);
+      const uint64_t a_desc = smem_desc_sw128(at, a_lbo, 1024u);
+      const uint64_t b_desc = smem_desc_sw128(at + A_BYTES, b_lbo, 1024u);
+      const auto mma = [&](int k) {
+        const uint64_t ad = a_desc + (k >> 2) * a_next + (k & 3) * a_step, bd = b_desc + (k >> 2) * b_next + (k & 3) * b_step;
+        if constexpr (PAIR) {
+          mma_bf16_pair(d, ad, bd, idesc, accumulate | (k > 0));
+        } else {
+          mma_bf16(d, ad, bd, idesc, accumulate | (k > 0));
+        }
+      };
+      if (left >= BK) {
+#pragma unroll
+        for (int k = 0; k < BK / 16; ++k) mma(k);
+      } else {
+        for (int k = 0; 16 * k < left; ++k) mma(k);  // behind K's end there are zeros
+      }
+      accumulate = 1;
+      any = true;
+      if constexpr (PAIR) {
+        mma_commit_pair_both(&s.empty[stage]);
+      } else {
+        mma_commit(&s.empty[stage]);
+      }
+      if (++stage == stages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+      if (kb == t.kb && item + units < a.items) next = tile_of(a, item + units);
+    }
+    if (!ok) break;
+    if constexpr (PAIR) {
+      mma_commit_pair_both(&s.acc_full[acc]);
+    } else {
+      mma_commit(&s.acc_full[acc]);
+    }
+    acc ^= 1;
+    if (acc == 0) acc_phase ^= 1u;
+  }
+  if (*abort_flag && any) {
+    if constexpr (PAIR) {
+      mma_commit_pair_local(s.drain);
+    } else {
+      mma_commit(s.drain);
+    }
+    volatile int none = 0;
+    wait_bounded(s.drain, 0, &none, nullptr);
+  }
+}
+
+// A warp has read its part of an accumulator: the values are in registers, so that nothing but the arrival has to reach
+// the other CTA.  (With a release the last chunk's stores had to land first: 2,000 cycles a tile.)
+template <bool PAIR>
+__device__ __forceinline__ void release_accumulator(const Shared& s, int acc, uint32_t lead) {
+  tc_fence_before();
+  __syncwarp();
+  if (lane_id() == 0) {
+    if constexpr (PAIR) {
+      mbar_arrive_cluster_relaxed(lead + 8u * static_cast<uint32_t>(acc));
+    } else {
+      mbar_arrive(&s.acc_empty[acc]);
+    }
+  }
+}
+
+// What a thread holds of a chunk's 32 columns j and R x 8 rows i: rows 8 apart of pairs of neighbouring columns, the
+// pairs 8 apart, as [pair][row][column of the pair].
+template <int R>
+struct Fragment {
+  float v[8 * R];
+
+  // As 16-bit values to the first n columns and `rows` rows (a multiple of 8) of a matrix whose rows start on 16 bytes;
+  // p: the thread's place in it, column lane / R and row 8 (lane % R).  `tile`: 16 R bytes of shared memory for each
+  // column, swizzled so that neither access has bank conflicts.
+  __device__ __forceinline__ void store_wide(uint32_t tile, uint16_t* p, int64_t pitch, bool bf16, int n, int rows) const {
+    const auto place = [&](uint32_t j, uint32_t vector) {
+      return tile + j * 16u * R + ((vector ^ (R == 4 ? j >> 1 & 3u : j >> 2 & 1u)) << 4);
+    };
+    const uint32_t lane = lane_id(), which = lane >> 3;
+    const uint32_t to = place(8u * (which / R) + (lane & 7u), which % R), from = place(lane / R, lane % R);
+    __syncwarp();  // what was there has been read
+#pragma unroll
+    for (int q = 0; q < R; ++q) {  // four matrices at a time: 4 / R pairs of columns
+      uint32_t two[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float lo = v[8 * q + 2 * x], hi = v[8 * q + 2 * x + 1];
+        if (bf16) {
+          two[x] = pack_bf16x2(lo, hi);
+        } else {
+          const __half2 h = __floats2half2_rn(lo, hi);
+          two[x] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+      }
+      stmatrix_columns(to + 512u * q, two[0], two[1], two[2], two[3]);  // 32 / R columns on, 512 bytes
+    }
+    __syncwarp();
+    uint4 w[R];
+#pragma unroll
+    for (int q = 0; q < R; ++q)
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[q].x), "=r"(w[q].y), "=r"(w[q].z), "=r"(w[q].w)
+                   : "r"(from + 512u * q)
+                   : "memory");
+    const int j = static_cast<int>(lane) / R;
+    if (8 * (static_cast<int>(lane) % R) >= rows) n = 0;
+#pragma unroll
+    for (int q = 0; q < R; ++q, p += 32 / R * pitch) {
+      if (q * (32 / R) + j < n) *reinterpret_cast<uint4*>(p) = w[q];
+    }
+  }
+  // To the first n columns and `rows` rows of a matrix, whose element of the thread's first place is at p.
+  template <typename T>
+  __device__ __forceinline__ void store(T* p, int64_t pitch, bool bf16, int n, int rows) const {
+    const int c0 = 2 * static_cast<int>(lane_id() & 3u), r0 = static_cast<int>(lane_id() >> 2);
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        T* row = p + (8 * b + c) * pitch;
+        if (8 * b + c0 + c >= n) continue;
+#pragma unroll
+        for (int m = 0; m < R; ++m) {
+          if (r0 + 8 * m >= rows) continue;
+          const float f = v[2 * R * b + 2 * m + c];
+          if constexpr (sizeof(T) == 4) {
+            row[8 * m] = f;
+          } else {
+            row[8 * m] = bf16 ? to_bits16<true>(f) : to_bits16<false>(f);
+          }
+        }
+      }
+    }
+  }
+};
+
+// The residual's values of a chunk as they are in memory, loaded ahead of what they are added to.
+struct Residuals {
+  uint32_t raw[32];
+
+  template <typename T>
+  __device__ __forceinline__ void load(const T* p, int64_t pitch, int n, int rows) {
+    const int c0 = 2 * static_cast<int>(lane_id() & 3u), r0 = static_cast<int>(lane_id() >> 2);
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const T* row = p + (8 * b + c) * pitch;
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+          raw[8 * b + 2 * m + c] = 8 * b + c0 + c < n && r0 + 8 * m < rows ? row[8 * m] : T(0);
+      }
+    }
+  }
+  __device__ __forceinline__ void add_to(Fragment<4>& f, bool y32, bool bf16) const {
+    if (y32) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) f.v[e] += __uint_as_float(raw[e]);
+    } else if (bf16) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) f.v[e] += __uint_as_float(raw[e] << 16);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) f.v[e] += __half2float(__ushort_as_half(static_cast<uint16_t>(raw[e])));
+    }
+  }
+};
+
+// A chunk of the accumulator as it comes from TMEM: lanes 0 to 15 and 16 to 31 of a warp's quarter (gated: the gate's
+// and the up projection's).
+struct Chunk {
+  uint32_t lo[16], hi[16];
+
+  __device__ __forceinline__ void load(uint32_t first, uint32_t second) {
+    tmem_ld_16x256(first, lo);
+    tmem_ld_16x256(second, hi);
+  }
+  __device__ __forceinline__ void wait() {
+    tmem_ld_wait16(lo);
+    tmem_ld_wait16(hi);
+  }
+  __device__ __forceinline__ void get(Fragment<4>& f) const {
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        f.v[8 * b + x] = __uint_as_float(lo[4 * b + x]);
+        f.v[8 * b + 4 + x] = __uint_as_float(hi[4 * b + x]);
+      }
+  }
+  __device__ __forceinline__ void get(Fragment<2>& gate, Fragment<2>& up) const {
+#pragma unroll
+    for (int x = 0; x < 16; ++x) {
+      gate.v[x] = __uint_as_float(lo[x]);
+      up.v[x] = __uint_as_float(hi[x]);
+    }
+  }
+};
+
+// A warp's share of a tile: `rows` rows i from i0 on, and chunks of 32 of the `cols` columns from j0 on, PHASES apart.
+struct Share {
+  int i0, j0, rows, cols, chunks;
+  uint32_t first, second;  // where chunk 0 is in TMEM, its halves
+  uint32_t tile;           // of the warp in shared memory
+  float bias[4];
+};
+
+// Wide results of the accumulator alone: the next chunk comes while one is finished, and nothing is decided on the way.
+template <bool PAIR, bool GATED, int ACT>
+__device__ __forceinline__ void finish_lean(const Shared& s, const Share& w, const LinEpilogue& e, bool bf16, int acc,
+                                            uint32_t release) {
+  constexpr int R = GATED ? 2 : 4;
+  const int lane = static_cast<int>(lane_id());
+  const int64_t pitch = e.y_pitch;
+  uint16_t* y = static_cast<uint16_t*>(e.y) + static_cast<int64_t>(w.j0 + lane / R) * pitch + w.i0 + 8 * (lane % R);
+  int n = w.cols;
+  const auto step = [&](Chunk& now, Chunk& next, int c) {
+    now.wait();
+    if (c + 1 < w.chunks) {
+      next.load(w.first + CHUNK * PHASES * (c + 1), w.second + CHUNK * PHASES * (c + 1));
+    } else {
+      release_accumulator<PAIR>(s, acc, release);
+    }
+    if constexpr (GATED) {
+      Fragment<2> gate, up;
+      now.get(gate, up);
+      activate_as<ACT>(gate.v);
+#pragma unroll
+      for (int x = 0; x < 16; ++x) gate.v[x] *= up.v[x];
+      gate.store_wide(w.tile, y, pitch, bf16, n, w.rows);
+    } else {
+      Fragment<4> f;
+      now.get(f);
+#pragma unroll
+      for (int x = 0; x < 32; ++x) f.v[x] += w.bias[x >> 1 & 3];
+      activate_as<ACT>(f.v);
+      f.store_wide(w.tile, y, pitch, bf16, n, w.rows);
+    }
+    y += CHUNK * PHASES * pitch;
+    n -= CHUNK * PHASES;
+  };
+  Chunk a, b;
+  a.load(w.first, w.second);
+  for (int c = 0; c < w.chunks; c += 2) {
+    step(a, b, c);
+    if (c + 1 < w.chunks) step(b, a, c + 1);
+  }
+}
+
+// Everything else: a residual, pre-activations for the backward pass, fp32 results and ones off 16 bytes.
+template <bool PAIR, bool GATED, int ACT>
+__device__ __forceinline__ void finish_any(const Shared& s, const Share& w, const LinEpilogue& e, bool wide, bool bf16,
+                                           int acc, uint32_t release) {
+  constexpr int R = GATED ? 2 : 4;
+  const int lane = static_cast<int>(lane_id());
+  const bool y32 = !GATED && e.y_type == CCE_F32, has_z = e.z[0] != nullptr, has_res = !GATED && e.res;
+  // the thread's first place of a chunk: as one of fragments, and of wide stores
+  const int64_t wide_y = static_cast<int64_t>(w.j0 + lane / R) * e.y_pitch + w.i0 + 8 * (lane % R);
+  const int64_t wide_z = static_cast<int64_t>(w.j0 + lane / R) * e.z_pitch + w.i0 + 8 * (lane % R);
+  const int64_t ti = w.i0 + lane / 4, tj = w.j0 + 2 * (lane & 3);
+  for (int c = 0; c < w.chunks; ++c) {
+    const int jc = CHUNK * PHASES * c, n = w.cols - jc;
+    Chunk chunk;
+    chunk.load(w.first + jc, w.second + jc);
+    Residuals res;
+    if (has_res) {
+      if (y32) {
+        res.load(static_cast<const uint32_t*>(e.res) + (tj + jc) * e.res_pitch + ti, e.res_pitch, n, w.rows);
+      } else {
+        res.load(static_cast<const uint16_t*>(e.res) + (tj + jc) * e.res_pitch + ti, e.res_pitch, n, w.rows);
+      }
+    }
+    chunk.wait();
+    if (c + 1 == w.chunks) {
+      release_accumulator<PAIR>(s, acc, release);
+    } else {
+      __syncwarp();
+    }
+    const auto put = [&](const Fragment<R>& f, void* to, int64_t wide_at, int64_t pitch) {
+      if (wide) {
+        f.store_wide(w.tile, static_cast<uint16_t*>(to) + wide_at + jc * pitch, pitch, bf16, n, w.rows);
+      } else {
+        f.store(static_cast<uint16_t*>(to) + (tj + jc) * pitch + ti, pitch, bf16, n, w.rows);
+      }
+    };
+    if constexpr (GATED) {
+      Fragment<2> gate, up;
+      chunk.get(gate, up);
+      if (has_z) {
+        put(gate, e.z[0], wide_z, e.z_pitch);
+        put(up, e.z[1], wide_z, e.z_pitch);
+      }
+      activate_as<ACT>(gate.v);
+#pragma unroll
+      for (int x = 0; x < 16; ++x) gate.v[x] *= up.v[x];
+      put(gate, e.y, wide_y, e.y_pitch);
+    } else {
+      Fragment<4> f;
+      chunk.get(f);
+#pragma unroll
+      for (int x = 0; x < 32; ++x) f.v[x] += w.bias[x >> 1 & 3];
+      if (has_z) put(f, e.z[0], wide_z, e.z_pitch);
+      activate_as<ACT>(f.v);
+      if (has_res) res.add_to(f, y32, bf16);
+      if (y32) {
+        f.store(static_cast<float*>(e.y) + (tj + jc) * e.y_pitch + ti, e.y_pitch, bf16, n, w.rows);
+      } else {
+        put(f, e.y, wide_y, e.y_pitch);
+      }
+    }
+  }
+}
+
+// Partial sums of a split of K.
+template <bool PAIR, bool GATED>
+__device__ __forceinline__ void store_partial(const Shared& s, const Share& w, const LinProblem& p, int split, int acc,
+                                              uint32_t release) {
+  const int lane = static_cast<int>(lane_id());
+  const int64_t mats = GATED ? 2 : 1;
+  float* to = p.part + (mats * split * p.J + w.j0 + 2 * (lane & 3)) * p.I + w.i0 + lane / 4;
+  for (int c = 0; c < w.chunks; ++c, to += static_cast<int64_t>(CHUNK * PHASES) * p.I) {
+    const int jc = CHUNK * PHASES * c, n = w.cols - jc;
+    Chunk chunk;
+    chunk.load(w.first + jc, w.second + jc);
+    chunk.wait();
+    if (c + 1 == w.chunks) {
+      release_accumulator<PAIR>(s, acc, release);
+    } else {
+      __syncwarp();
+    }
+    if constexpr (GATED) {
+      Fragment<2> gate, up;
+      chunk.get(gate, up);
+      gate.store(to, p.I, true, n, w.rows);
+      up.store(to + static_cast<int64_t>(p.J) * p.I, p.I, true, n, w.rows);
+    } else {
+      Fragment<4> f;
+      chunk.get(f);
+      f.store(to, p.I, true, n, w.rows);
+    }
+  }
+}
+
+template <bool PAIR, bool GATED, int ACT>
+__device__ __forceinline__ void epilogue_loop(const LinArgs& a, const Shared& s, uint32_t tmem, int warp) {
+  constexpr int ROWS = GATED ? TURN : 32;  // of the output, a warp
+  const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
+  const int unit = PAIR ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
+  const int units = PAIR ? static_cast<int>(cluster_count_x()) : static_cast<int>(gridDim.x);
+  const int lane = static_cast<int>(lane_id());
+  const int quarter = warp & 3, phase_of = (warp - 2) >> 2;
+  const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+  const uint32_t release = PAIR ? mapa_shared(smem_u32(s.acc_empty), 0) : smem_u32(s.acc_empty);
+  const bool bf16 = a.bf16;
+  Share w;
+  w.tile = smem_u32(s.staging + (quarter * PHASES + phase_of) * STAGING);
+  int acc = 0;
+  uint32_t acc_phase = 0;
+  for (int item = unit; item < a.items; item += units) {
+    const Tile t = tile_of(a, item);
+    const LinProblem& p = *t.p;
+    const LinEpilogue& e = p.e;
+    w.i0 = (t.it * (PAIR ? 2 : 1) + rank) * (GATED ? LIN_BI / 2 : LIN_BI) + quarter * ROWS;
+    w.j0 = t.jt * p.jt + CHUNK * phase_of;
+    w.rows = p.I - w.i0;
+    w.cols = p.J - w.j0;
+    w.chunks = min((p.jt / CHUNK - phase_of + PHASES - 1) / PHASES, (w.cols + CHUNK * PHASES - 1) / (CHUNK * PHASES));
+    const bool whole = p.splits == 1, wide = p.wide, lean = wide && !e.z[0] && (GATED || !e.res);
+    if constexpr (!GATED) {
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const int i = lane / 4 + 8 * m;
+        w.bias[m] = whole && e.bias && i < w.rows ? load_scalar(e.bias, e.bias_type, w.i0 + i) : 0.0f;
+      }
+    }
+    w.first = w.second = lane_base + static_cast<uint32_t>(acc * ACC_COLS + CHUNK * phase_of);
+    (GATED && p.up_first ? w.first : w.second) += 16u << 16;
+    bool ok = true;
+    if (lane == 0) ok = wait_bounded_long(&s.acc_full[acc], acc_phase, s.abort_flag, a.error);
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    if (!ok) break;
+    tc_fence_after();
+    if (w.chunks <= 0) {
+      release_accumulator<PAIR>(s, acc, release);
+    } else if (!whole) {
+      store_partial<PAIR, GATED>(s, w, p, t.split, acc, release);
+    } else if (lean) {
+      finish_lean<PAIR, GATED, ACT>(s, w, e, bf16, acc, release);
+    } else {
+      finish_any<PAIR, GATED, ACT>(s, w, e, wide, bf16, acc, release);
+    }
+    acc ^= 1;
+    if (acc == 0) acc_phase ^= 1u;
+  }
+}
+
+template <bool PAIR, bool GATED, int ACT>
+__global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constant__ LinArgs a) {
+  extern __shared__ uint8_t raw[];
+  const Shared s = carve(raw);
+  const int warp = static_cast<int>(threadIdx.x >> 5);
+  let_next_start();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < a.stages; ++i) {
+      mbar_init(&s.full[i], 1);
+      mbar_init(&s.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.acc_full[i], 1);
+      mbar_init(&s.acc_empty[i], PAIR ? 2 * EPI_WARPS : EPI_WARPS);
+    }
+    mbar_init(s.drain, 1);
+    *s.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane_id() < 2 * a.problems) {  // before the first copies need them
+    const LinProblem& p = a.p[lane_id() >> 1];
+    tma_prefetch_desc(lane_id() & 1 ? &p.b[0] : &p.a[0]);
+    if (GATED || p.klen[1] > 0) tma_prefetch_desc(lane_id() & 1 ? &p.b[GATED ? 0 : 1] : &p.a[1]);
+  }
+  if (warp == 1) {
+    if constexpr (PAIR) {
+      tmem_alloc_pair(s.tmem, TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(s.tmem, TMEM_COLS);
+      tmem_relinquish();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (PAIR) cluster_sync();  // the other CTA's barriers exist before anything reaches them
+  tc_fence_after();
+  const uint32_t tmem = *s.tmem;
+  wait_for_previous();
+
+  if (warp == 0) {
+    if (lane_id() == 0) load_loop<PAIR, GATED, true>(a, s);
+  } else if (warp == 1) {
+    if (lane_id() == 0) mma_loop<PAIR>(a, s, tmem);
+  } else if (warp == 2 + EPI_WARPS) {
+    if (lane_id() == 0) load_loop<PAIR, GATED, false>(a, s);
+  } else {
+    epilogue_loop<PAIR, GATED, ACT>(a, s, tmem, warp);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (PAIR) cluster_sync();  // no CTA leaves while the other may still signal its barriers
+  if (warp == 1) {
+    tc_fence_after();
+    if constexpr (PAIR) {
+      tmem_dealloc_pair(tmem, TMEM_COLS);
+    } else {
+      tmem_dealloc(tmem, TMEM_COLS);
+    }
+  }
+}
+
+// The kernels of one activation.
+template <int ACT>
+cudaError_t prepare() {
+  const auto set = [](auto kernel) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SHARED);
+  };
+  cudaError_t e = set(linear_kernel<false, false, ACT>);
+  if (e == cudaSuccess) e = set(linear_kernel<false, true, ACT>);
+  if (e == cudaSuccess) e = set(linear_kernel<true, false, ACT>);
+  if (e == cudaSuccess) e = set(linear_kernel<true, true, ACT>);
+  return e;
+}
+
+template <int ACT>
+cudaError_t launch(const LinArgs& a, bool pair, bool gated, int units, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>(pair ? 2 * units : units)), block(THREADS);
+  const auto with = [&](auto kernel) { return launch_after(kernel, grid, block, SHARED, pair ? 2u : 1u, s, a); };
+  if (pair) return gated ? with(linear_kernel<true, true, ACT>) : with(linear_kernel<true, false, ACT>);
+  return gated ? with(linear_kernel<false, true, ACT>) : with(linear_kernel<false, false, ACT>);
+}
+
+}  // namespace lin
+}  // namespace cce

@@ -22,12 +22,13 @@ __global__ void __launch_bounds__(THREADS) join_kernel(const float* part, int I,
   wait_for_previous();
   const int i = static_cast<int>(blockIdx.x) * THREADS + static_cast<int>(threadIdx.x);
   if (i >= I) return;
-  const float bias = e.bias ? load_scalar(e.bias, e.bias_type, i) : 0.0f;
   for (int64_t row = static_cast<int64_t>(blockIdx.y) * JOIN_ROWS; row < J; row += static_cast<int64_t>(gridDim.y) * JOIN_ROWS) {
     const int j0 = static_cast<int>(row), n = min(JOIN_ROWS, J - j0);
-    float z0[JOIN_ROWS] = {}, z1[JOIN_ROWS] = {};
+    Column col;
+    col.start<GATED>(e, bf16, i, j0);
     Residual<JOIN_ROWS> res;
-    if (!GATED && e.res) res.load(e, i, j0, n);
+    if (col.res) res.load(col, n);
+    float z0[JOIN_ROWS] = {}, z1[JOIN_ROWS] = {};
 #pragma unroll 4
     for (int s = 0; s < splits; ++s) {  // in order
       const float* p = part + (static_cast<int64_t>(s * (GATED ? 2 : 1)) * J + j0) * I + i;
@@ -39,7 +40,7 @@ __global__ void __launch_bounds__(THREADS) join_kernel(const float* part, int I,
         }
       }
     }
-    finish_column<GATED>(e, bf16, bias, i, j0, n, z0, z1, res);
+    finish_column<GATED>(e, col, n, z0, z1, res);
   }
 }
 

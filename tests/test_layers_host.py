@@ -67,20 +67,29 @@ CALLS = (_linear, _linear_backward, _gated, _gated_backward)
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(x=0), 1), (dict(w=0), 1), (dict(ws=0), 1), (dict(type=F32), 4), (dict(type=7), 4), (dict(act=5), 4),
+    (dict(x=0), 1), (dict(w=0), 1), (dict(type=F32), 4), (dict(type=7), 4), (dict(act=5), 4),
     (dict(act=-1), 4), (dict(M=-1), 2), (dict(N=0), 2), (dict(K=0), 2), (dict(M=1 << 31), 2), (dict(N=1 << 31), 2),
     (dict(M=(1 << 31) - 600, K=(1 << 31) - 600, xp=(1 << 31) - 8), 2), (dict(xp=56), 2), (dict(wp=56), 2),
-    (dict(xp=1 << 31), 2), (dict(xp=68), 3), (dict(wp=70), 3), (dict(x=FAKE + 8), 3), (dict(w=FAKE + 2), 3),
-    (dict(ws=FAKE + 16), 3), (dict(wsb=8), 5),
+    (dict(xp=1 << 31), 2), (dict(N=1 << 30, wp=1 << 30), 2), (dict(K=1 << 30, xp=1 << 30, wp=1 << 30), 2), (dict(xp=68), 3), (dict(wp=70), 3), (dict(x=FAKE + 8), 3), (dict(w=FAKE + 2), 3),
 ])
 def test_every_call_rejects_without_launch(lib, kw, status):
     for call in CALLS:
         assert call(lib, **kw) == status, call
 
 
+@pytest.mark.parametrize("kw,status", [(dict(ws=FAKE + 16), 3), (dict(wsb=8), 5), (dict(ws=0), 1)])
+def test_workspaces_are_checked_where_one_is_needed(lib, kw, status):
+    sizes = dict(M=100, N=600, K=9000, xp=9000, wp=9000)
+    pitches = {_linear: ("rp", "yp", "zp"), _linear_backward: ("gp", "zp"), _gated: ("yp", "zp"),
+               _gated_backward: ("gp", "zp", "gatep")}
+    for call in CALLS:
+        up = dict(up=9000) if call in (_gated, _gated_backward) else {}
+        assert call(lib, **sizes, **{k: 600 for k in pitches[call]}, **up, **kw) == status, call
+
+
 @pytest.mark.parametrize("kw,status", [
     (dict(bt=3), 4), (dict(yt=F16), 4), (dict(yt=5), 4), (dict(y=0), 1), (dict(rp=99), 2), (dict(yp=99), 2),
-    (dict(zp=99), 2), (dict(b=FAKE + 2), 3), (dict(r=FAKE + 1), 3), (dict(y=FAKE + 1), 3), (dict(z=FAKE + 1), 3),
+    (dict(rp=1 << 30), 2), (dict(yp=1 << 30), 2), (dict(zp=99), 2), (dict(b=FAKE + 2), 3), (dict(r=FAKE + 1), 3), (dict(y=FAKE + 1), 3), (dict(z=FAKE + 1), 3),
     (dict(yt=F32, y=FAKE + 2), 3), (dict(yt=F32, r=FAKE + 2), 3),
 ])
 def test_linear_forward_rejects(lib, kw, status):
@@ -121,6 +130,7 @@ def test_valid_arguments_without_gpu_report_cuda_error(lib):
     assert _linear_backward(lib, act=NONE, z=0) in (6, 7)
     assert _linear_backward(lib, dx=0, dw=0, db=0) in (6, 7)
     assert _gated(lib, gate=0, z=0) in (6, 7)
+    assert _linear(lib, M=16, ws=0, wsb=0) in (6, 7)  # few rows need no workspace
 
 
 def test_workspaces(cce):
