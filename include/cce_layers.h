@@ -110,6 +110,26 @@ cce_status cce_gated_linear_backward(const void* grad_y, int64_t g_pitch, const 
 size_t cce_gated_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /*
+ * Copies rows of up to CCE_MAX_ROW_COPIES matrices in one launch, for those whose
+ * rows are not as the products take them: row n of the source starts (n / inner) *
+ * outer_stride + (n % inner) * row_stride elements after src (strides >= 0, unit stride
+ * inside a row, aligned words of 16 bytes that hold an element are read whole), row n of
+ * the destination n * pitch elements after dst, on 16 bytes with a pitch of a multiple of
+ * 16 bytes; what completes a row's last 16 bytes is written as zeros.  Elements of 2 or
+ * 4 bytes, sources aligned to them.  Destinations overlap nothing.
+ */
+#define CCE_MAX_ROW_COPIES 8
+typedef struct {
+  const void* src;
+  void* dst;
+  int64_t inner, row_stride, outer_stride, pitch;
+  int64_t rows, cols; /* either may be 0 */
+  int32_t bytes;      /* of an element */
+} cce_row_copy;
+
+cce_status cce_copy_rows(const cce_row_copy* copies /* host */, int n, void* stream);
+
+/*
  * *word (host) = the errors (CCE_DEVERR_*) that the products of this header met
  * on the current device since the last call, 0 without any; waits for `stream`.
  * Only a wait that ran out sets one: the results of its call are undefined.

@@ -56,6 +56,13 @@ class Strided(ctypes.Structure):
                 ("out_stride", ctypes.c_int64 * 4)]
 
 
+class RowCopy(ctypes.Structure):
+    """cce_row_copy of include/cce_layers.h."""
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("inner", ctypes.c_int64),
+                ("row_stride", ctypes.c_int64), ("outer_stride", ctypes.c_int64), ("pitch", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("bytes", ctypes.c_int32)]
+
+
 class AdamWTensor(ctypes.Structure):
     """cce_adamw_tensor of include/cce_optim.h."""
     _fields_ = [("grad", ctypes.c_void_p), ("param", ctypes.c_void_p), ("master", ctypes.c_void_p),
@@ -191,8 +198,9 @@ def load() -> ctypes.CDLL:
                                              + [vp, vp, i64, vp, sz, vp])
     lib.cce_gated_linear_backward.argtypes = (mat * 4 + [ci] + mat + mat + [ci, i64, i64, i64, vp, vp, vp, vp, sz, vp])
     lib.cce_layers_take_error.argtypes = [vp, vp]
+    lib.cce_copy_rows.argtypes = [ctypes.POINTER(RowCopy), ci, vp]
     for name in ("cce_linear_forward", "cce_linear_backward", "cce_gated_linear_forward", "cce_gated_linear_backward",
-                 "cce_layers_take_error"):
+                 "cce_layers_take_error", "cce_copy_rows"):
         getattr(lib, name).restype = ci
     for name in ("linear_forward", "linear_backward", "gated_linear_forward", "gated_linear_backward"):
         query = getattr(lib, f"cce_{name}_workspace_bytes")

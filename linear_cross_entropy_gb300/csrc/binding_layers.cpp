@@ -1,8 +1,6 @@
 // The layers in front of the head on torch tensors, over the C ABI of
 // include/cce_layers.h: checks, operands that the tensor cores' copies can read,
 // results, workspaces and the autograd nodes.
-#include <ATen/ops/copy.h>
-
 #include <array>
 #include <atomic>
 
@@ -27,34 +25,40 @@ int activation_code(const std::string& name) {
   refuse("activation must be one of None, 'relu', 'gelu', 'gelu_tanh', 'silu', got '", name, "'");
 }
 
-bool on_16_bytes(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
-
 // Rows at one pitch.
 struct Pitched {
   Tensor t;
   int64_t pitch = 0;
 };
 
-// The matrix of a tensor's last dimension, copied only where its rows are not at
-// one pitch.
-Pitched matrix_of(const Tensor& given) {
-  if (!given.defined()) return {};
-  const Rows r = rows_of(given);
-  const int64_t cols = given.size(-1);
-  if (r.outer != 0 || r.row < cols) return {r.t.contiguous(), cols};
-  return {r.t, r.row};
-}
+// The matrices of a call.  Rows that are not as the products take them are copied, all of a call in one launch.
+class Matrices {
+ public:
+  // The matrix of a tensor's last dimension; others than operands of a product may have any one pitch.
+  Pitched matrix(const Tensor& given, bool operand = false) {
+    if (!given.defined()) return {};
+    const Rows r = rows_of(given);
+    const int64_t cols = given.size(-1), bytes = given.element_size(), vec = 16 / bytes;
+    const bool one_pitch = r.outer == 0 && r.row >= cols && r.row < (int64_t(1) << 30);
+    if (one_pitch && (!operand || (reinterpret_cast<uintptr_t>(r.t.data_ptr()) % 16 == 0 && r.row % vec == 0)))
+      return {r.t, r.row};
+    const int64_t rows = cols ? given.numel() / cols : 0, pitch = (cols + vec - 1) / vec * vec;
+    Tensor to = at::empty({rows, pitch}, given.options().requires_grad(false));
+    kept_.push_back(r.t);
+    copies_.push_back({r.t.data_ptr(), to.data_ptr(), r.inner, r.row, r.outer, pitch, rows, cols, static_cast<int32_t>(bytes)});
+    return {to, pitch};
+  }
+  Pitched operand(const Tensor& given) { return matrix(given, true); }
 
-// The same as an operand of a product: on 16 bytes, whole vectors of 8 a row.
-// Others are copied into rows of a padded pitch.
-Pitched operand_of(const Tensor& given) {
-  Pitched m = matrix_of(given);
-  if (on_16_bytes(m.t.data_ptr()) && m.pitch % 8 == 0 && m.pitch < (int64_t(1) << 31)) return m;
-  const int64_t cols = given.size(-1), rows = cols ? given.numel() / cols : 0, pitch = (cols + 7) / 8 * 8;
-  Tensor to = at::empty({rows, pitch}, given.options().requires_grad(false));
-  to.narrow(1, 0, cols).copy_(m.t.reshape({rows, cols}));
-  return {to, pitch};
-}
+  void copy(const Tensor& on) {
+    if (copies_.empty()) return;
+    check_status(cce_copy_rows(copies_.data(), static_cast<int>(copies_.size()), stream_of(on)), "cce_copy_rows", ARGS);
+  }
+
+ private:
+  std::vector<cce_row_copy> copies_;
+  std::vector<Tensor> kept_;
+};
 
 struct Sizes {
   int64_t M, N, K;
@@ -131,7 +135,9 @@ std::tuple<Tensor, Tensor> linear_forward(const Tensor& x, const Tensor& weight,
   const c10::cuda::CUDAGuard guard(x.device());
   const size_t need = cce_linear_forward_workspace_bytes(s.M, s.N, s.K);
   const Tensor ws = workspace(need, x);
-  const Pitched xp = operand_of(x), wp = operand_of(weight), rp = matrix_of(residual);
+  Matrices m;
+  const Pitched xp = m.operand(x), wp = m.operand(weight), rp = m.matrix(residual);
+  m.copy(x);
   const Tensor b = plain(bias);
   const auto shape = result_shape(x, s.N);
   Tensor y = at::empty(shape, x.options().dtype(y_type).requires_grad(false));
@@ -167,8 +173,10 @@ std::tuple<Tensor, Tensor, Tensor> linear_backward(const Tensor& g, const Tensor
   const c10::cuda::CUDAGuard guard(x.device());
   const size_t need = cce_linear_backward_workspace_bytes(s.M, s.N, s.K);
   const Tensor ws = workspace(need, x);
-  const Pitched gp = matrix_of(g), xp = operand_of(x), wp = operand_of(weight);
-  const Pitched zp = act != CCE_ACT_NONE ? matrix_of(z) : Pitched{};
+  Matrices m;
+  const Pitched gp = m.matrix(g), xp = m.operand(x), wp = m.operand(weight);
+  const Pitched zp = act != CCE_ACT_NONE ? m.matrix(z) : Pitched{};
+  m.copy(x);
   const auto plainly = x.options().requires_grad(false);
   Tensor dx = need_dx ? at::empty(x.sizes(), plainly) : Tensor();
   Tensor dw = need_dw ? at::empty({s.N, s.K}, plainly) : Tensor();
@@ -195,7 +203,9 @@ std::tuple<Tensor, Tensor, Tensor> gated_forward(const Tensor& x, const Tensor& 
   const c10::cuda::CUDAGuard guard(x.device());
   const size_t need = cce_gated_linear_forward_workspace_bytes(s.M, s.N, s.K);
   const Tensor ws = workspace(need, x);
-  const Pitched xp = operand_of(x), gp = operand_of(gate_weight), up = operand_of(up_weight);
+  Matrices m;
+  const Pitched xp = m.operand(x), gp = m.operand(gate_weight), up = m.operand(up_weight);
+  m.copy(x);
   const auto shape = result_shape(x, s.N);
   const auto plainly = x.options().requires_grad(false);
   Tensor y = at::empty(shape, plainly), z0 = save ? at::empty(shape, plainly) : Tensor(),
@@ -228,8 +238,10 @@ std::tuple<Tensor, Tensor, Tensor> gated_backward(const Tensor& g, const Tensor&
   const c10::cuda::CUDAGuard guard(x.device());
   const size_t need = cce_gated_linear_backward_workspace_bytes(s.M, s.N, s.K);
   const Tensor ws = workspace(need, x);
-  const Pitched gy = matrix_of(g), xp = operand_of(x), wg = operand_of(gate_weight), wu = operand_of(up_weight);
-  const Pitched z0 = matrix_of(gate), z1 = matrix_of(up);
+  Matrices m;
+  const Pitched gy = m.matrix(g), xp = m.operand(x), wg = m.operand(gate_weight), wu = m.operand(up_weight);
+  const Pitched z0 = m.matrix(gate), z1 = m.matrix(up);
+  m.copy(x);
   const auto plainly = x.options().requires_grad(false);
   Tensor dx = need_dx ? at::empty(x.sizes(), plainly) : Tensor();
   Tensor dg = need_dg ? at::empty({s.N, s.K}, plainly) : Tensor();

@@ -220,10 +220,10 @@ bool encode(CUtensorMap* m, bool bf16, const Operand& o, int K, int own, bool mn
                : encode_operand(m, bf16, o.p, inner, outer, o.pitch, 64, box_rows);
 }
 
-// The products in one launch, and the joins of those whose K is split.  `part`:
+// The products in one launch (at least one, with a sum of parts beside them), and the joins of those whose K is split.  `part`:
 // room for their partial sums.
-cce_status run_products(const Product* in, int n, bool gated, bool bf16, void* part, const Device& on, cudaStream_t s,
-                        int* launches) {
+cce_status run_products(const Product* in, int n, bool gated, bool bf16, const LinSum& sum, void* part, const Device& on,
+                        cudaStream_t s, int* launches) {
   Shape shapes[LIN_MAX_PROBLEMS];
   for (int q = 0; q < n; ++q) shapes[q] = in[q].s;
   const Plan plan = plan_of(shapes, n, gated);
@@ -236,6 +236,7 @@ cce_status run_products(const Product* in, int n, bool gated, bool bf16, void* p
   a.problems = n;
   a.bf16 = bf16;
   a.error = on.error;
+  a.sum = sum;
   char* at = static_cast<char*>(part);
   int64_t items = 0;
   int widest = 0;
@@ -360,7 +361,7 @@ cce_status forward(const Matrix& x, const Matrix* w, bool gated, int64_t M, int6
     for (int m = 0; m < (gated ? 2 : 1); ++m) p.a[m] = Operand{w[m].p, w[m].pitch};
     p.b[0] = Operand{x.p, x.pitch};
     p.e = e;
-    st = run_products(&p, 1, gated, bf16, ws, on, stream, &launches);
+    st = run_products(&p, 1, gated, bf16, LinSum{}, ws, on, stream, &launches);
   }
   count_launches(launches);
   return st;
@@ -410,8 +411,8 @@ LinEpilogue dense_out(void* y, int64_t pitch, int type) {
 
 // From the parts of dz to the gradients asked for.  weights, grad_w: mats of them.
 cce_status backward_products(const Operand* dz, const Matrix& x, const Matrix* w, int mats, int64_t M, int64_t N,
-                             int64_t K, void* grad_x, void* const* grad_w, void* parts, const Device& on,
-                             cudaStream_t s, int* launches) {
+                             int64_t K, void* grad_x, void* const* grad_w, const LinSum& sum, void* parts,
+                             const Device& on, cudaStream_t s, int* launches) {
   const BackwardShapes b = backward_shapes(M, N, K, mats);
   const int type = x.type;
   Product p[LIN_MAX_PROBLEMS]{};
@@ -433,7 +434,10 @@ cce_status backward_products(const Operand* dz, const Matrix& x, const Matrix* w
     p[n].a_mn = true;
     p[n++].e = dense_out(grad_x, K, type);
   }
-  return n == 0 ? CCE_OK : run_products(p, n, false, type == CCE_BF16, parts, on, s, launches);
+  if (n > 0) return run_products(p, n, false, type == CCE_BF16, sum, parts, on, s, launches);
+  if (sum.parts == 0) return CCE_OK;
+  ++*launches;
+  return launch_linear_sum(sum, s) == cudaSuccess ? CCE_OK : CCE_ERR_CUDA;
 }
 
 cce_status zero(void* p, size_t bytes, cudaStream_t s) {
@@ -523,6 +527,7 @@ cce_status cce_linear_backward(const void* grad_y, int64_t g_pitch, int y_type, 
                       g_pitch < (int64_t(1) << 31);
   const bool staged = !direct && (grad_x || grad_weight);
   if (staged) dz = Operand{ws, l.pitch};
+  LinSum sum{};
   if (staged || grad_bias) {
     LinGrad g{};
     g.dy = grad_y;
@@ -533,15 +538,16 @@ cce_status cce_linear_backward(const void* grad_y, int64_t g_pitch, int y_type, 
     g.dz[0] = staged ? ws : nullptr;
     g.dz_pitch = l.pitch;
     g.part = grad_bias ? reinterpret_cast<float*>(ws + l.dz) : nullptr;
-    g.db = grad_bias;
-    g.db_type = bias_type;
     g.M = static_cast<int>(M);
     g.N = static_cast<int>(N);
     g.act = act;
-    if (launch_linear_grad(g, false, type == CCE_BF16, on.sms, s, &launches) != cudaSuccess) st = CCE_ERR_CUDA;
+    int parts = 0;
+    if (launch_linear_grad(g, false, type == CCE_BF16, on.sms, s, &parts) != cudaSuccess) st = CCE_ERR_CUDA;
+    ++launches;
+    if (grad_bias) sum = LinSum{g.part, grad_bias, parts, g.N, bias_type};
   }
   if (st == CCE_OK)
-    st = backward_products(&dz, xm, &wm, 1, M, N, K, grad_x, &grad_weight, ws + l.dz + l.sums, on, s,
+    st = backward_products(&dz, xm, &wm, 1, M, N, K, grad_x, &grad_weight, sum, ws + l.dz + l.sums, on, s,
                            &launches);
   count_launches(launches);
   return st;
@@ -589,13 +595,39 @@ cce_status cce_gated_linear_backward(const void* grad_y, int64_t g_pitch, const 
   g.M = static_cast<int>(M);
   g.N = static_cast<int>(N);
   g.act = act;
-  if (launch_linear_grad(g, true, type == CCE_BF16, on.sms, s, &launches) != cudaSuccess) st = CCE_ERR_CUDA;
+  int rows = 0;
+  if (launch_linear_grad(g, true, type == CCE_BF16, on.sms, s, &rows) != cudaSuccess) st = CCE_ERR_CUDA;
+  ++launches;
   const Operand dz[2] = {{g.dz[0], l.pitch}, {g.dz[1], l.pitch}};
   void* grad_w[2] = {grad_gate_weight, grad_up_weight};
   if (st == CCE_OK)
-    st = backward_products(dz, xm, wm, 2, M, N, K, grad_x, grad_w, ws + l.dz, on, s, &launches);
+    st = backward_products(dz, xm, wm, 2, M, N, K, grad_x, grad_w, LinSum{}, ws + l.dz, on, s, &launches);
   count_launches(launches);
   return st;
+}
+
+cce_status cce_copy_rows(const cce_row_copy* copies, int n, void* stream) {
+  if (n < 0 || n > CCE_MAX_ROW_COPIES) return CCE_ERR_ARG;
+  if (n > 0 && !copies) return CCE_ERR_NULL;
+  LinCopies a{};
+  for (int i = 0; i < n; ++i) {
+    const cce_row_copy& c = copies[i];
+    if (c.bytes != 2 && c.bytes != 4) return CCE_ERR_ARG;
+    if (c.rows < 0 || c.cols < 0 || c.rows >= LIMIT || c.cols >= LIMIT || c.inner < 1 || c.row_stride < 0 ||
+        c.outer_stride < 0 || c.pitch < c.cols)
+      return CCE_ERR_SHAPE;
+    if (c.rows == 0 || c.cols == 0) continue;
+    if (!c.src || !c.dst) return CCE_ERR_NULL;
+    if (!multiple(c.src, c.bytes) || !multiple(c.dst, 16) || c.pitch * c.bytes % 16 != 0) return CCE_ERR_ALIGN;
+    a.first[a.n] = a.rows;
+    a.c[a.n++] = c;
+    a.rows += c.rows;
+  }
+  int sms = 0;
+  const cce_status st = static_cast<cce_status>(device_ready(&sms));
+  if (st != CCE_OK || a.n == 0) return st;
+  count_launches(1);
+  return launch_linear_copies(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CCE_OK : CCE_ERR_CUDA;
 }
 
 cce_status cce_layers_take_error(int32_t* word, void* stream) {

@@ -9,6 +9,8 @@
 #include <cstddef>
 #include <cstdint>
 
+#include "../../include/cce_layers.h"
+
 namespace cce {
 
 // What happens to an accumulator on its way out: z = acc + bias[i], y = f(z) +
@@ -49,9 +51,17 @@ struct LinProblem {
   LinEpilogue e;
 };
 
+// db[c] = the sum over the parts of part[p][c], in a fixed order.
+struct LinSum {
+  const float* part;
+  void* db;
+  int parts, N, type;
+};
+
 constexpr int LIN_MAX_PROBLEMS = 3;
 struct LinArgs {
   LinProblem p[LIN_MAX_PROBLEMS];
+  LinSum sum;  // made beside the products (parts = 0: none)
   int problems;
   int items;
   int bf16;  // operands are bf16, else fp16
@@ -109,11 +119,21 @@ struct LinGrad {
   void* dz[2];  // may be null (sums alone)
   int64_t dz_pitch;
   float* part;  // [parts][N], may be null (no sums)
-  void* db;
-  int db_type;
   int M, N, act;
 };
 constexpr int LIN_GRAD_PARTS = 256;
-cudaError_t launch_linear_grad(const LinGrad& a, bool gated, bool bf16, int sms, cudaStream_t s, int* launches);
+// *parts: how many parts there are of the sums.
+cudaError_t launch_linear_grad(const LinGrad& a, bool gated, bool bf16, int sms, cudaStream_t s, int* parts);
+cudaError_t launch_linear_sum(const LinSum& a, cudaStream_t s);
+
+
+// Rows of several matrices (include/cce_layers.h, cce_copy_rows); empty ones are left out.
+struct LinCopies {
+  cce_row_copy c[CCE_MAX_ROW_COPIES];
+  int64_t first[CCE_MAX_ROW_COPIES];  // row of the launch at which each begins
+  int64_t rows;
+  int n;
+};
+cudaError_t launch_linear_copies(const LinCopies& a, int sms, cudaStream_t s);
 
 }  // namespace cce

@@ -36,6 +36,27 @@ __device__ __forceinline__ float load_scalar(const void* p, int type, int64_t i)
   return f[0];
 }
 
+// Column c of the sums of a gradient's parts: eight running sums of every eighth part, then those in order.
+__device__ __forceinline__ void sum_columns(const LinSum& a, int c) {
+  if (c >= a.N) return;
+  float t[8] = {};
+  const float* p = a.part + c;
+  const int64_t n = a.N;
+  int at = 0;
+#pragma unroll 4
+  for (; at + 8 <= a.parts; at += 8) {
+#pragma unroll
+    for (int v = 0; v < 8; ++v) t[v] += p[(at + v) * n];
+  }
+#pragma unroll
+  for (int v = 0; v < 8; ++v) {
+    if (at + v < a.parts) t[v] += p[(at + v) * n];
+  }
+#pragma unroll
+  for (int v = 1; v < 8; ++v) t[0] += t[v];
+  store_param(a.db, a.type, c, t[0]);
+}
+
 // Loads and stores of a column's rows, a pitch apart.  They are volatile so that they
 // stay in order and each address is the last one and a pitch: with all addresses in
 // registers at once the epilogue spilled.

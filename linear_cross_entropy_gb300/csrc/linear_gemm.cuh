@@ -16,11 +16,12 @@
 // rows are 64 of each weight in turns of 16, so that its loads and MMAs are those of a
 // layer twice as wide, and a thread of the epilogue has both values of an output.
 //
-// Roles (352 threads): lane 0 of warp 0 loads A, that of warp 10 B (TMA; a pair's stages
+// Roles (384 threads): lane 0 of warp 0 loads A, that of warp 10 B (TMA; a pair's stages
 // are 128 deep in K, a single CTA's 64, as many as fit in 192 KiB; one thread for both
 // needed 560 of a stage's 950 cycles: TIME_TWO), warp 1 lane 0 issues tcgen05.mma into
 // one of two TMEM accumulators, warps 2 to 9 are the epilogue (warp w reads TMEM
-// lanes 32 (w % 4) to + 31, and every second 32 columns).  CTA pairs share an MMA of
+// lanes 32 (w % 4) to + 31, and every second 32 columns), and warp
+// 11 adds up the parts of a bias's gradient where there are some.  CTA pairs share an MMA of
 // M = 256: each CTA holds 128 rows of A and half of B's columns.
 //
 // The epilogue reads the accumulator in the layout of matrix fragments, so that 16-bit
@@ -43,7 +44,7 @@ namespace lin {
 
 constexpr int EPI_WARPS = 8;
 constexpr int PHASES = EPI_WARPS / 4;  // warps that share the columns of 32 TMEM lanes
-constexpr int THREADS = 96 + 32 * EPI_WARPS;
+constexpr int THREADS = 128 + 32 * EPI_WARPS;
 constexpr int ACC_COLS = 256;  // TMEM columns of one of the two accumulators
 constexpr int CHUNK = 32;           // columns of a warp at a time
 constexpr int GROUP = 64 * 128;  // bytes of 64 rows of 128 bytes
@@ -709,6 +710,11 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
     if (lane_id() == 0) mma_loop<PAIR>(a, s, tmem);
   } else if (warp == 2 + EPI_WARPS) {
     if (lane_id() == 0) load_loop<PAIR, GATED, false>(a, s);
+  } else if (warp == 3 + EPI_WARPS) {
+    if (a.sum.parts > 0) {
+      for (int c = static_cast<int>(blockIdx.x) * 32; c < a.sum.N; c += static_cast<int>(gridDim.x) * 32)
+        sum_columns(a.sum, c + static_cast<int>(lane_id()));
+    }
   } else {
     epilogue_loop<PAIR, GATED, ACT>(a, s, tmem, warp);
   }

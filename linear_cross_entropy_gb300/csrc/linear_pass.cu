@@ -3,6 +3,7 @@
 //   join  the epilogue over the partial sums of a product whose K was split
 //   grad  dz = dy f'(z), or of a gated layer dgate = dy u f'(g) and dup = dy f(g),
 //         in the type of the products that follow, and the sums of dz over the rows
+//   copy  rows that are off 16 bytes or at two pitches into ones that the products take
 #include <algorithm>
 
 #include "internal.h"
@@ -131,30 +132,58 @@ __global__ void __launch_bounds__(THREADS) grad_kernel(const __grid_constant__ L
   }
 }
 
-// db[c] = the sum of the blocks' sums, in a fixed order.
-__global__ void __launch_bounds__(THREADS) sum_kernel(const float* part, int parts, int N, void* db, int type) {
+// Without products, beside which it is made otherwise.
+__global__ void __launch_bounds__(32) sum_kernel(const __grid_constant__ LinSum a) {
   let_next_start();
   wait_for_previous();
-  __shared__ float sums[GROUPS][COLS];
-  const int tx = static_cast<int>(threadIdx.x) % COLS, ty = static_cast<int>(threadIdx.x) / COLS;
-  const int c = static_cast<int>(blockIdx.x) * COLS + tx;
-  float t = 0.0f;
-  if (c < N) {
-#pragma unroll 8
-    for (int p = ty; p < parts; p += GROUPS) t += part[static_cast<int64_t>(p) * N + c];
+  sum_columns(a, static_cast<int>(blockIdx.x) * 32 + static_cast<int>(threadIdx.x));
+}
+
+// --------------------------------------------------------------------- copies
+// A warp's row.  The vectors of a row off 16 bytes are joined from two.
+template <typename T>
+__device__ __forceinline__ void copy_row(const cce_row_copy& c, int64_t row) {
+  constexpr int VEC = 16 / sizeof(T);
+  const int64_t outer = row / c.inner;
+  const T* from = static_cast<const T*>(c.src) + outer * c.outer_stride + (row - outer * c.inner) * c.row_stride;
+  T* to = static_cast<T*>(c.dst) + row * c.pitch;
+  const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(from) / sizeof(T)) & (VEC - 1);
+  from -= shift;
+#pragma unroll 4
+  for (int64_t i = static_cast<int64_t>(threadIdx.x & 31) * VEC; i < c.cols; i += 32 * VEC) {
+    Vec<T, VEC> lo, hi, v;
+    lo.load(from + i);
+    if (shift == 0) {
+      v = lo;
+    } else {
+      hi.zero();
+      if (i + VEC - shift < c.cols) hi.load(from + i + VEC);
+      v.join(lo, hi, shift);
+    }
+    if (c.cols - i < VEC) v.keep(0, static_cast<int>(c.cols - i));
+    v.store(to + i);
   }
-  sums[ty][tx] = t;
-  __syncthreads();
-  if (ty != 0 || c >= N) return;
-#pragma unroll
-  for (int v = 1; v < GROUPS; ++v) t += sums[v][tx];
-  store_param(db, type, c, t);
+}
+
+__global__ void __launch_bounds__(THREADS) copy_kernel(const __grid_constant__ LinCopies a) {
+  let_next_start();
+  wait_for_previous();
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (THREADS / 32);
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5); r < a.rows; r += step) {
+    int m = 0;
+    while (m + 1 < a.n && r >= a.first[m + 1]) ++m;
+    if (a.c[m].bytes == 4) {
+      copy_row<float>(a.c[m], r - a.first[m]);
+    } else {
+      copy_row<__nv_bfloat16>(a.c[m], r - a.first[m]);
+    }
+  }
 }
 
 bool multiple(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(bytes) == 0; }
 
 template <typename T, typename TY, bool GATED>
-cudaError_t launch_grad(const LinGrad& a, int sms, cudaStream_t s, int* launches) {
+cudaError_t launch_grad(const LinGrad& a, int sms, cudaStream_t s, int* parts) {
   // vectors of 8: whole rows of them at 16 bytes in every matrix (dy of fp32 rows as two)
   bool wide = a.N % 8 == 0 && a.dy_pitch % 8 == 0 && multiple(a.dy, 16);
   for (int m = 0; m < (GATED ? 2 : 1); ++m) {
@@ -166,22 +195,16 @@ cudaError_t launch_grad(const LinGrad& a, int sms, cudaStream_t s, int* launches
   // six blocks an SM, no more than there are rows for
   const int y = std::max(1, std::min({LIN_GRAD_PARTS, (6 * sms + x - 1) / x, (a.M + GROUPS * UNROLL - 1) / (GROUPS * UNROLL)}));
   const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(y));
-  cudaError_t e = wide ? launch_after(grad_kernel<T, TY, GATED, 8>, grid, dim3(THREADS), 0, 1, s, a)
-                       : launch_after(grad_kernel<T, TY, GATED, 1>, grid, dim3(THREADS), 0, 1, s, a);
-  ++*launches;
-  if (e == cudaSuccess && a.part) {
-    e = launch_after(sum_kernel, dim3(static_cast<unsigned>((a.N + COLS - 1) / COLS)), dim3(THREADS), 0, 1, s,
-                     static_cast<const float*>(a.part), y, a.N, a.db, a.db_type);
-    ++*launches;
-  }
-  return e;
+  *parts = y;
+  return wide ? launch_after(grad_kernel<T, TY, GATED, 8>, grid, dim3(THREADS), 0, 1, s, a)
+              : launch_after(grad_kernel<T, TY, GATED, 1>, grid, dim3(THREADS), 0, 1, s, a);
 }
 
 template <typename T>
-cudaError_t launch_grad_of(const LinGrad& a, bool gated, int sms, cudaStream_t s, int* launches) {
-  if (gated) return launch_grad<T, T, true>(a, sms, s, launches);
-  return a.dy_type == CCE_F32 ? launch_grad<T, float, false>(a, sms, s, launches)
-                              : launch_grad<T, T, false>(a, sms, s, launches);
+cudaError_t launch_grad_of(const LinGrad& a, bool gated, int sms, cudaStream_t s, int* parts) {
+  if (gated) return launch_grad<T, T, true>(a, sms, s, parts);
+  return a.dy_type == CCE_F32 ? launch_grad<T, float, false>(a, sms, s, parts)
+                              : launch_grad<T, T, false>(a, sms, s, parts);
 }
 
 }  // namespace
@@ -195,9 +218,18 @@ cudaError_t launch_linear_join(const LinProblem& p, bool gated, bool bf16, int s
                : launch_after(join_kernel<false>, grid, dim3(THREADS), 0, 1, s, part, p.I, p.J, p.splits, p.e, bf16);
 }
 
-cudaError_t launch_linear_grad(const LinGrad& a, bool gated, bool bf16, int sms, cudaStream_t s, int* launches) {
-  return bf16 ? launch_grad_of<__nv_bfloat16>(a, gated, sms, s, launches)
-              : launch_grad_of<__half>(a, gated, sms, s, launches);
+cudaError_t launch_linear_grad(const LinGrad& a, bool gated, bool bf16, int sms, cudaStream_t s, int* parts) {
+  return bf16 ? launch_grad_of<__nv_bfloat16>(a, gated, sms, s, parts)
+              : launch_grad_of<__half>(a, gated, sms, s, parts);
+}
+
+cudaError_t launch_linear_copies(const LinCopies& a, int sms, cudaStream_t s) {
+  const int64_t blocks = (a.rows + THREADS / 32 - 1) / (THREADS / 32);
+  return launch_after(copy_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(blocks, 8 * sms))), dim3(THREADS), 0, 1, s, a);
+}
+
+cudaError_t launch_linear_sum(const LinSum& a, cudaStream_t s) {
+  return launch_after(sum_kernel, dim3(static_cast<unsigned>((a.N + 31) / 32)), dim3(32), 0, 1, s, a);
 }
 
 }  // namespace cce

@@ -188,6 +188,21 @@ def test_strides_and_alignment(cce, M, K):
                     assert all(torch.equal(a, b) for a, b in zip(one, two))
 
 
+@pytest.mark.parametrize("cols", [1, 3, 4, 7, 33, 130])
+def test_strided_fp32_matrices(cce, cols):
+    """Residuals and gradients in fp32 at two pitches and off 16 bytes."""
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    _, x, (w,) = inputs(3 * 20, cols, 24, BF16, 12)
+    x = x.view(3, 20, 24)
+    big = randn(gen, 3, 22, cols + 6)
+    for r in (big[:, :20, :cols], big[:, 1:21, 1:1 + cols], big[:, 2:, 3:3 + cols], big[0, 0, :cols].expand(3, 20, cols),
+              big.transpose(0, 1)[:3, :, :cols].expand(3, 3, cols)[:, :1].expand(3, 20, cols)):
+        assert torch.equal(cce.linear(x, w, residual=r, out_dtype=F32),
+                           cce.linear(x, w, residual=r.contiguous(), out_dtype=F32))
+        for a, b in zip(cce.cce_linear_backward(r, x, w), cce.cce_linear_backward(r.contiguous(), x, w)):
+            assert torch.equal(a, b)
+
+
 def test_what_lies_between_rows_is_not_read(cce):
     """NaN beside the views, in the columns that complete a vector and in the rows behind."""
     for M, N, K in [(3, 20, 20), (40, 50, 36), (300, 130, 100)]:

@@ -31,7 +31,7 @@ def cce(lib):
 def test_declared_symbols(lib):
     src = open(os.path.join(ROOT, "include", "cce_layers.h")).read()
     names = set(re.findall(r"\b(cce_[a-z0-9_]+)\s*\(", re.sub(r"/\*.*?\*/", "", src, flags=re.S)))
-    assert len(names) == 10 and all(hasattr(lib, n) for n in names)
+    assert len(names) == 11 and all(hasattr(lib, n) for n in names)
     assert lib.cce_layers_abi_version() == 100
 
 
@@ -130,7 +130,23 @@ def test_valid_arguments_without_gpu_report_cuda_error(lib):
     assert _linear_backward(lib, act=NONE, z=0) in (6, 7)
     assert _linear_backward(lib, dx=0, dw=0, db=0) in (6, 7)
     assert _gated(lib, gate=0, z=0) in (6, 7)
+    from linear_cross_entropy_gb300._lib import RowCopy
+    assert lib.cce_copy_rows((RowCopy * 1)(RowCopy(FAKE, 2 * FAKE, 3, 100, 400, 104, 9, 100, 2)), 1, 0) in (6, 7)
     assert _linear(lib, M=16, ws=0, wsb=0) in (6, 7)  # few rows need no workspace
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(src=0), 1), (dict(dst=0), 1), (dict(inner=0), 2), (dict(row_stride=-1), 2), (dict(outer_stride=-1), 2),
+    (dict(pitch=99), 2), (dict(pitch=108), 3), (dict(rows=-1), 2), (dict(cols=-1), 2), (dict(rows=1 << 31), 2),
+    (dict(bytes=8), 4), (dict(src=FAKE + 1), 3), (dict(dst=FAKE + 8), 3), (dict(bytes=4, src=FAKE + 2), 3),
+])
+def test_row_copies_are_checked(lib, kw, status):
+    from linear_cross_entropy_gb300._lib import RowCopy
+    a = dict(src=FAKE, dst=2 * FAKE, inner=3, row_stride=100, outer_stride=400, pitch=104, rows=9, cols=100, bytes=2)
+    good, bad = RowCopy(*a.values()), RowCopy(*(a | kw).values())
+    assert lib.cce_copy_rows((RowCopy * 2)(good, bad), 2, 0) == status
+    assert lib.cce_copy_rows(None, 1, 0) == 1 and lib.cce_copy_rows((RowCopy * 1)(good), -1, 0) == 4
+    assert lib.cce_copy_rows((RowCopy * 9)(*[good] * 9), 9, 0) == 4
 
 
 def test_workspaces(cce):
