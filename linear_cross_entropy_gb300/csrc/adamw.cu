@@ -90,13 +90,14 @@ __device__ __forceinline__ int find_tensor(const Batch<M>& b, uint32_t chunk) {
   return lo;
 }
 
-__host__ __device__ inline uint32_t mix(uint32_t x) {
-  x ^= x >> 16;
+// The finaliser of MurmurHash3, without its first step.
+__device__ __forceinline__ uint32_t mix_rest(uint32_t x) {
   x *= 0x85ebca6bu;
   x ^= x >> 13;
   x *= 0xc2b2ae35u;
-  return x ^ (x >> 16);
+  return x ^ x >> 16;
 }
+__device__ __forceinline__ uint32_t mix(uint32_t x) { return mix_rest(x ^ x >> 16); }
 
 // What an update needs beside its values; the same in all threads.
 struct Now {
@@ -236,21 +237,23 @@ __device__ __forceinline__ float warp_larger(float v) {
   return v;
 }
 
-// 16 random bits as a number in [1, 2).
-__device__ __forceinline__ float behind_one(uint32_t u16) { return __uint_as_float(u16 * 128u + 0x3f800000u); }
+// 2^23 + the low (HIGH: the high) 16 bits of a word.
+template <bool HIGH>
+__device__ __forceinline__ float behind_2_23(uint32_t w) {
+  return __uint_as_float(__byte_perm(w, 0x4b000000u, HIGH ? 0x7432 : 0x7410));
+}
 
-// Two a in [0, 448] to floor(a / step + u - 1) step; NaN stays NaN.  step: 2^-3 of a's power of two, 2^-9 at least; u
-// from behind_one().  An a that roundings brought above 448, by 2^-22 of it at most, becomes 448 all the same: a / step
-// is then below 14 + 2^-18, and u - 1 at most 1 - 2^-16.
-__device__ __forceinline__ float2 round_e4m3(float a_lo, float a_hi, float u_lo, float u_hi) {
-  constexpr uint32_t POWER = 0x7f800000u, THREE = 3u << 23, LEAST = 121u << 23, ONE_SQUARED = 254u << 23;
-  const uint32_t lo = max(__float_as_uint(a_lo) & POWER, LEAST) - THREE, hi = max(__float_as_uint(a_hi) & POWER, LEAST) - THREE;
-  const Pair step = Pair::of(__uint_as_float(lo), __uint_as_float(hi));
-  const Pair inv = Pair::of(__uint_as_float(ONE_SQUARED - lo), __uint_as_float(ONE_SQUARED - hi));  // powers of two: exact
-  const Pair u = add(Pair::of(u_lo, u_hi), Pair::both(-1.0f));
-  // below 2^22 a sum with 2^23 rounded down is the floor
-  const Pair q = add(add_down(fma(Pair::of(a_lo, a_hi), inv, u), Pair::both(0x1p23f)), Pair::both(-0x1p23f));
-  return mul(q, step).get();
+// Two a in [0, 448] to floor(a / step + u / 2^16) step; NaN stays NaN.  step: 2^-3 of a's power of two, 2^-9 at least; u:
+// 16 random bits, given as 2^23 + u.  All but one rounding is of what is exact: a + u 2^-16 step as
+// the formula rounds a / step + u 2^-16; the floor is a sum with 2^23 steps rounded down.  An a that roundings brought above
+// 448, by 2^-22 of it at most, becomes 448 all the same: a / step is then below 14 + 2^-18.
+__device__ __forceinline__ Pair round_e4m3(float a_lo, float a_hi, float u_lo, float u_hi) {
+  constexpr uint32_t POWER = 0x7f800000u, LEAST = 121u << 23;  // 2^-6
+  const Pair p = Pair::of(__uint_as_float(max(__float_as_uint(a_lo) & POWER, LEAST)),
+                          __uint_as_float(max(__float_as_uint(a_hi) & POWER, LEAST)));  // 8 steps
+  const Pair u = fma(Pair::of(u_lo, u_hi), Pair::both(0x1p-19f), Pair::both(-16.0f));
+  const Pair s = fma(u, p, Pair::of(a_lo, a_hi));
+  return fma(p, Pair::both(-0x1p20f), fma_down(p, Pair::both(0x1p20f), s));
 }
 
 // The n values (n <= 256) of one block from element `at` of t on, by a warp.
@@ -324,16 +327,21 @@ __device__ __forceinline__ void update_block(const Rule& r, const Now& now, floa
   const float m_inv = m_none ? 0.0f : __frcp_rn(m_most) * E4M3_MAX, r_inv = r_none ? 0.0f : __frcp_rn(r_most) * E4M3_MAX;
   const uint64_t place = static_cast<uint64_t>(t.first_block + block) * CCE_ADAMW_BLOCK + lane * VEC;
   const uint32_t key = mix(now.key ^ static_cast<uint32_t>(place >> 32));
+  // mix(place + e ^ key) for the lane's e: place is a multiple of 8, so that the first shift is the same for all
+  const uint32_t start = static_cast<uint32_t>(place) ^ key, shifted = start ^ start >> 16;
   float mo[VEC], ro[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; e += 2) {
-    const uint32_t x = mix((static_cast<uint32_t>(place) + e) ^ key), y = mix((static_cast<uint32_t>(place) + e + 1) ^ key);
+    const uint32_t x = mix_rest(shifted ^ e), y = mix_rest(shifted ^ (e + 1));
     const float2 mm = m2[e / 2].get(), b = mul(r2[e / 2], Pair::both(r_inv)).get();
-    const float2 mr = round_e4m3(fabsf(mm.x) * m_inv, fabsf(mm.y) * m_inv, behind_one(x & 0xffffu), behind_one(y & 0xffffu));
-    const float2 rr = round_e4m3(b.x, b.y, behind_one(x >> 16), behind_one(y >> 16));
+    const float2 mr = round_e4m3(fabsf(mm.x) * m_inv, fabsf(mm.y) * m_inv, behind_2_23<false>(x), behind_2_23<false>(y)).get();
+    const float2 rr = round_e4m3(b.x, b.y, behind_2_23<true>(x), behind_2_23<true>(y)).get();
     mo[e] = copysignf(mr.x, mm.x), mo[e + 1] = copysignf(mr.y, mm.y);
-    // a positive root stays one
-    ro[e] = larger(rr.x, b.x > 0.0f ? E4M3_MIN : 0.0f), ro[e + 1] = larger(rr.y, b.y > 0.0f ? E4M3_MIN : 0.0f);
+    // a positive root stays one (magnitudes compare as their bits do, NaN above all)
+    const auto positive = [](float q, float of) {
+      return __uint_as_float(max(__float_as_uint(q), min(__float_as_uint(of), 1u) * __float_as_uint(E4M3_MIN)));
+    };
+    ro[e] = positive(rr.x, b.x), ro[e + 1] = positive(rr.y, b.y);
   }
   uint32_t mw[2], rw[2];
 #pragma unroll

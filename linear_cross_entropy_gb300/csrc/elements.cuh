@@ -232,11 +232,6 @@ __device__ __forceinline__ Pair add(Pair a, Pair b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
   return r;
 }
-__device__ __forceinline__ Pair add_down(Pair a, Pair b) {  // rounded towards minus infinity
-  Pair r;
-  asm("add.rm.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
 __device__ __forceinline__ Pair mul(Pair a, Pair b) {
   Pair r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
@@ -245,6 +240,12 @@ __device__ __forceinline__ Pair mul(Pair a, Pair b) {
 __device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) {
   Pair r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+__device__ __forceinline__ Pair fma_down(Pair a, Pair b, Pair c) {  // rounded towards minus infinity
+  Pair r;
+  asm("fma.rm.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
   return r;
 }
 
