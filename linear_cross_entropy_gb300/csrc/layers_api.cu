@@ -58,9 +58,9 @@ int k_blocks(const Shape& s, bool pair) { return static_cast<int>(s.parts * cdiv
 // Cycles of one work item: its blocks of K at the slower of the tensor core (8,192
 // flops a cycle and SM) and the loads (56 bytes a cycle and SM from L2), and what a
 // tile costs beside them.
-double item_cycles(int jt, int kb, bool pair) {
+double item_cycles(int jt, int kb, bool pair, bool b_mn) {
   const double mma = 2.0 * jt;
-  const double load = (LIN_BI + (pair ? jt / 2 : jt)) * 128.0 / 56.0;
+  const double load = (LIN_BI + lin_b_rows(jt, pair, b_mn)) * 128.0 / 56.0;
   return kb * std::max(mma, load) * (lin_bk(pair) / 64) + 500.0;
 }
 
@@ -96,7 +96,7 @@ void choose(const Shape* s, int n, int q, bool pair, bool gated, Plan* best) {
   const int units = pair ? UNITS / 2 : UNITS;
   const int mats = gated ? 2 : 1;
   const int kb = k_blocks(s[q], pair);
-  const int step = s[q].b_mn ? (pair ? 128 : 64) : 32;
+  constexpr int step = 32;
   Plan p = *best;
   for (int jt = step; jt <= 256; jt += step) {
     if (jt > step && jt - step >= s[q].J) break;  // a narrower one holds all rows
@@ -111,7 +111,7 @@ void choose(const Shape* s, int n, int q, bool pair, bool gated, Plan* best) {
       c.splits = static_cast<int>(cdiv(kb, c.kb_split));
       if (c.splits != splits) continue;  // the same as fewer splits
       c.items = tiles * splits;
-      c.item_cycles = item_cycles(jt, c.kb_split, pair);
+      c.item_cycles = item_cycles(jt, c.kb_split, pair, s[q].b_mn);
       p.cycles = makespan(p.c, n, units);
       for (int r = 0; r < n; ++r) p.cycles += join_cycles(s[r], p.c[r], gated);
       if (best->cycles < 0.0 || p.cycles < best->cycles) *best = p;
@@ -255,7 +255,8 @@ cce_status run_products(const Product* in, int n, bool gated, bool bf16, const L
     p.b_mn = f.s.b_mn;
     // a third dimension of groups of 64 would reach past the row's end otherwise
     p.a_3d = !gated && (f.a_mn ? p.I : f.s.K) % 64 == 0;
-    p.b_3d = (f.s.b_mn ? p.J : f.s.K) % 64 == 0;
+    const int own_rows = plan.pair ? c.jt / 2 : c.jt, b_rows = lin_b_rows(c.jt, plan.pair, f.s.b_mn);
+    p.b_3d = f.s.b_mn ? p.J % 64 == 0 && own_rows % 64 == 0 : f.s.K % 64 == 0;
     p.jt = c.jt;
     p.i_tiles = static_cast<int>(i_tiles(f.s, plan.pair, gated));
     p.j_tiles = static_cast<int>(cdiv(f.s.J, c.jt));
@@ -271,7 +272,6 @@ cce_status run_products(const Product* in, int n, bool gated, bool bf16, const L
     const bool rows_16 = f.e.y_type != CCE_F32 && multiple(f.e.y, 16) && f.e.y_pitch % 8 == 0;
     const bool z_16 = !f.e.z[0] || (multiple(f.e.z[0], 16) && multiple(f.e.z[1], 16) && f.e.z_pitch % 8 == 0);
     p.wide = c.splits == 1 && rows_16 && z_16 && p.I % 8 == 0;
-    const int b_rows = plan.pair ? c.jt / 2 : c.jt;
     widest = std::max(widest, b_rows);
     if (gated) {
       const uintptr_t g = reinterpret_cast<uintptr_t>(f.a[0].p), u = reinterpret_cast<uintptr_t>(f.a[1].p);

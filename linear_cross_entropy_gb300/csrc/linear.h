@@ -72,6 +72,10 @@ struct LinArgs {
 constexpr int LIN_BI = 128;  // rows of the MMA a CTA: I extent of a tile (gated: 64 of each weight)
 // Blocks of K: a stage's depth.  A pair's loads are issued half as often with the deeper one.
 constexpr int lin_bk(bool pair) { return pair ? 128 : 64; }
+// Rows of B that a CTA loads for a tile: whole groups of 64 where they are stored along their own index.
+__host__ __device__ constexpr int lin_b_rows(int jt, bool pair, bool mn) {
+  return mn ? ((pair ? jt / 2 : jt) + 63) / 64 * 64 : pair ? jt / 2 : jt;
+}
 constexpr int LIN_TURN = 16;  // gated: rows of a weight after which the other's come
 constexpr int LIN_RING_BYTES = 192 * 1024;
 constexpr int LIN_MAX_STAGES = 10;
@@ -105,7 +109,7 @@ struct LinFew {
   int I, J, K;
   LinEpilogue e;
 };
-constexpr int LIN_FEW_ROWS = 16;
+constexpr int LIN_FEW_ROWS = 32;
 cudaError_t launch_linear_few(const LinFew& a, bool gated, bool bf16, cudaStream_t s);
 
 // The element-wise part of the backward pass: dz = dy f'(z) (gated: dgate = dy u

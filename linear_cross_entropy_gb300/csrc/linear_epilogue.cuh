@@ -1,5 +1,4 @@
-// What happens to an accumulator of a layer on its way out (LinEpilogue), for a
-// thread that holds consecutive rows j of one output column i.
+// What happens to a sum of products of a layer on its way out (LinEpilogue).
 #pragma once
 
 #include "activation.cuh"
@@ -57,163 +56,43 @@ __device__ __forceinline__ void sum_columns(const LinSum& a, int c) {
   store_param(a.db, a.type, c, t[0]);
 }
 
-// Loads and stores of a column's rows, a pitch apart.  They are volatile so that they
-// stay in order and each address is the last one and a pitch: with all addresses in
-// registers at once the epilogue spilled.
-__device__ __forceinline__ void store16(char* p, uint32_t v) {
-  asm volatile("{\n\t.reg .b16 h, g;\n\tmov.b32 {h, g}, %1;\n\tst.global.b16 [%0], h;\n\t}" ::"l"(p), "r"(v));
-}
-__device__ __forceinline__ void store16_high(char* p, uint32_t v) {
-  asm volatile("{\n\t.reg .b16 h, g;\n\tmov.b32 {h, g}, %1;\n\tst.global.b16 [%0], g;\n\t}" ::"l"(p), "r"(v));
-}
-__device__ __forceinline__ void store32(char* p, float v) {
-  asm volatile("st.global.f32 [%0], %1;" ::"l"(p), "f"(v));
-}
-__device__ __forceinline__ uint32_t load16(const char* p) {
-  uint16_t v;
-  asm volatile("ld.global.b16 %0, [%1];" : "=h"(v) : "l"(p));
-  return v;
-}
-__device__ __forceinline__ uint32_t load32(const char* p) {
-  uint32_t v;
-  asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
-  return v;
+template <typename T, int VEC>
+__device__ __forceinline__ void put(void* base, int64_t at, const float (&f)[VEC]) {
+  Vec<T, VEC> v;
+  v.set(f);
+  v.store(static_cast<T*>(base) + at);
 }
 
-// A thread's place in the matrices of an epilogue, in registers: kernel parameters
-// behind a run-time index cost a load for each use.
-struct Column {
-  char *y = nullptr, *z = nullptr;
-  const char* res = nullptr;
-  uint32_t y_step = 0, z_step = 0, res_step = 0;  // bytes from row to row
-  float bias = 0.0f;
-  int act = 0;
-  bool bf16 = false, y32 = false, has_bias = false;
-
-  template <bool GATED>
-  __device__ __forceinline__ void start(const LinEpilogue& e, bool operands_bf16, int i, int j) {
-    bf16 = operands_bf16;
-    y32 = !GATED && e.y_type == CCE_F32;
-    act = e.act;
-    const uint32_t bytes = y32 ? 4 : 2;
-    y_step = static_cast<uint32_t>(e.y_pitch) * bytes;
-    y = static_cast<char*>(e.y) + static_cast<int64_t>(j) * y_step + static_cast<int64_t>(i) * bytes;
-    if (e.z[0]) {
-      z_step = static_cast<uint32_t>(e.z_pitch) * 2;
-      z = static_cast<char*>(e.z[0]) + static_cast<int64_t>(j) * z_step + static_cast<int64_t>(i) * 2;
-    }
-    if (!GATED && e.res) {
-      res_step = static_cast<uint32_t>(e.res_pitch) * bytes;
-      res = static_cast<const char*>(e.res) + static_cast<int64_t>(j) * res_step + static_cast<int64_t>(i) * bytes;
-    }
-    has_bias = !GATED && e.bias;
-    if (has_bias) bias = load_scalar(e.bias, e.bias_type, i);
-  }
-  __device__ __forceinline__ void skip(uint32_t rows) {
-    y += static_cast<uint64_t>(rows) * y_step;
-    if (z) z += static_cast<uint64_t>(rows) * z_step;
-    if (res) res += static_cast<uint64_t>(rows) * res_step;
-  }
-};
-
-// M values to rows of a 16-bit matrix, rounded to nearest even; the first n of them.
-template <bool FULL, int M>
-__device__ __forceinline__ void store_rows16(char* p, uint32_t step, const uint32_t (&two)[(M + 1) / 2], int n) {
+// VEC neighbouring values i, ... of row j, all inside of the matrices, which VEC values of each start on their size.  z0:
+// the product with x (gated: the gate's), z1: gated: the up projection's.  T: the operands' type.
+template <typename T, bool GATED, int VEC>
+__device__ __forceinline__ void finish_row(const LinEpilogue& e, int64_t j, int64_t i, float (&z0)[VEC],
+                                           const float (&z1)[VEC]) {
+  const bool y32 = !GATED && e.y_type == CCE_F32;
+  if (!GATED && e.bias) {
+    float b[VEC];
+    load_param<VEC>(e.bias, e.bias_type, i, b);
 #pragma unroll
-  for (int u = 0; u < M; ++u, p += step) {
-    if (!FULL && u >= n) continue;
-    if (u & 1) {
-      store16_high(p, two[u / 2]);
-    } else {
-      store16(p, two[u / 2]);
-    }
+    for (int u = 0; u < VEC; ++u) z0[u] += b[u];
   }
-}
-
-template <int M>
-__device__ __forceinline__ void put_rows16(char* p, uint32_t step, bool bf16, const float (&f)[M], int n) {
-  uint32_t two[(M + 1) / 2];
-  if (bf16) {
-#pragma unroll
-    for (int u = 0; u < M; u += 2) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(f[u], u + 1 < M ? f[u + 1 < M ? u + 1 : u] : 0.0f);
-      two[u / 2] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-  } else {
-#pragma unroll
-    for (int u = 0; u < M; u += 2) {
-      const __half2 h = __floats2half2_rn(f[u], u + 1 < M ? f[u + 1 < M ? u + 1 : u] : 0.0f);
-      two[u / 2] = *reinterpret_cast<const uint32_t*>(&h);
-    }
+  if (e.z[0]) {
+    put<T>(e.z[0], j * e.z_pitch + i, z0);
+    if (GATED) put<T>(e.z[1], j * e.z_pitch + i, z1);
   }
-  if (n >= M) {
-    store_rows16<true, M>(p, step, two, n);
-  } else {
-    store_rows16<false, M>(p, step, two, n);
-  }
-}
-
-template <int M>
-__device__ __forceinline__ void put_rows32(char* p, uint32_t step, const float (&f)[M], int n) {
-#pragma unroll
-  for (int u = 0; u < M; ++u, p += step) {
-    if (u < n) store32(p, f[u]);
-  }
-}
-
-// The residual's rows as they are in memory: loaded ahead of what they are added to.
-template <int M>
-struct Residual {
-  uint32_t raw[M];
-
-  __device__ __forceinline__ void load(const Column& c, int n) {
-    const char* p = c.res;
-    if (c.y32) {
-#pragma unroll
-      for (int u = 0; u < M; ++u, p += c.res_step) raw[u] = u < n ? load32(p) : 0u;
-    } else {
-#pragma unroll
-      for (int u = 0; u < M; ++u, p += c.res_step) raw[u] = u < n ? load16(p) : 0u;
-    }
-  }
-  __device__ __forceinline__ void add_to(const Column& c, float (&f)[M]) const {
-    if (c.y32) {
-#pragma unroll
-      for (int u = 0; u < M; ++u) f[u] += __uint_as_float(raw[u]);
-    } else if (c.bf16) {
-#pragma unroll
-      for (int u = 0; u < M; ++u) f[u] += __uint_as_float(raw[u] << 16);
-    } else {
-#pragma unroll
-      for (int u = 0; u < M; ++u) f[u] += __half2float(__ushort_as_half(static_cast<uint16_t>(raw[u])));
-    }
-  }
-};
-
-// min(n, M) rows from the column's place on.  z0: the product with x (gated: the
-// gate's), z1: gated: the up projection's; res: loaded if there is a residual.
-template <bool GATED, int M>
-__device__ __forceinline__ void finish_column(const LinEpilogue& e, const Column& c, int n, float (&z0)[M], const float (&z1)[M],
-                                              const Residual<M>& res) {
-  if (!GATED && c.has_bias) {
-#pragma unroll
-    for (int u = 0; u < M; ++u) z0[u] += c.bias;
-  }
-  if (c.z) {
-    put_rows16(c.z, c.z_step, c.bf16, z0, n);
-    if (GATED) put_rows16(c.z + (static_cast<char*>(e.z[1]) - static_cast<char*>(e.z[0])), c.z_step, c.bf16, z1, n);
-  }
-  activate_all(c.act, z0);
+  activate_all(e.act, z0);
   if (GATED) {
 #pragma unroll
-    for (int u = 0; u < M; ++u) z0[u] *= z1[u];
-  } else if (c.res) {
-    res.add_to(c, z0);
+    for (int u = 0; u < VEC; ++u) z0[u] *= z1[u];
+  } else if (e.res) {
+    float r[VEC];
+    load_param<VEC>(e.res, y32 ? CCE_F32 : ElemType<T>::id, j * e.res_pitch + i, r);
+#pragma unroll
+    for (int u = 0; u < VEC; ++u) z0[u] += r[u];
   }
-  if (!GATED && c.y32) {
-    put_rows32(c.y, c.y_step, z0, n);
+  if (y32) {
+    put<float>(e.y, j * e.y_pitch + i, z0);
   } else {
-    put_rows16(c.y, c.y_step, c.bf16, z0, n);
+    put<T>(e.y, j * e.y_pitch + i, z0);
   }
 }
 

@@ -1,5 +1,5 @@
 // A layer over few rows (decoding): out[j][i] = epilogue(sum over k of w[i][k] x[j][k])
-// for up to 16 rows j.
+// for up to 32 rows j.
 //
 // Bound by reading the weights once, so nothing is staged: a warp reads 16-byte
 // vectors of 16 weight rows straight into the fragments of mma.m16n8k16, whose k
@@ -10,6 +10,8 @@
 #include "internal.h"
 #include "linear.h"
 #include "linear_epilogue.cuh"
+
+#include <type_traits>
 
 namespace cce {
 namespace {
@@ -129,22 +131,18 @@ __global__ void __launch_bounds__(32 * WARPS, 2) few_kernel(const __grid_constan
 #pragma unroll
       for (int q = 0; q < 4; ++q) sums[warp][m][g + 8 * (q >> 1)][8 * n + 2 * t + (q & 1)] = c[m][n][q];
   __syncthreads();
-  const int r = static_cast<int>(threadIdx.x) % ROWS, j = static_cast<int>(threadIdx.x) / ROWS;
-  const int i = i0 + r;
-  if (j >= 8 * NT || j >= a.J || i >= a.I) return;
-  float z0[1] = {0.0f}, z1[1] = {0.0f};
+  const int r = static_cast<int>(threadIdx.x) % ROWS, i = i0 + r;
+  if (i >= a.I) return;
+  for (int j = static_cast<int>(threadIdx.x) / ROWS; j < min(8 * NT, a.J); j += 32 * WARPS / ROWS) {
+    float z0[1] = {0.0f}, z1[1] = {0.0f};
 #pragma unroll
-  for (int v = 0; v < WARPS; ++v) {
-    z0[0] += sums[v][0][r][j];
-    if (GATED) z1[0] += sums[v][MATS - 1][r][j];
+    for (int v = 0; v < WARPS; ++v) {
+      z0[0] += sums[v][0][r][j];
+      if (GATED) z1[0] += sums[v][MATS - 1][r][j];
+    }
+    finish_row<typename std::conditional<BF16, __nv_bfloat16, __half>::type, GATED>(a.e, j, i, z0, z1);
   }
-  Column col;
-  col.start<GATED>(a.e, BF16, i, j);
-  Residual<1> res;
-  if (col.res) res.load(col, 1);
-  finish_column<GATED>(a.e, col, 1, z0, z1, res);
 }
-static_assert(32 * WARPS == ROWS * LIN_FEW_ROWS, "one result a thread");
 
 template <bool BF16, int NT>
 cudaError_t launch(const LinFew& a, bool gated, cudaStream_t s) {
@@ -156,8 +154,14 @@ cudaError_t launch(const LinFew& a, bool gated, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_linear_few(const LinFew& a, bool gated, bool bf16, cudaStream_t s) {
-  if (bf16) return a.J <= 8 ? launch<true, 1>(a, gated, s) : launch<true, 2>(a, gated, s);
-  return a.J <= 8 ? launch<false, 1>(a, gated, s) : launch<false, 2>(a, gated, s);
+  const int tiles = (a.J + 7) / 8;
+  if (bf16)
+    return tiles == 1   ? launch<true, 1>(a, gated, s)
+           : tiles == 2 ? launch<true, 2>(a, gated, s)
+                        : launch<true, 4>(a, gated, s);
+  return tiles == 1   ? launch<false, 1>(a, gated, s)
+         : tiles == 2 ? launch<false, 2>(a, gated, s)
+                      : launch<false, 4>(a, gated, s);
 }
 
 }  // namespace cce

@@ -186,9 +186,10 @@ __device__ __forceinline__ void load_loop(const LinArgs& a, const Shared& s) {
     const int kb_first = p.kb_first;
     const bool mn = A ? p.a_mn : p.b_mn, whole = A ? p.a_3d : p.b_3d;
     const int rows = PAIR ? p.jt / 2 : p.jt;
+    const int loaded = lin_b_rows(p.jt, PAIR, p.b_mn);
     const int i0 = (t.it * (PAIR ? 2 : 1) + rank) * (GATED ? LIN_BI / 2 : LIN_BI);
     const int j0 = t.jt * p.jt + rank * rows;
-    const uint32_t bytes = static_cast<uint32_t>((A_BYTES + rows * BK * 2) * (PAIR ? 2 : 1));
+    const uint32_t bytes = static_cast<uint32_t>((A_BYTES + loaded * BK * 2) * (PAIR ? 2 : 1));
     for (int kb = t.kb; kb < t.kb_end; ++kb) {
       if (!wait_bounded_long(&s.empty[stage], phase ^ 1u, abort_flag, a.error)) {
         ok = false;
