@@ -41,6 +41,14 @@
 extern "C" {
 #endif
 
+/*
+ * A type for what a forward pass keeps for its backward pass: 16 bits, a sign, 6 of
+ * exponent (bias 31) and 9 of fraction, with subnormals, infinities and NaN as in IEEE's
+ * types, to nearest.  Two bits of fraction more than bf16's between 2^-30 and 2^32;
+ * values beyond become infinite, ones below 2^-40 zero.
+ */
+#define CCE_KEPT16 3
+
 enum { CCE_ACT_NONE = 0, CCE_ACT_RELU = 1, CCE_ACT_GELU = 2, CCE_ACT_GELU_TANH = 3, CCE_ACT_SILU = 4 };
 
 /* ABI version of this header (major * 100 + minor): 100. */
@@ -53,13 +61,14 @@ int cce_layers_abi_version(void);
  *   bias      [N] of bias_type, any of the three types; NULL: 0
  *   residual  [M, N] of y_type; NULL: 0
  *   y         [M, N] of y_type: `type` or CCE_F32
- *   z         [M, N] of `type`, for the backward pass; NULL: not written
+ *   z         [M, N] of z_type, for the backward pass; NULL: not written.  z_type is
+ *             `type`, or CCE_KEPT16 with CCE_BF16
  * Everything behind the product is fp32, with one rounding to y and one to z.
  */
 cce_status cce_linear_forward(const void* x, int64_t x_pitch, const void* weight, int64_t w_pitch, int type,
                               const void* bias, int bias_type, const void* residual, int64_t res_pitch, int act,
                               int64_t M, int64_t N, int64_t K, void* y, int64_t y_pitch, int y_type, void* z,
-                              int64_t z_pitch, void* workspace, size_t ws_bytes, void* stream);
+                              int64_t z_pitch, int z_type, void* workspace, size_t ws_bytes, void* stream);
 
 /* Bytes of workspace (0 for invalid sizes; 16 where none is needed).  Pure host arithmetic; needs no GPU. */
 size_t cce_linear_forward_workspace_bytes(int64_t M, int64_t N, int64_t K);
@@ -72,26 +81,27 @@ size_t cce_linear_forward_workspace_bytes(int64_t M, int64_t N, int64_t K);
  *   grad_bias = sum of dz over the rows, in fp32 before that rounding
  *                               [N] of bias_type
  * Each may be NULL (not computed).  grad_y is [M, N] of y_type, `type` or
- * CCE_F32; z is the forward's, or NULL with CCE_ACT_NONE.  The residual's
+ * CCE_F32; z is the forward's, of z_type, or NULL with CCE_ACT_NONE.  The residual's
  * gradient is grad_y itself.
  */
 cce_status cce_linear_backward(const void* grad_y, int64_t g_pitch, int y_type, const void* x, int64_t x_pitch,
-                               const void* weight, int64_t w_pitch, int type, const void* z, int64_t z_pitch, int act,
-                               int64_t M, int64_t N, int64_t K, void* grad_x, void* grad_weight, void* grad_bias,
-                               int bias_type, void* workspace, size_t ws_bytes, void* stream);
+                               const void* weight, int64_t w_pitch, int type, const void* z, int64_t z_pitch,
+                               int z_type, int act, int64_t M, int64_t N, int64_t K, void* grad_x,
+                               void* grad_weight, void* grad_bias, int bias_type, void* workspace, size_t ws_bytes,
+                               void* stream);
 
 /* Bytes of workspace, as above. */
 size_t cce_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /*
  * Gated product, forward: gate = x gate_weight^T, up = x up_weight^T,
- * y = act(gate) up, all of `type`; both weights [N, K].  gate and up [M, N] of
- * one pitch are written for the backward pass unless both are NULL.
+ * y = act(gate) up, of `type`; both weights [N, K].  gate and up [M, N] of one
+ * pitch and of z_type (as above) are written for the backward pass unless both are NULL.
  */
 cce_status cce_gated_linear_forward(const void* x, int64_t x_pitch, const void* gate_weight, int64_t gw_pitch,
                                     const void* up_weight, int64_t uw_pitch, int type, int act, int64_t M, int64_t N,
                                     int64_t K, void* y, int64_t y_pitch, void* gate, void* up, int64_t z_pitch,
-                                    void* workspace, size_t ws_bytes, void* stream);
+                                    int z_type, void* workspace, size_t ws_bytes, void* stream);
 size_t cce_gated_linear_forward_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /*
@@ -99,13 +109,13 @@ size_t cce_gated_linear_forward_workspace_bytes(int64_t M, int64_t N, int64_t K)
  * dup = grad_y act(gate), both rounded to `type`:
  *   grad_x = dgate gate_weight + dup up_weight   [M, K], one fp32 sum
  *   grad_gate_weight = dgate^T x, grad_up_weight = dup^T x   [N, K]
- * Each may be NULL.  grad_y [M, N] of `type`.
+ * Each may be NULL.  grad_y [M, N] of `type`, gate and up of z_type.
  */
 cce_status cce_gated_linear_backward(const void* grad_y, int64_t g_pitch, const void* x, int64_t x_pitch,
                                      const void* gate_weight, int64_t gw_pitch, const void* up_weight,
                                      int64_t uw_pitch, int type, const void* gate, int64_t gate_pitch, const void* up,
-                                     int64_t up_pitch, int act, int64_t M, int64_t N, int64_t K, void* grad_x,
-                                     void* grad_gate_weight, void* grad_up_weight, void* workspace, size_t ws_bytes,
+                                     int64_t up_pitch, int z_type, int act, int64_t M, int64_t N, int64_t K,
+                                     void* grad_x, void* grad_gate_weight, void* grad_up_weight, void* workspace, size_t ws_bytes,
                                      void* stream);
 size_t cce_gated_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K);
 

@@ -191,12 +191,12 @@ def load() -> ctypes.CDLL:
     lib.cce_layers_abi_version.restype = ci
     mat = [vp, i64]  # pointer, pitch
     lib.cce_linear_forward.argtypes = (mat + mat + [ci, vp, ci] + mat + [ci, i64, i64, i64] + mat + [ci] + mat
-                                       + [vp, sz, vp])
-    lib.cce_linear_backward.argtypes = (mat + [ci] + mat + mat + [ci] + mat + [ci, i64, i64, i64, vp, vp, vp, ci, vp,
+                                       + [ci, vp, sz, vp])
+    lib.cce_linear_backward.argtypes = (mat + [ci] + mat + mat + [ci] + mat + [ci, ci, i64, i64, i64, vp, vp, vp, ci, vp,
                                                                                sz, vp])
     lib.cce_gated_linear_forward.argtypes = (mat + mat + mat + [ci, ci, i64, i64, i64] + mat
-                                             + [vp, vp, i64, vp, sz, vp])
-    lib.cce_gated_linear_backward.argtypes = (mat * 4 + [ci] + mat + mat + [ci, i64, i64, i64, vp, vp, vp, vp, sz, vp])
+                                             + [vp, vp, i64, ci, vp, sz, vp])
+    lib.cce_gated_linear_backward.argtypes = (mat * 4 + [ci] + mat + mat + [ci, ci, i64, i64, i64, vp, vp, vp, vp, sz, vp])
     lib.cce_layers_take_error.argtypes = [vp, vp]
     lib.cce_copy_rows.argtypes = [ctypes.POINTER(RowCopy), ci, vp]
     for name in ("cce_linear_forward", "cce_linear_backward", "cce_gated_linear_forward", "cce_gated_linear_backward",

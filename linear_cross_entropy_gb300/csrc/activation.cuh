@@ -156,16 +156,86 @@ __device__ __forceinline__ void activate_pair(float& lo, float& hi) {
   }
 }
 
-// One of the 16-bit operand types from fp32, to nearest even.
-template <bool BF16>
-__device__ __forceinline__ uint16_t to_bits16(float f) {
-  if constexpr (BF16) return __bfloat16_as_ushort(__float2bfloat16_rn(f));
-  return __half_as_ushort(__float2half_rn(f));
+// ---------------------------------------------------------------- 16 bits
+// CCE_KEPT16 (include/cce_layers.h): times 2^-96 an fp32 value's exponent is that of the format, whose subnormals are
+// then fp32's; what remains is to round off 14 bits.
+__device__ __forceinline__ uint32_t to_kept16(float f) {
+  const uint32_t b = __float_as_uint(f * 0x1p-96f), m = b & 0x7fffffffu;
+  const uint32_t r = min((m + 0x2000u) >> 14, 0x7e00u);
+  return (f == f ? r : 0x7fffu) | (b >> 16 & 0x8000u);
 }
-template <bool BF16>
-__device__ __forceinline__ float from_bits16(uint16_t b) {
-  if constexpr (BF16) return __uint_as_float(static_cast<uint32_t>(b) << 16);
-  return __half2float(__ushort_as_half(b));
+__device__ __forceinline__ float from_kept16(uint32_t h) {
+  const uint32_t m = h & 0x7fffu;
+  const float f = __uint_as_float(m << 14) * 0x1p96f;
+  return copysignf(m < 0x7e00u ? f : m == 0x7e00u ? INFINITY : NAN, __uint_as_float(h << 16));
+}
+
+// The largest magnitude, or NaN if there is one.
+template <int N>
+__device__ __forceinline__ float largest(const float (&f)[N]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int x = 0; x + 1 < N; x += 2)
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(f[x]), "f"(f[x + 1]));
+  if (N % 2) asm("max.NaN.abs.f32 %0, %1, %2, %2;" : "=f"(m) : "f"(m), "f"(f[N - 1]));
+  return m;
+}
+
+// Pairs of values, the first in the low half.  Where none comes near the format's largest, two bits of exponent are 0
+// and what lies below them moves up: 3 instructions a value and not 10.
+template <int M>
+__device__ __forceinline__ void to_kept16(const float (&f)[2 * M], uint32_t (&two)[M]) {
+  if (largest(f) < 0x1p31f) {
+#pragma unroll
+    for (int x = 0; x < M; ++x) {
+      const float2 scaled = mul(Pair::of(f[2 * x], f[2 * x + 1]), Pair::both(0x1p-96f)).get();
+      const uint32_t lo = __float_as_uint(scaled.x), hi = __float_as_uint(scaled.y);
+      two[x] = __byte_perm(((lo * 4u + 0x8000u) & 0x7fffffffu) | (lo & 0x80000000u),
+                           ((hi * 4u + 0x8000u) & 0x7fffffffu) | (hi & 0x80000000u), 0x7632);
+    }
+  } else {
+#pragma unroll
+    for (int x = 0; x < M; ++x) two[x] = to_kept16(f[2 * x]) | to_kept16(f[2 * x + 1]) << 16;
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void from_kept16(const uint32_t* two, float (&f)[VEC]) {
+  if constexpr (VEC == 1) {
+    f[0] = from_kept16(two[0]);
+  } else {
+#pragma unroll
+    for (int x = 0; x < VEC; ++x) {
+      const int32_t up = static_cast<int32_t>(x & 1 ? two[x / 2] : two[x / 2] << 16);
+      f[x] = __uint_as_float(static_cast<uint32_t>(up >> 2) & 0x9fffc000u) * 0x1p96f;
+    }
+    if (!(largest(f) < 0x1p32f)) {
+#pragma unroll
+      for (int x = 0; x < VEC; ++x) f[x] = from_kept16(two[x / 2] >> (16 * (x & 1)));
+    }
+  }
+}
+
+// 16-bit types that the layers write.
+enum Bits16 { BITS_F16 = CCE_F16, BITS_BF16 = CCE_BF16, BITS_KEPT = CCE_KEPT16 };
+
+// Pairs of values, the first in the low half; one branch for all of them.
+template <int M>
+__device__ __forceinline__ void to_bits16(int type, const float (&f)[2 * M], uint32_t (&two)[M]) {
+  if (type == BITS_BF16) {
+#pragma unroll
+    for (int x = 0; x < M; ++x) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * x], f[2 * x + 1]);
+      two[x] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  } else if (type == BITS_F16) {
+#pragma unroll
+    for (int x = 0; x < M; ++x) {
+      const __half2 h = __floats2half2_rn(f[2 * x], f[2 * x + 1]);
+      two[x] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  } else {
+    to_kept16<M>(f, two);
+  }
 }
 
 }  // namespace cce

@@ -119,6 +119,17 @@ Tensor workspace(size_t need, const Tensor& x) {
   return at::empty({static_cast<int64_t>(need)}, x.options().dtype(at::kByte).requires_grad(false));
 }
 
+// Pre-activations are kept in 16 bits of the library's own for bf16 (CCE_KEPT16, to torch int16), as they are for fp16.
+at::ScalarType kept_type(const Tensor& x) { return x.scalar_type() == at::kBFloat16 ? at::kShort : x.scalar_type(); }
+
+int kept_code(const Tensor& z, const Tensor& x, const char* name) {
+  if (z.scalar_type() == x.scalar_type()) return type_code(z.scalar_type());
+  if (z.scalar_type() != kept_type(x))
+    refuse(name, " must be what the forward pass kept, or ", type_name(x.scalar_type()), " as x is, got ",
+           type_name(z.scalar_type()));
+  return CCE_KEPT16;
+}
+
 std::tuple<Tensor, Tensor> linear_forward(const Tensor& x, const Tensor& weight, const Tensor& bias,
                                           const Tensor& residual, const std::string& activation, const OptType& out,
                                           bool save) {
@@ -141,11 +152,13 @@ std::tuple<Tensor, Tensor> linear_forward(const Tensor& x, const Tensor& weight,
   const Tensor b = plain(bias);
   const auto shape = result_shape(x, s.N);
   Tensor y = at::empty(shape, x.options().dtype(y_type).requires_grad(false));
-  Tensor z = save && act != CCE_ACT_NONE ? at::empty(shape, x.options().requires_grad(false)) : Tensor();
+  const auto kept = x.options().dtype(kept_type(x)).requires_grad(false);
+  Tensor z = save && act != CCE_ACT_NONE ? at::empty(shape, kept) : Tensor();
   note_device(x);
   check_status(cce_linear_forward(pointer(xp.t), xp.pitch, pointer(wp.t), wp.pitch, s.type, pointer(b),
                                   b.defined() ? type_code(b.scalar_type()) : s.type, pointer(rp.t), rp.pitch, act, s.M,
-                                  s.N, s.K, pointer(y), s.N, type_code(y_type), pointer(z), s.N, pointer(ws), need,
+                                  s.N, s.K, pointer(y), s.N, type_code(y_type), pointer(z), s.N,
+                                  z.defined() ? kept_code(z, x, "z") : s.type, pointer(ws), need,
                                   stream_of(x)),
                "cce_linear_forward", ARGS);
   return {y, z};
@@ -161,11 +174,11 @@ std::tuple<Tensor, Tensor, Tensor> linear_backward(const Tensor& g, const Tensor
   check_rows(g, x, s.N, "grad_y");
   if (g.scalar_type() != x.scalar_type() && g.scalar_type() != at::kFloat)
     refuse("grad_y must be ", type_name(x.scalar_type()), " or torch.float32, got ", type_name(g.scalar_type()));
+  int z_type = s.type;
   if (act != CCE_ACT_NONE) {
     if (!z.defined()) refuse("z, the forward's pre-activation, is needed with an activation");
     check_rows(z, x, s.N, "z");
-    if (z.scalar_type() != x.scalar_type())
-      refuse("z must be ", type_name(x.scalar_type()), " as x is, got ", type_name(z.scalar_type()));
+    z_type = kept_code(z, x, "z");
   }
   const at::ScalarType b_type = bias_type ? *bias_type : x.scalar_type();
   if (type_code(b_type) < 0) refuse("bias_dtype must be bfloat16, float16 or float32, got ", type_name(b_type));
@@ -183,7 +196,7 @@ std::tuple<Tensor, Tensor, Tensor> linear_backward(const Tensor& g, const Tensor
   Tensor db = need_db ? at::empty({s.N}, plainly.dtype(b_type)) : Tensor();
   note_device(x);
   check_status(cce_linear_backward(pointer(gp.t), gp.pitch, type_code(g.scalar_type()), pointer(xp.t), xp.pitch,
-                                   pointer(wp.t), wp.pitch, s.type, pointer(zp.t), zp.pitch, act, s.M, s.N, s.K,
+                                   pointer(wp.t), wp.pitch, s.type, pointer(zp.t), zp.pitch, z_type, act, s.M, s.N, s.K,
                                    pointer(dx), pointer(dw), pointer(db), type_code(b_type), pointer(ws), need,
                                    stream_of(x)),
                "cce_linear_backward", ARGS);
@@ -208,12 +221,13 @@ std::tuple<Tensor, Tensor, Tensor> gated_forward(const Tensor& x, const Tensor& 
   m.copy(x);
   const auto shape = result_shape(x, s.N);
   const auto plainly = x.options().requires_grad(false);
-  Tensor y = at::empty(shape, plainly), z0 = save ? at::empty(shape, plainly) : Tensor(),
-         z1 = save ? at::empty(shape, plainly) : Tensor();
+  const auto kept = plainly.dtype(kept_type(x));
+  Tensor y = at::empty(shape, plainly), z0 = save ? at::empty(shape, kept) : Tensor(),
+         z1 = save ? at::empty(shape, kept) : Tensor();
   note_device(x);
   check_status(cce_gated_linear_forward(pointer(xp.t), xp.pitch, pointer(gp.t), gp.pitch, pointer(up.t), up.pitch,
                                         s.type, act, s.M, s.N, s.K, pointer(y), s.N, pointer(z0), pointer(z1), s.N,
-                                        pointer(ws), need, stream_of(x)),
+                                        save ? kept_code(z0, x, "gate") : s.type, pointer(ws), need, stream_of(x)),
                "cce_gated_linear_forward", ARGS);
   return {y, z0, z1};
 }
@@ -229,11 +243,12 @@ std::tuple<Tensor, Tensor, Tensor> gated_backward(const Tensor& g, const Tensor&
   if (up_weight.size(0) != s.N)
     refuse("gate_weight and up_weight must have one shape, got ", gate_weight.sizes(), " and ", up_weight.sizes());
   const int act = activation_code(activation);
-  for (const auto& [t, name] : {std::pair{&g, "grad_y"}, std::pair{&gate, "gate"}, std::pair{&up, "up"}}) {
+  for (const auto& [t, name] : {std::pair{&g, "grad_y"}, std::pair{&gate, "gate"}, std::pair{&up, "up"}})
     check_rows(*t, x, s.N, name);
-    if (t->scalar_type() != x.scalar_type())
-      refuse(name, " must be ", type_name(x.scalar_type()), " as x is, got ", type_name(t->scalar_type()));
-  }
+  if (g.scalar_type() != x.scalar_type())
+    refuse("grad_y must be ", type_name(x.scalar_type()), " as x is, got ", type_name(g.scalar_type()));
+  const int z_type = kept_code(gate, x, "gate");
+  if (kept_code(up, x, "up") != z_type) refuse("gate and up must have one type");
   const at::NoGradGuard no_grad;
   const c10::cuda::CUDAGuard guard(x.device());
   const size_t need = cce_gated_linear_backward_workspace_bytes(s.M, s.N, s.K);
@@ -249,7 +264,7 @@ std::tuple<Tensor, Tensor, Tensor> gated_backward(const Tensor& g, const Tensor&
   note_device(x);
   check_status(cce_gated_linear_backward(pointer(gy.t), gy.pitch, pointer(xp.t), xp.pitch, pointer(wg.t), wg.pitch,
                                          pointer(wu.t), wu.pitch, s.type, pointer(z0.t), z0.pitch, pointer(z1.t),
-                                         z1.pitch, act, s.M, s.N, s.K, pointer(dx), pointer(dg), pointer(du),
+                                         z1.pitch, z_type, act, s.M, s.N, s.K, pointer(dx), pointer(dg), pointer(du),
                                          pointer(ws), need, stream_of(x)),
                "cce_gated_linear_backward", ARGS);
   return {dx, dg, du};

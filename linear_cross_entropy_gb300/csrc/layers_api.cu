@@ -23,6 +23,8 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t type_bytes(int t) { return t == CCE_F32 ? 4 : 2; }
 bool type_ok(int t) { return t == CCE_F32 || t == CCE_F16 || t == CCE_BF16; }
 bool operand_type(int t) { return t == CCE_F16 || t == CCE_BF16; }
+// How pre-activations are kept.
+bool kept_type(int z, int type) { return z == type || (z == CCE_KEPT16 && type == CCE_BF16); }
 bool act_ok(int act) { return act >= CCE_ACT_NONE && act <= CCE_ACT_SILU; }
 bool sizes_ok(int64_t M, int64_t N, int64_t K) {
   return M >= 0 && M < LIMIT && N >= 1 && N < WIDTH && K >= 1 && K < WIDTH && M * N < MATRIX && M * K < MATRIX &&
@@ -465,8 +467,9 @@ size_t cce_gated_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K
 cce_status cce_linear_forward(const void* x, int64_t x_pitch, const void* weight, int64_t w_pitch, int type,
                               const void* bias, int bias_type, const void* residual, int64_t res_pitch, int act,
                               int64_t M, int64_t N, int64_t K, void* y, int64_t y_pitch, int y_type, void* z,
-                              int64_t z_pitch, void* workspace, size_t ws_bytes, void* stream) {
-  if (!operand_type(type) || !type_ok(bias_type) || (y_type != type && y_type != CCE_F32) || !act_ok(act))
+                              int64_t z_pitch, int z_type, void* workspace, size_t ws_bytes, void* stream) {
+  if (!operand_type(type) || !type_ok(bias_type) || (y_type != type && y_type != CCE_F32) || !act_ok(act) ||
+      !kept_type(z_type, type))
     return CCE_ERR_ARG;
   if (!sizes_ok(M, N, K)) return CCE_ERR_SHAPE;
   const Matrix xm{x, x_pitch, type, M, K}, wm{weight, w_pitch, type, N, K};
@@ -476,15 +479,15 @@ cce_status cce_linear_forward(const void* x, int64_t x_pitch, const void* weight
                check_matrix({z, z_pitch, type, M, N}, true),
                check_workspace(workspace, ws_bytes, forward_bytes(M, N, K, false)));
   if (st != CCE_OK) return st;
-  const LinEpilogue e{y, y_pitch, bias, residual, res_pitch, {z, nullptr}, z_pitch, y_type, bias_type, act};
+  const LinEpilogue e{y, y_pitch, bias, residual, res_pitch, {z, nullptr}, z_pitch, y_type, bias_type, act, z_type};
   return forward(xm, &wm, false, M, N, K, e, workspace, static_cast<cudaStream_t>(stream));
 }
 
 cce_status cce_gated_linear_forward(const void* x, int64_t x_pitch, const void* gate_weight, int64_t gw_pitch,
                                     const void* up_weight, int64_t uw_pitch, int type, int act, int64_t M, int64_t N,
                                     int64_t K, void* y, int64_t y_pitch, void* gate, void* up, int64_t z_pitch,
-                                    void* workspace, size_t ws_bytes, void* stream) {
-  if (!operand_type(type) || !act_ok(act)) return CCE_ERR_ARG;
+                                    int z_type, void* workspace, size_t ws_bytes, void* stream) {
+  if (!operand_type(type) || !act_ok(act) || !kept_type(z_type, type)) return CCE_ERR_ARG;
   if (!sizes_ok(M, N, K)) return CCE_ERR_SHAPE;
   if (!gate != !up) return CCE_ERR_NULL;
   const Matrix xm{x, x_pitch, type, M, K};
@@ -494,15 +497,17 @@ cce_status cce_gated_linear_forward(const void* x, int64_t x_pitch, const void* 
                                  check_matrix({up, z_pitch, type, M, N}, true),
                                  check_workspace(workspace, ws_bytes, forward_bytes(M, N, K, true)));
   if (st != CCE_OK) return st;
-  const LinEpilogue e{y, y_pitch, nullptr, nullptr, 0, {gate, up}, z_pitch, type, type, act};
+  const LinEpilogue e{y, y_pitch, nullptr, nullptr, 0, {gate, up}, z_pitch, type, type, act, z_type};
   return forward(xm, wm, true, M, N, K, e, workspace, static_cast<cudaStream_t>(stream));
 }
 
 cce_status cce_linear_backward(const void* grad_y, int64_t g_pitch, int y_type, const void* x, int64_t x_pitch,
-                               const void* weight, int64_t w_pitch, int type, const void* z, int64_t z_pitch, int act,
-                               int64_t M, int64_t N, int64_t K, void* grad_x, void* grad_weight, void* grad_bias,
-                               int bias_type, void* workspace, size_t ws_bytes, void* stream) {
-  if (!operand_type(type) || !type_ok(bias_type) || (y_type != type && y_type != CCE_F32) || !act_ok(act))
+                               const void* weight, int64_t w_pitch, int type, const void* z, int64_t z_pitch,
+                               int z_type, int act, int64_t M, int64_t N, int64_t K, void* grad_x,
+                               void* grad_weight, void* grad_bias, int bias_type, void* workspace, size_t ws_bytes,
+                               void* stream) {
+  if (!operand_type(type) || !type_ok(bias_type) || (y_type != type && y_type != CCE_F32) || !act_ok(act) ||
+      !kept_type(z_type, type))
     return CCE_ERR_ARG;
   if (!sizes_ok(M, N, K)) return CCE_ERR_SHAPE;
   const Matrix xm{x, x_pitch, type, M, K}, wm{weight, w_pitch, type, N, K};
@@ -535,6 +540,7 @@ cce_status cce_linear_backward(const void* grad_y, int64_t g_pitch, int y_type, 
     g.dy_type = y_type;
     g.z[0] = act == CCE_ACT_NONE ? nullptr : z;
     g.z_pitch[0] = z_pitch;
+    g.kept = z_type == CCE_KEPT16;
     g.dz[0] = staged ? ws : nullptr;
     g.dz_pitch = l.pitch;
     g.part = grad_bias ? reinterpret_cast<float*>(ws + l.dz) : nullptr;
@@ -556,10 +562,10 @@ cce_status cce_linear_backward(const void* grad_y, int64_t g_pitch, int y_type, 
 cce_status cce_gated_linear_backward(const void* grad_y, int64_t g_pitch, const void* x, int64_t x_pitch,
                                      const void* gate_weight, int64_t gw_pitch, const void* up_weight,
                                      int64_t uw_pitch, int type, const void* gate, int64_t gate_pitch, const void* up,
-                                     int64_t up_pitch, int act, int64_t M, int64_t N, int64_t K, void* grad_x,
-                                     void* grad_gate_weight, void* grad_up_weight, void* workspace, size_t ws_bytes,
+                                     int64_t up_pitch, int z_type, int act, int64_t M, int64_t N, int64_t K,
+                                     void* grad_x, void* grad_gate_weight, void* grad_up_weight, void* workspace, size_t ws_bytes,
                                      void* stream) {
-  if (!operand_type(type) || !act_ok(act)) return CCE_ERR_ARG;
+  if (!operand_type(type) || !act_ok(act) || !kept_type(z_type, type)) return CCE_ERR_ARG;
   if (!sizes_ok(M, N, K)) return CCE_ERR_SHAPE;
   const Matrix xm{x, x_pitch, type, M, K};
   const Matrix wm[2] = {{gate_weight, gw_pitch, type, N, K}, {up_weight, uw_pitch, type, N, K}};
@@ -588,6 +594,7 @@ cce_status cce_gated_linear_backward(const void* grad_y, int64_t g_pitch, const 
   g.z[1] = up;
   g.z_pitch[0] = gate_pitch;
   g.z_pitch[1] = up_pitch;
+  g.kept = z_type == CCE_KEPT16;
   // one matrix after the other: rows of each start on 16 bytes
   g.dz[0] = ws;
   g.dz[1] = ws + size_t(2) * M * l.pitch;

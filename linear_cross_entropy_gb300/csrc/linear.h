@@ -21,9 +21,9 @@ struct LinEpilogue {
   const void* bias;  // [I], may be null
   const void* res;   // of y's type, may be null
   int64_t res_pitch;
-  void* z[2];  // pre-activations in the operands' type, may be null
+  void* z[2];  // pre-activations, may be null
   int64_t z_pitch;
-  int y_type, bias_type, act;
+  int y_type, bias_type, act, z_type;  // z_type: the operands', or CCE_KEPT16
 };
 
 // out[j][i] = epilogue(sum over k of A(i, k) B(j, k)).  The sum may run over two
@@ -120,6 +120,7 @@ struct LinGrad {
   int dy_type;
   const void* z[2];
   int64_t z_pitch[2];
+  int kept;  // z is CCE_KEPT16, else of the operands' type
   void* dz[2];  // may be null (sums alone)
   int64_t dz_pitch;
   float* part;  // [parts][N], may be null (no sums)

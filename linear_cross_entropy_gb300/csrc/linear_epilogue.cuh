@@ -63,6 +63,15 @@ __device__ __forceinline__ void put(void* base, int64_t at, const float (&f)[VEC
   v.store(static_cast<T*>(base) + at);
 }
 
+template <int VEC>
+__device__ __forceinline__ void put_kept(void* base, int64_t at, const float (&f)[VEC]) {
+  Vec<__nv_bfloat16, VEC> v;
+  v.zero();
+#pragma unroll
+  for (int u = 0; u < VEC; ++u) v.w[u / 2] |= to_kept16(f[u]) << (16 * (u & 1));
+  v.store(static_cast<__nv_bfloat16*>(base) + at);
+}
+
 // VEC neighbouring values i, ... of row j, all inside of the matrices, which VEC values of each start on their size.  z0:
 // the product with x (gated: the gate's), z1: gated: the up projection's.  T: the operands' type.
 template <typename T, bool GATED, int VEC>
@@ -76,8 +85,14 @@ __device__ __forceinline__ void finish_row(const LinEpilogue& e, int64_t j, int6
     for (int u = 0; u < VEC; ++u) z0[u] += b[u];
   }
   if (e.z[0]) {
-    put<T>(e.z[0], j * e.z_pitch + i, z0);
-    if (GATED) put<T>(e.z[1], j * e.z_pitch + i, z1);
+    const int64_t at = j * e.z_pitch + i;
+    if (e.z_type == CCE_KEPT16) {
+      put_kept(e.z[0], at, z0);
+      if (GATED) put_kept(e.z[1], at, z1);
+    } else {
+      put<T>(e.z[0], at, z0);
+      if (GATED) put<T>(e.z[1], at, z1);
+    }
   }
   activate_all(e.act, z0);
   if (GATED) {

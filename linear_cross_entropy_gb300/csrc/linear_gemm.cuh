@@ -343,28 +343,18 @@ struct Fragment {
   // As 16-bit values to the first n columns and `rows` rows (a multiple of 8) of a matrix whose rows start on 16 bytes;
   // p: the thread's place in it, column lane / R and row 8 (lane % R).  `tile`: 16 R bytes of shared memory for each
   // column, swizzled so that neither access has bank conflicts.
-  __device__ __forceinline__ void store_wide(uint32_t tile, uint16_t* p, int64_t pitch, bool bf16, int n, int rows) const {
+  __device__ __forceinline__ void store_wide(uint32_t tile, uint16_t* p, int64_t pitch, int type, int n, int rows) const {
     const auto place = [&](uint32_t j, uint32_t vector) {
       return tile + j * 16u * R + ((vector ^ (R == 4 ? j >> 1 & 3u : j >> 2 & 1u)) << 4);
     };
     const uint32_t lane = lane_id(), which = lane >> 3;
     const uint32_t to = place(8u * (which / R) + (lane & 7u), which % R), from = place(lane / R, lane % R);
+    uint32_t two[4 * R];
+    to_bits16(type, v, two);
     __syncwarp();  // what was there has been read
 #pragma unroll
-    for (int q = 0; q < R; ++q) {  // four matrices at a time: 4 / R pairs of columns
-      uint32_t two[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const float lo = v[8 * q + 2 * x], hi = v[8 * q + 2 * x + 1];
-        if (bf16) {
-          two[x] = pack_bf16x2(lo, hi);
-        } else {
-          const __half2 h = __floats2half2_rn(lo, hi);
-          two[x] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-      }
-      stmatrix_columns(to + 512u * q, two[0], two[1], two[2], two[3]);  // 32 / R columns on, 512 bytes
-    }
+    for (int q = 0; q < R; ++q)  // four matrices at a time: 32 / R columns, 512 bytes
+      stmatrix_columns(to + 512u * q, two[4 * q], two[4 * q + 1], two[4 * q + 2], two[4 * q + 3]);
     __syncwarp();
     uint4 w[R];
 #pragma unroll
@@ -381,8 +371,18 @@ struct Fragment {
     }
   }
   // To the first n columns and `rows` rows of a matrix, whose element of the thread's first place is at p.
-  template <typename T>
-  __device__ __forceinline__ void store(T* p, int64_t pitch, bool bf16, int n, int rows) const {
+  __device__ __forceinline__ void store(float* p, int64_t pitch, int n, int rows) const {
+    store_each<float>(p, pitch, n, rows, [&](int x) { return v[x]; });
+  }
+  __device__ __forceinline__ void store(uint16_t* p, int64_t pitch, int type, int n, int rows) const {
+    uint32_t two[4 * R];
+    to_bits16(type, v, two);
+    store_each<uint16_t>(p, pitch, n, rows, [&](int x) { return static_cast<uint16_t>(two[x / 2] >> (16 * (x & 1))); });
+  }
+
+ private:
+  template <typename T, typename Value>
+  __device__ __forceinline__ void store_each(T* p, int64_t pitch, int n, int rows, Value value) const {
     const int c0 = 2 * static_cast<int>(lane_id() & 3u), r0 = static_cast<int>(lane_id() >> 2);
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
@@ -392,13 +392,7 @@ struct Fragment {
         if (8 * b + c0 + c >= n) continue;
 #pragma unroll
         for (int m = 0; m < R; ++m) {
-          if (r0 + 8 * m >= rows) continue;
-          const float f = v[2 * R * b + 2 * m + c];
-          if constexpr (sizeof(T) == 4) {
-            row[8 * m] = f;
-          } else {
-            row[8 * m] = bf16 ? to_bits16<true>(f) : to_bits16<false>(f);
-          }
+          if (r0 + 8 * m < rows) row[8 * m] = value(2 * R * b + 2 * m + c);
         }
       }
     }
@@ -476,14 +470,21 @@ struct Share {
   float bias[4];
 };
 
-// Wide results of the accumulator alone: the next chunk comes while one is finished, and nothing is decided on the way.
-template <bool PAIR, bool GATED, int ACT>
-__device__ __forceinline__ void finish_lean(const Shared& s, const Share& w, const LinEpilogue& e, bool bf16, int acc,
+// Wide results of the accumulator alone, for gated layers with the values in front of the activation (KEEP) or without: the
+// next chunk comes while one is finished.  (4,096 x 4,864 x 896 with them took 57 us by finish_any and 54 so.  Layers without
+// a gate hold twice the values of one matrix: their registers ran out, 42 us became 50.)
+template <bool PAIR, bool GATED, int ACT, bool KEEP>
+__device__ __forceinline__ void finish_lean(const Shared& s, const Share& w, const LinEpilogue& e, int type, int acc,
                                             uint32_t release) {
   constexpr int R = GATED ? 2 : 4;
   const int lane = static_cast<int>(lane_id());
   const int64_t pitch = e.y_pitch;
   uint16_t* y = static_cast<uint16_t*>(e.y) + static_cast<int64_t>(w.j0 + lane / R) * pitch + w.i0 + 8 * (lane % R);
+  const int64_t z_pitch = e.z_pitch;
+  int64_t z = static_cast<int64_t>(w.j0 + lane / R) * z_pitch + w.i0 + 8 * (lane % R);
+  const auto keep = [&](const Fragment<2>& f, void* to, int n) {
+    f.store_wide(w.tile, static_cast<uint16_t*>(to) + z, z_pitch, e.z_type, n, w.rows);
+  };
   int n = w.cols;
   const auto step = [&](Chunk& now, Chunk& next, int c) {
     now.wait();
@@ -495,19 +496,24 @@ __device__ __forceinline__ void finish_lean(const Shared& s, const Share& w, con
     if constexpr (GATED) {
       Fragment<2> gate, up;
       now.get(gate, up);
+      if (KEEP) {
+        keep(gate, e.z[0], n);
+        keep(up, e.z[1], n);
+      }
       activate_as<ACT>(gate.v);
 #pragma unroll
       for (int x = 0; x < 16; ++x) gate.v[x] *= up.v[x];
-      gate.store_wide(w.tile, y, pitch, bf16, n, w.rows);
+      gate.store_wide(w.tile, y, pitch, type, n, w.rows);
     } else {
       Fragment<4> f;
       now.get(f);
 #pragma unroll
       for (int x = 0; x < 32; ++x) f.v[x] += w.bias[x >> 1 & 3];
       activate_as<ACT>(f.v);
-      f.store_wide(w.tile, y, pitch, bf16, n, w.rows);
+      f.store_wide(w.tile, y, pitch, type, n, w.rows);
     }
     y += CHUNK * PHASES * pitch;
+    z += CHUNK * PHASES * z_pitch;
     n -= CHUNK * PHASES;
   };
   Chunk a, b;
@@ -518,9 +524,9 @@ __device__ __forceinline__ void finish_lean(const Shared& s, const Share& w, con
   }
 }
 
-// Everything else: a residual, pre-activations for the backward pass, fp32 results and ones off 16 bytes.
+// Everything else: a residual, a layer's values in front of its activation, fp32 results and ones off 16 bytes.
 template <bool PAIR, bool GATED, int ACT>
-__device__ __forceinline__ void finish_any(const Shared& s, const Share& w, const LinEpilogue& e, bool wide, bool bf16,
+__device__ __forceinline__ void finish_any(const Shared& s, const Share& w, const LinEpilogue& e, bool wide, int type,
                                            int acc, uint32_t release) {
   constexpr int R = GATED ? 2 : 4;
   const int lane = static_cast<int>(lane_id());
@@ -547,36 +553,36 @@ __device__ __forceinline__ void finish_any(const Shared& s, const Share& w, cons
     } else {
       __syncwarp();
     }
-    const auto put = [&](const Fragment<R>& f, void* to, int64_t wide_at, int64_t pitch) {
+    const auto put = [&](const Fragment<R>& f, void* to, int64_t wide_at, int64_t pitch, int as) {
       if (wide) {
-        f.store_wide(w.tile, static_cast<uint16_t*>(to) + wide_at + jc * pitch, pitch, bf16, n, w.rows);
+        f.store_wide(w.tile, static_cast<uint16_t*>(to) + wide_at + jc * pitch, pitch, as, n, w.rows);
       } else {
-        f.store(static_cast<uint16_t*>(to) + (tj + jc) * pitch + ti, pitch, bf16, n, w.rows);
+        f.store(static_cast<uint16_t*>(to) + (tj + jc) * pitch + ti, pitch, as, n, w.rows);
       }
     };
     if constexpr (GATED) {
       Fragment<2> gate, up;
       chunk.get(gate, up);
       if (has_z) {
-        put(gate, e.z[0], wide_z, e.z_pitch);
-        put(up, e.z[1], wide_z, e.z_pitch);
+        put(gate, e.z[0], wide_z, e.z_pitch, e.z_type);
+        put(up, e.z[1], wide_z, e.z_pitch, e.z_type);
       }
       activate_as<ACT>(gate.v);
 #pragma unroll
       for (int x = 0; x < 16; ++x) gate.v[x] *= up.v[x];
-      put(gate, e.y, wide_y, e.y_pitch);
+      put(gate, e.y, wide_y, e.y_pitch, type);
     } else {
       Fragment<4> f;
       chunk.get(f);
 #pragma unroll
       for (int x = 0; x < 32; ++x) f.v[x] += w.bias[x >> 1 & 3];
-      if (has_z) put(f, e.z[0], wide_z, e.z_pitch);
+      if (has_z) put(f, e.z[0], wide_z, e.z_pitch, e.z_type);
       activate_as<ACT>(f.v);
-      if (has_res) res.add_to(f, y32, bf16);
+      if (has_res) res.add_to(f, y32, type == BITS_BF16);
       if (y32) {
-        f.store(static_cast<float*>(e.y) + (tj + jc) * e.y_pitch + ti, e.y_pitch, bf16, n, w.rows);
+        f.store(static_cast<float*>(e.y) + (tj + jc) * e.y_pitch + ti, e.y_pitch, n, w.rows);
       } else {
-        put(f, e.y, wide_y, e.y_pitch);
+        put(f, e.y, wide_y, e.y_pitch, type);
       }
     }
   }
@@ -602,12 +608,12 @@ __device__ __forceinline__ void store_partial(const Shared& s, const Share& w, c
     if constexpr (GATED) {
       Fragment<2> gate, up;
       chunk.get(gate, up);
-      gate.store(to, p.I, true, n, w.rows);
-      up.store(to + static_cast<int64_t>(p.J) * p.I, p.I, true, n, w.rows);
+      gate.store(to, p.I, n, w.rows);
+      up.store(to + static_cast<int64_t>(p.J) * p.I, p.I, n, w.rows);
     } else {
       Fragment<4> f;
       chunk.get(f);
-      f.store(to, p.I, true, n, w.rows);
+      f.store(to, p.I, n, w.rows);
     }
   }
 }
@@ -622,7 +628,7 @@ __device__ __forceinline__ void epilogue_loop(const LinArgs& a, const Shared& s,
   const int quarter = warp & 3, phase_of = (warp - 2) >> 2;
   const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
   const uint32_t release = PAIR ? mapa_shared(smem_u32(s.acc_empty), 0) : smem_u32(s.acc_empty);
-  const bool bf16 = a.bf16;
+  const int type = a.bf16 ? BITS_BF16 : BITS_F16;
   Share w;
   w.tile = smem_u32(s.staging + (quarter * PHASES + phase_of) * STAGING);
   int acc = 0;
@@ -636,7 +642,7 @@ __device__ __forceinline__ void epilogue_loop(const LinArgs& a, const Shared& s,
     w.rows = p.I - w.i0;
     w.cols = p.J - w.j0;
     w.chunks = min((p.jt / CHUNK - phase_of + PHASES - 1) / PHASES, (w.cols + CHUNK * PHASES - 1) / (CHUNK * PHASES));
-    const bool whole = p.splits == 1, wide = p.wide, lean = wide && !e.z[0] && (GATED || !e.res);
+    const bool whole = p.splits == 1, wide = p.wide;
     if constexpr (!GATED) {
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
@@ -655,10 +661,12 @@ __device__ __forceinline__ void epilogue_loop(const LinArgs& a, const Shared& s,
       release_accumulator<PAIR>(s, acc, release);
     } else if (!whole) {
       store_partial<PAIR, GATED>(s, w, p, t.split, acc, release);
-    } else if (lean) {
-      finish_lean<PAIR, GATED, ACT>(s, w, e, bf16, acc, release);
+    } else if (wide && !e.z[0] && !e.res) {
+      finish_lean<PAIR, GATED, ACT, false>(s, w, e, type, acc, release);
+    } else if (GATED && wide) {
+      finish_lean<PAIR, GATED, ACT, GATED>(s, w, e, type, acc, release);
     } else {
-      finish_any<PAIR, GATED, ACT>(s, w, e, wide, bf16, acc, release);
+      finish_any<PAIR, GATED, ACT>(s, w, e, wide, type, acc, release);
     }
     acc ^= 1;
     if (acc == 0) acc_phase ^= 1u;

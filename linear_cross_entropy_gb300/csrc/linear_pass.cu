@@ -66,12 +66,21 @@ __device__ __forceinline__ void grad_as(float (&d0)[VEC], float (&d1)[VEC], cons
   }
 }
 
+template <typename T, int VEC>
+__device__ __forceinline__ void set_part(uint32_t* w, const float (&f)[VEC]) {
+  Vec<T, VEC> v;
+  v.set(f);
+#pragma unroll
+  for (int x = 0; x < (VEC + 1) / 2; ++x) w[x] = v.w[x];
+}
+
 template <typename T, typename TY, bool GATED, int VEC>
 __global__ void __launch_bounds__(THREADS, 3) grad_kernel(const __grid_constant__ LinGrad a) {
   let_next_start();
   wait_for_previous();
   const int tx = static_cast<int>(threadIdx.x) % COLS, ty = static_cast<int>(threadIdx.x) / COLS;
   const int col = (static_cast<int>(blockIdx.x) * COLS + tx) * VEC;
+  constexpr int PART = VEC < 4 ? VEC : 4;  // values at a time, for fewer registers
   float sum[VEC] = {};
   if (col < a.N) {
     const int64_t step = static_cast<int64_t>(gridDim.y) * GROUPS;
@@ -91,46 +100,53 @@ __global__ void __launch_bounds__(THREADS, 3) grad_kernel(const __grid_constant_
       for (int u = 0; u < UNROLL; ++u) {
         const int64_t r = r0 + u * step;
         if (r >= a.M) break;
-        float g[VEC], f0[VEC], f1[VEC], d0[VEC], d1[VEC];
+        Vec<T, VEC> o0, o1;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          g[e] = dy[u].get(e);
-          f0[e] = z0[u].get(e);
-          if (GATED) f1[e] = z1[u].get(e);
-        }
-        switch (a.act) {
-          case CCE_ACT_RELU: grad_as<CCE_ACT_RELU, GATED>(d0, d1, g, f0, f1); break;
-          case CCE_ACT_GELU: grad_as<CCE_ACT_GELU, GATED>(d0, d1, g, f0, f1); break;
-          case CCE_ACT_GELU_TANH: grad_as<CCE_ACT_GELU_TANH, GATED>(d0, d1, g, f0, f1); break;
-          case CCE_ACT_SILU: grad_as<CCE_ACT_SILU, GATED>(d0, d1, g, f0, f1); break;
-          default: grad_as<CCE_ACT_NONE, GATED>(d0, d1, g, f0, f1); break;
-        }
-        Vec<T, VEC> o;
-        if (a.dz[0]) {
-          o.set(d0);
-          o.store(static_cast<T*>(a.dz[0]) + r * a.dz_pitch + col);
-        }
-        if (GATED) {
-          o.set(d1);
-          o.store(static_cast<T*>(a.dz[1]) + r * a.dz_pitch + col);
-        }
+        for (int h = 0; h < VEC; h += PART) {
+          float g[PART], f0[PART], f1[PART], d0[PART], d1[PART];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) sum[e] += d0[e];
+          for (int e = 0; e < PART; ++e) g[e] = dy[u].get(h + e);
+          if (a.kept) {
+            from_kept16<PART>(z0[u].w + h / 2, f0);
+            if (GATED) from_kept16<PART>(z1[u].w + h / 2, f1);
+          } else {
+#pragma unroll
+            for (int e = 0; e < PART; ++e) {
+              f0[e] = z0[u].get(h + e);
+              if (GATED) f1[e] = z1[u].get(h + e);
+            }
+          }
+          switch (a.act) {
+            case CCE_ACT_RELU: grad_as<CCE_ACT_RELU, GATED>(d0, d1, g, f0, f1); break;
+            case CCE_ACT_GELU: grad_as<CCE_ACT_GELU, GATED>(d0, d1, g, f0, f1); break;
+            case CCE_ACT_GELU_TANH: grad_as<CCE_ACT_GELU_TANH, GATED>(d0, d1, g, f0, f1); break;
+            case CCE_ACT_SILU: grad_as<CCE_ACT_SILU, GATED>(d0, d1, g, f0, f1); break;
+            default: grad_as<CCE_ACT_NONE, GATED>(d0, d1, g, f0, f1); break;
+          }
+          set_part<T>(o0.w + h / 2, d0);
+          if (GATED) set_part<T>(o1.w + h / 2, d1);
+#pragma unroll
+          for (int e = 0; e < PART; ++e) sum[h + e] += GATED ? 0.0f : d0[e];
+        }
+        if (a.dz[0]) o0.store(static_cast<T*>(a.dz[0]) + r * a.dz_pitch + col);
+        if (GATED) o1.store(static_cast<T*>(a.dz[1]) + r * a.dz_pitch + col);
       }
     }
   }
-  if (!a.part) return;
-  __shared__ float sums[GROUPS][COLS * VEC];
+  if constexpr (!GATED) {
+    if (!a.part) return;
+    __shared__ float sums[GROUPS][COLS * VEC];
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) sums[ty][tx * VEC + e] = sum[e];
-  __syncthreads();
-  for (int c = static_cast<int>(threadIdx.x); c < COLS * VEC; c += THREADS) {
-    const int at = static_cast<int>(blockIdx.x) * COLS * VEC + c;
-    if (at >= a.N) break;
-    float t = 0.0f;
+    for (int e = 0; e < VEC; ++e) sums[ty][tx * VEC + e] = sum[e];
+    __syncthreads();
+    for (int c = static_cast<int>(threadIdx.x); c < COLS * VEC; c += THREADS) {
+      const int at = static_cast<int>(blockIdx.x) * COLS * VEC + c;
+      if (at >= a.N) break;
+      float t = 0.0f;
 #pragma unroll
-    for (int v = 0; v < GROUPS; ++v) t += sums[v][c];
-    a.part[static_cast<int64_t>(blockIdx.y) * a.N + at] = t;
+      for (int v = 0; v < GROUPS; ++v) t += sums[v][c];
+      a.part[static_cast<int64_t>(blockIdx.y) * a.N + at] = t;
+    }
   }
 }
 

@@ -15,8 +15,9 @@ x's type or float32.  x, weights and gradients may be strided: rows at one pitch
 on 16 bytes and a multiple of 8 elements apart, are read in place, others
 (hidden[:, :-1], odd widths) are copied first.  Activations: None, "relu", "gelu"
 (exact), "gelu_tanh", "silu".  For the backward pass what goes into the
-activation is kept in x's type, and the gradient in front of it is rounded to
-that type for its products.
+activation is kept in 16 bits, two of which more are fraction than bf16 has (torch
+int16 words that only the backward reads; fp16 for fp16), and the gradient in front
+of it is rounded to x's type for its products.
 
 Calls run on the current stream of x's device and can be captured into a CUDA
 graph (a backward pass while no graph of autograd that was made outside of the
@@ -61,15 +62,16 @@ def _on(stream, call, *args):
 
 def cce_linear_forward(x, weight, bias=None, residual=None, activation=None, *, out_dtype=None, save=False,
                        stream=None):
-    """(y, z): y = act(z) + residual with z = x weight^T + bias.  z is in x's
-    type, for cce_linear_backward; None with save=False or without activation."""
+    """(y, z): y = act(z) + residual with z = x weight^T + bias.  z is for
+    cce_linear_backward alone: int16 words for bf16, else values of x's type; None with
+    save=False or without activation."""
     return _on(stream, _native.linear_forward, x, weight, bias, residual, _name(activation), out_dtype, save)
 
 
 def cce_linear_backward(grad_y, x, weight, z=None, activation=None, *, need_dx=True, need_dweight=True,
                         need_dbias=True, bias_dtype=None, stream=None):
-    """(dx, dweight, dbias) of a linear layer whose forward gave z; None for
-    those not needed.  dbias has bias_dtype (x's type if not given).  The
+    """(dx, dweight, dbias) of a linear layer whose forward gave z (or z in x's
+    type); None for those not needed.  dbias has bias_dtype (x's type if not given).  The
     residual's gradient is grad_y."""
     return _on(stream, _native.linear_backward, grad_y, x, weight, z, _name(activation), need_dx, need_dweight,
                need_dbias, bias_dtype)
@@ -77,14 +79,14 @@ def cce_linear_backward(grad_y, x, weight, z=None, activation=None, *, need_dx=T
 
 def cce_gated_linear_forward(x, gate_weight, up_weight, activation="silu", *, save=False, stream=None):
     """(y, gate, up): y = act(gate) * up with gate = x gate_weight^T and
-    up = x up_weight^T; gate and up are None with save=False."""
+    up = x up_weight^T.  gate and up are as z in cce_linear_forward, None with save=False."""
     return _on(stream, _native.gated_linear_forward, x, gate_weight, up_weight, _name(activation), save)
 
 
 def cce_gated_linear_backward(grad_y, x, gate_weight, up_weight, gate, up, activation="silu", *, need_dx=True,
                               need_dgate_weight=True, need_dup_weight=True, stream=None):
     """(dx, dgate_weight, dup_weight) of a gated linear layer whose forward
-    gave gate and up; None for those not needed."""
+    gave gate and up (or those in x's type); None for those not needed."""
     return _on(stream, _native.gated_linear_backward, grad_y, x, gate_weight, up_weight, gate, up, _name(activation),
                need_dx, need_dgate_weight, need_dup_weight)
 

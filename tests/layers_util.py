@@ -55,8 +55,26 @@ def steps(K):
 
 
 def half_step(ref, dtype):
-    fi = torch.finfo(dtype)
-    return ref.abs() * (fi.eps / 2) + fi.smallest_normal * fi.eps / 2
+    """Half a step at most; int16 stands for what the forward keeps: 9 bits of fraction, down to 2^-30."""
+    eps, least = (2.0 ** -9, 2.0 ** -30) if dtype == torch.int16 else (torch.finfo(dtype).eps, torch.finfo(dtype).smallest_normal)
+    return ref.abs() * (eps / 2) + least * eps / 2
+
+
+def kept(words):
+    """The values of what a forward keeps for its backward: sign, 6 bits of exponent (bias 31), 9 of fraction."""
+    if words.dtype != torch.int16:
+        return words.double()
+    w = words.to(torch.int64) & 0xFFFF
+    exponent, fraction = (w >> 9) & 63, (w & 511).double()
+    power = torch.tensor([2.0 ** (e - 31) for e in range(64)], dtype=torch.float64, device=w.device)
+    v = torch.where(exponent == 0, fraction * 2.0 ** -39, (1 + fraction / 512) * power[exponent])
+    v = torch.where(exponent == 63, torch.where(fraction == 0, math.inf, math.nan), v)
+    return torch.where(w >= 0x8000, -v, v)
+
+
+def within_kept(words, ref, slack, what=""):
+    tol = half_step(ref.abs() + slack, words.dtype) + slack
+    assert ((kept(words) - ref).abs() <= tol).all(), what
 
 
 def within(got, ref, slack, what=""):

@@ -66,8 +66,8 @@ def test_epilogue(cce, M, N, K, act, out, bias, residual):
         if act is None:
             assert kept is None
         else:
-            assert kept.dtype == dtype
-            L.within(kept, z, zs, "z")
+            assert kept.dtype == (torch.int16 if dtype == BF16 else dtype)
+            L.within_kept(kept, z, zs, "z")
             y2, none = cce.cce_linear_forward(x, w, b, r, act, out_dtype=out)
             assert none is None and torch.equal(y, y2)
 
@@ -112,8 +112,8 @@ def test_gated_forward(cce, M, N, K, act, dtype):
     ref, slack, (g, gs), (u, us) = L.gated(x, wg, wu, act)
     y, gate, up = cce.cce_gated_linear_forward(x, wg, wu, act, save=True)
     L.within(y, ref, slack, "y")
-    L.within(gate, g, gs, "gate")
-    L.within(up, u, us, "up")
+    L.within_kept(gate, g, gs, "gate")
+    L.within_kept(up, u, us, "up")
     assert torch.equal(y, cce.gated_linear(x, wg, wu, act))
 
 
@@ -139,6 +139,33 @@ def test_gated_backward(cce, M, N, K, act, dtype):
         one = cce.cce_gated_linear_backward(g, x, *ws, gate, up, act, **only)
         assert [t is not None for t in one] == [j == i for j in range(3)]
         L.within(one[i], (dx, dg, du)[i], (dxs, dgs, dus)[i], need)
+
+
+def test_kept_words(cce):
+    """Both passes through the 16 bits in which pre-activations are kept: rounding,
+    subnormals, the range's ends, infinities and NaN."""
+    exact = [0.0, 1.0, -1.5, 2.0 ** -30, 2.0 ** -39, -2.0 ** -39, 511 * 2.0 ** -39, 2.0 ** 31, 2.0 ** 31 * (2 - 2.0 ** -9)]
+    cases = {v: v for v in exact}
+    cases |= {1 + 2.0 ** -10 - 2.0 ** -14: 1.0, -1 - 2.0 ** -10 - 2.0 ** -14: -1 - 2.0 ** -9, 2.0 ** -41: 0.0,
+              3 * 2.0 ** -40: 2.0 ** -38, 2.0 ** 31 * (2 - 3 * 2.0 ** -11): 2.0 ** 31 * (2 - 2.0 ** -9), 2.0 ** 32: math.inf, -2.0 ** 40: -math.inf, math.inf: math.inf, -math.inf: -math.inf}
+    x = torch.ones(1, 1, device="cuda", dtype=BF16)
+    b = torch.tensor(list(cases) + [math.nan], device="cuda")  # z = 0 + bias, in fp32
+    w = torch.zeros(len(b), 1, device="cuda", dtype=BF16)
+    for rows in (1, 40):
+        _, z = cce.cce_linear_forward(x.expand(rows, 1), w, b, activation="relu", save=True)
+        want = torch.tensor(list(cases.values()), device="cuda", dtype=torch.float64)
+        for row in L.kept(z):
+            assert torch.equal(row[:-1], want) and row[-1].isnan()
+        small = torch.tensor([v if abs(v) < 2.0 ** 30 else 0.0 for v in cases], device="cuda")  # none at the range's end
+        _, zs = cce.cce_linear_forward(x.expand(rows, 1), w[:-1], small, activation="relu", save=True)
+        assert torch.equal(L.kept(zs), torch.where(small == 0, 0.0, want).expand(rows, -1))
+        # the gate's derivative and the product with it read them
+        one = torch.ones(rows, len(b), device="cuda", dtype=BF16)
+        fits = [i for i, v in enumerate(cases.values()) if v == torch.tensor(v).bfloat16().item() and abs(v) < 3e38]
+        dw = cce.cce_gated_linear_backward(one, x.expand(rows, 1), w, w, z, z, None)[2]
+        for i in fits:
+            assert dw[i, 0] == rows * torch.tensor(list(cases.values())[i]).bfloat16().item(), list(cases)[i]
+        assert dw[-1].isnan().all()
 
 
 def test_no_rows(cce):
@@ -311,7 +338,7 @@ def test_autograd_of_some_inputs(cce):
     w.requires_grad_()
     cce.gated_linear(x, w, w).sum().backward()  # one weight twice: both gradients add up
     _, gate, up = cce.cce_gated_linear_forward(x, w.detach(), w.detach(), save=True)
-    _, dg, du = cce.cce_gated_linear_backward(torch.ones_like(gate), x, w.detach(), w.detach(), gate, up)
+    _, dg, du = cce.cce_gated_linear_backward(torch.ones(6, 8, device="cuda").bfloat16(), x, w.detach(), w.detach(), gate, up)
     assert torch.equal(w.grad, dg + du)
     with pytest.raises(RuntimeError, match="not differentiable"):
         v = cce.linear(x.clone().requires_grad_(), w)
@@ -407,6 +434,8 @@ def test_refusals(cce):
         (lambda: cce.cce_linear_backward(y[:3], x, w), "grad_y"), (lambda: cce.cce_linear_backward(y.half(), x, w), "grad_y"),
         (lambda: cce.cce_linear_backward(y, x, w, None, "gelu"), "z"),
         (lambda: cce.cce_linear_backward(y, x, w, y.float(), "gelu"), "z must"),
+        (lambda: cce.cce_linear_backward(y.half(), x.half(), w.half(), y.short(), "gelu"), "z must"),
+        (lambda: cce.cce_gated_linear_backward(y, x, w, w, y.short(), y), "one type"),
         (lambda: cce.cce_linear_backward(y, x, w, y[:2], "gelu"), "z must"),
         (lambda: cce.cce_linear_backward(y, x, w, bias_dtype=torch.float64), "bias_dtype"),
         (lambda: cce.cce_gated_linear_backward(y, x, w, w, y[:2], y), "gate"),

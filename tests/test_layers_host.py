@@ -10,7 +10,7 @@ from torch.fx.experimental.proxy_tensor import make_fx
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 FAKE = 1 << 20  # an aligned non-null host integer: never dereferenced, checks fail first
-F32, F16, BF16 = 0, 1, 2
+F32, F16, BF16, KEPT = 0, 1, 2, 3
 NONE, RELU, GELU, GELU_TANH, SILU = range(5)
 
 
@@ -37,28 +37,28 @@ def test_declared_symbols(lib):
 
 def _linear(lib, **kw):
     a = dict(x=FAKE, xp=64, w=FAKE, wp=64, type=BF16, b=FAKE, bt=F32, r=FAKE, rp=100, act=GELU, M=32, N=100, K=64,
-             y=FAKE, yp=100, yt=BF16, z=FAKE, zp=100, ws=FAKE, wsb=1 << 40)
+             y=FAKE, yp=100, yt=BF16, z=FAKE, zp=100, zt=BF16, ws=FAKE, wsb=1 << 40)
     assert kw.keys() <= a.keys()
     return lib.cce_linear_forward(*(a | kw).values(), 0)
 
 
 def _linear_backward(lib, **kw):
-    a = dict(g=FAKE, gp=100, yt=BF16, x=FAKE, xp=64, w=FAKE, wp=64, type=BF16, z=FAKE, zp=100, act=GELU, M=32, N=100,
-             K=64, dx=FAKE, dw=FAKE, db=FAKE, bt=F32, ws=FAKE, wsb=1 << 40)
+    a = dict(g=FAKE, gp=100, yt=BF16, x=FAKE, xp=64, w=FAKE, wp=64, type=BF16, z=FAKE, zp=100, zt=KEPT, act=GELU, M=32,
+             N=100, K=64, dx=FAKE, dw=FAKE, db=FAKE, bt=F32, ws=FAKE, wsb=1 << 40)
     assert kw.keys() <= a.keys()
     return lib.cce_linear_backward(*(a | kw).values(), 0)
 
 
 def _gated(lib, **kw):
     a = dict(x=FAKE, xp=64, w=FAKE, wp=64, u=FAKE, up=64, type=BF16, act=SILU, M=32, N=100, K=64, y=FAKE, yp=100,
-             gate=FAKE, z=FAKE, zp=100, ws=FAKE, wsb=1 << 40)
+             gate=FAKE, z=FAKE, zp=100, zt=KEPT, ws=FAKE, wsb=1 << 40)
     assert kw.keys() <= a.keys()
     return lib.cce_gated_linear_forward(*(a | kw).values(), 0)
 
 
 def _gated_backward(lib, **kw):
     a = dict(g=FAKE, gp=100, x=FAKE, xp=64, w=FAKE, wp=64, u=FAKE, up=64, type=BF16, gate=FAKE, gatep=100, z=FAKE,
-             zp=100, act=SILU, M=32, N=100, K=64, dx=FAKE, dw=FAKE, du=FAKE, ws=FAKE, wsb=1 << 40)
+             zp=100, zt=BF16, act=SILU, M=32, N=100, K=64, dx=FAKE, dw=FAKE, du=FAKE, ws=FAKE, wsb=1 << 40)
     assert kw.keys() <= a.keys()
     return lib.cce_gated_linear_backward(*(a | kw).values(), 0)
 
@@ -67,6 +67,7 @@ CALLS = (_linear, _linear_backward, _gated, _gated_backward)
 
 
 @pytest.mark.parametrize("kw,status", [
+    (dict(zt=F16), 4), (dict(zt=F32), 4), (dict(type=F16, yt=F16, zt=KEPT), 4), (dict(zt=9), 4),
     (dict(x=0), 1), (dict(w=0), 1), (dict(type=F32), 4), (dict(type=7), 4), (dict(act=5), 4),
     (dict(act=-1), 4), (dict(M=-1), 2), (dict(N=0), 2), (dict(K=0), 2), (dict(M=1 << 31), 2), (dict(N=1 << 31), 2),
     (dict(M=(1 << 31) - 600, K=(1 << 31) - 600, xp=(1 << 31) - 8), 2), (dict(xp=56), 2), (dict(wp=56), 2),
@@ -74,7 +75,8 @@ CALLS = (_linear, _linear_backward, _gated, _gated_backward)
 ])
 def test_every_call_rejects_without_launch(lib, kw, status):
     for call in CALLS:
-        assert call(lib, **kw) == status, call
+        given = {k: v for k, v in kw.items() if k != "yt" or call in (_linear, _linear_backward)}
+        assert call(lib, **given) == status, call
 
 
 @pytest.mark.parametrize("kw,status", [(dict(ws=FAKE + 16), 3), (dict(wsb=8), 5), (dict(ws=0), 1)])
