@@ -39,7 +39,7 @@ __device__ __forceinline__ float gelu_tanh_gate(float z) {
 // The normal distribution function by the rational approximation 7.1.26 of Abramowitz and Stegun's Handbook of
 // Mathematical Functions: erfc(x) = t (a1 + t (a2 + ...)) e^(-x^2), t = 1 / (1 + p x), x >= 0, within 1.5e-7; here
 // x = |z| / sqrt(2), and Phi(z) is half of it below 0 and one less that above.  CUDA's erfcf takes twice the
-// instructions: with it 65,536 x 2,048 x 8,192 took 2,171 us and not 1,374.
+// instructions.
 __device__ __forceinline__ float gelu_gate(float z) {
   const float m = fabsf(z);
   const float t = reciprocal_fast(fmaf(0.3275911f * 0.70710678f, m, 1.0f));

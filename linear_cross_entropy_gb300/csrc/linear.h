@@ -109,6 +109,8 @@ struct LinFew {
   int I, J, K;
   LinEpilogue e;
 };
+// Beyond, a token more costs the GEMM nothing, and here a fourth tile of eight rows reads x again: 4,096 x 4,096 takes 9.8 us
+// for 32 rows here, 10.4 for 33 there; 17 rows 8.3 here and 11.1 there.
 constexpr int LIN_FEW_ROWS = 32;
 cudaError_t launch_linear_few(const LinFew& a, bool gated, bool bf16, cudaStream_t s);
 

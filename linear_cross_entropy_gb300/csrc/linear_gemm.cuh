@@ -18,19 +18,24 @@
 //
 // Roles (384 threads): lane 0 of warp 0 loads A, that of warp 10 B (TMA; a pair's stages
 // are 128 deep in K, a single CTA's 64, as many as fit in 192 KiB; one thread for both
-// needed 560 of a stage's 950 cycles: TIME_TWO), warp 1 lane 0 issues tcgen05.mma into
-// one of two TMEM accumulators, warps 2 to 9 are the epilogue (warp w reads TMEM
-// lanes 32 (w % 4) to + 31, and every second 32 columns), and warp
-// 11 adds up the parts of a bias's gradient where there are some.  CTA pairs share an MMA of
-// M = 256: each CTA holds 128 rows of A and half of B's columns.
+// needed 560 of a stage's 950 cycles: 16,384 x 2,048 x 4,096 took 161 us and not 155),
+// warp 1 lane 0 issues tcgen05.mma into one of two TMEM accumulators, warps 2 to 9
+// are the epilogue (warp w reads TMEM lanes 32 (w % 4) to + 31, and every second 32
+// columns), and warp 11 adds up the parts of a bias's gradient where there are some.
+// CTA pairs share an MMA of M = 256: each CTA holds 128 rows of A and half of B's
+// columns.
 //
 // The epilogue reads the accumulator in the layout of matrix fragments, so that 16-bit
 // results pass through shared memory by transposing matrix stores and leave in vectors of
-// 16 bytes: with a store of 2 bytes a thread and value a tile of 128 x 256 took 3.7 us
-// beside the MMAs, TIME_EPI so.  Results whose rows are off 16 bytes and fp32 ones are
-// stored directly, 8 values of a row together.
+// 16 bytes: with a store of 2 bytes a thread and value a tile of 128 x 256 took 3.7 us,
+// longer than its MMAs where K is short, and 8,192 x 896 x 4,864 49 us and not 44.
+// Results whose rows are off 16 bytes and fp32 ones are stored directly, 8 values of a
+// row together.
 //
-// Bound by the tensor cores for many rows, and by reading the weights for few.
+// Bound by the tensor cores for many rows: 65,536 x 2,048 x 8,192 with bias and gelu
+// 1.39 ms (1.58 PFLOP/s), 8,192 x 9,216 x 2,304 193 us (1.80), 16,384 x 2,048 x 4,096
+// 153 us (1.80); where K is short by the epilogue, 8,192 x 896 x 4,864 44 us (1.63).  A
+// launch costs some 6 us beside its products: 128 x 896 x 896 takes 7 us with any tile.
 #pragma once
 
 #include "gemm_args.h"
