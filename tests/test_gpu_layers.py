@@ -168,6 +168,43 @@ def test_kept_words(cce):
         assert dw[-1].isnan().all()
 
 
+@pytest.mark.parametrize("M,N,K", [(5, 17, 33), (40, 256, 4096), (64, 1000, 896), (129, 257, 65), (300, 640, 200)])
+def test_backward_of_kept_words(cce, M, N, K):
+    """What a bf16 forward keeps, whole rows on 16 bytes or not and from partial sums, through the backward; columns of
+    a wider matrix give the same."""
+    gen, x, ws = inputs(M, N, K, BF16, 12, weights=2)
+    g = randn(gen, M, N, scale=M ** -0.5, dtype=BF16)
+
+    def apart(words):
+        wide = torch.full((M, N + 3), 0x7FFF, dtype=torch.int16, device="cuda")
+        wide[:, :N] = words
+        return wide[:, :N]
+
+    _, kept = cce.cce_linear_forward(x, ws[0], activation="gelu", save=True)
+    _, _, z, zs = L.linear(x, ws[0], act="gelu")
+    L.within_kept(kept, z, zs, "z")
+    dz, slack = L.grad_out(g, L.kept(kept), "gelu")
+    (dx, dxs), [(dw, dws)] = L.backward_products([dz], [slack], x, ws[:1], BF16)
+    got = cce.cce_linear_backward(g, x, ws[0], kept, "gelu")
+    L.within(got[0], dx, dxs, "dx")
+    L.within(got[1], dw, dws, "dw")
+    for a, b in zip(got, cce.cce_linear_backward(g, x, ws[0], apart(kept), "gelu")):
+        L.within(b, a.double(), 0 * a.double(), "strided")
+
+    _, gate, up = cce.cce_gated_linear_forward(x, *ws, "silu", save=True)
+    zg, zu = L.kept(gate), L.kept(up)
+    d0, s0 = L.grad_out(g.double() * zu, zg, "silu")
+    d1 = g.double() * L.act64("silu", zg)
+    s0 = s0 + d0.abs() * 2.0 ** -23
+    s1 = g.double().abs() * L.FUNC * zg.abs() + d1.abs() * 2.0 ** -23
+    (dx, dxs), dws = L.backward_products([d0, d1], [s0, s1], x, ws, BF16)
+    got = cce.cce_gated_linear_backward(g, x, *ws, gate, up, "silu")
+    for t, (ref, slack) in zip(got, [(dx, dxs)] + dws):
+        L.within(t, ref, slack)
+    for a, b in zip(got, cce.cce_gated_linear_backward(g, x, *ws, apart(gate), apart(up), "silu")):
+        L.within(b, a.double(), 0 * a.double(), "strided")
+
+
 def test_no_rows(cce):
     w, w2 = (torch.randn(24, 16, device="cuda", dtype=BF16) for _ in range(2))
     x = torch.empty(3, 0, 16, device="cuda", dtype=BF16, requires_grad=True)
