@@ -40,30 +40,43 @@ def adamw_scales(numel) -> int:
     return -(-numel // BLOCK)
 
 
+def _tensor_or_none(value):
+    """A device tensor in place of a number."""
+    return value if type(value) not in (int, float) and isinstance(value, torch.Tensor) else None
+
+
 def _step(params, grads, states, bits, step, lr, betas, eps, weight_decay, masters, grad_norm, max_norm, seed, stream):
-    params, grads, states = list(params), list(grads), [list(s) for s in states]
-    masters = [None] * len(params) if masters is None else list(masters)
-    for name, given in [("grads", grads), ("masters", masters)] + [("states", s) for s in states if bits or s]:
-        if len(given) != len(params):
-            raise ValueError(f"{name} must have one tensor for each of the {len(params)} params, got {len(given)}")
-    decay = [float(weight_decay)] if isinstance(weight_decay, (int, float)) else [float(d) for d in weight_decay]
-    if not isinstance(weight_decay, (int, float)) and len(decay) != len(params):
-        raise ValueError(f"weight_decay must be a number or one for each of the {len(params)} params, got {len(decay)}")
+    params = list(params)
+    n = len(params)
+    args = [params]
+    names = ("grads", "masters", "states", "states", "states", "states")
+    for name, given in zip(names, (grads, (None,) * n if masters is None else masters, *states)):
+        given = list(given)
+        if len(given) != n:
+            raise ValueError(f"{name} must have one tensor for each of the {n} params, got {len(given)}")
+        args.append(given)
+    if type(weight_decay) is float or isinstance(weight_decay, (int, float)):
+        decay = [float(weight_decay)]
+    else:
+        decay = [float(d) for d in weight_decay]
+        if len(decay) != n:
+            raise ValueError(f"weight_decay must be a number or one for each of the {n} params, got {len(decay)}")
     if (grad_norm is None) != (max_norm is None):
         raise ValueError("grad_norm and max_norm come together")
-    if max_norm is not None and not float(max_norm) >= 0.0:
+    max_norm = 0.0 if max_norm is None else float(max_norm)
+    if not max_norm >= 0.0:
         raise ValueError(f"max_norm must be at least 0, got {max_norm}")
-    at = step if isinstance(step, torch.Tensor) else None
-    lr_at = lr if isinstance(lr, torch.Tensor) else None
-    if at is None and int(step) < 1:
+    at, lr_at = _tensor_or_none(step), _tensor_or_none(lr)
+    step = 1 if at is not None else int(step)
+    if step < 1:
         raise ValueError(f"step must be at least 1, got {step}")
     if not params:
         return
+    if bits == 32:
+        args += [], []
     beta1, beta2 = betas
-    states += [[]] * (4 - len(states))
-    args = (params, grads, masters, *states, bits, 1 if at is not None else int(step), at,
-            0.0 if lr_at is not None else float(lr), lr_at, float(beta1), float(beta2), float(eps), decay, grad_norm,
-            0.0 if max_norm is None else float(max_norm), CLIP_EPS, int(seed) & 0xFFFFFFFF)
+    args += (bits, step, at, 0.0 if lr_at is not None else float(lr), lr_at, float(beta1), float(beta2), float(eps), decay,
+             grad_norm, max_norm, CLIP_EPS, int(seed) & 0xFFFFFFFF)
     if stream is None:
         _native.adamw_step(*args)
     else:
