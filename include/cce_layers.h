@@ -59,16 +59,17 @@ int cce_layers_abi_version(void);
  *
  *   x         [M, K] of `type`     weight    [N, K] of `type`
  *   bias      [N] of bias_type, any of the three types; NULL: 0
- *   residual  [M, N] of y_type; NULL: 0
+ *   residual  [M, N] of y_type, rows as of cce_ops.h ("Rows"); NULL: 0
  *   y         [M, N] of y_type: `type` or CCE_F32
  *   z         [M, N] of z_type, for the backward pass; NULL: not written.  z_type is
  *             `type`, or CCE_KEPT16 with CCE_BF16
  * Everything behind the product is fp32, with one rounding to y and one to z.
  */
 cce_status cce_linear_forward(const void* x, int64_t x_pitch, const void* weight, int64_t w_pitch, int type,
-                              const void* bias, int bias_type, const void* residual, int64_t res_pitch, int act,
-                              int64_t M, int64_t N, int64_t K, void* y, int64_t y_pitch, int y_type, void* z,
-                              int64_t z_pitch, int z_type, void* workspace, size_t ws_bytes, void* stream);
+                              const void* bias, int bias_type, const void* residual, int64_t r_inner, int64_t r_row_stride,
+                              int64_t r_outer_stride, int act, int64_t M, int64_t N, int64_t K, void* y,
+                              int64_t y_pitch, int y_type, void* z, int64_t z_pitch, int z_type, void* workspace,
+                              size_t ws_bytes, void* stream);
 
 /* Bytes of workspace (0 for invalid sizes; 16 where none is needed).  Pure host arithmetic; needs no GPU. */
 size_t cce_linear_forward_workspace_bytes(int64_t M, int64_t N, int64_t K);

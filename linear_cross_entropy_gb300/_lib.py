@@ -190,7 +190,7 @@ def load() -> ctypes.CDLL:
     lib.cce_layers_abi_version.argtypes = []
     lib.cce_layers_abi_version.restype = ci
     mat = [vp, i64]  # pointer, pitch
-    lib.cce_linear_forward.argtypes = (mat + mat + [ci, vp, ci] + mat + [ci, i64, i64, i64] + mat + [ci] + mat
+    lib.cce_linear_forward.argtypes = (mat + mat + [ci, vp, ci, vp, i64, i64, i64] + [ci, i64, i64, i64] + mat + [ci] + mat
                                        + [ci, vp, sz, vp])
     lib.cce_linear_backward.argtypes = (mat + [ci] + mat + mat + [ci] + mat + [ci, ci, i64, i64, i64, vp, vp, vp, ci, vp,
                                                                                sz, vp])

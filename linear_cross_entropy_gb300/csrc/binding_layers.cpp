@@ -60,6 +60,13 @@ class Matrices {
   std::vector<Tensor> kept_;
 };
 
+// Rows that a kernel reads where they are, in runs at one pitch.
+Rows read_rows(const Tensor& given) {
+  Rows r = rows_of(given);
+  if (r.row >= int64_t(1) << 30 || r.outer >= int64_t(1) << 45) r = rows_of(given.contiguous());
+  return r;
+}
+
 struct Sizes {
   int64_t M, N, K;
   int type;
@@ -147,8 +154,9 @@ std::tuple<Tensor, Tensor> linear_forward(const Tensor& x, const Tensor& weight,
   const size_t need = cce_linear_forward_workspace_bytes(s.M, s.N, s.K);
   const Tensor ws = workspace(need, x);
   Matrices m;
-  const Pitched xp = m.operand(x), wp = m.operand(weight), rp = m.matrix(residual);
+  const Pitched xp = m.operand(x), wp = m.operand(weight);
   m.copy(x);
+  const Rows r = residual.defined() ? read_rows(residual) : Rows{};
   const Tensor b = plain(bias);
   const auto shape = result_shape(x, s.N);
   Tensor y = at::empty(shape, x.options().dtype(y_type).requires_grad(false));
@@ -156,8 +164,8 @@ std::tuple<Tensor, Tensor> linear_forward(const Tensor& x, const Tensor& weight,
   Tensor z = save && act != CCE_ACT_NONE ? at::empty(shape, kept) : Tensor();
   note_device(x);
   check_status(cce_linear_forward(pointer(xp.t), xp.pitch, pointer(wp.t), wp.pitch, s.type, pointer(b),
-                                  b.defined() ? type_code(b.scalar_type()) : s.type, pointer(rp.t), rp.pitch, act, s.M,
-                                  s.N, s.K, pointer(y), s.N, type_code(y_type), pointer(z), s.N,
+                                  b.defined() ? type_code(b.scalar_type()) : s.type, pointer(r.t), r.inner, r.row, r.outer, act,
+                                  s.M, s.N, s.K, pointer(y), s.N, type_code(y_type), pointer(z), s.N,
                                   z.defined() ? kept_code(z, x, "z") : s.type, pointer(ws), need,
                                   stream_of(x)),
                "cce_linear_forward", ARGS);

@@ -327,6 +327,13 @@ cce_status check_matrix(const Matrix& m, bool optional = false) {
   if (m.pitch < m.cols || m.pitch >= (int64_t(1) << 30)) return CCE_ERR_SHAPE;
   return multiple(m.p, type_bytes(m.type)) ? CCE_OK : CCE_ERR_ALIGN;
 }
+// Rows that are only read, in runs (include/cce_ops.h, "Rows").
+cce_status check_rows(const Matrix& m, int64_t inner, int64_t outer_stride) {
+  if (!m.p) return CCE_OK;
+  if (inner < 1 || m.pitch < 0 || m.pitch >= (int64_t(1) << 30) || outer_stride < 0 || outer_stride >= MATRIX)
+    return CCE_ERR_SHAPE;
+  return multiple(m.p, type_bytes(m.type)) ? CCE_OK : CCE_ERR_ALIGN;
+}
 cce_status check_workspace(const void* ws, size_t have, size_t need) {
   if (need <= NO_WORKSPACE) return CCE_OK;
   if (!ws) return CCE_ERR_NULL;
@@ -467,9 +474,10 @@ size_t cce_gated_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K
 }
 
 cce_status cce_linear_forward(const void* x, int64_t x_pitch, const void* weight, int64_t w_pitch, int type,
-                              const void* bias, int bias_type, const void* residual, int64_t res_pitch, int act,
-                              int64_t M, int64_t N, int64_t K, void* y, int64_t y_pitch, int y_type, void* z,
-                              int64_t z_pitch, int z_type, void* workspace, size_t ws_bytes, void* stream) {
+                              const void* bias, int bias_type, const void* residual, int64_t r_inner, int64_t r_row_stride,
+                              int64_t r_outer_stride, int act, int64_t M, int64_t N, int64_t K, void* y,
+                              int64_t y_pitch, int y_type, void* z, int64_t z_pitch, int z_type, void* workspace,
+                              size_t ws_bytes, void* stream) {
   if (!operand_type(type) || !type_ok(bias_type) || (y_type != type && y_type != CCE_F32) || !act_ok(act) ||
       !kept_type(z_type, type))
     return CCE_ERR_ARG;
@@ -477,11 +485,14 @@ cce_status cce_linear_forward(const void* x, int64_t x_pitch, const void* weight
   const Matrix xm{x, x_pitch, type, M, K}, wm{weight, w_pitch, type, N, K};
   const cce_status st =
       first_of(check_operand(xm), check_operand(wm), check_matrix({bias, N, bias_type, 1, N}, true),
-               check_matrix({residual, res_pitch, y_type, M, N}, true), check_matrix({y, y_pitch, y_type, M, N}),
+               check_rows({residual, r_row_stride, y_type, M, N}, r_inner, r_outer_stride),
+               check_matrix({y, y_pitch, y_type, M, N}),
                check_matrix({z, z_pitch, type, M, N}, true),
                check_workspace(workspace, ws_bytes, forward_bytes(M, N, K, false)));
   if (st != CCE_OK) return st;
-  const LinEpilogue e{y, y_pitch, bias, residual, res_pitch, {z, nullptr}, z_pitch, y_type, bias_type, act, z_type};
+  const bool runs = residual && r_inner < M;
+  const LinEpilogue e{y, y_pitch, bias, residual, r_row_stride, runs ? r_outer_stride : 0, runs ? static_cast<int>(r_inner) : 0,
+                      {z, nullptr}, z_pitch, y_type, bias_type, act, z_type};
   return forward(xm, &wm, false, M, N, K, e, workspace, static_cast<cudaStream_t>(stream));
 }
 
@@ -499,7 +510,7 @@ cce_status cce_gated_linear_forward(const void* x, int64_t x_pitch, const void* 
                                  check_matrix({up, z_pitch, type, M, N}, true),
                                  check_workspace(workspace, ws_bytes, forward_bytes(M, N, K, true)));
   if (st != CCE_OK) return st;
-  const LinEpilogue e{y, y_pitch, nullptr, nullptr, 0, {gate, up}, z_pitch, type, type, act, z_type};
+  const LinEpilogue e{y, y_pitch, nullptr, nullptr, 0, 0, 0, {gate, up}, z_pitch, type, type, act, z_type};
   return forward(xm, wm, true, M, N, K, e, workspace, static_cast<cudaStream_t>(stream));
 }
 

@@ -20,7 +20,8 @@ struct LinEpilogue {
   int64_t y_pitch;
   const void* bias;  // [I], may be null
   const void* res;   // of y's type, may be null
-  int64_t res_pitch;
+  int64_t res_pitch, res_outer;
+  int res_inner;  // rows of res at the pitch, such runs res_outer apart; 0: all of them are
   void* z[2];  // pre-activations, may be null
   int64_t z_pitch;
   int y_type, bias_type, act, z_type;  // z_type: the operands', or CCE_KEPT16

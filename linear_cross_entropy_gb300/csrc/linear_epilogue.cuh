@@ -72,6 +72,13 @@ __device__ __forceinline__ void put_kept(void* base, int64_t at, const float (&f
   v.store(static_cast<__nv_bfloat16*>(base) + at);
 }
 
+// Where row j of the residual starts.
+__device__ __forceinline__ int64_t res_row(const LinEpilogue& e, int64_t j) {
+  if (e.res_inner == 0) return j * e.res_pitch;
+  const uint32_t n = static_cast<uint32_t>(j), run = n / static_cast<uint32_t>(e.res_inner);
+  return run * e.res_outer + (n - run * static_cast<uint32_t>(e.res_inner)) * e.res_pitch;
+}
+
 // VEC neighbouring values i, ... of row j, all inside of the matrices, which VEC values of each start on their size.  z0:
 // the product with x (gated: the gate's), z1: gated: the up projection's.  T: the operands' type.
 template <typename T, bool GATED, int VEC>
@@ -100,7 +107,7 @@ __device__ __forceinline__ void finish_row(const LinEpilogue& e, int64_t j, int6
     for (int u = 0; u < VEC; ++u) z0[u] *= z1[u];
   } else if (e.res) {
     float r[VEC];
-    load_param<VEC>(e.res, y32 ? CCE_F32 : ElemType<T>::id, j * e.res_pitch + i, r);
+    load_param<VEC>(e.res, y32 ? CCE_F32 : ElemType<T>::id, res_row(e, j) + i, r);
 #pragma unroll
     for (int u = 0; u < VEC; ++u) z0[u] += r[u];
   }

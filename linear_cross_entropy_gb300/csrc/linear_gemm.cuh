@@ -408,17 +408,28 @@ struct Fragment {
 struct Residuals {
   uint32_t raw[32];
 
+  // p: the thread's first place in a row; j: its first row.
   template <typename T>
-  __device__ __forceinline__ void load(const T* p, int64_t pitch, int n, int rows) {
+  __device__ __forceinline__ void load(const T* p, const LinEpilogue& e, int64_t j, int n, int rows) {
+    if (e.res_inner == 0) {
+      const int64_t pitch = e.res_pitch;
+      p += j * pitch;
+      load_rows(n, rows, [&](int x) { return p + x * pitch; });
+    } else {
+      load_rows(n, rows, [&](int x) { return p + res_row(e, j + x); });
+    }
+  }
+  template <typename Row>
+  __device__ __forceinline__ void load_rows(int n, int rows, Row row_of) {
     const int c0 = 2 * static_cast<int>(lane_id() & 3u), r0 = static_cast<int>(lane_id() >> 2);
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const T* row = p + (8 * b + c) * pitch;
+        const auto row = row_of(8 * b + c);
 #pragma unroll
         for (int m = 0; m < 4; ++m)
-          raw[8 * b + 2 * m + c] = 8 * b + c0 + c < n && r0 + 8 * m < rows ? row[8 * m] : T(0);
+          raw[8 * b + 2 * m + c] = 8 * b + c0 + c < n && r0 + 8 * m < rows ? row[8 * m] : 0;
       }
     }
   }
@@ -547,9 +558,9 @@ __device__ __forceinline__ void finish_any(const Shared& s, const Share& w, cons
     Residuals res;
     if (has_res) {
       if (y32) {
-        res.load(static_cast<const uint32_t*>(e.res) + (tj + jc) * e.res_pitch + ti, e.res_pitch, n, w.rows);
+        res.load(static_cast<const uint32_t*>(e.res) + ti, e, tj + jc, n, w.rows);
       } else {
-        res.load(static_cast<const uint16_t*>(e.res) + (tj + jc) * e.res_pitch + ti, e.res_pitch, n, w.rows);
+        res.load(static_cast<const uint16_t*>(e.res) + ti, e, tj + jc, n, w.rows);
       }
     }
     chunk.wait();

@@ -233,7 +233,7 @@ cudaError_t launch_join(const LinProblem& p, int sms, cudaStream_t s) {
   const LinEpilogue& e = p.e;
   const auto fits = [](const void* m, int64_t pitch, int64_t bytes) { return !m || (pitch % 4 == 0 && multiple(m, 4 * bytes)); };
   const int64_t y_bytes = e.y_type == CCE_F32 ? 4 : 2;
-  const bool wide = p.I % 4 == 0 && fits(e.y, e.y_pitch, y_bytes) && fits(e.res, e.res_pitch, y_bytes) &&
+  const bool wide = p.I % 4 == 0 && fits(e.y, e.y_pitch, y_bytes) && fits(e.res, e.res_pitch | e.res_outer, y_bytes) &&
                     fits(e.z[0], e.z_pitch, 2) && fits(e.z[1], e.z_pitch, 2) &&
                     fits(e.bias, 0, e.bias_type == CCE_F32 ? 4 : 2);
   const int cols = JOIN_COLS * (wide ? 4 : 1), rows = THREADS / JOIN_COLS;

@@ -267,6 +267,22 @@ def test_strided_fp32_matrices(cce, cols):
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("M,N,K", [(3, 40, 64), (50, 1001, 72), (20, 256, 4096), (50, 264, 200)])
+@pytest.mark.parametrize("out", [None, F32])
+def test_residual_in_runs(cce, M, N, K, out):
+    """Residuals of every second sequence's rows, of sequences without their last token, and of one row for all, for few
+    rows, many and joined partial sums."""
+    gen, x, (w,) = inputs(4 * M, N, K, BF16, 14)
+    x = x.view(4, M, K)
+    big = randn(gen, 8, M + 1, N + 3, dtype=out or BF16)
+    for r in (big[::2, :M, :N], big[:4, 1:, 3:], big[::2, ::2, :N][:, :1].expand(4, M, N), big[0, 0, :N].expand(4, M, N),
+              big[:4, 0, :N].unsqueeze(1).expand(4, M, N)):
+        ref, slack, _, _ = L.linear(x.reshape(-1, K), w, None, r.reshape(-1, N), "silu")
+        y = cce.linear(x, w, residual=r, activation="silu", out_dtype=out)
+        L.within(y.view(-1, N), ref, slack)
+        assert torch.equal(y, cce.linear(x, w, residual=r.contiguous(), activation="silu", out_dtype=out))
+
+
 def test_what_lies_between_rows_is_not_read(cce):
     """NaN beside the views, in the columns that complete a vector and in the rows behind."""
     for M, N, K in [(3, 20, 20), (40, 50, 36), (300, 130, 100)]:

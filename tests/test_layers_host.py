@@ -36,8 +36,8 @@ def test_declared_symbols(lib):
 
 
 def _linear(lib, **kw):
-    a = dict(x=FAKE, xp=64, w=FAKE, wp=64, type=BF16, b=FAKE, bt=F32, r=FAKE, rp=100, act=GELU, M=32, N=100, K=64,
-             y=FAKE, yp=100, yt=BF16, z=FAKE, zp=100, zt=BF16, ws=FAKE, wsb=1 << 40)
+    a = dict(x=FAKE, xp=64, w=FAKE, wp=64, type=BF16, b=FAKE, bt=F32, r=FAKE, ri=32, rp=100, ro=0, act=GELU, M=32, N=100,
+             K=64, y=FAKE, yp=100, yt=BF16, z=FAKE, zp=100, zt=BF16, ws=FAKE, wsb=1 << 40)
     assert kw.keys() <= a.keys()
     return lib.cce_linear_forward(*(a | kw).values(), 0)
 
@@ -90,7 +90,8 @@ def test_workspaces_are_checked_where_one_is_needed(lib, kw, status):
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(bt=3), 4), (dict(yt=F16), 4), (dict(yt=5), 4), (dict(y=0), 1), (dict(rp=99), 2), (dict(yp=99), 2),
+    (dict(bt=3), 4), (dict(yt=F16), 4), (dict(yt=5), 4), (dict(y=0), 1), (dict(rp=-1), 2), (dict(ri=0), 2), (dict(ro=-1), 2),
+    (dict(ro=1 << 45), 2), (dict(yp=99), 2),
     (dict(rp=1 << 30), 2), (dict(yp=1 << 30), 2), (dict(zp=99), 2), (dict(b=FAKE + 2), 3), (dict(r=FAKE + 1), 3), (dict(y=FAKE + 1), 3), (dict(z=FAKE + 1), 3),
     (dict(yt=F32, y=FAKE + 2), 3), (dict(yt=F32, r=FAKE + 2), 3),
 ])
