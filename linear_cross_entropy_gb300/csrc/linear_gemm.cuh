@@ -19,7 +19,9 @@
 // Roles (384 threads): lane 0 of warp 0 loads A, that of warp 10 B (TMA; a pair's stages
 // are 128 deep in K, a single CTA's 64, as many as fit in 192 KiB; one thread for both
 // needed 560 of a stage's 950 cycles: 16,384 x 2,048 x 4,096 took 161 us and not 155),
-// warp 1 lane 0 issues tcgen05.mma into one of two TMEM accumulators, warps 2 to 9
+// warp 1 issues tcgen05.mma into one of two TMEM accumulators (the whole warp runs the
+// loop, one elected lane the instruction: its operands stay uniform, and a stage of a narrow
+// tile takes 760 cycles; on a path of one lane it took 950), warps 2 to 9
 // are the epilogue (warp w reads TMEM lanes 32 (w % 4) to + 31, and every second 32
 // columns), and warp 11 adds up the parts of a bias's gradient where there are some.
 // CTA pairs share an MMA of M = 256: each CTA holds 128 rows of A and half of B's
@@ -35,7 +37,8 @@
 // Bound by the tensor cores for many rows: 65,536 x 2,048 x 8,192 with bias and gelu
 // 1.39 ms (1.58 PFLOP/s), 8,192 x 9,216 x 2,304 193 us (1.80), 16,384 x 2,048 x 4,096
 // 153 us (1.80); where K is short by the epilogue, 8,192 x 896 x 4,864 44 us (1.63).  A
-// launch costs some 6 us beside its products: 128 x 896 x 896 takes 7 us with any tile.
+// launch costs some 5 us beside its products: 128 x 896 x 896 takes 5.8 us.  Narrow tiles
+// are bound by the MMAs' reading 128 rows of A from shared memory.
 #pragma once
 
 #include "gemm_args.h"
@@ -115,6 +118,12 @@ __device__ __forceinline__ Tile tile_of(const LinArgs& a, int item) {
   return t;
 }
 
+// The fields' lines of the constant cache, and a tile's numbers: they have to be there behind this.
+__device__ __forceinline__ void touch(const LinProblem& p, const Tile& t) {
+  asm volatile("" ::"r"(t.it), "r"(t.jt), "r"(t.kb), "r"(t.kb_end), "r"(p.I), "r"(p.klen[0]), "r"(p.jt), "r"(p.wide),
+               "l"(p.e.y), "l"(p.e.res), "r"(p.e.act));
+}
+
 // A box to `to`, whose bytes are counted on the stage's barrier (of a pair: the even CTA's).
 template <bool PAIR>
 struct Loader {
@@ -172,7 +181,7 @@ struct Loader {
 
 // The loads of A, whose thread announces the bytes of both, or of B.
 template <bool PAIR, bool GATED, bool A>
-__device__ __forceinline__ void load_loop(const LinArgs& a, const Shared& s) {
+__device__ __forceinline__ void load_loop(const LinArgs& a, const Shared& s, const Tile& first) {
   constexpr int BK = lin_bk(PAIR), A_BYTES = LIN_BI * BK * 2;
   volatile int* abort_flag = s.abort_flag;
   const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
@@ -184,7 +193,7 @@ __device__ __forceinline__ void load_loop(const LinArgs& a, const Shared& s) {
   uint32_t phase = 0;
   uint32_t issued = 0, issued_par = 0;  // per stage: ever issued, parity of its last phase
   bool ok = true;
-  Tile next = tile_of(a, unit);
+  Tile next = first;
   for (int item = unit; ok && item < a.items; item += units) {
     const Tile t = next;
     const LinProblem& p = *t.p;
@@ -221,7 +230,17 @@ __device__ __forceinline__ void load_loop(const LinArgs& a, const Shared& s) {
       if (kb == t.kb && item + units < a.items) next = tile_of(a, item + units);
     }
   }
-  if (!*abort_flag) return;
+  if (ok && !*abort_flag) {
+    // a pair's stages are handed back by the even CTA's MMAs: this CTA stays until all of them have been
+    for (int i = 0; A && PAIR && i < stages; ++i) {
+      if (!wait_bounded_long(&s.empty[stage], phase ^ 1u, abort_flag, a.error)) break;
+      if (++stage == stages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    return;
+  }
   if (PAIR && rank != 0) {
     // this CTA's copies complete on the other's barriers: 10 ms for those in flight
     const uint64_t t0 = globaltimer();
@@ -238,7 +257,7 @@ __device__ __forceinline__ void load_loop(const LinArgs& a, const Shared& s) {
 }
 
 template <bool PAIR>
-__device__ __forceinline__ void mma_loop(const LinArgs& a, const Shared& s, uint32_t tmem) {
+__device__ __forceinline__ void mma_loop(const LinArgs& a, const Shared& s, uint32_t tmem, const Tile& first) {
   if (PAIR && cluster_ctarank() != 0) return;  // the even CTA issues for both
   constexpr int BK = lin_bk(PAIR), A_BYTES = LIN_BI * BK * 2;
   volatile int* abort_flag = s.abort_flag;
@@ -248,8 +267,9 @@ __device__ __forceinline__ void mma_loop(const LinArgs& a, const Shared& s, uint
   int stage = 0, acc = 0;
   uint32_t phase = 0, acc_phase = 0;
   bool any = false, ok = true;
+  const uint32_t lead = elect_lane();
   // (the divisions for the next tile are made while this one's MMAs run: some 700 cycles between two tiles otherwise)
-  Tile next = tile_of(a, unit);
+  Tile next = first;
   for (int item = unit; ok && item < a.items; item += units) {
     const Tile t = next;
     const LinProblem& p = *t.p;
@@ -263,12 +283,15 @@ __device__ __forceinline__ void mma_loop(const LinArgs& a, const Shared& s, uint
     const uint32_t a_step = (a_mn ? 2048u : 32u) >> 4, b_step = (b_mn ? 2048u : 32u) >> 4;
     const uint32_t a_next = (a_mn ? 8192u : 2u * GROUP) >> 4;
     const uint32_t b_next = (b_mn ? 8192u : (PAIR ? p.jt / 2 : p.jt) * 128u) >> 4;
-    if (!wait_bounded_long(&s.acc_empty[acc], acc_phase ^ 1u, abort_flag, a.error)) break;
+    if (!__all_sync(0xffffffffu, wait_bounded_long(&s.acc_empty[acc], acc_phase ^ 1u, abort_flag, a.error))) {
+      ok = false;
+      break;
+    }
     tc_fence_after();
     const uint32_t d = tmem + static_cast<uint32_t>(acc * ACC_COLS);
     uint32_t accumulate = 0;
     for (int kb = t.kb; kb < t.kb_end; ++kb) {
-      if (!wait_bounded_long(&s.full[stage], phase, abort_flag, a.error)) {
+      if (!__all_sync(0xffffffffu, wait_bounded_long(&s.full[stage], phase, abort_flag, a.error))) {
         ok = false;
         break;
       }
@@ -280,9 +303,9 @@ __device__ __forceinline__ void mma_loop(const LinArgs& a, const Shared& s, uint
       const auto mma = [&](int k) {
         const uint64_t ad = a_desc + (k >> 2) * a_next + (k & 3) * a_step, bd = b_desc + (k >> 2) * b_next + (k & 3) * b_step;
         if constexpr (PAIR) {
-          mma_bf16_pair(d, ad, bd, idesc, accumulate | (k > 0));
+          mma_bf16_pair_by(lead, d, ad, bd, idesc, accumulate | (k > 0));
         } else {
-          mma_bf16(d, ad, bd, idesc, accumulate | (k > 0));
+          mma_bf16_by(lead, d, ad, bd, idesc, accumulate | (k > 0));
         }
       };
       if (left >= BK) {
@@ -293,11 +316,14 @@ __device__ __forceinline__ void mma_loop(const LinArgs& a, const Shared& s, uint
       }
       accumulate = 1;
       any = true;
-      if constexpr (PAIR) {
-        mma_commit_pair_both(&s.empty[stage]);
-      } else {
-        mma_commit(&s.empty[stage]);
+      if (lead) {
+        if constexpr (PAIR) {
+          mma_commit_pair_both(&s.empty[stage]);
+        } else {
+          mma_commit(&s.empty[stage]);
+        }
       }
+      __syncwarp();
       if (++stage == stages) {
         stage = 0;
         phase ^= 1u;
@@ -305,15 +331,24 @@ __device__ __forceinline__ void mma_loop(const LinArgs& a, const Shared& s, uint
       if (kb == t.kb && item + units < a.items) next = tile_of(a, item + units);
     }
     if (!ok) break;
-    if constexpr (PAIR) {
-      mma_commit_pair_both(&s.acc_full[acc]);
-    } else {
-      mma_commit(&s.acc_full[acc]);
+    if (lead) {
+      if constexpr (PAIR) {
+        mma_commit_pair_both(&s.acc_full[acc]);
+      } else {
+        mma_commit(&s.acc_full[acc]);
+      }
     }
+    __syncwarp();
     acc ^= 1;
     if (acc == 0) acc_phase ^= 1u;
   }
-  if (*abort_flag && any) {
+  // and the even one until both CTAs' epilogues have handed back its accumulators
+  for (int i = 0; PAIR && ok && i < 2; ++i) {
+    if (!__all_sync(0xffffffffu, wait_bounded_long(&s.acc_empty[acc], acc_phase ^ 1u, abort_flag, a.error))) break;
+    acc ^= 1;
+    if (acc == 0) acc_phase ^= 1u;
+  }
+  if (lead && *abort_flag && any) {
     if constexpr (PAIR) {
       mma_commit_pair_local(s.drain);
     } else {
@@ -693,7 +728,7 @@ template <bool PAIR, bool GATED, int ACT>
 __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constant__ LinArgs a) {
   extern __shared__ uint8_t raw[];
   const Shared s = carve(raw);
-  const int warp = static_cast<int>(threadIdx.x >> 5);
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   let_next_start();
   if (threadIdx.x == 0) {
     for (int i = 0; i < a.stages; ++i) {
@@ -727,14 +762,17 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
   if (PAIR) cluster_sync();  // the other CTA's barriers exist before anything reaches them
   tc_fence_after();
   const uint32_t tmem = *s.tmem;
+  // what the first tile needs of the arguments is read, and its divisions are made, while the kernel before still runs
+  const Tile first = tile_of(a, PAIR ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x));
+  touch(*first.p, first);
   wait_for_previous();
 
   if (warp == 0) {
-    if (lane_id() == 0) load_loop<PAIR, GATED, true>(a, s);
+    if (lane_id() == 0) load_loop<PAIR, GATED, true>(a, s, first);
   } else if (warp == 1) {
-    if (lane_id() == 0) mma_loop<PAIR>(a, s, tmem);
+    mma_loop<PAIR>(a, s, tmem, first);
   } else if (warp == 2 + EPI_WARPS) {
-    if (lane_id() == 0) load_loop<PAIR, GATED, false>(a, s);
+    if (lane_id() == 0) load_loop<PAIR, GATED, false>(a, s, first);
   } else if (warp == 3 + EPI_WARPS) {
     if (a.sum.parts > 0) {
       for (int c = static_cast<int>(blockIdx.x) * 32; c < a.sum.N; c += static_cast<int>(gridDim.x) * 32)
@@ -746,7 +784,15 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
 
   tc_fence_before();
   __syncthreads();
-  if (PAIR) cluster_sync();  // no CTA leaves while the other may still signal its barriers
+  // no CTA leaves while the other may still signal its barriers: what is signalled has arrived (load_loop and mma_loop
+  // end with waits for it), unless a wait ran out
+  if constexpr (PAIR) {
+    if (*s.abort_flag) {
+      cluster_sync();
+    } else {
+      cluster_sync_relaxed();
+    }
+  }
   if (warp == 1) {
     tc_fence_after();
     if constexpr (PAIR) {
