@@ -295,6 +295,8 @@ cce_status run_products(const Product* in, int n, bool gated, bool bf16, const L
   if (items >= LIMIT) return CCE_ERR_SHAPE;
   a.items = static_cast<int>(items);
   a.stage_bytes = (LIN_BI + widest) * static_cast<int>(bk) * 2;
+  if (n == 1 && !gated && in[0].e.y_type == CCE_F32 && plan.c[0].kb_split > LIN_CHUNK_K / static_cast<int>(bk))
+    a.chunk = LIN_CHUNK_K / static_cast<int>(bk);
   a.stages = std::min(LIN_MAX_STAGES, LIN_RING_BYTES / a.stage_bytes);
   const int units = static_cast<int>(std::min<int64_t>(plan.pair ? on.pairs : on.sms, items));
   cudaError_t e = launch_linear_gemm(a, plan.pair, gated, units, s);

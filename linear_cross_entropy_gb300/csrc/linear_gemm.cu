@@ -32,7 +32,7 @@ int linear_pair_units(int sms) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, lin::linear_kernel<true, false, CCE_ACT_NONE>, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, lin::linear_kernel<true, false, CCE_ACT_NONE, false>, &cfg) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }

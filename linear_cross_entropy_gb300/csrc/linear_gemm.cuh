@@ -256,7 +256,9 @@ __device__ __forceinline__ void load_loop(const LinArgs& a, const Shared& s, con
   }
 }
 
-template <bool PAIR>
+// PARTS, here and below: results whose sum goes on in another accumulator every LIN_CHUNK_K (in kernels of their own: as a
+// choice at run time it cost the others 0.3 to 0.7 us a launch).
+template <bool PAIR, bool PARTS>
 __device__ __forceinline__ void mma_loop(const LinArgs& a, const Shared& s, uint32_t tmem, const Tile& first) {
   if (PAIR && cluster_ctarank() != 0) return;  // the even CTA issues for both
   constexpr int BK = lin_bk(PAIR), A_BYTES = LIN_BI * BK * 2;
@@ -268,6 +270,8 @@ __device__ __forceinline__ void mma_loop(const LinArgs& a, const Shared& s, uint
   uint32_t phase = 0, acc_phase = 0;
   bool any = false, ok = true;
   const uint32_t lead = elect_lane();
+  // parts of K, and whether they take the accumulators in turn
+  const int chunk = PARTS ? a.chunk : 1 << 30, other = PARTS ? 0 : 1;
   // (the divisions for the next tile are made while this one's MMAs run: some 700 cycles between two tiles otherwise)
   Tile next = first;
   for (int item = unit; ok && item < a.items; item += units) {
@@ -283,67 +287,71 @@ __device__ __forceinline__ void mma_loop(const LinArgs& a, const Shared& s, uint
     const uint32_t a_step = (a_mn ? 2048u : 32u) >> 4, b_step = (b_mn ? 2048u : 32u) >> 4;
     const uint32_t a_next = (a_mn ? 8192u : 2u * GROUP) >> 4;
     const uint32_t b_next = (b_mn ? 8192u : (PAIR ? p.jt / 2 : p.jt) * 128u) >> 4;
-    if (!__all_sync(0xffffffffu, wait_bounded_long(&s.acc_empty[acc], acc_phase ^ 1u, abort_flag, a.error))) {
-      ok = false;
-      break;
-    }
-    tc_fence_after();
-    const uint32_t d = tmem + static_cast<uint32_t>(acc * ACC_COLS);
-    uint32_t accumulate = 0;
-    for (int kb = t.kb; kb < t.kb_end; ++kb) {
-      if (!__all_sync(0xffffffffu, wait_bounded_long(&s.full[stage], phase, abort_flag, a.error))) {
+    for (int from = t.kb; from < t.kb_end; from += chunk) {
+      if (!__all_sync(0xffffffffu, wait_bounded_long(&s.acc_empty[acc], acc_phase ^ 1u, abort_flag, a.error))) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const int left = kb < kb_first ? klen0 - kb * BK : klen1 - (kb - kb_first) * BK;
-      const uint32_t at = smem_u32(s.ring + stage * stage_bytes);
-      const uint64_t a_desc = smem_desc_sw128(at, a_lbo, 1024u);
-      const uint64_t b_desc = smem_desc_sw128(at + A_BYTES, b_lbo, 1024u);
-      const auto mma = [&](int k) {
-        const uint64_t ad = a_desc + (k >> 2) * a_next + (k & 3) * a_step, bd = b_desc + (k >> 2) * b_next + (k & 3) * b_step;
-        if constexpr (PAIR) {
-          mma_bf16_pair_by(lead, d, ad, bd, idesc, accumulate | (k > 0));
-        } else {
-          mma_bf16_by(lead, d, ad, bd, idesc, accumulate | (k > 0));
+      const uint32_t d = tmem + static_cast<uint32_t>(acc * ACC_COLS);
+      uint32_t accumulate = 0;
+      const int part_end = min(from + chunk, t.kb_end);
+      for (int kb = from; kb < part_end; ++kb) {
+        if (!__all_sync(0xffffffffu, wait_bounded_long(&s.full[stage], phase, abort_flag, a.error))) {
+          ok = false;
+          break;
         }
-      };
-      if (left >= BK) {
+        tc_fence_after();
+        const int left = kb < kb_first ? klen0 - kb * BK : klen1 - (kb - kb_first) * BK;
+        const uint32_t at = smem_u32(s.ring + stage * stage_bytes);
+        const uint64_t a_desc = smem_desc_sw128(at, a_lbo, 1024u);
+        const uint64_t b_desc = smem_desc_sw128(at + A_BYTES, b_lbo, 1024u);
+        const auto mma = [&](int k) {
+          const uint64_t ad = a_desc + (k >> 2) * a_next + (k & 3) * a_step, bd = b_desc + (k >> 2) * b_next + (k & 3) * b_step;
+          if constexpr (PAIR) {
+            mma_bf16_pair_by(lead, d, ad, bd, idesc, accumulate | (k > 0));
+          } else {
+            mma_bf16_by(lead, d, ad, bd, idesc, accumulate | (k > 0));
+          }
+        };
+        if (left >= BK) {
 #pragma unroll
-        for (int k = 0; k < BK / 16; ++k) mma(k);
-      } else {
-        for (int k = 0; 16 * k < left; ++k) mma(k);  // behind K's end there are zeros
+          for (int k = 0; k < BK / 16; ++k) mma(k);
+        } else {
+          for (int k = 0; 16 * k < left; ++k) mma(k);  // behind K's end there are zeros
+        }
+        accumulate = 1;
+        any = true;
+        if (lead) {
+          if constexpr (PAIR) {
+            mma_commit_pair_both(&s.empty[stage]);
+          } else {
+            mma_commit(&s.empty[stage]);
+          }
+        }
+        __syncwarp();
+        if (++stage == stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        if (kb == t.kb && item + units < a.items) next = tile_of(a, item + units);
       }
-      accumulate = 1;
-      any = true;
+      if (!ok) break;
       if (lead) {
         if constexpr (PAIR) {
-          mma_commit_pair_both(&s.empty[stage]);
+          mma_commit_pair_both(&s.acc_full[acc]);
         } else {
-          mma_commit(&s.empty[stage]);
+          mma_commit(&s.acc_full[acc]);
         }
       }
       __syncwarp();
-      if (++stage == stages) {
-        stage = 0;
-        phase ^= 1u;
-      }
-      if (kb == t.kb && item + units < a.items) next = tile_of(a, item + units);
+      acc ^= other;
+      if (acc == 0) acc_phase ^= 1u;
     }
     if (!ok) break;
-    if (lead) {
-      if constexpr (PAIR) {
-        mma_commit_pair_both(&s.acc_full[acc]);
-      } else {
-        mma_commit(&s.acc_full[acc]);
-      }
-    }
-    __syncwarp();
-    acc ^= 1;
-    if (acc == 0) acc_phase ^= 1u;
   }
   // and the even one until both CTAs' epilogues have handed back its accumulators
-  for (int i = 0; PAIR && ok && i < 2; ++i) {
+  for (int i = 0; PAIR && ok && i < (PARTS ? 1 : 2); ++i) {
     if (!__all_sync(0xffffffffu, wait_bounded_long(&s.acc_empty[acc], acc_phase ^ 1u, abort_flag, a.error))) break;
     acc ^= 1;
     if (acc == 0) acc_phase ^= 1u;
@@ -495,6 +503,22 @@ struct Chunk {
     tmem_ld_wait16(lo);
     tmem_ld_wait16(hi);
   }
+  // To what there is, the sum so far at those places is added.
+  __device__ __forceinline__ void add(uint32_t first, uint32_t second) {
+    add_half(first, lo);
+    add_half(second, hi);
+  }
+  __device__ __forceinline__ void store(uint32_t first, uint32_t second) const {
+    tmem_st_16x256(first, lo);
+    tmem_st_16x256(second, hi);
+  }
+  __device__ __forceinline__ static void add_half(uint32_t at, uint32_t (&to)[16]) {
+    uint32_t so_far[16];
+    tmem_ld_16x256(at, so_far);
+    tmem_ld_wait16(so_far);
+#pragma unroll
+    for (int x = 0; x < 16; ++x) to[x] = __float_as_uint(__uint_as_float(so_far[x]) + __uint_as_float(to[x]));
+  }
   __device__ __forceinline__ void get(Fragment<4>& f) const {
 #pragma unroll
     for (int b = 0; b < 4; ++b)
@@ -517,6 +541,7 @@ struct Chunk {
 struct Share {
   int i0, j0, rows, cols, chunks;
   uint32_t first, second;  // where chunk 0 is in TMEM, its halves
+  uint32_t total;          // the sum of K's parts before this one, so far behind them; 0: there is none
   uint32_t tile;           // of the warp in shared memory
   float bias[4];
 };
@@ -576,7 +601,7 @@ __device__ __forceinline__ void finish_lean(const Shared& s, const Share& w, con
 }
 
 // Everything else: a residual, a layer's values in front of its activation, fp32 results and ones off 16 bytes.
-template <bool PAIR, bool GATED, int ACT>
+template <bool PAIR, bool GATED, int ACT, bool PARTS>
 __device__ __forceinline__ void finish_any(const Shared& s, const Share& w, const LinEpilogue& e, bool wide, int type,
                                            int acc, uint32_t release) {
   constexpr int R = GATED ? 2 : 4;
@@ -599,6 +624,7 @@ __device__ __forceinline__ void finish_any(const Shared& s, const Share& w, cons
       }
     }
     chunk.wait();
+    if (PARTS && w.total) chunk.add(w.first + w.total + jc, w.second + w.total + jc);
     if (c + 1 == w.chunks) {
       release_accumulator<PAIR>(s, acc, release);
     } else {
@@ -640,7 +666,7 @@ __device__ __forceinline__ void finish_any(const Shared& s, const Share& w, cons
 }
 
 // Partial sums of a split of K.
-template <bool PAIR, bool GATED>
+template <bool PAIR, bool GATED, bool PARTS>
 __device__ __forceinline__ void store_partial(const Shared& s, const Share& w, const LinProblem& p, int split, int acc,
                                               uint32_t release) {
   const int lane = static_cast<int>(lane_id());
@@ -651,6 +677,7 @@ __device__ __forceinline__ void store_partial(const Shared& s, const Share& w, c
     Chunk chunk;
     chunk.load(w.first + jc, w.second + jc);
     chunk.wait();
+    if (PARTS && w.total) chunk.add(w.first + w.total + jc, w.second + w.total + jc);
     if (c + 1 == w.chunks) {
       release_accumulator<PAIR>(s, acc, release);
     } else {
@@ -669,7 +696,23 @@ __device__ __forceinline__ void store_partial(const Shared& s, const Share& w, c
   }
 }
 
-template <bool PAIR, bool GATED, int ACT>
+// A part of K that others follow, to the sum so far.
+template <bool PAIR>
+__device__ __forceinline__ void add_to_total(const Shared& s, const Share& w, bool none_yet, int acc, uint32_t release) {
+  for (int c = 0; c < w.chunks; ++c) {
+    const int jc = CHUNK * PHASES * c;
+    const uint32_t first = w.first + ACC_COLS + jc, second = w.second + ACC_COLS + jc;
+    Chunk chunk;
+    chunk.load(w.first + jc, w.second + jc);
+    chunk.wait();
+    if (!none_yet) chunk.add(first, second);
+    chunk.store(first, second);
+  }
+  tmem_st_wait();
+  release_accumulator<PAIR>(s, acc, release);
+}
+
+template <bool PAIR, bool GATED, int ACT, bool PARTS>
 __device__ __forceinline__ void epilogue_loop(const LinArgs& a, const Shared& s, uint32_t tmem, int warp) {
   constexpr int ROWS = GATED ? TURN : 32;  // of the output, a warp
   const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
@@ -703,28 +746,47 @@ __device__ __forceinline__ void epilogue_loop(const LinArgs& a, const Shared& s,
     }
     w.first = w.second = lane_base + static_cast<uint32_t>(acc * ACC_COLS + CHUNK * phase_of);
     (GATED && p.up_first ? w.first : w.second) += 16u << 16;
+    const auto filled = [&] {
+      bool ok = true;
+      if (lane == 0) ok = wait_bounded_long(&s.acc_full[acc], acc_phase, s.abort_flag, a.error);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      tc_fence_after();
+      return ok;
+    };
+    w.total = 0;
     bool ok = true;
-    if (lane == 0) ok = wait_bounded_long(&s.acc_full[acc], acc_phase, s.abort_flag, a.error);
-    ok = __shfl_sync(0xffffffffu, ok, 0);
-    if (!ok) break;
-    tc_fence_after();
+    if constexpr (PARTS) {
+      // parts of K one after the other in the first accumulator, their sum in the second one's place
+      for (int kb = t.kb; kb + a.chunk < t.kb_end; kb += a.chunk) {
+        ok = filled();
+        if (!ok) break;
+        add_to_total<PAIR>(s, w, kb == t.kb, acc, release);
+        acc_phase ^= 1u;
+        w.total = ACC_COLS;
+      }
+    }
+    if (!ok || !filled()) break;
     if (w.chunks <= 0) {
       release_accumulator<PAIR>(s, acc, release);
     } else if (!whole) {
-      store_partial<PAIR, GATED>(s, w, p, t.split, acc, release);
+      store_partial<PAIR, GATED, PARTS>(s, w, p, t.split, acc, release);
     } else if (wide && !e.z[0] && !e.res) {
       finish_lean<PAIR, GATED, ACT, false>(s, w, e, type, acc, release);
     } else if (GATED && wide) {
       finish_lean<PAIR, GATED, ACT, GATED>(s, w, e, type, acc, release);
     } else {
-      finish_any<PAIR, GATED, ACT>(s, w, e, wide, type, acc, release);
+      finish_any<PAIR, GATED, ACT, PARTS>(s, w, e, wide, type, acc, release);
     }
-    acc ^= 1;
-    if (acc == 0) acc_phase ^= 1u;
+    if (PARTS) {
+      acc_phase ^= 1u;
+    } else {
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+    }
   }
 }
 
-template <bool PAIR, bool GATED, int ACT>
+template <bool PAIR, bool GATED, int ACT, bool PARTS>
 __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constant__ LinArgs a) {
   extern __shared__ uint8_t raw[];
   const Shared s = carve(raw);
@@ -770,7 +832,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
   if (warp == 0) {
     if (lane_id() == 0) load_loop<PAIR, GATED, true>(a, s, first);
   } else if (warp == 1) {
-    mma_loop<PAIR>(a, s, tmem, first);
+    mma_loop<PAIR, PARTS>(a, s, tmem, first);
   } else if (warp == 2 + EPI_WARPS) {
     if (lane_id() == 0) load_loop<PAIR, GATED, false>(a, s, first);
   } else if (warp == 3 + EPI_WARPS) {
@@ -779,7 +841,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
         sum_columns(a.sum, c + static_cast<int>(lane_id()));
     }
   } else {
-    epilogue_loop<PAIR, GATED, ACT>(a, s, tmem, warp);
+    epilogue_loop<PAIR, GATED, ACT, PARTS>(a, s, tmem, warp);
   }
 
   tc_fence_before();
@@ -809,10 +871,12 @@ cudaError_t prepare() {
   const auto set = [](auto kernel) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SHARED);
   };
-  cudaError_t e = set(linear_kernel<false, false, ACT>);
-  if (e == cudaSuccess) e = set(linear_kernel<false, true, ACT>);
-  if (e == cudaSuccess) e = set(linear_kernel<true, false, ACT>);
-  if (e == cudaSuccess) e = set(linear_kernel<true, true, ACT>);
+  cudaError_t e = set(linear_kernel<false, false, ACT, false>);
+  if (e == cudaSuccess) e = set(linear_kernel<false, true, ACT, false>);
+  if (e == cudaSuccess) e = set(linear_kernel<true, false, ACT, false>);
+  if (e == cudaSuccess) e = set(linear_kernel<true, true, ACT, false>);
+  if (e == cudaSuccess) e = set(linear_kernel<false, false, ACT, true>);
+  if (e == cudaSuccess) e = set(linear_kernel<true, false, ACT, true>);
   return e;
 }
 
@@ -820,8 +884,9 @@ template <int ACT>
 cudaError_t launch(const LinArgs& a, bool pair, bool gated, int units, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(pair ? 2 * units : units)), block(THREADS);
   const auto with = [&](auto kernel) { return launch_after(kernel, grid, block, SHARED, pair ? 2u : 1u, s, a); };
-  if (pair) return gated ? with(linear_kernel<true, true, ACT>) : with(linear_kernel<true, false, ACT>);
-  return gated ? with(linear_kernel<false, true, ACT>) : with(linear_kernel<false, false, ACT>);
+  if (a.chunk > 0) return pair ? with(linear_kernel<true, false, ACT, true>) : with(linear_kernel<false, false, ACT, true>);
+  if (pair) return gated ? with(linear_kernel<true, true, ACT, false>) : with(linear_kernel<true, false, ACT, false>);
+  return gated ? with(linear_kernel<false, true, ACT, false>) : with(linear_kernel<false, false, ACT, false>);
 }
 
 }  // namespace lin

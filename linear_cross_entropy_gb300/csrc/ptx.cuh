@@ -316,6 +316,17 @@ __device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, uint32_t (&r)[16]
       : "memory");
 }
 
+// The way back, and the wait for it.
+__device__ __forceinline__ void tmem_st_16x256(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 // Four 8 x 8 matrices of 16-bit values, of which thread t holds row t / 4, columns 2 (t % 4) and + 1, to shared memory
 // by columns: lane l has the address of column l % 8 of matrix l / 8 (eight rows, 16 bytes).
 __device__ __forceinline__ void stmatrix_columns(uint32_t saddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {

@@ -72,6 +72,21 @@ def test_epilogue(cce, M, N, K, act, out, bias, residual):
             assert none is None and torch.equal(y, y2)
 
 
+@pytest.mark.parametrize("M,N", [(300, 512), (4100, 1001), (40, 264)])
+def test_long_sums_in_fp32(cce, M, N):
+    """An fp32 result's sum goes on in another accumulator every 1,024 of K: its error is the parts', relative to the norm
+    that of K = 1,024 (parts' errors grow together as their sums do, and 8 additions to nearest make 2^-24 each), where one
+    accumulator's would be 8 times that.  Twice is allowed."""
+    off = []
+    for K in (1024, 8192 + 72):
+        _, x, (w,) = inputs(M, N, K, BF16, 15)
+        ref = x.double() @ w.double().T
+        off.append(((cce.linear(x, w, out_dtype=F32) - ref).norm() / ref.norm()).item())
+        y, kept = cce.cce_linear_forward(x, w, activation="relu", out_dtype=F32, save=True)
+        assert torch.equal(y, cce.linear(x, w, out_dtype=F32).relu())
+    assert off[1] < 2 * off[0] + 2.0 ** -23, off
+
+
 BACKWARD = [(1, 1, 1), (1, 300, 72), (5, 17, 33), (16, 8, 2048), (33, 100, 72), (129, 257, 65), (128, 128, 128),
             (1000, 640, 200), (2048, 896, 896), (4100, 72, 640), (9000, 130, 70), (20000, 8, 8), (256, 4096, 1024)]
 
