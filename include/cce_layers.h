@@ -28,7 +28,8 @@
  *
  * Activations
  * -----------
- * relu max(z, 0); gelu z Phi(z) with the normal distribution function; gelu_tanh
+ * relu max(z, 0); gelu z Phi(z) with the normal distribution function, whose smaller
+ * half is within (z^2 + 16) 2^-23 of its own value (below 2^-126 it may be 0); gelu_tanh
  * z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2; silu z / (1 + e^-z).  The
  * derivative of relu at 0 is 0.
  */

@@ -14,7 +14,7 @@ product is fp32 with one rounding to the result.  The result is contiguous, of
 x's type or float32.  x, weights and gradients may be strided: rows at one pitch,
 on 16 bytes and a multiple of 8 elements apart, are read in place, others
 (hidden[:, :-1], odd widths) are copied first.  Activations: None, "relu", "gelu"
-(exact), "gelu_tanh", "silu".  For the backward pass what goes into the
+(z Phi(z), Phi within (z^2 + 16) 2^-23 of itself), "gelu_tanh", "silu".  For the backward pass what goes into the
 activation is kept in 16 bits, two of which more are fraction than bf16 has (torch
 int16 words that only the backward reads; fp16 for fp16), and the gradient in front
 of it is rounded to x's type for its products.
