@@ -9,8 +9,8 @@
  *   m = beta1 m + (1 - beta1) g
  *   v = beta2 v + (1 - beta2) g^2
  *   w = w (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
- * in fp32.  w is the fp32 master weight where there is one, which is updated, and the
- * parameter is w rounded once to its type.
+ * in fp32 (an eps below 2^-150 counts as 0, and 0 / 0 is NaN).  w is the fp32 master weight
+ * where there is one, which is updated, and the parameter is w rounded once to its type.
  *
  * States in 8 bits
  * ----------------

@@ -64,8 +64,10 @@ struct Batch {
 };
 
 struct Rule {
-  float beta1, rest1, beta2, rest2, eps;  // rest: 1 - beta
-  float log1, log2;                       // natural logarithms of the betas
+  float beta1, rest1, beta2, rest2;  // rest: 1 - beta
+  float eps;                         // times scale
+  float scale;                       // a power of two on both sides of the quotient, so that a divisor is no subnormal
+  float log1, log2;                  // natural logarithms of the betas
   float lr;
   float correct1, correct2;  // 1 - beta^t
   const int64_t* step;       // may be null
@@ -104,8 +106,8 @@ __device__ __forceinline__ uint32_t mix(uint32_t x) { return mix_rest(x ^ x >> 1
 struct Now {
   float factor;    // of the gradients
   float lr;
-  float size;      // lr / (1 - beta1^t)
-  float inv_root;  // 1 / sqrt(1 - beta2^t)
+  float size;      // lr / (1 - beta1^t), times scale
+  float inv_root;  // 1 / sqrt(1 - beta2^t), times scale
   uint32_t key;
 };
 
@@ -125,8 +127,8 @@ __device__ __forceinline__ Now now_of(const Rule& r) {
     c1 = -expm1f(static_cast<float>(step) * r.log1);
     c2 = -expm1f(static_cast<float>(step) * r.log2);
   }
-  n.size = n.lr / c1;
-  n.inv_root = 1.0f / sqrtf(c2);
+  n.size = n.lr / c1 * r.scale;
+  n.inv_root = 1.0f / sqrtf(c2) * r.scale;
   n.key = mix(mix(r.seed) ^ t);
   return n;
 }
@@ -140,7 +142,8 @@ __device__ __forceinline__ void average(const Rule& r, const Now& now, Pair g, P
   v = fma(mul(Pair::both(r.beta2), v), one, mul(mul(Pair::both(r.rest2), g), g));
 }
 
-// Two new weights.  (The divisor is 0 or at least 2^-75, a root of fp32's least value.)
+// Two new weights.  (A divisor's root is 0 or at least 2^-75, that of fp32's least value, and eps is normal by its scale: the
+// reciprocal, which takes subnormals for 0, sees none.  0 by 0, with eps = 0, is NaN.)
 __device__ __forceinline__ Pair step_weights(const Rule& r, const Now& now, float keep, Pair w, Pair m, Pair root) {
   const float2 by = fma(root, Pair::both(now.inv_root), Pair::both(r.eps)).get();
   float lo, hi;
@@ -626,7 +629,9 @@ cce_status cce_adamw_step(const cce_adamw_tensor* tensors, int64_t n_tensors, in
   r.rest1 = static_cast<float>(1.0 - o->beta1);
   r.beta2 = static_cast<float>(o->beta2);
   r.rest2 = static_cast<float>(1.0 - o->beta2);
-  r.eps = static_cast<float>(o->eps);
+  // an eps among fp32's subnormals, from 2^-150 on, becomes a normal value, and what stands beside it is scaled likewise
+  r.scale = o->eps > 0.0 && o->eps < 0x1p-126 ? 0x1p24f : 1.0f;
+  r.eps = static_cast<float>(o->eps * r.scale);
   r.log1 = static_cast<float>(std::log(o->beta1));
   r.log2 = static_cast<float>(std::log(o->beta2));
   r.lr = static_cast<float>(o->lr);
