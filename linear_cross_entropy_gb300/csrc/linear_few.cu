@@ -77,7 +77,10 @@ struct Step {
   }
 };
 
-template <bool BF16, int NT, bool GATED>
+// PARTS: fp32 results of a long K.  mma.sync cuts where it could round, as tcgen05.mma does: a warp's sum goes on in other
+// registers every LIN_CHUNK_K of its k, and the parts are added to nearest, where they wait in shared memory.  With K = 65,536
+// a sum is 1.0e-6 of the norm off and not 9.1e-6.  (In kernels of their own: in all it cost a gated layer of 32 rows 7%.)
+template <bool BF16, int NT, bool GATED, bool PARTS>
 __global__ void __launch_bounds__(32 * WARPS, 2) few_kernel(const __grid_constant__ LinFew a) {
   constexpr int MATS = GATED ? 2 : 1;
   constexpr int UNROLL = GATED ? 2 : 4;  // steps in flight: eight vectors of the weights a thread
@@ -101,6 +104,21 @@ __global__ void __launch_bounds__(32 * WARPS, 2) few_kernel(const __grid_constan
     x[n] = static_cast<const uint16_t*>(a.x) + static_cast<int64_t>(min(g + 8 * n, a.J - 1)) * a.x_pitch;
 
   float c[MATS][NT][4] = {};
+  bool first = true;
+  const auto put_aside = [&] {
+#pragma unroll
+    for (int m = 0; m < MATS; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float& to = sums[warp][m][g + 8 * (q >> 1)][8 * n + 2 * t + (q & 1)];
+          to = PARTS && !first ? to + c[m][n][q] : c[m][n][q];
+          if (PARTS) c[m][n][q] = 0.0f;
+        }
+    first = false;
+  };
+  int left = LIN_CHUNK_K / 64;
   // a warp's k: two steps at 64 (warp + WARPS q), q = 0, 1, ...
   constexpr int STRIDE = 64 * WARPS;
   int k = warp * 64 + 8 * t;
@@ -112,6 +130,10 @@ __global__ void __launch_bounds__(32 * WARPS, 2) few_kernel(const __grid_constan
     for (int u = 0; u < UNROLL; ++u) s[u].template load<true>(w, x, k + (u >> 1) * STRIDE + (u & 1) * 32, a.K);
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) s[u].add_to(c);
+    if (PARTS && (left -= UNROLL / 2) == 0) {
+      put_aside();
+      left = LIN_CHUNK_K / 64;
+    }
   }
 #pragma unroll 1
   for (; k - 8 * t < a.K; k += STRIDE) {
@@ -126,12 +148,7 @@ __global__ void __launch_bounds__(32 * WARPS, 2) few_kernel(const __grid_constan
     s[0].add_to(c);
     s[1].add_to(c);
   }
-#pragma unroll
-  for (int m = 0; m < MATS; ++m)
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) sums[warp][m][g + 8 * (q >> 1)][8 * n + 2 * t + (q & 1)] = c[m][n][q];
+  put_aside();
   __syncthreads();
   const int r = static_cast<int>(threadIdx.x) % ROWS, i = i0 + r;
   if (i >= a.I) return;
@@ -149,8 +166,9 @@ __global__ void __launch_bounds__(32 * WARPS, 2) few_kernel(const __grid_constan
 template <bool BF16, int NT>
 cudaError_t launch(const LinFew& a, bool gated, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>((a.I + ROWS - 1) / ROWS)), block(32 * WARPS);
-  return gated ? launch_after(few_kernel<BF16, NT, true>, grid, block, 0, 1, s, a)
-               : launch_after(few_kernel<BF16, NT, false>, grid, block, 0, 1, s, a);
+  if (gated) return launch_after(few_kernel<BF16, NT, true, false>, grid, block, 0, 1, s, a);
+  return a.e.y_type == CCE_F32 && a.K > WARPS * LIN_CHUNK_K ? launch_after(few_kernel<BF16, NT, false, true>, grid, block, 0, 1, s, a)
+                                                            : launch_after(few_kernel<BF16, NT, false, false>, grid, block, 0, 1, s, a);
 }
 
 }  // namespace
