@@ -206,6 +206,9 @@ def load() -> ctypes.CDLL:
         query = getattr(lib, f"cce_{name}_workspace_bytes")
         query.argtypes = [i64, i64, i64]
         query.restype = sz
+    # include/cce_layers_ex.h
+    lib.cce_layers_plan_searches.argtypes = []
+    lib.cce_layers_plan_searches.restype = ctypes.c_uint64
     # include/cce_optim.h
     lib.cce_optim_abi_version.argtypes = []
     lib.cce_optim_abi_version.restype = ci

@@ -1,11 +1,13 @@
-// Entry points of the layers in front of the head (include/cce_layers.h):
+// Entry points of the layers in front of the head (include/cce_layers.h and include/cce_layers_ex.h):
 // argument checks, workspace layout, the choice of tiles, launches.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <mutex>
 
-#include "../../include/cce_layers.h"
+#include "../../include/cce_layers_ex.h"
 #include "internal.h"
 #include "linear.h"
 
@@ -146,38 +148,67 @@ Plan plan_tiles(const Shape* s, int n, bool gated) {
   return best;
 }
 
-// Plans are functions of sizes alone; searching one takes some 10 us.
-struct Planned {
-  Shape s[LIN_MAX_PROBLEMS];
-  int n = 0;
-  bool gated;
-  Plan plan;
-};
-
-Plan plan_of(const Shape* s, int n, bool gated) {
-  static thread_local Planned kept[64];
-  uint64_t h = static_cast<uint64_t>(n * 2 + gated);
-  for (int q = 0; q < n; ++q) {
-    for (const int v : {s[q].I, s[q].J, s[q].K, s[q].parts, static_cast<int>(s[q].b_mn)})
-      h = (h ^ static_cast<uint64_t>(v)) * 0x9e3779b97f4a7c15ull;
+// Plans are functions of sizes alone, and searching one takes up to some 20 us: the last ones are kept, for all threads.  A set
+// has room for sixteen, so that a model's layers, a few hundred plans, do not push each other out.
+class Plans {
+ public:
+  Plan of(const Shape* s, int n, bool gated) {
+    uint64_t h = static_cast<uint64_t>(n * 2 + gated);
+    for (int q = 0; q < n; ++q) {
+      for (const int v : {s[q].I, s[q].J, s[q].K, s[q].parts, static_cast<int>(s[q].b_mn)})
+        h = (h ^ static_cast<uint64_t>(v)) * 0x9e3779b97f4a7c15ull;
+    }
+    Set& set = sets_[h >> 58];
+    {
+      const std::lock_guard<std::mutex> lock(mutex_);
+      for (int w = 0; w < WAYS; ++w) {
+        if (set.hash[w] == h && same(set.kept[w], s, n, gated)) return set.kept[w].plan;
+      }
+    }
+    ++searches_;
+    Planned made;
+    std::copy(s, s + n, made.s);
+    made.n = n;
+    made.gated = gated;
+    made.plan = plan_tiles(s, n, gated);
+    const std::lock_guard<std::mutex> lock(mutex_);
+    set.hash[set.oldest] = h;
+    set.kept[set.oldest] = made;
+    set.oldest = (set.oldest + 1) % WAYS;
+    return made.plan;
   }
-  Planned& k = kept[h >> 58];
-  const auto same = [&] {
+  uint64_t searches() const { return searches_; }
+
+ private:
+  static constexpr int WAYS = 16;
+  struct Planned {
+    Shape s[LIN_MAX_PROBLEMS];
+    int n;  // 0: none
+    bool gated;
+    Plan plan;
+  };
+  struct Set {
+    uint64_t hash[WAYS];
+    Planned kept[WAYS];
+    int oldest;
+  };
+  static bool same(const Planned& k, const Shape* s, int n, bool gated) {
     if (k.n != n || k.gated != gated) return false;
     for (int q = 0; q < n; ++q) {
       const Shape &a = k.s[q], &b = s[q];
       if (a.I != b.I || a.J != b.J || a.K != b.K || a.parts != b.parts || a.b_mn != b.b_mn) return false;
     }
     return true;
-  };
-  if (!same()) {
-    for (int q = 0; q < n; ++q) k.s[q] = s[q];
-    k.n = n;
-    k.gated = gated;
-    k.plan = plan_tiles(s, n, gated);
   }
-  return k.plan;
-}
+
+  std::mutex mutex_;
+  std::atomic<uint64_t> searches_{0};
+  Set sets_[64] = {};
+};
+
+Plans g_plans;
+
+Plan plan_of(const Shape* s, int n, bool gated) { return g_plans.of(s, n, gated); }
 
 size_t part_bytes(const Shape& s, const Choice& c, bool gated) {
   return c.splits == 1 ? 0 : round256(size_t(4) * c.splits * (gated ? 2 : 1) * s.I * s.J);
@@ -465,6 +496,7 @@ using namespace cce;
 extern "C" {
 
 int cce_layers_abi_version(void) { return 100; }
+uint64_t cce_layers_plan_searches(void) { return g_plans.searches(); }
 
 size_t cce_linear_forward_workspace_bytes(int64_t M, int64_t N, int64_t K) { return forward_bytes(M, N, K, false); }
 size_t cce_gated_linear_forward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
