@@ -92,7 +92,7 @@ cce_status cce_linear_backward(const void* grad_y, int64_t g_pitch, int y_type, 
                                void* grad_weight, void* grad_bias, int bias_type, void* workspace, size_t ws_bytes,
                                void* stream);
 
-/* Bytes of workspace, as above. */
+/* Bytes of workspace, as above, for any call of these sizes; cce_layers_ex.h has what one call needs. */
 size_t cce_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /*

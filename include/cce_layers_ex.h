@@ -17,6 +17,19 @@ extern "C" {
  */
 uint64_t cce_layers_plan_searches(void);
 
+/*
+ * Bytes of workspace of one backward call, which takes less than any (the queries of
+ * cce_layers.h) where it computes less.  want: the results that are not NULL (DX grad_x, DW
+ * grad_weight or grad_gate_weight, DW_UP grad_up_weight, DB grad_bias), and for a linear
+ * layer DZ unless its products can read grad_y itself: act is CCE_ACT_NONE, y_type is `type`
+ * and grad_y starts on 16 bytes at a pitch of a multiple of 8 elements (or neither DX nor DW
+ * is wanted).  A call checks for no more than this.  0 for invalid sizes or flags.
+ */
+enum { CCE_WANT_DX = 1, CCE_WANT_DW = 2, CCE_WANT_DW_UP = 4, CCE_WANT_DB = 8, CCE_WANT_DZ = 16 };
+
+size_t cce_linear_backward_workspace_bytes_ex(int64_t M, int64_t N, int64_t K, int want);
+size_t cce_gated_linear_backward_workspace_bytes_ex(int64_t M, int64_t N, int64_t K, int want);
+
 #ifdef __cplusplus
 }
 #endif

@@ -209,6 +209,10 @@ def load() -> ctypes.CDLL:
     # include/cce_layers_ex.h
     lib.cce_layers_plan_searches.argtypes = []
     lib.cce_layers_plan_searches.restype = ctypes.c_uint64
+    for name in ("linear_backward", "gated_linear_backward"):
+        query = getattr(lib, f"cce_{name}_workspace_bytes_ex")
+        query.argtypes = [i64, i64, i64, ci]
+        query.restype = sz
     # include/cce_optim.h
     lib.cce_optim_abi_version.argtypes = []
     lib.cce_optim_abi_version.restype = ci

@@ -1,10 +1,10 @@
 // The layers in front of the head on torch tensors, over the C ABI of
-// include/cce_layers.h: checks, operands that the tensor cores' copies can read,
+// include/cce_layers.h and include/cce_layers_ex.h: checks, operands that the tensor cores' copies can read,
 // results, workspaces and the autograd nodes.
 #include <array>
 #include <atomic>
 
-#include "../../include/cce_layers.h"
+#include "../../include/cce_layers_ex.h"
 #include "binding.h"
 
 using namespace binding;
@@ -192,12 +192,16 @@ std::tuple<Tensor, Tensor, Tensor> linear_backward(const Tensor& g, const Tensor
   if (type_code(b_type) < 0) refuse("bias_dtype must be bfloat16, float16 or float32, got ", type_name(b_type));
   const at::NoGradGuard no_grad;
   const c10::cuda::CUDAGuard guard(x.device());
-  const size_t need = cce_linear_backward_workspace_bytes(s.M, s.N, s.K);
-  const Tensor ws = workspace(need, x);
   Matrices m;
   const Pitched gp = m.matrix(g), xp = m.operand(x), wp = m.operand(weight);
   const Pitched zp = act != CCE_ACT_NONE ? m.matrix(z) : Pitched{};
   m.copy(x);
+  const bool direct = act == CCE_ACT_NONE && g.scalar_type() == x.scalar_type() &&
+                      reinterpret_cast<uintptr_t>(pointer(gp.t)) % 16 == 0 && gp.pitch % 8 == 0;
+  const int want = (need_dx ? CCE_WANT_DX : 0) | (need_dw ? CCE_WANT_DW : 0) | (need_db ? CCE_WANT_DB : 0);
+  const size_t need = cce_linear_backward_workspace_bytes_ex(
+      s.M, s.N, s.K, want | (!direct && (need_dx || need_dw) ? CCE_WANT_DZ : 0));
+  const Tensor ws = workspace(need, x);
   const auto plainly = x.options().requires_grad(false);
   Tensor dx = need_dx ? at::empty(x.sizes(), plainly) : Tensor();
   Tensor dw = need_dw ? at::empty({s.N, s.K}, plainly) : Tensor();
@@ -259,7 +263,8 @@ std::tuple<Tensor, Tensor, Tensor> gated_backward(const Tensor& g, const Tensor&
   if (kept_code(up, x, "up") != z_type) refuse("gate and up must have one type");
   const at::NoGradGuard no_grad;
   const c10::cuda::CUDAGuard guard(x.device());
-  const size_t need = cce_gated_linear_backward_workspace_bytes(s.M, s.N, s.K);
+  const size_t need = cce_gated_linear_backward_workspace_bytes_ex(
+      s.M, s.N, s.K, (need_dx ? CCE_WANT_DX : 0) | (need_dg ? CCE_WANT_DW : 0) | (need_du ? CCE_WANT_DW_UP : 0));
   const Tensor ws = workspace(need, x);
   Matrices m;
   const Pitched gy = m.matrix(g), xp = m.operand(x), wg = m.operand(gate_weight), wu = m.operand(up_weight);

@@ -53,7 +53,7 @@ struct Plan {
   double cycles;
 };
 
-constexpr int UNITS = 152;                       // SMs
+constexpr int UNITS = LIN_SMS;
 constexpr int64_t MAX_PART_BYTES = 256ll << 20;  // of a product's partial sums
 
 int64_t i_tiles(const Shape& s, bool pair, bool gated) { return cdiv(s.I, (pair ? 2 : 1) * (gated ? LIN_BI / 2 : LIN_BI)); }
@@ -419,6 +419,16 @@ BackwardShapes backward_shapes(int64_t M, int64_t N, int64_t K, int mats) {
   return {shape_of(K, M, N, mats, false), shape_of(K, N, M, 1, true)};
 }
 
+// What a backward call computes, and whether dz is written for its products.
+struct Wanted {
+  bool dx, dw[2], db, staged;
+
+  static Wanted of(int flags) {
+    return {(flags & CCE_WANT_DX) != 0, {(flags & CCE_WANT_DW) != 0, (flags & CCE_WANT_DW_UP) != 0}, (flags & CCE_WANT_DB) != 0,
+            (flags & CCE_WANT_DZ) != 0};
+  }
+};
+
 // dz for the products, the row sums' parts, and the products' partial sums, in this order.
 struct BackwardLayout {
   size_t dz, sums, parts;
@@ -426,23 +436,32 @@ struct BackwardLayout {
   size_t total() const { return std::max<size_t>(NO_WORKSPACE, dz + sums + parts); }
 };
 
-BackwardLayout backward_layout(int64_t M, int64_t N, int64_t K, int mats) {
+BackwardLayout backward_layout(int64_t M, int64_t N, int64_t K, int mats, const Wanted& want) {
   BackwardLayout l{};
   l.pitch = cdiv(N, 8) * 8;
-  l.dz = round256(size_t(2) * mats * M * l.pitch);
-  l.sums = mats == 1 ? round256(size_t(4) * LIN_GRAD_PARTS * N) : 0;
   if (M == 0) return l;
+  if (want.staged) l.dz = round256(size_t(2) * mats * M * l.pitch);
+  if (want.db) l.sums = round256(size_t(4) * linear_grad_parts(M, N) * N);
   const BackwardShapes b = backward_shapes(M, N, K, mats);
-  const Shape all[3] = {b.dw, mats == 2 ? b.dw : b.dx, b.dx};
-  // whatever is asked for: dx alone, the weights' alone, one of a gated layer's with dx, all
-  const Shape with_one[2] = {b.dw, b.dx}, twice[2] = {b.dw, b.dw};
-  l.parts = std::max({parts_bytes(&b.dx, 1, false), parts_bytes(&b.dw, 1, false), parts_bytes(with_one, 2, false),
-                      mats == 2 ? parts_bytes(twice, 2, false) : 0, mats == 2 ? parts_bytes(all, 3, false) : 0});
+  Shape all[LIN_MAX_PROBLEMS];
+  int n = 0;
+  for (int m = 0; m < mats; ++m) {
+    if (want.dw[m]) all[n++] = b.dw;
+  }
+  if (want.dx) all[n++] = b.dx;
+  if (n > 0) l.parts = parts_bytes(all, n, false);
   return l;
 }
 
-size_t backward_bytes(int64_t M, int64_t N, int64_t K, int mats) {
-  return sizes_ok(M, N, K) ? backward_layout(M, N, K, mats).total() : 0;
+// Enough for any call of these sizes.
+size_t any_backward_bytes(int64_t M, int64_t N, int64_t K, int mats) {
+  if (!sizes_ok(M, N, K)) return 0;
+  size_t most = 0;
+  for (int products = 0; products < (mats == 2 ? 8 : 4); ++products) {  // which of dx, dW and the up projection's dW
+    const Wanted want{(products & 1) != 0, {(products & 2) != 0, (products & 4) != 0}, mats == 1, true};
+    most = std::max(most, backward_layout(M, N, K, mats, want).total());
+  }
+  return most;
 }
 
 LinEpilogue dense_out(void* y, int64_t pitch, int type) {
@@ -502,9 +521,17 @@ size_t cce_linear_forward_workspace_bytes(int64_t M, int64_t N, int64_t K) { ret
 size_t cce_gated_linear_forward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   return forward_bytes(M, N, K, true);
 }
-size_t cce_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) { return backward_bytes(M, N, K, 1); }
+size_t cce_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) { return any_backward_bytes(M, N, K, 1); }
 size_t cce_gated_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  return backward_bytes(M, N, K, 2);
+  return any_backward_bytes(M, N, K, 2);
+}
+size_t cce_linear_backward_workspace_bytes_ex(int64_t M, int64_t N, int64_t K, int want) {
+  if (!sizes_ok(M, N, K) || (want & ~(CCE_WANT_DX | CCE_WANT_DW | CCE_WANT_DB | CCE_WANT_DZ))) return 0;
+  return backward_layout(M, N, K, 1, Wanted::of(want)).total();
+}
+size_t cce_gated_linear_backward_workspace_bytes_ex(int64_t M, int64_t N, int64_t K, int want) {
+  if (!sizes_ok(M, N, K) || (want & ~(CCE_WANT_DX | CCE_WANT_DW | CCE_WANT_DW_UP))) return 0;
+  return backward_layout(M, N, K, 2, Wanted::of(want == 0 ? 0 : want | CCE_WANT_DZ)).total();
 }
 
 cce_status cce_linear_forward(const void* x, int64_t x_pitch, const void* weight, int64_t w_pitch, int type,
@@ -561,8 +588,13 @@ cce_status cce_linear_backward(const void* grad_y, int64_t g_pitch, int y_type, 
   cce_status st = first_of(
       check_matrix({grad_y, g_pitch, y_type, M, N}), check_operand(xm), check_operand(wm),
       check_matrix({z, z_pitch, type, M, N}, act == CCE_ACT_NONE), check_matrix({grad_x, K, type, M, K}, true),
-      check_matrix({grad_weight, K, type, N, K}, true), check_matrix({grad_bias, N, bias_type, 1, N}, true),
-      check_workspace(workspace, ws_bytes, backward_bytes(M, N, K, 1)));
+      check_matrix({grad_weight, K, type, N, K}, true), check_matrix({grad_bias, N, bias_type, 1, N}, true));
+  if (st != CCE_OK) return st;
+  // without an activation the products read grad_y itself where they can
+  const bool direct = act == CCE_ACT_NONE && y_type == type && multiple(grad_y, 16) && g_pitch % 8 == 0;
+  const bool staged = !direct && (grad_x || grad_weight);
+  const BackwardLayout l = backward_layout(M, N, K, 1, Wanted{grad_x != nullptr, {grad_weight != nullptr}, grad_bias != nullptr, staged});
+  st = check_workspace(workspace, ws_bytes, l.total());
   if (st != CCE_OK) return st;
   Device on;
   int launches = 0;
@@ -571,13 +603,8 @@ cce_status cce_linear_backward(const void* grad_y, int64_t g_pitch, int y_type, 
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (M == 0)
     return first_of(zero(grad_weight, size_t(2) * N * K, s), zero(grad_bias, size_t(type_bytes(bias_type)) * N, s));
-  const BackwardLayout l = backward_layout(M, N, K, 1);
   char* ws = static_cast<char*>(workspace);
-  // without an activation the products read grad_y itself where they can
   Operand dz{grad_y, g_pitch};
-  const bool direct = act == CCE_ACT_NONE && y_type == type && multiple(grad_y, 16) && g_pitch % 8 == 0 &&
-                      g_pitch < (int64_t(1) << 31);
-  const bool staged = !direct && (grad_x || grad_weight);
   if (staged) dz = Operand{ws, l.pitch};
   LinSum sum{};
   if (staged || grad_bias) {
@@ -595,7 +622,7 @@ cce_status cce_linear_backward(const void* grad_y, int64_t g_pitch, int y_type, 
     g.N = static_cast<int>(N);
     g.act = act;
     int parts = 0;
-    if (launch_linear_grad(g, false, type == CCE_BF16, on.sms, s, &parts) != cudaSuccess) st = CCE_ERR_CUDA;
+    if (launch_linear_grad(g, false, type == CCE_BF16, s, &parts) != cudaSuccess) st = CCE_ERR_CUDA;
     ++launches;
     if (grad_bias) sum = LinSum{g.part, grad_bias, parts, g.N, bias_type};
   }
@@ -620,8 +647,12 @@ cce_status cce_gated_linear_backward(const void* grad_y, int64_t g_pitch, const 
       check_matrix({grad_y, g_pitch, type, M, N}), check_operand(xm), check_operand(wm[0]), check_operand(wm[1]),
       check_matrix({gate, gate_pitch, type, M, N}), check_matrix({up, up_pitch, type, M, N}),
       check_matrix({grad_x, K, type, M, K}, true), check_matrix({grad_gate_weight, K, type, N, K}, true),
-      check_matrix({grad_up_weight, K, type, N, K}, true),
-      check_workspace(workspace, ws_bytes, backward_bytes(M, N, K, 2)));
+      check_matrix({grad_up_weight, K, type, N, K}, true));
+  if (st != CCE_OK) return st;
+  const bool any = grad_x || grad_gate_weight || grad_up_weight;
+  const BackwardLayout l = backward_layout(
+      M, N, K, 2, Wanted{grad_x != nullptr, {grad_gate_weight != nullptr, grad_up_weight != nullptr}, false, any});
+  st = check_workspace(workspace, ws_bytes, l.total());
   if (st != CCE_OK) return st;
   Device on;
   int launches = 0;
@@ -630,8 +661,7 @@ cce_status cce_gated_linear_backward(const void* grad_y, int64_t g_pitch, const 
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (M == 0)
     return first_of(zero(grad_gate_weight, size_t(2) * N * K, s), zero(grad_up_weight, size_t(2) * N * K, s));
-  if (!grad_x && !grad_gate_weight && !grad_up_weight) return CCE_OK;
-  const BackwardLayout l = backward_layout(M, N, K, 2);
+  if (!any) return CCE_OK;
   char* ws = static_cast<char*>(workspace);
   LinGrad g{};
   g.dy = grad_y;
@@ -650,7 +680,7 @@ cce_status cce_gated_linear_backward(const void* grad_y, int64_t g_pitch, const 
   g.N = static_cast<int>(N);
   g.act = act;
   int rows = 0;
-  if (launch_linear_grad(g, true, type == CCE_BF16, on.sms, s, &rows) != cudaSuccess) st = CCE_ERR_CUDA;
+  if (launch_linear_grad(g, true, type == CCE_BF16, s, &rows) != cudaSuccess) st = CCE_ERR_CUDA;
   ++launches;
   const Operand dz[2] = {{g.dz[0], l.pitch}, {g.dz[1], l.pitch}};
   void* grad_w[2] = {grad_gate_weight, grad_up_weight};

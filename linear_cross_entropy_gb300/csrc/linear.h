@@ -71,6 +71,7 @@ struct LinArgs {
   int32_t* error;  // the device's error word (CCE_DEVERR_*)
 };
 
+constexpr int LIN_SMS = 152;  // what sizes of grids and workspaces count with, on any device
 constexpr int LIN_BI = 128;  // rows of the MMA a CTA: I extent of a tile (gated: 64 of each weight)
 // Blocks of K: a stage's depth.  A pair's loads are issued half as often with the deeper one.
 constexpr int lin_bk(bool pair) { return pair ? 128 : 64; }
@@ -135,8 +136,10 @@ struct LinGrad {
   int M, N, act;
 };
 constexpr int LIN_GRAD_PARTS = 256;
-// *parts: how many parts there are of the sums.
-cudaError_t launch_linear_grad(const LinGrad& a, bool gated, bool bf16, int sms, cudaStream_t s, int* parts);
+// How many parts of the sums there are, at most (whole vectors; fewer otherwise).
+int linear_grad_parts(int64_t M, int64_t N);
+// *parts: how many there are.
+cudaError_t launch_linear_grad(const LinGrad& a, bool gated, bool bf16, cudaStream_t s, int* parts);
 cudaError_t launch_linear_sum(const LinSum& a, cudaStream_t s);
 
 

@@ -203,8 +203,15 @@ __global__ void __launch_bounds__(THREADS) copy_kernel(const __grid_constant__ L
 
 bool multiple(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(bytes) == 0; }
 
+// Blocks for the rows: six an SM in all, no more than there are rows for.
+int grad_rows(int64_t M, int64_t N, int vec) {
+  const int64_t x = (N + COLS * vec - 1) / (COLS * vec);
+  return static_cast<int>(std::max<int64_t>(
+      1, std::min({int64_t(LIN_GRAD_PARTS), (6 * LIN_SMS + x - 1) / x, (M + GROUPS * UNROLL - 1) / (GROUPS * UNROLL)})));
+}
+
 template <typename T, typename TY, bool GATED>
-cudaError_t launch_grad(const LinGrad& a, int sms, cudaStream_t s, int* parts) {
+cudaError_t launch_grad(const LinGrad& a, cudaStream_t s, int* parts) {
   // vectors of 8: whole rows of them at 16 bytes in every matrix (dy of fp32 rows as two)
   bool wide = a.N % 8 == 0 && a.dy_pitch % 8 == 0 && multiple(a.dy, 16);
   for (int m = 0; m < (GATED ? 2 : 1); ++m) {
@@ -212,9 +219,7 @@ cudaError_t launch_grad(const LinGrad& a, int sms, cudaStream_t s, int* parts) {
     if (a.dz[m]) wide = wide && a.dz_pitch % 8 == 0 && multiple(a.dz[m], 16);
   }
   const int vec = wide ? 8 : 1;
-  const int x = (a.N + COLS * vec - 1) / (COLS * vec);
-  // six blocks an SM, no more than there are rows for
-  const int y = std::max(1, std::min({LIN_GRAD_PARTS, (6 * sms + x - 1) / x, (a.M + GROUPS * UNROLL - 1) / (GROUPS * UNROLL)}));
+  const int x = (a.N + COLS * vec - 1) / (COLS * vec), y = grad_rows(a.M, a.N, vec);
   const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(y));
   *parts = y;
   return wide ? launch_after(grad_kernel<T, TY, GATED, 8>, grid, dim3(THREADS), 0, 1, s, a)
@@ -222,10 +227,9 @@ cudaError_t launch_grad(const LinGrad& a, int sms, cudaStream_t s, int* parts) {
 }
 
 template <typename T>
-cudaError_t launch_grad_of(const LinGrad& a, bool gated, int sms, cudaStream_t s, int* parts) {
-  if (gated) return launch_grad<T, T, true>(a, sms, s, parts);
-  return a.dy_type == CCE_F32 ? launch_grad<T, float, false>(a, sms, s, parts)
-                              : launch_grad<T, T, false>(a, sms, s, parts);
+cudaError_t launch_grad_of(const LinGrad& a, bool gated, cudaStream_t s, int* parts) {
+  if (gated) return launch_grad<T, T, true>(a, s, parts);
+  return a.dy_type == CCE_F32 ? launch_grad<T, float, false>(a, s, parts) : launch_grad<T, T, false>(a, s, parts);
 }
 
 template <typename T, bool GATED>
@@ -252,9 +256,10 @@ cudaError_t launch_linear_join(const LinProblem& p, bool gated, bool bf16, int s
   return gated ? launch_join<__half, true>(p, sms, s) : launch_join<__half, false>(p, sms, s);
 }
 
-cudaError_t launch_linear_grad(const LinGrad& a, bool gated, bool bf16, int sms, cudaStream_t s, int* parts) {
-  return bf16 ? launch_grad_of<__nv_bfloat16>(a, gated, sms, s, parts)
-              : launch_grad_of<__half>(a, gated, sms, s, parts);
+int linear_grad_parts(int64_t M, int64_t N) { return grad_rows(M, N, 8); }
+
+cudaError_t launch_linear_grad(const LinGrad& a, bool gated, bool bf16, cudaStream_t s, int* parts) {
+  return bf16 ? launch_grad_of<__nv_bfloat16>(a, gated, s, parts) : launch_grad_of<__half>(a, gated, s, parts);
 }
 
 cudaError_t launch_linear_copies(const LinCopies& a, int sms, cudaStream_t s) {
