@@ -137,9 +137,15 @@ int kept_code(const Tensor& z, const Tensor& x, const char* name) {
   return CCE_KEPT16;
 }
 
+// What a relu's backward pass reads of z is its sign, and bf16 has one for all but z's last subnormals.
+at::ScalarType kept_type(const Tensor& x, const std::string& activation) {
+  return activation == "relu" ? x.scalar_type() : kept_type(x);
+}
+
+// z is kept in the type of `keep`, if there is one.
 std::tuple<Tensor, Tensor> linear_forward(const Tensor& x, const Tensor& weight, const Tensor& bias,
                                           const Tensor& residual, const std::string& activation, const OptType& out,
-                                          bool save) {
+                                          const OptType& keep) {
   refuse_tracing();
   refuse_tangents(tangents_live(), x, weight, bias, residual);
   const Sizes s = check_layer(x, weight, "weight");
@@ -160,8 +166,7 @@ std::tuple<Tensor, Tensor> linear_forward(const Tensor& x, const Tensor& weight,
   const Tensor b = plain(bias);
   const auto shape = result_shape(x, s.N);
   Tensor y = at::empty(shape, x.options().dtype(y_type).requires_grad(false));
-  const auto kept = x.options().dtype(kept_type(x)).requires_grad(false);
-  Tensor z = save && act != CCE_ACT_NONE ? at::empty(shape, kept) : Tensor();
+  Tensor z = keep && act != CCE_ACT_NONE ? at::empty(shape, x.options().dtype(*keep).requires_grad(false)) : Tensor();
   note_device(x);
   check_status(cce_linear_forward(pointer(xp.t), xp.pitch, pointer(wp.t), wp.pitch, s.type, pointer(b),
                                   b.defined() ? type_code(b.scalar_type()) : s.type, pointer(r.t), r.inner, r.row, r.outer, act,
@@ -290,7 +295,7 @@ using torch::autograd::variable_list;
 struct Linear : torch::autograd::Function<Linear> {
   static Tensor forward(AutogradContext* ctx, const Tensor& x, const Tensor& weight, const OptTensor& bias,
                         const OptTensor& residual, const std::string& activation, OptType out) {
-    auto [y, z] = linear_forward(x, weight, given(bias), given(residual), activation, out, true);
+    auto [y, z] = linear_forward(x, weight, given(bias), given(residual), activation, out, kept_type(x, activation));
     ctx->save_for_backward({x, weight, z});
     ctx->saved_data["activation"] = activation;
     if (bias) ctx->saved_data["bias_type"] = static_cast<int64_t>(bias->scalar_type());
@@ -350,7 +355,7 @@ Tensor linear(const Tensor& x, const Tensor& weight, const OptTensor& bias, cons
   const Tensor b = given(bias), r = given(residual);
   if (at::GradMode::is_enabled() && (records(x) || records(weight) || records(b) || records(r)))
     return Linear::apply(x, weight, bias, residual, activation, out);
-  return std::get<0>(linear_forward(x, weight, b, r, activation, out, false));
+  return std::get<0>(linear_forward(x, weight, b, r, activation, out, {}));
 }
 
 Tensor gated_linear(const Tensor& x, const Tensor& gate_weight, const Tensor& up_weight,
@@ -384,7 +389,9 @@ void binding::bind_layers(py::module_& m) {
   m.def(
       "linear_forward",
       [](const Tensor& x, const Tensor& w, const OptTensor& b, const OptTensor& r, const std::string& activation,
-         const OptType& out, bool save) { return linear_forward(x, w, given(b), given(r), activation, out, save); },
+         const OptType& out, bool save) {
+        return linear_forward(x, w, given(b), given(r), activation, out, save ? OptType(kept_type(x)) : OptType());
+      },
       Free());
   m.def(
       "linear_backward",

@@ -17,7 +17,11 @@ on 16 bytes and a multiple of 8 elements apart, are read in place, others
 (z Phi(z), Phi within (z^2 + 16) 2^-23 of itself), "gelu_tanh", "silu".  For the backward pass what goes into the
 activation is kept in 16 bits, two of which more are fraction than bf16 has (torch
 int16 words that only the backward reads; fp16 for fp16), and the gradient in front
-of it is rounded to x's type for its products.
+of it is rounded to x's type for its products.  The words hold values from 2^-30 to
+2^32 so, with fewer bits down to 2^-40; beyond, they count as infinite or 0 in the
+backward pass: a bf16 gated layer whose gate or up projection passes 2^32 has a finite
+result and an infinite or NaN gradient.  (linear with relu keeps x's type, whose sign
+holds over all of its range.)
 
 Calls run on the current stream of x's device and can be captured into a CUDA
 graph (a backward pass while no graph of autograd that was made outside of the
@@ -63,7 +67,8 @@ def _on(stream, call, *args):
 def cce_linear_forward(x, weight, bias=None, residual=None, activation=None, *, out_dtype=None, save=False,
                        stream=None):
     """(y, z): y = act(z) + residual with z = x weight^T + bias.  z is for
-    cce_linear_backward alone: int16 words for bf16, else values of x's type; None with
+    cce_linear_backward alone: int16 words for bf16, of the range above (a positive z
+    below 2^-40 counts as 0, also for relu), else values of x's type; None with
     save=False or without activation."""
     return _on(stream, _native.linear_forward, x, weight, bias, residual, _name(activation), out_dtype, save)
 
