@@ -121,6 +121,15 @@ class AdamW(torch.optim.Optimizer):
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, *, state_bits=32,
                  master_weights=False, min_8bit_size=4096, seed=0, capturable=False):
+        super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, state_bits=state_bits,
+                                      master_weights=master_weights, min_8bit_size=min_8bit_size, seed=seed,
+                                      capturable=capturable))
+
+    def add_param_group(self, param_group):
+        """As of any optimiser; a group's own options are checked as the optimiser's are."""
+        options = self.defaults | param_group
+        state_bits, lr, betas = options["state_bits"], options["lr"], options["betas"]
+        eps, weight_decay = options["eps"], options["weight_decay"]
         if state_bits not in (8, 32):
             raise ValueError(f"state_bits must be 8 or 32, got {state_bits}")
         if not isinstance(lr, torch.Tensor) and not lr >= 0.0:
@@ -129,9 +138,7 @@ class AdamW(torch.optim.Optimizer):
             raise ValueError(f"betas must be in [0, 1), got {betas}")
         if not eps >= 0.0 or not weight_decay >= 0.0:
             raise ValueError(f"eps and weight_decay must be at least 0, got {eps} and {weight_decay}")
-        super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, state_bits=state_bits,
-                                      master_weights=master_weights, min_8bit_size=min_8bit_size, seed=seed,
-                                      capturable=capturable))
+        super().add_param_group(param_group)
 
     def _counter(self, device, group):
         """The group's count of steps on that device."""
