@@ -207,13 +207,20 @@ class AdamW(torch.optim.Optimizer):
         return loss
 
     def load_state_dict(self, state_dict):
-        """As of any optimiser, but the states keep their own types."""
+        """As of any optimiser, but the states keep their own types.  32-bit states and
+        masters take the parameters' strides; 8-bit ones, whose scales go by the order
+        in memory, are for parameters of the strides that they were made for."""
         super().load_state_dict(state_dict)
         saved = [i for g in state_dict["param_groups"] for i in g["params"]]
         own = [p for g in self.param_groups for p in g["params"]]
         for i, p in zip(saved, own):
             for k, v in state_dict["state"].get(i, {}).items():
-                if isinstance(v, torch.Tensor):
+                if not isinstance(v, torch.Tensor):
+                    continue
+                if k in ("exp_avg", "exp_avg_sq", "master") and v.dtype == torch.float32 and v.shape == p.shape:
+                    own_order = torch.empty_like(p, dtype=v.dtype, requires_grad=False, memory_format=torch.preserve_format)
+                    self.state[p][k] = own_order.copy_(v.detach())
+                else:
                     self.state[p][k] = v.detach().to(p.device).clone(memory_format=torch.preserve_format)
         for group in self.param_groups:
             if group["capturable"]:
