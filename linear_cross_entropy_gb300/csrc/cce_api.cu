@@ -563,7 +563,8 @@ struct DeviceInfo {
   bool ok = false;
   int sms = 0;
   int pair_clusters = 0;  // CTA pairs of the forward GEMM resident at once
-  int linear_pairs = 0;   // and of the layers' GEMM
+  bool linear_init = false;  // the layers' GEMM is prepared, when a layer first runs
+  int linear_pairs = 0;      // its CTA pairs resident at once
   int32_t* linear_error = nullptr;  // its error word
 };
 std::mutex g_mu;
@@ -571,7 +572,7 @@ DeviceInfo g_dev[64];
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
 cce_status device_check(int* sms, int* pair_clusters = nullptr, int* linear_pairs = nullptr,
-                        int32_t** linear_error = nullptr) {
+                        int32_t** linear_error = nullptr) {  // linear_error: of a layer's call
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
     cudaGetLastError();
@@ -590,12 +591,11 @@ cce_status device_check(int* sms, int* pair_clusters = nullptr, int* linear_pair
     d.ok = (major == 10 && minor == 3);
     d.sms = sms;
     if (d.ok) {
-      if (prepare_gemm_kernels() != cudaSuccess || prepare_linear_gemm(&d.linear_error) != cudaSuccess) {
+      if (prepare_gemm_kernels() != cudaSuccess) {
         cudaGetLastError();
         return CCE_ERR_CUDA;
       }
       d.pair_clusters = gemm_pair_clusters(sms);
-      d.linear_pairs = linear_pair_units(sms);
       if (!g_encode) {
         cudaDriverEntryPointQueryResult q;
         void* fn = nullptr;
@@ -611,6 +611,14 @@ cce_status device_check(int* sms, int* pair_clusters = nullptr, int* linear_pair
     d.init = true;
   }
   if (!d.ok) return CCE_ERR_DEVICE;
+  if (linear_error && !d.linear_init) {
+    if (prepare_linear_gemm(&d.linear_error) != cudaSuccess) {
+      cudaGetLastError();
+      return CCE_ERR_CUDA;
+    }
+    d.linear_pairs = linear_pair_units(d.sms);
+    d.linear_init = true;
+  }
   *sms = d.sms;
   if (pair_clusters) *pair_clusters = d.pair_clusters;
   if (linear_pairs) *linear_pairs = d.linear_pairs;
