@@ -30,6 +30,14 @@ enum { CCE_WANT_DX = 1, CCE_WANT_DW = 2, CCE_WANT_DW_UP = 4, CCE_WANT_DB = 8, CC
 size_t cce_linear_backward_workspace_bytes_ex(int64_t M, int64_t N, int64_t K, int want);
 size_t cce_gated_linear_backward_workspace_bytes_ex(int64_t M, int64_t N, int64_t K, int want);
 
+/*
+ * Self-test of the failure path of the products' waits: one thread waits, as their roles do,
+ * on a barrier that nothing arrives on; after timeout_us (1 .. 10^7) microseconds the wait
+ * gives up and sets the device's error word, which cce_layers_take_error then gives
+ * (CCE_DEVERR_TIMEOUT).  No fault, no hang: the context stays usable.
+ */
+cce_status cce_selftest_layers_wait_timeout(uint32_t timeout_us, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

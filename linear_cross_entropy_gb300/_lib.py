@@ -213,6 +213,8 @@ def load() -> ctypes.CDLL:
         query = getattr(lib, f"cce_{name}_workspace_bytes_ex")
         query.argtypes = [i64, i64, i64, ci]
         query.restype = sz
+    lib.cce_selftest_layers_wait_timeout.argtypes = [ctypes.c_uint32, vp]
+    lib.cce_selftest_layers_wait_timeout.restype = ci
     # include/cce_optim.h
     lib.cce_optim_abi_version.argtypes = []
     lib.cce_optim_abi_version.restype = ci

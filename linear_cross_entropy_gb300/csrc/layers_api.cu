@@ -722,4 +722,15 @@ cce_status cce_layers_take_error(int32_t* word, void* stream) {
   return take_linear_error(word, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CCE_OK : CCE_ERR_CUDA;
 }
 
+cce_status cce_selftest_layers_wait_timeout(uint32_t timeout_us, void* stream) {
+  if (timeout_us == 0 || timeout_us > 10000000u) return CCE_ERR_ARG;
+  Device on;
+  const cce_status st = on.ready();
+  if (st != CCE_OK) return st;
+  count_launches(1);
+  return launch_linear_wait_timeout(on.error, uint64_t(timeout_us) * 1000u, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? CCE_OK
+             : CCE_ERR_CUDA;
+}
+
 }  // extern "C"

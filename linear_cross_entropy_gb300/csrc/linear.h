@@ -103,6 +103,8 @@ int linear_pair_units(int sms);
 cudaError_t prepare_linear_gemm(int32_t** error);
 // The device's error word (CCE_DEVERR_*) of these kernels, taken and cleared behind `s`.
 cudaError_t take_linear_error(int32_t* word, cudaStream_t s);
+// A wait that runs out and sets `error` (cce_selftest_layers_wait_timeout).
+cudaError_t launch_linear_wait_timeout(int32_t* error, uint64_t timeout_ns, cudaStream_t s);
 
 // y = epilogue of the sums over the splits of a problem.
 cudaError_t launch_linear_join(const LinProblem& p, bool gated, bool bf16, int sms, cudaStream_t s);

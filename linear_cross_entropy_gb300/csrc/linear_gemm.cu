@@ -5,6 +5,21 @@ namespace cce {
 
 namespace {
 __device__ int32_t linear_error;  // CCE_DEVERR_* of waits that ran out
+
+// The wait of the GEMM's roles, on a barrier that nothing arrives on.
+__global__ void wait_timeout_kernel(int32_t* error, uint64_t timeout_ns) {
+  __shared__ uint64_t bar;
+  __shared__ int abort_flag;
+  mbar_init(&bar, 1);
+  abort_flag = 0;
+  fence_mbar_init();
+  wait_bounded_long(&bar, 0, &abort_flag, error, timeout_ns);
+}
+}
+
+cudaError_t launch_linear_wait_timeout(int32_t* error, uint64_t timeout_ns, cudaStream_t s) {
+  wait_timeout_kernel<<<1, 1, 0, s>>>(error, timeout_ns);
+  return cudaGetLastError();
 }
 
 cudaError_t prepare_linear_gemm(int32_t** error) {

@@ -119,14 +119,14 @@ __device__ __forceinline__ bool mbar_try_wait_long(uint32_t bar, uint32_t parity
 }
 
 __device__ __forceinline__ bool wait_bounded_long(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                                  int32_t* dev_err) {
+                                                  int32_t* dev_err, uint64_t timeout_ns = CCE_WAIT_TIMEOUT_NS) {
   const uint32_t b = smem_u32(bar);
   if (mbar_try_wait_long(b, parity)) return true;
   const uint64_t t0 = globaltimer();
   while (true) {
     if (mbar_try_wait_long(b, parity)) return true;
     if (*abort_flag) return false;
-    if (globaltimer() - t0 > CCE_WAIT_TIMEOUT_NS) {
+    if (globaltimer() - t0 > timeout_ns) {
       *abort_flag = 1;
       if (dev_err) atomicOr(reinterpret_cast<int*>(dev_err), CCE_DEVERR_TIMEOUT);
       return false;
@@ -369,8 +369,6 @@ __device__ __forceinline__ uint32_t cluster_count_x() {
   return r;
 }
 
-// Every thread of both CTAs: memory operations before it are visible to the
-// peer after it.
 // All threads of the cluster are here; orders no memory (with a release the threads' own stores land first: 1,200 cycles).
 __device__ __forceinline__ void cluster_sync_relaxed() {
   asm volatile(
@@ -378,6 +376,8 @@ __device__ __forceinline__ void cluster_sync_relaxed() {
       "barrier.cluster.wait.aligned;" ::
           : "memory");
 }
+// Every thread of both CTAs: memory operations before it are visible to the
+// peer after it.
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
