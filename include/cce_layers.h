@@ -8,8 +8,9 @@
  * allocates no device memory), argument checks run before anything is launched
  * and return a cce_status, calls are asynchronous on `stream`, outputs are
  * overwritten and overlap no input.  Every result is deterministic: the order of
- * every sum is fixed by the sizes, types and alignments of the arguments and by
- * the device.
+ * every sum is fixed by the sizes, types and alignments of the arguments, by which
+ * results are asked for and by the device (a grad_x alone and one beside weight
+ * gradients may sum in another order).
  *
  * Matrices
  * --------
